@@ -379,6 +379,117 @@ CP_API cp_status_t causal_product_bwd_favor(const void* xq, const void* xk, cons
                                             cp_dtype_t dtype, void* workspace,
                                             size_t workspace_bytes, void* stream);
 
+/* The gated delta rule: the causal product's state with a decay, where a
+ * write first takes out what the key already holds.  For every (b, h), from
+ * S_0 (D x M, zero when absent), with a_t = e^{g_t}:
+ *     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),
+ *     out_t = scale S_t^T q_t.
+ * q, k [B][Hk][N][D] in `dtype`, Hk a divisor of H: value head h reads key
+ * head h / (H / Hk).  v, out [B][H][N][M] in `dtype`; g (log decay, <= 0) and
+ * beta [B][H][N] fp32; states [B][H][D][M] fp32.  D, M in [1, 256], multiples
+ * of 8 for bf16.  Contiguous device pointers, 16-byte aligned (g, beta: 4);
+ * outputs overlap nothing.  N = 0 passes the state through.
+ *
+ * g_t = -inf clears the state before token t (any g_t below -120 does, e^-120
+ * being 0 in fp32); beta_t = 0 writes nothing, so a token with g = beta = 0 is
+ * padding.  A NaN or inf among a head's inputs reaches that head's later
+ * outputs.  Keys longer than 1 (beta |k|^2 > 2) can make the state grow without
+ * bound; causal_product_qk_rope leaves them with the norm the rule wants.
+ *
+ * State, products and sums are fp32 (CUDA cores) for every dtype; results are
+ * bitwise reproducible.
+ *
+ * Training: the forward writes the state before every chunk of rows into
+ * `ckpt` (causal_product_delta_checkpoint_size bytes; NULL: not kept), and the
+ * backward, given the same inputs and that buffer, writes the gradients of
+ *     L = <grad_out, out> + <grad_state_out, S_N>
+ * (grad_state_out NULL: zero): grad_q, grad_k [B][Hk][N][D] (summed over the
+ * value heads that share a key head), grad_v, grad_g and grad_beta (fp32), and
+ * grad_state_in = dL/dS_0 (NULL: not written).  grad_g is 0 where g < -120.
+ * S_0 is not an argument: the checkpoints begin with it.
+ *
+ * Workspace: causal_product_delta_workspace_size bytes, or NULL (allocated and
+ * freed on `stream`).  Errors as causal_product_fwd; CP_ERR_INVALID_ARG too
+ * when Hk does not divide H or scale is not finite. */
+CP_API size_t causal_product_delta_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N,
+                                                  int64_t D, int64_t M, cp_dtype_t dtype,
+                                                  int backward);
+CP_API size_t causal_product_delta_checkpoint_size(int64_t B, int64_t H, int64_t Hk, int64_t N,
+                                                   int64_t D, int64_t M, cp_dtype_t dtype);
+CP_API cp_status_t causal_product_fwd_delta(const void* q, const void* k, const void* v,
+                                            const float* g, const float* beta, void* out,
+                                            const float* state_in, float* state_out, float* ckpt,
+                                            size_t ckpt_bytes, float scale, int64_t B, int64_t H,
+                                            int64_t Hk, int64_t N, int64_t D, int64_t M,
+                                            cp_dtype_t dtype, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+CP_API cp_status_t causal_product_bwd_delta(const void* q, const void* k, const void* v,
+                                            const float* g, const float* beta,
+                                            const void* grad_out, const float* ckpt,
+                                            size_t ckpt_bytes, const float* grad_state_out,
+                                            void* grad_q, void* grad_k, void* grad_v,
+                                            float* grad_g, float* grad_beta, float* grad_state_in,
+                                            float scale, int64_t B, int64_t H, int64_t Hk,
+                                            int64_t N, int64_t D, int64_t M, cp_dtype_t dtype,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of the gated delta rule for every (b, h), the state updated in
+ * place: causal_product_fwd_delta with N = 1.  q, k [B][Hk][D], v, out
+ * [B][H][M] in `dtype`; g, beta [B][H] fp32.  state [pool][H][D][M] fp32; with
+ * slots ([B] int32, device) sequence b's state is state[slots[b]], and a slot
+ * outside [0, pool) is an idle row (out zero, no state touched); with slots
+ * NULL it is state[b] and pool must be at least B.  Two sequences of one call
+ * must not share a slot (their updates would race).  fp32 arithmetic for every
+ * dtype.  No workspace. */
+CP_API cp_status_t causal_product_decode_delta(const void* q, const void* k, const void* v,
+                                               const float* g, const float* beta, void* out,
+                                               float* state, const int32_t* slots, int64_t pool,
+                                               float scale, int64_t B, int64_t H, int64_t Hk,
+                                               int64_t D, int64_t M, cp_dtype_t dtype,
+                                               void* stream);
+
+/* The norm of queries and keys per head with the position rotation, which
+ * makes the rows the causal product and the delta rule take out of a
+ * projection's.  For every row x of D features:
+ *     y = w o x r,   r = (c sum x^2 + eps)^-1/2,
+ * c = 1 / D for CP_QK_NORM_RMS and 1 for CP_QK_NORM_L2, then features (i,
+ * i + R/2), i < R/2, become (y_i cos_i - y_{i+R/2} sin_i, y_{i+R/2} cos_i +
+ * y_i sin_i); features from R on are not turned (R even, 0 <= R <= D).
+ * xq, xk: rows [B][Hq or Hk][N] of D dense features in `dtype`, at the strides
+ * (batch, head, row; elements, >= 0) given in stride_q, stride_k: a
+ * projection's token-major rows are read where they are.  wq, wk: [D] in
+ * `dtype`, NULL for ones.  cos, sin: [N][R/2] fp32 for each batch, cs_batch
+ * elements apart (0: one table for all; R = 0: may be NULL).  q, k: dense
+ * [B][H][N][D] in `dtype`, 16-byte aligned.  D a multiple of 8, 8 .. 256; eps
+ * finite, >= 0 (with eps = 0 a zero row gives NaN).  fp32 arithmetic, rounded
+ * once.  Outputs overlap nothing.
+ *
+ * Backward, from grad_q, grad_k (dense as q, k): grad_xq, grad_xk, dense
+ * [B][H][N][D], and grad_wq, grad_wk [D] in `dtype` (NULL exactly where the
+ * weight is), summed in a fixed order.  Workspace:
+ * causal_product_qk_rope_workspace_size bytes, or NULL (allocated on
+ * `stream`). */
+typedef enum { CP_QK_NORM_RMS = 0, CP_QK_NORM_L2 = 1 } cp_qk_norm_t;
+CP_API cp_status_t causal_product_qk_rope(const void* xq, const int64_t* stride_q, const void* xk,
+                                          const int64_t* stride_k, const void* wq, const void* wk,
+                                          const float* cos, const float* sin, int64_t cs_batch,
+                                          void* q, void* k, cp_qk_norm_t norm, float eps,
+                                          int64_t B, int64_t Hq, int64_t Hk, int64_t N, int64_t D,
+                                          int64_t R, cp_dtype_t dtype, void* stream);
+CP_API size_t causal_product_qk_rope_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t N,
+                                                    int64_t D, cp_dtype_t dtype);
+CP_API cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* stride_q,
+                                              const void* xk, const int64_t* stride_k,
+                                              const void* wq, const void* wk, const float* cos,
+                                              const float* sin, int64_t cs_batch,
+                                              const void* grad_q, const void* grad_k,
+                                              void* grad_xq, void* grad_xk, void* grad_wq,
+                                              void* grad_wk, cp_qk_norm_t norm, float eps,
+                                              int64_t B, int64_t Hq, int64_t Hk, int64_t N,
+                                              int64_t D, int64_t R, cp_dtype_t dtype,
+                                              void* workspace, size_t workspace_bytes,
+                                              void* stream);
+
 /* Size of the static device scratch array behind causal_product_fwd_noalloc. */
 #define CP_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 

@@ -36,6 +36,10 @@ __all__ = [
     "causal_product_launch_count", "causal_product_status",
     "causal_product_checkpoint_size", "causal_product_fwd_ckpt", "causal_product_bwd_ckpt",
     "causal_product_fwd_favor", "causal_product_bwd_favor", "causal_product_favor",
+    "causal_product_fwd_delta", "causal_product_bwd_delta", "causal_product_delta",
+    "causal_product_decode_delta", "causal_product_delta_workspace_size",
+    "causal_product_delta_checkpoint_size",
+    "causal_product_qk_rope", "causal_product_qk_rope_bwd", "qk_rope", "QK_NORMS",
     "causal_product_error_string", "library_path", "load_library",
 ]
 
@@ -46,6 +50,9 @@ _DTYPES = {torch.float32: CP_DTYPE_F32, torch.bfloat16: CP_DTYPE_BF16,
            torch.float16: CP_DTYPE_F16}
 # feature maps applied to q and k inside the kernels (cp_feature_t)
 FEATURES = {None: 0, "none": 0, "elu1": 1}
+
+# norms of queries and keys (cp_qk_norm_t)
+QK_NORMS = {"rms": 0, "l2": 1}
 
 
 def _feature_code(feature) -> int:
@@ -145,6 +152,28 @@ def load_library(rebuild: bool = True) -> ctypes.CDLL:
             lib.causal_product_bwd_favor.argtypes = [p, p, p, p, p, p, p, p, i64, i64, i64, i64,
                                                      i64, i64, c_int, p, sz, p]
             lib.causal_product_bwd_favor.restype = c_int
+            f32 = ctypes.c_float
+            lib.causal_product_delta_workspace_size.argtypes = [i64] * 6 + [c_int, c_int]
+            lib.causal_product_delta_workspace_size.restype = sz
+            lib.causal_product_delta_checkpoint_size.argtypes = [i64] * 6 + [c_int]
+            lib.causal_product_delta_checkpoint_size.restype = sz
+            lib.causal_product_fwd_delta.argtypes = ([p] * 9 + [sz, f32] + [i64] * 6
+                                                     + [c_int, p, sz, p])
+            lib.causal_product_fwd_delta.restype = c_int
+            lib.causal_product_bwd_delta.argtypes = ([p] * 7 + [sz] + [p] * 7 + [f32] + [i64] * 6
+                                                     + [c_int, p, sz, p])
+            lib.causal_product_bwd_delta.restype = c_int
+            lib.causal_product_decode_delta.argtypes = [p] * 8 + [i64, f32] + [i64] * 5 + [c_int, p]
+            lib.causal_product_decode_delta.restype = c_int
+            p64 = ctypes.POINTER(i64)
+            lib.causal_product_qk_rope.argtypes = ([p, p64, p, p64, p, p, p, p, i64, p, p, c_int, f32]
+                                                   + [i64] * 6 + [c_int, p])
+            lib.causal_product_qk_rope.restype = c_int
+            lib.causal_product_qk_rope_workspace_size.argtypes = [i64] * 5 + [c_int]
+            lib.causal_product_qk_rope_workspace_size.restype = sz
+            lib.causal_product_qk_rope_bwd.argtypes = ([p, p64, p, p64, p, p, p, p, i64] + [p] * 6
+                                                       + [c_int, f32] + [i64] * 6 + [c_int, p, sz, p])
+            lib.causal_product_qk_rope_bwd.restype = c_int
             lib.causal_product_status.argtypes = [p, p]
             lib.causal_product_status.restype = c_int
             lib.causal_product_error_string.argtypes = [c_int]
@@ -695,6 +724,290 @@ def causal_product_noalloc_status(stream: Optional[torch.cuda.Stream] = None,
     return int(load_library().causal_product_noalloc_status(_stream_ptr(stream, dev)))
 
 
+def _delta_dims(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                beta: torch.Tensor):
+    if (q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[0] != q.shape[0]
+            or v.shape[2] != q.shape[2] or q.shape[1] == 0 or v.shape[1] % q.shape[1] != 0):
+        raise ValueError(f"expected q,k [B,Hk,N,D] and v [B,H,N,M], H a multiple of Hk; got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    B, Hk, N, D = q.shape
+    H, M = v.shape[1], v.shape[3]
+    _check_like(g, (B, H, N), torch.float32, "g")
+    _check_like(beta, (B, H, N), torch.float32, "beta")
+    return B, H, Hk, N, D, M
+
+
+def causal_product_delta_workspace_size(B: int, H: int, Hk: int, N: int, D: int, M: int,
+                                        dtype: torch.dtype = torch.bfloat16,
+                                        backward: bool = False) -> int:
+    """Workspace bytes of causal_product_fwd_delta / _bwd_delta."""
+    return int(load_library().causal_product_delta_workspace_size(B, H, Hk, N, D, M, _DTYPES[dtype],
+                                                                  int(bool(backward))))
+
+
+def causal_product_delta_checkpoint_size(B: int, H: int, Hk: int, N: int, D: int, M: int,
+                                         dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of the states causal_product_fwd_delta keeps for the backward."""
+    return int(load_library().causal_product_delta_checkpoint_size(B, H, Hk, N, D, M,
+                                                                   _DTYPES[dtype]))
+
+
+def _delta_workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    # with no workspace of the caller's nobody reads the status word, so it
+    # need not begin at zero
+    if workspace is None:
+        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                             beta: torch.Tensor, out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None,
+                             state_in: Optional[torch.Tensor] = None, return_state: bool = False,
+                             state_out: Optional[torch.Tensor] = None, scale: float = 1.0,
+                             save: bool = False, ckpt: Optional[torch.Tensor] = None):
+    """The gated delta rule: S_t = a_t S_{t-1} + k_t u_t^T with u_t = beta_t
+    (v_t - a_t S_{t-1}^T k_t) and a_t = exp(g_t); out_t = scale S_t^T q_t.
+
+    q, k: [B,Hk,N,D]; v: [B,H,N,M], value head h reading key head h // (H //
+    Hk); g (log decay) and beta: float32 [B,H,N]; ``state_in`` is S_0 (float32
+    [B,H,D,M], None = zero).  Returns out, followed by S_N with
+    ``return_state`` and by the checkpoints causal_product_bwd_delta needs with
+    ``save`` (written into ``ckpt`` when given)."""
+    B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
+    code = _dtype_code(q, k, v)
+    if out is None:
+        out = torch.empty((B, H, N, M), dtype=v.dtype, device=v.device)
+    _check_like(out, (B, H, N, M), v.dtype, "out")
+    _check_device(q, k, v, g, beta, out)
+    if return_state and state_out is None:
+        state_out = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
+    lib = load_library()
+    if save or ckpt is not None:
+        ckpt = _delta_ckpt(B, H, Hk, N, D, M, v, ckpt)
+    need = lib.causal_product_delta_workspace_size(B, H, Hk, N, D, M, code, 0)
+    workspace = _delta_workspace(workspace, need, v.device)
+    rc = lib.causal_product_fwd_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
+        _state_arg(state_in, (B, H, D, M), v.device, "state_in"),
+        _state_arg(state_out, (B, H, D, M), v.device, "state_out"),
+        0 if ckpt is None else ckpt.data_ptr(), 0 if ckpt is None else ckpt.numel() * 4,
+        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
+        _stream_ptr(stream, v.device))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_fwd_delta")
+    got = (out,) + ((state_out,) if return_state else ()) + ((ckpt,) if save else ())
+    return got if len(got) > 1 else out
+
+
+def _delta_ckpt(B, H, Hk, N, D, M, v, ckpt):
+    n = causal_product_delta_checkpoint_size(B, H, Hk, N, D, M, v.dtype)
+    if ckpt is None:
+        ckpt = torch.empty(max(n // 4, 1), dtype=torch.float32, device=v.device)
+    if ckpt.dtype != torch.float32 or ckpt.numel() * 4 < n:
+        raise ValueError(f"ckpt must be a contiguous float32 tensor of at least {n} bytes")
+    _check_device(v, ckpt)
+    return ckpt
+
+
+def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                             beta: torch.Tensor, grad_out: torch.Tensor, ckpt: torch.Tensor,
+                             grad_q: Optional[torch.Tensor] = None,
+                             grad_k: Optional[torch.Tensor] = None,
+                             grad_v: Optional[torch.Tensor] = None,
+                             grad_g: Optional[torch.Tensor] = None,
+                             grad_beta: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None, scale: float = 1.0,
+                             grad_state_out: Optional[torch.Tensor] = None,
+                             return_state_grad: bool = False,
+                             grad_state_in: Optional[torch.Tensor] = None):
+    """(dq, dk, dv, dg, dbeta) of L = <grad_out, out> + <grad_state_out, S_N>
+    for causal_product_fwd_delta(..., save=True) on the same inputs, ``ckpt``
+    being the checkpoints it returned; with ``return_state_grad`` dL/dS_0
+    follows.  dq and dk are summed over the value heads of a key head."""
+    B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
+    code = _dtype_code(q, k, v, grad_out)
+    if grad_out.shape != v.shape:
+        raise ValueError("grad_out must have v's shape")
+    outs = []
+    for t, ref, name in ((grad_q, q, "grad_q"), (grad_k, k, "grad_k"), (grad_v, v, "grad_v"),
+                         (grad_g, g, "grad_g"), (grad_beta, beta, "grad_beta")):
+        t = torch.empty_like(ref) if t is None else t
+        _check_like(t, ref.shape, ref.dtype, name)
+        outs.append(t)
+    _check_device(q, k, v, g, beta, grad_out, *outs)
+    if return_state_grad and grad_state_in is None:
+        grad_state_in = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
+    if ckpt is None:
+        raise ValueError("ckpt must be the checkpoints causal_product_fwd_delta returned")
+    ckpt = _delta_ckpt(B, H, Hk, N, D, M, v, ckpt)
+    lib = load_library()
+    need = lib.causal_product_delta_workspace_size(B, H, Hk, N, D, M, code, 1)
+    workspace = _delta_workspace(workspace, need, v.device)
+    shape = (B, H, D, M)
+    rc = lib.causal_product_bwd_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        grad_out.data_ptr(), ckpt.data_ptr(), ckpt.numel() * 4,
+        _state_arg(grad_state_out, shape, v.device, "grad_state_out"),
+        *(t.data_ptr() for t in outs),
+        _state_arg(grad_state_in, shape, v.device, "grad_state_in"),
+        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
+        _stream_ptr(stream, v.device))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_bwd_delta")
+    return tuple(outs) + ((grad_state_in,) if return_state_grad else ())
+
+
+def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                                beta: torch.Tensor, state: torch.Tensor,
+                                out: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None, scale: float = 1.0,
+                                slots: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated delta rule, the state updated in place.
+
+    q, k: [B,Hk,D]; v: [B,H,M]; g, beta: float32 [B,H]; state: float32
+    [P,H,D,M].  ``slots`` (int32 [B], on the device) names each sequence's
+    state; one outside [0, P) is an idle row (out zero, no state touched).
+    Without ``slots`` sequence b has state b.  No two sequences may share a
+    slot."""
+    if (q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0]
+            or q.shape[1] == 0 or v.shape[1] % q.shape[1] != 0):
+        raise ValueError(f"expected q,k [B,Hk,D] and v [B,H,M], H a multiple of Hk; got "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    B, Hk, D = q.shape
+    H, M = v.shape[1], v.shape[2]
+    code = _dtype_code(q, k, v)
+    if out is None:
+        out = torch.empty((B, H, M), dtype=v.dtype, device=v.device)
+    _check_like(out, (B, H, M), v.dtype, "out")
+    _check_like(g, (B, H), torch.float32, "g")
+    _check_like(beta, (B, H), torch.float32, "beta")
+    _check_device(q, k, v, g, beta, out, state)
+    P = state.shape[0] if state.dim() == 4 else 0
+    _state_arg(state, (P, H, D, M), v.device, "state")
+    if slots is not None:
+        _check_like(slots, (B,), torch.int32, "slots")
+        _check_device(q, slots)
+    elif P < B:
+        raise ValueError(f"state holds {P} sequences, fewer than the {B} of this call")
+    rc = load_library().causal_product_decode_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
+        state.data_ptr(), 0 if slots is None else slots.data_ptr(), P, float(scale), B, H, Hk, D, M,
+        code, _stream_ptr(stream, v.device))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_decode_delta")
+    return out
+
+
+class _QkRope:
+    """Checked arguments of the q/k norm with rotation, as the C ABI takes them."""
+
+    def __init__(self, xq, xk, wq, wk, cos, sin, norm, eps):
+        if (xq.dim() != 4 or xk.dim() != 4 or xk.shape[0] != xq.shape[0]
+                or xk.shape[2:] != xq.shape[2:]):
+            raise ValueError(f"expected xq [B,Hq,N,D] and xk [B,Hk,N,D]; got {tuple(xq.shape)}, "
+                             f"{tuple(xk.shape)}")
+        if norm not in QK_NORMS:
+            raise ValueError(f"unknown norm {norm!r}; expected one of {list(QK_NORMS)}")
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin are given together")
+        B, Hq, N, D = xq.shape
+        Hk = xk.shape[1]
+        self.code = _dtype_code(xq, xk, *(w for w in (wq, wk) if w is not None))
+        for w, name in ((wq, "wq"), (wk, "wk")):
+            if w is not None:
+                _check_like(w, (D,), xq.dtype, name)
+        half = 0 if cos is None else cos.shape[-1]
+        tables = [] if cos is None else [cos, sin]
+        for t, name in zip(tables, ("cos", "sin")):
+            if t.dtype != torch.float32 or tuple(t.shape) not in ((N, half), (1, N, half),
+                                                                   (B, N, half)):
+                raise ValueError(f"{name} must be float32 of shape [N,R/2] or [B,N,R/2]; got "
+                                 f"{t.dtype} {tuple(t.shape)}")
+        if tables and sin.shape != cos.shape:
+            raise ValueError("cos and sin must have the same shape")
+        weights = [w for w in (wq, wk) if w is not None]
+        if xq.device.type != "cuda":
+            raise RuntimeError("causal_product runs on CUDA tensors only (no CPU path)")
+        if xk.device != xq.device:
+            raise RuntimeError("all tensors must be on the same CUDA device")
+        if weights + tables:
+            _check_device(*weights, *tables)
+            if (weights + tables)[0].device != xq.device:
+                raise RuntimeError("all tensors must be on the same CUDA device")
+        for x, name in ((xq, "xq"), (xk, "xk")):
+            if x.stride(3) != 1 and D > 1:
+                raise ValueError(f"the rows of {name} must be dense (stride 1 in the last dimension)")
+        strides = ctypes.c_int64 * 3
+        per_batch = cos is not None and cos.dim() == 3 and cos.shape[0] == B and B > 1
+        ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+        self.head = (xq.data_ptr(), strides(*xq.stride()[:3]), xk.data_ptr(),
+                     strides(*xk.stride()[:3]), ptr(wq), ptr(wk), ptr(cos), ptr(sin),
+                     N * half if per_batch else 0)
+        self.tail = (QK_NORMS[norm], float(eps), B, Hq, Hk, N, D, 2 * half, self.code)
+        self.q_shape, self.k_shape = (B, Hq, N, D), (B, Hk, N, D)
+
+
+def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor] = None,
+                           wk: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                           sin: Optional[torch.Tensor] = None, norm: str = "rms",
+                           eps: float = 1e-6, q: Optional[torch.Tensor] = None,
+                           k: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None):
+    """(q, k): the norm of every row of xq [B,Hq,N,D] and xk [B,Hk,N,D] over its
+    features (``norm``: "rms", or "l2" for length 1), times the weights wq, wk
+    ([D], None = ones), then features (i, i + R/2) of the first R turned by cos,
+    sin (float32 [N,R/2] or [B,N,R/2]; None = no rotation).  xq and xk may be
+    strided views (rows dense): a projection's ``x.view(B,N,H,D).transpose(1,
+    2)`` is read in place.  q and k come dense."""
+    a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
+    q = torch.empty(a.q_shape, dtype=xq.dtype, device=xq.device) if q is None else q
+    k = torch.empty(a.k_shape, dtype=xq.dtype, device=xq.device) if k is None else k
+    _check_like(q, a.q_shape, xq.dtype, "q")
+    _check_like(k, a.k_shape, xq.dtype, "k")
+    _check_device(q, k)
+    if q.device != xq.device:
+        raise RuntimeError("all tensors must be on the same CUDA device")
+    rc = load_library().causal_product_qk_rope(*a.head, q.data_ptr(), k.data_ptr(), *a.tail,
+                                               _stream_ptr(stream, xq.device))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_qk_rope")
+    return q, k
+
+
+def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor],
+                               wk: Optional[torch.Tensor], grad_q: torch.Tensor,
+                               grad_k: torch.Tensor, cos: Optional[torch.Tensor] = None,
+                               sin: Optional[torch.Tensor] = None, norm: str = "rms",
+                               eps: float = 1e-6, workspace: Optional[torch.Tensor] = None,
+                               stream: Optional[torch.cuda.Stream] = None):
+    """(dxq, dxk, dwq, dwk) of L = <grad_q, q> + <grad_k, k> for
+    causal_product_qk_rope; dxq and dxk dense, dwq and dwk None where the
+    weight is."""
+    a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
+    _check_like(grad_q, a.q_shape, xq.dtype, "grad_q")
+    _check_like(grad_k, a.k_shape, xq.dtype, "grad_k")
+    _check_device(grad_q, grad_k)
+    if grad_q.device != xq.device:
+        raise RuntimeError("all tensors must be on the same CUDA device")
+    dxq, dxk = torch.empty_like(grad_q), torch.empty_like(grad_k)
+    dwq = None if wq is None else torch.empty_like(wq)
+    dwk = None if wk is None else torch.empty_like(wk)
+    lib = load_library()
+    need = lib.causal_product_qk_rope_workspace_size(*a.q_shape[:2], a.k_shape[1], *a.q_shape[2:],
+                                                     a.code)
+    workspace = _delta_workspace(workspace, need, xq.device)
+    rc = lib.causal_product_qk_rope_bwd(
+        *a.head, grad_q.data_ptr(), grad_k.data_ptr(), dxq.data_ptr(), dxk.data_ptr(),
+        0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), *a.tail,
+        workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, xq.device))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_qk_rope_bwd")
+    return dxq, dxk, dwq, dwk
+
+
 class CausalProduct(torch.autograd.Function):
     """Autograd wrapper: forward and backward both call the C ABI; the
     forward keeps checkpoints of the state for the backward's dq scans."""
@@ -796,6 +1109,72 @@ def causal_product_favor(xq: torch.Tensor, xk: torch.Tensor, v: torch.Tensor,
     |x|^2 / 2) / sqrt(D) of the raw rows xq, xk, with autograd support for
     xq, xk and v (W is treated as a constant)."""
     return CausalProductFavor.apply(xq, xk, v, W)
+
+
+class CausalProductDelta(torch.autograd.Function):
+    """Autograd wrapper of the gated delta rule: (q, k, v, g, beta, S_0) ->
+    (out, S_N)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state, scale):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        g, beta = g.contiguous(), beta.contiguous()
+        state = None if state is None else state.contiguous()
+        out, s_n, ckpt = causal_product_fwd_delta(q, k, v, g, beta, state_in=state,
+                                                  return_state=True, scale=scale, save=True)
+        ctx.save_for_backward(q, k, v, g, beta, ckpt)
+        ctx.scale, ctx.has_state = scale, state is not None
+        ctx.set_materialize_grads(False)
+        return out, s_n
+
+    @staticmethod
+    def backward(ctx, go, gs):
+        q, k, v, g, beta, ckpt = ctx.saved_tensors
+        go = torch.zeros_like(v) if go is None else go.contiguous().to(v.dtype)
+        gs = None if gs is None else gs.contiguous().float()
+        d = causal_product_bwd_delta(q, k, v, g, beta, go, ckpt, scale=ctx.scale,
+                                     grad_state_out=gs, return_state_grad=ctx.has_state)
+        return d[:5] + (d[5] if ctx.has_state else None, None)
+
+
+def causal_product_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                         beta: torch.Tensor, state: Optional[torch.Tensor] = None,
+                         return_state: bool = False, scale: float = 1.0):
+    """The gated delta rule with autograd support (causal_product_fwd_delta);
+    with ``return_state`` the result is (out, state after the last row)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (q, k, v, g, beta, state)):
+        out, s_n = CausalProductDelta.apply(q, k, v, g, beta, state, scale)
+        return (out, s_n) if return_state else out
+    # no gradient is wanted: no checkpoints
+    return causal_product_fwd_delta(q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous(),
+                                    beta.contiguous(),
+                                    state_in=None if state is None else state.contiguous(),
+                                    return_state=return_state, scale=scale)
+
+
+class QkRope(torch.autograd.Function):
+    """Autograd wrapper of the q/k norm with rotation."""
+
+    @staticmethod
+    def forward(ctx, xq, xk, wq, wk, cos, sin, norm, eps):
+        ctx.save_for_backward(xq, xk, wq, wk, cos, sin)
+        ctx.norm, ctx.eps = norm, eps
+        return causal_product_qk_rope(xq, xk, wq, wk, cos, sin, norm, eps)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        xq, xk, wq, wk, cos, sin = ctx.saved_tensors
+        gq, gk = gq.contiguous().to(xq.dtype), gk.contiguous().to(xq.dtype)
+        return causal_product_qk_rope_bwd(xq, xk, wq, wk, gq, gk, cos, sin, ctx.norm,
+                                          ctx.eps) + (None, None, None, None)
+
+
+def qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor] = None,
+            wk: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+            sin: Optional[torch.Tensor] = None, norm: str = "rms", eps: float = 1e-6):
+    """causal_product_qk_rope with autograd support for xq, xk, wq and wk."""
+    return QkRope.apply(xq, xk, wq, wk, cos, sin, norm, eps)
 
 
 def causal_product(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

@@ -2,6 +2,7 @@
 // carving and the launches of the per-dtype kernels.  See
 // include/causal_product.h for the contract.
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <cstdint>
@@ -1045,3 +1046,305 @@ extern "C" cp_status_t causal_product_noalloc_status(void* stream) {
   if (st != CP_OK) return st;
   return causal_product_status(scratch, stream);
 }
+
+// ---------------------------------------------------------------- delta rule
+namespace cp {
+namespace {
+
+cp_status_t check_delta(const DeltaShape& s) {
+  const cp_status_t st = check_dims(s.B, s.H, s.N, s.D, s.M, s.dtype);
+  if (st != CP_OK) return st;
+  if (s.Hk <= 0 || s.H % s.Hk != 0 || !std::isfinite(s.scale)) return CP_ERR_INVALID_ARG;
+  return CP_OK;
+}
+
+size_t delta_ckpt_bytes(const DeltaShape& s) {
+  const int64_t c = delta_simt_chunk();
+  return (size_t)((s.N + c - 1) / c) * s.B * s.H * s.D * s.M * sizeof(float);
+}
+
+size_t delta_ws_bytes(const DeltaShape& s, bool backward) {
+  return kStatusBytes + round_up(s.N == 0 ? 0 : delta_simt_scratch(s, backward));
+}
+
+// Sizes in bytes of one call's tensors.
+struct DeltaBytes {
+  size_t qk, vo, gate, state, ckpt;
+  explicit DeltaBytes(const DeltaShape& s) {
+    const size_t es = s.dtype == CP_DTYPE_F32 ? 4 : 2;
+    qk = (size_t)s.B * s.Hk * s.N * s.D * es;
+    vo = (size_t)s.B * s.H * s.N * s.M * es;
+    gate = (size_t)s.B * s.H * s.N * sizeof(float);
+    state = (size_t)s.B * s.H * s.D * s.M * sizeof(float);
+    ckpt = delta_ckpt_bytes(s);
+  }
+};
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// Outputs overlap neither an input nor one another.
+template <size_t NI, size_t NO>
+bool disjoint(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (size_t o = 0; o < NO; ++o) {
+    for (const Span& i : in)
+      if (overlaps(out[o].p, out[o].n, i.p, i.n)) return false;
+    for (size_t x = 0; x < o; ++x)
+      if (overlaps(out[o].p, out[o].n, out[x].p, out[x].n)) return false;
+  }
+  return true;
+}
+
+template <size_t NI>
+bool all_aligned(const Span (&s)[NI]) {
+  for (const Span& x : s)
+    if (!aligned16(x.p)) return false;
+  return true;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+}  // namespace cp
+
+extern "C" {
+
+size_t causal_product_delta_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int64_t D,
+                                           int64_t M, cp_dtype_t dtype, int backward) {
+  const cp::DeltaShape s{B, H, Hk, N, D, M, dtype, 1.f};
+  return cp::check_delta(s) == CP_OK ? cp::delta_ws_bytes(s, backward != 0) : 0;
+}
+
+size_t causal_product_delta_checkpoint_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int64_t D,
+                                            int64_t M, cp_dtype_t dtype) {
+  const cp::DeltaShape s{B, H, Hk, N, D, M, dtype, 1.f};
+  return cp::check_delta(s) == CP_OK ? cp::delta_ckpt_bytes(s) : 0;
+}
+
+cp_status_t causal_product_fwd_delta(const void* q, const void* k, const void* v, const float* g,
+                                     const float* beta, void* out, const float* state_in,
+                                     float* state_out, float* ckpt, size_t ckpt_bytes, float scale,
+                                     int64_t B, int64_t H, int64_t Hk, int64_t N, int64_t D,
+                                     int64_t M, cp_dtype_t dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream_) {
+  const cp::DeltaShape s{B, H, Hk, N, D, M, dtype, scale};
+  cp_status_t st = cp::check_delta(s);
+  if (st != CP_OK) return st;
+  if (N > 0 && (!q || !k || !v || !g || !beta || !out)) return CP_ERR_INVALID_ARG;
+  const cp::DeltaBytes n(s);
+  if (ckpt != nullptr && ckpt_bytes < n.ckpt) return CP_ERR_WORKSPACE_TOO_SMALL;
+  const cp::Span in[6] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {state_in, n.state}, {g, n.gate},
+                          {beta, n.gate}};
+  const cp::Span outs[3] = {{out, n.vo}, {state_out, n.state}, {ckpt, n.ckpt}};
+  const cp::Span wide[4] = {in[0], in[1], in[2], in[3]};
+  if (!cp::all_aligned(wide) || !cp::all_aligned(outs) || !cp::aligned4(g) || !cp::aligned4(beta))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::delta_ws_bytes(s, false);
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) return cp::pass_state(state_in, state_out, n.state, stream);
+  const cp::DeltaFwd f{q, k, v, g, beta, state_in, out, state_out, ckpt};
+  return cp::delta_simt_fwd(s, f, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_bwd_delta(const void* q, const void* k, const void* v, const float* g,
+                                     const float* beta, const void* grad_out, const float* ckpt,
+                                     size_t ckpt_bytes, const float* grad_state_out, void* grad_q,
+                                     void* grad_k, void* grad_v, float* grad_g, float* grad_beta,
+                                     float* grad_state_in, float scale, int64_t B, int64_t H,
+                                     int64_t Hk, int64_t N, int64_t D, int64_t M, cp_dtype_t dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream_) {
+  const cp::DeltaShape s{B, H, Hk, N, D, M, dtype, scale};
+  cp_status_t st = cp::check_delta(s);
+  if (st != CP_OK) return st;
+  if (N > 0 && (!q || !k || !v || !g || !beta || !grad_out || !ckpt || !grad_q || !grad_k ||
+                !grad_v || !grad_g || !grad_beta))
+    return CP_ERR_INVALID_ARG;
+  const cp::DeltaBytes n(s);
+  if (ckpt_bytes < n.ckpt) return CP_ERR_WORKSPACE_TOO_SMALL;
+  const cp::Span in[8] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {grad_out, n.vo}, {ckpt, n.ckpt},
+                          {grad_state_out, n.state}, {g, n.gate}, {beta, n.gate}};
+  const cp::Span outs[6] = {{grad_q, n.qk}, {grad_k, n.qk}, {grad_v, n.vo},
+                            {grad_state_in, n.state}, {grad_g, n.gate}, {grad_beta, n.gate}};
+  const cp::Span wide[10] = {in[0], in[1], in[2], in[3], in[4], in[5], outs[0], outs[1], outs[2],
+                             outs[3]};
+  if (!cp::all_aligned(wide) || !cp::aligned4(g) || !cp::aligned4(beta) || !cp::aligned4(grad_g) ||
+      !cp::aligned4(grad_beta))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::delta_ws_bytes(s, true);
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) return cp::pass_state(grad_state_out, grad_state_in, n.state, stream);
+  cp::Scratch sc;
+  st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+  if (st != CP_OK) return st;
+  const cp::DeltaBwd f{q,      k,      v,      g,      beta,   grad_out,  ckpt, grad_state_out,
+                       grad_q, grad_k, grad_v, grad_g, grad_beta, grad_state_in};
+  void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  return cp::delta_simt_bwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_decode_delta(const void* q, const void* k, const void* v,
+                                        const float* g, const float* beta, void* out, float* state,
+                                        const int32_t* slots, int64_t pool, float scale, int64_t B,
+                                        int64_t H, int64_t Hk, int64_t D, int64_t M,
+                                        cp_dtype_t dtype, void* stream) {
+  const cp::DeltaShape s{B, H, Hk, 1, D, M, dtype, scale};
+  const cp_status_t st = cp::check_delta(s);
+  if (st != CP_OK) return st;
+  if (!q || !k || !v || !g || !beta || !out || !state || pool < 1 || (!slots && pool < B))
+    return CP_ERR_INVALID_ARG;
+  const cp::DeltaBytes n(s);
+  const cp::Span in[6] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {g, n.gate}, {beta, n.gate},
+                          {slots, (size_t)B * sizeof(int32_t)}};
+  const cp::Span outs[2] = {{out, n.vo}, {state, (size_t)pool * H * D * M * sizeof(float)}};
+  const cp::Span wide[3] = {in[0], in[1], in[2]};
+  if (!cp::all_aligned(wide) || !cp::all_aligned(outs) || !cp::aligned4(g) ||
+      !cp::aligned4(beta) || !cp::aligned4(slots))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const cp::DeltaDecode f{q, k, v, g, beta, slots, out, state, pool};
+  return cp::delta_decode_launch(s, f, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------- q/k norm, rotation
+namespace cp {
+namespace {
+
+cp_status_t check_qk_rope(const QkRope& f, cp_qk_norm_t norm) {
+  if (f.B <= 0 || f.Hq <= 0 || f.Hk <= 0 || f.N < 0) return CP_ERR_INVALID_ARG;
+  if (f.dtype != CP_DTYPE_F32 && f.dtype != CP_DTYPE_BF16 && f.dtype != CP_DTYPE_F16)
+    return CP_ERR_UNSUPPORTED_DTYPE;
+  if (f.D < 8 || f.D > 256 || f.D % 8 != 0 || f.R < 0 || f.R > f.D || f.R % 2 != 0)
+    return CP_ERR_UNSUPPORTED_SHAPE;
+  if (std::max(f.Hq, f.Hk) > 1 << 16 || f.B * std::max(f.Hq, f.Hk) > (int64_t)1 << 24 ||
+      f.N > (int64_t)1 << 31)
+    return CP_ERR_UNSUPPORTED_SHAPE;
+  if (norm != CP_QK_NORM_RMS && norm != CP_QK_NORM_L2) return CP_ERR_INVALID_ARG;
+  if (!(f.eps >= 0.f) || !std::isfinite(f.eps) || f.cs_batch < 0) return CP_ERR_INVALID_ARG;
+  return CP_OK;
+}
+
+// Bytes from the first to past the last element of rows [B][H][N][D] at the
+// given strides.
+size_t strided_bytes(const int64_t* st, int64_t B, int64_t H, int64_t N, int64_t D, size_t es) {
+  if (N == 0) return 0;
+  return (size_t)((B - 1) * st[0] + (H - 1) * st[1] + (N - 1) * st[2] + D) * es;
+}
+
+}  // namespace
+}  // namespace cp
+
+extern "C" {
+
+size_t causal_product_qk_rope_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t N,
+                                             int64_t D, cp_dtype_t dtype) {
+  cp::QkRope f{};
+  f.B = B; f.Hq = Hq; f.Hk = Hk; f.N = N; f.D = D; f.dtype = dtype;
+  if (cp::check_qk_rope(f, CP_QK_NORM_RMS) != CP_OK) return 0;
+  return cp::kStatusBytes + cp::round_up(cp::qk_rope_scratch(f));
+}
+
+cp_status_t causal_product_qk_rope(const void* xq, const int64_t* stride_q, const void* xk,
+                                   const int64_t* stride_k, const void* wq, const void* wk,
+                                   const float* cos, const float* sin, int64_t cs_batch, void* q,
+                                   void* k, cp_qk_norm_t norm, float eps, int64_t B, int64_t Hq,
+                                   int64_t Hk, int64_t N, int64_t D, int64_t R, cp_dtype_t dtype,
+                                   void* stream) {
+  cp::QkRope f{};
+  f.xq = xq; f.xk = xk; f.wq = wq; f.wk = wk; f.yq = q; f.yk = k; f.cos = cos; f.sin = sin;
+  f.cs_batch = cs_batch; f.B = B; f.Hq = Hq; f.Hk = Hk; f.N = N; f.D = D; f.R = R;
+  f.rms = norm == CP_QK_NORM_RMS; f.eps = eps; f.dtype = dtype;
+  const cp_status_t st = cp::check_qk_rope(f, norm);
+  if (st != CP_OK) return st;
+  if (!stride_q || !stride_k) return CP_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (stride_q[i] < 0 || stride_k[i] < 0) return CP_ERR_INVALID_ARG;
+    f.stride_q[i] = stride_q[i];
+    f.stride_k[i] = stride_k[i];
+  }
+  if (N > 0 && (!xq || !xk || !q || !k || (R > 0 && (!cos || !sin)))) return CP_ERR_INVALID_ARG;
+  const size_t es = dtype == CP_DTYPE_F32 ? 4 : 2, ncs = (size_t)N * (R / 2) * sizeof(float);
+  const size_t ncs_all = ncs + (size_t)(B - 1) * cs_batch * sizeof(float);
+  const cp::Span in[6] = {{xq, cp::strided_bytes(stride_q, B, Hq, N, D, es)},
+                          {xk, cp::strided_bytes(stride_k, B, Hk, N, D, es)},
+                          {wq, D * es}, {wk, D * es}, {cos, ncs_all}, {sin, ncs_all}};
+  const cp::Span outs[2] = {{q, (size_t)B * Hq * N * D * es}, {k, (size_t)B * Hk * N * D * es}};
+  const size_t mask = es - 1;
+  for (const void* p : {xq, xk, wq, wk})
+    if ((reinterpret_cast<uintptr_t>(p) & mask) != 0) return CP_ERR_MISALIGNED;
+  if (!cp::all_aligned(outs) || !cp::aligned4(cos) || !cp::aligned4(sin)) return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  if (N == 0) return CP_OK;
+  return cp::qk_rope_launch(f, nullptr, false, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* stride_q, const void* xk,
+                                       const int64_t* stride_k, const void* wq, const void* wk,
+                                       const float* cos, const float* sin, int64_t cs_batch,
+                                       const void* grad_q, const void* grad_k, void* grad_xq,
+                                       void* grad_xk, void* grad_wq, void* grad_wk,
+                                       cp_qk_norm_t norm, float eps, int64_t B, int64_t Hq,
+                                       int64_t Hk, int64_t N, int64_t D, int64_t R,
+                                       cp_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                       void* stream_) {
+  cp::QkRope f{};
+  f.xq = xq; f.xk = xk; f.wq = wq; f.wk = wk; f.gq = grad_q; f.gk = grad_k;
+  f.yq = grad_xq; f.yk = grad_xk; f.dwq = grad_wq; f.dwk = grad_wk; f.cos = cos; f.sin = sin;
+  f.cs_batch = cs_batch; f.B = B; f.Hq = Hq; f.Hk = Hk; f.N = N; f.D = D; f.R = R;
+  f.rms = norm == CP_QK_NORM_RMS; f.eps = eps; f.dtype = dtype;
+  cp_status_t st = cp::check_qk_rope(f, norm);
+  if (st != CP_OK) return st;
+  if (!stride_q || !stride_k) return CP_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (stride_q[i] < 0 || stride_k[i] < 0) return CP_ERR_INVALID_ARG;
+    f.stride_q[i] = stride_q[i];
+    f.stride_k[i] = stride_k[i];
+  }
+  if (N > 0 && (!xq || !xk || !grad_q || !grad_k || !grad_xq || !grad_xk ||
+                (R > 0 && (!cos || !sin))))
+    return CP_ERR_INVALID_ARG;
+  if ((wq != nullptr) != (grad_wq != nullptr) || (wk != nullptr) != (grad_wk != nullptr))
+    return CP_ERR_INVALID_ARG;
+  const size_t es = dtype == CP_DTYPE_F32 ? 4 : 2, ncs = (size_t)N * (R / 2) * sizeof(float);
+  const size_t ncs_all = ncs + (size_t)(B - 1) * cs_batch * sizeof(float);
+  const size_t nq = (size_t)B * Hq * N * D * es, nk = (size_t)B * Hk * N * D * es;
+  const cp::Span in[8] = {{xq, cp::strided_bytes(stride_q, B, Hq, N, D, es)},
+                          {xk, cp::strided_bytes(stride_k, B, Hk, N, D, es)},
+                          {wq, D * es}, {wk, D * es}, {cos, ncs_all}, {sin, ncs_all},
+                          {grad_q, nq}, {grad_k, nk}};
+  const cp::Span outs[4] = {{grad_xq, nq}, {grad_xk, nk}, {grad_wq, D * es}, {grad_wk, D * es}};
+  const size_t mask = es - 1;
+  for (const void* p : {xq, xk, wq, wk, (const void*)grad_wq, (const void*)grad_wk})
+    if ((reinterpret_cast<uintptr_t>(p) & mask) != 0) return CP_ERR_MISALIGNED;
+  for (const void* p : {grad_q, grad_k, (const void*)grad_xq, (const void*)grad_xk})
+    if (!cp::aligned16(p)) return CP_ERR_MISALIGNED;
+  if (!cp::aligned4(cos) || !cp::aligned4(sin)) return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::kStatusBytes + cp::round_up(cp::qk_rope_scratch(f));
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) {
+    // no rows: the weights' gradients are sums of nothing
+    for (void* p : {grad_wq, grad_wk})
+      if (p != nullptr && cudaMemsetAsync(p, 0, D * es, stream) != cudaSuccess) return CP_ERR_CUDA;
+    return CP_OK;
+  }
+  cp::Scratch sc;
+  st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+  if (st != CP_OK) return st;
+  void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  return cp::qk_rope_launch(f, area, true, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

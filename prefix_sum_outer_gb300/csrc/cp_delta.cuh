@@ -1,0 +1,72 @@
+// Pieces shared by the gated delta rule's kernels.
+//
+// The rule, per head (S: D x M state, fp32):
+//     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = b_t (v_t - a_t S_{t-1}^T k_t),
+//     out_t = s S_t^T q_t,             a_t = e^{g_t}.
+// Over a chunk of C rows that starts from S, with G the running sum of g,
+// Gam_ij = e^{G_i - G_j} (j <= i), gam_i = e^{G_i}, del_j = e^{G_C - G_j}:
+//     A_ij = b_i Gam_ij k_i.k_j (j < i),     P_ij = s Gam_ij q_i.k_j (j <= i),
+//     R = V - gam K S,   U = (I + A)^-1 (b R),
+//     out = s gam Q S + P U,   S' = gam_C S + K^T (del U).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cp_internal.h"
+
+namespace cp {
+namespace delta {
+
+template <typename T>
+__device__ __forceinline__ float ld_f32(const T* p);
+template <>
+__device__ __forceinline__ float ld_f32<float>(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float ld_f32<__nv_bfloat16>(const __nv_bfloat16* p) {
+  return __bfloat162float(*p);
+}
+template <>
+__device__ __forceinline__ float ld_f32<__half>(const __half* p) { return __half2float(*p); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// A log decay as two parts whose running sums over a chunk stay exact to
+// fp32: a multiple of 1/16 (sums of up to 256 of them at |g| <= 120 are exact)
+// and the rest (|f| <= 1/32).  With one fp32 sum, a decay near e^-100 (a
+// cleared state) would leave every later difference G_i - G_j of its chunk
+// 1e-5 off.  Below -120 the decay is 0 in fp32, and -inf becomes finite, so
+// that differences of sums are never inf - inf.  NaN stays NaN.
+constexpr float kMinLogDecay = -120.f;
+__device__ __forceinline__ float2 split_decay(float g) {
+  g = g < kMinLogDecay ? kMinLogDecay : g;
+  const float c = rintf(g * 16.f) * 0.0625f;
+  return make_float2(c, g - c);
+}
+// e^{G_i - G_j} from the two-part running sums
+__device__ __forceinline__ float decay_between(float2 gi, float2 gj) {
+  return expf((gi.x - gj.x) + (gi.y - gj.y));
+}
+// inclusive running sums of one pair per lane over a warp
+__device__ __forceinline__ float2 warp_scan(float2 x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const float cx = __shfl_up_sync(0xffffffffu, x.x, o), cy = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) {
+      x.x += cx;
+      x.y += cy;
+    }
+  }
+  return x;
+}
+
+}  // namespace delta
+}  // namespace cp

@@ -237,6 +237,65 @@ cp_status_t favor_fused_fwd_launch(const void* xq, const void* xk, const void* v
                                    void* out, int64_t BH, int64_t N, int64_t R, int64_t D,
                                    int64_t M, float* agg, int* status, cudaStream_t stream);
 
+// ---- the gated delta rule: S_t = a_t S_{t-1} + k_t u_t^T, u_t = b_t (v_t -
+// a_t S_{t-1}^T k_t), out_t = scale S_t^T q_t, a_t = e^{g_t}.  q, k are
+// [B][Hk][N][D] (value head h reads key head h / (H / Hk)), v and out
+// [B][H][N][M], g and beta [B][H][N] fp32, states [B][H][D][M] fp32.
+struct DeltaShape {
+  int64_t B, H, Hk, N, D, M;
+  cp_dtype_t dtype;
+  float scale;
+};
+struct DeltaFwd {
+  const void *q, *k, *v;
+  const float *g, *beta, *state_in;  // state_in may be null (zero)
+  void* out;
+  float *state_out, *ckpt;           // may be null; ckpt: the state before every chunk
+};
+struct DeltaBwd {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const void* grad_out;
+  const float *ckpt, *grad_state_out;  // grad_state_out may be null (zero)
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *grad_state_in;   // grad_state_in may be null
+};
+struct DeltaDecode {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const int* slots;  // [B], or null: sequence b has state b
+  void* out;
+  float* state;      // [pool][H][D][M]
+  int64_t pool;
+};
+// CUDA-core path (any dtype); chunks of delta_simt_chunk() rows
+int delta_simt_chunk();
+size_t delta_simt_scratch(const DeltaShape& s, bool backward);
+cudaError_t delta_simt_fwd(const DeltaShape& s, const DeltaFwd& f, cudaStream_t stream);
+cudaError_t delta_simt_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch,
+                           cudaStream_t stream);
+// out[head][row] = the sum of fp32 parts [n_mb][heads][group][rows] over n_mb
+// and group, in that order
+cudaError_t delta_join_launch(const float* part, void* out, int64_t rows, int64_t heads, int group,
+                              int n_mb, cp_dtype_t dtype, cudaStream_t stream);
+cudaError_t delta_decode_launch(const DeltaShape& s, const DeltaDecode& f, cudaStream_t stream);
+
+// ---- per-head norm of queries and keys with the position rotation; forward:
+// yq, yk from xq, xk; backward: yq, yk receive dx from gq, gk (and xq, xk), dwq
+// and dwk (may be null) the weights' gradients, through qk_rope_scratch bytes
+struct QkRope {
+  const void *xq, *xk, *wq, *wk, *gq, *gk;  // weights may be null (ones)
+  void *yq, *yk, *dwq, *dwk;
+  const float *cos, *sin;
+  int64_t stride_q[3], stride_k[3];  // batch, head, row strides of xq, xk (elements)
+  int64_t cs_batch, B, Hq, Hk, N, D, R;
+  bool rms;
+  float eps;
+  cp_dtype_t dtype;
+};
+size_t qk_rope_scratch(const QkRope& f);
+cudaError_t qk_rope_launch(const QkRope& f, void* scratch, bool backward, cudaStream_t stream);
+
 // ---- failure-path self-test: records CP_ERR_TIMEOUT after `wait_ns`
 cudaError_t selftest_timeout_launch(int* status, uint64_t wait_ns, cudaStream_t stream);
 
