@@ -393,20 +393,23 @@ CP_API cp_status_t causal_product_bwd_favor(const void* xq, const void* xk, cons
  * g_t = -inf clears the state before token t (any g_t below -120 does, e^-120
  * being 0 in fp32); beta_t = 0 writes nothing, so a token with g = beta = 0 is
  * padding.  A NaN or inf among a head's inputs reaches that head's later
- * outputs.  Keys longer than 1 (beta |k|^2 > 2) can make the state grow without
+ * outputs, and may reach those of the same 64 rows.  Keys longer than 1 (beta |k|^2 > 2) can make the state grow without
  * bound; causal_product_qk_rope leaves them with the norm the rule wants.
  *
- * State, products and sums are fp32 (CUDA cores) for every dtype; results are
- * bitwise reproducible.
+ * State and sums are fp32.  bf16 with D <= 128 runs on the tensor cores, each
+ * computed factor of a product as the sum of two bf16 numbers (16 bits) or
+ * three; other shapes, fp32 and fp16 run on the CUDA cores in fp32.  Results
+ * are bitwise reproducible.
  *
- * Training: the forward writes the state before every chunk of rows into
+ * Training: the forward leaves what the backward needs of it (the states
+ * before its chunks of rows, and on the tensor cores the chunks' inverses) in
  * `ckpt` (causal_product_delta_checkpoint_size bytes; NULL: not kept), and the
  * backward, given the same inputs and that buffer, writes the gradients of
  *     L = <grad_out, out> + <grad_state_out, S_N>
  * (grad_state_out NULL: zero): grad_q, grad_k [B][Hk][N][D] (summed over the
  * value heads that share a key head), grad_v, grad_g and grad_beta (fp32), and
  * grad_state_in = dL/dS_0 (NULL: not written).  grad_g is 0 where g < -120.
- * S_0 is not an argument: the checkpoints begin with it.
+ * S_0 is not an argument: the checkpoints hold it.
  *
  * Workspace: causal_product_delta_workspace_size bytes, or NULL (allocated and
  * freed on `stream`).  Errors as causal_product_fwd; CP_ERR_INVALID_ARG too

@@ -23,8 +23,8 @@ LIB = os.path.join(BUILD, "libcausal_product.so")
 SOURCES = ["cp_api.cu", "cp_simt.cu", "cp_tc.cu", "cp_tc_dkdv.cu", "cp_decode.cu",
            "cp_selftest.cu", "cp_norm.cu", "cp_feature.cu", "cp_segscan.cu", "cp_favor.cu", "cp_favor_fwd.cu",
            "cp_tc_lookback.cu", "cp_norm_pp.cu", "cp_delta.cu", "cp_delta_decode.cu",
-           "cp_qk_rope.cu"]
-HEADERS = ["cp_internal.h", "cp_tc_common.cuh", "cp_tc_causal.cuh", "cp_tc_dkdv.cuh", "cp_delta.cuh",
+           "cp_delta_tc_fwd.cu", "cp_delta_tc_bwd.cu", "cp_qk_rope.cu"]
+HEADERS = ["cp_internal.h", "cp_tc_common.cuh", "cp_tc_causal.cuh", "cp_tc_dkdv.cuh", "cp_delta.cuh", "cp_delta_tc.cuh",
            "sm103_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

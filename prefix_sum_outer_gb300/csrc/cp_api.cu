@@ -1059,12 +1059,15 @@ cp_status_t check_delta(const DeltaShape& s) {
 }
 
 size_t delta_ckpt_bytes(const DeltaShape& s) {
+  if (delta_tc_supported(s)) return delta_tc_ckpt_bytes(s);
   const int64_t c = delta_simt_chunk();
   return (size_t)((s.N + c - 1) / c) * s.B * s.H * s.D * s.M * sizeof(float);
 }
 
 size_t delta_ws_bytes(const DeltaShape& s, bool backward) {
-  return kStatusBytes + round_up(s.N == 0 ? 0 : delta_simt_scratch(s, backward));
+  if (s.N == 0 || (delta_tc_supported(s) && !backward)) return kStatusBytes;
+  return kStatusBytes +
+         round_up(delta_tc_supported(s) ? delta_tc_scratch(s) : delta_simt_scratch(s, backward));
 }
 
 // Sizes in bytes of one call's tensors.
@@ -1147,6 +1150,12 @@ cp_status_t causal_product_fwd_delta(const void* q, const void* k, const void* v
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (N == 0) return cp::pass_state(state_in, state_out, n.state, stream);
   const cp::DeltaFwd f{q, k, v, g, beta, state_in, out, state_out, ckpt};
+  if (cp::delta_tc_supported(s)) {
+    cp::Scratch sc;
+    st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+    if (st != CP_OK) return st;
+    return cp::delta_tc_fwd(s, f, static_cast<int*>(sc.base), stream);
+  }
   return cp::delta_simt_fwd(s, f, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -1185,6 +1194,8 @@ cp_status_t causal_product_bwd_delta(const void* q, const void* k, const void* v
   const cp::DeltaBwd f{q,      k,      v,      g,      beta,   grad_out,  ckpt, grad_state_out,
                        grad_q, grad_k, grad_v, grad_g, grad_beta, grad_state_in};
   void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  if (cp::delta_tc_supported(s))
+    return cp::delta_tc_bwd(s, f, area, static_cast<int*>(sc.base), stream);
   return cp::delta_simt_bwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

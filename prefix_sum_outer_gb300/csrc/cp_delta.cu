@@ -1,5 +1,6 @@
-// The gated delta rule on the CUDA cores in fp32 (bf16 and fp16 widened on
-// load).  The formulas are in cp_delta.cuh.
+// The gated delta rule on the CUDA cores in fp32: the path of fp32 and fp16
+// inputs (widened on load) and of the bf16 shapes the tensor-core kernels do
+// not take (D > 128).  The formulas are in cp_delta.cuh.
 //
 // Forward: one CTA per (head, block of MB value columns) walks the sequence in
 // chunks of 32 rows with the D x MB state in shared memory; the value columns

@@ -1,0 +1,524 @@
+// The gated delta rule on the 5th-generation tensor cores: what its forward
+// and backward kernels share (formulas in cp_delta.cuh).
+//
+// Every contraction is a tcgen05.mma with bf16 operands in shared memory and
+// an fp32 accumulator of 128 lanes in tensor memory.  q, k, v and the output's
+// gradient are bf16 as they come; what is computed (S, R, U, P, the inverse) is
+// fp32 and enters a product as hi + lo, two bf16 numbers that keep 16 bits of
+// it, so a product of two such factors is four MMAs and of one with an input
+// two.  One bf16 number per factor would do
+// for bf16 outputs, but leaves 2^-9 in the carried state and in the gradients
+// of the gates, which are fp32.
+//
+// An operand tile is 64 columns wide (128 bytes, 128-byte swizzle), so it can
+// enter as [rows x K] or transposed, by its descriptor alone.
+#pragma once
+#include "cp_delta.cuh"
+#include "cp_tc_common.cuh"
+
+namespace cp {
+namespace delta {
+
+using namespace cp::ptx;
+
+constexpr int kCh = 64;               // rows of a chunk
+constexpr int kBox = kCh * 128;       // bytes of a [64 x 64] bf16 tile
+constexpr uint32_t kDescHi = desc_hi(1024);
+
+// The gates of a chunk.  Every decay between two rows is a product of the a =
+// e^g between them, never a difference of sums: a cleared state's zero stays
+// an exact zero, 64 factors cost 64 roundings (4e-6 at worst), and a product
+// takes one instruction where an exponential of a difference takes eight.
+// Pieces are 16 rows.
+struct GateSlot {
+  float a[kCh + 4];                   // e^g (past the end: read, not used)
+  float b[kCh];
+  float gam[kCh], del[kCh];           // products of a up to row i, after row j
+  float e[kCh];                       // product of a after row j, in its piece
+  float half[32];                     // product of a from row 32 to row 32 + i
+  float piece[4];                     // product of a over a piece
+};
+
+// One warp: the slot from the lane's two rows' (lane, lane + 32) log decays and
+// strengths.
+__device__ __forceinline__ void write_gates(GateSlot* s, int lane, float g0, float g1, float b0,
+                                            float b1) {
+  const unsigned all = 0xffffffffu;
+  float a[2] = {expf(g0), expf(g1)}, pre[2], suf[2], tot[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x = a[h], y = a[h];
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2) {
+      const float u = __shfl_up_sync(all, x, o, 16), d = __shfl_down_sync(all, y, o, 16);
+      if (lane % 16 >= o) x *= u;
+      if (lane % 16 + o < 16) y *= d;
+    }
+    pre[h] = x;
+    const float d = __shfl_down_sync(all, y, 1, 16);
+    suf[h] = lane % 16 == 15 ? 1.f : d;
+    tot[2 * h] = __shfl_sync(all, x, 15);
+    tot[2 * h + 1] = __shfl_sync(all, x, 31);
+  }
+  const bool up = lane >= 16;
+  s->a[lane] = a[0];
+  s->a[lane + 32] = a[1];
+  s->b[lane] = b0;
+  s->b[lane + 32] = b1;
+  s->gam[lane] = up ? tot[0] * pre[0] : pre[0];
+  const float half = up ? tot[2] * pre[1] : pre[1];
+  s->half[lane] = half;
+  s->gam[lane + 32] = (tot[0] * tot[1]) * half;
+  s->del[lane] = (up ? suf[0] : suf[0] * tot[1]) * (tot[2] * tot[3]);
+  s->del[lane + 32] = up ? suf[1] : suf[1] * tot[3];
+  s->e[lane] = suf[0];
+  s->e[lane + 32] = suf[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane == i) s->piece[i] = tot[i];
+}
+
+// pairs of fp32 in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "sub.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// x = hi + lo in bf16; each packed as pairs
+__device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = tc::pack_bf16x2(x.x, x.y);
+  const float2 d =
+      sub2(x, make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+  lo = tc::pack_bf16x2(d.x, d.y);
+}
+
+__device__ __forceinline__ void split16(const float2 (&x)[8], uint4 (&hi)[2], uint4 (&lo)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    split_pair(x[4 * i], hi[i].x, lo[i].x);
+    split_pair(x[4 * i + 1], hi[i].y, lo[i].y);
+    split_pair(x[4 * i + 2], hi[i].z, lo[i].z);
+    split_pair(x[4 * i + 3], hi[i].w, lo[i].w);
+  }
+}
+// x as three bf16 numbers (all of fp32's bits)
+__device__ __forceinline__ void split_pair3(float2 x, uint32_t& a, uint32_t& b, uint32_t& c) {
+  a = tc::pack_bf16x2(x.x, x.y);
+  const float2 d = sub2(x, make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)));
+  split_pair(d, b, c);
+}
+__device__ __forceinline__ void split16_3(const float2 (&x)[8], uint4 (&a)[2], uint4 (&b)[2],
+                                          uint4 (&c)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    split_pair3(x[4 * i], a[i].x, b[i].x, c[i].x);
+    split_pair3(x[4 * i + 1], a[i].y, b[i].y, c[i].y);
+    split_pair3(x[4 * i + 2], a[i].z, b[i].z, c[i].z);
+    split_pair3(x[4 * i + 3], a[i].w, b[i].w, c[i].w);
+  }
+}
+// columns [8 ch, 8 ch + 16) of row `row` of a 64-column tile
+__device__ __forceinline__ void put16(uint8_t* tile, int row, int ch, const uint4 (&v)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4*>(tile + row * 128 + (((ch + i) ^ (row & 7)) << 4)) = v[i];
+}
+// 16 fp32 values into a tile's hi and lo parts
+__device__ __forceinline__ void store16_split(uint8_t* hi, uint8_t* lo, int row, int ch,
+                                              const float2 (&x)[8]) {
+  uint4 h[2], l[2];
+  split16(x, h, l);
+  put16(hi, row, ch, h);
+  put16(lo, row, ch, l);
+}
+// the same 16 columns to global memory, of which `nc` are inside the matrix
+__device__ __forceinline__ void write16(__nv_bfloat16* dst, int nc, const uint4 (&v)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (8 * i < nc) *reinterpret_cast<uint4*>(dst + 8 * i) = v[i];
+}
+
+// acc (128 lanes x 64 columns at tmem d) (+)= A B over K, with A and B at
+// shared addresses a, b and their tiles' K steps of 16.
+//   KA / KB: the operand's rows run along K (transposed use): a step is 16
+//   rows (2048 bytes); otherwise 16 columns (32 bytes), and every fourth step
+//   moves to the next 64-column tile, `box` bytes on.
+// lbo: distance of the second 64-lane block of a transposed A (or of the
+// second 64 columns of a transposed B).
+template <int STEPS, bool KA, bool KB>
+__device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t a_lbo, uint32_t b_lbo, uint32_t a_box,
+                                         uint32_t b_box, bool fresh) {
+  const uint32_t a_lo = desc_lo(a, a_lbo), b_lo = desc_lo(b, b_lbo);
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const uint32_t ao = KA ? k * 2048 : (k / 4) * a_box + (k % 4) * 32;
+    const uint32_t bo = KB ? k * 2048 : (k / 4) * b_box + (k % 4) * 32;
+    mma_ss_lo<kDescHi, kDescHi>(d, a_lo + (ao >> 4), b_lo + (bo >> 4), idesc,
+                                (fresh && k == 0) ? 0u : 1u);
+  }
+}
+
+// Wait; a wait that gives up records the timeout and sets the CTA's abort
+// flag, after which every other wait of the CTA gives up at once and no more
+// work is issued: the CTA runs to its end on whatever it holds.
+// The polling is out of line: these kernels' instruction stream is long and
+// mostly straight, and its fetch is the first stall when it grows (with the
+// loops below unrolled, 118 KB, a third of all stalls).
+static __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, int* status,
+                                              volatile int* abort_flag) {
+  if (!mbar_wait(bar, parity, abort_flag)) tc::record_timeout(status, abort_flag);
+}
+__device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, int* status,
+                                              volatile int* abort_flag) {
+  if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, status, abort_flag);
+}
+
+// 16 consecutive 32-bit columns of the warp's lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 16 columns of a product whose second factor entered as [hi | lo], 64 columns
+// each: the two accumulators' sum
+__device__ __forceinline__ void load16_sum(uint32_t taddr, float2 (&x)[8]) {
+  uint32_t h[16], l[16];
+  tmem_ld16(taddr, h);
+  tmem_ld16(taddr + 64, l);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = add2(make_float2(__uint_as_float(h[2 * i]), __uint_as_float(h[2 * i + 1])),
+                make_float2(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])));
+}
+
+// ------------------------------------------------ the inverse of I + A
+// T = (I + A)^-1 for a 64 x 64 strictly lower triangular A, by four warps, warp
+// a the columns of block a (16 columns).  The four diagonal blocks are inverted
+// by substitution, a lane to a column; the blocks below follow from
+//     X_ba = -X_bb sum_{a <= c < b} A_bc X_ca,
+// transposed (Z_ab = X_ba^T = -(sum_c Z_ac A_bc^T) X_bb^T) so that a result
+// tile is the next product's left factor without leaving its registers.  These
+// are 16 x 16 products of a few hundred cycles' latency in all: mma.sync, each
+// factor as hi + lo; a tcgen05 product's way through tensor memory costs more
+// than the product.  Blockwise substitution keeps the inverse to about the
+// factors' precision whatever A is; the doubling product (I - A)(I + A^2) ..
+// loses everything to cancellation when keys repeat.
+constexpr int kDiagPitch = 16 * 16 + 16;   // floats between diagonal blocks
+struct InvTiles {
+  // diagonal blocks of A, fp32, transposed: [block][column l][row i]; then,
+  // in its place, the block's inverse, transposed, bf16, hi then lo
+  float diag[4 * kDiagPitch];
+  // blocks below the diagonal, bf16, row major, at index b (b - 1) / 2 + c for
+  // block (b, c), in three parts: two would leave 2^-18 of A, which repeated
+  // keys at full strength multiply by ten in the solution
+  __nv_bfloat16 low[6][3][16 * 16];
+  __device__ __forceinline__ __nv_bfloat16* xt(int b, int part) {
+    return reinterpret_cast<__nv_bfloat16*>(diag + b * kDiagPitch) + part * 256;
+  }
+};
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// Block column c (16 columns) of row i of A, into the tiles.
+__device__ __forceinline__ void put_a16(InvTiles* it, int i, int c, const float2 (&v)[8]) {
+  const int b = i / 16;
+  if (c == b) {
+    float* d = it->diag + b * kDiagPitch + i % 16;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      d[32 * x] = v[x].x;
+      d[32 * x + 16] = v[x].y;
+    }
+  } else if (c < b) {
+    const int idx = b * (b - 1) / 2 + c;
+    uint4 part[3][2];
+    split16_3(v, part[0], part[1], part[2]);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      uint4* to = reinterpret_cast<uint4*>(it->low[idx][x] + (i % 16) * 16);
+      to[0] = part[x][0];
+      to[1] = part[x][1];
+    }
+  }
+}
+
+// Warp b: the inverse of diagonal block b; lane l: column l % 16 in x, which
+// also goes to xt (lanes 0-15 the hi part, 16-31 the lo part).
+__device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, float (&x)[16]) {
+  const int c = lane & 15;
+  const float* d = it->diag + b * kDiagPitch;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
+#pragma unroll
+  for (int l = 0; l < 15; ++l) {
+#pragma unroll
+    for (int i = (l + 1) / 4 * 4; i < 16; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(d + 16 * l + i);
+      if (i > l) x[i] = fmaf(-a.x, x[l], x[i]);
+      if (i + 1 > l) x[i + 1] = fmaf(-a.y, x[l], x[i + 1]);
+      if (i + 2 > l) x[i + 2] = fmaf(-a.z, x[l], x[i + 2]);
+      if (i + 3 > l) x[i + 3] = fmaf(-a.w, x[l], x[i + 3]);
+    }
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h, l;
+    split_pair(make_float2(x[2 * i], x[2 * i + 1]), h, l);
+    w[i] = lane < 16 ? h : l;
+  }
+  __syncwarp();  // the block has been read by every lane
+  uint4* to = reinterpret_cast<uint4*>(it->xt(b, lane >> 4) + c * 16);
+  to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// d[n tile] += (a_hi + a_lo) (b_hi + b_lo), b fragments as {tile 0: k low, k
+// high, tile 1: k low, k high}
+__device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&a_hi)[4],
+                                          const uint32_t (&a_lo)[4], const uint32_t (&b_hi)[4],
+                                          const uint32_t (&b_lo)[4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    mma_16816(d[n], a_hi, b_hi[2 * n], b_hi[2 * n + 1]);
+    mma_16816(d[n], a_lo, b_hi[2 * n], b_hi[2 * n + 1]);
+    mma_16816(d[n], a_hi, b_lo[2 * n], b_lo[2 * n + 1]);
+    mma_16816(d[n], a_lo, b_lo[2 * n], b_lo[2 * n + 1]);
+  }
+}
+
+// Warp a: z[b - 1] = Z_ab = X_ba^T for b > a, as accumulator tiles: element
+// [n][e] is column (row of X) 16 b + 8 n + 2 (lane % 4) + e % 2, row (column of
+// X) 16 a + lane / 4 + 8 (e / 2).  After invert_diag and a barrier.
+__device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane,
+                                             float (&z)[3][2][4]) {
+  const int g = lane / 4, t = lane % 4;
+  uint32_t zh[3][4], zl[3][4];  // Z_ac as left factors, c = a, a + 1, a + 2
+  {
+    const uint32_t* h = reinterpret_cast<const uint32_t*>(it->xt(a, 0));
+    const uint32_t* l = reinterpret_cast<const uint32_t*>(it->xt(a, 1));
+    const int at[4] = {g * 8 + t, (g + 8) * 8 + t, g * 8 + t + 4, (g + 8) * 8 + t + 4};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      zh[0][i] = h[at[i]];
+      zl[0][i] = l[at[i]];
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < 4; ++s) {  // b = a + s
+    const int b = a + s;
+    if (b > 3) break;
+    float y[2][4] = {};
+#pragma unroll
+    for (int c = 0; c < s; ++c) {
+      const int idx = b * (b - 1) / 2 + a + c;
+      const uint32_t* h = reinterpret_cast<const uint32_t*>(it->low[idx][0]);
+      const uint32_t* l = reinterpret_cast<const uint32_t*>(it->low[idx][1]);
+      uint32_t bh[4], bl[4], b3[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int w = (8 * n + g) * 8 + 4 * k + t;
+          bh[2 * n + k] = h[w];
+          bl[2 * n + k] = l[w];
+          b3[2 * n + k] = l[128 + w];
+        }
+      mma_split(y, zh[c], zl[c], bh, bl);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) mma_16816(y[n], zh[c], b3[2 * n], b3[2 * n + 1]);
+    }
+    uint32_t yh[4], yl[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        split_pair(make_float2(-y[n][2 * r], -y[n][2 * r + 1]), yh[2 * n + r], yl[2 * n + r]);
+    // X_bb^T as a right factor: rows k of xt, transposed on load; lane -> row
+    // lane % 16, column half lane / 16
+    uint32_t bh[4], bl[4];
+    const uint32_t row = (uint32_t)((lane % 16) * 32 + (lane / 16) * 16);
+    ldmatrix_x4_trans(bh, smem_u32(it->xt(b, 0)) + row);
+    ldmatrix_x4_trans(bl, smem_u32(it->xt(b, 1)) + row);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[s - 1][n][e] = 0.f;
+    mma_split(z[s - 1], yh, yl, bh, bl);
+    if (s < 3) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          split_pair(make_float2(z[s - 1][n][2 * r], z[s - 1][n][2 * r + 1]), zh[s][2 * n + r],
+                     zl[s][2 * n + r]);
+    }
+  }
+}
+
+// Warp a's columns of the inverse X, as rows of the transposed tile (row j,
+// column i: element (i, j)): the diagonal block from x, those below from z.
+// Blocks above the diagonal are never written and must be zero.
+__device__ __forceinline__ void put_t_transposed(uint8_t* hi, uint8_t* lo, int a, int lane,
+                                                 const float (&x)[16], const float (&z)[3][2][4]) {
+  if (lane < 16) {
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+    store16_split(hi, lo, 16 * a + lane, 2 * a, v);
+  }
+  const int g = lane / 4, t = lane % 4;
+#pragma unroll
+  for (int s = 1; s < 4; ++s) {
+    if (a + s > 3) break;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int j = 16 * a + g + 8 * r, ch = 2 * (a + s) + n;
+        uint32_t h, l;
+        split_pair(make_float2(z[s - 1][n][2 * r], z[s - 1][n][2 * r + 1]), h, l);
+        const int off = j * 128 + ((ch ^ (j & 7)) << 4) + 4 * t;
+        *reinterpret_cast<uint32_t*>(hi + off) = h;
+        *reinterpret_cast<uint32_t*>(lo + off) = l;
+      }
+  }
+}
+
+// Row i of the chunk's k.k or q.k (lane of the accumulator at t_kk), weighted
+// by the decays: w times the product of a after row j up to row i, for j < i
+// (and for j = i, where it is w, with `diag`), 0 elsewhere; f(c, v) takes
+// columns 16 c .. 16 c + 15.  row32: the row's half of the chunk, uniform over
+// the warp.  From the row's own half the product runs down the columns; below
+// it, a piece's columns share a row factor.
+template <class F>
+__device__ __forceinline__ void decayed_row(uint32_t t_kk, const GateSlot* gs, int i, bool diag,
+                                            int row32, float w, F f) {
+  const int last = diag ? i : i - 1;
+  float p = w;
+#pragma unroll 1
+  for (int c = 2 * row32 + 1; c >= 0; --c) {
+    uint32_t r[16];
+    tmem_ld16(t_kk + 16 * c, r);
+    float2 v[8];
+    if (c >= 2 * row32) {
+      float a[17];
+#pragma unroll
+      for (int x = 0; x < 16; x += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(gs->a + 16 * c + x);
+        a[x] = t.x; a[x + 1] = t.y; a[x + 2] = t.z; a[x + 3] = t.w;
+      }
+      a[16] = gs->a[16 * c + 16];
+      float u[16];
+#pragma unroll
+      for (int x = 15; x >= 0; --x) {
+        if (16 * c + x < i) p *= a[x + 1];
+        u[x] = 16 * c + x <= last ? p : 0.f;
+      }
+      // on to the columns of the half below
+      if (c == 2 * row32) p *= a[0];
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        v[x].x = 16 * c + 2 * x <= last ? u[2 * x] * __uint_as_float(r[2 * x]) : 0.f;
+        v[x].y = 16 * c + 2 * x + 1 <= last ? u[2 * x + 1] * __uint_as_float(r[2 * x + 1]) : 0.f;
+      }
+    } else {
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 8; x += 2) {
+        const float4 t = *reinterpret_cast<const float4*>(gs->e + 16 * c + 2 * x);
+        v[x] = mul2(mul2(both(p), make_float2(t.x, t.y)),
+                    make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
+        v[x + 1] = mul2(mul2(both(p), make_float2(t.z, t.w)),
+                        make_float2(__uint_as_float(r[2 * x + 2]), __uint_as_float(r[2 * x + 3])));
+      }
+      p *= gs->piece[c];
+    }
+    f(c, v);
+  }
+}
+
+// one contiguous shared -> global copy (16-byte aligned, a multiple of 16)
+__device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),
+               "r"(smem_u32(smem_src)), "r"(bytes)
+               : "memory");
+}
+
+// What the forward keeps for the backward, all as bf16 hi and lo parts:
+//   S  [BH][chunks][2][D][M]  the state before every chunk
+//   U  [2][BH][N][M]          what every row wrote
+//   TP [BH][chunks] x 32 KB   the tiles of the inverse (transposed) and of P
+// With them neither of the backward's kernels recomputes the chunk's inverse.
+struct Saved {
+  int64_t n, s_bytes, u_bytes, tp_bytes;
+  Saved(const DeltaShape& s)
+      : n((s.N + kCh - 1) / kCh),
+        s_bytes(4 * s.B * s.H * n * s.D * s.M),
+        u_bytes((4 * s.B * s.H * s.N * s.M + 255) / 256 * 256),
+        tp_bytes(s.B * s.H * n * 4 * kBox) {}
+  int64_t bytes() const { return s_bytes + u_bytes + tp_bytes; }
+};
+
+// [heads][N][cols] bf16, boxes of 64 columns x `rows` rows, 128-byte swizzle
+inline bool make_chunk_map(CUtensorMap* m, const void* ptr, int64_t heads, int64_t N, int64_t cols,
+                           int rows = kCh) {
+  auto enc = tc::get_encode();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)N, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(N * cols * 2)};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace delta
+}  // namespace cp

@@ -250,7 +250,7 @@ struct DeltaFwd {
   const void *q, *k, *v;
   const float *g, *beta, *state_in;  // state_in may be null (zero)
   void* out;
-  float *state_out, *ckpt;           // may be null; ckpt: the state before every chunk
+  float *state_out, *ckpt;           // may be null; ckpt: what the backward needs
 };
 struct DeltaBwd {
   const void *q, *k, *v;
@@ -274,6 +274,13 @@ size_t delta_simt_scratch(const DeltaShape& s, bool backward);
 cudaError_t delta_simt_fwd(const DeltaShape& s, const DeltaFwd& f, cudaStream_t stream);
 cudaError_t delta_simt_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch,
                            cudaStream_t stream);
+// tensor-core path (bf16, D <= 128)
+bool delta_tc_supported(const DeltaShape& s);
+size_t delta_tc_ckpt_bytes(const DeltaShape& s);
+size_t delta_tc_scratch(const DeltaShape& s);  // of the backward
+cp_status_t delta_tc_fwd(const DeltaShape& s, const DeltaFwd& f, int* status, cudaStream_t stream);
+cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, int* status,
+                         cudaStream_t stream);
 // out[head][row] = the sum of fp32 parts [n_mb][heads][group][rows] over n_mb
 // and group, in that order
 cudaError_t delta_join_launch(const float* part, void* out, int64_t rows, int64_t heads, int group,
