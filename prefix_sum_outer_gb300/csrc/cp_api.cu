@@ -1065,9 +1065,10 @@ size_t delta_ckpt_bytes(const DeltaShape& s) {
 }
 
 size_t delta_ws_bytes(const DeltaShape& s, bool backward) {
-  if (s.N == 0 || (delta_tc_supported(s) && !backward)) return kStatusBytes;
-  return kStatusBytes +
-         round_up(delta_tc_supported(s) ? delta_tc_scratch(s) : delta_simt_scratch(s, backward));
+  if (s.N == 0) return kStatusBytes;
+  if (delta_tc_supported(s))
+    return kStatusBytes + round_up(backward ? delta_tc_scratch(s) : delta_tc_fwd_scratch(s));
+  return kStatusBytes + round_up(delta_simt_scratch(s, backward));
 }
 
 // Sizes in bytes of one call's tensors.
@@ -1154,7 +1155,8 @@ cp_status_t causal_product_fwd_delta(const void* q, const void* k, const void* v
     cp::Scratch sc;
     st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
     if (st != CP_OK) return st;
-    return cp::delta_tc_fwd(s, f, static_cast<int*>(sc.base), stream);
+    void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+    return cp::delta_tc_fwd(s, f, area, static_cast<int*>(sc.base), stream);
   }
   return cp::delta_simt_fwd(s, f, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }

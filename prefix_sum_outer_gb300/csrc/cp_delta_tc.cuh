@@ -44,38 +44,39 @@ struct GateSlot {
 __device__ __forceinline__ void write_gates(GateSlot* s, int lane, float g0, float g1, float b0,
                                             float b1) {
   const unsigned all = 0xffffffffu;
-  float a[2] = {expf(g0), expf(g1)}, pre[2], suf[2], tot[4];
-#pragma unroll
+  const bool up = lane >= 16;
+  float before = 1.f, suf0 = 0.f;  // of the first half: its product, and that after the row
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    float x = a[h], y = a[h];
+    // (2^-22 of a, and 2^-24 of g: as 64 roundings)
+    const float a = __expf(h ? g1 : g0);
+    float x = a, y = a;
 #pragma unroll
     for (int o = 1; o < 16; o *= 2) {
       const float u = __shfl_up_sync(all, x, o, 16), d = __shfl_down_sync(all, y, o, 16);
       if (lane % 16 >= o) x *= u;
       if (lane % 16 + o < 16) y *= d;
     }
-    pre[h] = x;
     const float d = __shfl_down_sync(all, y, 1, 16);
-    suf[h] = lane % 16 == 15 ? 1.f : d;
-    tot[2 * h] = __shfl_sync(all, x, 15);
-    tot[2 * h + 1] = __shfl_sync(all, x, 31);
+    const float suf = lane % 16 == 15 ? 1.f : d;
+    const float lo = __shfl_sync(all, x, 15), hi = __shfl_sync(all, x, 31);
+    const float half = up ? lo * x : x;
+    s->a[lane + 32 * h] = a;
+    s->b[lane + 32 * h] = h ? b1 : b0;
+    s->gam[lane + 32 * h] = before * half;
+    s->e[lane + 32 * h] = suf;
+    const float after = up ? suf : suf * hi;  // product after the row, in its half
+    if (lane == 0) s->piece[2 * h] = lo;
+    if (lane == 1) s->piece[2 * h + 1] = hi;
+    if (h == 0) {
+      before = lo * hi;
+      suf0 = after;
+    } else {
+      s->half[lane] = half;
+      s->del[lane] = suf0 * (lo * hi);
+      s->del[lane + 32] = after;
+    }
   }
-  const bool up = lane >= 16;
-  s->a[lane] = a[0];
-  s->a[lane + 32] = a[1];
-  s->b[lane] = b0;
-  s->b[lane + 32] = b1;
-  s->gam[lane] = up ? tot[0] * pre[0] : pre[0];
-  const float half = up ? tot[2] * pre[1] : pre[1];
-  s->half[lane] = half;
-  s->gam[lane + 32] = (tot[0] * tot[1]) * half;
-  s->del[lane] = (up ? suf[0] : suf[0] * tot[1]) * (tot[2] * tot[3]);
-  s->del[lane + 32] = up ? suf[1] : suf[1] * tot[3];
-  s->e[lane] = suf[0];
-  s->e[lane + 32] = suf[1];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane == i) s->piece[i] = tot[i];
 }
 
 // pairs of fp32 in one instruction
@@ -148,6 +149,24 @@ __device__ __forceinline__ void put16(uint8_t* tile, int row, int ch, const uint
   for (int i = 0; i < 2; ++i)
     *reinterpret_cast<uint4*>(tile + row * 128 + (((ch + i) ^ (row & 7)) << 4)) = v[i];
 }
+// the same columns of a tile of inputs, as fp32
+__device__ __forceinline__ void get16(const uint8_t* tile, int row, int ch, float2 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + row * 128 + (((ch + i) ^ (row & 7)) << 4));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[4 * i + e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void pack16(const float2 (&x)[8], uint4 (&w)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = make_uint4(tc::pack_bf16x2(x[4 * i].x, x[4 * i].y), tc::pack_bf16x2(x[4 * i + 1].x, x[4 * i + 1].y),
+                      tc::pack_bf16x2(x[4 * i + 2].x, x[4 * i + 2].y),
+                      tc::pack_bf16x2(x[4 * i + 3].x, x[4 * i + 3].y));
+}
 // 16 fp32 values into a tile's hi and lo parts
 __device__ __forceinline__ void store16_split(uint8_t* hi, uint8_t* lo, int row, int ch,
                                               const float2 (&x)[8]) {
@@ -163,30 +182,33 @@ __device__ __forceinline__ void write16(__nv_bfloat16* dst, int nc, const uint4 
     if (8 * i < nc) *reinterpret_cast<uint4*>(dst + 8 * i) = v[i];
 }
 
-// acc (128 lanes x 64 columns at tmem d) (+)= A B over K, with A and B at
-// shared addresses a, b and their tiles' K steps of 16.
+// acc (128 lanes at tmem d) (+)= A B over K, with A and B at shared addresses
+// a, b and their tiles' K steps of 16.  Run by a whole converged warp, issued by
+// its elected lane: with one thread in the branch every MMA took 125 cycles to
+// issue, its descriptors going from vector to uniform registers; so it takes 62.
 //   KA / KB: the operand's rows run along K (transposed use): a step is 16
 //   rows (2048 bytes); otherwise 16 columns (32 bytes), and every fourth step
 //   moves to the next 64-column tile, `box` bytes on.
 // lbo: distance of the second 64-lane block of a transposed A (or of the
 // second 64 columns of a transposed B).
 template <int STEPS, bool KA, bool KB>
-__device__ __forceinline__ void mma_tile(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                         uint32_t a_lbo, uint32_t b_lbo, uint32_t a_box,
-                                         uint32_t b_box, bool fresh) {
+__device__ __forceinline__ void mma_tile(uint32_t el, uint32_t d, uint32_t a, uint32_t b,
+                                         uint32_t idesc, uint32_t a_lbo, uint32_t b_lbo,
+                                         uint32_t a_box, uint32_t b_box, bool fresh) {
   const uint32_t a_lo = desc_lo(a, a_lbo), b_lo = desc_lo(b, b_lbo);
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
     const uint32_t ao = KA ? k * 2048 : (k / 4) * a_box + (k % 4) * 32;
     const uint32_t bo = KB ? k * 2048 : (k / 4) * b_box + (k % 4) * 32;
-    mma_ss_lo<kDescHi, kDescHi>(d, a_lo + (ao >> 4), b_lo + (bo >> 4), idesc,
-                                (fresh && k == 0) ? 0u : 1u);
+    mma_ss_lo_elect<kDescHi, kDescHi>(d, a_lo + (ao >> 4), b_lo + (bo >> 4), idesc,
+                                      (fresh && k == 0) ? 0u : 1u, el);
   }
 }
 
 // Wait; a wait that gives up records the timeout and sets the CTA's abort
-// flag, after which every other wait of the CTA gives up at once and no more
-// work is issued: the CTA runs to its end on whatever it holds.
+// flag, after which every other wait of the CTA gives up at once: the CTA runs
+// to its end on whatever it holds (every address stays the same), and its
+// results are undefined.
 // The polling is out of line: these kernels' instruction stream is long and
 // mostly straight, and its fetch is the first stall when it grows (with the
 // loops below unrolled, 118 KB, a third of all stalls).
@@ -199,6 +221,14 @@ __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, in
   if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, status, abort_flag);
 }
 
+// After an abort, a millisecond for the copies and MMAs in flight to land
+// before the CTA gives its memory back.
+static __device__ __noinline__ void linger() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) {
+  }
+}
+
 // 16 consecutive 32-bit columns of the warp's lanes
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -209,6 +239,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float2 (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(r[0].x), "f"(r[0].y), "f"(r[1].x), "f"(r[1].y), "f"(r[2].x), "f"(r[2].y), "f"(r[3].x),
+      "f"(r[3].y), "f"(r[4].x), "f"(r[4].y), "f"(r[5].x), "f"(r[5].y), "f"(r[6].x), "f"(r[6].y),
+      "f"(r[7].x), "f"(r[7].y)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&x)[8]) {
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
 // 16 columns of a product whose second factor entered as [hi | lo], 64 columns
@@ -287,10 +335,11 @@ __device__ __forceinline__ void put_a16(InvTiles* it, int i, int c, const float2
   }
 }
 
-// Warp b: the inverse of diagonal block b; lane l: column l % 16 in x, which
-// also goes to xt (lanes 0-15 the hi part, 16-31 the lo part).
-__device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, float (&x)[16]) {
+// Warp b: the inverse of diagonal block b, column l % 16 by lane l, to xt and
+// packed in w (lanes 0-15 the hi part, 16-31 the lo part).
+__device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, uint4 (&w)[2]) {
   const int c = lane & 15;
+  float x[16];
   const float* d = it->diag + b * kDiagPitch;
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
@@ -305,17 +354,19 @@ __device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, float
       if (i + 3 > l) x[i + 3] = fmaf(-a.w, x[l], x[i + 3]);
     }
   }
-  uint32_t w[8];
+  uint32_t p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t h, l;
     split_pair(make_float2(x[2 * i], x[2 * i + 1]), h, l);
-    w[i] = lane < 16 ? h : l;
+    p[i] = lane < 16 ? h : l;
   }
+  w[0] = make_uint4(p[0], p[1], p[2], p[3]);
+  w[1] = make_uint4(p[4], p[5], p[6], p[7]);
   __syncwarp();  // the block has been read by every lane
   uint4* to = reinterpret_cast<uint4*>(it->xt(b, lane >> 4) + c * 16);
-  to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  to[0] = w[0];
+  to[1] = w[1];
 }
 
 // d[n tile] += (a_hi + a_lo) (b_hi + b_lo), b fragments as {tile 0: k low, k
@@ -332,13 +383,12 @@ __device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&a_h
   }
 }
 
-// Warp a: z[b - 1] = Z_ab = X_ba^T for b > a, as accumulator tiles: element
-// [n][e] is column (row of X) 16 b + 8 n + 2 (lane % 4) + e % 2, row (column of
-// X) 16 a + lane / 4 + 8 (e / 2).  After invert_diag and a barrier.
-__device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane,
-                                             float (&z)[3][2][4]) {
+// Warp a: Z_ab = X_ba^T for b = a + s, packed in zh[s], zl[s]: word 2 n + r is
+// columns (rows of X) 16 b + 8 n + 2 (lane % 4) and the next, row (column of X)
+// 16 a + lane / 4 + 8 r.  After invert_diag and a barrier.
+__device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane, uint32_t (&zh)[4][4],
+                                             uint32_t (&zl)[4][4]) {
   const int g = lane / 4, t = lane % 4;
-  uint32_t zh[3][4], zl[3][4];  // Z_ac as left factors, c = a, a + 1, a + 2
   {
     const uint32_t* h = reinterpret_cast<const uint32_t*>(it->xt(a, 0));
     const uint32_t* l = reinterpret_cast<const uint32_t*>(it->xt(a, 1));
@@ -385,55 +435,48 @@ __device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane,
     const uint32_t row = (uint32_t)((lane % 16) * 32 + (lane / 16) * 16);
     ldmatrix_x4_trans(bh, smem_u32(it->xt(b, 0)) + row);
     ldmatrix_x4_trans(bl, smem_u32(it->xt(b, 1)) + row);
+    float z[2][4] = {};
+    mma_split(z, yh, yl, bh, bl);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[s - 1][n][e] = 0.f;
-    mma_split(z[s - 1], yh, yl, bh, bl);
-    if (s < 3) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          split_pair(make_float2(z[s - 1][n][2 * r], z[s - 1][n][2 * r + 1]), zh[s][2 * n + r],
-                     zl[s][2 * n + r]);
-    }
+      for (int r = 0; r < 2; ++r)
+        split_pair(make_float2(z[n][2 * r], z[n][2 * r + 1]), zh[s][2 * n + r], zl[s][2 * n + r]);
   }
 }
 
 // Warp a's columns of the inverse X, as rows of the transposed tile (row j,
-// column i: element (i, j)): the diagonal block from x, those below from z.
-// Blocks above the diagonal are never written and must be zero.
-__device__ __forceinline__ void put_t_transposed(uint8_t* hi, uint8_t* lo, int a, int lane,
-                                                 const float (&x)[16], const float (&z)[3][2][4]) {
-  if (lane < 16) {
-    float2 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
-    store16_split(hi, lo, 16 * a + lane, 2 * a, v);
-  }
-  const int g = lane / 4, t = lane % 4;
+// column i: element (i, j)), the parts `part` bytes apart: the diagonal block
+// from w, those below from zh, zl, those above zero.
+__device__ __forceinline__ void put_t_transposed(uint8_t* hi, int part, int a, int lane,
+                                                 const uint4 (&w)[2], const uint32_t (&zh)[4][4],
+                                                 const uint32_t (&zl)[4][4]) {
+  uint8_t* own = hi + (lane < 16 ? 0 : part);
+  put16(own, 16 * a + (lane & 15), 2 * a, w);
+  const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+#pragma unroll 1
+  for (int b = 0; b < a; ++b) put16(own, 16 * a + (lane & 15), 2 * b, zero);
+  const int g = lane / 4;
+  uint8_t* row = hi + (16 * a + g) * 128 + 4 * (lane % 4);
 #pragma unroll
   for (int s = 1; s < 4; ++s) {
     if (a + s > 3) break;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2; ++n) {
+      uint8_t* to = row + (((2 * (a + s) + n) ^ g) << 4);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int j = 16 * a + g + 8 * r, ch = 2 * (a + s) + n;
-        uint32_t h, l;
-        split_pair(make_float2(z[s - 1][n][2 * r], z[s - 1][n][2 * r + 1]), h, l);
-        const int off = j * 128 + ((ch ^ (j & 7)) << 4) + 4 * t;
-        *reinterpret_cast<uint32_t*>(hi + off) = h;
-        *reinterpret_cast<uint32_t*>(lo + off) = l;
+        *reinterpret_cast<uint32_t*>(to + 1024 * r) = zh[s][2 * n + r];
+        *reinterpret_cast<uint32_t*>(to + 1024 * r + part) = zl[s][2 * n + r];
       }
+    }
   }
 }
 
 // Row i of the chunk's k.k or q.k (lane of the accumulator at t_kk), weighted
 // by the decays: w times the product of a after row j up to row i, for j < i
-// (and for j = i, where it is w, with `diag`), 0 elsewhere; f(c, v) takes
-// columns 16 c .. 16 c + 15.  row32: the row's half of the chunk, uniform over
+// (and for j = i, where it is w, with `diag`), 0 elsewhere, last columns first;
+// f(c, v) takes columns 16 c .. 16 c + 15.  row32: the row's half of the chunk, uniform over
 // the warp.  From the row's own half the product runs down the columns; below
 // it, a piece's columns share a row factor.
 template <class F>
@@ -442,11 +485,15 @@ __device__ __forceinline__ void decayed_row(uint32_t t_kk, const GateSlot* gs, i
   const int last = diag ? i : i - 1;
   float p = w;
 #pragma unroll 1
-  for (int c = 2 * row32 + 1; c >= 0; --c) {
+  for (int c = 3; c >= 0; --c) {
     uint32_t r[16];
     tmem_ld16(t_kk + 16 * c, r);
     float2 v[8];
-    if (c >= 2 * row32) {
+    if (c >= 2 * row32 + 2) {
+      tmem_ld_wait();
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = both(0.f);
+    } else if (c >= 2 * row32) {
       float a[17];
 #pragma unroll
       for (int x = 0; x < 16; x += 4) {
@@ -494,16 +541,17 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uin
 // What the forward keeps for the backward, all as bf16 hi and lo parts:
 //   S  [BH][chunks][2][D][M]  the state before every chunk
 //   U  [2][BH][N][M]          what every row wrote
-//   TP [BH][chunks] x 32 KB   the tiles of the inverse (transposed) and of P
-// With them neither of the backward's kernels recomputes the chunk's inverse.
+//   T  [BH][chunks] x 16 KB   the tile of the inverse (transposed)
+//   P  [BH][chunks] x 16 KB   the tile of P
+// With them neither of the backward's kernels recomputes a chunk's inverse.
 struct Saved {
-  int64_t n, s_bytes, u_bytes, tp_bytes;
+  int64_t n, s_bytes, u_bytes, t_bytes;  // t_bytes: of T, and of P
   Saved(const DeltaShape& s)
       : n((s.N + kCh - 1) / kCh),
         s_bytes(4 * s.B * s.H * n * s.D * s.M),
         u_bytes((4 * s.B * s.H * s.N * s.M + 255) / 256 * 256),
-        tp_bytes(s.B * s.H * n * 4 * kBox) {}
-  int64_t bytes() const { return s_bytes + u_bytes + tp_bytes; }
+        t_bytes(s.B * s.H * n * 2 * kBox) {}
+  int64_t bytes() const { return s_bytes + u_bytes + 2 * t_bytes; }
 };
 
 // [heads][N][cols] bf16, boxes of 64 columns x `rows` rows, 128-byte swizzle

@@ -4,16 +4,17 @@
 //
 // 1. The reverse chain, as sequential as the forward's and laid out like it: a
 //    CTA per head and 64 value columns, two warpgroups of 32 columns, lane d
-//    holding row d of the state's gradient dS'.  A chunk is
+//    holding row d of the state's gradient dS' in tensor memory.  A chunk is
 //        K dS'                          (lanes 0-63)
 //        dU = P^T dO + del K dS'         -> shared memory
-//        T^T dU                         -> dX;  dV = b dX
-//        [K; Q]^T [-gam b dX; s gam dO]  -> dS = gam_C dS' + it
-//    P^T dO of the next chunk is issued behind the last product and runs while
-//    the gradient is converted.  dU enters in three parts: P^T dO sums up to 64
-//    rows, of which T^T leaves the differences when keys repeat, so dU's
-//    rounding is the largest error of dX.  It leaves dX and the dS' of every chunk, split
-//    into hi and lo as it needs them itself.
+//        T^T dU                         -> dX
+//        [K; Q]^T [-gam b dX; s gam dO]  -> dS = gam_C dS' + it, -> shared memory
+//    P^T dO of the next chunk is issued behind the last product; while that
+//    one runs, dX is read out a second time for what the chain does not wait
+//    for (dX itself, dV = b dX, dX . V).  dU enters in three parts: P^T dO sums
+//    up to 64 rows, of which T^T leaves the differences when keys repeat, so
+//    dU's rounding is the largest error of dX.  It leaves dX and the dS' of
+//    every chunk as hi and lo parts.
 //
 // 2. The gradients, one CTA per head and chunk, all chunks at once: with every
 //    factor already in hi and lo parts in global memory, TMA puts them straight
@@ -39,14 +40,12 @@ using namespace delta;
 
 // ------------------------------------------------------------ reverse chain
 struct ChainArgs {
-  const __nv_bfloat16 *v, *go;
   const float *g, *beta, *grad_state_out;
-  const uint8_t* tp;
-  __nv_bfloat16 *dv, *ds, *dx;  // ds [BH][chunks][2][D][M], dx [2][BH][N][M]
+  const uint8_t *t, *pm;        // tiles of T and P
   float *xv, *grad_state_in;    // xv [M / 32 blocks][BH][N]: dX . V over the block
   int* status;
-  int64_t N, x_part;            // x_part: elements between dx's parts
-  int n_chunks, H, group, D, M;
+  int64_t N;
+  int n_chunks, BH, H, group, D, M;
   float scale;
 };
 
@@ -56,14 +55,16 @@ struct ChainLayout {
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
   static constexpr int kS = DP * 128;
-  static constexpr int NST = 2;
-  static constexpr int oT = NST * kKQ;         // hi, lo
+  static constexpr int oT = 2 * kKQ;           // hi, lo
   static constexpr int oP = oT + 2 * kBox;     // hi, lo
   static constexpr int oS = oP + 2 * kBox;     // hi, lo
   static constexpr int oB = oS + 2 * kS;       // [128 x 64]: dU, then -gam b dX; s gam dO; hi, lo
   static constexpr int oB3 = oB + 4 * kBox;    // [64 x 64]: dU's third part
   static constexpr int oO = oB3 + kBox;        // dO
-  static constexpr int oG = oO + kBox;
+  static constexpr int oV = oO + kBox;
+  static constexpr int oX = oV + kBox;         // dX: hi, lo
+  static constexpr int oDV = oX + 2 * kBox;
+  static constexpr int oG = oDV + kBox;
   static constexpr int oBar = oG + 2 * (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 128 + 1024;
   static_assert(kBytes <= tc::kSmemLimit, "shared memory");
@@ -72,196 +73,173 @@ struct ChainLayout {
 template <int DP>
 __global__ void __launch_bounds__(256, 1)
     delta_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_k, const ChainArgs a) {
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ CUtensorMap tm_do,
+                          const __grid_constant__ CUtensorMap tm_dv,
+                          const __grid_constant__ CUtensorMap tm_x,
+                          const __grid_constant__ CUtensorMap tm_ds, const ChainArgs a) {
   using L = ChainLayout<DP>;
-  constexpr int NST = L::NST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   GateSlot* gates = reinterpret_cast<GateSlot*>(sm + L::oG);
-  uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [NST]
-  uint64_t* t_full = kq_full + NST;
-  uint64_t* p_full = t_full + 1;
-  uint64_t* done = p_full + 1;  // [3]
+  uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [2]
+  uint64_t *t_full = kq_full + 2, *p_full = kq_full + 3, *v_full = kq_full + 4, *o_full = kq_full + 5;
+  uint64_t* done = kq_full + 6;  // [3]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sub = warp / 4, t = threadIdx.x % 128;
-  const bool issuer = threadIdx.x == 0;
-  const int64_t p = blockIdx.x;  // b * H + h
-  const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
-  const int n = a.n_chunks;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
+  const int lane = threadIdx.x % 32, sub = warp / 4, t = threadIdx.x % 128;
+  const int p = blockIdx.x;  // b * H + h
+  const int pk = (p / a.H) * (a.H / a.group) + (p % a.H) / a.group;
+  const int n = a.n_chunks, c64 = blockIdx.y * 64;
 
-  if (issuer) {
-    for (int i = 0; i < NST; ++i) mbar_init(kq_full + i, 1);
-    mbar_init(t_full, 1);
-    mbar_init(p_full, 1);
-    for (int i = 0; i < 3; ++i) mbar_init(done + i, 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 9; ++i) mbar_init(kq_full + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(tmem_holder, 256);
+    tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder, s_base = smem_u32(sm);
-  const uint32_t t_acc = tmem, t_e0 = tmem + 128;
-  const uint32_t lane_base = (uint32_t)(warp % 4) << 21;
-  const uint32_t t_mine = t_acc + lane_base + 32 * sub, t_e0_mine = t_e0 + lane_base + 32 * sub;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
+  const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 32 * sub;  // this thread's columns
+  // K dS', then dX; P^T dO, then dX's third accumulator; the update; dS
+  const uint32_t t_acc = tmem, t_e0 = tmem + 128, t_up = tmem + 192, t_s = tmem + 320;
   const uint32_t T_addr = s_base + L::oT, P_addr = s_base + L::oP, S_addr = s_base + L::oS;
   const uint32_t B_addr = s_base + L::oB, O_addr = s_base + L::oO;
   uint8_t *S_hi = sm + L::oS, *S_lo = S_hi + L::kS;
   uint8_t *B_hi = sm + L::oB, *B_lo = B_hi + 2 * kBox;
-  uint8_t* O = sm + L::oO;
   constexpr uint32_t id_nt128 = idesc_bf16_f32(128, 128, 0, 1);
   constexpr uint32_t id_nt192 = idesc_bf16_f32(128, 192, 0, 1);
   constexpr uint32_t id_tt64 = idesc_bf16_f32(128, 64, 1, 1);
   constexpr uint32_t id_tt128 = idesc_bf16_f32(128, 128, 1, 1);
-
-  const int c0 = blockIdx.y * 64 + 32 * sub;
-  const int nc = max(0, min(32, a.M - c0));
-  const bool row_on = t < a.D;
-  const int64_t at = p * a.N * a.M + c0;
-  const uint64_t keep = policy_evict_first();
+  const uint64_t once = policy_evict_first();
   // step s of the walk is chunk n - 1 - s
   auto load_kq = [&](int s) {
-    uint8_t* dst = sm + (s % NST) * L::kKQ;
-    mbar_arrive_expect_tx(kq_full + s % NST, L::kKQ);
+    uint64_t* bar = kq_full + (s & 1);
+    uint8_t* dst = sm + (s & 1) * L::kKQ;
+    mbar_arrive_expect_tx(bar, L::kKQ);
     for (int x = 0; x < L::kBoxes; ++x) {
-      tma_load_3d(dst + x * L::kKQBox, &tm_k, kq_full + s % NST, 64 * x, (n - 1 - s) * kCh, pk, keep);
-      tma_load_3d(dst + x * L::kKQBox + kBox, &tm_q, kq_full + s % NST, 64 * x, (n - 1 - s) * kCh,
-                  pk, keep);
+      tma_load_3d(dst + x * L::kKQBox, &tm_k, bar, 64 * x, (n - 1 - s) * kCh, pk, once);
+      tma_load_3d(dst + x * L::kKQBox + kBox, &tm_q, bar, 64 * x, (n - 1 - s) * kCh, pk, once);
     }
   };
-  auto tp_of = [&](int s) { return a.tp + (p * n + n - 1 - s) * (int64_t)(4 * kBox); };
-  auto load_t = [&](int s) {
-    mbar_arrive_expect_tx(t_full, 2 * kBox);
-    bulk_load(sm + L::oT, tp_of(s), 2 * kBox, t_full);
+  auto load_tile = [&](int at, const uint8_t* src, uint64_t* bar, int s) {
+    mbar_arrive_expect_tx(bar, 2 * kBox);
+    bulk_load(sm + at, src + ((int64_t)p * n + n - 1 - s) * (2 * kBox), 2 * kBox, bar);
   };
-  auto load_p = [&](int s) {
-    mbar_arrive_expect_tx(p_full, 2 * kBox);
-    bulk_load(sm + L::oP, tp_of(s) + 2 * kBox, 2 * kBox, p_full);
+  auto load_rows = [&](int at, const CUtensorMap* map, uint64_t* bar, int s) {
+    mbar_arrive_expect_tx(bar, kBox);
+    tma_load_3d(sm + at, map, bar, c64, (n - 1 - s) * kCh, p, once);
   };
-  // P^T dO of step s
-  auto issue_e0 = [&](int s) {
+  auto issue_e0 = [&](int s) {  // warp 0: P^T dO of step s
     wait_or_abort(p_full, s & 1, a.status, abort_flag);
-    if (*abort_flag) return;
-    mma_tile<4, true, true>(t_e0, P_addr, O_addr, id_tt64, kBox, 16, 0, 0, true);
-    mma_tile<4, true, true>(t_e0, P_addr + kBox, O_addr, id_tt64, kBox, 16, 0, 0, false);
+    wait_or_abort(o_full, s & 1, a.status, abort_flag);
+    __syncwarp();
+    const uint32_t el = elect_one();
+    mma_tile<4, true, true>(el, t_e0, P_addr, O_addr, id_tt64, kBox, 16, 0, 0, true);
+    mma_tile<4, true, true>(el, t_e0, P_addr + kBox, O_addr, id_tt64, kBox, 16, 0, 0, false);
   };
-  // lanes 0-63: a row of V; lanes 64-127: a row of dO; the thread's 32 columns
-  uint4 row[4];
-  auto load_rows = [&](int s) {
-    const int64_t i = (int64_t)(n - 1 - s) * kCh + (t & 63);
-    const __nv_bfloat16* src = (t < 64 ? a.v : a.go) + at + i * a.M;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      row[j] = make_uint4(0, 0, 0, 0);
-      if (i < a.N && 8 * j < nc) row[j] = *reinterpret_cast<const uint4*>(src + 8 * j);
-    }
-  };
-  auto put_do = [&]() {
-    put16(O, t - 64, 4 * sub, *reinterpret_cast<const uint4(*)[2]>(row));
-    put16(O, t - 64, 4 * sub + 2, *reinterpret_cast<const uint4(*)[2]>(row + 2));
-  };
-  // one warp writes the gates of step s
-  auto put_gates = [&](int s) {
+  // one warp: the gates, loaded a step before they are written
+  float4 gb;
+  auto load_gates = [&](int s) {
     const int64_t i = (int64_t)(n - 1 - s) * kCh + lane;
     const float* g = a.g + p * a.N;
     const float* b = a.beta + p * a.N;
-    write_gates(gates + s % 2, lane, i < a.N ? g[i] : 0.f, i + 32 < a.N ? g[i + 32] : 0.f,
-                i < a.N ? b[i] : 0.f, i + 32 < a.N ? b[i + 32] : 0.f);
+    gb = make_float4(i < a.N ? g[i] : 0.f, i + 32 < a.N ? g[i + 32] : 0.f, i < a.N ? b[i] : 0.f,
+                     i + 32 < a.N ? b[i + 32] : 0.f);
+  };
+  auto put_gates = [&](int s) {
+    write_gates(gates + (s & 1), lane, gb.x, gb.y, gb.z, gb.w);
+    if (s + 1 < n) load_gates(s + 1);
   };
 
-  if (issuer) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    for (int s = 0; s < min(n, NST); ++s) load_kq(s);
-    load_t(0);
-    load_p(0);
+  if (threadIdx.x == 96) {
+    load_kq(0);
+    load_tile(L::oP, a.pm, p_full, 0);
+    load_rows(L::oO, &tm_do, o_full, 0);
+    load_tile(L::oT, a.t, t_full, 0);
+    load_rows(L::oV, &tm_v, v_full, 0);
+    if (n > 1) load_kq(1);
   }
-  float2 dS[16];
-  {
-    const float* src = a.grad_state_out == nullptr ? nullptr
-                                                   : a.grad_state_out + (p * a.D + t) * a.M + c0;
+  const bool row_on = t < a.D;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int c0 = c64 + 32 * sub + 16 * h;
+    float2 s[8];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
+    for (int j = 0; j < 8; j += 2) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (src != nullptr && row_on && j < nc) v = *reinterpret_cast<const float4*>(src + j);
-      dS[j / 2] = make_float2(v.x, v.y);
-      dS[j / 2 + 1] = make_float2(v.z, v.w);
+      if (a.grad_state_out != nullptr && row_on && c0 + 2 * j < a.M)
+        v = *reinterpret_cast<const float4*>(a.grad_state_out + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j);
+      s[j] = make_float2(v.x, v.y);
+      s[j + 1] = make_float2(v.z, v.w);
     }
+    tmem_st16(t_s + lane_col + 16 * h, s);
+    if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, s);
   }
-  load_rows(0);
-  if (t >= 64) put_do();
-  if (warp == 3) put_gates(0);
-  fence_proxy_async_smem();
-  __syncthreads();
-  if (issuer) issue_e0(0);
+  tmem_st_wait();
+  if (warp == 7) {
+    load_gates(0);
+    put_gates(0);
+  }
+  if (warp == 0) issue_e0(0);
 
   for (int s = 0; s < n; ++s) {
-    const int st = s % NST;
-    const uint32_t kq = s_base + st * L::kKQ;
-    const GateSlot* gs = gates + s % 2;
-    const int64_t chunk = n - 1 - s;
-    if (t < DP) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 hi[2], lo[2];
-        split16(*reinterpret_cast<const float2(*)[8]>(dS + 8 * h), hi, lo);
-        put16(S_hi, t, 4 * sub + 2 * h, hi);
-        put16(S_lo, t, 4 * sub + 2 * h, lo);
-        if (row_on) {
-          __nv_bfloat16* to = a.ds + (((p * n + chunk) * 2) * a.D + t) * a.M + c0 + 16 * h;
-          write16(to, nc - 16 * h, hi);
-          write16(to + (int64_t)a.D * a.M, nc - 16 * h, lo);
-        }
-      }
-    }
+    const uint32_t kq = s_base + (s & 1) * L::kKQ, phase = s & 1;
+    const GateSlot* gs = gates + (s & 1);
+    const int chunk = n - 1 - s;
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (issuer) {
-      wait_or_abort(kq_full + st, (s / NST) & 1, a.status, abort_flag);
-      if (!*abort_flag) {
-        tc_fence_after();
-        mma_tile<DP / 16, false, true>(t_acc, kq, S_addr, id_nt128, 16, L::kS, L::kKQBox, 0, true);
-        mma_commit(done);
+    if (warp == 0) {
+      wait_or_abort(kq_full + (s & 1), (s >> 1) & 1, a.status, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t el = elect_one();
+      mma_tile<DP / 16, false, true>(el, t_acc, kq, S_addr, id_nt128, 16, L::kS, L::kKQBox, 0, true);
+      if (el) mma_commit(done);
+    }
+    if (threadIdx.x == 128) {
+      const int at = (p * n + chunk) * 2;
+      tma_store_3d(&tm_ds, S_hi, c64, 0, at);
+      tma_store_3d(&tm_ds, S_lo, c64, 0, at + 1);
+      if (s > 0) {  // the step before's dX and dV
+        tma_store_3d(&tm_x, sm + L::oX, c64, (chunk + 1) * kCh, p);
+        tma_store_3d(&tm_x, sm + L::oX + kBox, c64, (chunk + 1) * kCh, a.BH + p);
+        tma_store_3d(&tm_dv, sm + L::oDV, c64, (chunk + 1) * kCh, p);
       }
+      tma_store_commit();
     }
     if (t >= 64) {  // s gam dO, under the product
       const float2 w = both(a.scale * gs->gam[t - 64]);
-#pragma unroll
+      wait_or_abort(o_full, phase, a.status, abort_flag);
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float2 x[8];
+        get16(sm + L::oO, t - 64, 4 * sub + 2 * h, x);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 u4 = row[2 * h + j];
-          const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[4 * j + e] = mul2(w, make_float2(__uint_as_float(u[e] << 16),
-                                               __uint_as_float(u[e] & 0xffff0000u)));
-        }
+        for (int j = 0; j < 8; ++j) x[j] = mul2(w, x[j]);
         store16_split(B_hi, B_lo, t, 4 * sub + 2 * h, x);
       }
-      if (s + 1 < n) load_rows(s + 1);
     }
-    wait_or_abort(done, s & 1, a.status, abort_flag);
+    wait_or_abort(done, phase, a.status, abort_flag);
     tc_fence_after();
-    if (issuer && s + 1 < n && !*abort_flag) load_p(s + 1);  // P^T dO has read P
     if (t < 64) {
       const float2 del = both(gs->del[t]);
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t e0[16];
-        tmem_ld16(t_e0_mine + 16 * h, e0);
+        tmem_ld16(t_e0 + lane_col + 16 * h, e0);
         float2 r[8];
-        load16_sum(t_mine + 16 * h, r);
+        load16_sum(t_acc + lane_col + 16 * h, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           r[j] = fma2(del, r[j], make_float2(__uint_as_float(e0[2 * j]), __uint_as_float(e0[2 * j + 1])));
@@ -272,111 +250,132 @@ __global__ void __launch_bounds__(256, 1)
         put16(sm + L::oB3, t, 4 * sub + 2 * h, x2);
       }
     }
+    // the stores out of the S, dX and dV tiles have read them
+    if (threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (issuer) {
-      wait_or_abort(t_full, s & 1, a.status, abort_flag);
-      if (!*abort_flag) {
-        tc_fence_after();
-        // T^T hi with dU's three parts (the third's accumulator takes P^T dO's
-        // place, which has been read), T^T lo with two
-        mma_tile<4, false, true>(t_acc, T_addr, B_addr, id_nt192, 16, 2 * kBox, 0, 0, true);
-        mma_tile<4, false, true>(t_acc, T_addr + kBox, B_addr, id_nt128, 16, 2 * kBox, 0, 0, false);
-        mma_commit(done + 1);
-      }
+    if (warp == 0) {
+      wait_or_abort(t_full, phase, a.status, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t el = elect_one();
+      // T^T hi with dU's three parts (the third's accumulator takes P^T dO's
+      // place, which has been read), T^T lo with two
+      mma_tile<4, false, true>(el, t_acc, T_addr, B_addr, id_nt192, 16, 2 * kBox, 0, 0, true);
+      mma_tile<4, false, true>(el, t_acc, T_addr + kBox, B_addr, id_nt128, 16, 2 * kBox, 0, 0, false);
+      if (el) mma_commit(done + 1);
     }
-    if (t >= 64 && s + 1 < n) put_do();
-    if (warp == 3 && s + 1 < n) put_gates(s + 1);
-    wait_or_abort(done + 1, s & 1, a.status, abort_flag);
+    if (threadIdx.x == 96 && s + 1 < n) {  // P^T dO and s gam dO have read them
+      load_tile(L::oP, a.pm, p_full, s + 1);
+      load_rows(L::oO, &tm_do, o_full, s + 1);
+    }
+    if (warp == 7 && s + 1 < n) put_gates(s + 1);
+    wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
-    if (issuer && s + 1 < n && !*abort_flag) load_t(s + 1);
+    float2 r3[8];
+    const float2 w = both(t < 64 ? -gs->b[t] * gs->gam[t] : 0.f);
     if (t < 64) {
-      const int64_t i = chunk * kCh + t;
-      const float b = gs->b[t];
-      const float2 w = both(-b * gs->gam[t]);
-      float2 dot = both(0.f);
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        uint32_t r3[16];
-        tmem_ld16(t_e0_mine + 16 * h, r3);
         float2 r[8];
-        load16_sum(t_mine + 16 * h, r);
+        tmem_ld16(t_e0 + lane_col + 16 * h, r3);
+        load16_sum(t_acc + lane_col + 16 * h, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          r[j] = add2(r[j], make_float2(__uint_as_float(r3[2 * j]), __uint_as_float(r3[2 * j + 1])));
-        uint4 hi[2], lo[2], dv[2];
-        split16(r, hi, lo);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 u4 = row[2 * h + j];
-          const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dot = fma2(r[4 * j + e], make_float2(__uint_as_float(u[e] << 16),
-                                                 __uint_as_float(u[e] & 0xffff0000u)), dot);
-          dv[j].x = tc::pack_bf16x2(b * r[4 * j].x, b * r[4 * j].y);
-          dv[j].y = tc::pack_bf16x2(b * r[4 * j + 1].x, b * r[4 * j + 1].y);
-          dv[j].z = tc::pack_bf16x2(b * r[4 * j + 2].x, b * r[4 * j + 2].y);
-          dv[j].w = tc::pack_bf16x2(b * r[4 * j + 3].x, b * r[4 * j + 3].y);
-        }
-        if (i < a.N) {
-          __nv_bfloat16* to = a.dx + at + i * a.M + 16 * h;
-          write16(to, nc - 16 * h, hi);
-          write16(to + a.x_part, nc - 16 * h, lo);
-          write16(a.dv + at + i * a.M + 16 * h, nc - 16 * h, dv);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = mul2(w, r[j]);
+        for (int j = 0; j < 8; ++j) r[j] = mul2(w, add2(r[j], r3[j]));
         store16_split(B_hi, B_lo, t, 4 * sub + 2 * h, r);
       }
-      if (i < a.N && nc > 0)
-        a.xv[((int64_t)(c0 / 32) * gridDim.x + p) * a.N + i] = dot.x + dot.y;
-      if (s + 1 < n) load_rows(s + 1);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (issuer && !*abort_flag) {
+    if (warp == 0) {
       tc_fence_after();
+      const uint32_t el = elect_one();
       // [K; Q]^T: 128 rows along K; with one 64-column block the lanes past 64
       // read on into the tiles behind, and are not used
       constexpr uint32_t lbo = DP == 128 ? L::kKQBox : kBox;
-      mma_tile<8, true, true>(t_acc, kq, B_addr, id_tt128, lbo, 2 * kBox, 0, 0, true);
-      mma_commit(done + 2);
-      if (s + 1 < n) issue_e0(s + 1);
+      mma_tile<8, true, true>(el, t_up, kq, B_addr, id_tt128, lbo, 2 * kBox, 0, 0, true);
+      if (el) mma_commit(done + 2);
     }
-    wait_or_abort(done + 2, s & 1, a.status, abort_flag);
+    if (threadIdx.x == 96 && s + 1 < n) load_tile(L::oT, a.t, t_full, s + 1);
+    if (t < 64) {  // under the product
+      const int64_t i = (int64_t)chunk * kCh + t;
+      const float2 b = both(gs->b[t]);
+      float2 dot = both(0.f);
+      wait_or_abort(v_full, phase, a.status, abort_flag);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float2 r[8], v[8];
+        tmem_ld16(t_e0 + lane_col + 16 * h, r3);
+        load16_sum(t_acc + lane_col + 16 * h, r);
+        get16(sm + L::oV, t, 4 * sub + 2 * h, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          r[j] = add2(r[j], r3[j]);
+          dot = fma2(r[j], v[j], dot);
+        }
+        store16_split(sm + L::oX, sm + L::oX + kBox, t, 4 * sub + 2 * h, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = mul2(b, r[j]);
+        uint4 dv[2];
+        pack16(r, dv);
+        put16(sm + L::oDV, t, 4 * sub + 2 * h, dv);
+      }
+      if (i < a.N && c64 + 32 * sub < a.M)
+        a.xv[((int64_t)(c64 / 32 + sub) * a.BH + p) * a.N + i] = dot.x + dot.y;
+    }
+    tc_fence_before();
+    __syncthreads();  // dX has been read, and V
+    if (warp == 0 && s + 1 < n) {
+      tc_fence_after();
+      issue_e0(s + 1);
+    }
+    if (threadIdx.x == 96 && s + 1 < n) load_rows(L::oV, &tm_v, v_full, s + 1);
+    wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
-    if (issuer && s + NST < n && !*abort_flag) load_kq(s + NST);
+    if (threadIdx.x == 96 && s + 2 < n) load_kq(s + 2);
     const float2 last = both(gs->gam[kCh - 1]);
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
-      float2 r[8];
-      load16_sum(t_mine + 16 * h, r);
+      float2 r[8], x[8];
+      load16_sum(t_up + lane_col + 16 * h, r);
+      tmem_ld16(t_s + lane_col + 16 * h, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dS[8 * h + j] = fma2(last, dS[8 * h + j], r[j]);
+      for (int j = 0; j < 8; ++j) x[j] = fma2(last, x[j], r[j]);
+      tmem_st16(t_s + lane_col + 16 * h, x);
+      if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, x);
+    }
+    tmem_st_wait();
+  }
+  if (a.grad_state_in != nullptr) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int c0 = c64 + 32 * sub + 16 * h;
+      float2 s[8];
+      tmem_ld16(t_s + lane_col + 16 * h, s);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        if (row_on && c0 + 2 * j < a.M)
+          *reinterpret_cast<float4*>(a.grad_state_in + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j) =
+              make_float4(s[j].x, s[j].y, s[j + 1].x, s[j + 1].y);
     }
   }
-  if (a.grad_state_in != nullptr && row_on) {
-    float* dst = a.grad_state_in + (p * a.D + t) * a.M + c0;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4)
-      if (j < nc)
-        *reinterpret_cast<float4*>(dst + j) =
-            make_float4(dS[j / 2].x, dS[j / 2].y, dS[j / 2 + 1].x, dS[j / 2 + 1].y);
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 128) {  // the last step's (chunk 0) dX and dV
+    tma_store_3d(&tm_x, sm + L::oX, c64, 0, p);
+    tma_store_3d(&tm_x, sm + L::oX + kBox, c64, 0, a.BH + p);
+    tma_store_3d(&tm_dv, sm + L::oDV, c64, 0, p);
+    tma_store_commit();
+    tma_store_wait_all();
+    if (*abort_flag) linger();
   }
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag) {  // what is in flight lands before the memory goes
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 1000000ull) {
-    }
-  }
-  __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -478,8 +477,8 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int wg = warp / 4, t = threadIdx.x % 128;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
+  const int lane = threadIdx.x % 32, wg = warp / 4, t = threadIdx.x % 128;
   const bool issuer = threadIdx.x == 0;
   const int64_t p = blockIdx.x / a.n_chunks;
   const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder, s_base = smem_u32(sm);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
   const uint32_t t_kk = tmem, t_p2 = tmem + 64, t_in = tmem + 128, t_u = t_in + DP;
   const uint32_t lane_base = (uint32_t)(warp % 4) << 21;
   const uint32_t A_addr = s_base + L::oA, U_addr = s_base + L::oU, S_addr = s_base + L::oS;
@@ -538,27 +537,29 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       tma_load_3d(sm + x * L::kKQBox + kBox, &tm_q, kq_full, 64 * x, i0, pk, keep);
     }
     load_mb(0);
+  }
+  if (warp == 0) {
     wait_or_abort(kq_full, 0, a.status, abort_flag);
-    if (!*abort_flag)
-      mma_tile<DP / 16, false, false>(t_kk, s_base, s_base, id_nn64, 16, 16, L::kKQBox, L::kKQBox, true);
+    __syncwarp();
+    mma_tile<DP / 16, false, false>(elect_one(), t_kk, s_base, s_base, id_nn64, 16, 16, L::kKQBox, L::kKQBox, true);
   }
   float z = 0.f;  // <S, dS'>, this thread's share
   for (int m = 0; m < n_mb; ++m) {
-    if (issuer) {
+    if (warp == 0) {
       wait_or_abort(full, m & 1, a.status, abort_flag);
-      if (!*abort_flag) {
-        const bool fresh = m == 0;
+      __syncwarp();
+      const uint32_t el = elect_one();
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          // (A hi, B hi), (A lo, B hi), (A hi, B lo), (A lo, B lo)
-          const uint32_t ap = (x & 1) * 2 * kBox, up = (x & 1) * kBox, b = x >> 1;
-          mma_tile<4, false, false>(t_p2, A_addr + ap, U_addr + b * kBox, id_nn64, 16, 16, 0, 0, fresh && x == 0);
-          mma_tile<4, false, false>(t_in, A_addr + ap, S_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh && x == 0);
-          // lanes past 64 read on behind U and are not used
-          mma_tile<4, false, false>(t_u, U_addr + up, D_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh && x == 0);
-        }
-        mma_commit(done);
+      for (int x = 0; x < 4; ++x) {
+        // (A hi, B hi), (A lo, B hi), (A hi, B lo), (A lo, B lo)
+        const uint32_t ap = (x & 1) * 2 * kBox, up = (x & 1) * kBox, b = x >> 1;
+        const bool fresh = m == 0 && x == 0;
+        mma_tile<4, false, false>(el, t_p2, A_addr + ap, U_addr + b * kBox, id_nn64, 16, 16, 0, 0, fresh);
+        mma_tile<4, false, false>(el, t_in, A_addr + ap, S_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh);
+        // lanes past 64 read on behind U and are not used
+        mma_tile<4, false, false>(el, t_u, U_addr + up, D_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh);
       }
+      if (el) mma_commit(done);
     }
     wait_or_abort(full, m & 1, a.status, abort_flag);
     // the MMAs read the tiles at the same time
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     if (m + 1 < n_mb) {
       fence_proxy_async_smem();
       __syncthreads();  // every thread has read the tiles
-      if (issuer && !*abort_flag) load_mb(m + 1);
+      if (issuer) load_mb(m + 1);
     }
   }
   tc_fence_after();
@@ -675,15 +676,18 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   tc_fence_before();
   fence_proxy_async_smem();
   __syncthreads();
-  if (issuer && !*abort_flag) {
+  if (warp == 0) {
     tc_fence_after();
-    // [Ma; Mq] K
-    mma_tile<4, false, true>(t_in, A_addr, s_base, id_ntD, 16, L::kKQBox, 0, 0, true);
-    mma_tile<4, false, true>(t_in, A_addr + 2 * kBox, s_base, id_ntD, 16, L::kKQBox, 0, 0, false);
-    // Ma^T K + Mq^T Q; lanes past 64 read on and are not used
-    mma_tile<8, true, true>(t_u, A_addr, s_base, id_ttD, kBox, L::kKQBox, 0, 0, true);
-    mma_tile<8, true, true>(t_u, A_addr + 2 * kBox, s_base, id_ttD, kBox, L::kKQBox, 0, 0, false);
-    mma_commit(done + 1);
+    const uint32_t el = elect_one();
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {  // the tile's hi and lo parts
+      const uint32_t ap = A_addr + x * 2 * kBox;
+      // [Ma; Mq] K
+      mma_tile<4, false, true>(el, t_in, ap, s_base, id_ntD, 16, L::kKQBox, 0, 0, x == 0);
+      // Ma^T K + Mq^T Q; lanes past 64 read on and are not used
+      mma_tile<8, true, true>(el, t_u, ap, s_base, id_ttD, kBox, L::kKQBox, 0, 0, x == 0);
+    }
+    if (el) mma_commit(done + 1);
   }
   // under the products: dg_t's pairs, sum over rows i >= t of the row's columns
   // before t.  Running sums along the row first; column 32 wg + k of `part`
@@ -801,13 +805,8 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       if (live) write16(to, a.D - c, w);
     }
   }
+  if (*abort_flag) linger();
   tc_fence_before();
-  __syncthreads();
-  if (*abort_flag) {
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 1000000ull) {
-    }
-  }
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
@@ -818,20 +817,26 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
 // What the chain leaves for the gradients.
 struct Scratch {
   int64_t ds, dx, xv, part;  // bytes
-  explicit Scratch(const DeltaShape& s) {
+  uint8_t *ds_at, *dx_at, *xv_at, *part_at;
+  explicit Scratch(const DeltaShape& s, void* at = nullptr) {
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     const int64_t BH = s.B * s.H, n = (s.N + kCh - 1) / kCh;
     ds = up(4 * BH * n * s.D * s.M);
     dx = up(4 * BH * s.N * s.M);
     xv = up(4 * ((s.M + 31) / 32) * BH * s.N);
     part = s.H == s.Hk ? 0 : up(4 * BH * s.N * s.D);
+    ds_at = static_cast<uint8_t*>(at);
+    dx_at = ds_at + ds;
+    xv_at = dx_at + dx;
+    part_at = xv_at + xv;
   }
   int64_t bytes() const { return ds + dx + xv + 2 * part; }
 };
 
 template <int DP>
-cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const uint8_t* kept, const ChainArgs& c,
+cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const Scratch& w, const ChainArgs& c,
                    const GradArgs& g, cudaStream_t stream) {
+  const uint8_t* kept = reinterpret_cast<const uint8_t*>(f.ckpt);
   using LC = ChainLayout<DP>;
   using LG = GradLayout<DP>;
   auto chain = delta_tc_chain_kernel<DP>;
@@ -843,17 +848,18 @@ cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const uint8_t* kept, 
   // calls above see to that)
   const Saved k(s);
   const int64_t heads = s.B * s.H;
-  CUtensorMap m[7];
-  if (!make_chunk_map(&m[0], f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&m[1], f.k, s.B * s.Hk, s.N, s.D) ||
-      !make_chunk_map(&m[2], f.grad_out, heads, s.N, s.M) || !make_chunk_map(&m[3], c.dx, 2 * heads, s.N, s.M) ||
-      !make_chunk_map(&m[4], kept + k.s_bytes, 2 * heads, s.N, s.M) ||
-      !make_chunk_map(&m[5], kept, heads * k.n * 2, s.D, s.M, DP) ||
-      !make_chunk_map(&m[6], c.ds, heads * k.n * 2, s.D, s.M, DP))
+  CUtensorMap q, kk, v, go, dv, x, u, st, ds;
+  if (!make_chunk_map(&q, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&kk, f.k, s.B * s.Hk, s.N, s.D) ||
+      !make_chunk_map(&v, f.v, heads, s.N, s.M) || !make_chunk_map(&go, f.grad_out, heads, s.N, s.M) ||
+      !make_chunk_map(&dv, f.dv, heads, s.N, s.M) || !make_chunk_map(&x, w.dx_at, 2 * heads, s.N, s.M) ||
+      !make_chunk_map(&u, kept + k.s_bytes, 2 * heads, s.N, s.M) ||
+      !make_chunk_map(&st, kept, heads * k.n * 2, s.D, s.M, DP) ||
+      !make_chunk_map(&ds, w.ds_at, heads * k.n * 2, s.D, s.M, DP))
     return CP_ERR_CUDA;
   const unsigned BH = (unsigned)heads;
-  chain<<<dim3(BH, (unsigned)((s.M + 63) / 64)), 256, LC::kBytes, stream>>>(m[0], m[1], c);
+  chain<<<dim3(BH, (unsigned)((s.M + 63) / 64)), 256, LC::kBytes, stream>>>(q, kk, v, go, dv, x, ds, c);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
-  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], g);
+  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, go, x, u, st, ds, g);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -864,35 +870,29 @@ size_t delta_tc_scratch(const DeltaShape& s) { return (size_t)Scratch(s).bytes()
 cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, int* status,
                          cudaStream_t stream) {
   const Saved k(s);
-  const Scratch w(s);
-  const uint8_t* kept = reinterpret_cast<const uint8_t*>(f.ckpt);
-  uint8_t* at = static_cast<uint8_t*>(scratch);
+  const Scratch w(s, scratch);
   const int64_t BH = s.B * s.H;
   ChainArgs c{};
-  c.v = static_cast<const __nv_bfloat16*>(f.v);
-  c.go = static_cast<const __nv_bfloat16*>(f.grad_out);
   c.g = f.g; c.beta = f.beta; c.grad_state_out = f.grad_state_out;
-  c.tp = kept + k.s_bytes + k.u_bytes;
-  c.dv = static_cast<__nv_bfloat16*>(f.dv);
-  c.ds = reinterpret_cast<__nv_bfloat16*>(at);
-  c.dx = reinterpret_cast<__nv_bfloat16*>(at + w.ds);
-  c.xv = reinterpret_cast<float*>(at + w.ds + w.dx);
+  c.t = reinterpret_cast<const uint8_t*>(f.ckpt) + k.s_bytes + k.u_bytes;
+  c.pm = c.t + k.t_bytes;
+  c.xv = reinterpret_cast<float*>(w.xv_at);
   c.grad_state_in = f.grad_state_in;
   c.status = status;
-  c.N = s.N; c.x_part = BH * s.N * s.M; c.n_chunks = (int)k.n;
+  c.N = s.N; c.n_chunks = (int)k.n; c.BH = (int)BH;
   c.H = (int)s.H; c.group = (int)(s.H / s.Hk); c.D = (int)s.D; c.M = (int)s.M; c.scale = s.scale;
   GradArgs g{};
   g.g = f.g; g.beta = f.beta; g.xv = c.xv;
   g.dq = static_cast<__nv_bfloat16*>(f.dq);
   g.dk = static_cast<__nv_bfloat16*>(f.dk);
   if (w.part != 0) {
-    g.dq_part = reinterpret_cast<float*>(at + w.ds + w.dx + w.xv);
-    g.dk_part = reinterpret_cast<float*>(at + w.ds + w.dx + w.xv + w.part);
+    g.dq_part = reinterpret_cast<float*>(w.part_at);
+    g.dk_part = reinterpret_cast<float*>(w.part_at + w.part);
   }
   g.dg = f.dg; g.dbeta = f.dbeta; g.status = status;
   g.N = s.N; g.n_chunks = (int)k.n; g.BH = (int)BH; g.H = c.H; g.group = c.group; g.D = c.D;
   g.M = c.M; g.scale = s.scale;
-  cp_status_t st = s.D <= 64 ? launch<64>(s, f, kept, c, g, stream) : launch<128>(s, f, kept, c, g, stream);
+  cp_status_t st = s.D <= 64 ? launch<64>(s, f, w, c, g, stream) : launch<128>(s, f, w, c, g, stream);
   if (st != CP_OK || w.part == 0) return st;
   const int64_t heads = s.B * s.Hk;
   cudaError_t e = delta_join_launch(g.dq_part, f.dq, s.N * s.D, heads, c.group, 1, s.dtype, stream);

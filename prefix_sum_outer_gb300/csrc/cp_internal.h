@@ -278,7 +278,9 @@ cudaError_t delta_simt_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch
 bool delta_tc_supported(const DeltaShape& s);
 size_t delta_tc_ckpt_bytes(const DeltaShape& s);
 size_t delta_tc_scratch(const DeltaShape& s);  // of the backward
-cp_status_t delta_tc_fwd(const DeltaShape& s, const DeltaFwd& f, int* status, cudaStream_t stream);
+size_t delta_tc_fwd_scratch(const DeltaShape& s);
+cp_status_t delta_tc_fwd(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* status,
+                         cudaStream_t stream);
 cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, int* status,
                          cudaStream_t stream);
 // out[head][row] = the sum of fp32 parts [n_mb][heads][group][rows] over n_mb
