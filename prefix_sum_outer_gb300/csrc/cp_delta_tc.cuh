@@ -149,17 +149,6 @@ __device__ __forceinline__ void put16(uint8_t* tile, int row, int ch, const uint
   for (int i = 0; i < 2; ++i)
     *reinterpret_cast<uint4*>(tile + row * 128 + (((ch + i) ^ (row & 7)) << 4)) = v[i];
 }
-// the same columns of a tile of inputs, as fp32
-__device__ __forceinline__ void get16(const uint8_t* tile, int row, int ch, float2 (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(tile + row * 128 + (((ch + i) ^ (row & 7)) << 4));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[4 * i + e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-  }
-}
 __device__ __forceinline__ void pack16(const float2 (&x)[8], uint4 (&w)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -241,15 +230,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float2 (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "f"(r[0].x), "f"(r[0].y), "f"(r[1].x), "f"(r[1].y), "f"(r[2].x), "f"(r[2].y), "f"(r[3].x),
-      "f"(r[3].y), "f"(r[4].x), "f"(r[4].y), "f"(r[5].x), "f"(r[5].y), "f"(r[6].x), "f"(r[6].y),
-      "f"(r[7].x), "f"(r[7].y)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&x)[8]) {
   uint32_t r[16];
   tmem_ld16(taddr, r);
@@ -259,17 +239,63 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&x)[8]) {
     x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// 16 columns of a product whose second factor entered as [hi | lo], 64 columns
-// each: the two accumulators' sum
+// The chains run 32 value columns to a CTA, 16 to a thread: a factor's hi part
+// is columns 0-31 of its 64-column tile and its lo part columns 32-63, and one
+// MMA of 64 columns takes both.
+constexpr int kCB = 32;
+
+// 16 columns of such a product: the two accumulators' sum
 __device__ __forceinline__ void load16_sum(uint32_t taddr, float2 (&x)[8]) {
   uint32_t h[16], l[16];
   tmem_ld16(taddr, h);
-  tmem_ld16(taddr + 64, l);
+  tmem_ld16(taddr + kCB, l);
   tmem_ld_wait();
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     x[i] = add2(make_float2(__uint_as_float(h[2 * i]), __uint_as_float(h[2 * i + 1])),
                 make_float2(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])));
+}
+// .. and 16 fp32 values into such a tile, the thread's columns being 16 sub ..
+__device__ __forceinline__ void put_parts(uint8_t* tile, int row, int sub, const uint4 (&hi)[2],
+                                          const uint4 (&lo)[2]) {
+  put16(tile, row, 2 * sub, hi);
+  put16(tile, row, 4 + 2 * sub, lo);
+}
+__device__ __forceinline__ void store_parts(uint8_t* tile, int row, int sub, const float2 (&x)[8]) {
+  uint4 h[2], l[2];
+  split16(x, h, l);
+  put_parts(tile, row, sub, h, l);
+}
+// 16 columns of a row of inputs, of which nc are inside the matrix
+__device__ __forceinline__ void read16(const __nv_bfloat16* src, int nc, bool on, uint4 (&v)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v[i] = on && 8 * i < nc ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void unpack16(const uint4 (&v)[2], float2 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[4 * i + e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  }
+}
+// 16 columns of a row of fp32 (zero outside)
+__device__ __forceinline__ void read16(const float* src, int nc, bool on, float2 (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on && 2 * j < nc) v = *reinterpret_cast<const float4*>(src + 2 * j);
+    x[j] = make_float2(v.x, v.y);
+    x[j + 1] = make_float2(v.z, v.w);
+  }
+}
+__device__ __forceinline__ void write16(float* dst, int nc, const float2 (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2)
+    if (2 * j < nc)
+      *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(x[j].x, x[j].y, x[j + 1].x, x[j + 1].y);
 }
 
 // ------------------------------------------------ the inverse of I + A
@@ -538,30 +564,33 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uin
                : "memory");
 }
 
-// What the forward keeps for the backward, all as bf16 hi and lo parts:
-//   S  [BH][chunks][2][D][M]  the state before every chunk
-//   U  [2][BH][N][M]          what every row wrote
-//   T  [BH][chunks] x 16 KB   the tile of the inverse (transposed)
-//   P  [BH][chunks] x 16 KB   the tile of P
+// What the forward keeps for the backward: operand tiles, as they lie in shared
+// memory (fp32 values as hi and lo bf16 parts, swizzled), so that the
+// backward's copies bring them ready for the tensor cores:
+//   S  [BH][chunks][blocks of 32 columns]  the state before every chunk
+//   U  [BH][chunks][blocks of 32 columns]  what every row wrote
+//   T  [BH][chunks]                        the inverse (transposed), 16 KB
+//   P  [BH][chunks]                        16 KB
 // With them neither of the backward's kernels recomputes a chunk's inverse.
 struct Saved {
-  int64_t n, s_bytes, u_bytes, t_bytes;  // t_bytes: of T, and of P
+  int64_t n, blocks, s_tile, s_bytes, u_bytes, t_bytes;  // t_bytes: of T, and of P
   Saved(const DeltaShape& s)
       : n((s.N + kCh - 1) / kCh),
-        s_bytes(4 * s.B * s.H * n * s.D * s.M),
-        u_bytes((4 * s.B * s.H * s.N * s.M + 255) / 256 * 256),
+        blocks((s.M + kCB - 1) / kCB),
+        s_tile(s.D <= 64 ? 64 * 128 : 128 * 128),
+        s_bytes(s.B * s.H * n * blocks * s_tile),
+        u_bytes(s.B * s.H * n * blocks * kBox),
         t_bytes(s.B * s.H * n * 2 * kBox) {}
   int64_t bytes() const { return s_bytes + u_bytes + 2 * t_bytes; }
 };
 
-// [heads][N][cols] bf16, boxes of 64 columns x `rows` rows, 128-byte swizzle
-inline bool make_chunk_map(CUtensorMap* m, const void* ptr, int64_t heads, int64_t N, int64_t cols,
-                           int rows = kCh) {
+// [heads][N][cols] bf16, boxes of 64 columns x 64 rows, 128-byte swizzle
+inline bool make_chunk_map(CUtensorMap* m, const void* ptr, int64_t heads, int64_t N, int64_t cols) {
   auto enc = tc::get_encode();
   if (enc == nullptr) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)N, (cuuint64_t)heads};
   cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(N * cols * 2)};
-  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)kCh, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

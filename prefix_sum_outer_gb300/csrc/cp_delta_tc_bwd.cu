@@ -3,22 +3,20 @@
 // T = (I + A)^-1 and P).  Two launches:
 //
 // 1. The reverse chain, as sequential as the forward's and laid out like it: a
-//    CTA per head and 64 value columns, two warpgroups of 32 columns, lane d
-//    holding row d of the state's gradient dS' in tensor memory.  A chunk is
+//    CTA per head and 32 value columns, two warpgroups of 16 columns, lane d
+//    holding row d of the state's gradient dS' in registers.  A chunk is
 //        K dS'                          (lanes 0-63)
 //        dU = P^T dO + del K dS'         -> shared memory
 //        T^T dU                         -> dX
 //        [K; Q]^T [-gam b dX; s gam dO]  -> dS = gam_C dS' + it, -> shared memory
 //    P^T dO of the next chunk is issued behind the last product; while that
-//    one runs, dX is read out a second time for what the chain does not wait
-//    for (dX itself, dV = b dX, dX . V).  dU enters in three parts: P^T dO sums
-//    up to 64 rows, of which T^T leaves the differences when keys repeat, so
-//    dU's rounding is the largest error of dX.  It leaves dX and the dS' of
-//    every chunk as hi and lo parts.
+//    one runs, dX, dV = b dX and dX . V go out.  dU enters in three parts: P^T
+//    dO sums up to 64 rows, of which T^T leaves the differences when keys
+//    repeat, so dU's rounding is the largest error of dX.  It leaves dX and the
+//    dS' of every chunk as hi and lo parts.
 //
-// 2. The gradients, one CTA per head and chunk, all chunks at once: with every
-//    factor already in hi and lo parts in global memory, TMA puts them straight
-//    into operand tiles.  Lanes 0-63 are the rows of K, 64-127 those of Q:
+// 2. The gradients, one CTA per head and chunk, all chunks at once: every factor
+//    comes as the operand tile that the chains left.  Lanes 0-63 are the rows of K, 64-127 those of Q:
 //        [dX; dO] U^T  -> Ma (A's part), Mq (P's part), by the decays
 //        [dX; dO] S^T,  U dS'^T,  [Ma; Mq] K,  Ma^T K + Mq^T Q
 //        dK = -gam b dX S^T + del U dS'^T + Ma K + Ma^T K + Mq^T Q
@@ -40,12 +38,15 @@ using namespace delta;
 
 // ------------------------------------------------------------ reverse chain
 struct ChainArgs {
+  const __nv_bfloat16 *v, *go;
   const float *g, *beta, *grad_state_out;
   const uint8_t *t, *pm;        // tiles of T and P
-  float *xv, *grad_state_in;    // xv [M / 32 blocks][BH][N]: dX . V over the block
+  __nv_bfloat16* dv;
+  uint8_t *ds, *dx;             // tiles of dS' and dX, as Saved's of S and U
+  float *xv, *grad_state_in;    // xv [M / 16 blocks][BH][N]: dX . V over the block
   int* status;
   int64_t N;
-  int n_chunks, BH, H, group, D, M;
+  int n_chunks, H, group, D, M;
   float scale;
 };
 
@@ -54,72 +55,63 @@ struct ChainLayout {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
-  static constexpr int kS = DP * 128;
-  static constexpr int oT = 2 * kKQ;           // hi, lo
+  static constexpr int oT = 2 * kKQ;           // hi, lo (after two stages of K, Q)
   static constexpr int oP = oT + 2 * kBox;     // hi, lo
-  static constexpr int oS = oP + 2 * kBox;     // hi, lo
-  static constexpr int oB = oS + 2 * kS;       // [128 x 64]: dU, then -gam b dX; s gam dO; hi, lo
-  static constexpr int oB3 = oB + 4 * kBox;    // [64 x 64]: dU's third part
-  static constexpr int oO = oB3 + kBox;        // dO
-  static constexpr int oV = oO + kBox;
-  static constexpr int oX = oV + kBox;         // dX: hi, lo
-  static constexpr int oDV = oX + 2 * kBox;
-  static constexpr int oG = oDV + kBox;
+  static constexpr int oS = oP + 2 * kBox;     // [DP x (hi | lo)]
+  static constexpr int oB = oS + DP * 128;     // [128 x (hi | lo)]: dU, then -gam b dX; s gam dO
+  static constexpr int oO = oB + 2 * kBox;     // [64 x (dU's third part | dO)]
+  static constexpr int oX = oO + kBox;         // [64 x (hi | lo)]: dX
+  static constexpr int oG = oX + kBox;
   static constexpr int oBar = oG + 2 * (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 128 + 1024;
-  static_assert(kBytes <= tc::kSmemLimit, "shared memory");
+  static constexpr int kPerSM = DP == 64 ? 2 : 1;
+  static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
 };
 
 template <int DP>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
     delta_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
-                          const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v,
-                          const __grid_constant__ CUtensorMap tm_do,
-                          const __grid_constant__ CUtensorMap tm_dv,
-                          const __grid_constant__ CUtensorMap tm_x,
-                          const __grid_constant__ CUtensorMap tm_ds, const ChainArgs a) {
+                          const __grid_constant__ CUtensorMap tm_k, const ChainArgs a) {
   using L = ChainLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   GateSlot* gates = reinterpret_cast<GateSlot*>(sm + L::oG);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [2]
-  uint64_t *t_full = kq_full + 2, *p_full = kq_full + 3, *v_full = kq_full + 4, *o_full = kq_full + 5;
-  uint64_t* done = kq_full + 6;  // [3]
+  uint64_t *t_full = kq_full + 2, *p_full = kq_full + 3;
+  uint64_t* done = kq_full + 4;  // [3]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
   const int lane = threadIdx.x % 32, sub = warp / 4, t = threadIdx.x % 128;
-  const int p = blockIdx.x;  // b * H + h
-  const int pk = (p / a.H) * (a.H / a.group) + (p % a.H) / a.group;
-  const int n = a.n_chunks, c64 = blockIdx.y * 64;
+  const int64_t p = blockIdx.x;  // b * H + h
+  const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
+  const int n = a.n_chunks, c0 = blockIdx.y * kCB + 16 * sub, nc = a.M - c0;  // 16 columns
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 9; ++i) mbar_init(kq_full + i, 1);
+    for (int i = 0; i < 7; ++i) mbar_init(kq_full + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(tmem_holder, 512);
+    tmem_alloc(tmem_holder, 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
-  const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 32 * sub;  // this thread's columns
-  // K dS', then dX; P^T dO, then dX's third accumulator; the update; dS
-  const uint32_t t_acc = tmem, t_e0 = tmem + 128, t_up = tmem + 192, t_s = tmem + 320;
+  const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 16 * sub;
+  // K dS' (64 columns), then T^T dU (96); P^T dO (32); the update (64)
+  const uint32_t t_acc = tmem, t_e0 = tmem + 96, t_up = tmem + 128;
   const uint32_t T_addr = s_base + L::oT, P_addr = s_base + L::oP, S_addr = s_base + L::oS;
-  const uint32_t B_addr = s_base + L::oB, O_addr = s_base + L::oO;
-  uint8_t *S_hi = sm + L::oS, *S_lo = S_hi + L::kS;
-  uint8_t *B_hi = sm + L::oB, *B_lo = B_hi + 2 * kBox;
-  constexpr uint32_t id_nt128 = idesc_bf16_f32(128, 128, 0, 1);
-  constexpr uint32_t id_nt192 = idesc_bf16_f32(128, 192, 0, 1);
+  const uint32_t B_addr = s_base + L::oB, O_addr = s_base + L::oO + 64;
+  uint8_t *S_tile = sm + L::oS, *B_tile = sm + L::oB, *O_tile = sm + L::oO, *X_tile = sm + L::oX;
+  constexpr uint32_t id_nt64 = idesc_bf16_f32(128, 64, 0, 1);
+  constexpr uint32_t id_nt96 = idesc_bf16_f32(128, 96, 0, 1);
+  constexpr uint32_t id_tt32 = idesc_bf16_f32(128, 32, 1, 1);
   constexpr uint32_t id_tt64 = idesc_bf16_f32(128, 64, 1, 1);
-  constexpr uint32_t id_tt128 = idesc_bf16_f32(128, 128, 1, 1);
   const uint64_t once = policy_evict_first();
   // step s of the walk is chunk n - 1 - s
   auto load_kq = [&](int s) {
@@ -133,19 +125,21 @@ __global__ void __launch_bounds__(256, 1)
   };
   auto load_tile = [&](int at, const uint8_t* src, uint64_t* bar, int s) {
     mbar_arrive_expect_tx(bar, 2 * kBox);
-    bulk_load(sm + at, src + ((int64_t)p * n + n - 1 - s) * (2 * kBox), 2 * kBox, bar);
-  };
-  auto load_rows = [&](int at, const CUtensorMap* map, uint64_t* bar, int s) {
-    mbar_arrive_expect_tx(bar, kBox);
-    tma_load_3d(sm + at, map, bar, c64, (n - 1 - s) * kCh, p, once);
+    bulk_load(sm + at, src + (p * n + n - 1 - s) * (2 * kBox), 2 * kBox, bar);
   };
   auto issue_e0 = [&](int s) {  // warp 0: P^T dO of step s
     wait_or_abort(p_full, s & 1, a.status, abort_flag);
-    wait_or_abort(o_full, s & 1, a.status, abort_flag);
     __syncwarp();
     const uint32_t el = elect_one();
-    mma_tile<4, true, true>(el, t_e0, P_addr, O_addr, id_tt64, kBox, 16, 0, 0, true);
-    mma_tile<4, true, true>(el, t_e0, P_addr + kBox, O_addr, id_tt64, kBox, 16, 0, 0, false);
+    mma_tile<4, true, true>(el, t_e0, P_addr, O_addr, id_tt32, kBox, 16, 0, 0, true);
+    mma_tile<4, true, true>(el, t_e0, P_addr + kBox, O_addr, id_tt32, kBox, 16, 0, 0, false);
+  };
+  // lanes 0-63: the row of V, loaded a step ahead; lanes 64-127: that of dO
+  const int64_t at = p * a.N * a.M + c0;
+  uint4 row[2];
+  auto load_row = [&](int s) {
+    const int64_t i = (int64_t)(n - 1 - s) * kCh + (t & 63);
+    read16((t < 64 ? a.v : a.go) + at + i * a.M, nc, i < a.N, row);
   };
   // one warp: the gates, loaded a step before they are written
   float4 gb;
@@ -164,38 +158,28 @@ __global__ void __launch_bounds__(256, 1)
   if (threadIdx.x == 96) {
     load_kq(0);
     load_tile(L::oP, a.pm, p_full, 0);
-    load_rows(L::oO, &tm_do, o_full, 0);
     load_tile(L::oT, a.t, t_full, 0);
-    load_rows(L::oV, &tm_v, v_full, 0);
     if (n > 1) load_kq(1);
   }
   const bool row_on = t < a.D;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int c0 = c64 + 32 * sub + 16 * h;
-    float2 s[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.grad_state_out != nullptr && row_on && c0 + 2 * j < a.M)
-        v = *reinterpret_cast<const float4*>(a.grad_state_out + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j);
-      s[j] = make_float2(v.x, v.y);
-      s[j + 1] = make_float2(v.z, v.w);
-    }
-    tmem_st16(t_s + lane_col + 16 * h, s);
-    if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, s);
-  }
-  tmem_st_wait();
+  float2 dS[8];
+  read16(a.grad_state_out + (p * a.D + t) * a.M + c0, nc, a.grad_state_out != nullptr && row_on, dS);
+  load_row(0);
+  if (t >= 64) put16(O_tile, t - 64, 4 + 2 * sub, row);
   if (warp == 7) {
     load_gates(0);
     put_gates(0);
   }
+  fence_proxy_async_smem();
+  __syncthreads();
   if (warp == 0) issue_e0(0);
 
   for (int s = 0; s < n; ++s) {
     const uint32_t kq = s_base + (s & 1) * L::kKQ, phase = s & 1;
     const GateSlot* gs = gates + (s & 1);
     const int chunk = n - 1 - s;
+    const int64_t tile = (p * n + chunk) * gridDim.y + blockIdx.y;
+    if (t < DP) store_parts(S_tile, t, sub, dS);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -204,53 +188,38 @@ __global__ void __launch_bounds__(256, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<DP / 16, false, true>(el, t_acc, kq, S_addr, id_nt128, 16, L::kS, L::kKQBox, 0, true);
+      mma_tile<DP / 16, false, true>(el, t_acc, kq, S_addr, id_nt64, 16, 16, L::kKQBox, 0, true);
       if (el) mma_commit(done);
     }
     if (threadIdx.x == 128) {
-      const int at = (p * n + chunk) * 2;
-      tma_store_3d(&tm_ds, S_hi, c64, 0, at);
-      tma_store_3d(&tm_ds, S_lo, c64, 0, at + 1);
-      if (s > 0) {  // the step before's dX and dV
-        tma_store_3d(&tm_x, sm + L::oX, c64, (chunk + 1) * kCh, p);
-        tma_store_3d(&tm_x, sm + L::oX + kBox, c64, (chunk + 1) * kCh, a.BH + p);
-        tma_store_3d(&tm_dv, sm + L::oDV, c64, (chunk + 1) * kCh, p);
-      }
+      bulk_store(a.ds + tile * (DP * 128), S_tile, DP * 128);
+      if (s > 0) bulk_store(a.dx + (tile + gridDim.y) * kBox, X_tile, kBox);  // the step before's
       tma_store_commit();
     }
+    float2 x[8];
     if (t >= 64) {  // s gam dO, under the product
       const float2 w = both(a.scale * gs->gam[t - 64]);
-      wait_or_abort(o_full, phase, a.status, abort_flag);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 x[8];
-        get16(sm + L::oO, t - 64, 4 * sub + 2 * h, x);
+      unpack16(row, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = mul2(w, x[j]);
-        store16_split(B_hi, B_lo, t, 4 * sub + 2 * h, x);
-      }
+      for (int j = 0; j < 8; ++j) x[j] = mul2(w, x[j]);
+      store_parts(B_tile, t, sub, x);
+      if (s + 1 < n) load_row(s + 1);
     }
     wait_or_abort(done, phase, a.status, abort_flag);
     tc_fence_after();
     if (t < 64) {
       const float2 del = both(gs->del[t]);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t e0[16];
-        tmem_ld16(t_e0 + lane_col + 16 * h, e0);
-        float2 r[8];
-        load16_sum(t_acc + lane_col + 16 * h, r);
+      float2 e0[8];
+      tmem_ld16(t_e0 + lane_col, e0);
+      load16_sum(t_acc + lane_col, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          r[j] = fma2(del, r[j], make_float2(__uint_as_float(e0[2 * j]), __uint_as_float(e0[2 * j + 1])));
-        uint4 x0[2], x1[2], x2[2];
-        split16_3(r, x0, x1, x2);
-        put16(B_hi, t, 4 * sub + 2 * h, x0);
-        put16(B_lo, t, 4 * sub + 2 * h, x1);
-        put16(sm + L::oB3, t, 4 * sub + 2 * h, x2);
-      }
+      for (int j = 0; j < 8; ++j) x[j] = fma2(del, x[j], e0[j]);
+      uint4 x0[2], x1[2], x2[2];
+      split16_3(x, x0, x1, x2);
+      put_parts(B_tile, t, sub, x0, x1);
+      put16(O_tile, t, 2 * sub, x2);
     }
-    // the stores out of the S, dX and dV tiles have read them
+    // the copies out of the S and X tiles have read them
     if (threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
@@ -260,31 +229,29 @@ __global__ void __launch_bounds__(256, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      // T^T hi with dU's three parts (the third's accumulator takes P^T dO's
-      // place, which has been read), T^T lo with two
-      mma_tile<4, false, true>(el, t_acc, T_addr, B_addr, id_nt192, 16, 2 * kBox, 0, 0, true);
-      mma_tile<4, false, true>(el, t_acc, T_addr + kBox, B_addr, id_nt128, 16, 2 * kBox, 0, 0, false);
+      // T^T hi with dU's three parts, T^T lo with two
+      mma_tile<4, false, true>(el, t_acc, T_addr, B_addr, id_nt96, 16, 2 * kBox, 0, 0, true);
+      mma_tile<4, false, true>(el, t_acc, T_addr + kBox, B_addr, id_nt64, 16, 16, 0, 0, false);
       if (el) mma_commit(done + 1);
     }
-    if (threadIdx.x == 96 && s + 1 < n) {  // P^T dO and s gam dO have read them
-      load_tile(L::oP, a.pm, p_full, s + 1);
-      load_rows(L::oO, &tm_do, o_full, s + 1);
+    if (s + 1 < n) {  // P^T dO has read P and dO
+      if (threadIdx.x == 96) load_tile(L::oP, a.pm, p_full, s + 1);
+      if (t >= 64) put16(O_tile, t - 64, 4 + 2 * sub, row);
+      if (warp == 7) put_gates(s + 1);
     }
-    if (warp == 7 && s + 1 < n) put_gates(s + 1);
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
-    float2 r3[8];
-    const float2 w = both(t < 64 ? -gs->b[t] * gs->gam[t] : 0.f);
     if (t < 64) {
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 r[8];
-        tmem_ld16(t_e0 + lane_col + 16 * h, r3);
-        load16_sum(t_acc + lane_col + 16 * h, r);
+      float2 r[8];
+      tmem_ld16(t_acc + 64 + lane_col, r);
+      load16_sum(t_acc + lane_col, x);
+      const float2 w = both(-gs->b[t] * gs->gam[t]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = mul2(w, add2(r[j], r3[j]));
-        store16_split(B_hi, B_lo, t, 4 * sub + 2 * h, r);
+      for (int j = 0; j < 8; ++j) {
+        x[j] = add2(x[j], r[j]);
+        r[j] = mul2(w, x[j]);
       }
+      store_parts(B_tile, t, sub, r);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -295,95 +262,62 @@ __global__ void __launch_bounds__(256, 1)
       // [K; Q]^T: 128 rows along K; with one 64-column block the lanes past 64
       // read on into the tiles behind, and are not used
       constexpr uint32_t lbo = DP == 128 ? L::kKQBox : kBox;
-      mma_tile<8, true, true>(el, t_up, kq, B_addr, id_tt128, lbo, 2 * kBox, 0, 0, true);
+      mma_tile<8, true, true>(el, t_up, kq, B_addr, id_tt64, lbo, 16, 0, 0, true);
       if (el) mma_commit(done + 2);
+      if (s + 1 < n) issue_e0(s + 1);
     }
     if (threadIdx.x == 96 && s + 1 < n) load_tile(L::oT, a.t, t_full, s + 1);
-    if (t < 64) {  // under the product
+    if (t < 64) {  // under the product: x is dX
       const int64_t i = (int64_t)chunk * kCh + t;
       const float2 b = both(gs->b[t]);
-      float2 dot = both(0.f);
-      wait_or_abort(v_full, phase, a.status, abort_flag);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 r[8], v[8];
-        tmem_ld16(t_e0 + lane_col + 16 * h, r3);
-        load16_sum(t_acc + lane_col + 16 * h, r);
-        get16(sm + L::oV, t, 4 * sub + 2 * h, v);
+      float2 dot = both(0.f), v[8];
+      unpack16(row, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          r[j] = add2(r[j], r3[j]);
-          dot = fma2(r[j], v[j], dot);
-        }
-        store16_split(sm + L::oX, sm + L::oX + kBox, t, 4 * sub + 2 * h, r);
+      for (int j = 0; j < 8; ++j) dot = fma2(x[j], v[j], dot);
+      store_parts(X_tile, t, sub, x);
+      uint4 dv[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = mul2(b, r[j]);
-        uint4 dv[2];
-        pack16(r, dv);
-        put16(sm + L::oDV, t, 4 * sub + 2 * h, dv);
+      for (int j = 0; j < 8; ++j) v[j] = mul2(b, x[j]);
+      pack16(v, dv);
+      if (i < a.N) {
+        write16(a.dv + at + i * a.M, nc, dv);
+        if (nc > 0) a.xv[((int64_t)(c0 / 16) * gridDim.x + p) * a.N + i] = dot.x + dot.y;
       }
-      if (i < a.N && c64 + 32 * sub < a.M)
-        a.xv[((int64_t)(c64 / 32 + sub) * a.BH + p) * a.N + i] = dot.x + dot.y;
+      if (s + 1 < n) load_row(s + 1);
     }
-    tc_fence_before();
-    __syncthreads();  // dX has been read, and V
-    if (warp == 0 && s + 1 < n) {
-      tc_fence_after();
-      issue_e0(s + 1);
-    }
-    if (threadIdx.x == 96 && s + 1 < n) load_rows(L::oV, &tm_v, v_full, s + 1);
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
     if (threadIdx.x == 96 && s + 2 < n) load_kq(s + 2);
     const float2 last = both(gs->gam[kCh - 1]);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float2 r[8], x[8];
-      load16_sum(t_up + lane_col + 16 * h, r);
-      tmem_ld16(t_s + lane_col + 16 * h, x);
+    load16_sum(t_up + lane_col, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = fma2(last, x[j], r[j]);
-      tmem_st16(t_s + lane_col + 16 * h, x);
-      if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, x);
-    }
-    tmem_st_wait();
+    for (int j = 0; j < 8; ++j) dS[j] = fma2(last, dS[j], x[j]);
   }
-  if (a.grad_state_in != nullptr) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int c0 = c64 + 32 * sub + 16 * h;
-      float2 s[8];
-      tmem_ld16(t_s + lane_col + 16 * h, s);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2)
-        if (row_on && c0 + 2 * j < a.M)
-          *reinterpret_cast<float4*>(a.grad_state_in + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j) =
-              make_float4(s[j].x, s[j].y, s[j + 1].x, s[j + 1].y);
-    }
-  }
+  if (a.grad_state_in != nullptr && row_on)
+    write16(a.grad_state_in + (p * a.D + t) * a.M + c0, nc, dS);
   fence_proxy_async_smem();
   __syncthreads();
-  if (threadIdx.x == 128) {  // the last step's (chunk 0) dX and dV
-    tma_store_3d(&tm_x, sm + L::oX, c64, 0, p);
-    tma_store_3d(&tm_x, sm + L::oX + kBox, c64, 0, a.BH + p);
-    tma_store_3d(&tm_dv, sm + L::oDV, c64, 0, p);
+  if (threadIdx.x == 128) {  // the last step's, chunk 0
+    bulk_store(a.dx + (p * n * gridDim.y + blockIdx.y) * kBox, X_tile, kBox);
     tma_store_commit();
-    tma_store_wait_all();
-    if (*abort_flag) linger();
+    tma_store_wait_read_all();
   }
+  // every load and MMA has been waited for by the loop that used it
+  if (*abort_flag) linger();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
 // ---------------------------------------------------------------- gradients
 struct GradArgs {
+  const __nv_bfloat16* go;
   const float *g, *beta, *xv;
-  __nv_bfloat16 *dq, *dk;       // written whole (one value head to a key head) ..
-  float *dq_part, *dk_part;     // .. or [BH][N][D] fp32 parts
+  const uint8_t *s, *u, *ds, *dx;  // tiles
+  float *dq_part, *dk_part;     // [BH][N][D] fp32, where value heads share a key head; else null
   float *dg, *dbeta;
   int* status;
   int64_t N;
@@ -397,16 +331,17 @@ struct GradLayout {
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
   static constexpr int kS = DP * 128;
-  static constexpr int oA = kKQ;              // [dX; dO] hi, [dX lo; 0]; then [Ma; Mq] hi, lo
-  static constexpr int oU = oA + 4 * kBox;    // hi, lo
-  static constexpr int oS = oU + 2 * kBox;    // hi, lo
-  static constexpr int oD = oS + 2 * kS;      // dS' hi, lo
+  // two blocks of 32 value columns, every tile hi | lo
+  static constexpr int oA = kKQ;              // [dX; dO | 0]; then [Ma; Mq] hi, lo
+  static constexpr int oU = oA + 4 * kBox;
+  static constexpr int oS = oU + 2 * kBox;
+  static constexpr int oD = oS + 2 * kS;      // dS'
   static constexpr int oG = oD + 2 * kS;
   static constexpr int oX = oG + (int)sizeof(GateSlot);  // sums for the gates
   static constexpr int kXFloats = 8 * 64 + 2 * 64 * 6 + 16;
   static constexpr int oBar = oX + kXFloats * 4;
   static constexpr int kBytes = oBar + 64 + 1024;
-  static constexpr int kStage = 3 * kBox + 2 * kBox + 4 * kS;  // bytes TMA brings per 64 value columns
+  static constexpr int kBlock = 2 * kBox + 2 * kS;             // bytes copied per block
   static constexpr int kCols = DP == 64 ? 256 : 512;           // tensor memory
   static constexpr int kPerSM = DP == 64 ? 2 : 1;
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
@@ -459,11 +394,8 @@ template <int DP>
 __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     delta_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_do,
-                         const __grid_constant__ CUtensorMap tm_x,
-                         const __grid_constant__ CUtensorMap tm_u,
-                         const __grid_constant__ CUtensorMap tm_s,
-                         const __grid_constant__ CUtensorMap tm_ds, const GradArgs a) {
+                         const __grid_constant__ CUtensorMap tm_dq,
+                         const __grid_constant__ CUtensorMap tm_dk, const GradArgs a) {
   using L = GradLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -483,14 +415,34 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   const int64_t p = blockIdx.x / a.n_chunks;
   const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
-  const int n_mb = (a.M + 63) / 64;
+  const int blocks = (a.M + kCB - 1) / kCB, n_mb = (blocks + 1) / 2;
 
+  const uint64_t keep = policy_evict_first();
+  const int64_t tile0 = (p * a.n_chunks + chunk) * blocks;
+  auto load_mb = [&](int m) {  // blocks 2 m and 2 m + 1
+    const int nb = min(2, blocks - 2 * m);
+    mbar_arrive_expect_tx(full, nb * L::kBlock);
+    for (int h = 0; h < nb; ++h) {
+      const int64_t tile = tile0 + 2 * m + h;
+      bulk_load(sm + L::oA + h * 2 * kBox, a.dx + tile * kBox, kBox, full);
+      bulk_load(sm + L::oU + h * kBox, a.u + tile * kBox, kBox, full);
+      bulk_load(sm + L::oS + h * L::kS, a.s + tile * L::kS, L::kS, full);
+      bulk_load(sm + L::oD + h * L::kS, a.ds + tile * L::kS, L::kS, full);
+    }
+  };
   if (issuer) {
     for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    mbar_arrive_expect_tx(kq_full, L::kKQ);
+    for (int x = 0; x < L::kBoxes; ++x) {
+      tma_load_3d(sm + x * L::kKQBox, &tm_k, kq_full, 64 * x, i0, pk, keep);
+      tma_load_3d(sm + x * L::kKQBox + kBox, &tm_q, kq_full, 64 * x, i0, pk, keep);
+    }
+    load_mb(0);
   }
   if (warp == 0) {
+    __syncwarp();
     tmem_alloc(tmem_holder, L::kCols);
     tmem_relinquish();
   }
@@ -499,9 +451,6 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     write_gates(gs, lane, i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
                 i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
   }
-  // no lo part under dO
-  for (int i = threadIdx.x; i < kBox / 16; i += 256)
-    reinterpret_cast<uint4*>(sm + L::oA + 3 * kBox)[i] = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < 512; i += 256) e_sum[i] = 0.f;
   fence_proxy_async_smem();
   tc_fence_before();
@@ -516,28 +465,15 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   constexpr uint32_t id_nnD = idesc_bf16_f32(128, DP, 0, 0);
   constexpr uint32_t id_ntD = idesc_bf16_f32(128, DP, 0, 1);
   constexpr uint32_t id_ttD = idesc_bf16_f32(128, DP, 1, 1);
-  const uint64_t keep = policy_evict_first();
-  auto load_mb = [&](int m) {
-    mbar_arrive_expect_tx(full, L::kStage);
-    const int c = 64 * m, s0 = (int)((p * a.n_chunks + chunk) * 2);
-    tma_load_3d(sm + L::oA, &tm_x, full, c, i0, (int)p, keep);
-    tma_load_3d(sm + L::oA + kBox, &tm_do, full, c, i0, (int)p, keep);
-    tma_load_3d(sm + L::oA + 2 * kBox, &tm_x, full, c, i0, a.BH + (int)p, keep);
-    tma_load_3d(sm + L::oU, &tm_u, full, c, i0, (int)p, keep);
-    tma_load_3d(sm + L::oU + kBox, &tm_u, full, c, i0, a.BH + (int)p, keep);
-    for (int h = 0; h < 2; ++h) {
-      tma_load_3d(sm + L::oS + h * L::kS, &tm_s, full, c, 0, s0 + h, keep);
-      tma_load_3d(sm + L::oD + h * L::kS, &tm_ds, full, c, 0, s0 + h, keep);
-    }
+  // dO's part of the A tiles: a row's 32 columns, no lo part
+  auto put_do = [&](int m) {
+    const int r = threadIdx.x % 64, h = (threadIdx.x / 64) % 2, q = threadIdx.x / 128;
+    const int col = 64 * m + 32 * h + 16 * q;
+    uint4 v[2];
+    read16(a.go + (p * a.N + i0 + r) * a.M + col, a.M - col, i0 + r < a.N, v);
+    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    put_parts(sm + L::oA + h * 2 * kBox + kBox, r, q, v, zero);
   };
-  if (issuer) {
-    mbar_arrive_expect_tx(kq_full, L::kKQ);
-    for (int x = 0; x < L::kBoxes; ++x) {
-      tma_load_3d(sm + x * L::kKQBox, &tm_k, kq_full, 64 * x, i0, pk, keep);
-      tma_load_3d(sm + x * L::kKQBox + kBox, &tm_q, kq_full, 64 * x, i0, pk, keep);
-    }
-    load_mb(0);
-  }
   if (warp == 0) {
     wait_or_abort(kq_full, 0, a.status, abort_flag);
     __syncwarp();
@@ -545,29 +481,39 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   }
   float z = 0.f;  // <S, dS'>, this thread's share
   for (int m = 0; m < n_mb; ++m) {
+    const int nb = min(2, blocks - 2 * m);
+    put_do(m);
+    fence_proxy_async_smem();
+    __syncthreads();
     if (warp == 0) {
       wait_or_abort(full, m & 1, a.status, abort_flag);
       __syncwarp();
       const uint32_t el = elect_one();
 #pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        // (A hi, B hi), (A lo, B hi), (A hi, B lo), (A lo, B lo)
-        const uint32_t ap = (x & 1) * 2 * kBox, up = (x & 1) * kBox, b = x >> 1;
+      for (int x = 0; x < 4 * nb; ++x) {
+        // per block: (A hi, B hi), (A lo, B hi), (A hi, B lo), (A lo, B lo)
+        const int h = x >> 2;
+        const uint32_t ap = (x & 1) * 64, b = ((x >> 1) & 1) * 64;
         const bool fresh = m == 0 && x == 0;
-        mma_tile<4, false, false>(el, t_p2, A_addr + ap, U_addr + b * kBox, id_nn64, 16, 16, 0, 0, fresh);
-        mma_tile<4, false, false>(el, t_in, A_addr + ap, S_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh);
+        const uint32_t u = U_addr + h * kBox;
+        mma_tile<2, false, false>(el, t_p2, A_addr + h * 2 * kBox + ap, u + b, id_nn64, 16, 16, 0, 0, fresh);
+        mma_tile<2, false, false>(el, t_in, A_addr + h * 2 * kBox + ap, S_addr + h * L::kS + b, id_nnD,
+                                  16, 16, 0, 0, fresh);
         // lanes past 64 read on behind U and are not used
-        mma_tile<4, false, false>(el, t_u, U_addr + up, D_addr + b * L::kS, id_nnD, 16, 16, 0, 0, fresh);
+        mma_tile<2, false, false>(el, t_u, u + ap, D_addr + h * L::kS + b, id_nnD, 16, 16, 0, 0, fresh);
       }
       if (el) mma_commit(done);
     }
     wait_or_abort(full, m & 1, a.status, abort_flag);
     // the MMAs read the tiles at the same time
-    for (int e = threadIdx.x; e < DP * 8; e += 256) {
-      const uint4 sh = *reinterpret_cast<const uint4*>(sm + L::oS + 16 * e);
-      const uint4 sl = *reinterpret_cast<const uint4*>(sm + L::oS + L::kS + 16 * e);
-      const uint4 dh = *reinterpret_cast<const uint4*>(sm + L::oD + 16 * e);
-      const uint4 dl = *reinterpret_cast<const uint4*>(sm + L::oD + L::kS + 16 * e);
+    for (int e = threadIdx.x; e < nb * DP * 4; e += 256) {
+      // 16-byte pieces: a row's hi columns, their lo parts 64 bytes on in the
+      // same row, which the swizzle leaves at piece ^ 4
+      const int row = e / 4, ch = e % 4, hi = row * 128 + ((ch ^ (row & 7)) << 4), lo = hi ^ 64;
+      const uint4 sh = *reinterpret_cast<const uint4*>(sm + L::oS + hi);
+      const uint4 sl = *reinterpret_cast<const uint4*>(sm + L::oS + lo);
+      const uint4 dh = *reinterpret_cast<const uint4*>(sm + L::oD + hi);
+      const uint4 dl = *reinterpret_cast<const uint4*>(sm + L::oD + lo);
       const uint32_t w[4][4] = {{sh.x, sh.y, sh.z, sh.w}, {sl.x, sl.y, sl.z, sl.w},
                                 {dh.x, dh.y, dh.z, dh.w}, {dl.x, dl.y, dl.z, dl.w}};
 #pragma unroll
@@ -763,7 +709,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
         const int64_t at = p * a.N + i0 + j;
         a.dg[at] = s;
         float d = dots[192 + j] + dots[576 + j] - gs->gam[j] * kx[h];
-        for (int x = 0; x < (a.M + 31) / 32; ++x) d += a.xv[(int64_t)x * a.BH * a.N + at];
+        for (int x = 0; x < (a.M + 15) / 16; ++x) d += a.xv[(int64_t)x * a.BH * a.N + at];
         // U carries b as a factor, far above the smallest number down to 2^-80
         const float b = gs->b[j];
         a.dbeta[at] = fabsf(b) < 0x1p-80f ? d : dots[256 + j] / b;
@@ -795,14 +741,23 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
         if (live && c + 2 * e < a.D)
           *reinterpret_cast<float4*>(to + 2 * e) = make_float4(o[e].x, o[e].y, o[e + 1].x, o[e + 1].y);
     } else {
-      __nv_bfloat16* to = (is_k ? a.dk : a.dq) + orow * a.D + c;
+      // over k and q, which the last products have read
       uint4 w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        w[j] = make_uint4(tc::pack_bf16x2(o[4 * j].x, o[4 * j].y), tc::pack_bf16x2(o[4 * j + 1].x, o[4 * j + 1].y),
-                          tc::pack_bf16x2(o[4 * j + 2].x, o[4 * j + 2].y),
-                          tc::pack_bf16x2(o[4 * j + 3].x, o[4 * j + 3].y));
-      if (live) write16(to, a.D - c, w);
+      pack16(o, w);
+      put16(sm + (c / 64) * L::kKQBox, t, (c % 64) / 8, w);
+    }
+  }
+  if (a.dq_part == nullptr) {
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (issuer) {
+      for (int x = 0; x < L::kBoxes; ++x) {
+        if (64 * x >= a.D) break;
+        tma_store_3d(&tm_dk, sm + x * L::kKQBox, 64 * x, i0, (int)p);
+        tma_store_3d(&tm_dq, sm + x * L::kKQBox + kBox, 64 * x, i0, (int)p);
+      }
+      tma_store_commit();
+      tma_store_wait_read_all();
     }
   }
   if (*abort_flag) linger();
@@ -816,14 +771,15 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
 
 // What the chain leaves for the gradients.
 struct Scratch {
-  int64_t ds, dx, xv, part;  // bytes
+  int64_t ds, dx, xv, part;  // bytes; dS' and dX in tiles
   uint8_t *ds_at, *dx_at, *xv_at, *part_at;
   explicit Scratch(const DeltaShape& s, void* at = nullptr) {
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-    const int64_t BH = s.B * s.H, n = (s.N + kCh - 1) / kCh;
-    ds = up(4 * BH * n * s.D * s.M);
-    dx = up(4 * BH * s.N * s.M);
-    xv = up(4 * ((s.M + 31) / 32) * BH * s.N);
+    const int64_t BH = s.B * s.H;
+    const Saved k(s);
+    ds = k.s_bytes;
+    dx = k.u_bytes;
+    xv = up(4 * ((s.M + 15) / 16) * BH * s.N);
     part = s.H == s.Hk ? 0 : up(4 * BH * s.N * s.D);
     ds_at = static_cast<uint8_t*>(at);
     dx_at = ds_at + ds;
@@ -834,9 +790,8 @@ struct Scratch {
 };
 
 template <int DP>
-cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const Scratch& w, const ChainArgs& c,
-                   const GradArgs& g, cudaStream_t stream) {
-  const uint8_t* kept = reinterpret_cast<const uint8_t*>(f.ckpt);
+cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const ChainArgs& c, const GradArgs& g,
+                   cudaStream_t stream) {
   using LC = ChainLayout<DP>;
   using LG = GradLayout<DP>;
   auto chain = delta_tc_chain_kernel<DP>;
@@ -846,20 +801,14 @@ cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const Scratch& w, con
     return CP_ERR_CUDA;
   // (encoding a map needs the device's context current in this thread: the
   // calls above see to that)
-  const Saved k(s);
-  const int64_t heads = s.B * s.H;
-  CUtensorMap q, kk, v, go, dv, x, u, st, ds;
+  CUtensorMap q, kk, dq, dk;
   if (!make_chunk_map(&q, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&kk, f.k, s.B * s.Hk, s.N, s.D) ||
-      !make_chunk_map(&v, f.v, heads, s.N, s.M) || !make_chunk_map(&go, f.grad_out, heads, s.N, s.M) ||
-      !make_chunk_map(&dv, f.dv, heads, s.N, s.M) || !make_chunk_map(&x, w.dx_at, 2 * heads, s.N, s.M) ||
-      !make_chunk_map(&u, kept + k.s_bytes, 2 * heads, s.N, s.M) ||
-      !make_chunk_map(&st, kept, heads * k.n * 2, s.D, s.M, DP) ||
-      !make_chunk_map(&ds, w.ds_at, heads * k.n * 2, s.D, s.M, DP))
+      !make_chunk_map(&dq, f.dq, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&dk, f.dk, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
-  const unsigned BH = (unsigned)heads;
-  chain<<<dim3(BH, (unsigned)((s.M + 63) / 64)), 256, LC::kBytes, stream>>>(q, kk, v, go, dv, x, ds, c);
+  const unsigned BH = (unsigned)(s.B * s.H);
+  chain<<<dim3(BH, (unsigned)((s.M + kCB - 1) / kCB)), 256, LC::kBytes, stream>>>(q, kk, c);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
-  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, go, x, u, st, ds, g);
+  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, dq, dk, g);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -876,15 +825,21 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
   c.g = f.g; c.beta = f.beta; c.grad_state_out = f.grad_state_out;
   c.t = reinterpret_cast<const uint8_t*>(f.ckpt) + k.s_bytes + k.u_bytes;
   c.pm = c.t + k.t_bytes;
+  c.v = static_cast<const __nv_bfloat16*>(f.v);
+  c.go = static_cast<const __nv_bfloat16*>(f.grad_out);
+  c.dv = static_cast<__nv_bfloat16*>(f.dv);
+  c.ds = w.ds_at;
+  c.dx = w.dx_at;
   c.xv = reinterpret_cast<float*>(w.xv_at);
   c.grad_state_in = f.grad_state_in;
   c.status = status;
-  c.N = s.N; c.n_chunks = (int)k.n; c.BH = (int)BH;
+  c.N = s.N; c.n_chunks = (int)k.n;
   c.H = (int)s.H; c.group = (int)(s.H / s.Hk); c.D = (int)s.D; c.M = (int)s.M; c.scale = s.scale;
   GradArgs g{};
-  g.g = f.g; g.beta = f.beta; g.xv = c.xv;
-  g.dq = static_cast<__nv_bfloat16*>(f.dq);
-  g.dk = static_cast<__nv_bfloat16*>(f.dk);
+  g.go = c.go; g.g = f.g; g.beta = f.beta; g.xv = c.xv;
+  g.s = reinterpret_cast<const uint8_t*>(f.ckpt);
+  g.u = g.s + k.s_bytes;
+  g.ds = w.ds_at; g.dx = w.dx_at;
   if (w.part != 0) {
     g.dq_part = reinterpret_cast<float*>(w.part_at);
     g.dk_part = reinterpret_cast<float*>(w.part_at + w.part);
@@ -892,7 +847,7 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
   g.dg = f.dg; g.dbeta = f.dbeta; g.status = status;
   g.N = s.N; g.n_chunks = (int)k.n; g.BH = (int)BH; g.H = c.H; g.group = c.group; g.D = c.D;
   g.M = c.M; g.scale = s.scale;
-  cp_status_t st = s.D <= 64 ? launch<64>(s, f, w, c, g, stream) : launch<128>(s, f, w, c, g, stream);
+  cp_status_t st = s.D <= 64 ? launch<64>(s, f, c, g, stream) : launch<128>(s, f, c, g, stream);
   if (st != CP_OK || w.part == 0) return st;
   const int64_t heads = s.B * s.Hk;
   cudaError_t e = delta_join_launch(g.dq_part, f.dq, s.N * s.D, heads, c.group, 1, s.dtype, stream);

@@ -6,9 +6,9 @@
 //    A)^-1 by blocks, P T by MMA; the tiles of T, P T (and, for a backward, P)
 //    go to memory as they lie in shared memory.
 //
-// 2. The chain.  A CTA walks one head's chunks of 64 rows for 64 value columns
-//    (columns never meet), two warpgroups of 32 columns each; lane d holds row
-//    d of the fp32 state, in tensor memory.  A chunk is three MMAs:
+// 2. The chain.  A CTA walks one head's chunks of 64 rows for 32 value columns
+//    (columns never meet), two warpgroups of 16 columns each; lane d holds row
+//    d of the fp32 state in registers.  A chunk is three MMAs:
 //        [K; Q] S          -> KS (lanes 0-63), QS (lanes 64-127)
 //        R = b (V - gam KS) -> shared memory
 //        [T; P T] R        -> U (lanes 0-63), P U (lanes 64-127)
@@ -16,14 +16,12 @@
 //        K^T (del U)       -> S = gam_C S + it, -> shared memory
 //    P T in place of P takes a fourth dependent step (P U) off the chain and
 //    gives both products one 128-lane MMA.  The chain is bound by its own
-//    latency: a product is 530 cycles from its first MMA to its result, a
-//    conversion some 300.  So the conversions are spread over 256 threads, a
-//    factor's hi and lo parts enter as one 128-column operand (an MMA of 64
-//    columns takes 45 to 48 cycles, one of 128 columns 63), all loads and
-//    stores go by TMA, and the loops over columns are rolled: past 32 KB of
-//    instructions every one of them takes 3.1 cycles to fetch (measured), and
-//    the two launches' work in one kernel, with a chunk's matrices made two
-//    ahead by warps beside the chain, took 7.4k cycles a chunk.
+//    latency, some 550 cycles to a product of four MMAs and 150 to 250 to a
+//    conversion of 16 columns, so it is cut into few columns a CTA (64 columns
+//    took 4.6k cycles a chunk at D = 64).  Past 32 KB of instructions every one
+//    of them takes 3.1 cycles to fetch (measured): the two launches' work in
+//    one kernel, with a chunk's matrices made two ahead by warps beside the
+//    chain, took 7.4k cycles a chunk.
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"
@@ -78,6 +76,12 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
   const int64_t p = blockIdx.x / a.n_chunks;
   const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
+  float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (w == 3) {
+    const int64_t i = i0 + lane, at = p * a.N;
+    gb = make_float4(i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
+                     i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
+  }
   if (t == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(full + i, 1);
     *abort_flag = 0;
@@ -93,11 +97,6 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     tmem_alloc(tmem_holder, 128);
     tmem_relinquish();
   }
-  if (w == 3) {
-    const int64_t i = i0 + lane, at = p * a.N;
-    write_gates(gs, lane, i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
-                i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -112,6 +111,10 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     mma_tile<DP / 16, false, false>(el, tmem, s_base, s_base, id_nn64, 16, 16, L::kKQBox, L::kKQBox, true);
     if (el) mma_commit(done);
   }
+  if (w == 3) {  // under the product
+    write_gates(gs, lane, gb.x, gb.y, gb.z, gb.w);
+  }
+  __syncthreads();
   wait_or_abort(done, 0, a.status, abort_flag);
   tc_fence_after();
   // A by the lanes of K, P by those of Q
@@ -179,12 +182,15 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
 
 // ------------------------------------------------------------------- chain
 struct FwdArgs {
+  const __nv_bfloat16* v;
   const float *g, *beta, *state_in;
-  const uint8_t *t, *pt;  // of the first launch
+  const uint8_t *t, *pt;             // of the first launch
+  __nv_bfloat16* out;
+  uint8_t *keep_s, *keep_u;          // see Saved
   float* state_out;
   int* status;
   int64_t N;
-  int n_chunks, BH, H, group, D, M;
+  int n_chunks, H, group, D, M;
   float scale;
 };
 
@@ -194,67 +200,58 @@ struct FwdLayout {
   static constexpr int kKQBox = 2 * kBox;               // 64 columns of K over Q: [128 x 64]
   static constexpr int kKQ = kBoxes * kKQBox;
   static constexpr int kT = 2 * kBox;                   // [T; P T] transposed, one part
-  static constexpr int kS = DP * 128;                   // [DP x 64], one part
-  static constexpr int NST = 2;                         // K, Q stages
-  static constexpr int oT = NST * kKQ;                  // hi, lo
-  static constexpr int oS = oT + 2 * kT;                // hi, lo
-  static constexpr int oR = oS + 2 * kS;                // hi, lo
-  static constexpr int oV = oR + 2 * kBox;
-  static constexpr int oO = oV + kBox;
-  static constexpr int oU = oO + kBox;                  // hi, lo (KEEP)
-  static constexpr int oG = oU + (KEEP ? 2 * kBox : 0);
+  static constexpr int oT = 2 * kKQ;                    // hi, lo (after two stages of K, Q)
+  static constexpr int oS = oT + 2 * kT;                // [DP x (hi | lo)]
+  static constexpr int oR = oS + DP * 128;              // [64 x (hi | lo)]
+  static constexpr int oU = oR + kBox;                  // the same of U (KEEP)
+  static constexpr int oG = oU + (KEEP ? kBox : 0);
   static constexpr int oBar = oG + 2 * (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 128 + 1024;
-  static_assert(kBytes <= tc::kSmemLimit, "shared memory");
+  static constexpr int kPerSM = DP == 64 ? 2 : 1;
+  static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
 };
 
-// KEEP: leave what the backward needs (Saved): the states' and U's parts are
-// stored from tiles.
+// KEEP: leave what the backward needs (Saved).
 template <int DP, bool KEEP>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
     delta_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
-                        const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v,
-                        const __grid_constant__ CUtensorMap tm_o,
-                        const __grid_constant__ CUtensorMap tm_s,
-                        const __grid_constant__ CUtensorMap tm_u, const FwdArgs a) {
+                        const __grid_constant__ CUtensorMap tm_k, const FwdArgs a) {
   using L = FwdLayout<DP, KEEP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   GateSlot* gates = reinterpret_cast<GateSlot*>(sm + L::oG);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [2]
-  uint64_t *t_full = kq_full + 2, *v_full = kq_full + 3;
-  uint64_t* done = kq_full + 4;  // [3]
+  uint64_t* t_full = kq_full + 2;
+  uint64_t* done = kq_full + 3;  // [3]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
   const int lane = threadIdx.x % 32, sub = warp / 4, t = threadIdx.x % 128;
-  const bool issuer = threadIdx.x == 0;
-  const int p = blockIdx.x;  // b * H + h
-  const int pk = (p / a.H) * (a.H / a.group) + (p % a.H) / a.group;
-  const int n = a.n_chunks, c64 = blockIdx.y * 64;
+  const int64_t p = blockIdx.x;  // b * H + h
+  const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
+  const int n = a.n_chunks, c0 = blockIdx.y * kCB + 16 * sub, nc = a.M - c0;  // 16 columns
 
-  if (issuer) {
-    for (int i = 0; i < 7; ++i) mbar_init(kq_full + i, 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 6; ++i) mbar_init(kq_full + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(tmem_holder, 512);
+    tmem_alloc(tmem_holder, 128);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
-  const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 32 * sub;  // this thread's columns
-  const uint32_t t_kqs = tmem, t_tr = tmem + 128, t_s = tmem + 256;
+  const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 16 * sub;
+  const uint32_t t_kqs = tmem, t_tr = tmem + 64;
   const uint32_t T_addr = s_base + L::oT, S_addr = s_base + L::oS, R_addr = s_base + L::oR;
-  uint8_t *S_hi = sm + L::oS, *S_lo = S_hi + L::kS, *R_hi = sm + L::oR, *R_lo = R_hi + kBox;
-  constexpr uint32_t id_nt128 = idesc_bf16_f32(128, 128, 0, 1);  // A [rows x K], B [K x cols]
-  constexpr uint32_t id_tt128 = idesc_bf16_f32(128, 128, 1, 1);  // A [K x rows], B [K x cols]
+  uint8_t *S_tile = sm + L::oS, *R_tile = sm + L::oR;
+  constexpr uint32_t id_nt = idesc_bf16_f32(128, 64, 0, 1);  // A [rows x K], B [K x cols]
+  constexpr uint32_t id_tt = idesc_bf16_f32(128, 64, 1, 1);  // A [K x rows], B [K x cols]
   const uint64_t once = policy_evict_first();
   auto load_kq = [&](int c) {
     uint64_t* bar = kq_full + (c & 1);
@@ -266,17 +263,13 @@ __global__ void __launch_bounds__(256, 1)
     }
   };
   auto load_t = [&](int c) {
-    const int64_t tile = ((int64_t)p * n + c) * (2 * kBox);
+    const int64_t tile = (p * n + c) * (2 * kBox);
     mbar_arrive_expect_tx(t_full, 4 * kBox);
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       bulk_load(sm + L::oT + h * L::kT, a.t + tile + h * kBox, kBox, t_full);
       bulk_load(sm + L::oT + h * L::kT + kBox, a.pt + tile + h * kBox, kBox, t_full);
     }
-  };
-  auto load_v = [&](int c) {
-    mbar_arrive_expect_tx(v_full, kBox);
-    tma_load_3d(sm + L::oV, &tm_v, v_full, c64, c * kCh, p, once);
   };
   // one warp: the gates, loaded a chunk before they are written
   float4 gb;
@@ -291,29 +284,22 @@ __global__ void __launch_bounds__(256, 1)
     write_gates(gates + (c & 1), lane, gb.x, gb.y, gb.z, gb.w);
     load_gates(c + 1);
   };
+  // lanes 0-63: the row of V, loaded a chunk ahead
+  const int64_t at = p * a.N * a.M + c0;
+  uint4 vv[2];
+  auto load_v = [&](int c) {
+    const int64_t row = (int64_t)c * kCh + t;
+    read16(a.v + at + row * a.M, nc, t < 64 && row < a.N, vv);
+  };
   if (threadIdx.x == 96) {
     load_kq(0);
     load_t(0);
-    load_v(0);
     if (n > 1) load_kq(1);
   }
   const bool row_on = t < a.D;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int c0 = c64 + 32 * sub + 16 * h;
-    float2 s[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.state_in != nullptr && row_on && c0 + 2 * j < a.M)
-        v = *reinterpret_cast<const float4*>(a.state_in + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j);
-      s[j] = make_float2(v.x, v.y);
-      s[j + 1] = make_float2(v.z, v.w);
-    }
-    tmem_st16(t_s + lane_col + 16 * h, s);
-    if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, s);
-  }
-  tmem_st_wait();
+  float2 S[8];
+  read16(a.state_in + (p * a.D + t) * a.M + c0, nc, a.state_in != nullptr && row_on, S);
+  load_v(0);
   if (warp == 7) {
     load_gates(0);
     put_gates(0);
@@ -322,6 +308,7 @@ __global__ void __launch_bounds__(256, 1)
   for (int c = 0; c < n; ++c) {
     const uint32_t kq = s_base + (c & 1) * L::kKQ, phase = c & 1;
     const GateSlot* gs = gates + (c & 1);
+    if (t < DP) store_parts(S_tile, t, sub, S);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -330,32 +317,33 @@ __global__ void __launch_bounds__(256, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<DP / 16, false, true>(el, t_kqs, kq, S_addr, id_nt128, 16, L::kS, L::kKQBox, 0, true);
+      mma_tile<DP / 16, false, true>(el, t_kqs, kq, S_addr, id_nt, 16, 16, L::kKQBox, 0, true);
       if (el) mma_commit(done);
     }
+    const int64_t kept = (p * n + c) * gridDim.y + blockIdx.y;
     if (KEEP && threadIdx.x == 128) {
-      const int at = (p * n + c) * 2;
-      tma_store_3d(&tm_s, S_hi, c64, 0, at);
-      tma_store_3d(&tm_s, S_lo, c64, 0, at + 1);
+      bulk_store(a.keep_s + kept * (DP * 128), S_tile, DP * 128);
       tma_store_commit();
     }
-    wait_or_abort(v_full, phase, a.status, abort_flag);
     wait_or_abort(done, phase, a.status, abort_flag);
     tc_fence_after();
+    float2 x[8];
+    load16_sum(t_kqs + lane_col, x);
     if (t < 64) {
       const float2 b = both(gs->b[t]), bg = both(-gs->b[t] * gs->gam[t]);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 v[8], r[8];
-        get16(sm + L::oV, t, 4 * sub + 2 * h, v);
-        load16_sum(t_kqs + lane_col + 16 * h, r);
+      float2 v[8];
+      unpack16(vv, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = fma2(bg, r[j], mul2(b, v[j]));
-        store16_split(R_hi, R_lo, t, 4 * sub + 2 * h, r);
-      }
+      for (int j = 0; j < 8; ++j) x[j] = fma2(bg, x[j], mul2(b, v[j]));
+      store_parts(R_tile, t, sub, x);
+      if (c + 1 < n) load_v(c + 1);
+    } else {
+      const float2 gam = both(a.scale * gs->gam[t - 64]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = mul2(gam, x[j]);  // waits for P U
     }
-    // the stores out of the S, O and U tiles have read them
-    if (threadIdx.x == 128) tma_store_wait_read_all();
+    // the copies out of the S and U tiles have read them
+    if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -364,37 +352,29 @@ __global__ void __launch_bounds__(256, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<4, true, true>(el, t_tr, T_addr, R_addr, id_tt128, kBox, kBox, 0, 0, true);
-      mma_tile<4, true, true>(el, t_tr, T_addr + L::kT, R_addr, id_tt128, kBox, kBox, 0, 0, false);
+      mma_tile<4, true, true>(el, t_tr, T_addr, R_addr, id_tt, kBox, 16, 0, 0, true);
+      mma_tile<4, true, true>(el, t_tr, T_addr + L::kT, R_addr, id_tt, kBox, 16, 0, 0, false);
       if (el) mma_commit(done + 1);
     }
-    if (threadIdx.x == 96 && c + 1 < n) load_v(c + 1);
     if (warp == 7 && c + 1 < n) put_gates(c + 1);
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
-    if (t < 64) {
-      const float2 del = both(gs->del[t]);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 r[8];
-        load16_sum(t_tr + lane_col + 16 * h, r);
-        if (KEEP) store16_split(sm + L::oU, sm + L::oU + kBox, t, 4 * sub + 2 * h, r);
+    {
+      const int64_t row = (int64_t)c * kCh + (t & 63);
+      float2 r[8];
+      load16_sum(t_tr + lane_col, r);
+      if (t < 64) {
+        if (KEEP) store_parts(sm + L::oU, t, sub, r);
+        const float2 del = both(gs->del[t]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = mul2(del, r[j]);
-        store16_split(R_hi, R_lo, t, 4 * sub + 2 * h, r);
-      }
-    } else {
-      const float2 gam = both(a.scale * gs->gam[t - 64]);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 r[8], qs[8];
-        load16_sum(t_tr + lane_col + 16 * h, r);
-        load16_sum(t_kqs + lane_col + 16 * h, qs);
+        store_parts(R_tile, t, sub, r);
+      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = fma2(gam, qs[j], r[j]);
+        for (int j = 0; j < 8; ++j) r[j] = add2(x[j], r[j]);
         uint4 w[2];
         pack16(r, w);
-        put16(sm + L::oO, t - 64, 4 * sub + 2 * h, w);
+        if (row < a.N) write16(a.out + at + row * a.M, nc, w);
       }
     }
     fence_proxy_async_smem();
@@ -406,57 +386,31 @@ __global__ void __launch_bounds__(256, 1)
       // K^T: 64 columns of K to a 64-lane block; with one such block the
       // lanes past 64 take Q's, and are not read
       constexpr uint32_t lbo = DP == 128 ? L::kKQBox : kBox;
-      mma_tile<4, true, true>(el, t_tr, kq, R_addr, id_tt128, lbo, kBox, 0, 0, true);
+      mma_tile<4, true, true>(el, t_tr, kq, R_addr, id_tt, lbo, 16, 0, 0, true);
       if (el) mma_commit(done + 2);
     }
-    if (threadIdx.x == 96 && c + 1 < n) load_t(c + 1);
-    if (threadIdx.x == 128) {
-      tma_store_3d(&tm_o, sm + L::oO, c64, c * kCh, p);
-      if (KEEP) {
-        tma_store_3d(&tm_u, sm + L::oU, c64, c * kCh, p);
-        tma_store_3d(&tm_u, sm + L::oU + kBox, c64, c * kCh, a.BH + p);
-      }
+    if (KEEP && threadIdx.x == 128) {
+      bulk_store(a.keep_u + kept * kBox, sm + L::oU, kBox);
       tma_store_commit();
     }
+    if (threadIdx.x == 96 && c + 1 < n) load_t(c + 1);
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
     if (threadIdx.x == 96 && c + 2 < n) load_kq(c + 2);
     const float2 last = both(gs->gam[kCh - 1]);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float2 r[8], s[8];
-      load16_sum(t_tr + lane_col + 16 * h, r);
-      tmem_ld16(t_s + lane_col + 16 * h, s);
+    load16_sum(t_tr + lane_col, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = fma2(last, s[j], r[j]);
-      tmem_st16(t_s + lane_col + 16 * h, s);
-      if (t < DP) store16_split(S_hi, S_lo, t, 4 * sub + 2 * h, s);
-    }
-    tmem_st_wait();
+    for (int j = 0; j < 8; ++j) S[j] = fma2(last, S[j], x[j]);
   }
-  if (a.state_out != nullptr) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int c0 = c64 + 32 * sub + 16 * h;
-      float2 s[8];
-      tmem_ld16(t_s + lane_col + 16 * h, s);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2)
-        if (row_on && c0 + 2 * j < a.M)
-          *reinterpret_cast<float4*>(a.state_out + ((int64_t)p * a.D + t) * a.M + c0 + 2 * j) =
-              make_float4(s[j].x, s[j].y, s[j + 1].x, s[j + 1].y);
-    }
-  }
-  if (threadIdx.x == 128) {
-    tma_store_wait_all();
-    // every load and MMA has been waited for by the loop that used it
-    if (*abort_flag) linger();
-  }
+  if (a.state_out != nullptr && row_on) write16(a.state_out + (p * a.D + t) * a.M + c0, nc, S);
+  if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
+  // every load and MMA has been waited for by the loop that used it
+  if (*abort_flag) linger();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 128);
   }
 }
 
@@ -487,24 +441,25 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
   a.status = status;
   a.N = s.N; a.n_chunks = (int)k.n; a.H = (int)s.H; a.group = (int)(s.H / s.Hk); a.scale = s.scale;
   FwdArgs c{};
+  c.v = static_cast<const __nv_bfloat16*>(f.v);
+  c.out = static_cast<__nv_bfloat16*>(f.out);
+  if (KEEP) {
+    c.keep_s = kept;
+    c.keep_u = kept + k.s_bytes;
+  }
   c.g = f.g; c.beta = f.beta; c.state_in = f.state_in; c.t = a.t; c.pt = a.pt;
   c.state_out = f.state_out; c.status = status;
-  c.N = s.N; c.n_chunks = (int)k.n; c.BH = (int)BH; c.H = a.H; c.group = a.group;
+  c.N = s.N; c.n_chunks = (int)k.n; c.H = a.H; c.group = a.group;
   c.D = (int)s.D; c.M = (int)s.M; c.scale = s.scale;
   // (encoding a map needs the device's context current in this thread: the
   // calls above see to that)
-  CUtensorMap m[6];
-  if (!make_chunk_map(&m[0], f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&m[1], f.k, s.B * s.Hk, s.N, s.D) ||
-      !make_chunk_map(&m[2], f.v, BH, s.N, s.M) || !make_chunk_map(&m[3], f.out, BH, s.N, s.M))
+  CUtensorMap mq, mk;
+  if (!make_chunk_map(&mq, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&mk, f.k, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
-  m[4] = m[5] = m[3];
-  if (KEEP && (!make_chunk_map(&m[4], kept, BH * k.n * 2, s.D, s.M, DP) ||
-               !make_chunk_map(&m[5], kept + k.s_bytes, 2 * BH, s.N, s.M)))
-    return CP_ERR_CUDA;
-  prep<<<(unsigned)(BH * k.n), 128, LP::kBytes, stream>>>(m[0], m[1], a);
+  prep<<<(unsigned)(BH * k.n), 128, LP::kBytes, stream>>>(mq, mk, a);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
-  const dim3 grid((unsigned)BH, (unsigned)((s.M + 63) / 64));
-  chain<<<grid, 256, L::kBytes, stream>>>(m[0], m[1], m[2], m[3], m[4], m[5], c);
+  const dim3 grid((unsigned)BH, (unsigned)((s.M + kCB - 1) / kCB));
+  chain<<<grid, 256, L::kBytes, stream>>>(mq, mk, c);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
