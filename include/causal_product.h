@@ -463,8 +463,8 @@ CP_API cp_status_t causal_product_decode_delta(const void* q, const void* k, con
  * projection's token-major rows are read where they are.  wq, wk: [D] in
  * `dtype`, NULL for ones.  cos, sin: [N][R/2] fp32 for each batch, cs_batch
  * elements apart (0: one table for all; R = 0: may be NULL).  q, k: dense
- * [B][H][N][D] in `dtype`, 16-byte aligned.  D a multiple of 8, 8 .. 256; eps
- * finite, >= 0 (with eps = 0 a zero row gives NaN).  fp32 arithmetic, rounded
+ * [B][H][N][D] in `dtype`, 16-byte aligned.  D a multiple of 8, 8 .. 256; at
+ * most 2^31 rows; eps finite, >= 0 (with eps = 0 a zero row gives NaN).  fp32 arithmetic, rounded
  * once.  Outputs overlap nothing.
  *
  * Backward, from grad_q, grad_k (dense as q, k): grad_xq, grad_xk, dense

@@ -77,6 +77,8 @@ def library_path() -> str:
 def load_library(rebuild: bool = True) -> ctypes.CDLL:
     """Load the C ABI library (building it first if its sources changed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if rebuild else _build.LIB
@@ -724,16 +726,38 @@ def causal_product_noalloc_status(stream: Optional[torch.cuda.Stream] = None,
     return int(load_library().causal_product_noalloc_status(_stream_ptr(stream, dev)))
 
 
+def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    # (torch.cuda.current_stream builds a Stream object: 2 us of a 10 us step)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _all_plain(device: int, *ts: torch.Tensor) -> bool:
+    for t in ts:
+        if t.get_device() != device or not t.is_contiguous():
+            return False
+    return device >= 0
+
+
+def _check_plain(device: int, *ts: torch.Tensor):
+    """_check_device, for the calls whose time is that of their checks."""
+    if not _all_plain(device, *ts):
+        _check_device(*ts)
+
+
 def _delta_dims(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                 beta: torch.Tensor):
-    if (q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[0] != q.shape[0]
-            or v.shape[2] != q.shape[2] or q.shape[1] == 0 or v.shape[1] % q.shape[1] != 0):
+    qs, vs = q.shape, v.shape
+    if (len(qs) != 4 or k.shape != qs or len(vs) != 4 or vs[0] != qs[0] or vs[2] != qs[2]
+            or qs[1] == 0 or vs[1] % qs[1] != 0):
         raise ValueError(f"expected q,k [B,Hk,N,D] and v [B,H,N,M], H a multiple of Hk; got "
-                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    B, Hk, N, D = q.shape
-    H, M = v.shape[1], v.shape[3]
-    _check_like(g, (B, H, N), torch.float32, "g")
-    _check_like(beta, (B, H, N), torch.float32, "beta")
+                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
+    B, Hk, N, D = qs
+    H, M = vs[1], vs[3]
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t.shape != (B, H, N) or t.dtype is not torch.float32:
+            _check_like(t, (B, H, N), torch.float32, name)
     return B, H, Hk, N, D, M
 
 
@@ -777,10 +801,13 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     ``save`` (written into ``ckpt`` when given)."""
     B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
     code = _dtype_code(q, k, v)
+    dev = v.get_device()
     if out is None:
-        out = torch.empty((B, H, N, M), dtype=v.dtype, device=v.device)
-    _check_like(out, (B, H, N, M), v.dtype, "out")
-    _check_device(q, k, v, g, beta, out)
+        _check_plain(dev, q, k, v, g, beta)
+        out = torch.empty_like(v)
+    else:
+        _check_like(out, (B, H, N, M), v.dtype, "out")
+        _check_plain(dev, q, k, v, g, beta, out)
     if return_state and state_out is None:
         state_out = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
     lib = load_library()
@@ -794,7 +821,7 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         _state_arg(state_out, (B, H, D, M), v.device, "state_out"),
         0 if ckpt is None else ckpt.data_ptr(), 0 if ckpt is None else ckpt.numel() * 4,
         float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
-        _stream_ptr(stream, v.device))
+        _raw_stream(stream, dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_fwd_delta")
     got = (out,) + ((state_out,) if return_state else ()) + ((ckpt,) if save else ())
@@ -837,7 +864,8 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         t = torch.empty_like(ref) if t is None else t
         _check_like(t, ref.shape, ref.dtype, name)
         outs.append(t)
-    _check_device(q, k, v, g, beta, grad_out, *outs)
+    dev = v.get_device()
+    _check_plain(dev, q, k, v, g, beta, grad_out, *outs)
     if return_state_grad and grad_state_in is None:
         grad_state_in = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
     if ckpt is None:
@@ -854,7 +882,7 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         *(t.data_ptr() for t in outs),
         _state_arg(grad_state_in, shape, v.device, "grad_state_in"),
         float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
-        _stream_ptr(stream, v.device))
+        _raw_stream(stream, dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_bwd_delta")
     return tuple(outs) + ((grad_state_in,) if return_state_grad else ())
@@ -872,30 +900,37 @@ def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     state; one outside [0, P) is an idle row (out zero, no state touched).
     Without ``slots`` sequence b has state b.  No two sequences may share a
     slot."""
-    if (q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0]
-            or q.shape[1] == 0 or v.shape[1] % q.shape[1] != 0):
+    qs, vs = q.shape, v.shape
+    if (len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or qs[1] == 0
+            or vs[1] % qs[1] != 0):
         raise ValueError(f"expected q,k [B,Hk,D] and v [B,H,M], H a multiple of Hk; got "
-                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    B, Hk, D = q.shape
-    H, M = v.shape[1], v.shape[2]
+                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
+    B, Hk, D = qs
+    _, H, M = vs
     code = _dtype_code(q, k, v)
+    for t, name in ((g, "g"), (beta, "beta")):
+        if t.shape != (B, H) or t.dtype is not torch.float32:
+            _check_like(t, (B, H), torch.float32, name)
+    dev = q.get_device()
     if out is None:
-        out = torch.empty((B, H, M), dtype=v.dtype, device=v.device)
-    _check_like(out, (B, H, M), v.dtype, "out")
-    _check_like(g, (B, H), torch.float32, "g")
-    _check_like(beta, (B, H), torch.float32, "beta")
-    _check_device(q, k, v, g, beta, out, state)
-    P = state.shape[0] if state.dim() == 4 else 0
-    _state_arg(state, (P, H, D, M), v.device, "state")
+        _check_plain(dev, q, k, v, g, beta, state)
+        out = torch.empty_like(v)
+    else:
+        _check_like(out, vs, v.dtype, "out")
+        _check_plain(dev, q, k, v, g, beta, state, out)
+    ss = state.shape
+    if len(ss) != 4 or ss[1:] != (H, D, M) or state.dtype is not torch.float32:
+        _check_like(state, (ss[0] if len(ss) == 4 else 0, H, D, M), torch.float32, "state")
+    P = ss[0]
     if slots is not None:
         _check_like(slots, (B,), torch.int32, "slots")
-        _check_device(q, slots)
+        _check_plain(dev, q, slots)
     elif P < B:
         raise ValueError(f"state holds {P} sequences, fewer than the {B} of this call")
     rc = load_library().causal_product_decode_delta(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
-        state.data_ptr(), 0 if slots is None else slots.data_ptr(), P, float(scale), B, H, Hk, D, M,
-        code, _stream_ptr(stream, v.device))
+        state.data_ptr(), 0 if slots is None else slots.data_ptr(), P, scale, B, H, Hk, D, M,
+        code, _raw_stream(stream, dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_decode_delta")
     return out
@@ -904,50 +939,65 @@ def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
 class _QkRope:
     """Checked arguments of the q/k norm with rotation, as the C ABI takes them."""
 
+    __slots__ = ("head", "tail", "q_shape", "k_shape", "code", "dev")
+
     def __init__(self, xq, xk, wq, wk, cos, sin, norm, eps):
-        if (xq.dim() != 4 or xk.dim() != 4 or xk.shape[0] != xq.shape[0]
-                or xk.shape[2:] != xq.shape[2:]):
-            raise ValueError(f"expected xq [B,Hq,N,D] and xk [B,Hk,N,D]; got {tuple(xq.shape)}, "
-                             f"{tuple(xk.shape)}")
+        qs, ks = xq.shape, xk.shape
+        if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[2:] != qs[2:]:
+            raise ValueError(f"expected xq [B,Hq,N,D] and xk [B,Hk,N,D]; got {tuple(qs)}, {tuple(ks)}")
         if norm not in QK_NORMS:
             raise ValueError(f"unknown norm {norm!r}; expected one of {list(QK_NORMS)}")
         if (cos is None) != (sin is None):
             raise ValueError("cos and sin are given together")
-        B, Hq, N, D = xq.shape
-        Hk = xk.shape[1]
-        self.code = _dtype_code(xq, xk, *(w for w in (wq, wk) if w is not None))
+        B, Hq, N, D = qs
+        plain = []
+        weights = []
         for w, name in ((wq, "wq"), (wk, "wk")):
             if w is not None:
-                _check_like(w, (D,), xq.dtype, name)
-        half = 0 if cos is None else cos.shape[-1]
-        tables = [] if cos is None else [cos, sin]
-        for t, name in zip(tables, ("cos", "sin")):
-            if t.dtype != torch.float32 or tuple(t.shape) not in ((N, half), (1, N, half),
-                                                                   (B, N, half)):
-                raise ValueError(f"{name} must be float32 of shape [N,R/2] or [B,N,R/2]; got "
-                                 f"{t.dtype} {tuple(t.shape)}")
-        if tables and sin.shape != cos.shape:
-            raise ValueError("cos and sin must have the same shape")
-        weights = [w for w in (wq, wk) if w is not None]
-        if xq.device.type != "cuda":
+                weights.append(w)
+                if w.shape != (D,) or w.dtype is not xq.dtype:
+                    _dtype_code(xq, w)
+                    _check_like(w, (D,), xq.dtype, name)
+        self.code = _dtype_code(xq, xk)
+        half, per_batch = 0, 0
+        if cos is not None:
+            cs = cos.shape
+            half = cs[-1] if len(cs) > 1 else -1
+            if (cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or sin.shape != cs
+                    or cs not in ((N, half), (1, N, half), (B, N, half))):
+                raise ValueError(f"cos and sin must be float32 of one shape, [N,R/2] or [B,N,R/2]; got "
+                                 f"{cos.dtype} {tuple(cs)}, {sin.dtype} {tuple(sin.shape)}")
+            plain = [cos, sin]
+            if len(cs) == 3 and B > 1 and cs[0] == B:
+                per_batch = N * half
+        self.dev = xq.get_device()
+        if self.dev < 0:
             raise RuntimeError("causal_product runs on CUDA tensors only (no CPU path)")
-        if xk.device != xq.device:
+        if xk.get_device() != self.dev:
             raise RuntimeError("all tensors must be on the same CUDA device")
-        if weights + tables:
-            _check_device(*weights, *tables)
-            if (weights + tables)[0].device != xq.device:
-                raise RuntimeError("all tensors must be on the same CUDA device")
-        for x, name in ((xq, "xq"), (xk, "xk")):
-            if x.stride(3) != 1 and D > 1:
-                raise ValueError(f"the rows of {name} must be dense (stride 1 in the last dimension)")
-        strides = ctypes.c_int64 * 3
-        per_batch = cos is not None and cos.dim() == 3 and cos.shape[0] == B and B > 1
-        ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-        self.head = (xq.data_ptr(), strides(*xq.stride()[:3]), xk.data_ptr(),
-                     strides(*xk.stride()[:3]), ptr(wq), ptr(wk), ptr(cos), ptr(sin),
-                     N * half if per_batch else 0)
-        self.tail = (QK_NORMS[norm], float(eps), B, Hq, Hk, N, D, 2 * half, self.code)
-        self.q_shape, self.k_shape = (B, Hq, N, D), (B, Hk, N, D)
+        plain += weights
+        if plain and not _all_plain(self.dev, *plain):
+            _check_device(*plain)
+            raise RuntimeError("all tensors must be on the same CUDA device")
+        sq, sk = xq.stride(), xk.stride()
+        if (sq[3] != 1 or sk[3] != 1) and D > 1:
+            raise ValueError("the rows of xq and xk must be dense (stride 1 in the last dimension)")
+        self.head = (xq.data_ptr(), _Strides(*sq[:3]), xk.data_ptr(), _Strides(*sk[:3]),
+                     0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(),
+                     0 if cos is None else cos.data_ptr(), 0 if sin is None else sin.data_ptr(),
+                     per_batch)
+        self.tail = (QK_NORMS[norm], eps, B, Hq, ks[1], N, D, 2 * half, self.code)
+        self.q_shape, self.k_shape = qs, ks
+
+    def dense(self, t, shape, dtype, name):
+        if t.shape != shape or t.dtype is not dtype:
+            _check_like(t, shape, dtype, name)
+        if t.get_device() != self.dev or not t.is_contiguous():
+            _check_device(t)
+            raise RuntimeError("all tensors must be on the same CUDA device")
+
+
+_Strides = ctypes.c_int64 * 3
 
 
 def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor] = None,
@@ -963,15 +1013,16 @@ def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torc
     strided views (rows dense): a projection's ``x.view(B,N,H,D).transpose(1,
     2)`` is read in place.  q and k come dense."""
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
-    q = torch.empty(a.q_shape, dtype=xq.dtype, device=xq.device) if q is None else q
-    k = torch.empty(a.k_shape, dtype=xq.dtype, device=xq.device) if k is None else k
-    _check_like(q, a.q_shape, xq.dtype, "q")
-    _check_like(k, a.k_shape, xq.dtype, "k")
-    _check_device(q, k)
-    if q.device != xq.device:
-        raise RuntimeError("all tensors must be on the same CUDA device")
+    if q is None:
+        q = torch.empty_like(xq, memory_format=torch.contiguous_format)
+    else:
+        a.dense(q, a.q_shape, xq.dtype, "q")
+    if k is None:
+        k = torch.empty_like(xk, memory_format=torch.contiguous_format)
+    else:
+        a.dense(k, a.k_shape, xq.dtype, "k")
     rc = load_library().causal_product_qk_rope(*a.head, q.data_ptr(), k.data_ptr(), *a.tail,
-                                               _stream_ptr(stream, xq.device))
+                                               _raw_stream(stream, a.dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_qk_rope")
     return q, k
@@ -987,11 +1038,8 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     causal_product_qk_rope; dxq and dxk dense, dwq and dwk None where the
     weight is."""
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
-    _check_like(grad_q, a.q_shape, xq.dtype, "grad_q")
-    _check_like(grad_k, a.k_shape, xq.dtype, "grad_k")
-    _check_device(grad_q, grad_k)
-    if grad_q.device != xq.device:
-        raise RuntimeError("all tensors must be on the same CUDA device")
+    a.dense(grad_q, a.q_shape, xq.dtype, "grad_q")
+    a.dense(grad_k, a.k_shape, xq.dtype, "grad_k")
     dxq, dxk = torch.empty_like(grad_q), torch.empty_like(grad_k)
     dwq = None if wq is None else torch.empty_like(wq)
     dwk = None if wk is None else torch.empty_like(wk)
@@ -1002,7 +1050,7 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     rc = lib.causal_product_qk_rope_bwd(
         *a.head, grad_q.data_ptr(), grad_k.data_ptr(), dxq.data_ptr(), dxk.data_ptr(),
         0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), *a.tail,
-        workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, xq.device))
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, a.dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_qk_rope_bwd")
     return dxq, dxk, dwq, dwk

@@ -1238,8 +1238,9 @@ cp_status_t check_qk_rope(const QkRope& f, cp_qk_norm_t norm) {
     return CP_ERR_UNSUPPORTED_DTYPE;
   if (f.D < 8 || f.D > 256 || f.D % 8 != 0 || f.R < 0 || f.R > f.D || f.R % 2 != 0)
     return CP_ERR_UNSUPPORTED_SHAPE;
+  // rows are counted in 32 bits
   if (std::max(f.Hq, f.Hk) > 1 << 16 || f.B * std::max(f.Hq, f.Hk) > (int64_t)1 << 24 ||
-      f.N > (int64_t)1 << 31)
+      f.B * std::max(f.Hq, f.Hk) * f.N > (int64_t)1 << 31)
     return CP_ERR_UNSUPPORTED_SHAPE;
   if (norm != CP_QK_NORM_RMS && norm != CP_QK_NORM_L2) return CP_ERR_INVALID_ARG;
   if (!(f.eps >= 0.f) || !std::isfinite(f.eps) || f.cs_batch < 0) return CP_ERR_INVALID_ARG;

@@ -90,6 +90,10 @@ __global__ void __launch_bounds__(kThreads)
     const int d = rg + r * RG;
     if (on && d < D) st[r] = ld_state<STREAM, V>(S + (int64_t)d * M + c);
   }
+  // everything else the step reads goes out behind the state, before any use
+  float vv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) vv[i] = on ? ld_f32<T>(v + p * M + c + i) : 0.f;
   const float a = expf(g[p]), bt = beta[p];
   float sk[V] = {}, sq[V] = {}, kq = 0.f, kd[ROWS];
 #pragma unroll
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kThreads)
       x += part[0][s][cg * V + i];
       y += part[1][s][cg * V + i];
     }
-    u[i] = on ? bt * (ld_f32<T>(v + p * M + c + i) - a * x) : 0.f;
+    u[i] = bt * (vv[i] - a * x);
     o[i] = scale * fmaf(dot, u[i], a * y);
   }
   if (!on) return;
