@@ -3,10 +3,14 @@
 // not take (D > 128).  The formulas are in cp_delta.cuh.
 //
 // Forward: one CTA per (head, block of MB value columns) walks the sequence in
-// chunks of 32 rows with the D x MB state in shared memory; the value columns
-// of a head never meet, so a block of them is a problem of its own.  A chunk is
-// six small products on shared-memory tiles and a triangular solve by
-// substitution, one thread per value column.
+// chunks of 32 rows with the MB x D state, transposed, in shared memory; the
+// value columns of a head never meet, so a block of them is a problem of its
+// own.  A chunk is six small products on shared-memory tiles and a triangular
+// solve by substitution, a lane to a row.  Tiles lie so that both operands of a
+// product run along its contraction and load 16 bytes at a time; the rows of
+// the next chunk are loaded under the solve.  What bounds the walk is the
+// latency of its steps on the few SMs a small batch fills: about 11,000 cycles
+// a chunk, half of them issue slots (FP32 D = M = 64, 8 heads, N = 509: 107 us).
 //
 // Backward: the same walk in reverse with the state's gradient in shared
 // memory, from the states the forward left before each chunk:
@@ -32,42 +36,84 @@ namespace {
 
 using namespace delta;
 
-constexpr int kThreads = 256;
-constexpr int kC = 32;  // rows of a chunk
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kC = 32;        // rows of a chunk
+constexpr int kLdc = kC + 4;  // pitch of a tile with a chunk's rows along its columns
 
-// out(i, j) = sum_k a(i, k) b(k, j) for i < R, j < N over the CTA: warp w takes
-// rows w, w + 8, .., lane l columns l, l + 32, ..; a is read as a broadcast and
-// b by consecutive lanes (rows of odd pitch keep either orientation free of
-// bank conflicts).
-template <int RT, int CT, class FA, class FB, class FE>
-__device__ __forceinline__ void mm(int R, int N, int K, FA a, FB b, FE e) {
-  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
-  for (int i0 = w; i0 < R; i0 += 8 * RT) {
-    for (int j0 = l; j0 < N; j0 += 32 * CT) {
-      float acc[RT][CT] = {};
-      int ii[RT], jj[CT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) ii[r] = min(i0 + 8 * r, R - 1);
-#pragma unroll
-      for (int c = 0; c < CT; ++c) jj[c] = min(j0 + 32 * c, N - 1);
+// Pitch of a tile row of n floats: a multiple of 16 bytes whose number of
+// 16-byte words is odd, so that eight rows' words fall in different banks.
+__host__ __device__ __forceinline__ int pitch(int n) { return 4 * (((n + 3) / 4) | 1); }
+
+// Where a thread's outputs of a [kC] x [MB] product lie: LC lanes along the
+// columns, RT consecutive rows and CT columns LC apart to a thread.
+template <int MB>
+struct Place {
+  static constexpr int LC = MB < 32 ? MB : 32, CT = MB / LC, RT = LC / 16;
+  int row, col;
+  __device__ __forceinline__ Place() {
+    const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+    row = (w * (32 / LC) + l / LC) * RT;
+    col = l % LC;
+  }
+};
+
+__device__ __forceinline__ void fma4(float& acc, float4 a, float4 b) {
+  acc = fmaf(a.x, b.x, acc);
+  acc = fmaf(a.y, b.y, acc);
+  acc = fmaf(a.z, b.z, acc);
+  acc = fmaf(a.w, b.w, acc);
+}
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// acc[r][c] += sum_k a[row + r][k] b[col + LC c][k], k < n (a multiple of 4):
+// both operands run along the contraction in 16-byte loads.
+template <int MB>
+__device__ __forceinline__ void dot(float (&acc)[Place<MB>::RT][Place<MB>::CT], const Place<MB>& at,
+                                    const float* a, int lda, const float* b, int ldb, int n) {
+  constexpr int RT = Place<MB>::RT, CT = Place<MB>::CT, LC = Place<MB>::LC;
+  a += at.row * lda;
+  b += at.col * ldb;
 #pragma unroll 4
-      for (int k = 0; k < K; ++k) {
-        float av[RT], bv[CT];
+  for (int k = 0; k < n; k += 4) {
+    float4 av[RT], bv[CT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) av[r] = a(ii[r], k);
+    for (int r = 0; r < RT; ++r) av[r] = at4(a + r * lda + k);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) bv[c] = b(k, jj[c]);
+    for (int c = 0; c < CT; ++c) bv[c] = at4(b + c * LC * ldb + k);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
-      }
+      for (int c = 0; c < CT; ++c) fma4(acc[r][c], av[r], bv[c]);
+  }
+}
+// the same for two left operands over one right one
+template <int MB>
+__device__ __forceinline__ void dot2(float (&acc)[Place<MB>::RT][Place<MB>::CT],
+                                     float (&acc2)[Place<MB>::RT][Place<MB>::CT],
+                                     const Place<MB>& at, const float* a, const float* a2, int lda,
+                                     const float* b, int ldb, int n) {
+  constexpr int RT = Place<MB>::RT, CT = Place<MB>::CT, LC = Place<MB>::LC;
+  a += at.row * lda;
+  a2 += at.row * lda;
+  b += at.col * ldb;
+#pragma unroll 4
+  for (int k = 0; k < n; k += 4) {
+    float4 av[RT], aw[RT], bv[CT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          if (i0 + 8 * r < R && j0 + 32 * c < N) e(ii[r], jj[c], acc[r][c]);
+    for (int r = 0; r < RT; ++r) {
+      av[r] = at4(a + r * lda + k);
+      aw[r] = at4(a2 + r * lda + k);
     }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) bv[c] = at4(b + c * LC * ldb + k);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        fma4(acc[r][c], av[r], bv[c]);
+        fma4(acc2[r][c], aw[r], bv[c]);
+      }
   }
 }
 
@@ -82,393 +128,567 @@ struct Args {
   float scale;
 };
 
-// rows [i0, i0 + 32) of a [N][ncol] matrix (columns [c0, c0 + nc)) as fp32
-// rows of pitch ld; rows past N are zero
+// A chunk's rows of q or k on their way to shared memory: the first 128
+// columns wait in registers, loaded while the chunk before is worked on.
 template <typename T>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t i0, int64_t N,
-                                          int ncol, int c0, int nc) {
-  for (int e = threadIdx.x; e < kC * nc; e += kThreads) {
-    const int i = e / nc, c = e % nc;
-    dst[i * ld + c] = i0 + i < N ? ld_f32<T>(src + (i0 + i) * ncol + c0 + c) : 0.f;
+struct Rows {
+  T x[2][4];
+  __device__ __forceinline__ void fetch(const T* src, int64_t i0, int64_t N, int D) {
+    const int i = threadIdx.x / 32 * 2, l = threadIdx.x % 32;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[r][c] = i0 + i + r < N && l + 32 * c < D ? src[(i0 + i + r) * D + l + 32 * c]
+                                                   : from_f32<T>(0.f);
   }
-}
+  // rows past N and columns from D to the next multiple of 4 are zero
+  __device__ __forceinline__ void put(float* dst, int ld, const T* src, int64_t i0, int64_t N,
+                                      int D) {
+    const int i = threadIdx.x / 32 * 2, l = threadIdx.x % 32, Dp = (D + 3) & ~3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (l + 32 * c < Dp) dst[(i + r) * ld + l + 32 * c] = ld_f32<T>(&x[r][c]);
+#pragma unroll 1
+      for (int c = l + 128; c < Dp; c += 32)
+        dst[(i + r) * ld + c] =
+            i0 + i + r < N && c < D ? ld_f32<T>(src + (i0 + i + r) * D + c) : 0.f;
+    }
+  }
+};
+// A chunk's rows of a block of MB value columns, kept transposed: [MB][kLdc].
+template <typename T, int MB>
+struct Cols {
+  static constexpr int kN = kC * MB / kThreads;
+  T x[kN];
+  __device__ __forceinline__ void fetch(const T* src, int64_t i0, int64_t N, int M, int c0) {
+    const int c = threadIdx.x % MB;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+      const int64_t i = i0 + threadIdx.x / MB + u * (kThreads / MB);
+      x[u] = i < N && c0 + c < M ? src[i * M + c0 + c] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void put(float* dst) {
+#pragma unroll
+    for (int u = 0; u < kN; ++u)
+      dst[threadIdx.x % MB * kLdc + threadIdx.x / MB + u * (kThreads / MB)] = ld_f32<T>(&x[u]);
+  }
+};
 
-struct Gates {
+struct alignas(16) Gates {
   float2 G[kC];   // running sums of the log decay
   float b[kC], gam[kC], del[kC];
   float last;     // gam of the last row
 };
 
+// by one warp
 __device__ __forceinline__ void load_gates(Gates& s, const float* g, const float* beta, int64_t i0,
                                            int64_t N) {
-  if (threadIdx.x < 32) {
-    const int i = threadIdx.x;
-    const bool on = i0 + i < N;
-    const float2 G = warp_scan(split_decay(on ? g[i0 + i] : 0.f), i);
-    const float2 E = make_float2(__shfl_sync(0xffffffffu, G.x, 31), __shfl_sync(0xffffffffu, G.y, 31));
-    const float2 zero = make_float2(0.f, 0.f);
-    s.G[i] = G;
-    s.b[i] = on ? beta[i0 + i] : 0.f;
-    s.gam[i] = decay_between(G, zero);
-    s.del[i] = decay_between(E, G);
-    if (i == 0) s.last = decay_between(E, zero);
+  const int i = threadIdx.x % 32;
+  const bool on = i0 + i < N;
+  const float2 G = warp_scan(split_decay(on ? g[i0 + i] : 0.f), i);
+  const float2 E = make_float2(__shfl_sync(0xffffffffu, G.x, 31), __shfl_sync(0xffffffffu, G.y, 31));
+  const float2 zero = make_float2(0.f, 0.f);
+  s.G[i] = G;
+  s.b[i] = on ? beta[i0 + i] : 0.f;
+  s.gam[i] = decay_between(G, zero);
+  s.del[i] = decay_between(E, G);
+  if (i == 0) s.last = decay_between(E, zero);
+}
+
+// (I + A) u = x in place for a warp's columns of x [MB][kLdc], at[j][i] = A_ij;
+// a lane holds a row, and each solved row leaves the rows below it at once.
+template <int MB>
+__device__ __forceinline__ void solve_down(float* x, const float* at) {
+  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+  float u[MB / kWarps];
+#pragma unroll
+  for (int c = 0; c < MB / kWarps; ++c) u[c] = x[(w + kWarps * c) * kLdc + l];
+#pragma unroll 8
+  for (int j = 0; j < kC - 1; ++j) {
+    const float a = at[j * kLdc + l];
+#pragma unroll
+    for (int c = 0; c < MB / kWarps; ++c) {
+      const float s = __shfl_sync(0xffffffffu, u[c], j);
+      if (l > j) u[c] = fmaf(-a, s, u[c]);
+    }
   }
+#pragma unroll
+  for (int c = 0; c < MB / kWarps; ++c) x[(w + kWarps * c) * kLdc + l] = u[c];
+}
+// and beside it (I + A)^T v = y from the last row up, a[j][i] = A_ji: two
+// chains of steps that do not wait for one another
+template <int MB>
+__device__ __forceinline__ void solve_both(float* x, const float* at, float* y, const float* a) {
+  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+  float u[MB / kWarps], v[MB / kWarps];
+#pragma unroll
+  for (int c = 0; c < MB / kWarps; ++c) {
+    u[c] = x[(w + kWarps * c) * kLdc + l];
+    v[c] = y[(w + kWarps * c) * kLdc + l];
+  }
+#pragma unroll 4
+  for (int j = 0; j < kC - 1; ++j) {
+    const int i = kC - 1 - j;
+    const float ad = at[j * kLdc + l], au = a[i * kLdc + l];
+#pragma unroll
+    for (int c = 0; c < MB / kWarps; ++c) {
+      const float s = __shfl_sync(0xffffffffu, u[c], j), t = __shfl_sync(0xffffffffu, v[c], i);
+      if (l > j) u[c] = fmaf(-ad, s, u[c]);
+      if (l < i) v[c] = fmaf(-au, t, v[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < MB / kWarps; ++c) {
+    x[(w + kWarps * c) * kLdc + l] = u[c];
+    y[(w + kWarps * c) * kLdc + l] = v[c];
+  }
+}
+
+// s[c][d] = D x MB block of a state, or zero; the padding of both is zero
+template <int MB>
+__device__ __forceinline__ void load_state(float* s, int ldd, const float* src, int D, int M,
+                                           int c0) {
+  const int Dp = (D + 3) & ~3, c = threadIdx.x % MB;
+  for (int d = threadIdx.x / MB; d < Dp; d += kThreads / MB)
+    s[c * ldd + d] = src != nullptr && d < D && c0 + c < M ? src[(int64_t)d * M + c0 + c] : 0.f;
+}
+template <int MB>
+__device__ __forceinline__ void store_state(float* dst, const float* s, int ldd, int D, int M,
+                                            int c0) {
+  const int c = threadIdx.x % MB;
+  if (c0 + c < M)
+    for (int d = threadIdx.x / MB; d < D; d += kThreads / MB)
+      dst[(int64_t)d * M + c0 + c] = s[c * ldd + d];
 }
 
 template <typename T, int MB>
 __global__ void __launch_bounds__(kThreads) delta_fwd_kernel(Args p) {
-  extern __shared__ float sm[];
-  const int D = p.D, M = p.M, ldd = D + 1;
-  constexpr int ldm = MB + 1, ldc = kC + 1;
-  float* S = sm;                 // [D][ldm]
-  float* K = S + D * ldm;        // [kC][ldd]
+  extern __shared__ __align__(16) float sm[];
+  using PM = Place<MB>;
+  using PC = Place<kC>;
+  const int D = p.D, M = p.M, ldd = pitch(D), Dp = (D + 3) & ~3;
+  float* S = sm;                 // [MB][ldd]
+  float* K = S + MB * ldd;       // [kC][ldd]
   float* Q = K + kC * ldd;       // [kC][ldd]
-  float* U = Q + kC * ldd;       // [kC][ldm]  V, then b R, then U
-  float* O = U + kC * ldm;       // [kC][ldm]
-  float* A = O + kC * ldm;       // [kC][ldc]
-  float* P = A + kC * ldc;       // [kC][ldc]
-  __shared__ Gates gt;
+  float* U = Q + kC * ldd;       // [MB][kLdc]  V, then b R, then U
+  float* At = U + MB * kLdc;     // [kC][kLdc]  A transposed
+  float* P = At + kC * kLdc;     // [kC][kLdc]
+  __shared__ Gates gates[2];
+  const int w = threadIdx.x / 32, l = threadIdx.x % 32;
   const int64_t p_ = blockIdx.x;
-  const int c0 = blockIdx.y * MB, nc = min(MB, M - c0);
+  const int c0 = blockIdx.y * MB;
   const int64_t N = p.N, pk = (p_ / p.H) * (p.H / p.group) + (p_ % p.H) / p.group;
   const T* q = static_cast<const T*>(p.q) + pk * N * D;
   const T* k = static_cast<const T*>(p.k) + pk * N * D;
   const T* v = static_cast<const T*>(p.v) + p_ * N * M;
+  const float *g = p.g + p_ * N, *beta = p.beta + p_ * N;
   T* out = static_cast<T*>(p.out) + p_ * N * M;
   const int64_t n_chunks = (N + kC - 1) / kC;
-  for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-    const int d = e / nc, c = e % nc;
-    S[d * ldm + c] = p.state_in != nullptr ? p.state_in[(p_ * D + d) * M + c0 + c] : 0.f;
-  }
+  const PM at;
+  const PC pair;
+  Rows<T> kr, qr;
+  Cols<T, MB> vr;
+  load_state<MB>(S, ldd, p.state_in != nullptr ? p.state_in + p_ * D * M : nullptr, D, M, c0);
+  kr.fetch(k, 0, N, D);
+  qr.fetch(q, 0, N, D);
+  vr.fetch(v, 0, N, M, c0);
+  if (w == kWarps - 1) load_gates(gates[0], g, beta, 0, N);
   for (int64_t ch = 0; ch < n_chunks; ++ch) {
     const int64_t i0 = ch * kC;
+    const Gates& gt = gates[ch & 1];
     __syncthreads();
-    load_rows<T>(K, ldd, k, i0, N, D, 0, D);
-    load_rows<T>(Q, ldd, q, i0, N, D, 0, D);
-    load_rows<T>(U, ldm, v, i0, N, M, c0, nc);
-    load_gates(gt, p.g + p_ * N, p.beta + p_ * N, i0, N);
-    if (p.ckpt != nullptr)
-      for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-        const int d = e / nc, c = e % nc;
-        p.ckpt[((p_ * n_chunks + ch) * D + d) * M + c0 + c] = S[d * ldm + c];
-      }
+    kr.put(K, ldd, k, i0, N, D);
+    qr.put(Q, ldd, q, i0, N, D);
+    vr.put(U);
+    if (p.ckpt != nullptr) store_state<MB>(p.ckpt + (p_ * n_chunks + ch) * D * M, S, ldd, D, M, c0);
     __syncthreads();
-    mm<4, 1>(kC, kC, D, [&](int i, int x) { return K[i * ldd + x]; },
-             [&](int x, int j) { return K[j * ldd + x]; }, [&](int i, int j, float a) {
-               A[i * ldc + j] = j < i ? gt.b[i] * decay_between(gt.G[i], gt.G[j]) * a : 0.f;
-             });
-    mm<4, 1>(kC, kC, D, [&](int i, int x) { return Q[i * ldd + x]; },
-             [&](int x, int j) { return K[j * ldd + x]; }, [&](int i, int j, float a) {
-               P[i * ldc + j] = j <= i ? p.scale * decay_between(gt.G[i], gt.G[j]) * a : 0.f;
-             });
-    mm<4, 2>(kC, nc, D, [&](int i, int x) { return K[i * ldd + x]; },
-             [&](int x, int j) { return S[x * ldm + j]; }, [&](int i, int j, float a) {
-               U[i * ldm + j] = gt.b[i] * (U[i * ldm + j] - gt.gam[i] * a);
-             });
-    mm<4, 2>(kC, nc, D, [&](int i, int x) { return Q[i * ldd + x]; },
-             [&](int x, int j) { return S[x * ldm + j]; },
-             [&](int i, int j, float a) { O[i * ldm + j] = p.scale * gt.gam[i] * a; });
-    __syncthreads();
-    if (threadIdx.x < nc) {
-      const int c = threadIdx.x;
-      float u[kC];
+    {
+      float kk[PC::RT][1] = {}, qk[PC::RT][1] = {};
+      dot2<kC>(kk, qk, pair, K, Q, ldd, K, ldd, Dp);
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        float x = U[i * ldm + c];
-#pragma unroll
-        for (int j = 0; j < i; ++j) x = fmaf(-A[i * ldc + j], u[j], x);
-        u[i] = x;
-        U[i * ldm + c] = x;
+      for (int r = 0; r < PC::RT; ++r) {
+        const int i = pair.row + r, j = pair.col;
+        const float e = j <= i ? decay_between(gt.G[i], gt.G[j]) : 0.f;
+        At[j * kLdc + i] = j < i ? gt.b[i] * e * kk[r][0] : 0.f;
+        P[i * kLdc + j] = j <= i ? p.scale * e * qk[r][0] : 0.f;
       }
     }
+    float o[PM::RT][PM::CT] = {};
+    {
+      float ks[PM::RT][PM::CT] = {};
+      dot2<MB>(ks, o, at, K, Q, ldd, S, ldd, Dp);
+#pragma unroll
+      for (int r = 0; r < PM::RT; ++r)
+#pragma unroll
+        for (int c = 0; c < PM::CT; ++c) {
+          const int i = at.row + r;
+          float* x = U + (at.col + PM::LC * c) * kLdc + i;
+          *x = gt.b[i] * (*x - gt.gam[i] * ks[r][c]);
+          o[r][c] *= p.scale * gt.gam[i];
+        }
+    }
     __syncthreads();
-    mm<4, 2>(kC, nc, kC, [&](int i, int x) { return P[i * ldc + x]; },
-             [&](int x, int j) { return U[x * ldm + j]; }, [&](int i, int j, float a) {
-               if (i0 + i < N) out[(i0 + i) * M + c0 + j] = from_f32<T>(O[i * ldm + j] + a);
-             });
-    mm<4, 2>(D, nc, kC, [&](int d, int x) { return K[x * ldd + d] * gt.del[x]; },
-             [&](int x, int j) { return U[x * ldm + j]; },
-             [&](int d, int j, float a) { S[d * ldm + j] = fmaf(gt.last, S[d * ldm + j], a); });
+    if (ch + 1 < n_chunks) {
+      kr.fetch(k, i0 + kC, N, D);
+      qr.fetch(q, i0 + kC, N, D);
+      vr.fetch(v, i0 + kC, N, M, c0);
+      if (w == kWarps - 1) load_gates(gates[(ch + 1) & 1], g, beta, i0 + kC, N);
+    }
+    solve_down<MB>(U, At);
+    __syncthreads();
+    dot<MB>(o, at, P, kLdc, U, kLdc, kC);
+#pragma unroll
+    for (int r = 0; r < PM::RT; ++r)
+#pragma unroll
+      for (int c = 0; c < PM::CT; ++c) {
+        const int64_t i = i0 + at.row + r;
+        const int j = c0 + at.col + PM::LC * c;
+        if (i < N && j < M) out[i * M + j] = from_f32<T>(o[r][c]);
+      }
+    // the state: lanes along its rows d, a warp's columns 16 apart
+#pragma unroll 1
+    for (int d = l; d < Dp; d += 32) {
+      float acc[MB / kWarps] = {};
+#pragma unroll
+      for (int x = 0; x < kC; x += 4) {
+        const float4 del = at4(gt.del + x);
+        const float4 kd = make_float4(K[x * ldd + d] * del.x, K[(x + 1) * ldd + d] * del.y,
+                                      K[(x + 2) * ldd + d] * del.z, K[(x + 3) * ldd + d] * del.w);
+#pragma unroll
+        for (int c = 0; c < MB / kWarps; ++c) fma4(acc[c], kd, at4(U + (w + kWarps * c) * kLdc + x));
+      }
+#pragma unroll
+      for (int c = 0; c < MB / kWarps; ++c) {
+        float* s = S + (w + kWarps * c) * ldd + d;
+        *s = fmaf(gt.last, *s, acc[c]);
+      }
+    }
   }
   __syncthreads();
-  if (p.state_out != nullptr)
-    for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-      const int d = e / nc, c = e % nc;
-      p.state_out[(p_ * D + d) * M + c0 + c] = S[d * ldm + c];
-    }
+  if (p.state_out != nullptr) store_state<MB>(p.state_out + p_ * D * M, S, ldd, D, M, c0);
 }
 
 template <typename T, int MB>
 __global__ void __launch_bounds__(kThreads) delta_bwd_kernel(Args p) {
-  extern __shared__ float sm[];
-  const int D = p.D, M = p.M, ldd = D + 1;
-  constexpr int ldm = MB + 1, ldc = kC + 1;
-  float* S = sm;                   // [D][ldm]  state before the chunk
-  float* dS = S + D * ldm;         // [D][ldm]  gradient of the state after it
-  float* K = dS + D * ldm;         // [kC][ldd]
+  extern __shared__ __align__(16) float sm[];
+  using PM = Place<MB>;
+  using PC = Place<kC>;
+  constexpr int RT = PM::RT, CT = PM::CT, LC = PM::LC;
+  const int D = p.D, M = p.M, ldd = pitch(D), Dp = (D + 3) & ~3;
+  float* S = sm;                   // [MB][ldd]  state before the chunk
+  float* dS = S + MB * ldd;        // [MB][ldd]  gradient of the state after it
+  float* K = dS + MB * ldd;        // [kC][ldd]
   float* Q = K + kC * ldd;         // [kC][ldd]
-  float* R = Q + kC * ldd;         // [kC][ldm]  V, then R
-  float* dO = R + kC * ldm;        // [kC][ldm]
-  float* U = dO + kC * ldm;        // [kC][ldm]
-  float* dX = U + kC * ldm;        // [kC][ldm]  dU, then dX
-  float* QS = dX + kC * ldm;       // [kC][ldm]
-  float* KS = QS + kC * ldm;       // [kC][ldm]
-  float* KD = KS + kC * ldm;       // [kC][ldm]  K dS'
-  float* KK = KD + kC * ldm;       // [kC][ldc]
-  float* QK = KK + kC * ldc;       // [kC][ldc]
-  float* Gm = QK + kC * ldc;       // [kC][ldc]  Gam
-  float* Mq = Gm + kC * ldc;       // [kC][ldc]
-  float* Ma = Mq + kC * ldc;       // [kC][ldc]
-  float* row = Ma + kC * ldc;      // [kC] r_i, [kC] c_j
-  __shared__ Gates gt;
-  __shared__ float red[8], zdot;
+  float* dO = Q + kC * ldd;        // [MB][kLdc]  then s gam dO
+  float* U = dO + MB * kLdc;       // [MB][kLdc]  V, b R, U, then del U
+  float* dX = U + MB * kLdc;       // [MB][kLdc]  dU, dX, then gam dR
+  float* A = dX + MB * kLdc;       // [kC][kLdc]  A, then the pairs' weights in dg
+  float* At = A + kC * kLdc;       // [kC][kLdc]  A transposed, then Mq
+  float* Pt = At + kC * kLdc;      // [kC][kLdc]  P transposed, then Mq transposed
+  float* Ms = Pt + kC * kLdc;      // [kC][kLdc]  Ma + Ma^T
+  __shared__ Gates gates[2];
+  __shared__ float red[kWarps], rows[2][kC];  // of dg: row i's part with S, row j's with dS'
   const int64_t p_ = blockIdx.x;
-  const int c0 = blockIdx.y * MB, nc = min(MB, M - c0);
+  const int c0 = blockIdx.y * MB;
   const int64_t N = p.N, pk = (p_ / p.H) * (p.H / p.group) + (p_ % p.H) / p.group;
   const T* q = static_cast<const T*>(p.q) + pk * N * D;
   const T* k = static_cast<const T*>(p.k) + pk * N * D;
   const T* v = static_cast<const T*>(p.v) + p_ * N * M;
   const T* go = static_cast<const T*>(p.go) + p_ * N * M;
+  const float *g = p.g + p_ * N, *beta = p.beta + p_ * N;
   T* dv = static_cast<T*>(p.dv) + p_ * N * M;
   const int64_t part = ((int64_t)blockIdx.y * gridDim.x + p_) * N;
   const int64_t n_chunks = (N + kC - 1) / kC;
+  const float* ckpt = p.ckpt + p_ * n_chunks * D * M;
   const int w = threadIdx.x / 32, l = threadIdx.x % 32;
-  for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-    const int d = e / nc, c = e % nc;
-    dS[d * ldm + c] = p.grad_state_out != nullptr ? p.grad_state_out[(p_ * D + d) * M + c0 + c] : 0.f;
+  const PM at;
+  const PC pair;
+  Rows<T> kr, qr;
+  Cols<T, MB> vr, gr;
+  load_state<MB>(dS, ldd, p.grad_state_out != nullptr ? p.grad_state_out + p_ * D * M : nullptr, D,
+                 M, c0);
+  if (n_chunks > 0) {
+    const int64_t i0 = (n_chunks - 1) * kC;
+    load_state<MB>(S, ldd, ckpt + (n_chunks - 1) * D * M, D, M, c0);
+    kr.fetch(k, i0, N, D);
+    qr.fetch(q, i0, N, D);
+    vr.fetch(v, i0, N, M, c0);
+    gr.fetch(go, i0, N, M, c0);
+    if (w == kWarps - 1) load_gates(gates[(n_chunks - 1) & 1], g, beta, i0, N);
   }
   for (int64_t ch = n_chunks - 1; ch >= 0; --ch) {
     const int64_t i0 = ch * kC;
+    const Gates& gt = gates[ch & 1];
     __syncthreads();
-    load_rows<T>(K, ldd, k, i0, N, D, 0, D);
-    load_rows<T>(Q, ldd, q, i0, N, D, 0, D);
-    load_rows<T>(R, ldm, v, i0, N, M, c0, nc);
-    load_rows<T>(dO, ldm, go, i0, N, M, c0, nc);
-    load_gates(gt, p.g + p_ * N, p.beta + p_ * N, i0, N);
-    for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-      const int d = e / nc, c = e % nc;
-      S[d * ldm + c] = p.ckpt[((p_ * n_chunks + ch) * D + d) * M + c0 + c];
+    kr.put(K, ldd, k, i0, N, D);
+    qr.put(Q, ldd, q, i0, N, D);
+    vr.put(U);
+    gr.put(dO);
+    __syncthreads();
+    // a thread's pairs (i, j) of the chunk: k.k, q.k and the decay between them
+    float kk[PC::RT][1] = {}, qk[PC::RT][1] = {}, gm[PC::RT];
+    dot2<kC>(kk, qk, pair, K, Q, ldd, K, ldd, Dp);
+#pragma unroll
+    for (int r = 0; r < PC::RT; ++r) {
+      const int i = pair.row + r, j = pair.col;
+      gm[r] = j <= i ? decay_between(gt.G[i], gt.G[j]) : 0.f;
+      const float a = j < i ? gt.b[i] * gm[r] * kk[r][0] : 0.f;
+      A[i * kLdc + j] = a;
+      At[j * kLdc + i] = a;
+      Pt[j * kLdc + i] = j <= i ? p.scale * gm[r] * qk[r][0] : 0.f;
     }
-    __syncthreads();
-    mm<4, 1>(kC, kC, D, [&](int i, int x) { return K[i * ldd + x]; },
-             [&](int x, int j) { return K[j * ldd + x]; }, [&](int i, int j, float a) {
-               KK[i * ldc + j] = a;
-               Gm[i * ldc + j] = j <= i ? decay_between(gt.G[i], gt.G[j]) : 0.f;
-             });
-    mm<4, 1>(kC, kC, D, [&](int i, int x) { return Q[i * ldd + x]; },
-             [&](int x, int j) { return K[j * ldd + x]; },
-             [&](int i, int j, float a) { QK[i * ldc + j] = a; });
-    mm<4, 2>(kC, nc, D, [&](int i, int x) { return K[i * ldd + x]; },
-             [&](int x, int j) { return S[x * ldm + j]; }, [&](int i, int j, float a) {
-               KS[i * ldm + j] = a;
-               R[i * ldm + j] -= gt.gam[i] * a;
-               U[i * ldm + j] = gt.b[i] * R[i * ldm + j];
-             });
-    mm<4, 2>(kC, nc, D, [&](int i, int x) { return Q[i * ldd + x]; },
-             [&](int x, int j) { return S[x * ldm + j]; },
-             [&](int i, int j, float a) { QS[i * ldm + j] = a; });
-    mm<4, 2>(kC, nc, D, [&](int i, int x) { return K[i * ldd + x]; },
-             [&](int x, int j) { return dS[x * ldm + j]; },
-             [&](int i, int j, float a) { KD[i * ldm + j] = a; });
-    __syncthreads();
-    // dU, and <S, dS'>
-    mm<4, 2>(kC, nc, kC, [&](int i, int x) { return QK[x * ldc + i] * Gm[x * ldc + i]; },
-             [&](int x, int j) { return dO[x * ldm + j]; }, [&](int i, int j, float a) {
-               dX[i * ldm + j] = p.scale * a + gt.del[i] * KD[i * ldm + j];
-             });
+    // and its entries (i, c) of the products with S and dS'
+    float ks[RT][CT] = {}, qs[RT][CT] = {}, kd[RT][CT] = {}, rr[RT][CT];
+    dot2<MB>(ks, qs, at, K, Q, ldd, S, ldd, Dp);
+    dot<MB>(kd, at, K, ldd, dS, ldd, Dp);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int i = at.row + r;
+        float* x = U + (at.col + LC * c) * kLdc + i;
+        rr[r][c] = *x - gt.gam[i] * ks[r][c];
+        *x = gt.b[i] * rr[r][c];
+      }
     float z = 0.f;
-    for (int d = w; d < D; d += 8)
-      for (int c = l; c < nc; c += 32) z = fmaf(S[d * ldm + c], dS[d * ldm + c], z);
+#pragma unroll 2
+    for (int d = l; d < D; d += 32)
+#pragma unroll
+      for (int c = w; c < MB; c += kWarps) z = fmaf(S[c * ldd + d], dS[c * ldd + d], z);
     for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (l == 0) red[w] = z;
     __syncthreads();
-    if (threadIdx.x < nc) {
-      const int c = threadIdx.x;
-      float u[kC];
-#pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        float x = 0.f;
-#pragma unroll
-        for (int j = 0; j < i; ++j) x = fmaf(KK[i * ldc + j] * Gm[i * ldc + j], u[j], x);
-        u[i] = U[i * ldm + c] - gt.b[i] * x;
-        U[i * ldm + c] = u[i];
-      }
-    } else if (threadIdx.x >= 128 && threadIdx.x < 128 + nc) {
-      const int c = threadIdx.x - 128;
-      float x[kC];
-#pragma unroll
-      for (int i = kC - 1; i >= 0; --i) {
-        float y = dX[i * ldm + c];
-#pragma unroll
-        for (int j = i + 1; j < kC; ++j)
-          y = fmaf(-gt.b[j] * KK[j * ldc + i] * Gm[j * ldc + i], x[j], y);
-        x[i] = y;
-        dX[i * ldm + c] = y;
-        if (i0 + i < N) dv[(i0 + i) * M + c0 + c] = from_f32<T>(gt.b[i] * y);
-      }
-    }
-    if (threadIdx.x == 255) {
-      float s = 0.f;
-      for (int i = 0; i < 8; ++i) s += red[i];
-      zdot = gt.last * s;
-    }
-    __syncthreads();
-    // dP and dA, weighted
-    mm<4, 1>(kC, kC, nc, [&](int i, int x) { return dO[i * ldm + x]; },
-             [&](int x, int j) { return U[j * ldm + x]; },
-             [&](int i, int j, float a) { Mq[i * ldc + j] = p.scale * Gm[i * ldc + j] * a; });
-    mm<4, 1>(kC, kC, nc, [&](int i, int x) { return dX[i * ldm + x]; },
-             [&](int x, int j) { return U[j * ldm + x]; }, [&](int i, int j, float a) {
-               // without b: db needs it so, and b enters below
-               Ma[i * ldc + j] = j < i ? -Gm[i * ldc + j] * a : 0.f;
-             });
-    __syncthreads();
-    // row sums: db, the parts of dg with S and with dS'
-    for (int i = w; i < kC; i += 8) {
-      float db = 0.f, r = 0.f, cc = 0.f;
-      for (int c = l; c < nc; c += 32) {
-        const float x = dX[i * ldm + c];
-        db = fmaf(x, R[i * ldm + c], db);
-        r += p.scale * dO[i * ldm + c] * QS[i * ldm + c] - gt.b[i] * x * KS[i * ldm + c];
-        cc = fmaf(U[i * ldm + c], KD[i * ldm + c], cc);
-      }
-      db = fmaf(Ma[i * ldc + l], KK[i * ldc + l], db);
-      for (int o = 16; o > 0; o /= 2) {
-        db += __shfl_xor_sync(0xffffffffu, db, o);
-        r += __shfl_xor_sync(0xffffffffu, r, o);
-        cc += __shfl_xor_sync(0xffffffffu, cc, o);
-      }
-      if (l == 0) {
-        row[i] = gt.gam[i] * r;
-        row[kC + i] = gt.del[i] * cc;
-        if (i0 + i < N) {
-          if (p.db_part != nullptr)
-            p.db_part[part + i0 + i] = db;
-          else
-            p.dbeta[p_ * N + i0 + i] = db;
-        }
-      }
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < kC * kC; e += kThreads) {
-      const int i = e / kC, j = e % kC;
-      Ma[i * ldc + j] *= gt.b[i];
-      // the pair's weight in dg takes the place of q.k, which it is made from
-      QK[i * ldc + j] = Mq[i * ldc + j] * QK[i * ldc + j] + Ma[i * ldc + j] * KK[i * ldc + j];
-    }
-    __syncthreads();
-    // dg_t: warp w takes t = w, w + 8, ..: lane j < t sums its column from row
-    // t on; lane l >= t adds row l's part
-    for (int t = w; t < kC; t += 8) {
-      float s = 0.f;
-      if (l < t) {
-        for (int i = t; i < kC; ++i) s += QK[i * ldc + l];
-        s += row[kC + l];
-      } else {
-        s = row[l];
-      }
-      for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s += zdot;
-      if (l == 0 && i0 + t < N) {
-        if (p.dg_part != nullptr)
-          p.dg_part[part + i0 + t] = s;
-        else
-          p.dg[p_ * N + i0 + t] = s;
-      }
-    }
-    // dQ and dK, two products each into registers by way of shared memory:
-    // KS and QS become s gam dO and gam dR
-    __syncthreads();
-    for (int e = threadIdx.x; e < kC * nc; e += kThreads) {
-      const int i = e / nc, c = e % nc;
-      QS[i * ldm + c] = p.scale * gt.gam[i] * dO[i * ldm + c];
-      KS[i * ldm + c] = gt.gam[i] * gt.b[i] * dX[i * ldm + c];
-      KD[i * ldm + c] = gt.del[i] * U[i * ldm + c];
-    }
-    __syncthreads();
     {
-      constexpr int RT = 4, CT = 2;
-      for (int j0 = l; j0 < D; j0 += 32 * CT) {
-        float aq[RT][CT] = {}, ak[RT][CT] = {};
-        int jj[CT];
+      float du[RT][CT] = {};
+      dot<MB>(du, at, Pt, kLdc, dO, kLdc, kC);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) jj[c] = min(j0 + 32 * c, D - 1);
-        for (int x = 0; x < nc; ++x) {
-          float sv[CT], dsv[CT];
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            sv[c] = S[jj[c] * ldm + x];
-            dsv[c] = dS[jj[c] * ldm + x];
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const int i = w + 8 * r;
-            const float a = QS[i * ldm + x], b = KS[i * ldm + x], u = KD[i * ldm + x];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              aq[r][c] = fmaf(a, sv[c], aq[r][c]);
-              ak[r][c] = fmaf(u, dsv[c], fmaf(-b, sv[c], ak[r][c]));
-            }
-          }
-        }
-        for (int x = 0; x < kC; ++x) {
-          float kv[CT], qv[CT];
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            kv[c] = K[x * ldd + jj[c]];
-            qv[c] = Q[x * ldd + jj[c]];
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const int i = w + 8 * r;
-            const float a = Mq[i * ldc + x], at = Mq[x * ldc + i];
-            const float m = Ma[i * ldc + x] + Ma[x * ldc + i];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              aq[r][c] = fmaf(a, kv[c], aq[r][c]);
-              ak[r][c] = fmaf(at, qv[c], fmaf(m, kv[c], ak[r][c]));
-            }
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int64_t i = i0 + w + 8 * r;
-            const int d = j0 + 32 * c;
-            if (i >= N || d >= D) continue;
-            if (p.dq_part != nullptr) {
-              p.dq_part[(part + i) * D + d] = aq[r][c];
-              p.dk_part[(part + i) * D + d] = ak[r][c];
-            } else {
-              static_cast<T*>(p.dq)[(p_ * N + i) * D + d] = from_f32<T>(aq[r][c]);
-              static_cast<T*>(p.dk)[(p_ * N + i) * D + d] = from_f32<T>(ak[r][c]);
-            }
-          }
-      }
+        for (int c = 0; c < CT; ++c)
+          dX[(at.col + LC * c) * kLdc + at.row + r] = du[r][c] + gt.del[at.row + r] * kd[r][c];
     }
     __syncthreads();
-    mm<4, 2>(D, nc, kC, [&](int d, int x) { return Q[x * ldd + d]; },
-             [&](int x, int j) { return QS[x * ldm + j]; },
-             [&](int d, int j, float a) { dS[d * ldm + j] = fmaf(gt.last, dS[d * ldm + j], a); });
-    mm<4, 2>(D, nc, kC, [&](int d, int x) { return K[x * ldd + d]; },
-             [&](int x, int j) { return KS[x * ldm + j]; },
-             [&](int d, int j, float a) { dS[d * ldm + j] -= a; });
+    if (ch > 0) {
+      kr.fetch(k, i0 - kC, N, D);
+      qr.fetch(q, i0 - kC, N, D);
+      vr.fetch(v, i0 - kC, N, M, c0);
+      gr.fetch(go, i0 - kC, N, M, c0);
+      if (w == kWarps - 1) load_gates(gates[(ch - 1) & 1], g, beta, i0 - kC, N);
+    }
+    solve_both<MB>(U, At, dX, A);
+    __syncthreads();
+    // dP and dA of the pairs: the sums over the columns, weighted
+    float db[PC::RT], wt[PC::RT], mq[PC::RT], ma[PC::RT];
+    {
+      float dp[PC::RT] = {}, da[PC::RT] = {};
+      static_assert(PC::RT == 2, "a pair's two rows are read as one word");
+#pragma unroll 8
+      for (int c = 0; c < MB; ++c) {
+        const float u = U[c * kLdc + pair.col];
+        const float2 o = *reinterpret_cast<const float2*>(dO + c * kLdc + pair.row);
+        const float2 x = *reinterpret_cast<const float2*>(dX + c * kLdc + pair.row);
+        dp[0] = fmaf(o.x, u, dp[0]);
+        dp[1] = fmaf(o.y, u, dp[1]);
+        da[0] = fmaf(x.x, u, da[0]);
+        da[1] = fmaf(x.y, u, da[1]);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = pair.row + r, j = pair.col;
+        mq[r] = p.scale * gm[r] * dp[r];
+        const float t = j < i ? -gm[r] * da[r] : 0.f;  // without b: db needs it so
+        db[r] = t * kk[r][0];
+        ma[r] = gt.b[i] * t;
+        wt[r] = mq[r] * qk[r][0] + ma[r] * kk[r][0];
+      }
+    }
+    // the rows' sums: of db, and of dg's parts with S and with dS'
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      for (int o = 16; o > 0; o /= 2) db[r] += __shfl_xor_sync(0xffffffffu, db[r], o);
+    float dbr[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int i = at.row + r;
+      float b = 0.f, s = 0.f, t = 0.f;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int e = (at.col + LC * c) * kLdc + i;
+        const float x = dX[e];
+        b = fmaf(x, rr[r][c], b);
+        s += p.scale * dO[e] * qs[r][c] - gt.b[i] * x * ks[r][c];
+        t = fmaf(U[e], kd[r][c], t);
+      }
+      for (int o = LC / 2; o > 0; o /= 2) {
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+      }
+      dbr[r] = b;
+      if (at.col == 0) {
+        rows[0][i] = gt.gam[i] * s;
+        rows[1][i] = gt.del[i] * t;
+      }
+    }
+    // a warp's two rows are 2w and 2w + 1 in both placements
+    if (at.col == 0)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int i = at.row + r;
+        if (i0 + i < N) {
+          const float s = dbr[r] + (i % 2 == 0 ? db[0] : db[1]);
+          if (p.db_part != nullptr)
+            p.db_part[part + i0 + i] = s;
+          else
+            p.dbeta[p_ * N + i0 + i] = s;
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = pair.row + r, j = pair.col;
+      A[i * kLdc + j] = wt[r];
+      At[i * kLdc + j] = mq[r];
+      Pt[j * kLdc + i] = mq[r];
+      if (j <= i) {
+        Ms[i * kLdc + j] = ma[r];
+        Ms[j * kLdc + i] = ma[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int i = at.row + r, j = c0 + at.col + LC * c;
+        const int e = (at.col + LC * c) * kLdc + i;
+        const float x = gt.b[i] * dX[e];
+        if (i0 + i < N && j < M) dv[(i0 + i) * M + j] = from_f32<T>(x);
+        dX[e] = gt.gam[i] * x;
+        dO[e] *= p.scale * gt.gam[i];
+        U[e] *= gt.del[i];
+      }
+    __syncthreads();
+    // dg_t: warp w takes t = w and w + 16: lane j < t sums its column from row
+    // t on; lane l >= t adds row l's part
+    {
+      float zs = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) zs += red[i];
+      zs *= gt.last;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = w + kWarps * u;
+        float s = 0.f;
+        if (l < t) {
+#pragma unroll 8
+          for (int i = t; i < kC; ++i) s += A[i * kLdc + l];
+          s += rows[1][l];
+        } else {
+          s = rows[0][l];
+        }
+        for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s += zs;
+        if (l == 0 && i0 + t < N) {
+          if (p.dg_part != nullptr)
+            p.dg_part[part + i0 + t] = s;
+          else
+            p.dg[p_ * N + i0 + t] = s;
+        }
+      }
+    }
+    // dQ and dK of rows 2w and 2w + 1: lanes along d
+#pragma unroll 1
+    for (int j0 = l; j0 < Dp; j0 += 64) {
+      const bool two = j0 + 32 < Dp;
+      const int j1 = two ? j0 + 32 : j0;
+      float aq[2][2] = {}, ak[2][2] = {};
+#pragma unroll 4
+      for (int x = 0; x < MB; ++x) {
+        const float s0 = S[x * ldd + j0], s1 = S[x * ldd + j1];
+        const float t0 = dS[x * ldd + j0], t1 = dS[x * ldd + j1];
+        const float2 a = *reinterpret_cast<const float2*>(dO + x * kLdc + 2 * w);
+        const float2 b = *reinterpret_cast<const float2*>(dX + x * kLdc + 2 * w);
+        const float2 u = *reinterpret_cast<const float2*>(U + x * kLdc + 2 * w);
+        aq[0][0] = fmaf(a.x, s0, aq[0][0]);
+        aq[0][1] = fmaf(a.x, s1, aq[0][1]);
+        aq[1][0] = fmaf(a.y, s0, aq[1][0]);
+        aq[1][1] = fmaf(a.y, s1, aq[1][1]);
+        ak[0][0] = fmaf(u.x, t0, fmaf(-b.x, s0, ak[0][0]));
+        ak[0][1] = fmaf(u.x, t1, fmaf(-b.x, s1, ak[0][1]));
+        ak[1][0] = fmaf(u.y, t0, fmaf(-b.y, s0, ak[1][0]));
+        ak[1][1] = fmaf(u.y, t1, fmaf(-b.y, s1, ak[1][1]));
+      }
+#pragma unroll 4
+      for (int x = 0; x < kC; ++x) {
+        const float k0 = K[x * ldd + j0], k1 = K[x * ldd + j1];
+        const float q0 = Q[x * ldd + j0], q1 = Q[x * ldd + j1];
+        const float2 a = *reinterpret_cast<const float2*>(Pt + x * kLdc + 2 * w);
+        const float2 t = *reinterpret_cast<const float2*>(At + x * kLdc + 2 * w);
+        const float2 m = *reinterpret_cast<const float2*>(Ms + x * kLdc + 2 * w);
+        aq[0][0] = fmaf(a.x, k0, aq[0][0]);
+        aq[0][1] = fmaf(a.x, k1, aq[0][1]);
+        aq[1][0] = fmaf(a.y, k0, aq[1][0]);
+        aq[1][1] = fmaf(a.y, k1, aq[1][1]);
+        ak[0][0] = fmaf(t.x, q0, fmaf(m.x, k0, ak[0][0]));
+        ak[0][1] = fmaf(t.x, q1, fmaf(m.x, k1, ak[0][1]));
+        ak[1][0] = fmaf(t.y, q0, fmaf(m.y, k0, ak[1][0]));
+        ak[1][1] = fmaf(t.y, q1, fmaf(m.y, k1, ak[1][1]));
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int64_t i = i0 + 2 * w + r;
+          const int d = j0 + 32 * c;
+          if (i >= N || d >= D) continue;
+          if (p.dq_part != nullptr) {
+            p.dq_part[(part + i) * D + d] = aq[r][c];
+            p.dk_part[(part + i) * D + d] = ak[r][c];
+          } else {
+            static_cast<T*>(p.dq)[(p_ * N + i) * D + d] = from_f32<T>(aq[r][c]);
+            static_cast<T*>(p.dk)[(p_ * N + i) * D + d] = from_f32<T>(ak[r][c]);
+          }
+        }
+    }
+    __syncthreads();
+    // the states of the chunk before: S from memory, dS from this chunk
+    if (ch > 0) load_state<MB>(S, ldd, ckpt + (ch - 1) * D * M, D, M, c0);
+#pragma unroll 1
+    for (int d = l; d < Dp; d += 32) {
+      float acc[MB / kWarps] = {};
+#pragma unroll
+      for (int x = 0; x < kC; x += 4) {
+        const float4 qv = make_float4(Q[x * ldd + d], Q[(x + 1) * ldd + d], Q[(x + 2) * ldd + d],
+                                      Q[(x + 3) * ldd + d]);
+        const float4 kv = make_float4(-K[x * ldd + d], -K[(x + 1) * ldd + d],
+                                      -K[(x + 2) * ldd + d], -K[(x + 3) * ldd + d]);
+#pragma unroll
+        for (int c = 0; c < MB / kWarps; ++c) {
+          fma4(acc[c], qv, at4(dO + (w + kWarps * c) * kLdc + x));
+          fma4(acc[c], kv, at4(dX + (w + kWarps * c) * kLdc + x));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < MB / kWarps; ++c) {
+        float* s = dS + (w + kWarps * c) * ldd + d;
+        *s = fmaf(gt.last, *s, acc[c]);
+      }
+    }
   }
   __syncthreads();
-  if (p.grad_state_in != nullptr)
-    for (int e = threadIdx.x; e < D * nc; e += kThreads) {
-      const int d = e / nc, c = e % nc;
-      p.grad_state_in[(p_ * D + d) * M + c0 + c] = dS[d * ldm + c];
-    }
+  if (p.grad_state_in != nullptr) store_state<MB>(p.grad_state_in + p_ * D * M, dS, ldd, D, M, c0);
 }
 
-// out[b][hk][i] = sum over the column blocks and the group's heads of parts
-// [n_mb][B][Hk][group][rows], in that order
+// out[head][row] = sum over the column blocks and the group's heads of parts
+// [n_mb][heads][group][rows], in that order; the launch's rows of blocks are
+// dq, dk and, where they have parts, dg and db
 template <typename T>
-__global__ void __launch_bounds__(256)
-    delta_join_kernel(const float* __restrict__ part, T* __restrict__ out, int64_t rows,
-                      int64_t heads, int group, int n_mb) {
+__device__ __forceinline__ void join(const float* __restrict__ part, T* __restrict__ out,
+                                     int64_t rows, int64_t heads, int group, int n_mb) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = rows * heads;
   if (i >= n) return;
   const int64_t h = i / rows, r = i % rows;
@@ -477,17 +697,33 @@ __global__ void __launch_bounds__(256)
     for (int g = 0; g < group; ++g) s += part[((int64_t)m * heads * group + h * group + g) * rows + r];
   out[i] = from_f32<T>(s);
 }
-
-// Value columns of a CTA: 64 while two D x 64 fp32 tiles and the row tiles fit
-// the shared memory (D <= 128), else 32.
-int block_cols(int64_t D, int64_t M) { return D <= 128 && M > 32 ? 64 : 32; }
-
-size_t fwd_smem(int64_t D, int mb) {
-  return sizeof(float) * (size_t)(D * (mb + 1) + 2 * kC * (D + 1) + 2 * kC * (mb + 1) + 2 * kC * (kC + 1));
+template <typename T>
+__global__ void __launch_bounds__(256) delta_join_kernel(DeltaJoin x) {
+  switch (blockIdx.y) {
+    case 0: return join(x.dq_part, static_cast<T*>(x.dq), x.N * x.D, x.heads, x.group, x.n_mb);
+    case 1: return join(x.dk_part, static_cast<T*>(x.dk), x.N * x.D, x.heads, x.group, x.n_mb);
+    case 2: return join(x.dg_part, x.dg, x.N, x.heads * x.group, 1, x.n_mb);
+    default: return join(x.db_part, x.db, x.N, x.heads * x.group, 1, x.n_mb);
+  }
 }
-size_t bwd_smem(int64_t D, int mb) {
-  return sizeof(float) *
-         (size_t)(2 * D * (mb + 1) + 2 * kC * (D + 1) + 7 * kC * (mb + 1) + 5 * kC * (kC + 1) + 2 * kC);
+
+// Value columns of a CTA: 64 while the state's tiles and the row tiles fit the
+// shared memory (D <= 128), else 32; halved while the halves still get an SM
+// each: the walk's time is its own latency then, and the columns lengthen it.
+// (fp32, D = M = 64, N = 512, forward and gradients' kernels: 8 heads 106 + 266
+// us with 16 columns, 163 + 438 with 64; 64 heads 127 + 362 with 32, 163 + 442
+// with 64, 204 + 555 with 16, two turns of the SMs.)
+int block_cols(int64_t BH, int64_t D, int64_t M) {
+  int mb = D <= 128 && M > 32 ? 64 : 32;
+  while (mb > 16 && BH * ((M + mb / 2 - 1) / (mb / 2)) <= kPlanSMs) mb /= 2;
+  return mb;
+}
+
+size_t fwd_smem(int D, int mb) {
+  return sizeof(float) * (size_t)((mb + 2 * kC) * pitch(D) + (mb + 2 * kC) * kLdc);
+}
+size_t bwd_smem(int D, int mb) {
+  return sizeof(float) * (size_t)((2 * mb + 2 * kC) * pitch(D) + (3 * mb + 4 * kC) * kLdc);
 }
 
 template <typename T, int MB>
@@ -503,8 +739,11 @@ cudaError_t launch(const Args& a, int64_t BH, bool backward, cudaStream_t stream
 
 template <typename T>
 cudaError_t run(const Args& a, int64_t BH, bool backward, cudaStream_t stream) {
-  return block_cols(a.D, a.M) == 64 ? launch<T, 64>(a, BH, backward, stream)
-                                    : launch<T, 32>(a, BH, backward, stream);
+  switch (block_cols(BH, a.D, a.M)) {
+    case 64: return launch<T, 64>(a, BH, backward, stream);
+    case 32: return launch<T, 32>(a, BH, backward, stream);
+    default: return launch<T, 16>(a, BH, backward, stream);
+  }
 }
 
 cudaError_t run(const Args& a, int64_t BH, cp_dtype_t dtype, bool backward, cudaStream_t stream) {
@@ -513,26 +752,23 @@ cudaError_t run(const Args& a, int64_t BH, cp_dtype_t dtype, bool backward, cuda
   return run<float>(a, BH, backward, stream);
 }
 
-int n_blocks(int64_t D, int64_t M) {
-  const int mb = block_cols(D, M);
-  return (int)((M + mb - 1) / mb);
+int n_blocks(const DeltaShape& s) {
+  const int mb = block_cols(s.B * s.H, s.D, s.M);
+  return (int)((s.M + mb - 1) / mb);
 }
-bool has_parts(const DeltaShape& s) { return s.H != s.Hk || n_blocks(s.D, s.M) > 1; }
+bool has_parts(const DeltaShape& s) { return s.H != s.Hk || n_blocks(s) > 1; }
 
 }  // namespace
 
-cudaError_t delta_join_launch(const float* part, void* out, int64_t rows, int64_t heads, int group,
-                              int n_mb, cp_dtype_t dtype, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((rows * heads + 255) / 256);
+cudaError_t delta_join_launch(const DeltaJoin& x, cp_dtype_t dtype, cudaStream_t stream) {
+  const int64_t n = std::max(x.N * x.D * x.heads, x.dg == nullptr ? 0 : x.N * x.heads * x.group);
+  const dim3 grid((unsigned)((n + 255) / 256), x.dg == nullptr ? 2 : 4);
   if (dtype == CP_DTYPE_BF16)
-    delta_join_kernel<<<grid, 256, 0, stream>>>(part, static_cast<__nv_bfloat16*>(out), rows, heads,
-                                                group, n_mb);
+    delta_join_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(x);
   else if (dtype == CP_DTYPE_F16)
-    delta_join_kernel<<<grid, 256, 0, stream>>>(part, static_cast<__half*>(out), rows, heads, group,
-                                                n_mb);
+    delta_join_kernel<__half><<<grid, 256, 0, stream>>>(x);
   else
-    delta_join_kernel<<<grid, 256, 0, stream>>>(part, static_cast<float*>(out), rows, heads, group,
-                                                n_mb);
+    delta_join_kernel<float><<<grid, 256, 0, stream>>>(x);
   return cudaGetLastError();
 }
 
@@ -540,7 +776,7 @@ int delta_simt_chunk() { return kC; }
 
 size_t delta_simt_scratch(const DeltaShape& s, bool backward) {
   if (!backward || !has_parts(s)) return 0;
-  return sizeof(float) * (size_t)n_blocks(s.D, s.M) * s.B * s.H * s.N * (2 * s.D + 2);
+  return sizeof(float) * (size_t)n_blocks(s) * s.B * s.H * s.N * (2 * s.D + 2);
 }
 
 cudaError_t delta_simt_fwd(const DeltaShape& s, const DeltaFwd& f, cudaStream_t stream) {
@@ -563,7 +799,7 @@ cudaError_t delta_simt_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch
   a.scale = s.scale;
   const int64_t BH = s.B * s.H;
   if (!has_parts(s)) return run(a, BH, s.dtype, true, stream);
-  const int n_mb = n_blocks(s.D, s.M);
+  const int n_mb = n_blocks(s);
   const int64_t rows = n_mb * BH * s.N;
   a.dq_part = static_cast<float*>(scratch);
   a.dk_part = a.dq_part + rows * s.D;
@@ -571,15 +807,9 @@ cudaError_t delta_simt_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch
   a.db_part = a.dg_part + rows;
   cudaError_t e = run(a, BH, s.dtype, true, stream);
   if (e != cudaSuccess) return e;
-  const int64_t heads = s.B * s.Hk;
-  e = delta_join_launch(a.dq_part, f.dq, s.N * s.D, heads, a.group, n_mb, s.dtype, stream);
-  if (e == cudaSuccess)
-    e = delta_join_launch(a.dk_part, f.dk, s.N * s.D, heads, a.group, n_mb, s.dtype, stream);
-  if (e == cudaSuccess)
-    e = delta_join_launch(a.dg_part, f.dg, s.N, BH, 1, n_mb, CP_DTYPE_F32, stream);
-  if (e == cudaSuccess)
-    e = delta_join_launch(a.db_part, f.dbeta, s.N, BH, 1, n_mb, CP_DTYPE_F32, stream);
-  return e;
+  return delta_join_launch({a.dq_part, a.dk_part, a.dg_part, a.db_part, f.dq, f.dk, f.dg, f.dbeta,
+                            s.N, s.D, s.B * s.Hk, a.group, n_mb},
+                           s.dtype, stream);
 }
 
 }  // namespace cp

@@ -849,10 +849,9 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
   g.M = c.M; g.scale = s.scale;
   cp_status_t st = s.D <= 64 ? launch<64>(s, f, c, g, stream) : launch<128>(s, f, c, g, stream);
   if (st != CP_OK || w.part == 0) return st;
-  const int64_t heads = s.B * s.Hk;
-  cudaError_t e = delta_join_launch(g.dq_part, f.dq, s.N * s.D, heads, c.group, 1, s.dtype, stream);
-  if (e == cudaSuccess)
-    e = delta_join_launch(g.dk_part, f.dk, s.N * s.D, heads, c.group, 1, s.dtype, stream);
+  const cudaError_t e = delta_join_launch({g.dq_part, g.dk_part, nullptr, nullptr, f.dq, f.dk, nullptr,
+                                           nullptr, s.N, s.D, s.B * s.Hk, c.group, 1},
+                                          s.dtype, stream);
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

@@ -283,10 +283,17 @@ cp_status_t delta_tc_fwd(const DeltaShape& s, const DeltaFwd& f, void* scratch, 
                          cudaStream_t stream);
 cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, int* status,
                          cudaStream_t stream);
-// out[head][row] = the sum of fp32 parts [n_mb][heads][group][rows] over n_mb
-// and group, in that order
-cudaError_t delta_join_launch(const float* part, void* out, int64_t rows, int64_t heads, int group,
-                              int n_mb, cp_dtype_t dtype, cudaStream_t stream);
+// The sums of the backward's fp32 parts [n_mb][heads][group][rows] over n_mb
+// and group, in that order, in one launch: dq and dk [heads][N][D] in dtype;
+// dg and db [heads * group][N] in fp32, per value head, unless dg is null.
+struct DeltaJoin {
+  const float *dq_part, *dk_part, *dg_part, *db_part;
+  void *dq, *dk;
+  float *dg, *db;
+  int64_t N, D, heads;
+  int group, n_mb;
+};
+cudaError_t delta_join_launch(const DeltaJoin& x, cp_dtype_t dtype, cudaStream_t stream);
 cudaError_t delta_decode_launch(const DeltaShape& s, const DeltaDecode& f, cudaStream_t stream);
 
 // ---- per-head norm of queries and keys with the position rotation; forward:
