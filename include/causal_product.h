@@ -393,8 +393,9 @@ CP_API cp_status_t causal_product_bwd_favor(const void* xq, const void* xk, cons
  * g_t = -inf clears the state before token t (any g_t below -120 does, e^-120
  * being 0 in fp32); beta_t = 0 writes nothing, so a token with g = beta = 0 is
  * padding.  A NaN or inf among a head's inputs reaches that head's later
- * outputs, and may reach those of the same 64 rows.  Keys longer than 1 (beta |k|^2 > 2) can make the state grow without
- * bound; causal_product_qk_rope leaves them with the norm the rule wants.
+ * outputs, and may reach those of the same 64 rows.  Keys longer than 1
+ * (beta |k|^2 > 2) can make the state grow without bound;
+ * causal_product_qk_rope leaves them with the norm the rule wants.
  *
  * State and sums are fp32.  bf16 with D <= 128 runs on the tensor cores, each
  * computed factor of a product as the sum of two bf16 numbers (16 bits) or
@@ -464,8 +465,8 @@ CP_API cp_status_t causal_product_decode_delta(const void* q, const void* k, con
  * `dtype`, NULL for ones.  cos, sin: [N][R/2] fp32 for each batch, cs_batch
  * elements apart (0: one table for all; R = 0: may be NULL).  q, k: dense
  * [B][H][N][D] in `dtype`, 16-byte aligned.  D a multiple of 8, 8 .. 256; at
- * most 2^31 rows; eps finite, >= 0 (with eps = 0 a zero row gives NaN).  fp32 arithmetic, rounded
- * once.  Outputs overlap nothing.
+ * most 2^31 rows; eps finite, >= 0 (with eps = 0 a zero row gives NaN).  fp32
+ * arithmetic, rounded once.  Outputs overlap nothing.
  *
  * Backward, from grad_q, grad_k (dense as q, k): grad_xq, grad_xk, dense
  * [B][H][N][D], and grad_wq, grad_wk [D] in `dtype` (NULL exactly where the
