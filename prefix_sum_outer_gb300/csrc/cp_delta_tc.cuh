@@ -212,6 +212,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&x)[8]) {
 // is columns 0-31 of its 64-column tile and its lo part columns 32-63, and one
 // MMA of 64 columns takes both.
 constexpr int kCB = 32;
+// .. by two warpgroups, and a ninth warp for the copies and the gates: written
+// by one of the eight, they kept the others at a barrier for 340 to 440 cycles
+// of a chunk's 3,600 to 3,900.
+constexpr int kChainThreads = 256 + 32;
 
 // 16 columns of such a product: the two accumulators' sum
 __device__ __forceinline__ void load16_sum(uint32_t taddr, float2 (&x)[8]) {

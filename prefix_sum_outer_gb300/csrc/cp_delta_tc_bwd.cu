@@ -69,7 +69,7 @@ struct ChainLayout {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
+__global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     delta_tc_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k, const ChainArgs a) {
   using L = ChainLayout<DP>;
@@ -155,25 +155,41 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
     if (s + 1 < n) load_gates(s + 1);
   };
 
-  if (threadIdx.x == 96) {
-    load_kq(0);
-    load_tile(L::oP, a.pm, p_full, 0);
-    load_tile(L::oT, a.t, t_full, 0);
-    if (n > 1) load_kq(1);
-  }
   const bool row_on = t < a.D;
   float2 dS[8];
+
+  if (warp == 8) {  // the copies and the gates, a step ahead
+    if (lane == 0) {
+      load_kq(0);
+      load_tile(L::oP, a.pm, p_full, 0);
+      load_tile(L::oT, a.t, t_full, 0);
+      if (n > 1) load_kq(1);
+    }
+    __syncwarp();
+    load_gates(0);
+    put_gates(0);
+    __syncthreads();
+    for (int s = 0; s < n; ++s) {
+      __syncthreads();
+      const bool more = s + 1 < n;
+      wait_or_abort(done, s & 1, a.status, abort_flag);
+      if (lane == 0 && more) load_tile(L::oP, a.pm, p_full, s + 1);  // P^T dO has read P
+      __syncwarp();
+      if (more) put_gates(s + 1);
+      wait_or_abort(done + 1, s & 1, a.status, abort_flag);
+      if (lane == 0 && more) load_tile(L::oT, a.t, t_full, s + 1);
+      __syncwarp();
+      wait_or_abort(done + 2, s & 1, a.status, abort_flag);
+      if (lane == 0 && s + 2 < n) load_kq(s + 2);
+      __syncwarp();
+    }
+  } else {
   read16(a.grad_state_out + (p * a.D + t) * a.M + c0, nc, a.grad_state_out != nullptr && row_on, dS);
   load_row(0);
   if (t >= 64) put16(O_tile, t - 64, 4 + 2 * sub, row);
-  if (warp == 7) {
-    load_gates(0);
-    put_gates(0);
-  }
   fence_proxy_async_smem();
   __syncthreads();
   if (warp == 0) issue_e0(0);
-
   for (int s = 0; s < n; ++s) {
     const uint32_t kq = s_base + (s & 1) * L::kKQ, phase = s & 1;
     const GateSlot* gs = gates + (s & 1);
@@ -223,7 +239,7 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
     if (threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    named_barrier_sync(1, 256);
     if (warp == 0) {
       wait_or_abort(t_full, phase, a.status, abort_flag);
       __syncwarp();
@@ -234,11 +250,7 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
       mma_tile<4, false, true>(el, t_acc, T_addr + kBox, B_addr, id_nt64, 16, 16, 0, 0, false);
       if (el) mma_commit(done + 1);
     }
-    if (s + 1 < n) {  // P^T dO has read P and dO
-      if (threadIdx.x == 96) load_tile(L::oP, a.pm, p_full, s + 1);
-      if (t >= 64) put16(O_tile, t - 64, 4 + 2 * sub, row);
-      if (warp == 7) put_gates(s + 1);
-    }
+    if (t >= 64 && s + 1 < n) put16(O_tile, t - 64, 4 + 2 * sub, row);  // P^T dO has read dO
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
     if (t < 64) {
@@ -255,7 +267,7 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    named_barrier_sync(1, 256);
     if (warp == 0) {
       tc_fence_after();
       const uint32_t el = elect_one();
@@ -266,7 +278,6 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
       if (el) mma_commit(done + 2);
       if (s + 1 < n) issue_e0(s + 1);
     }
-    if (threadIdx.x == 96 && s + 1 < n) load_tile(L::oT, a.t, t_full, s + 1);
     if (t < 64) {  // under the product: x is dX
       const int64_t i = (int64_t)chunk * kCh + t;
       const float2 b = both(gs->b[t]);
@@ -287,7 +298,6 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
     }
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
-    if (threadIdx.x == 96 && s + 2 < n) load_kq(s + 2);
     const float2 last = both(gs->gam[kCh - 1]);
     load16_sum(t_up + lane_col, x);
 #pragma unroll
@@ -295,6 +305,7 @@ __global__ void __launch_bounds__(256, ChainLayout<DP>::kPerSM)
   }
   if (a.grad_state_in != nullptr && row_on)
     write16(a.grad_state_in + (p * a.D + t) * a.M + c0, nc, dS);
+  }
   fence_proxy_async_smem();
   __syncthreads();
   if (threadIdx.x == 128) {  // the last step's, chunk 0
@@ -806,7 +817,7 @@ cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const ChainArgs& c, c
       !make_chunk_map(&dq, f.dq, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&dk, f.dk, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
   const unsigned BH = (unsigned)(s.B * s.H);
-  chain<<<dim3(BH, (unsigned)((s.M + kCB - 1) / kCB)), 256, LC::kBytes, stream>>>(q, kk, c);
+  chain<<<dim3(BH, (unsigned)((s.M + kCB - 1) / kCB)), kChainThreads, LC::kBytes, stream>>>(q, kk, c);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
   grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, dq, dk, g);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;

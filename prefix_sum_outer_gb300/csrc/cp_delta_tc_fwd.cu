@@ -213,7 +213,7 @@ struct FwdLayout {
 
 // KEEP: leave what the backward needs (Saved).
 template <int DP, bool KEEP>
-__global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
+__global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     delta_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k, const FwdArgs a) {
   using L = FwdLayout<DP, KEEP>;
@@ -291,20 +291,31 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
     const int64_t row = (int64_t)c * kCh + t;
     read16(a.v + at + row * a.M, nc, t < 64 && row < a.N, vv);
   };
-  if (threadIdx.x == 96) {
-    load_kq(0);
-    load_t(0);
-    if (n > 1) load_kq(1);
-  }
   const bool row_on = t < a.D;
   float2 S[8];
-  read16(a.state_in + (p * a.D + t) * a.M + c0, nc, a.state_in != nullptr && row_on, S);
-  load_v(0);
-  if (warp == 7) {
+
+  if (warp == 8) {  // the copies and the gates, a chunk ahead
+    if (lane == 0) {
+      load_kq(0);
+      load_t(0);
+      if (n > 1) load_kq(1);
+    }
+    __syncwarp();
     load_gates(0);
     put_gates(0);
-  }
-
+    for (int c = 0; c < n; ++c) {
+      __syncthreads();
+      if (c + 1 < n) put_gates(c + 1);
+      wait_or_abort(done + 1, c & 1, a.status, abort_flag);
+      if (lane == 0 && c + 1 < n) load_t(c + 1);
+      __syncwarp();
+      wait_or_abort(done + 2, c & 1, a.status, abort_flag);
+      if (lane == 0 && c + 2 < n) load_kq(c + 2);
+      __syncwarp();
+    }
+  } else {
+  read16(a.state_in + (p * a.D + t) * a.M + c0, nc, a.state_in != nullptr && row_on, S);
+  load_v(0);
   for (int c = 0; c < n; ++c) {
     const uint32_t kq = s_base + (c & 1) * L::kKQ, phase = c & 1;
     const GateSlot* gs = gates + (c & 1);
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
     if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    named_barrier_sync(1, 256);
     if (warp == 0) {
       wait_or_abort(t_full, phase, a.status, abort_flag);
       __syncwarp();
@@ -356,7 +367,6 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
       mma_tile<4, true, true>(el, t_tr, T_addr + L::kT, R_addr, id_tt, kBox, 16, 0, 0, false);
       if (el) mma_commit(done + 1);
     }
-    if (warp == 7 && c + 1 < n) put_gates(c + 1);
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
     {
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    named_barrier_sync(1, 256);
     if (warp == 0) {
       tc_fence_after();
       const uint32_t el = elect_one();
@@ -393,10 +403,8 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
       bulk_store(a.keep_u + kept * kBox, sm + L::oU, kBox);
       tma_store_commit();
     }
-    if (threadIdx.x == 96 && c + 1 < n) load_t(c + 1);
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
-    if (threadIdx.x == 96 && c + 2 < n) load_kq(c + 2);
     const float2 last = both(gs->gam[kCh - 1]);
     load16_sum(t_tr + lane_col, x);
 #pragma unroll
@@ -404,6 +412,7 @@ __global__ void __launch_bounds__(256, FwdLayout<DP, KEEP>::kPerSM)
   }
   if (a.state_out != nullptr && row_on) write16(a.state_out + (p * a.D + t) * a.M + c0, nc, S);
   if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
+  }
   // every load and MMA has been waited for by the loop that used it
   if (*abort_flag) linger();
   tc_fence_before();
@@ -459,7 +468,7 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
   prep<<<(unsigned)(BH * k.n), 128, LP::kBytes, stream>>>(mq, mk, a);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
   const dim3 grid((unsigned)BH, (unsigned)((s.M + kCB - 1) / kCB));
-  chain<<<grid, 256, L::kBytes, stream>>>(mq, mk, c);
+  chain<<<grid, kChainThreads, L::kBytes, stream>>>(mq, mk, c);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
