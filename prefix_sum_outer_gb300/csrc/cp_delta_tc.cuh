@@ -25,6 +25,13 @@ constexpr int kCh = 64;               // rows of a chunk
 constexpr int kBox = kCh * 128;       // bytes of a [64 x 64] bf16 tile
 constexpr uint32_t kDescHi = desc_hi(1024);
 
+// The first 1024-byte boundary of the shared memory, as an offset from its
+// array: the compiler then knows what follows for shared memory and addresses
+// it with 32 bits.
+__device__ __forceinline__ uint8_t* align_tiles(uint8_t* smem) {
+  return smem + (-smem_u32(smem) & 1023u);
+}
+
 // The gates of a chunk.  Every decay between two rows is a product of the a =
 // e^g between them, never a difference of sums: a cleared state's zero stays
 // an exact zero, 64 factors cost 64 roundings (4e-6 at worst), and a product

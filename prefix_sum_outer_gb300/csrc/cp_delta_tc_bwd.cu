@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
                           const __grid_constant__ CUtensorMap tm_k, const ChainArgs a) {
   using L = ChainLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = align_tiles(smem_raw);
   GateSlot* gates = reinterpret_cast<GateSlot*>(sm + L::oG);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [2]
   uint64_t *t_full = kq_full + 2, *p_full = kq_full + 3;
@@ -409,8 +408,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
                          const __grid_constant__ CUtensorMap tm_dk, const GradArgs a) {
   using L = GradLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = align_tiles(smem_raw);
   GateSlot* gs = reinterpret_cast<GateSlot*>(sm + L::oG);
   float* e_sum = reinterpret_cast<float*>(sm + L::oX);  // [8 warps][64]: pairs' part of dg
   float* dots = e_sum + 512;     // [2 column halves][6][64]: rows' sums, as written below

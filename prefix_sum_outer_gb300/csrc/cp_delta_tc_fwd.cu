@@ -63,8 +63,7 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
                          const __grid_constant__ CUtensorMap tm_k, const PrepArgs a) {
   using L = PrepLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = align_tiles(smem_raw);
   GateSlot* gs = reinterpret_cast<GateSlot*>(sm + L::oG);
   InvTiles* it = reinterpret_cast<InvTiles*>(sm + L::oInv);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::oBar);
@@ -218,8 +217,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
                         const __grid_constant__ CUtensorMap tm_k, const FwdArgs a) {
   using L = FwdLayout<DP, KEEP>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = align_tiles(smem_raw);
   GateSlot* gates = reinterpret_cast<GateSlot*>(sm + L::oG);
   uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + L::oBar);  // [2]
   uint64_t* t_full = kq_full + 2;
