@@ -46,13 +46,19 @@ struct PrepLayout {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
-  static constexpr int oP = 0;                 // P, then P T, hi, lo: over K, Q, done with by then
-  static constexpr int oT = kKQ;               // hi, lo
-  static constexpr int oInv = oT + 2 * kBox;
-  static constexpr int oG = oInv + (int)sizeof(InvTiles);
+  // T (hi, lo) lies over the blocks that it is made from, or over the second
+  // half of K, Q; P and then P T (hi, lo) over K, Q, done with by then.  The
+  // product with T's lo part reads 64 rows past it, which the tiles behind hold.
+  static constexpr bool kTOverInv = DP == 64;
+  static constexpr int oT = kTOverInv ? 0 : 2 * kBox;
+  static constexpr int oKQ = kTOverInv ? 2 * kBox : 0;
+  static constexpr int oP = oKQ;
+  static constexpr int oInv = kTOverInv ? 0 : kKQ;
+  static constexpr int oG = kTOverInv ? oKQ + kKQ : oInv + (int)sizeof(InvTiles);
   static constexpr int oBar = oG + (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 64 + 1024;
-  static constexpr int kPerSM = DP == 64 ? 4 : 3;
+  static constexpr int kPerSM = DP == 64 ? 6 : 4;
+  static_assert(kTOverInv ? sizeof(InvTiles) <= 2 * kBox : sizeof(InvTiles) >= kBox, "T's places");
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
   static_assert(sizeof(InvTiles) % 16 == 0 && sizeof(GateSlot) % 16 == 0, "alignment");
 };
@@ -88,18 +94,18 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     mbar_arrive_expect_tx(full, L::kKQ);
     const uint64_t keep = policy_evict_last();  // the chain reads K and Q again
     for (int x = 0; x < L::kBoxes; ++x) {
-      tma_load_3d(sm + x * L::kKQBox, &tm_k, full, 64 * x, i0, pk, keep);
-      tma_load_3d(sm + x * L::kKQBox + kBox, &tm_q, full, 64 * x, i0, pk, keep);
+      tma_load_3d(sm + L::oKQ + x * L::kKQBox, &tm_k, full, 64 * x, i0, pk, keep);
+      tma_load_3d(sm + L::oKQ + x * L::kKQBox + kBox, &tm_q, full, 64 * x, i0, pk, keep);
     }
   }
   if (w == 0) {
-    tmem_alloc(tmem_holder, 128);
+    tmem_alloc(tmem_holder, 64);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), t_pt = tmem + 64;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), t_pt = tmem;  // one after the other
   const uint32_t s_base = smem_u32(sm), lane_base = (uint32_t)w << 21;
   const uint32_t T_addr = s_base + L::oT, P_addr = s_base + L::oP;
   constexpr uint32_t id_nn64 = idesc_bf16_f32(128, 64, 0, 0);  // A [rows x K], B [cols x K]
@@ -107,7 +113,8 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     wait_or_abort(full, 0, a.status, abort_flag);
     __syncwarp();
     const uint32_t el = elect_one();
-    mma_tile<DP / 16, false, false>(el, tmem, s_base, s_base, id_nn64, 16, 16, L::kKQBox, L::kKQBox, true);
+    mma_tile<DP / 16, false, false>(el, tmem, s_base + L::oKQ, s_base + L::oKQ, id_nn64, 16, 16,
+                                    L::kKQBox, L::kKQBox, true);
     if (el) mma_commit(done);
   }
   if (w == 3) {  // under the product
@@ -131,6 +138,7 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
   invert_diag(it, w, lane, xw);
   __syncthreads();
   invert_below(it, w, lane, zh, zl);
+  if (L::kTOverInv) __syncthreads();
   put_t_transposed(sm + L::oT, kBox, w, lane, xw, zh, zl);
   tc_fence_before();
   fence_proxy_async_smem();
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
   __syncthreads();
   if (w == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 64);
   }
 }
 
