@@ -327,6 +327,7 @@ struct GradArgs {
   const __nv_bfloat16* go;
   const float *g, *beta, *xv;
   const uint8_t *s, *u, *ds, *dx;  // tiles
+  __nv_bfloat16 *dq, *dk;
   float *dq_part, *dk_part;     // [BH][N][D] fp32, where value heads share a key head; else null
   float *dg, *dbeta;
   int* status;
@@ -403,9 +404,7 @@ __device__ __forceinline__ void decayed_half(uint32_t t_acc, const GateSlot* gs,
 template <int DP>
 __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     delta_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_q,
-                         const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_dq,
-                         const __grid_constant__ CUtensorMap tm_dk, const GradArgs a) {
+                         const __grid_constant__ CUtensorMap tm_k, const GradArgs a) {
   using L = GradLayout<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_tiles(smem_raw);
@@ -455,11 +454,21 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     tmem_alloc(tmem_holder, L::kCols);
     tmem_relinquish();
   }
+  // what comes by plain loads sets out here, beside the copies: the gates of
+  // one warp's rows, and dO's part of the A tiles, a row's 16 columns
+  float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
   if (warp == 1) {
     const int64_t i = i0 + lane, at = p * a.N;
-    write_gates(gs, lane, i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
-                i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
+    gb = make_float4(i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
+                     i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
   }
+  const int do_row = threadIdx.x % 64, do_block = (threadIdx.x / 64) % 2, do_sub = threadIdx.x / 128;
+  uint4 dov[2];
+  auto load_do = [&](int m) {
+    const int col = 64 * m + 32 * do_block + 16 * do_sub;
+    read16(a.go + (p * a.N + i0 + do_row) * a.M + col, a.M - col, i0 + do_row < a.N, dov);
+  };
+  load_do(0);
   for (int i = threadIdx.x; i < 512; i += 256) e_sum[i] = 0.f;
   fence_proxy_async_smem();
   tc_fence_before();
@@ -474,15 +483,6 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   constexpr uint32_t id_nnD = idesc_bf16_f32(128, DP, 0, 0);
   constexpr uint32_t id_ntD = idesc_bf16_f32(128, DP, 0, 1);
   constexpr uint32_t id_ttD = idesc_bf16_f32(128, DP, 1, 1);
-  // dO's part of the A tiles: a row's 32 columns, no lo part
-  auto put_do = [&](int m) {
-    const int r = threadIdx.x % 64, h = (threadIdx.x / 64) % 2, q = threadIdx.x / 128;
-    const int col = 64 * m + 32 * h + 16 * q;
-    uint4 v[2];
-    read16(a.go + (p * a.N + i0 + r) * a.M + col, a.M - col, i0 + r < a.N, v);
-    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    put_parts(sm + L::oA + h * 2 * kBox + kBox, r, q, v, zero);
-  };
   if (warp == 0) {
     wait_or_abort(kq_full, 0, a.status, abort_flag);
     __syncwarp();
@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   float z = 0.f;  // <S, dS'>, this thread's share
   for (int m = 0; m < n_mb; ++m) {
     const int nb = min(2, blocks - 2 * m);
-    put_do(m);
+    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // no lo part
+    put_parts(sm + L::oA + do_block * 2 * kBox + kBox, do_row, do_sub, dov, zero);
+    if (m + 1 < n_mb) load_do(m + 1);
     fence_proxy_async_smem();
     __syncthreads();
     if (warp == 0) {
@@ -513,6 +515,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       }
       if (el) mma_commit(done);
     }
+    if (warp == 1 && m == 0) write_gates(gs, lane, gb.x, gb.y, gb.z, gb.w);
     wait_or_abort(full, m & 1, a.status, abort_flag);
     // the MMAs read the tiles at the same time
     for (int e = threadIdx.x; e < nb * DP * 4; e += 256) {
@@ -544,6 +547,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   tc_fence_after();
   for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
   if (lane == 0) z_sum[warp] = z;
+  __syncthreads();  // the gates
 
   // lanes 0-63 ("K rows"): i = t; lanes 64-127 ("Q rows"): i = t - 64
   const bool is_k = t < 64;
@@ -757,16 +761,17 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     }
   }
   if (a.dq_part == nullptr) {
-    fence_proxy_async_smem();
+    // by plain stores: a copy waits its turn behind the other CTA's loads and
+    // holds this one's memory for 5,200 of its 20,000 cycles
     __syncthreads();
-    if (issuer) {
-      for (int x = 0; x < L::kBoxes; ++x) {
-        if (64 * x >= a.D) break;
-        tma_store_3d(&tm_dk, sm + x * L::kKQBox, 64 * x, i0, (int)p);
-        tma_store_3d(&tm_dq, sm + x * L::kKQBox + kBox, 64 * x, i0, (int)p);
-      }
-      tma_store_commit();
-      tma_store_wait_read_all();
+#pragma unroll 4
+    for (int e = threadIdx.x; e < L::kBoxes * 1024; e += 256) {
+      const int row = (e / 8) % 128, ch = e % 8, col = e / 1024 * 64 + 8 * ch;
+      const uint4 w = *reinterpret_cast<const uint4*>(sm + e / 1024 * L::kKQBox + row * 128 +
+                                                      ((ch ^ (row & 7)) << 4));
+      const int64_t at = p * a.N + i0 + (row & 63);
+      if (i0 + (row & 63) < a.N && col < a.D)
+        *reinterpret_cast<uint4*>((row < 64 ? a.dk : a.dq) + at * a.D + col) = w;
     }
   }
   if (*abort_flag) linger();
@@ -810,14 +815,13 @@ cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const ChainArgs& c, c
     return CP_ERR_CUDA;
   // (encoding a map needs the device's context current in this thread: the
   // calls above see to that)
-  CUtensorMap q, kk, dq, dk;
-  if (!make_chunk_map(&q, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&kk, f.k, s.B * s.Hk, s.N, s.D) ||
-      !make_chunk_map(&dq, f.dq, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&dk, f.dk, s.B * s.Hk, s.N, s.D))
+  CUtensorMap q, kk;
+  if (!make_chunk_map(&q, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&kk, f.k, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
   const unsigned BH = (unsigned)(s.B * s.H);
   chain<<<dim3(BH, (unsigned)((s.M + kCB - 1) / kCB)), kChainThreads, LC::kBytes, stream>>>(q, kk, c);
   if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
-  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, dq, dk, g);
+  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, g);
   return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -853,6 +857,7 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
     g.dq_part = reinterpret_cast<float*>(w.part_at);
     g.dk_part = reinterpret_cast<float*>(w.part_at + w.part);
   }
+  g.dq = static_cast<__nv_bfloat16*>(f.dq); g.dk = static_cast<__nv_bfloat16*>(f.dk);
   g.dg = f.dg; g.dbeta = f.dbeta; g.status = status;
   g.N = s.N; g.n_chunks = (int)k.n; g.BH = (int)BH; g.H = c.H; g.group = c.group; g.D = c.D;
   g.M = c.M; g.scale = s.scale;
