@@ -516,6 +516,14 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       if (el) mma_commit(done);
     }
     if (warp == 1 && m == 0) write_gates(gs, lane, gb.x, gb.y, gb.z, gb.w);
+    if (warp >= 6 && m == 0) {  // dX . V of the rows, from the chain's blocks
+      const int i = threadIdx.x - 192;
+      float d = 0.f;
+      if (i0 + i < a.N)
+#pragma unroll 4
+        for (int x = 0; x < (a.M + 15) / 16; ++x) d += a.xv[((int64_t)x * a.BH + p) * a.N + i0 + i];
+      dots[640 + i] = d;
+    }
     wait_or_abort(full, m & 1, a.status, abort_flag);
     // the MMAs read the tiles at the same time
     for (int e = threadIdx.x; e < nb * DP * 4; e += 256) {
@@ -721,8 +729,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
         for (int x = 0; x < 8; ++x) s += e_sum[x * 64 + j];
         const int64_t at = p * a.N + i0 + j;
         a.dg[at] = s;
-        float d = dots[192 + j] + dots[576 + j] - gs->gam[j] * kx[h];
-        for (int x = 0; x < (a.M + 15) / 16; ++x) d += a.xv[(int64_t)x * a.BH * a.N + at];
+        const float d = dots[192 + j] + dots[576 + j] + dots[640 + j] - gs->gam[j] * kx[h];
         // U carries b as a factor, far above the smallest number down to 2^-80
         const float b = gs->b[j];
         a.dbeta[at] = fabsf(b) < 0x1p-80f ? d : dots[256 + j] / b;
@@ -761,8 +768,6 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     }
   }
   if (a.dq_part == nullptr) {
-    // by plain stores: a copy waits its turn behind the other CTA's loads and
-    // holds this one's memory for 5,200 of its 20,000 cycles
     __syncthreads();
 #pragma unroll 4
     for (int e = threadIdx.x; e < L::kBoxes * 1024; e += 256) {
