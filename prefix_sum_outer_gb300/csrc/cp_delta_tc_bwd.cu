@@ -695,45 +695,40 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     if (row32 == wg) dots[256 + i] = own;
   }
   __syncthreads();
-  if (warp == 7) {
-    // the gates' gradients: lane l has rows l and l + 32
+  if (warp >= 6) {
+    // the gates' gradients, a warp to a half of the rows: lane l has row l of it
+    const int h = warp - 6, j = lane + 32 * h, far = lane + 32 * (1 - h);
     const float zt = gs->gam[kCh - 1] * (((z_sum[0] + z_sum[1]) + (z_sum[2] + z_sum[3])) +
                                          ((z_sum[4] + z_sum[5]) + (z_sum[6] + z_sum[7])));
-    float r[2], c[2], own[2], kx[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = lane + 32 * h;
-      kx[h] = dots[j] + dots[384 + j];
-      const float qo = dots[64 + j] + dots[448 + j], ku = dots[128 + j] + dots[512 + j];
-      r[h] = gs->gam[j] * (a.scale * qo - gs->b[j] * kx[h]);
-      own[h] = c[h] = gs->del[j] * ku;
-    }
-    // sums of r from the row on, of c before it
+    const auto kx = [&](int x) { return dots[x] + dots[384 + x]; };
+    const auto with_s = [&](int x) {   // row x's part with S
+      return gs->gam[x] * (a.scale * (dots[64 + x] + dots[448 + x]) - gs->b[x] * kx(x));
+    };
+    const auto with_ds = [&](int x) {  // and with dS'
+      return gs->del[x] * (dots[128 + x] + dots[512 + x]);
+    };
+    // sums of the first from the row on, of the second before it; the other
+    // half gives one of them whole
+    float r = with_s(j), c = with_ds(j), rest = h ? with_ds(far) : with_s(far);
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float x = __shfl_down_sync(0xffffffffu, r[h], o), y = __shfl_up_sync(0xffffffffu, c[h], o);
-        if (lane + o < 32) r[h] += x;
-        if (lane >= o) c[h] += y;
-      }
+      const float x = __shfl_down_sync(0xffffffffu, r, o), y = __shfl_up_sync(0xffffffffu, c, o);
+      rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      if (lane + o < 32) r += x;
+      if (lane >= o) c += y;
     }
-    const float r_hi = __shfl_sync(0xffffffffu, r[1], 0), c_lo = __shfl_sync(0xffffffffu, c[0], 31);
-    c[0] -= own[0];
-    c[1] -= own[1];
+    c = __shfl_up_sync(0xffffffffu, c, 1);
+    if (lane == 0) c = 0.f;
+    float pairs = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = lane + 32 * h;
-      if (i0 + j < a.N) {
-        float s = zt + r[h] + c[h] + (h ? c_lo : r_hi);
-        for (int x = 0; x < 8; ++x) s += e_sum[x * 64 + j];
-        const int64_t at = p * a.N + i0 + j;
-        a.dg[at] = s;
-        const float d = dots[192 + j] + dots[576 + j] + dots[640 + j] - gs->gam[j] * kx[h];
-        // U carries b as a factor, far above the smallest number down to 2^-80
-        const float b = gs->b[j];
-        a.dbeta[at] = fabsf(b) < 0x1p-80f ? d : dots[256 + j] / b;
-      }
+    for (int x = 0; x < 8; ++x) pairs += e_sum[x * 64 + j];
+    if (i0 + j < a.N) {
+      const int64_t at = p * a.N + i0 + j;
+      a.dg[at] = zt + r + c + rest + pairs;
+      const float d = dots[192 + j] + dots[576 + j] + dots[640 + j] - gs->gam[j] * kx(j);
+      // U carries b as a factor, far above the smallest number down to 2^-80
+      const float b = gs->b[j];
+      a.dbeta[at] = fabsf(b) < 0x1p-80f ? d : dots[256 + j] / b;
     }
   }
   wait_or_abort(done + 1, 0, a.status, abort_flag);
@@ -768,12 +763,15 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     }
   }
   if (a.dq_part == nullptr) {
-    __syncthreads();
-#pragma unroll 4
-    for (int e = threadIdx.x; e < L::kBoxes * 1024; e += 256) {
-      const int row = (e / 8) % 128, ch = e % 8, col = e / 1024 * 64 + 8 * ch;
-      const uint4 w = *reinterpret_cast<const uint4*>(sm + e / 1024 * L::kKQBox + row * 128 +
-                                                      ((ch ^ (row & 7)) << 4));
+    // the warp's 32 rows, its half of the columns, in whole sectors
+    __syncwarp();
+    constexpr int kPieces = HC / 8;
+#pragma unroll
+    for (int x = 0; x < kPieces; ++x) {
+      const int row = 32 * (warp % 4) + (32 * x + lane) / kPieces;
+      const int col = wg * HC + 8 * (lane % kPieces);
+      const uint4 w = *reinterpret_cast<const uint4*>(
+          sm + (col / 64) * L::kKQBox + row * 128 + (((col % 64) / 8 ^ (row & 7)) << 4));
       const int64_t at = p * a.N + i0 + (row & 63);
       if (i0 + (row & 63) < a.N && col < a.D)
         *reinterpret_cast<uint4*>((row < 64 ? a.dk : a.dq) + at * a.D + col) = w;
