@@ -9,12 +9,14 @@
 // Input rows may have any strides (the projection's token-major rows, read in
 // place); output rows are head-major and dense, as the products take them, so
 // the transposition costs nothing beside the norm.  The pass is bound by its
-// reads and writes, so what counts is loads in flight: a row is held by D/8
-// lanes, eight features each (16 bytes of bf16 or fp16), as many rows to a warp
-// as fit, a warp takes four rows to a lane group (backward: two) at once and
-// loads the next four before it works on them.  The partner of a feature under the rotation comes from its
-// lane by shuffle.  Everything between the load and the store is fp32 and
-// rounded once.
+// reads and writes, so what counts is loads in flight and few instructions
+// beside them: a row is held by D / 16 lanes, each with eight features and the
+// eight they turn with (two 16-byte pieces of bf16 or fp16), so that the turn
+// stays within a lane and a sum over the row takes few shuffles; as many rows
+// to a warp as fit, two turns of them at once (backward: one), and the next
+// ones loaded before these are worked on.  Where R or D is not a multiple of 16
+// a lane has eight features and asks for their partners by shuffle.  Everything
+// between the load and the store is fp32 and rounded once.
 #include <algorithm>
 
 #include "cp_delta.cuh"
@@ -43,7 +45,7 @@ struct Args {
   int64_t cs_batch;        // elements between batches (0: shared)
   float* dw_part;          // [2][blocks][D]
   int64_t N;
-  int D, R, lanes;         // lanes of a row: D / 8 rounded up to a power of two
+  int D, R, lanes;         // lanes of a row, a power of two
   float c, eps;
 };
 
@@ -88,85 +90,89 @@ __device__ __forceinline__ float dot8(const float2 (&x)[4], const float2 (&y)[4]
   return s.x + s.y;
 }
 
-// The cosines of a lane's eight features and their sines with the rotation's
-// sign (dir = -1 turns back); features from R on stand still.  FAST: R/2 is a
-// multiple of 8, so the lane's features all lie in one half.
-template <bool FAST>
+// FAST (R and D multiples of 16): the cosines and sines of a lane's eight
+// features f0 .. of the turned ones' first half, dir = -1 turning back; the rest
+// stands still.
 __device__ __forceinline__ void load_angles(float2 (&c)[4], float2 (&s)[4], const float* cs,
-                                            const float* sn, int R, int f0, bool wide, float dir) {
+                                            const float* sn, bool turned, int f0, bool wide,
+                                            float dir) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = both(1.f);
+    s[i] = both(0.f);
+  }
+  if (!turned) return;
+  const float2 d = both(dir);
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + f0 + 2 * i);
+      const float4 y = *reinterpret_cast<const float4*>(sn + f0 + 2 * i);
+      c[i] = make_float2(x.x, x.y);
+      c[i + 1] = make_float2(x.z, x.w);
+      s[i] = mul2(d, make_float2(y.x, y.y));
+      s[i + 1] = mul2(d, make_float2(y.z, y.w));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = make_float2(cs[f0 + 2 * i], cs[f0 + 2 * i + 1]);
+      s[i] = mul2(d, make_float2(sn[f0 + 2 * i], sn[f0 + 2 * i + 1]));
+    }
+  }
+}
+// the turn of the lane's two pieces
+__device__ __forceinline__ void rotate8(float2 (&y)[2][4], const float2 (&c)[4],
+                                        const float2 (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 lo = y[0][i], hi = y[1][i];
+    y[0][i] = fma2(hi, mul2(s[i], both(-1.f)), mul2(lo, c[i]));
+    y[1][i] = fma2(lo, s[i], mul2(hi, c[i]));
+  }
+}
+
+// Otherwise: those of the lane's eight features f0 .., wherever they lie, the
+// sines with the rotation's sign, features from R on standing still ..
+__device__ __forceinline__ void load_angles_any(float2 (&c)[4], float2 (&s)[4], const float* cs,
+                                                const float* sn, int R, int f0, float dir) {
   const int half = R / 2;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     c[i] = both(1.f);
     s[i] = both(0.f);
   }
-  if constexpr (FAST) {
-    if (f0 >= R) return;
-    const int a = f0 < half ? f0 : f0 - half;
-    const float2 d = both(f0 < half ? -dir : dir);
-    if (wide) {
+  float* cf = reinterpret_cast<float*>(c);
+  float* sf = reinterpret_cast<float*>(s);
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const float4 x = *reinterpret_cast<const float4*>(cs + a + 2 * i);
-        const float4 y = *reinterpret_cast<const float4*>(sn + a + 2 * i);
-        c[i] = make_float2(x.x, x.y);
-        c[i + 1] = make_float2(x.z, x.w);
-        s[i] = mul2(d, make_float2(y.x, y.y));
-        s[i + 1] = mul2(d, make_float2(y.z, y.w));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = make_float2(cs[a + 2 * i], cs[a + 2 * i + 1]);
-        s[i] = mul2(d, make_float2(sn[a + 2 * i], sn[a + 2 * i + 1]));
-      }
-    }
-  } else {
-    float* cf = reinterpret_cast<float*>(c);
-    float* sf = reinterpret_cast<float*>(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int f = f0 + i;
-      if (f < R) {
-        cf[i] = cs[f < half ? f : f - half];
-        sf[i] = (f < half ? -dir : dir) * sn[f < half ? f : f - half];
-      }
+  for (int i = 0; i < 8; ++i) {
+    const int f = f0 + i;
+    if (f < R) {
+      cf[i] = cs[f < half ? f : f - half];
+      sf[i] = (f < half ? -dir : dir) * sn[f < half ? f : f - half];
     }
   }
 }
-
-// Turn a row spread over `lanes` lanes (lane l: features 8 l ..).  A feature f <
-// R has its partner R/2 away: with FAST the whole lanes trade, otherwise every
-// feature asks for its partner's lane in turn.
-template <bool FAST>
-__device__ __forceinline__ void rotate8(float2 (&y)[4], const float2 (&c)[4], const float2 (&s)[4],
-                                        int R, int l, int lanes) {
+// .. and the turn of a row spread over `lanes` lanes (lane l: features 8 l ..):
+// a feature f < R has its partner R / 2 away and asks for that one's lane.
+__device__ __forceinline__ void rotate8_any(float2 (&y)[4], const float2 (&c)[4],
+                                            const float2 (&s)[4], int R, int l, int lanes) {
   const int half = R / 2, f0 = 8 * l;
   if (half == 0) return;
-  if constexpr (FAST) {
-    const int src = f0 >= R ? l : (f0 < half ? l + half / 8 : l - half / 8);
+  float* yf = reinterpret_cast<float*>(y);
+  float z[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 z = make_float2(__shfl_sync(0xffffffffu, y[i].x, src, lanes),
-                                   __shfl_sync(0xffffffffu, y[i].y, src, lanes));
-      y[i] = fma2(z, s[i], mul2(y[i], c[i]));
+  for (int i = 0; i < 8; ++i) {
+    const int f = f0 + i, want = f < half ? f + half : (f < R ? f - half : f);
+    z[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = __shfl_sync(0xffffffffu, yf[j], want / 8, lanes);
+      if (want % 8 == j) z[i] = t;
     }
-  } else {
-    float* yf = reinterpret_cast<float*>(y);
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int f = f0 + i, want = f < half ? f + half : (f < R ? f - half : f);
-      z[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = __shfl_sync(0xffffffffu, yf[j], want / 8, lanes);
-        if (want % 8 == j) z[i] = t;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fma2(make_float2(z[2 * i], z[2 * i + 1]), s[i], mul2(y[i], c[i]));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = fma2(make_float2(z[2 * i], z[2 * i + 1]), s[i], mul2(y[i], c[i]));
 }
 
 // A row's place: token (batch b, position n) and head, advanced by a fixed
@@ -180,11 +186,12 @@ struct Place {
 template <typename T, bool BWD, bool FAST>
 __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
   extern __shared__ float sm[];  // BWD: [kWarps][D] partial weight gradients
-  constexpr int U = FAST ? (BWD ? 2 : 4) : 1;  // turns in flight
+  constexpr int U = FAST && !BWD ? 2 : 1;  // turns in flight
+  constexpr int P = FAST ? 2 : 1;          // a lane's pieces of eight features
   const Side& s = a.side[blockIdx.y];
   const int lanes = a.lanes, per_warp = 32 / lanes;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, l = lane % lanes;
-  const bool on = 8 * l < a.D;
+  const bool on = 8 * P * l < a.D;
   const T* x = static_cast<const T*>(s.x);
   T* y = static_cast<T*>(s.y);
   const T* gy = static_cast<const T*>(s.gy);
@@ -193,19 +200,33 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && s.sb % piece == 0 &&
                     s.sh % piece == 0 && s.sn % piece == 0;
   const int half = a.R / 2;
+  // the pieces' first features: FAST pairs the turned features' halves, and
+  // those of the rest
+  int f[P];
+  f[0] = 8 * l;
+  const bool turned = 8 * l < half;  // (FAST)
+  if constexpr (FAST) {
+    f[1] = f[0] + half;
+    if (!turned) {
+      f[0] += half;
+      f[1] = f[0] + (a.D - a.R) / 2;
+    }
+  }
   const bool wide_cs = ((reinterpret_cast<uintptr_t>(a.cos) | reinterpret_cast<uintptr_t>(a.sin)) & 15) == 0 &&
                        half % 4 == 0 && a.cs_batch % 4 == 0;
-  float2 wt[4], dw[4];
+  float2 wt[P][4], dw[P][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wt[i] = both(1.f);
-    if (s.w != nullptr && on)
-      wt[i] = make_float2(ld_f32<T>(static_cast<const T*>(s.w) + 8 * l + 2 * i),
-                          ld_f32<T>(static_cast<const T*>(s.w) + 8 * l + 2 * i + 1));
-    dw[i] = both(0.f);
-  }
+  for (int e = 0; e < P; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wt[e][i] = both(1.f);
+      if (s.w != nullptr && on)
+        wt[e][i] = make_float2(ld_f32<T>(static_cast<const T*>(s.w) + f[e] + 2 * i),
+                               ld_f32<T>(static_cast<const T*>(s.w) + f[e] + 2 * i + 1));
+      dw[e][i] = both(0.f);
+    }
   // a warp takes U x per_warp consecutive rows, then jumps by `step`
-  const uint32_t step = gridDim.x * kWarps * per_warp * U;  // (at most 152 x 8 x 32 x 4)
+  const uint32_t step = gridDim.x * kWarps * per_warp * U;  // (at most 152 x 8 x 32 x 2)
   const uint32_t H = (uint32_t)s.H, N = (uint32_t)a.N;
   const bool per_batch = a.cs_batch != 0;
   const uint32_t step_tok = step / H, step_h = step % H;
@@ -219,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
   }
   // a turn's rows, as loaded
   struct Turn {
-    Raw8<T> x[U], g[BWD ? U : 1];
+    Raw8<T> x[U][P], g[BWD ? U : 1][P];
     uint32_t out_row[U], tok[U];  // rows of the output, of the angles
     bool live[U];
   };
@@ -230,11 +251,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
       q.live[u] = r_warp + u * per_warp + lane / lanes < s.rows && on;
       q.out_row[u] = (at.b * H + at.h) * N + at.n;
       q.tok[u] = (per_batch ? at.b * N : 0) + at.n;
-      q.x[u] = Raw8<T>{};
-      if constexpr (BWD) q.g[u] = Raw8<T>{};
-      if (q.live[u]) {
-        load8<T>(q.x[u], x + at.b * s.sb + at.h * s.sh + at.n * s.sn + 8 * l, wide);
-        if constexpr (BWD) load8<T>(q.g[u], gy + (int64_t)q.out_row[u] * a.D + 8 * l, true);
+      const T* xr = x + at.b * s.sb + at.h * s.sh + at.n * s.sn;
+      const T* gr = gy + (int64_t)q.out_row[u] * a.D;
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        q.x[u][e] = Raw8<T>{};
+        if (q.live[u]) load8<T>(q.x[u][e], xr + f[e], wide);
+        if constexpr (BWD) {
+          q.g[u][e] = Raw8<T>{};
+          if (q.live[u]) load8<T>(q.g[u][e], gr + f[e], true);
+        }
       }
       at.h += per_warp;
       while (at.h >= H) {
@@ -272,35 +298,61 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
       if (u == 0 || q.tok[u] != q.tok[u - 1]) {
         const int64_t cs = per_batch ? q.tok[u] / N * a.cs_batch + (int64_t)(q.tok[u] % N) * half
                                      : (int64_t)q.tok[u] * half;
-        load_angles<FAST>(c, si, a.cos + cs, a.sin + cs, q.live[u] ? a.R : 0, 8 * l, wide_cs,
+        if constexpr (FAST)
+          load_angles(c, si, a.cos + cs, a.sin + cs, q.live[u] && turned, 8 * l, wide_cs,
+                      BWD ? -1.f : 1.f);
+        else
+          load_angles_any(c, si, a.cos + cs, a.sin + cs, q.live[u] ? a.R : 0, 8 * l,
                           BWD ? -1.f : 1.f);
       }
-      T* to = y + (int64_t)q.out_row[u] * a.D + 8 * l;
-      float2 v[4];
-      unpack8<T>(v, q.x[u]);
-      float ss = dot8(v, v);
+      const auto turn = [&](float2(&y8)[P][4]) {
+        if constexpr (FAST)
+          rotate8(y8, c, si);
+        else
+          rotate8_any(y8[0], c, si, a.R, l, lanes);
+      };
+      T* to = y + (int64_t)q.out_row[u] * a.D;
+      float2 v[P][4];
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        unpack8<T>(v[e], q.x[u][e]);
+        ss += dot8(v[e], v[e]);
+      }
       for (int o = lanes / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float inv = rsqrtf(fmaf(a.c, ss, a.eps));  // 2 ulp
       if constexpr (!BWD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mul2(both(inv), wt[i]));
-        rotate8<FAST>(v, c, si, a.R, l, lanes);
-        if (q.live[u]) store8<T>(to, v);
-      } else {
-        float2 d[4];
-        unpack8<T>(d, q.g[u]);
-        rotate8<FAST>(d, c, si, a.R, l, lanes);
+        for (int e = 0; e < P; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[e][i] = mul2(v[e][i], mul2(both(inv), wt[e][i]));
+        turn(v);
         if (q.live[u])
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dw[i] = fma2(d[i], mul2(v[i], both(inv)), dw[i]);
+          for (int e = 0; e < P; ++e) store8<T>(to + f[e], v[e]);
+      } else {
+        float2 d[P][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = mul2(d[i], wt[i]);
-        float xt = dot8(v, d);
+        for (int e = 0; e < P; ++e) unpack8<T>(d[e], q.g[u][e]);
+        turn(d);
+        float xt = 0.f;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (q.live[u]) dw[e][i] = fma2(d[e][i], mul2(v[e][i], both(inv)), dw[e][i]);
+            d[e][i] = mul2(d[e][i], wt[e][i]);
+          }
+          xt += dot8(v[e], d[e]);
+        }
         for (int o = lanes / 2; o > 0; o /= 2) xt += __shfl_xor_sync(0xffffffffu, xt, o);
         const float2 m = both(-a.c * inv * inv * xt);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = mul2(both(inv), fma2(m, v[i], d[i]));
-        if (q.live[u]) store8<T>(to, d);
+        for (int e = 0; e < P; ++e) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[e][i] = mul2(both(inv), fma2(m, v[e][i], d[e][i]));
+          if (q.live[u]) store8<T>(to + f[e], d[e]);
+        }
       }
     }
   }
@@ -308,17 +360,20 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
     if (s.w == nullptr) return;
     // rows of a warp, then the warps, in a fixed order
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      for (int o = lanes; o < 32; o *= 2) {
-        dw[i].x += __shfl_xor_sync(0xffffffffu, dw[i].x, o);
-        dw[i].y += __shfl_xor_sync(0xffffffffu, dw[i].y, o);
-      }
-    if (lane < lanes && on)
+    for (int e = 0; e < P; ++e) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sm[w * a.D + 8 * l + 2 * i] = dw[i].x;
-        sm[w * a.D + 8 * l + 2 * i + 1] = dw[i].y;
-      }
+      for (int i = 0; i < 4; ++i)
+        for (int o = lanes; o < 32; o *= 2) {
+          dw[e][i].x += __shfl_xor_sync(0xffffffffu, dw[e][i].x, o);
+          dw[e][i].y += __shfl_xor_sync(0xffffffffu, dw[e][i].y, o);
+        }
+      if (lane < lanes && on)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sm[w * a.D + f[e] + 2 * i] = dw[e][i].x;
+          sm[w * a.D + f[e] + 2 * i + 1] = dw[e][i].y;
+        }
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < a.D; d += kThreads) {
       float t = 0.f;
@@ -345,17 +400,17 @@ __global__ void __launch_bounds__(128)
   if (threadIdx.x == 0) out[blockIdx.x] = from_f32<T>(red[0] + red[1] + red[2] + red[3]);
 }
 
-int row_lanes(int64_t D) {
+int row_lanes(int64_t D, int features) {
   int l = 1;
-  while (8 * l < D) l *= 2;
+  while (features * l < D) l *= 2;
   return l;
 }
 
 // one CTA of each side to an SM, two resident; fewer when the rows do not fill
 // them
 int n_blocks(const QkRope& f) {
-  // (a CTA's turn; the kernel takes up to four of them at once)
-  const int64_t per = kWarps * (32 / row_lanes(f.D));
+  // (the smallest turn that a CTA takes: rows of eight features a lane)
+  const int64_t per = kWarps * (32 / row_lanes(f.D, 8));
   const int64_t rows = f.B * f.N * std::max(f.Hq, f.Hk);
   return (int)std::min<int64_t>((rows + per - 1) / per, kPlanSMs);
 }
@@ -376,11 +431,11 @@ cudaError_t run(const QkRope& f, float* scratch, bool backward, cudaStream_t str
   }
   a.cos = f.cos; a.sin = f.sin; a.cs_batch = f.cs_batch;
   a.dw_part = scratch;
-  a.N = f.N; a.D = (int)f.D; a.R = (int)f.R; a.lanes = row_lanes(f.D);
+  const bool fast = f.R % 16 == 0 && f.D % 16 == 0;
+  a.N = f.N; a.D = (int)f.D; a.R = (int)f.R; a.lanes = row_lanes(f.D, fast ? 16 : 8);
   a.c = f.rms ? 1.f / (float)f.D : 1.f;
   a.eps = f.eps;
   const dim3 grid((unsigned)n_blocks(f), 2);
-  const bool fast = f.R % 16 == 0;
   if (!backward) {
     (fast ? qk_rope_kernel<T, false, true> : qk_rope_kernel<T, false, false>)<<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
