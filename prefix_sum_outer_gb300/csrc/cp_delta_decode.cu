@@ -4,7 +4,7 @@
 //     S'^T q = a S^T q + (k . q) u,
 // so both sums over the rows of S run while S is in registers and the state is
 // read and written once: 8 D M bytes per head, which bound the step.  A CTA
-// takes 64 value columns of one head, as 16 groups of four or, where rows are
+// takes 32 value columns of one head, as 8 groups of four or, where rows are
 // not whole 16-byte pieces, one by one; its threads hold every row of them,
 // ROWS each.
 //
@@ -19,8 +19,12 @@ namespace {
 
 using namespace delta;
 
-constexpr int kThreads = 256;
-constexpr int kCols = 64;  // value columns of a CTA
+// A CTA has one barrier between its loads and its stores, so an SM wants many
+// small ones out of step: bf16, B = 512, H = 16, D = M = 64, back to back, 49.6
+// us with ten CTAs of 32 columns, 51.7 with five of 64.
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCols = 32;  // value columns of a CTA
 
 template <int V>
 struct Vec;
@@ -60,16 +64,16 @@ __device__ __forceinline__ void st_state(float* p, Vec<V> v) {
 // Consecutive threads take consecutive columns, so a warp reads whole pieces of
 // state rows.
 template <typename T, int V, int ROWS, bool STREAM>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, ROWS <= 4 ? 10 : 1)
     delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                         const float* __restrict__ g, const float* __restrict__ beta,
                         const int* __restrict__ slots, T* __restrict__ out,
                         float* __restrict__ state, int64_t pool, int H, int group, int D, int M,
                         float scale) {
-  constexpr int CG = kCols / V;         // column groups
+  constexpr int CG = kCols / V;         // column groups (8 or 32: a warp has whole row groups)
   constexpr int RG = kThreads / CG;     // row groups
-  __shared__ float part[2][8][kCols];   // per-warp sums: a S^T k and a S^T q, unscaled
-  __shared__ float kq_part[8];
+  __shared__ float part[2][kWarps][kCols];   // per-warp sums: a S^T k and a S^T q, unscaled
+  __shared__ float kq_part[kWarps];
   const int64_t p = blockIdx.x;         // b * H + h
   const int64_t b = p / H;
   const int h = (int)(p % H), c0 = blockIdx.y * kCols;
@@ -122,25 +126,22 @@ __global__ void __launch_bounds__(kThreads)
       sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], o);
     }
   }
-  // with 64 column groups a warp covers half the columns of one row group
-  constexpr int SLOTS = CG >= 32 ? RG : 8;
-  const int at = CG >= 32 ? rg : w;
   if (lane < CG)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      part[0][at][cg * V + i] = sk[i];
-      part[1][at][cg * V + i] = sq[i];
+      part[0][w][cg * V + i] = sk[i];
+      part[1][w][cg * V + i] = sq[i];
     }
-  if (lane == 0 && cg == 0) kq_part[at] = kq;
+  if (lane == 0 && cg == 0) kq_part[w] = kq;
   __syncthreads();
   float u[V], o[V], dot = 0.f;
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) dot += kq_part[s];
+  for (int s = 0; s < kWarps; ++s) dot += kq_part[s];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) {
+    for (int s = 0; s < kWarps; ++s) {
       x += part[0][s][cg * V + i];
       y += part[1][s][cg * V + i];
     }
