@@ -8,6 +8,10 @@
 // not whole 16-byte pieces, one by one; its threads hold every row of them,
 // ROWS each.
 //
+// bf16, B = 512, H = 16, D = M = 64: 47.5 us a step back to back, 5.7 TB/s; every
+// store of a head waits for all of its loads, which the plain step's do not
+// (42.8 us for the same state).
+//
 // A state of a pool is addressed by the sequence's slot; a slot outside the
 // pool is an idle row: out is zero and no state is touched.
 #include <algorithm>
@@ -20,7 +24,7 @@ namespace {
 using namespace delta;
 
 // A CTA has one barrier between its loads and its stores, so an SM wants many
-// small ones out of step: bf16, B = 512, H = 16, D = M = 64, back to back, 49.6
+// small ones out of step: bf16, B = 512, H = 16, D = M = 64, back to back, 47.5
 // us with ten CTAs of 32 columns, 51.7 with five of 64.
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;

@@ -6,9 +6,9 @@
 // gradient are bf16 as they come; what is computed (S, R, U, P, the inverse) is
 // fp32 and enters a product as hi + lo, two bf16 numbers that keep 16 bits of
 // it, so a product of two such factors is four MMAs and of one with an input
-// two.  One bf16 number per factor would do
-// for bf16 outputs, but leaves 2^-9 in the carried state and in the gradients
-// of the gates, which are fp32.
+// two.  One bf16 number per factor would do for bf16 outputs, but leaves 2^-9 in
+// the carried state and in the gradients of the gates, which are fp32; two leave
+// 3e-6 to 6e-6 there, ten times fp32's own.
 //
 // An operand tile is 64 columns wide (128 bytes, 128-byte swizzle), so it can
 // enter as [rows x K] or transposed, by its descriptor alone.
@@ -482,9 +482,9 @@ __device__ __forceinline__ void put_t_transposed(uint8_t* hi, int part, int a, i
 // Row i of the chunk's k.k or q.k (lane of the accumulator at t_kk), weighted
 // by the decays: w times the product of a after row j up to row i, for j < i
 // (and for j = i, where it is w, with `diag`), 0 elsewhere, last columns first;
-// f(c, v) takes columns 16 c .. 16 c + 15.  row32: the row's half of the chunk, uniform over
-// the warp.  From the row's own half the product runs down the columns; below
-// it, a piece's columns share a row factor.
+// f(c, v) takes columns 16 c .. 16 c + 15.  row32: the row's half of the chunk,
+// uniform over the warp.  From the row's own half the product runs down the
+// columns; below it, a piece's columns share a row factor.
 template <class F>
 __device__ __forceinline__ void decayed_row(uint32_t t_kk, const GateSlot* gs, int i, bool diag,
                                             int row32, float w, F f) {

@@ -13,10 +13,12 @@
 //    one runs, dX, dV = b dX and dX . V go out.  dU enters in three parts: P^T
 //    dO sums up to 64 rows, of which T^T leaves the differences when keys
 //    repeat, so dU's rounding is the largest error of dX.  It leaves dX and the
-//    dS' of every chunk as hi and lo parts.
+//    dS' of every chunk as hi and lo parts.  Bound by its latency as the forward's
+//    is: B = 8, H = 16, N = 4096, D = M = 64, 213 us, 4.4 TB/s.
 //
 // 2. The gradients, one CTA per head and chunk, all chunks at once: every factor
-//    comes as the operand tile that the chains left.  Lanes 0-63 are the rows of K, 64-127 those of Q:
+//    comes as the operand tile that the chains left.  Lanes 0-63 are the rows of
+//    K, 64-127 those of Q:
 //        [dX; dO] U^T  -> Ma (A's part), Mq (P's part), by the decays
 //        [dX; dO] S^T,  U dS'^T,  [Ma; Mq] K,  Ma^T K + Mq^T Q
 //        dK = -gam b dX S^T + del U dS'^T + Ma K + Ma^T K + Mq^T Q
@@ -26,7 +28,11 @@
 //             = dX_i . V_i - gam_i k_i . (S dX_i) + sum_j Ma_ij / b_i k_i.k_j
 //    (Ma / b is what is at hand), with dX . V from the chain.  The first is the
 //    diagonal of dX U^T; the second, its value at b_i = 0 too, is a difference
-//    of terms that nearly cancel when keys repeat.
+//    of terms that nearly cancel when keys repeat.  Two CTAs fill an SM's tensor
+//    and shared memory (one at D > 64), and a CTA is a line of stages: 4k of its
+//    16k cycles are the products, 3k the copies, the rest the lanes' work, of
+//    which whatever can runs under the products.  B = 8, H = 16, N = 4096, D = M
+//    = 64: 252 us, 3.5 TB/s, 45 % of the issue slots.
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"

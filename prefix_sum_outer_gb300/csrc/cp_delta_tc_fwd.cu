@@ -4,7 +4,10 @@
 // 1. What a chunk needs of its own keys, queries and gates, one CTA per value
 //    head and chunk: [K; Q] K^T by MMA, A and P from it by the decays, T = (I +
 //    A)^-1 by blocks, P T by MMA; the tiles of T, P T (and, for a backward, P)
-//    go to memory as they lie in shared memory.
+//    go to memory as they lie in shared memory.  A CTA's steps wait for one
+//    another, so what counts is CTAs to an SM: T lies over what it is made from
+//    and P T over P, in both memories, and six fit (D <= 64; four fit before,
+//    122 us).  B = 8, H = 16, N = 4096, D = 64, with P kept: 94 us, 5.1 TB/s.
 //
 // 2. The chain.  A CTA walks one head's chunks of 64 rows for 32 value columns
 //    (columns never meet), two warpgroups of 16 columns each; lane d holds row
@@ -21,7 +24,9 @@
 //    took 4.6k cycles a chunk at D = 64).  Past 32 KB of instructions every one
 //    of them takes 3.1 cycles to fetch (measured): the two launches' work in
 //    one kernel, with a chunk's matrices made two ahead by warps beside the
-//    chain, took 7.4k cycles a chunk.
+//    chain, took 7.4k cycles a chunk.  B = 8, H = 16, N = 4096, D = M = 64, two
+//    CTAs to an SM: 161 us with what a backward needs kept, 5.4 TB/s.  B = 4, H =
+//    8, N = 8229, D = 128, M = 64, 64 CTAs: 223 us, 3.3k cycles a chunk.
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"
