@@ -391,7 +391,7 @@ CP_API cp_status_t causal_product_bwd_favor(const void* xq, const void* xk, cons
  * outputs overlap nothing.  N = 0 passes the state through.
  *
  * g_t = -inf clears the state before token t (any g_t below -120 does, e^-120
- * being 0 in fp32); beta_t = 0 writes nothing, so a token with g = beta = 0 is
+ * being 0 in fp32; a NaN or inf in it stays, 0 times it being NaN); beta_t = 0 writes nothing, so a token with g = beta = 0 is
  * padding.  A NaN or inf among a head's inputs reaches that head's later
  * outputs, and may reach those of the same 64 rows.  Keys longer than 1
  * (beta |k|^2 > 2) can make the state grow without bound;
