@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
 
   const bool row_on = t < a.D;
   float2 dS[8];
+  grid_dep_wait();
 
   if (warp == 8) {  // the copies and the gates, a step ahead
     if (lane == 0) {
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
   if (*abort_flag) linger();
   tc_fence_before();
   __syncthreads();
+  grid_dep_launch_dependents();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       bulk_load(sm + L::oD + h * L::kS, a.ds + tile * L::kS, L::kS, full);
     }
   };
+  grid_dep_wait();
   if (issuer) {
     for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
     *abort_flag = 0;
@@ -786,6 +789,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   if (*abort_flag) linger();
   tc_fence_before();
   __syncthreads();
+  grid_dep_launch_dependents();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
@@ -828,10 +832,11 @@ cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const ChainArgs& c, c
   if (!make_chunk_map(&q, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&kk, f.k, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
   const unsigned BH = (unsigned)(s.B * s.H);
-  chain<<<dim3(BH, (unsigned)((s.M + kCB - 1) / kCB)), kChainThreads, LC::kBytes, stream>>>(q, kk, c);
-  if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
-  grad<<<BH * (unsigned)c.n_chunks, 256, LG::kBytes, stream>>>(q, kk, g);
-  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  const dim3 grid(BH, (unsigned)((s.M + kCB - 1) / kCB));
+  if (launch_dependent(chain, grid, kChainThreads, LC::kBytes, stream, q, kk, c) != cudaSuccess ||
+      launch_dependent(grad, dim3(BH * (unsigned)c.n_chunks), 256, LG::kBytes, stream, q, kk, g) != cudaSuccess)
+    return CP_ERR_CUDA;
+  return CP_OK;
 }
 
 }  // namespace

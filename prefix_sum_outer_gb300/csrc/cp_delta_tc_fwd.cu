@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
   const int64_t p = blockIdx.x / a.n_chunks;
   const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
+  grid_dep_wait();
   float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
   if (w == 3) {
     const int64_t i = i0 + lane, at = p * a.N;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     if (*abort_flag) linger();
   }
   __syncthreads();
+  grid_dep_launch_dependents();
   if (w == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 64);
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   };
   const bool row_on = t < a.D;
   float2 S[8];
+  grid_dep_wait();
 
   if (warp == 8) {  // the copies and the gates, a chunk ahead
     if (lane == 0) {
@@ -428,6 +431,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   if (*abort_flag) linger();
   tc_fence_before();
   __syncthreads();
+  grid_dep_launch_dependents();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
@@ -476,11 +480,12 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
   CUtensorMap mq, mk;
   if (!make_chunk_map(&mq, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&mk, f.k, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
-  prep<<<(unsigned)(BH * k.n), 128, LP::kBytes, stream>>>(mq, mk, a);
-  if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;
+  if (launch_dependent(prep, dim3((unsigned)(BH * k.n)), 128, LP::kBytes, stream, mq, mk, a) != cudaSuccess)
+    return CP_ERR_CUDA;
   const dim3 grid((unsigned)BH, (unsigned)((s.M + kCB - 1) / kCB));
-  chain<<<grid, kChainThreads, L::kBytes, stream>>>(mq, mk, c);
-  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  return launch_dependent(chain, grid, kChainThreads, L::kBytes, stream, mq, mk, c) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
 }
 
 }  // namespace
