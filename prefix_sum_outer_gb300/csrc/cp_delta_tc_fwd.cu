@@ -42,7 +42,8 @@ struct PrepArgs {
   uint8_t *t, *pt, *p;  // [BH][chunks] x 16 KB each (hi, lo); p may be null
   int* status;
   int64_t N;
-  int n_chunks, H, group;
+  int n_chunks, chunk0, span, H, group;  // of n_chunks: span chunks from chunk0 on
+  bool beside;                           // beside the chain over the piece before
   float scale;
 };
 
@@ -83,10 +84,10 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
   const int lane = threadIdx.x % 32, t = threadIdx.x;
-  const int64_t p = blockIdx.x / a.n_chunks;
-  const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
+  const int64_t p = blockIdx.x / a.span;
+  const int chunk = a.chunk0 + blockIdx.x % a.span, i0 = chunk * kCh;
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
-  grid_dep_wait();
+  if (!a.beside) grid_dep_wait();
   float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
   if (w == 3) {
     const int64_t i = i0 + lane, at = p * a.N;
@@ -192,6 +193,8 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     tc_fence_after();
     tmem_dealloc(tmem, 64);
   }
+  // this grid ends after the chain beside it, so that the next one follows both
+  if (a.beside && blockIdx.x == 0) grid_dep_wait();
 }
 
 // ------------------------------------------------------------------- chain
@@ -204,7 +207,8 @@ struct FwdArgs {
   float* state_out;
   int* status;
   int64_t N;
-  int n_chunks, H, group, D, M;
+  int n_chunks, chunk0, span, H, group, D, M;
+  bool lead;  // the next piece's matrices run beside this chain
   float scale;
 };
 
@@ -244,7 +248,8 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   const int lane = threadIdx.x % 32, sub = warp / 4, t = threadIdx.x % 128;
   const int64_t p = blockIdx.x;  // b * H + h
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
-  const int n = a.n_chunks, c0 = blockIdx.y * kCB + 16 * sub, nc = a.M - c0;  // 16 columns
+  const int n = a.span, c0 = blockIdx.y * kCB + 16 * sub, nc = a.M - c0;  // 16 columns
+  const int64_t tile0 = p * a.n_chunks + a.chunk0, row0 = (int64_t)a.chunk0 * kCh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(kq_full + i, 1);
@@ -271,12 +276,12 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     uint8_t* dst = sm + (c & 1) * L::kKQ;
     mbar_arrive_expect_tx(bar, L::kKQ);
     for (int x = 0; x < L::kBoxes; ++x) {
-      tma_load_3d(dst + x * L::kKQBox, &tm_k, bar, 64 * x, c * kCh, pk, once);
-      tma_load_3d(dst + x * L::kKQBox + kBox, &tm_q, bar, 64 * x, c * kCh, pk, once);
+      tma_load_3d(dst + x * L::kKQBox, &tm_k, bar, 64 * x, (int)row0 + c * kCh, pk, once);
+      tma_load_3d(dst + x * L::kKQBox + kBox, &tm_q, bar, 64 * x, (int)row0 + c * kCh, pk, once);
     }
   };
   auto load_t = [&](int c) {
-    const int64_t tile = (p * n + c) * (2 * kBox);
+    const int64_t tile = (tile0 + c) * (2 * kBox);
     mbar_arrive_expect_tx(t_full, 4 * kBox);
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   // one warp: the gates, loaded a chunk before they are written
   float4 gb;
   auto load_gates = [&](int c) {
-    const int64_t i = (int64_t)c * kCh + lane;
+    const int64_t i = row0 + (int64_t)c * kCh + lane;
     const float* g = a.g + p * a.N;
     const float* b = a.beta + p * a.N;
     gb = make_float4(i < a.N ? g[i] : 0.f, i + 32 < a.N ? g[i + 32] : 0.f, i < a.N ? b[i] : 0.f,
@@ -301,12 +306,13 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   const int64_t at = p * a.N * a.M + c0;
   uint4 vv[2];
   auto load_v = [&](int c) {
-    const int64_t row = (int64_t)c * kCh + t;
+    const int64_t row = row0 + (int64_t)c * kCh + t;
     read16(a.v + at + row * a.M, nc, t < 64 && row < a.N, vv);
   };
   const bool row_on = t < a.D;
   float2 S[8];
   grid_dep_wait();
+  if (a.lead) grid_dep_launch_dependents();
 
   if (warp == 8) {  // the copies and the gates, a chunk ahead
     if (lane == 0) {
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
       mma_tile<DP / 16, false, true>(el, t_kqs, kq, S_addr, id_nt, 16, 16, L::kKQBox, 0, true);
       if (el) mma_commit(done);
     }
-    const int64_t kept = (p * n + c) * gridDim.y + blockIdx.y;
+    const int64_t kept = (tile0 + c) * gridDim.y + blockIdx.y;
     if (KEEP && threadIdx.x == 128) {
       bulk_store(a.keep_s + kept * (DP * 128), S_tile, DP * 128);
       tma_store_commit();
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
     {
-      const int64_t row = (int64_t)c * kCh + (t & 63);
+      const int64_t row = row0 + (int64_t)c * kCh + (t & 63);
       float2 r[8];
       load16_sum(t_tr + lane_col, r);
       if (t < 64) {
@@ -438,9 +444,20 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   }
 }
 
-// Device scratch of a forward: P T, and T when it is not kept.
+// Device scratch of a forward: P T, T when it is not kept, and the state
+// between pieces.
 size_t tiles_bytes(const DeltaShape& s) {
   return (size_t)(s.B * s.H * ((s.N + kCh - 1) / kCh)) * 2 * kBox;
+}
+
+// Pieces of the sequence: where the chain leaves half of the SMs idle, a
+// piece's matrices are made under the chain over the piece before, at a few
+// microseconds a piece (B = 4, H = 8, N = 8229, D = 128, M = 64: 254 us in four
+// pieces, 274 whole; B = 2, H = 8, N = 32768, D = M = 128: 896 in six, 969).
+int n_pieces(const DeltaShape& s) {
+  const int64_t ctas = s.B * s.H * ((s.M + kCB - 1) / kCB), n = (s.N + kCh - 1) / kCh;
+  if (ctas > kPlanSMs / 2) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(n / 32, 6));
 }
 
 template <int DP, bool KEEP>
@@ -464,6 +481,8 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
   a.p = KEEP ? a.t + k.t_bytes : nullptr;
   a.status = status;
   a.N = s.N; a.n_chunks = (int)k.n; a.H = (int)s.H; a.group = (int)(s.H / s.Hk); a.scale = s.scale;
+  const int pieces = n_pieces(s);
+  float* between = reinterpret_cast<float*>(area + 2 * tiles_bytes(s));
   FwdArgs c{};
   c.v = static_cast<const __nv_bfloat16*>(f.v);
   c.out = static_cast<__nv_bfloat16*>(f.out);
@@ -471,8 +490,7 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
     c.keep_s = kept;
     c.keep_u = kept + k.s_bytes;
   }
-  c.g = f.g; c.beta = f.beta; c.state_in = f.state_in; c.t = a.t; c.pt = a.pt;
-  c.state_out = f.state_out; c.status = status;
+  c.g = f.g; c.beta = f.beta; c.t = a.t; c.pt = a.pt; c.status = status;
   c.N = s.N; c.n_chunks = (int)k.n; c.H = a.H; c.group = a.group;
   c.D = (int)s.D; c.M = (int)s.M; c.scale = s.scale;
   // (encoding a map needs the device's context current in this thread: the
@@ -480,12 +498,23 @@ cp_status_t launch(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* s
   CUtensorMap mq, mk;
   if (!make_chunk_map(&mq, f.q, s.B * s.Hk, s.N, s.D) || !make_chunk_map(&mk, f.k, s.B * s.Hk, s.N, s.D))
     return CP_ERR_CUDA;
-  if (launch_dependent(prep, dim3((unsigned)(BH * k.n)), 128, LP::kBytes, stream, mq, mk, a) != cudaSuccess)
-    return CP_ERR_CUDA;
   const dim3 grid((unsigned)BH, (unsigned)((s.M + kCB - 1) / kCB));
-  return launch_dependent(chain, grid, kChainThreads, L::kBytes, stream, mq, mk, c) == cudaSuccess
-             ? CP_OK
-             : CP_ERR_CUDA;
+  for (int i = 0; i < pieces; ++i) {
+    const bool last = i + 1 == pieces;
+    // the first piece, under whose matrices nothing runs, is half as long
+    const auto start = [&](int x) { return (int)(k.n * std::max(2 * x - 1, 0) / (2 * pieces - 1)); };
+    a.chunk0 = c.chunk0 = start(i);
+    a.span = c.span = start(i + 1) - a.chunk0;
+    a.beside = i > 0;
+    c.lead = !last;
+    // (a chain's CTA reads only what it wrote itself)
+    c.state_in = i > 0 ? between : f.state_in;
+    c.state_out = last ? f.state_out : between;
+    if (launch_dependent(prep, dim3((unsigned)(BH * a.span)), 128, LP::kBytes, stream, mq, mk, a) != cudaSuccess ||
+        launch_dependent(chain, grid, kChainThreads, L::kBytes, stream, mq, mk, c) != cudaSuccess)
+      return CP_ERR_CUDA;
+  }
+  return CP_OK;
 }
 
 }  // namespace
@@ -497,7 +526,9 @@ bool delta_tc_supported(const DeltaShape& s) {
 
 size_t delta_tc_ckpt_bytes(const DeltaShape& s) { return (size_t)Saved(s).bytes(); }
 
-size_t delta_tc_fwd_scratch(const DeltaShape& s) { return 2 * tiles_bytes(s); }
+size_t delta_tc_fwd_scratch(const DeltaShape& s) {
+  return 2 * tiles_bytes(s) + (n_pieces(s) > 1 ? sizeof(float) * (size_t)(s.B * s.H * s.D * s.M) : 0);
+}
 
 cp_status_t delta_tc_fwd(const DeltaShape& s, const DeltaFwd& f, void* scratch, int* status,
                          cudaStream_t stream) {
