@@ -1,5 +1,5 @@
 // Forward of the gated delta rule on the tensor cores (bf16, D <= 128), two
-// launches:
+// launches for the sequence or for each of a few pieces of it:
 //
 // 1. What a chunk needs of its own keys, queries and gates, one CTA per value
 //    head and chunk: [K; Q] K^T by MMA, A and P from it by the decays, T = (I +
@@ -26,7 +26,8 @@
 //    one kernel, with a chunk's matrices made two ahead by warps beside the
 //    chain, took 7.4k cycles a chunk.  B = 8, H = 16, N = 4096, D = M = 64, two
 //    CTAs to an SM: 161 us with what a backward needs kept, 5.4 TB/s.  B = 4, H =
-//    8, N = 8229, D = 128, M = 64, 64 CTAs: 223 us, 3.3k cycles a chunk.
+//    8, N = 8229, D = 128, M = 64, 64 CTAs: 223 us, 3.3k cycles a chunk, in one
+//    piece.
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"
