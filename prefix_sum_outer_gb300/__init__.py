@@ -799,6 +799,10 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     [B,H,D,M], None = zero).  Returns out, followed by S_N with
     ``return_state`` and by the checkpoints causal_product_bwd_delta needs with
     ``save`` (written into ``ckpt`` when given)."""
+    if stream is not None:  # what is allocated below belongs to it
+        with torch.cuda.stream(stream):
+            return causal_product_fwd_delta(q, k, v, g, beta, out, workspace, None, state_in,
+                                            return_state, state_out, scale, save, ckpt)
     B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
     code = _dtype_code(q, k, v)
     dev = v.get_device()
@@ -854,6 +858,11 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     for causal_product_fwd_delta(..., save=True) on the same inputs, ``ckpt``
     being the checkpoints it returned; with ``return_state_grad`` dL/dS_0
     follows.  dq and dk are summed over the value heads of a key head."""
+    if stream is not None:  # what is allocated below belongs to it
+        with torch.cuda.stream(stream):
+            return causal_product_bwd_delta(q, k, v, g, beta, grad_out, ckpt, grad_q, grad_k, grad_v,
+                                            grad_g, grad_beta, workspace, None, scale,
+                                            grad_state_out, return_state_grad, grad_state_in)
     B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
     code = _dtype_code(q, k, v, grad_out)
     if grad_out.shape != v.shape:
@@ -900,6 +909,9 @@ def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     state; one outside [0, P) is an idle row (out zero, no state touched).
     Without ``slots`` sequence b has state b.  No two sequences may share a
     slot."""
+    if stream is not None and out is None:
+        with torch.cuda.stream(stream):
+            return causal_product_decode_delta(q, k, v, g, beta, state, None, None, scale, slots)
     qs, vs = q.shape, v.shape
     if (len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or qs[1] == 0
             or vs[1] % qs[1] != 0):
@@ -1012,6 +1024,9 @@ def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torc
     sin (float32 [N,R/2] or [B,N,R/2]; None = no rotation).  xq and xk may be
     strided views (rows dense): a projection's ``x.view(B,N,H,D).transpose(1,
     2)`` is read in place.  q and k come dense."""
+    if stream is not None:  # what is allocated below belongs to it
+        with torch.cuda.stream(stream):
+            return causal_product_qk_rope(xq, xk, wq, wk, cos, sin, norm, eps, q, k)
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
     if q is None:
         q = torch.empty_like(xq, memory_format=torch.contiguous_format)
@@ -1037,6 +1052,10 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     """(dxq, dxk, dwq, dwk) of L = <grad_q, q> + <grad_k, k> for
     causal_product_qk_rope; dxq and dxk dense, dwq and dwk None where the
     weight is."""
+    if stream is not None:  # what is allocated below belongs to it
+        with torch.cuda.stream(stream):
+            return causal_product_qk_rope_bwd(xq, xk, wq, wk, grad_q, grad_k, cos, sin, norm, eps,
+                                              workspace)
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
     a.dense(grad_q, a.q_shape, xq.dtype, "grad_q")
     a.dense(grad_k, a.k_shape, xq.dtype, "grad_k")
