@@ -157,22 +157,38 @@ __device__ __forceinline__ void load_angles_any(float2 (&c)[4], float2 (&s)[4], 
   }
 }
 // .. and the turn of a row spread over `lanes` lanes (lane l: features 8 l ..):
-// a feature f < R has its partner R / 2 away and asks for that one's lane.
+// a feature f < R has its partner half = R / 2 away, in the lane half / 8 away or
+// the next, at an offset that is the same for every lane: with the registers
+// turned by half % 8 (three rounds of selects), each feature takes one shuffle
+// from above and one from below.
 __device__ __forceinline__ void rotate8_any(float2 (&y)[4], const float2 (&c)[4],
                                             const float2 (&s)[4], int R, int l, int lanes) {
-  const int half = R / 2, f0 = 8 * l;
+  const int half = R / 2, f0 = 8 * l, o = half % 8;
   if (half == 0) return;
-  float* yf = reinterpret_cast<float*>(y);
+  const float* yf = reinterpret_cast<const float*>(y);
+  float up[8], down[8];  // elements (i + o) % 8 and (i - o) % 8
+#pragma unroll
+  for (int i = 0; i < 8; ++i) up[i] = down[i] = yf[i];
+#pragma unroll
+  for (int n = 4; n > 0; n /= 2) {
+    float u[8], d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = o & n ? up[(i + n) % 8] : up[i];
+      d[i] = o & n ? down[(i + 8 - n) % 8] : down[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      up[i] = u[i];
+      down[i] = d[i];
+    }
+  }
   float z[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int f = f0 + i, want = f < half ? f + half : (f < R ? f - half : f);
-    z[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = __shfl_sync(0xffffffffu, yf[j], want / 8, lanes);
-      if (want % 8 == j) z[i] = t;
-    }
+    const float a = __shfl_sync(0xffffffffu, up[i], l + half / 8 + (i + o >= 8), lanes);
+    const float b = __shfl_sync(0xffffffffu, down[i], l - half / 8 - (i < o), lanes);
+    z[i] = f0 + i < half ? a : (f0 + i < R ? b : 0.f);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = fma2(make_float2(z[2 * i], z[2 * i + 1]), s[i], mul2(y[i], c[i]));
