@@ -15,9 +15,10 @@
 // stays within a lane and a sum over the row takes few shuffles; as many rows
 // to a warp as fit, two turns of them at once (backward: one), and the next
 // ones loaded before these are worked on.  Where R or D is not a multiple of 16
-// a lane has eight features and asks for their partners by shuffle (so it took
-// 78 + 125 us for what follows).  Everything between the load and the store is
-// fp32 and rounded once.  bf16, B = 8, H = 16, N = 4096, D = R = 64, with weights:
+// a lane has eight features, asks for their partners by shuffle and takes twice
+// the turns (what follows at N = 2048: 33 + 55 us by pairs, with R = 40 80 + 123
+// us by shuffles).  Everything between the load and the store is fp32 and
+// rounded once.  bf16, B = 8, H = 16, N = 4096, D = R = 64, with weights:
 // forward 59 us, 4.6 TB/s, backward 96 us, 4.2 TB/s; registers hold the loads in
 // flight, two CTAs to an SM.
 #include <algorithm>
@@ -205,8 +206,8 @@ struct Place {
 template <typename T, bool BWD, bool FAST>
 __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
   extern __shared__ float sm[];  // BWD: [kWarps][D] partial weight gradients
-  constexpr int U = FAST && !BWD ? 2 : 1;  // turns in flight
-  constexpr int P = FAST ? 2 : 1;          // a lane's pieces of eight features
+  constexpr int P = FAST ? 2 : 1;         // a lane's pieces of eight features
+  constexpr int U = (BWD ? 2 : 4) / P;    // turns in flight
   const Side& s = a.side[blockIdx.y];
   const int lanes = a.lanes, per_warp = 32 / lanes;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, l = lane % lanes;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
       dw[e][i] = both(0.f);
     }
   // a warp takes U x per_warp consecutive rows, then jumps by `step`
-  const uint32_t step = gridDim.x * kWarps * per_warp * U;  // (at most 152 x 8 x 32 x 2)
+  const uint32_t step = gridDim.x * kWarps * per_warp * U;  // (at most 152 x 8 x 32 x 4)
   const uint32_t H = (uint32_t)s.H, N = (uint32_t)a.N;
   const bool per_batch = a.cs_batch != 0;
   const uint32_t step_tok = step / H, step_h = step % H;
