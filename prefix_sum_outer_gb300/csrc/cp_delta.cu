@@ -183,7 +183,7 @@ struct Cols {
 struct alignas(16) Gates {
   float2 G[kC];   // running sums of the log decay
   float b[kC], gam[kC], del[kC];
-  float last;     // gam of the last row
+  float2 last;    // gam of the last row, hi + lo
 };
 
 // by one warp
@@ -198,7 +198,7 @@ __device__ __forceinline__ void load_gates(Gates& s, const float* g, const float
   s.b[i] = on ? beta[i0 + i] : 0.f;
   s.gam[i] = decay_between(G, zero);
   s.del[i] = decay_between(E, G);
-  if (i == 0) s.last = decay_between(E, zero);
+  if (i == 0) s.last = decay_parts(E);
 }
 
 // (I + A) u = x in place for a warp's columns of x [MB][kLdc], at[j][i] = A_ij;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) delta_fwd_kernel(Args p) {
 #pragma unroll
       for (int c = 0; c < MB / kWarps; ++c) {
         float* s = S + (w + kWarps * c) * ldd + d;
-        *s = fmaf(gt.last, *s, acc[c]);
+        *s = fmaf(gt.last.x, *s, fmaf(gt.last.y, *s, acc[c]));
       }
     }
   }
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads) delta_bwd_kernel(Args p) {
       float zs = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) zs += red[i];
-      zs *= gt.last;
+      zs *= gt.last.x;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int t = w + kWarps * u;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads) delta_bwd_kernel(Args p) {
 #pragma unroll
       for (int c = 0; c < MB / kWarps; ++c) {
         float* s = dS + (w + kWarps * c) * ldd + d;
-        *s = fmaf(gt.last, *s, acc[c]);
+        *s = fmaf(gt.last.x, *s, fmaf(gt.last.y, *s, acc[c]));
       }
     }
   }

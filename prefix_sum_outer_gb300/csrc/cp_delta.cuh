@@ -70,21 +70,51 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// A log decay as two parts whose running sums over a chunk stay exact to
-// fp32: a multiple of 1/16 (sums of up to 256 of them at |g| <= 120 are exact)
-// and the rest (|f| <= 1/32).  With one fp32 sum, a decay near e^-100 (a
-// cleared state) would leave every later difference G_i - G_j of its chunk
-// 1e-5 off.  Below -120 the decay is 0 in fp32, and -inf becomes finite, so
-// that differences of sums are never inf - inf.  NaN stays NaN.
+// A log decay, in powers of two, as two parts whose running sums over a chunk
+// stay exact to fp32: a multiple of 2^-10 (sums of up to 64 of them at |g| <= 120
+// are exact) and the rest (|f| <= 2^-11, with what rounding g log2(e) left over).
+// With one fp32 sum, a decay near e^-100 (a cleared state) would leave every
+// later difference G_i - G_j of its chunk 1e-5 off.  Below -120 the decay is 0
+// in fp32, and -inf becomes finite, so that differences of sums are never inf -
+// inf.  NaN stays NaN.
 constexpr float kMinLogDecay = -120.f;
 __device__ __forceinline__ float2 split_decay(float g) {
+  constexpr double kLog2e = 1.4426950408889634;
+  constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
   g = g < kMinLogDecay ? kMinLogDecay : g;
-  const float c = rintf(g * 16.f) * 0.0625f;
-  return make_float2(c, g - c);
+  const float l = g * kHi, c = rintf(l * 1024.f) * 0x1p-10f;
+  return make_float2(c, (l - c) + fmaf(g, kLo, fmaf(g, kHi, -l)));
 }
 // e^{G_i - G_j} from the two-part running sums
 __device__ __forceinline__ float decay_between(float2 gi, float2 gj) {
-  return expf((gi.x - gj.x) + (gi.y - gj.y));
+  return exp2f((gi.x - gj.x) + (gi.y - gj.y));
+}
+// The decay of a state over a step, e^{g + f} with f below g's rounding, as hi +
+// lo.  One fp32 number is up to 2^-25 off, the same way at every step where the
+// decay is the same, and a state that remembers n steps would be n times as far
+// off (4e-4 after 8,000 tokens at g = -1e-4, one by one).  lo is what rounding
+// e^g left over: e^g - 1 is g (exact) and the rest of the series, which for |g| <
+// 0.34 is below 0.07 and so good to 4e-9 in fp32; g - (hi - 1) has no rounding.
+// Past that the state forgets within a few steps, and lo is 0.
+__device__ __forceinline__ float2 decay_parts(float g, float f) {
+  const float hi = expf(g);
+  if (!(fabsf(g) < 0.34f)) return make_float2(hi, 0.f);
+  float q = 1.f / 40320.f;
+  q = fmaf(q, g, 1.f / 5040.f);
+  q = fmaf(q, g, 1.f / 720.f);
+  q = fmaf(q, g, 1.f / 120.f);
+  q = fmaf(q, g, 1.f / 24.f);
+  q = fmaf(q, g, 1.f / 6.f);
+  q = fmaf(q, g, 0.5f);
+  const float left = (g - (hi - 1.f)) + q * (g * g);
+  return make_float2(hi, fmaf(hi, f, left));
+}
+__device__ __forceinline__ float2 decay_parts(float2 G) {  // from a two-part sum
+  constexpr double kLn2 = 0.6931471805599453;
+  constexpr float kHi = (float)kLn2, kLo = (float)(kLn2 - (double)kHi);
+  const float x = G.x * kHi, y = fmaf(G.y, kHi, fmaf(G.x, kLo, fmaf(G.x, kHi, -x)));
+  const float g = x + y, z = g - x;  // x + y = g + f exactly
+  return decay_parts(g, (x - (g - z)) + (y - z));
 }
 // inclusive running sums of one pair per lane over a warp
 __device__ __forceinline__ float2 warp_scan(float2 x, int lane) {

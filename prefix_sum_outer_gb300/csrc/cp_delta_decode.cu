@@ -3,7 +3,8 @@
 // The update needs S^T k before it, and the readout of the updated state is
 //     S'^T q = a S^T q + (k . q) u,
 // so both sums over the rows of S run while S is in registers and the state is
-// read and written once: 8 D M bytes per head, which bound the step.  A CTA
+// read and written once: 8 D M bytes per head, which bound the step.  The state's
+// decay is applied as hi + lo, for it is applied token after token (cp_delta.cuh).  A CTA
 // takes 32 value columns of one head, as 8 groups of four or, where rows are
 // not whole 16-byte pieces, one by one; its threads hold every row of them,
 // ROWS each.
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 4 ? 10 : 1)
   float vv[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) vv[i] = on ? ld_f32<T>(v + p * M + c + i) : 0.f;
-  const float a = expf(g[p]), bt = beta[p];
+  const float2 decay = decay_parts(g[p], 0.f);
+  const float a = decay.x, bt = beta[p];
   float sk[V] = {}, sq[V] = {}, kq = 0.f, kd[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 4 ? 10 : 1)
     const int d = rg + r * RG;
     if (d < D) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) st[r][i] = fmaf(kd[r], u[i], a * st[r][i]);
+      for (int i = 0; i < V; ++i) st[r][i] = fmaf(a, st[r][i], fmaf(kd[r], u[i], decay.y * st[r][i]));
       st_state<STREAM, V>(S + (int64_t)d * M + c, st[r]);
     }
   }

@@ -32,56 +32,72 @@ __device__ __forceinline__ uint8_t* align_tiles(uint8_t* smem) {
   return smem + (-smem_u32(smem) & 1023u);
 }
 
-// The gates of a chunk.  Every decay between two rows is a product of the a =
-// e^g between them, never a difference of sums: a cleared state's zero stays
-// an exact zero, 64 factors cost 64 roundings (4e-6 at worst), and a product
-// takes one instruction where an exponential of a difference takes eight.
-// Pieces are 16 rows.
-struct GateSlot {
-  float a[kCh + 4];                   // e^g (past the end: read, not used)
+// The gates of a chunk.  Every decay between two rows is the exponential of a
+// difference of running sums (in two parts, cp_delta.cuh), of which the sums'
+// rounding leaves 1e-7; a product of up to 64 factors e^g would leave each one's
+// rounding, the same way at every row where the decay is constant.  A cleared
+// state's decay stays an exact zero.
+struct alignas(16) GateSlot {
+  float2 G[kCh];                      // running sums of the log decay
   float b[kCh];
-  float gam[kCh], del[kCh];           // products of a up to row i, after row j
-  float e[kCh];                       // product of a after row j, in its piece
-  float half[32];                     // product of a from row 32 to row 32 + i
-  float piece[4];                     // product of a over a piece
+  float gam[kCh], del[kCh];           // decay up to row i, after row j
+  float tail[32], half[32];           // decay after row j up to row 31, from row 32 to row 32 + i
+  float2 last;                        // decay over the chunk, hi + lo
 };
+
+// 2^x for x <= 0, to 2^-22; 0 below 2^-126
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // One warp: the slot from the lane's two rows' (lane, lane + 32) log decays and
 // strengths.
 __device__ __forceinline__ void write_gates(GateSlot* s, int lane, float g0, float g1, float b0,
                                             float b1) {
-  const unsigned all = 0xffffffffu;
-  const bool up = lane >= 16;
-  float before = 1.f, suf0 = 0.f;  // of the first half: its product, and that after the row
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    // (2^-22 of a, and 2^-24 of g: as 64 roundings)
-    const float a = __expf(h ? g1 : g0);
-    float x = a, y = a;
+  const float2 zero = make_float2(0.f, 0.f);
+  const auto total = [](float2 x) {
+    return make_float2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+  };
+  const float2 G0 = warp_scan(split_decay(g0), lane), mid = total(G0);
+  const float2 H1 = warp_scan(split_decay(g1), lane), G1 = add2(mid, H1), end = total(G1);
+  s->G[lane] = G0;
+  s->G[lane + 32] = G1;
+  s->b[lane] = b0;
+  s->b[lane + 32] = b1;
+  s->gam[lane] = decay_between(G0, zero);
+  s->gam[lane + 32] = decay_between(G1, zero);
+  s->del[lane] = decay_between(end, G0);
+  s->del[lane + 32] = decay_between(end, G1);
+  s->tail[lane] = decay_between(mid, G0);
+  s->half[lane] = decay_between(H1, zero);
+  if (lane == 0) s->last = decay_parts(end);
+}
+
+// w times the decay from row j to row i of the chunk for the 16 columns j = 16
+// c .. of row i (own: with those of the row's half, row32), 0 past column last.
+__device__ __forceinline__ void decays16(const GateSlot* gs, int i, int row32, int c, int last,
+                                         float w, float2 (&v)[8]) {
+  if (c >= 2 * row32 + 2) {
 #pragma unroll
-    for (int o = 1; o < 16; o *= 2) {
-      const float u = __shfl_up_sync(all, x, o, 16), d = __shfl_down_sync(all, y, o, 16);
-      if (lane % 16 >= o) x *= u;
-      if (lane % 16 + o < 16) y *= d;
+    for (int x = 0; x < 8; ++x) v[x] = both(0.f);
+  } else if (c >= 2 * row32) {
+    const float2 Gi = gs->G[i];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 g = *reinterpret_cast<const float4*>(gs->G + 16 * c + 2 * x);
+      const float2 d0 = sub2(Gi, make_float2(g.x, g.y)), d1 = sub2(Gi, make_float2(g.z, g.w));
+      v[x].x = 16 * c + 2 * x <= last ? w * exp2_fast(d0.x + d0.y) : 0.f;
+      v[x].y = 16 * c + 2 * x + 1 <= last ? w * exp2_fast(d1.x + d1.y) : 0.f;
     }
-    const float d = __shfl_down_sync(all, y, 1, 16);
-    const float suf = lane % 16 == 15 ? 1.f : d;
-    const float lo = __shfl_sync(all, x, 15), hi = __shfl_sync(all, x, 31);
-    const float half = up ? lo * x : x;
-    s->a[lane + 32 * h] = a;
-    s->b[lane + 32 * h] = h ? b1 : b0;
-    s->gam[lane + 32 * h] = before * half;
-    s->e[lane + 32 * h] = suf;
-    const float after = up ? suf : suf * hi;  // product after the row, in its half
-    if (lane == 0) s->piece[2 * h] = lo;
-    if (lane == 1) s->piece[2 * h + 1] = hi;
-    if (h == 0) {
-      before = lo * hi;
-      suf0 = after;
-    } else {
-      s->half[lane] = half;
-      s->del[lane] = suf0 * (lo * hi);
-      s->del[lane + 32] = after;
+  } else {
+    const float2 p = both(w * gs->half[i - 32]);
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {
+      const float4 t = *reinterpret_cast<const float4*>(gs->tail + 16 * c + 2 * x);
+      v[x] = mul2(p, make_float2(t.x, t.y));
+      v[x + 1] = mul2(p, make_float2(t.z, t.w));
     }
   }
 }
@@ -480,58 +496,27 @@ __device__ __forceinline__ void put_t_transposed(uint8_t* hi, int part, int a, i
 }
 
 // Row i of the chunk's k.k or q.k (lane of the accumulator at t_kk), weighted
-// by the decays: w times the product of a after row j up to row i, for j < i
-// (and for j = i, where it is w, with `diag`), 0 elsewhere, last columns first;
-// f(c, v) takes columns 16 c .. 16 c + 15.  row32: the row's half of the chunk,
-// uniform over the warp.  From the row's own half the product runs down the
-// columns; below it, a piece's columns share a row factor.
+// by the decays: w times the decay from row j to row i, for j < i (and for j =
+// i, where it is w, with `diag`), 0 elsewhere; f(c, v) takes columns 16 c .. 16 c
+// + 15.  row32: the row's half of the chunk, uniform over the warp.
 template <class F>
 __device__ __forceinline__ void decayed_row(uint32_t t_kk, const GateSlot* gs, int i, bool diag,
                                             int row32, float w, F f) {
   const int last = diag ? i : i - 1;
-  float p = w;
 #pragma unroll 1
-  for (int c = 3; c >= 0; --c) {
+  for (int c = 0; c < 4; ++c) {
     uint32_t r[16];
     tmem_ld16(t_kk + 16 * c, r);
     float2 v[8];
-    if (c >= 2 * row32 + 2) {
-      tmem_ld_wait();
+    decays16(gs, i, row32, c, last, w, v);
+    tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = both(0.f);
-    } else if (c >= 2 * row32) {
-      float a[17];
-#pragma unroll
-      for (int x = 0; x < 16; x += 4) {
-        const float4 t = *reinterpret_cast<const float4*>(gs->a + 16 * c + x);
-        a[x] = t.x; a[x + 1] = t.y; a[x + 2] = t.z; a[x + 3] = t.w;
-      }
-      a[16] = gs->a[16 * c + 16];
-      float u[16];
-#pragma unroll
-      for (int x = 15; x >= 0; --x) {
-        if (16 * c + x < i) p *= a[x + 1];
-        u[x] = 16 * c + x <= last ? p : 0.f;
-      }
-      // on to the columns of the half below
-      if (c == 2 * row32) p *= a[0];
-      tmem_ld_wait();
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        v[x].x = 16 * c + 2 * x <= last ? u[2 * x] * __uint_as_float(r[2 * x]) : 0.f;
-        v[x].y = 16 * c + 2 * x + 1 <= last ? u[2 * x + 1] * __uint_as_float(r[2 * x + 1]) : 0.f;
-      }
-    } else {
-      tmem_ld_wait();
-#pragma unroll
-      for (int x = 0; x < 8; x += 2) {
-        const float4 t = *reinterpret_cast<const float4*>(gs->e + 16 * c + 2 * x);
-        v[x] = mul2(mul2(both(p), make_float2(t.x, t.y)),
-                    make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
-        v[x + 1] = mul2(mul2(both(p), make_float2(t.z, t.w)),
-                        make_float2(__uint_as_float(r[2 * x + 2]), __uint_as_float(r[2 * x + 3])));
-      }
-      p *= gs->piece[c];
+    for (int x = 0; x < 8; ++x) {
+      // masked places stay 0 whatever the accumulators hold
+      const float2 y =
+          mul2(v[x], make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
+      v[x].x = 16 * c + 2 * x <= last ? y.x : 0.f;
+      v[x].y = 16 * c + 2 * x + 1 <= last ? y.y : 0.f;
     }
     f(c, v);
   }

@@ -304,10 +304,10 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     }
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
-    const float2 last = both(gs->gam[kCh - 1]);
+    const float2 last = both(gs->last.x), last_lo = both(gs->last.y);
     load16_sum(t_up + lane_col, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dS[j] = fma2(last, dS[j], x[j]);
+    for (int j = 0; j < 8; ++j) dS[j] = fma2(last, dS[j], fma2(last_lo, dS[j], x[j]));
   }
   if (a.grad_state_in != nullptr && row_on)
     write16(a.grad_state_in + (p * a.D + t) * a.M + c0, nc, dS);
@@ -365,49 +365,6 @@ struct GradLayout {
   static constexpr int kPerSM = DP == 64 ? 2 : 1;
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
 };
-
-// The 32 columns 32 ch .. of the row's decayed products, as decayed_row gives
-// them; f(c, v, r): v the weights alone (0 where masked), r the accumulator.
-template <class F>
-__device__ __forceinline__ void decayed_half(uint32_t t_acc, const GateSlot* gs, int i, bool diag,
-                                             int row32, int ch, float w, F f) {
-  const int last = diag ? i : i - 1;
-  float p = w;
-  if (ch < row32) p *= gs->half[i - 32];
-#pragma unroll 1
-  for (int c = 2 * ch + 1; c >= 2 * ch; --c) {
-    float2 v[8];
-    if (ch == row32) {
-      float x[17];
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const float4 t = *reinterpret_cast<const float4*>(gs->a + 16 * c + e);
-        x[e] = t.x; x[e + 1] = t.y; x[e + 2] = t.z; x[e + 3] = t.w;
-      }
-      x[16] = gs->a[16 * c + 16];
-      float u[16];
-#pragma unroll
-      for (int e = 15; e >= 0; --e) {
-        if (16 * c + e < i) p *= x[e + 1];
-        u[e] = 16 * c + e <= last ? p : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = make_float2(u[2 * e], u[2 * e + 1]);
-    } else if (ch < row32) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 t = *reinterpret_cast<const float4*>(gs->e + 16 * c + 2 * e);
-        v[e] = mul2(both(p), make_float2(t.x, t.y));
-        v[e + 1] = mul2(both(p), make_float2(t.z, t.w));
-      }
-      p *= gs->piece[c];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = both(0.f);
-    }
-    f(c, v);
-  }
-}
 
 template <int DP>
 __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
@@ -618,17 +575,22 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   uint8_t *M_hi = sm + L::oA, *M_lo = M_hi + 2 * kBox;
   float part[32];    // columns 32 wg ..: the pair's weight in dg, then its running sum
   float db = 0.f, own = 0.f;  // own: dX_i . U_i
-  decayed_half(t_p2, gs, i, !is_k, row32, wg, is_k ? -1.f : a.scale, [&](int c, float2(&v)[8]) {
+  const int last = is_k ? i - 1 : i;
+  const float wm = is_k ? bt : 1.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = 2 * wg + h;
     uint32_t r[16], kk[16];
     tmem_ld16(t_p2 + lane_base + 16 * c, r);
     tmem_ld16(t_kk + lane_base + 16 * c, kk);
+    float2 v[8];
+    decays16(gs, i, row32, c, last, is_k ? -1.f : a.scale, v);
     tmem_ld_wait();
-    const float wm = is_k ? bt : 1.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       // masked places stay 0 whatever the accumulators hold
       float2 m = mul2(v[e], make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
-      const int j = 16 * c + 2 * e, last = is_k ? i - 1 : i;
+      const int j = 16 * c + 2 * e;
       if (j > last) m.x = 0.f;
       if (j + 1 > last) m.y = 0.f;
       float2 x = mul2(m, make_float2(__uint_as_float(kk[2 * e]), __uint_as_float(kk[2 * e + 1])));
@@ -639,16 +601,11 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       if (j + 1 == i) own = __uint_as_float(r[2 * e + 1]);
       v[e] = mul2(both(wm), m);
       x = mul2(both(wm), x);
-      if ((c & 1) == 0) {
-        part[2 * e] = x.x;
-        part[2 * e + 1] = x.y;
-      } else {
-        part[16 + 2 * e] = x.x;
-        part[16 + 2 * e + 1] = x.y;
-      }
+      part[16 * h + 2 * e] = x.x;
+      part[16 * h + 2 * e + 1] = x.y;
     }
     store16_split(M_hi, M_lo, t, 2 * c, v);
-  });
+  }
   tc_fence_before();
   fence_proxy_async_smem();
   __syncthreads();

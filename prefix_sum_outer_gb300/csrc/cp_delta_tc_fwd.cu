@@ -426,10 +426,10 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     }
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
-    const float2 last = both(gs->gam[kCh - 1]);
+    const float2 last = both(gs->last.x), last_lo = both(gs->last.y);
     load16_sum(t_tr + lane_col, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) S[j] = fma2(last, S[j], x[j]);
+    for (int j = 0; j < 8; ++j) S[j] = fma2(last, S[j], fma2(last_lo, S[j], x[j]));
   }
   if (a.state_out != nullptr && row_on) write16(a.state_out + (p * a.D + t) * a.M + c0, nc, S);
   if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
