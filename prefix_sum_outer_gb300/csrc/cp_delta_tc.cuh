@@ -3,12 +3,14 @@
 //
 // Every contraction is a tcgen05.mma with bf16 operands in shared memory and
 // an fp32 accumulator of 128 lanes in tensor memory.  q, k, v and the output's
-// gradient are bf16 as they come; what is computed (S, R, U, P, the inverse) is
-// fp32 and enters a product as hi + lo, two bf16 numbers that keep 16 bits of
-// it, so a product of two such factors is four MMAs and of one with an input
-// two.  One bf16 number per factor would do for bf16 outputs, but leaves 2^-9 in
-// the carried state and in the gradients of the gates, which are fp32; two leave
-// 3e-6 to 6e-6 there, ten times fp32's own.
+// gradient are bf16 as they come; what is computed (S, R, U, P, the inverse and
+// the gradients' factors) is fp32 and enters a product as three bf16 numbers, all
+// of its 24 bits, so a product with an input is three MMAs and one of two such
+// factors six (the terms left out are 2^-27 of it).  With two numbers each (16
+// bits) the carried state and the gates' gradients, which are fp32, were 3e-6 to
+// 7e-6 off; with three they are where fp32 arithmetic leaves them, at 2e-7 to
+// 5e-7.  Terms of one size share an accumulator where there is room, and elsewhere
+// the small ones go first: an MMA rounds its sum toward zero.
 //
 // An operand tile is 64 columns wide (128 bytes, 128-byte swizzle), so it can
 // enter as [rows x K] or transposed, by its descriptor alone.
@@ -102,7 +104,7 @@ __device__ __forceinline__ void decays16(const GateSlot* gs, int i, int row32, i
   }
 }
 
-// x = hi + lo in bf16; each packed as pairs
+// x as two bf16 numbers; each packed as pairs
 __device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = tc::pack_bf16x2(x.x, x.y);
   const float2 d =
@@ -110,15 +112,6 @@ __device__ __forceinline__ void split_pair(float2 x, uint32_t& hi, uint32_t& lo)
   lo = tc::pack_bf16x2(d.x, d.y);
 }
 
-__device__ __forceinline__ void split16(const float2 (&x)[8], uint4 (&hi)[2], uint4 (&lo)[2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    split_pair(x[4 * i], hi[i].x, lo[i].x);
-    split_pair(x[4 * i + 1], hi[i].y, lo[i].y);
-    split_pair(x[4 * i + 2], hi[i].z, lo[i].z);
-    split_pair(x[4 * i + 3], hi[i].w, lo[i].w);
-  }
-}
 // x as three bf16 numbers (all of fp32's bits)
 __device__ __forceinline__ void split_pair3(float2 x, uint32_t& a, uint32_t& b, uint32_t& c) {
   a = tc::pack_bf16x2(x.x, x.y);
@@ -148,13 +141,22 @@ __device__ __forceinline__ void pack16(const float2 (&x)[8], uint4 (&w)[2]) {
                       tc::pack_bf16x2(x[4 * i + 2].x, x[4 * i + 2].y),
                       tc::pack_bf16x2(x[4 * i + 3].x, x[4 * i + 3].y));
 }
-// 16 fp32 values into a tile's hi and lo parts
-__device__ __forceinline__ void store16_split(uint8_t* hi, uint8_t* lo, int row, int ch,
+// 16 fp32 values into a matrix's three parts, `part` bytes apart
+__device__ __forceinline__ void store16_split(uint8_t* tile, int part, int row, int ch,
                                               const float2 (&x)[8]) {
-  uint4 h[2], l[2];
-  split16(x, h, l);
-  put16(hi, row, ch, h);
-  put16(lo, row, ch, l);
+  uint4 a[2], b[2], c[2];
+  split16_3(x, a, b, c);
+  put16(tile, row, ch, a);
+  put16(tile + part, row, ch, b);
+  put16(tile + 2 * part, row, ch, c);
+}
+// .. and into a tile of fp32 rows of 32 columns, as it goes to memory (16-byte
+// pieces of a row in an order of its own, so that rows fall in different banks)
+__device__ __forceinline__ void put_f32(uint8_t* tile, int row, int sub, const float2 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(tile + row * 128 + (((4 * sub + i) ^ (row & 7)) << 4)) =
+        make_float4(x[2 * i].x, x[2 * i].y, x[2 * i + 1].x, x[2 * i + 1].y);
 }
 // the same 16 columns to global memory, of which `nc` are inside the matrix
 __device__ __forceinline__ void write16(__nv_bfloat16* dst, int nc, const uint4 (&v)[2]) {
@@ -231,36 +233,54 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&x)[8]) {
     x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// The chains run 32 value columns to a CTA, 16 to a thread: a factor's hi part
-// is columns 0-31 of its 64-column tile and its lo part columns 32-63, and one
-// MMA of 64 columns takes both.
+// The chains run 32 value columns to a CTA, 16 to a thread: a factor's first part
+// is columns 0-31 of a 64-column tile and its second columns 32-63; the third
+// parts of two factors share another.  One MMA of 96 columns takes all three.
 constexpr int kCB = 32;
 // .. by two warpgroups, and a ninth warp for the copies and the gates: written
 // by one of the eight, they kept the others at a barrier for 340 to 440 cycles
 // of a chunk's 3,600 to 3,900.
 constexpr int kChainThreads = 256 + 32;
 
-// 16 columns of such a product: the two accumulators' sum
+// 16 columns of such a product: the sum of its three accumulators, the small
+// ones first (and in turn, for the registers)
 __device__ __forceinline__ void load16_sum(uint32_t taddr, float2 (&x)[8]) {
   uint32_t h[16], l[16];
-  tmem_ld16(taddr, h);
-  tmem_ld16(taddr + kCB, l);
+  tmem_ld16(taddr + kCB, h);
+  tmem_ld16(taddr + 2 * kCB, l);
   tmem_ld_wait();
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     x[i] = add2(make_float2(__uint_as_float(h[2 * i]), __uint_as_float(h[2 * i + 1])),
                 make_float2(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])));
+  tmem_ld16(taddr, h);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = add2(make_float2(__uint_as_float(h[2 * i]), __uint_as_float(h[2 * i + 1])), x[i]);
 }
-// .. and 16 fp32 values into such a tile, the thread's columns being 16 sub ..
-__device__ __forceinline__ void put_parts(uint8_t* tile, int row, int sub, const uint4 (&hi)[2],
-                                          const uint4 (&lo)[2]) {
-  put16(tile, row, 2 * sub, hi);
-  put16(tile, row, 4 + 2 * sub, lo);
+// .. and 16 fp32 values into such a factor's tiles, the thread's columns being 16
+// sub ..; third: the third parts' tile, the factor's columns beginning at 8 ch
+__device__ __forceinline__ void store_parts(uint8_t* tile, uint8_t* third, int ch, int row, int sub,
+                                            const float2 (&x)[8]) {
+  uint4 a[2], b[2], c[2];
+  split16_3(x, a, b, c);
+  put16(tile, row, 2 * sub, a);
+  put16(tile, row, 4 + 2 * sub, b);
+  put16(third, row, ch + 2 * sub, c);
 }
-__device__ __forceinline__ void store_parts(uint8_t* tile, int row, int sub, const float2 (&x)[8]) {
-  uint4 h[2], l[2];
-  split16(x, h, l);
-  put_parts(tile, row, sub, h, l);
+// T B of two computed factors at acc, whose columns then hold the products' terms
+// by size: A's first part with all three of B's, its second with two, its third
+// with one.  A's parts are a_part bytes apart.
+template <bool KA>
+__device__ __forceinline__ void mma_parts(uint32_t el, uint32_t acc, uint32_t a, uint32_t a_part,
+                                          uint32_t a_lbo, uint32_t b, uint32_t b_third) {
+  mma_tile<4, KA, true>(el, acc, a, b, idesc_bf16_f32(128, 3 * kCB, KA, 1), a_lbo, b_third - b, 0, 0,
+                        true);
+  mma_tile<4, KA, true>(el, acc + kCB, a + a_part, b, idesc_bf16_f32(128, 2 * kCB, KA, 1), a_lbo, 16,
+                        0, 0, false);
+  mma_tile<4, KA, true>(el, acc + 2 * kCB, a + 2 * a_part, b, idesc_bf16_f32(128, kCB, KA, 1), a_lbo,
+                        16, 0, 0, false);
 }
 // 16 columns of a row of inputs, of which nc are inside the matrix
 __device__ __forceinline__ void read16(const __nv_bfloat16* src, int nc, bool on, uint4 (&v)[2]) {
@@ -302,18 +322,17 @@ __device__ __forceinline__ void write16(float* dst, int nc, const float2 (&x)[8]
 // transposed (Z_ab = X_ba^T = -(sum_c Z_ac A_bc^T) X_bb^T) so that a result
 // tile is the next product's left factor without leaving its registers.  These
 // are 16 x 16 products of a few hundred cycles' latency in all: mma.sync, each
-// factor as hi + lo; a tcgen05 product's way through tensor memory costs more
+// factor in three parts; a tcgen05 product's way through tensor memory costs more
 // than the product.  Blockwise substitution keeps the inverse to about the
 // factors' precision whatever A is; the doubling product (I - A)(I + A^2) ..
 // loses everything to cancellation when keys repeat.
-constexpr int kDiagPitch = 16 * 16 + 16;   // floats between diagonal blocks
+constexpr int kDiagPitch = 16 * 24 + 16;   // floats between diagonal blocks
 struct InvTiles {
   // diagonal blocks of A, fp32, transposed: [block][column l][row i]; then,
-  // in its place, the block's inverse, transposed, bf16, hi then lo
+  // in its place, the block's inverse, transposed, three bf16 parts
   float diag[4 * kDiagPitch];
   // blocks below the diagonal, bf16, row major, at index b (b - 1) / 2 + c for
-  // block (b, c), in three parts: two would leave 2^-18 of A, which repeated
-  // keys at full strength multiply by ten in the solution
+  // block (b, c), in three parts
   __nv_bfloat16 low[6][3][16 * 16];
   __device__ __forceinline__ __nv_bfloat16* xt(int b, int part) {
     return reinterpret_cast<__nv_bfloat16*>(diag + b * kDiagPitch) + part * 256;
@@ -358,8 +377,9 @@ __device__ __forceinline__ void put_a16(InvTiles* it, int i, int c, const float2
 }
 
 // Warp b: the inverse of diagonal block b, column l % 16 by lane l, to xt and
-// packed in w (lanes 0-15 the hi part, 16-31 the lo part).
-__device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, uint4 (&w)[2]) {
+// packed in w (lanes 0-15 the first part, 16-31 the second) and w3 (the third).
+__device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, uint4 (&w)[2],
+                                            uint4 (&w3)[2]) {
   const int c = lane & 15;
   float x[16];
   const float* d = it->diag + b * kDiagPitch;
@@ -376,110 +396,118 @@ __device__ __forceinline__ void invert_diag(InvTiles* it, int b, int lane, uint4
       if (i + 3 > l) x[i + 3] = fmaf(-a.w, x[l], x[i + 3]);
     }
   }
-  uint32_t p[8];
+  uint32_t p[8], p3[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t h, l;
-    split_pair(make_float2(x[2 * i], x[2 * i + 1]), h, l);
+    split_pair3(make_float2(x[2 * i], x[2 * i + 1]), h, l, p3[i]);
     p[i] = lane < 16 ? h : l;
   }
   w[0] = make_uint4(p[0], p[1], p[2], p[3]);
   w[1] = make_uint4(p[4], p[5], p[6], p[7]);
+  w3[0] = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+  w3[1] = make_uint4(p3[4], p3[5], p3[6], p3[7]);
   __syncwarp();  // the block has been read by every lane
   uint4* to = reinterpret_cast<uint4*>(it->xt(b, lane >> 4) + c * 16);
   to[0] = w[0];
   to[1] = w[1];
-}
-
-// d[n tile] += (a_hi + a_lo) (b_hi + b_lo), b fragments as {tile 0: k low, k
-// high, tile 1: k low, k high}
-__device__ __forceinline__ void mma_split(float (&d)[2][4], const uint32_t (&a_hi)[4],
-                                          const uint32_t (&a_lo)[4], const uint32_t (&b_hi)[4],
-                                          const uint32_t (&b_lo)[4]) {
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    mma_16816(d[n], a_hi, b_hi[2 * n], b_hi[2 * n + 1]);
-    mma_16816(d[n], a_lo, b_hi[2 * n], b_hi[2 * n + 1]);
-    mma_16816(d[n], a_hi, b_lo[2 * n], b_lo[2 * n + 1]);
-    mma_16816(d[n], a_lo, b_lo[2 * n], b_lo[2 * n + 1]);
+  if (lane < 16) {
+    to = reinterpret_cast<uint4*>(it->xt(b, 2) + c * 16);
+    to[0] = w3[0];
+    to[1] = w3[1];
   }
 }
 
-// Warp a: Z_ab = X_ba^T for b = a + s, packed in zh[s], zl[s]: word 2 n + r is
-// columns (rows of X) 16 b + 8 n + 2 (lane % 4) and the next, row (column of X)
+// big, small [n tile] += a b, both in three parts, small taking all but the first
+// parts' product; b fragments as {tile 0: k low, k high, tile 1: k low, k high}
+__device__ __forceinline__ void mma_split(float (&big)[2][4], float (&small)[2][4],
+                                          const uint32_t (&a)[3][4], const uint32_t (&b)[3][4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    mma_16816(big[n], a[0], b[0][2 * n], b[0][2 * n + 1]);
+#pragma unroll
+    for (int x = 2; x > 0; --x)
+#pragma unroll
+      for (int y = x; y >= 0; --y) mma_16816(small[n], a[y], b[x - y][2 * n], b[x - y][2 * n + 1]);
+  }
+}
+// sign (big + small) as the next product's left factor
+__device__ __forceinline__ void next_factor(uint32_t (&z)[3][4], const float (&big)[2][4],
+                                            const float (&small)[2][4], float sign) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      split_pair3(make_float2(sign * (big[n][2 * r] + small[n][2 * r]),
+                              sign * (big[n][2 * r + 1] + small[n][2 * r + 1])),
+                  z[0][2 * n + r], z[1][2 * n + r], z[2][2 * n + r]);
+}
+
+// Warp a: Z_ab = X_ba^T for b = a + s, packed in z[s], three parts: word 2 n + r
+// is columns (rows of X) 16 b + 8 n + 2 (lane % 4) and the next, row (column of X)
 // 16 a + lane / 4 + 8 r.  After invert_diag and a barrier.
-__device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane, uint32_t (&zh)[4][4],
-                                             uint32_t (&zl)[4][4]) {
+__device__ __forceinline__ void invert_below(InvTiles* it, int a, int lane, uint32_t (&z)[4][3][4]) {
   const int g = lane / 4, t = lane % 4;
   {
-    const uint32_t* h = reinterpret_cast<const uint32_t*>(it->xt(a, 0));
-    const uint32_t* l = reinterpret_cast<const uint32_t*>(it->xt(a, 1));
     const int at[4] = {g * 8 + t, (g + 8) * 8 + t, g * 8 + t + 4, (g + 8) * 8 + t + 4};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      zh[0][i] = h[at[i]];
-      zl[0][i] = l[at[i]];
-    }
+    for (int x = 0; x < 3; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[0][x][i] = reinterpret_cast<const uint32_t*>(it->xt(a, x))[at[i]];
   }
 #pragma unroll
   for (int s = 1; s < 4; ++s) {  // b = a + s
     const int b = a + s;
     if (b > 3) break;
-    float y[2][4] = {};
+    float big[2][4] = {}, small[2][4] = {};
+    uint32_t f[3][4];
 #pragma unroll
     for (int c = 0; c < s; ++c) {
       const int idx = b * (b - 1) / 2 + a + c;
-      const uint32_t* h = reinterpret_cast<const uint32_t*>(it->low[idx][0]);
-      const uint32_t* l = reinterpret_cast<const uint32_t*>(it->low[idx][1]);
-      uint32_t bh[4], bl[4], b3[4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int x = 0; x < 3; ++x)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int w = (8 * n + g) * 8 + 4 * k + t;
-          bh[2 * n + k] = h[w];
-          bl[2 * n + k] = l[w];
-          b3[2 * n + k] = l[128 + w];
-        }
-      mma_split(y, zh[c], zl[c], bh, bl);
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) mma_16816(y[n], zh[c], b3[2 * n], b3[2 * n + 1]);
+          for (int k = 0; k < 2; ++k)
+            f[x][2 * n + k] =
+                reinterpret_cast<const uint32_t*>(it->low[idx][x])[(8 * n + g) * 8 + 4 * k + t];
+      mma_split(big, small, z[c], f);
     }
-    uint32_t yh[4], yl[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        split_pair(make_float2(-y[n][2 * r], -y[n][2 * r + 1]), yh[2 * n + r], yl[2 * n + r]);
+    uint32_t y[3][4];
+    next_factor(y, big, small, -1.f);
     // X_bb^T as a right factor: rows k of xt, transposed on load; lane -> row
     // lane % 16, column half lane / 16
-    uint32_t bh[4], bl[4];
     const uint32_t row = (uint32_t)((lane % 16) * 32 + (lane / 16) * 16);
-    ldmatrix_x4_trans(bh, smem_u32(it->xt(b, 0)) + row);
-    ldmatrix_x4_trans(bl, smem_u32(it->xt(b, 1)) + row);
-    float z[2][4] = {};
-    mma_split(z, yh, yl, bh, bl);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) ldmatrix_x4_trans(f[x], smem_u32(it->xt(b, x)) + row);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        split_pair(make_float2(z[n][2 * r], z[n][2 * r + 1]), zh[s][2 * n + r], zl[s][2 * n + r]);
+      for (int i = 0; i < 4; ++i) big[n][i] = small[n][i] = 0.f;
+    mma_split(big, small, y, f);
+    next_factor(z[s], big, small, 1.f);
   }
 }
 
 // Warp a's columns of the inverse X, as rows of the transposed tile (row j,
-// column i: element (i, j)), the parts `part` bytes apart: the diagonal block
-// from w, those below from zh, zl, those above zero.
-__device__ __forceinline__ void put_t_transposed(uint8_t* hi, int part, int a, int lane,
-                                                 const uint4 (&w)[2], const uint32_t (&zh)[4][4],
-                                                 const uint32_t (&zl)[4][4]) {
-  uint8_t* own = hi + (lane < 16 ? 0 : part);
-  put16(own, 16 * a + (lane & 15), 2 * a, w);
+// column i: element (i, j)), the three parts `part` bytes apart: the diagonal
+// block from w and w3, those below from z, those above zero.
+__device__ __forceinline__ void put_t_transposed(uint8_t* tile, int part, int a, int lane,
+                                                 const uint4 (&w)[2], const uint4 (&w3)[2],
+                                                 const uint32_t (&z)[4][3][4]) {
+  uint8_t* own = tile + (lane < 16 ? 0 : part);
+  const int own_row = 16 * a + (lane & 15);
+  put16(own, own_row, 2 * a, w);
+  if (lane < 16) put16(tile + 2 * part, own_row, 2 * a, w3);
   const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
 #pragma unroll 1
-  for (int b = 0; b < a; ++b) put16(own, 16 * a + (lane & 15), 2 * b, zero);
+  for (int b = 0; b < a; ++b) {
+    put16(own, own_row, 2 * b, zero);
+    if (lane < 16) put16(tile + 2 * part, own_row, 2 * b, zero);
+  }
   const int g = lane / 4;
-  uint8_t* row = hi + (16 * a + g) * 128 + 4 * (lane % 4);
+  uint8_t* row = tile + (16 * a + g) * 128 + 4 * (lane % 4);
 #pragma unroll
   for (int s = 1; s < 4; ++s) {
     if (a + s > 3) break;
@@ -487,10 +515,10 @@ __device__ __forceinline__ void put_t_transposed(uint8_t* hi, int part, int a, i
     for (int n = 0; n < 2; ++n) {
       uint8_t* to = row + (((2 * (a + s) + n) ^ g) << 4);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        *reinterpret_cast<uint32_t*>(to + 1024 * r) = zh[s][2 * n + r];
-        *reinterpret_cast<uint32_t*>(to + 1024 * r + part) = zl[s][2 * n + r];
-      }
+      for (int x = 0; x < 3; ++x)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<uint32_t*>(to + 1024 * r + x * part) = z[s][x][2 * n + r];
     }
   }
 }
@@ -550,14 +578,16 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uin
                : "memory");
 }
 
-// What the forward keeps for the backward: operand tiles, as they lie in shared
-// memory (fp32 values as hi and lo bf16 parts, swizzled), so that the
-// backward's copies bring them ready for the tensor cores:
-//   S  [BH][chunks][blocks of 32 columns]  the state before every chunk
-//   U  [BH][chunks][blocks of 32 columns]  what every row wrote
-//   T  [BH][chunks]                        the inverse (transposed), 16 KB
-//   P  [BH][chunks]                        16 KB
-// With them neither of the backward's kernels recomputes a chunk's inverse.
+// What the forward keeps for the backward:
+//   S  [BH][chunks][blocks of 32 columns]  the state before every chunk, fp32
+//   U  [BH][chunks][blocks of 32 columns]  what every row wrote, fp32
+//   T  [BH][chunks]                        the inverse (transposed), 24 KB
+//   P  [BH][chunks]                        24 KB
+// S and U as put_f32 lays them out; T and P as operand tiles, as they lie in
+// shared memory (fp32 values in three bf16 parts, swizzled), so that the reverse
+// chain's copies bring them ready for the tensor cores.  With them neither of the
+// backward's kernels recomputes a chunk's inverse.
+constexpr int kTTile = 3 * kBox;
 struct Saved {
   int64_t n, blocks, s_tile, s_bytes, u_bytes, t_bytes;  // t_bytes: of T, and of P
   Saved(const DeltaShape& s)
@@ -566,7 +596,7 @@ struct Saved {
         s_tile(s.D <= 64 ? 64 * 128 : 128 * 128),
         s_bytes(s.B * s.H * n * blocks * s_tile),
         u_bytes(s.B * s.H * n * blocks * kBox),
-        t_bytes(s.B * s.H * n * 2 * kBox) {}
+        t_bytes(s.B * s.H * n * kTTile) {}
   int64_t bytes() const { return s_bytes + u_bytes + 2 * t_bytes; }
 };
 

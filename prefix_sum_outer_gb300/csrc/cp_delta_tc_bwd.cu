@@ -48,7 +48,7 @@ struct ChainArgs {
   const float *g, *beta, *grad_state_out;
   const uint8_t *t, *pm;        // tiles of T and P
   __nv_bfloat16* dv;
-  uint8_t *ds, *dx;             // tiles of dS' and dX, as Saved's of S and U
+  uint8_t *ds, *dx;             // dS' and dX, fp32, as Saved's S and U
   float *xv, *grad_state_in;    // xv [M / 16 blocks][BH][N]: dX . V over the block
   int* status;
   int64_t N;
@@ -61,16 +61,18 @@ struct ChainLayout {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
-  static constexpr int oT = 2 * kKQ;           // hi, lo (after two stages of K, Q)
-  static constexpr int oP = oT + 2 * kBox;     // hi, lo
-  static constexpr int oS = oP + 2 * kBox;     // [DP x (hi | lo)]
-  static constexpr int oB = oS + DP * 128;     // [128 x (hi | lo)]: dU, then -gam b dX; s gam dO
-  static constexpr int oO = oB + 2 * kBox;     // [64 x (dU's third part | dO)]
-  static constexpr int oX = oO + kBox;         // [64 x (hi | lo)]: dX
-  static constexpr int oG = oX + kBox;
+  static constexpr int oT = 2 * kKQ;           // three parts (after two stages of K, Q)
+  static constexpr int oP = oT + kTTile;       // three parts
+  static constexpr int oS = oP + kTTile;       // [DP x (first | second part)]
+  static constexpr int oB = oS + DP * 128;     // [128 x (first | second)]: dU, then -gam b dX; s gam dO
+  static constexpr int oX = oB + 2 * kBox;     // [128 x (dS's third | B's third)]
+  static constexpr int oO = oX + 2 * kBox;     // [64 x dO]
+  static constexpr int oKeepS = oO + kBox;     // fp32 copies of dS' and dX on their way to memory
+  static constexpr int oKeepX = oKeepS + DP * 128;
+  static constexpr int oG = oKeepX + kBox;
   static constexpr int oBar = oG + 2 * (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 128 + 1024;
-  static constexpr int kPerSM = DP == 64 ? 2 : 1;
+  static constexpr int kPerSM = 1;
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
 };
 
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(tmem_holder, 256);
+    tmem_alloc(tmem_holder, 128);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -108,15 +110,15 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
   const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 16 * sub;
-  // K dS' (64 columns), then T^T dU (96); P^T dO (32); the update (64)
-  const uint32_t t_acc = tmem, t_e0 = tmem + 96, t_up = tmem + 128;
+  // K dS', T^T dU and the update, one after the other (96 columns); P^T dO (32)
+  const uint32_t t_acc = tmem, t_e0 = tmem + 96;
   const uint32_t T_addr = s_base + L::oT, P_addr = s_base + L::oP, S_addr = s_base + L::oS;
-  const uint32_t B_addr = s_base + L::oB, O_addr = s_base + L::oO + 64;
-  uint8_t *S_tile = sm + L::oS, *B_tile = sm + L::oB, *O_tile = sm + L::oO, *X_tile = sm + L::oX;
-  constexpr uint32_t id_nt64 = idesc_bf16_f32(128, 64, 0, 1);
+  const uint32_t B_addr = s_base + L::oB, S_third = s_base + L::oX, B_third = S_third + 64;
+  const uint32_t O_addr = s_base + L::oO;
+  uint8_t *S_tile = sm + L::oS, *B_tile = sm + L::oB, *X_tile = sm + L::oX, *O_tile = sm + L::oO;
   constexpr uint32_t id_nt96 = idesc_bf16_f32(128, 96, 0, 1);
   constexpr uint32_t id_tt32 = idesc_bf16_f32(128, 32, 1, 1);
-  constexpr uint32_t id_tt64 = idesc_bf16_f32(128, 64, 1, 1);
+  constexpr uint32_t id_tt96 = idesc_bf16_f32(128, 96, 1, 1);
   const uint64_t once = policy_evict_first();
   // step s of the walk is chunk n - 1 - s
   auto load_kq = [&](int s) {
@@ -129,15 +131,16 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     }
   };
   auto load_tile = [&](int at, const uint8_t* src, uint64_t* bar, int s) {
-    mbar_arrive_expect_tx(bar, 2 * kBox);
-    bulk_load(sm + at, src + (p * n + n - 1 - s) * (2 * kBox), 2 * kBox, bar);
+    mbar_arrive_expect_tx(bar, kTTile);
+    bulk_load(sm + at, src + (p * n + n - 1 - s) * (int64_t)kTTile, kTTile, bar);
   };
   auto issue_e0 = [&](int s) {  // warp 0: P^T dO of step s
     wait_or_abort(p_full, s & 1, a.status, abort_flag);
     __syncwarp();
     const uint32_t el = elect_one();
-    mma_tile<4, true, true>(el, t_e0, P_addr, O_addr, id_tt32, kBox, 16, 0, 0, true);
-    mma_tile<4, true, true>(el, t_e0, P_addr + kBox, O_addr, id_tt32, kBox, 16, 0, 0, false);
+#pragma unroll 1
+    for (int x = 2; x >= 0; --x)
+      mma_tile<4, true, true>(el, t_e0, P_addr + x * kBox, O_addr, id_tt32, kBox, 16, 0, 0, x == 2);
   };
   // lanes 0-63: the row of V, loaded a step ahead; lanes 64-127: that of dO
   const int64_t at = p * a.N * a.M + c0;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
   } else {
   read16(a.grad_state_out + (p * a.D + t) * a.M + c0, nc, a.grad_state_out != nullptr && row_on, dS);
   load_row(0);
-  if (t >= 64) put16(O_tile, t - 64, 4 + 2 * sub, row);
+  if (t >= 64) put16(O_tile, t - 64, 2 * sub, row);
   fence_proxy_async_smem();
   __syncthreads();
   if (warp == 0) issue_e0(0);
@@ -201,7 +204,10 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     const GateSlot* gs = gates + (s & 1);
     const int chunk = n - 1 - s;
     const int64_t tile = (p * n + chunk) * gridDim.y + blockIdx.y;
-    if (t < DP) store_parts(S_tile, t, sub, dS);
+    if (t < DP) {
+      store_parts(S_tile, X_tile, 0, t, sub, dS);
+      put_f32(sm + L::oKeepS, t, sub, dS);
+    }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -210,12 +216,13 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<DP / 16, false, true>(el, t_acc, kq, S_addr, id_nt64, 16, 16, L::kKQBox, 0, true);
+      mma_tile<DP / 16, false, true>(el, t_acc, kq, S_addr, id_nt96, 16, S_third - S_addr, L::kKQBox, 0,
+                                     true);
       if (el) mma_commit(done);
     }
     if (threadIdx.x == 128) {
-      bulk_store(a.ds + tile * (DP * 128), S_tile, DP * 128);
-      if (s > 0) bulk_store(a.dx + (tile + gridDim.y) * kBox, X_tile, kBox);  // the step before's
+      bulk_store(a.ds + tile * (DP * 128), sm + L::oKeepS, DP * 128);
+      if (s > 0) bulk_store(a.dx + (tile + gridDim.y) * kBox, sm + L::oKeepX, kBox);  // the step before's
       tma_store_commit();
     }
     float2 x[8];
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       unpack16(row, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = mul2(w, x[j]);
-      store_parts(B_tile, t, sub, x);
+      store_parts(B_tile, X_tile, 4, t, sub, x);
       if (s + 1 < n) load_row(s + 1);
     }
     wait_or_abort(done, phase, a.status, abort_flag);
@@ -236,12 +243,9 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       load16_sum(t_acc + lane_col, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = fma2(del, x[j], e0[j]);
-      uint4 x0[2], x1[2], x2[2];
-      split16_3(x, x0, x1, x2);
-      put_parts(B_tile, t, sub, x0, x1);
-      put16(O_tile, t, 2 * sub, x2);
+      store_parts(B_tile, X_tile, 4, t, sub, x);
     }
-    // the copies out of the S and X tiles have read them
+    // the copies out of dS' and dX have read them
     if (threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
@@ -251,25 +255,19 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      // T^T hi with dU's three parts, T^T lo with two
-      mma_tile<4, false, true>(el, t_acc, T_addr, B_addr, id_nt96, 16, 2 * kBox, 0, 0, true);
-      mma_tile<4, false, true>(el, t_acc, T_addr + kBox, B_addr, id_nt64, 16, 16, 0, 0, false);
+      mma_parts<false>(el, t_acc, T_addr, kBox, 16, B_addr, B_third);
       if (el) mma_commit(done + 1);
     }
-    if (t >= 64 && s + 1 < n) put16(O_tile, t - 64, 4 + 2 * sub, row);  // P^T dO has read dO
+    if (t >= 64 && s + 1 < n) put16(O_tile, t - 64, 2 * sub, row);  // P^T dO has read dO
     wait_or_abort(done + 1, phase, a.status, abort_flag);
     tc_fence_after();
     if (t < 64) {
       float2 r[8];
-      tmem_ld16(t_acc + 64 + lane_col, r);
       load16_sum(t_acc + lane_col, x);
       const float2 w = both(-gs->b[t] * gs->gam[t]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = add2(x[j], r[j]);
-        r[j] = mul2(w, x[j]);
-      }
-      store_parts(B_tile, t, sub, r);
+      for (int j = 0; j < 8; ++j) r[j] = mul2(w, x[j]);
+      store_parts(B_tile, X_tile, 4, t, sub, r);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -280,7 +278,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       // [K; Q]^T: 128 rows along K; with one 64-column block the lanes past 64
       // read on into the tiles behind, and are not used
       constexpr uint32_t lbo = DP == 128 ? L::kKQBox : kBox;
-      mma_tile<8, true, true>(el, t_up, kq, B_addr, id_tt64, lbo, 16, 0, 0, true);
+      mma_tile<8, true, true>(el, t_acc, kq, B_addr, id_tt96, lbo, B_third - B_addr, 0, 0, true);
       if (el) mma_commit(done + 2);
       if (s + 1 < n) issue_e0(s + 1);
     }
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
       unpack16(row, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dot = fma2(x[j], v[j], dot);
-      store_parts(X_tile, t, sub, x);
+      put_f32(sm + L::oKeepX, t, sub, x);
       uint4 dv[2];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = mul2(b, x[j]);
@@ -305,7 +303,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
     const float2 last = both(gs->last.x), last_lo = both(gs->last.y);
-    load16_sum(t_up + lane_col, x);
+    load16_sum(t_acc + lane_col, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dS[j] = fma2(last, dS[j], fma2(last_lo, dS[j], x[j]));
   }
@@ -315,7 +313,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
   fence_proxy_async_smem();
   __syncthreads();
   if (threadIdx.x == 128) {  // the last step's, chunk 0
-    bulk_store(a.dx + (p * n * gridDim.y + blockIdx.y) * kBox, X_tile, kBox);
+    bulk_store(a.dx + (p * n * gridDim.y + blockIdx.y) * kBox, sm + L::oKeepX, kBox);
     tma_store_commit();
     tma_store_wait_read_all();
   }
@@ -326,7 +324,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
   grid_dep_launch_dependents();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 128);
   }
 }
 
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(kChainThreads, ChainLayout<DP>::kPerSM)
 struct GradArgs {
   const __nv_bfloat16* go;
   const float *g, *beta, *xv;
-  const uint8_t *s, *u, *ds, *dx;  // tiles
+  const float4 *s, *u, *ds, *dx;   // fp32 tiles, in their 16-byte pieces
   __nv_bfloat16 *dq, *dk;
   float *dq_part, *dk_part;     // [BH][N][D] fp32, where value heads share a key head; else null
   float *dg, *dbeta;
@@ -344,33 +342,49 @@ struct GradArgs {
   float scale;
 };
 
-template <int DP>
+// WIDE: more than 64 value columns.
+template <int DP, bool WIDE>
 struct GradLayout {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
-  static constexpr int kS = DP * 128;
-  // two blocks of 32 value columns, every tile hi | lo
-  static constexpr int oA = kKQ;              // [dX; dO | 0]; then [Ma; Mq] hi, lo
-  static constexpr int oU = oA + 4 * kBox;
-  static constexpr int oS = oU + 2 * kBox;
-  static constexpr int oD = oS + 2 * kS;      // dS'
-  static constexpr int oG = oD + 2 * kS;
+  // a block of 32 value columns: tiles of (first | second part), the third
+  // parts two to a tile; then [Ma; Mq] in three parts over the first 48 KB
+  static constexpr int kRows = DP == 64 ? 64 : 128;
+  static constexpr int oA = kKQ;              // [dX; dO]
+  static constexpr int oA3 = oA + 2 * kBox;   // [128 x ([dX; dO]'s third | dS's)]
+  static constexpr int oU3 = oA3 + 2 * kBox;  // [(U's third | S's)]
+  static constexpr int oU = oU3 + kRows * 128;
+  static constexpr int oS = oU + kBox;
+  static constexpr int oD = oS + DP * 128;    // dS'
+  static constexpr int oG = oD + DP * 128;
   static constexpr int oX = oG + (int)sizeof(GateSlot);  // sums for the gates
   static constexpr int kXFloats = 8 * 64 + 2 * 64 * 6 + 16;
   static constexpr int oBar = oX + kXFloats * 4;
   static constexpr int kBytes = oBar + 64 + 1024;
-  static constexpr int kBlock = 2 * kBox + 2 * kS;             // bytes copied per block
   static constexpr int kCols = DP == 64 ? 256 : 512;           // tensor memory
-  static constexpr int kPerSM = DP == 64 ? 2 : 1;
+  static constexpr int kPerSM = DP == 64 && !WIDE ? 2 : 1;
+  static_assert(oA + 6 * kBox <= oG, "[Ma; Mq]");
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
 };
 
-template <int DP>
-__global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
+// Four fp32 values, columns 4 c .. of a block's row, into its factor's parts.
+__device__ __forceinline__ void put4(uint8_t* tile, uint8_t* third, int third_ch, int row, int c,
+                                     float4 v) {
+  uint2 a, b, d;
+  split_pair3(make_float2(v.x, v.y), a.x, b.x, d.x);
+  split_pair3(make_float2(v.z, v.w), a.y, b.y, d.y);
+  const int at = row * 128 + 8 * (c & 1), x = row & 7, ch = c / 2;
+  *reinterpret_cast<uint2*>(tile + at + ((ch ^ x) << 4)) = a;
+  *reinterpret_cast<uint2*>(tile + at + (((4 + ch) ^ x) << 4)) = b;
+  *reinterpret_cast<uint2*>(third + at + (((third_ch + ch) ^ x) << 4)) = d;
+}
+
+template <int DP, bool WIDE>
+__global__ void __launch_bounds__(256, GradLayout<DP, WIDE>::kPerSM)
     delta_tc_grad_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k, const GradArgs a) {
-  using L = GradLayout<DP>;
+  using L = GradLayout<DP, WIDE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align_tiles(smem_raw);
   GateSlot* gs = reinterpret_cast<GateSlot*>(sm + L::oG);
@@ -378,8 +392,8 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   float* dots = e_sum + 512;     // [2 column halves][6][64]: rows' sums, as written below
   float* z_sum = dots + 768;     // [8]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::oBar);
-  uint64_t *kq_full = bars, *full = bars + 1, *done = bars + 2;  // done [2]
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 4);
+  uint64_t *kq_full = bars, *done = bars + 1;  // done [2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform to the compiler)
@@ -388,24 +402,37 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   const int64_t p = blockIdx.x / a.n_chunks;
   const int chunk = blockIdx.x % a.n_chunks, i0 = chunk * kCh;
   const int pk = (int)((p / a.H) * (a.H / a.group) + (p % a.H) / a.group);
-  const int blocks = (a.M + kCB - 1) / kCB, n_mb = (blocks + 1) / 2;
+  const int blocks = (a.M + kCB - 1) / kCB;
 
   const uint64_t keep = policy_evict_first();
   const int64_t tile0 = (p * a.n_chunks + chunk) * blocks;
-  auto load_mb = [&](int m) {  // blocks 2 m and 2 m + 1
-    const int nb = min(2, blocks - 2 * m);
-    mbar_arrive_expect_tx(full, nb * L::kBlock);
-    for (int h = 0; h < nb; ++h) {
-      const int64_t tile = tile0 + 2 * m + h;
-      bulk_load(sm + L::oA + h * 2 * kBox, a.dx + tile * kBox, kBox, full);
-      bulk_load(sm + L::oU + h * kBox, a.u + tile * kBox, kBox, full);
-      bulk_load(sm + L::oS + h * L::kS, a.s + tile * L::kS, L::kS, full);
-      bulk_load(sm + L::oD + h * L::kS, a.ds + tile * L::kS, L::kS, full);
+  // What comes by plain loads sets out first, beside the copies, and then a
+  // block ahead under the products: a thread's 16-byte pieces of the block's fp32
+  // tiles, of dO eight columns of a row, and the gates of one warp's rows.
+  constexpr int kUP = 64 * 8 / 256, kSP = DP * 8 / 256;  // pieces of a 64-row tile, of a state
+  float4 xu[kUP], xx[kUP], xs[kSP], xd[kSP];
+  uint4 dov;
+  const int do_row = threadIdx.x / 4, do_ch = threadIdx.x % 4;
+  auto load_block = [&](int m) {
+    const int64_t u = (tile0 + m) * (64 * 8) + threadIdx.x, s = (tile0 + m) * (DP * 8) + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < kUP; ++e) {
+      xx[e] = __ldcs(a.dx + u + 256 * e);
+      xu[e] = __ldcs(a.u + u + 256 * e);
     }
+#pragma unroll
+    for (int e = 0; e < kSP; ++e) {
+      xs[e] = __ldcs(a.s + s + 256 * e);
+      xd[e] = __ldcs(a.ds + s + 256 * e);
+    }
+    const int col = kCB * m + 8 * do_ch;
+    dov = i0 + do_row < a.N && col < a.M
+              ? *reinterpret_cast<const uint4*>(a.go + (p * a.N + i0 + do_row) * a.M + col)
+              : make_uint4(0, 0, 0, 0);
   };
   grid_dep_wait();
   if (issuer) {
-    for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(bars + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
     mbar_arrive_expect_tx(kq_full, L::kKQ);
@@ -413,28 +440,25 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       tma_load_3d(sm + x * L::kKQBox, &tm_k, kq_full, 64 * x, i0, pk, keep);
       tma_load_3d(sm + x * L::kKQBox + kBox, &tm_q, kq_full, 64 * x, i0, pk, keep);
     }
-    load_mb(0);
   }
   if (warp == 0) {
     __syncwarp();
     tmem_alloc(tmem_holder, L::kCols);
     tmem_relinquish();
   }
-  // what comes by plain loads sets out here, beside the copies: the gates of
-  // one warp's rows, and dO's part of the A tiles, a row's 16 columns
   float4 gb = make_float4(0.f, 0.f, 0.f, 0.f);
   if (warp == 1) {
     const int64_t i = i0 + lane, at = p * a.N;
     gb = make_float4(i < a.N ? a.g[at + i] : 0.f, i + 32 < a.N ? a.g[at + i + 32] : 0.f,
                      i < a.N ? a.beta[at + i] : 0.f, i + 32 < a.N ? a.beta[at + i + 32] : 0.f);
   }
-  const int do_row = threadIdx.x % 64, do_block = (threadIdx.x / 64) % 2, do_sub = threadIdx.x / 128;
-  uint4 dov[2];
-  auto load_do = [&](int m) {
-    const int col = 64 * m + 32 * do_block + 16 * do_sub;
-    read16(a.go + (p * a.N + i0 + do_row) * a.M + col, a.M - col, i0 + do_row < a.N, dov);
-  };
-  load_do(0);
+  load_block(0);
+  {  // dO has no second and third part
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int at = (64 + do_row) * 128, x = do_row & 7;
+    *reinterpret_cast<uint4*>(sm + L::oA + at + (((4 + do_ch) ^ x) << 4)) = zero;
+    *reinterpret_cast<uint4*>(sm + L::oA3 + at + ((do_ch ^ x) << 4)) = zero;
+  }
   for (int i = threadIdx.x; i < 512; i += 256) e_sum[i] = 0.f;
   fence_proxy_async_smem();
   tc_fence_before();
@@ -443,8 +467,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
   const uint32_t t_kk = tmem, t_p2 = tmem + 64, t_in = tmem + 128, t_u = t_in + DP;
   const uint32_t lane_base = (uint32_t)(warp % 4) << 21;
-  const uint32_t A_addr = s_base + L::oA, U_addr = s_base + L::oU, S_addr = s_base + L::oS;
-  const uint32_t D_addr = s_base + L::oD;
+  const uint32_t A_addr = s_base + L::oA;
   constexpr uint32_t id_nn64 = idesc_bf16_f32(128, 64, 0, 0);
   constexpr uint32_t id_nnD = idesc_bf16_f32(128, DP, 0, 0);
   constexpr uint32_t id_ntD = idesc_bf16_f32(128, DP, 0, 1);
@@ -454,86 +477,24 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     __syncwarp();
     mma_tile<DP / 16, false, false>(elect_one(), t_kk, s_base, s_base, id_nn64, 16, 16, L::kKQBox, L::kKQBox, true);
   }
-  float z = 0.f;  // <S, dS'>, this thread's share
-  for (int m = 0; m < n_mb; ++m) {
-    const int nb = min(2, blocks - 2 * m);
-    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // no lo part
-    put_parts(sm + L::oA + do_block * 2 * kBox + kBox, do_row, do_sub, dov, zero);
-    if (m + 1 < n_mb) load_do(m + 1);
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (warp == 0) {
-      wait_or_abort(full, m & 1, a.status, abort_flag);
-      __syncwarp();
-      const uint32_t el = elect_one();
-#pragma unroll 1
-      for (int x = 0; x < 4 * nb; ++x) {
-        // per block: (A hi, B hi), (A lo, B hi), (A hi, B lo), (A lo, B lo)
-        const int h = x >> 2;
-        const uint32_t ap = (x & 1) * 64, b = ((x >> 1) & 1) * 64;
-        const bool fresh = m == 0 && x == 0;
-        const uint32_t u = U_addr + h * kBox;
-        mma_tile<2, false, false>(el, t_p2, A_addr + h * 2 * kBox + ap, u + b, id_nn64, 16, 16, 0, 0, fresh);
-        mma_tile<2, false, false>(el, t_in, A_addr + h * 2 * kBox + ap, S_addr + h * L::kS + b, id_nnD,
-                                  16, 16, 0, 0, fresh);
-        // lanes past 64 read on behind U and are not used
-        mma_tile<2, false, false>(el, t_u, u + ap, D_addr + h * L::kS + b, id_nnD, 16, 16, 0, 0, fresh);
-      }
-      if (el) mma_commit(done);
-    }
-    if (warp == 1 && m == 0) write_gates(gs, lane, gb.x, gb.y, gb.z, gb.w);
-    if (warp >= 6 && m == 0) {  // dX . V of the rows, from the chain's blocks
-      const int i = threadIdx.x - 192;
-      float d = 0.f;
-      if (i0 + i < a.N)
-#pragma unroll 4
-        for (int x = 0; x < (a.M + 15) / 16; ++x) d += a.xv[((int64_t)x * a.BH + p) * a.N + i0 + i];
-      dots[640 + i] = d;
-    }
-    wait_or_abort(full, m & 1, a.status, abort_flag);
-    // the MMAs read the tiles at the same time
-    for (int e = threadIdx.x; e < nb * DP * 4; e += 256) {
-      // 16-byte pieces: a row's hi columns, their lo parts 64 bytes on in the
-      // same row, which the swizzle leaves at piece ^ 4
-      const int row = e / 4, ch = e % 4, hi = row * 128 + ((ch ^ (row & 7)) << 4), lo = hi ^ 64;
-      const uint4 sh = *reinterpret_cast<const uint4*>(sm + L::oS + hi);
-      const uint4 sl = *reinterpret_cast<const uint4*>(sm + L::oS + lo);
-      const uint4 dh = *reinterpret_cast<const uint4*>(sm + L::oD + hi);
-      const uint4 dl = *reinterpret_cast<const uint4*>(sm + L::oD + lo);
-      const uint32_t w[4][4] = {{sh.x, sh.y, sh.z, sh.w}, {sl.x, sl.y, sl.z, sl.w},
-                                {dh.x, dh.y, dh.z, dh.w}, {dl.x, dl.y, dl.z, dl.w}};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s0 = __uint_as_float(w[0][i] << 16) + __uint_as_float(w[1][i] << 16);
-        const float s1 = __uint_as_float(w[0][i] & 0xffff0000u) + __uint_as_float(w[1][i] & 0xffff0000u);
-        const float d0 = __uint_as_float(w[2][i] << 16) + __uint_as_float(w[3][i] << 16);
-        const float d1 = __uint_as_float(w[2][i] & 0xffff0000u) + __uint_as_float(w[3][i] & 0xffff0000u);
-        z = fmaf(s1, d1, fmaf(s0, d0, z));
-      }
-    }
-    wait_or_abort(done, m & 1, a.status, abort_flag);
-    if (m + 1 < n_mb) {
-      fence_proxy_async_smem();
-      __syncthreads();  // every thread has read the tiles
-      if (issuer) load_mb(m + 1);
-    }
-  }
-  tc_fence_after();
-  for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
-  if (lane == 0) z_sum[warp] = z;
-  __syncthreads();  // the gates
-
+  float z = 0.f;           // <S, dS'>, this thread's share
+  float own[kUP] = {};     // dX . U of the thread's rows
   // lanes 0-63 ("K rows"): i = t; lanes 64-127 ("Q rows"): i = t - 64
   const bool is_k = t < 64;
   const int i = t & 63, row32 = i / 32;
-  const float gam = gs->gam[i], del = gs->del[i], bt = gs->b[i];
-  // the products with the state: a half of D's columns a thread
-  constexpr int HC = DP / 2;
-  float2 g2[HC / 2];
-  {
-    const uint8_t* xr = sm;  // the row of k or q
-    const float w = is_k ? -gam * bt : a.scale * gam;
-    float2 din = both(0.f), du = both(0.f);
+  // The products with the states and the pairs are read out every two blocks, and
+  // summed here: an MMA rounds its sum toward zero, and six a step of 16 columns,
+  // all into one accumulator, would leave 1.6e-6 of dg at 200 columns.
+  constexpr int HC = DP / 2;  // a half of D's columns a thread
+  float2 g2[HC / 2], din = both(0.f), du = both(0.f), p2[2][8];
+  if (WIDE) {
+#pragma unroll
+    for (int e = 0; e < HC / 2; ++e) g2[e] = both(0.f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p2[e / 8][e % 8] = both(0.f);
+  }
+  const auto read_states = [&]() {
+    const float w = is_k ? -gs->gam[i] * gs->b[i] : a.scale * gs->gam[i], del = gs->del[i];
 #pragma unroll
     for (int h = 0; h < HC / 16; ++h) {
       const int c = wg * HC + 16 * h;
@@ -541,7 +502,7 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       tmem_ld16(t_in + lane_base + c, r);
       tmem_ld16(t_u + lane_base + c, u);
       tmem_ld_wait();
-      const uint8_t* src = xr + (c / 64) * L::kKQBox + t * 128;
+      const uint8_t* src = sm + (c / 64) * L::kKQBox + t * 128;  // the row of k or q
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint4 x4 = *reinterpret_cast<const uint4*>(src + ((((c & 63) / 8 + j) ^ (t & 7)) << 4));
@@ -558,10 +519,95 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
             du = fma2(x, uu, du);
             o = fma2(both(del), uu, o);
           }
-          g2[8 * h + k / 2] = o;
+          g2[8 * h + k / 2] = WIDE ? add2(g2[8 * h + k / 2], o) : o;
         }
       }
     }
+  };
+  for (int m = 0; m < blocks; ++m) {
+    if (m > 0) wait_or_abort(done, (m - 1) & 1, a.status, abort_flag);  // the tiles have been read
+    if (WIDE && m > 0 && m % 2 == 0) {
+      tc_fence_after();
+      read_states();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 r[8];
+        tmem_ld16(t_p2 + lane_base + 16 * (2 * wg + h), r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p2[h][e] = add2(p2[h][e], r[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kUP; ++e) {
+      const int i = threadIdx.x + 256 * e, row = i / 8, c = (i % 8) ^ (row & 7);
+      put4(sm + L::oA, sm + L::oA3, 0, row, c, xx[e]);
+      put4(sm + L::oU, sm + L::oU3, 0, row, c, xu[e]);
+      own[e] = fmaf(xx[e].x, xu[e].x, own[e]);
+      own[e] = fmaf(xx[e].y, xu[e].y, own[e]);
+      own[e] = fmaf(xx[e].z, xu[e].z, own[e]);
+      own[e] = fmaf(xx[e].w, xu[e].w, own[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kSP; ++e) {
+      const int i = threadIdx.x + 256 * e, row = i / 8, c = (i % 8) ^ (row & 7);
+      put4(sm + L::oS, sm + L::oU3, 4, row, c, xs[e]);
+      put4(sm + L::oD, sm + L::oA3, 4, row, c, xd[e]);
+      z = fmaf(xs[e].x, xd[e].x, z);
+      z = fmaf(xs[e].y, xd[e].y, z);
+      z = fmaf(xs[e].z, xd[e].z, z);
+      z = fmaf(xs[e].w, xd[e].w, z);
+    }
+    *reinterpret_cast<uint4*>(sm + L::oA + (64 + do_row) * 128 + ((do_ch ^ (do_row & 7)) << 4)) = dov;
+    tc_fence_before();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+      const uint32_t el = elect_one();
+      // part x of a factor: 64 bytes on for the second, another tile for the third
+      const auto part = [&](uint32_t first, uint32_t third, int x) {
+        return x == 2 ? third : first + 64 * x;
+      };
+#pragma unroll 1
+      for (int x = 2; x >= 0; --x)
+#pragma unroll 1
+        for (int y = x; y >= 0; --y) {
+          const bool fresh = m % 2 == 0 && x == 2 && y == 2;
+          const uint32_t dx = part(A_addr, s_base + L::oA3, y), u = part(s_base + L::oU, s_base + L::oU3, y);
+          mma_tile<2, false, false>(el, t_p2, dx, part(s_base + L::oU, s_base + L::oU3, x - y), id_nn64, 16,
+                                    16, 0, 0, fresh);
+          mma_tile<2, false, false>(el, t_in, dx, part(s_base + L::oS, s_base + L::oU3 + 64, x - y), id_nnD,
+                                    16, 16, 0, 0, fresh);
+          // lanes past 64 read on behind U and are not used
+          mma_tile<2, false, false>(el, t_u, u, part(s_base + L::oD, s_base + L::oA3 + 64, x - y), id_nnD, 16,
+                                    16, 0, 0, fresh);
+        }
+      if (el) mma_commit(done);
+    }
+    if (m + 1 < blocks) load_block(m + 1);
+    if (warp == 1 && m == 0) write_gates(gs, lane, gb.x, gb.y, gb.z, gb.w);
+    if (warp >= 6 && m == 0) {  // dX . V of the rows, from the chain's blocks
+      const int i = threadIdx.x - 192;
+      float d = 0.f;
+      if (i0 + i < a.N)
+#pragma unroll 4
+        for (int x = 0; x < (a.M + 15) / 16; ++x) d += a.xv[((int64_t)x * a.BH + p) * a.N + i0 + i];
+      dots[640 + i] = d;
+    }
+  }
+  wait_or_abort(done, (blocks - 1) & 1, a.status, abort_flag);
+  tc_fence_after();
+  for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+  if (lane == 0) z_sum[warp] = z;
+#pragma unroll
+  for (int e = 0; e < kUP; ++e) {  // a row's eight pieces lie side by side
+    for (int o = 4; o > 0; o /= 2) own[e] += __shfl_xor_sync(0xffffffffu, own[e], o);
+    if (lane % 8 == 0) dots[256 + threadIdx.x / 8 + 32 * e] = own[e];
+  }
+  __syncthreads();  // the gates
+  const float bt = gs->b[i];
+  read_states();
+  {
     // [0] k . (dX S^T), [1] q . (dO S^T), [2] k . (U dS'^T)
     float* d = dots + wg * 384;
     if (is_k) {
@@ -572,9 +618,8 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     }
   }
   // Ma and Mq, their tiles, and the pairs' sums
-  uint8_t *M_hi = sm + L::oA, *M_lo = M_hi + 2 * kBox;
   float part[32];    // columns 32 wg ..: the pair's weight in dg, then its running sum
-  float db = 0.f, own = 0.f;  // own: dX_i . U_i
+  float db = 0.f;
   const int last = is_k ? i - 1 : i;
   const float wm = is_k ? bt : 1.f;
 #pragma unroll
@@ -588,8 +633,10 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     tmem_ld_wait();
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+      float2 m = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+      if (WIDE) m = add2(m, p2[h][e]);
       // masked places stay 0 whatever the accumulators hold
-      float2 m = mul2(v[e], make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
+      m = mul2(v[e], m);
       const int j = 16 * c + 2 * e;
       if (j > last) m.x = 0.f;
       if (j + 1 > last) m.y = 0.f;
@@ -597,14 +644,12 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
       if (j > last) x.x = 0.f;
       if (j + 1 > last) x.y = 0.f;
       db += x.x + x.y;
-      if (j == i) own = __uint_as_float(r[2 * e]);
-      if (j + 1 == i) own = __uint_as_float(r[2 * e + 1]);
       v[e] = mul2(both(wm), m);
       x = mul2(both(wm), x);
       part[16 * h + 2 * e] = x.x;
       part[16 * h + 2 * e + 1] = x.y;
     }
-    store16_split(M_hi, M_lo, t, 2 * c, v);
+    store16_split(sm + L::oA, 2 * kBox, t, 2 * c, v);
   }
   tc_fence_before();
   fence_proxy_async_smem();
@@ -613,12 +658,12 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
     tc_fence_after();
     const uint32_t el = elect_one();
 #pragma unroll 1
-    for (int x = 0; x < 2; ++x) {  // the tile's hi and lo parts
+    for (int x = 2; x >= 0; --x) {  // the tile's parts
       const uint32_t ap = A_addr + x * 2 * kBox;
       // [Ma; Mq] K
-      mma_tile<4, false, true>(el, t_in, ap, s_base, id_ntD, 16, L::kKQBox, 0, 0, x == 0);
+      mma_tile<4, false, true>(el, t_in, ap, s_base, id_ntD, 16, L::kKQBox, 0, 0, x == 2);
       // Ma^T K + Mq^T Q; lanes past 64 read on and are not used
-      mma_tile<8, true, true>(el, t_u, ap, s_base, id_ttD, kBox, L::kKQBox, 0, 0, x == 0);
+      mma_tile<8, true, true>(el, t_u, ap, s_base, id_ttD, kBox, L::kKQBox, 0, 0, x == 2);
     }
     if (el) mma_commit(done + 1);
   }
@@ -658,7 +703,6 @@ __global__ void __launch_bounds__(256, GradLayout<DP>::kPerSM)
   }
   if (is_k) {
     dots[wg * 384 + 192 + i] = db;
-    if (row32 == wg) dots[256 + i] = own;
   }
   __syncthreads();
   if (warp >= 6) {
@@ -773,13 +817,13 @@ struct Scratch {
   int64_t bytes() const { return ds + dx + xv + 2 * part; }
 };
 
-template <int DP>
+template <int DP, bool WIDE>
 cp_status_t launch(const DeltaShape& s, const DeltaBwd& f, const ChainArgs& c, const GradArgs& g,
                    cudaStream_t stream) {
   using LC = ChainLayout<DP>;
-  using LG = GradLayout<DP>;
+  using LG = GradLayout<DP, WIDE>;
   auto chain = delta_tc_chain_kernel<DP>;
-  auto grad = delta_tc_grad_kernel<DP>;
+  auto grad = delta_tc_grad_kernel<DP, WIDE>;
   if (cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, LC::kBytes) != cudaSuccess ||
       cudaFuncSetAttribute(grad, cudaFuncAttributeMaxDynamicSharedMemorySize, LG::kBytes) != cudaSuccess)
     return CP_ERR_CUDA;
@@ -821,9 +865,10 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
   c.H = (int)s.H; c.group = (int)(s.H / s.Hk); c.D = (int)s.D; c.M = (int)s.M; c.scale = s.scale;
   GradArgs g{};
   g.go = c.go; g.g = f.g; g.beta = f.beta; g.xv = c.xv;
-  g.s = reinterpret_cast<const uint8_t*>(f.ckpt);
-  g.u = g.s + k.s_bytes;
-  g.ds = w.ds_at; g.dx = w.dx_at;
+  g.s = reinterpret_cast<const float4*>(f.ckpt);
+  g.u = g.s + k.s_bytes / 16;
+  g.ds = reinterpret_cast<const float4*>(w.ds_at);
+  g.dx = reinterpret_cast<const float4*>(w.dx_at);
   if (w.part != 0) {
     g.dq_part = reinterpret_cast<float*>(w.part_at);
     g.dk_part = reinterpret_cast<float*>(w.part_at + w.part);
@@ -832,7 +877,8 @@ cp_status_t delta_tc_bwd(const DeltaShape& s, const DeltaBwd& f, void* scratch, 
   g.dg = f.dg; g.dbeta = f.dbeta; g.status = status;
   g.N = s.N; g.n_chunks = (int)k.n; g.BH = (int)BH; g.H = c.H; g.group = c.group; g.D = c.D;
   g.M = c.M; g.scale = s.scale;
-  cp_status_t st = s.D <= 64 ? launch<64>(s, f, c, g, stream) : launch<128>(s, f, c, g, stream);
+  cp_status_t st = s.D <= 64 ? (s.M <= 64 ? launch<64, false> : launch<64, true>)(s, f, c, g, stream)
+                             : (s.M <= 64 ? launch<128, false> : launch<128, true>)(s, f, c, g, stream);
   if (st != CP_OK || w.part == 0) return st;
   const cudaError_t e = delta_join_launch({g.dq_part, g.dk_part, nullptr, nullptr, f.dq, f.dk, nullptr,
                                            nullptr, s.N, s.D, s.B * s.Hk, c.group, 1},

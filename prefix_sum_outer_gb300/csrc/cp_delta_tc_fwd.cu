@@ -40,7 +40,7 @@ using namespace delta;
 // ------------------------------------------------------- a chunk's matrices
 struct PrepArgs {
   const float *g, *beta;
-  uint8_t *t, *pt, *p;  // [BH][chunks] x 16 KB each (hi, lo); p may be null
+  uint8_t *t, *pt, *p;  // [BH][chunks] x 24 KB each (three parts); p may be null
   int* status;
   int64_t N;
   int n_chunks, chunk0, span, H, group;  // of n_chunks: span chunks from chunk0 on
@@ -53,19 +53,18 @@ struct PrepLayout {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kKQBox = 2 * kBox;
   static constexpr int kKQ = kBoxes * kKQBox;
-  // T (hi, lo) lies over the blocks that it is made from, or over the second
-  // half of K, Q; P and then P T (hi, lo) over K, Q, done with by then.  The
-  // product with T's lo part reads 64 rows past it, which the tiles behind hold.
-  static constexpr bool kTOverInv = DP == 64;
-  static constexpr int oT = kTOverInv ? 0 : 2 * kBox;
-  static constexpr int oKQ = kTOverInv ? 2 * kBox : 0;
-  static constexpr int oP = oKQ;
-  static constexpr int oInv = kTOverInv ? 0 : kKQ;
-  static constexpr int oG = kTOverInv ? oKQ + kKQ : oInv + (int)sizeof(InvTiles);
+  // K and Q are done with before A and P are written: T (three parts) lies over
+  // the blocks that it is made from and these over K and Q, P and then P T behind
+  // them.  A product with a part of T reads 64 rows past it, of the next.
+  static constexpr int oKQ = 0;
+  static constexpr int oInv = 0;
+  static constexpr int oT = 0;
+  static constexpr int oP = kTTile;
+  static constexpr int oG = 2 * kTTile;
   static constexpr int oBar = oG + (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 64 + 1024;
-  static constexpr int kPerSM = DP == 64 ? 6 : 4;
-  static_assert(kTOverInv ? sizeof(InvTiles) <= 2 * kBox : sizeof(InvTiles) >= kBox, "T's places");
+  static constexpr int kPerSM = 4;
+  static_assert(kKQ <= oG && sizeof(InvTiles) <= kTTile, "places");
   static_assert(kPerSM * (kBytes + 1024) <= 233472, "shared memory");
   static_assert(sizeof(InvTiles) % 16 == 0 && sizeof(GateSlot) % 16 == 0, "alignment");
 };
@@ -138,33 +137,35 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
                 if (w < 2)
                   put_a16(it, i, cb, v);
                 else
-                  store16_split(sm + L::oP, sm + L::oP + kBox, i, 2 * cb, v);
+                  store16_split(sm + L::oP, kBox, i, 2 * cb, v);
               });
   __syncthreads();
-  uint4 xw[2];
-  uint32_t zh[4][4], zl[4][4];
-  invert_diag(it, w, lane, xw);
+  uint4 xw[2], xw3[2];
+  uint32_t z[4][3][4];
+  invert_diag(it, w, lane, xw, xw3);
   __syncthreads();
-  invert_below(it, w, lane, zh, zl);
-  if (L::kTOverInv) __syncthreads();
-  put_t_transposed(sm + L::oT, kBox, w, lane, xw, zh, zl);
+  invert_below(it, w, lane, z);
+  __syncthreads();
+  put_t_transposed(sm + L::oT, kBox, w, lane, xw, xw3, z);
   tc_fence_before();
   fence_proxy_async_smem();
   __syncthreads();
-  const int64_t tile = (p * a.n_chunks + chunk) * (int64_t)(2 * kBox);
+  const int64_t tile = (p * a.n_chunks + chunk) * (int64_t)kTTile;
   if (w == 0) {
     tc_fence_after();
     const uint32_t el = elect_one();
     // (P T)^T = T^T P^T; lanes 0-63 are read
 #pragma unroll 1
-    for (int x = 0; x < 4; ++x)
-      mma_tile<4, false, false>(el, t_pt, T_addr + (x & 1) * kBox, P_addr + (x >> 1) * kBox, id_nn64,
-                                16, 16, 0, 0, x == 0);
+    for (int x = 2; x >= 0; --x)
+#pragma unroll 1
+      for (int y = x; y >= 0; --y)
+        mma_tile<4, false, false>(el, t_pt, T_addr + y * kBox, P_addr + (x - y) * kBox, id_nn64, 16, 16,
+                                  0, 0, x == 2 && y == 2);
     if (el) mma_commit(done + 1);
   }
   if (t == 0) {
-    bulk_store(a.t + tile, sm + L::oT, 2 * kBox);
-    if (a.p != nullptr) bulk_store(a.p + tile, sm + L::oP, 2 * kBox);
+    bulk_store(a.t + tile, sm + L::oT, kTTile);
+    if (a.p != nullptr) bulk_store(a.p + tile, sm + L::oP, kTTile);
     tma_store_commit();
     if (a.p != nullptr) tma_store_wait_read_all();
   }
@@ -176,14 +177,14 @@ __global__ void __launch_bounds__(128, PrepLayout<DP>::kPerSM)
     for (int h = 0; h < 4; ++h) {
       float2 v[8];
       tmem_ld16(t_pt + lane_base + 16 * h, v);
-      store16_split(sm + L::oP, sm + L::oP + kBox, t, 2 * h, v);
+      store16_split(sm + L::oP, kBox, t, 2 * h, v);
     }
   }
   tc_fence_before();
   fence_proxy_async_smem();
   __syncthreads();
   if (t == 0) {
-    bulk_store(a.pt + tile, sm + L::oP, 2 * kBox);
+    bulk_store(a.pt + tile, sm + L::oP, kTTile);
     tma_store_commit();
     tma_store_wait_read_all();
     if (*abort_flag) linger();
@@ -219,11 +220,15 @@ struct FwdLayout {
   static constexpr int kKQBox = 2 * kBox;               // 64 columns of K over Q: [128 x 64]
   static constexpr int kKQ = kBoxes * kKQBox;
   static constexpr int kT = 2 * kBox;                   // [T; P T] transposed, one part
-  static constexpr int oT = 2 * kKQ;                    // hi, lo (after two stages of K, Q)
-  static constexpr int oS = oT + 2 * kT;                // [DP x (hi | lo)]
-  static constexpr int oR = oS + DP * 128;              // [64 x (hi | lo)]
-  static constexpr int oU = oR + kBox;                  // the same of U (KEEP)
-  static constexpr int oG = oU + (KEEP ? kBox : 0);
+  static constexpr int oT = 2 * kKQ;                    // three (after two stages of K, Q)
+  static constexpr int oS = oT + 3 * kT;                // [DP x (first | second part)]
+  static constexpr int oR = oS + DP * 128;              // [64 x (first | second part)]
+  static constexpr int oX = oR + kBox;                  // [DP x (S's third | R's third)]
+  // fp32 copies on their way to memory (KEEP): U's may lie over S, done with when
+  // it is made, and at D <= 64 S's over R
+  static constexpr int oKeepU = oS;
+  static constexpr int oKeepS = DP == 64 ? oR : oX + DP * 128;
+  static constexpr int oG = KEEP && DP > 64 ? oKeepS + DP * 128 : oX + DP * 128;
   static constexpr int oBar = oG + 2 * (int)sizeof(GateSlot);
   static constexpr int kBytes = oBar + 128 + 1024;
   static constexpr int kPerSM = DP == 64 ? 2 : 1;
@@ -254,6 +259,10 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(kq_full + i, 1);
+    if (KEEP) {  // the first and last products, and the copies out of S and U
+      mbar_init(done, 2);
+      mbar_init(done + 2, 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -266,11 +275,11 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0), s_base = smem_u32(sm);
   const uint32_t lane_col = ((uint32_t)(warp % 4) << 21) + 16 * sub;
-  const uint32_t t_kqs = tmem, t_tr = tmem + 64;
   const uint32_t T_addr = s_base + L::oT, S_addr = s_base + L::oS, R_addr = s_base + L::oR;
-  uint8_t *S_tile = sm + L::oS, *R_tile = sm + L::oR;
-  constexpr uint32_t id_nt = idesc_bf16_f32(128, 64, 0, 1);  // A [rows x K], B [K x cols]
-  constexpr uint32_t id_tt = idesc_bf16_f32(128, 64, 1, 1);  // A [K x rows], B [K x cols]
+  const uint32_t S_third = s_base + L::oX, R_third = S_third + 64;
+  uint8_t *S_tile = sm + L::oS, *R_tile = sm + L::oR, *X_tile = sm + L::oX;
+  constexpr uint32_t id_nt = idesc_bf16_f32(128, 96, 0, 1);  // A [rows x K], B [K x cols]
+  constexpr uint32_t id_tt = idesc_bf16_f32(128, 96, 1, 1);  // A [K x rows], B [K x cols]
   const uint64_t once = policy_evict_first();
   auto load_kq = [&](int c) {
     uint64_t* bar = kq_full + (c & 1);
@@ -282,10 +291,10 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     }
   };
   auto load_t = [&](int c) {
-    const int64_t tile = (tile0 + c) * (2 * kBox);
-    mbar_arrive_expect_tx(t_full, 4 * kBox);
+    const int64_t tile = (tile0 + c) * kTTile;
+    mbar_arrive_expect_tx(t_full, 2 * kTTile);
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 3; ++h) {
       bulk_load(sm + L::oT + h * L::kT, a.t + tile + h * kBox, kBox, t_full);
       bulk_load(sm + L::oT + h * L::kT + kBox, a.pt + tile + h * kBox, kBox, t_full);
     }
@@ -340,7 +349,10 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
   for (int c = 0; c < n; ++c) {
     const uint32_t kq = s_base + (c & 1) * L::kKQ, phase = c & 1;
     const GateSlot* gs = gates + (c & 1);
-    if (t < DP) store_parts(S_tile, t, sub, S);
+    if (t < DP) {
+      store_parts(S_tile, X_tile, 0, t, sub, S);
+      if (KEEP) put_f32(sm + L::oKeepS, t, sub, S);
+    }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -349,33 +361,34 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<DP / 16, false, true>(el, t_kqs, kq, S_addr, id_nt, 16, 16, L::kKQBox, 0, true);
+      mma_tile<DP / 16, false, true>(el, tmem, kq, S_addr, id_nt, 16, S_third - S_addr, L::kKQBox, 0,
+                                     true);
       if (el) mma_commit(done);
     }
     const int64_t kept = (tile0 + c) * gridDim.y + blockIdx.y;
     if (KEEP && threadIdx.x == 128) {
-      bulk_store(a.keep_s + kept * (DP * 128), S_tile, DP * 128);
+      bulk_store(a.keep_s + kept * (DP * 128), sm + L::oKeepS, DP * 128);
       tma_store_commit();
+      tma_store_wait_read_all();
+      mbar_arrive(done);
     }
     wait_or_abort(done, phase, a.status, abort_flag);
     tc_fence_after();
     float2 x[8];
-    load16_sum(t_kqs + lane_col, x);
+    load16_sum(tmem + lane_col, x);
     if (t < 64) {
       const float2 b = both(gs->b[t]), bg = both(-gs->b[t] * gs->gam[t]);
       float2 v[8];
       unpack16(vv, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = fma2(bg, x[j], mul2(b, v[j]));
-      store_parts(R_tile, t, sub, x);
+      store_parts(R_tile, X_tile, 4, t, sub, x);
       if (c + 1 < n) load_v(c + 1);
     } else {
       const float2 gam = both(a.scale * gs->gam[t - 64]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = mul2(gam, x[j]);  // waits for P U
     }
-    // the copies out of the S and U tiles have read them
-    if (KEEP && threadIdx.x == 128) tma_store_wait_read_all();
     fence_proxy_async_smem();
     tc_fence_before();
     named_barrier_sync(1, 256);
@@ -384,8 +397,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
       __syncwarp();
       tc_fence_after();
       const uint32_t el = elect_one();
-      mma_tile<4, true, true>(el, t_tr, T_addr, R_addr, id_tt, kBox, 16, 0, 0, true);
-      mma_tile<4, true, true>(el, t_tr, T_addr + L::kT, R_addr, id_tt, kBox, 16, 0, 0, false);
+      mma_parts<true>(el, tmem, T_addr, L::kT, kBox, R_addr, R_third);
       if (el) mma_commit(done + 1);
     }
     wait_or_abort(done + 1, phase, a.status, abort_flag);
@@ -393,13 +405,13 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
     {
       const int64_t row = row0 + (int64_t)c * kCh + (t & 63);
       float2 r[8];
-      load16_sum(t_tr + lane_col, r);
+      load16_sum(tmem + lane_col, r);
       if (t < 64) {
-        if (KEEP) store_parts(sm + L::oU, t, sub, r);
+        if (KEEP) put_f32(sm + L::oKeepU, t, sub, r);
         const float2 del = both(gs->del[t]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = mul2(del, r[j]);
-        store_parts(R_tile, t, sub, r);
+        store_parts(R_tile, X_tile, 4, t, sub, r);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = add2(x[j], r[j]);
@@ -417,17 +429,19 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
       // K^T: 64 columns of K to a 64-lane block; with one such block the
       // lanes past 64 take Q's, and are not read
       constexpr uint32_t lbo = DP == 128 ? L::kKQBox : kBox;
-      mma_tile<4, true, true>(el, t_tr, kq, R_addr, id_tt, lbo, 16, 0, 0, true);
+      mma_tile<4, true, true>(el, tmem, kq, R_addr, id_tt, lbo, R_third - R_addr, 0, 0, true);
       if (el) mma_commit(done + 2);
     }
     if (KEEP && threadIdx.x == 128) {
-      bulk_store(a.keep_u + kept * kBox, sm + L::oU, kBox);
+      bulk_store(a.keep_u + kept * kBox, sm + L::oKeepU, kBox);
       tma_store_commit();
+      tma_store_wait_read_all();
+      mbar_arrive(done + 2);
     }
     wait_or_abort(done + 2, phase, a.status, abort_flag);
     tc_fence_after();
     const float2 last = both(gs->last.x), last_lo = both(gs->last.y);
-    load16_sum(t_tr + lane_col, x);
+    load16_sum(tmem + lane_col, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) S[j] = fma2(last, S[j], fma2(last_lo, S[j], x[j]));
   }
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kChainThreads, FwdLayout<DP, KEEP>::kPerSM)
 // Device scratch of a forward: P T, T when it is not kept, and the state
 // between pieces.
 size_t tiles_bytes(const DeltaShape& s) {
-  return (size_t)(s.B * s.H * ((s.N + kCh - 1) / kCh)) * 2 * kBox;
+  return (size_t)(s.B * s.H * ((s.N + kCh - 1) / kCh)) * kTTile;
 }
 
 // Pieces of the sequence: where the chain leaves half of the SMs idle, a
