@@ -781,6 +781,10 @@ def _delta_workspace(workspace: Optional[torch.Tensor], need: int, device) -> to
     # need not begin at zero
     if workspace is None:
         return torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
+    if workspace.device != device:
+        raise RuntimeError(f"workspace must be on {device}; got one on {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace
 
 
@@ -824,7 +828,7 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         _state_arg(state_in, (B, H, D, M), v.device, "state_in"),
         _state_arg(state_out, (B, H, D, M), v.device, "state_out"),
         0 if ckpt is None else ckpt.data_ptr(), 0 if ckpt is None else ckpt.numel() * 4,
-        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
+        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.nbytes,
         _raw_stream(stream, dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_fwd_delta")
@@ -890,7 +894,7 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         _state_arg(grad_state_out, shape, v.device, "grad_state_out"),
         *(t.data_ptr() for t in outs),
         _state_arg(grad_state_in, shape, v.device, "grad_state_in"),
-        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.numel(),
+        float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.nbytes,
         _raw_stream(stream, dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_bwd_delta")
@@ -1069,7 +1073,7 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     rc = lib.causal_product_qk_rope_bwd(
         *a.head, grad_q.data_ptr(), grad_k.data_ptr(), dxq.data_ptr(), dxk.data_ptr(),
         0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), *a.tail,
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, a.dev))
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, a.dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_qk_rope_bwd")
     return dxq, dxk, dwq, dwk
