@@ -726,11 +726,23 @@ def causal_product_noalloc_status(stream: Optional[torch.cuda.Stream] = None,
     return int(load_library().causal_product_noalloc_status(_stream_ptr(stream, dev)))
 
 
-def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+def _raw_stream(device: int) -> int:
     # (torch.cuda.current_stream builds a Stream object: 2 us of a 10 us step)
-    if stream is not None:
-        return int(stream.cuda_stream)
     return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _elsewhere(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+    """What a call on t's device has to enter first: the named stream, to which
+    what it allocates then belongs, or the device where it is not the current
+    one (a kernel starts on the current device).  None: nothing."""
+    device = t.get_device()
+    if stream is not None:
+        if device >= 0 and stream.device.index != device:
+            raise RuntimeError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+        return torch.cuda.stream(stream)
+    if device >= 0 and device != torch._C._cuda_getDevice():
+        return torch.cuda.device(device)
+    return None
 
 
 def _all_plain(device: int, *ts: torch.Tensor) -> bool:
@@ -803,8 +815,9 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     [B,H,D,M], None = zero).  Returns out, followed by S_N with
     ``return_state`` and by the checkpoints causal_product_bwd_delta needs with
     ``save`` (written into ``ckpt`` when given)."""
-    if stream is not None:  # what is allocated below belongs to it
-        with torch.cuda.stream(stream):
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
             return causal_product_fwd_delta(q, k, v, g, beta, out, workspace, None, state_in,
                                             return_state, state_out, scale, save, ckpt)
     B, H, Hk, N, D, M = _delta_dims(q, k, v, g, beta)
@@ -829,7 +842,7 @@ def causal_product_fwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         _state_arg(state_out, (B, H, D, M), v.device, "state_out"),
         0 if ckpt is None else ckpt.data_ptr(), 0 if ckpt is None else ckpt.numel() * 4,
         float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(stream, dev))
+        _raw_stream(dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_fwd_delta")
     got = (out,) + ((state_out,) if return_state else ()) + ((ckpt,) if save else ())
@@ -862,8 +875,9 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     for causal_product_fwd_delta(..., save=True) on the same inputs, ``ckpt``
     being the checkpoints it returned; with ``return_state_grad`` dL/dS_0
     follows.  dq and dk are summed over the value heads of a key head."""
-    if stream is not None:  # what is allocated below belongs to it
-        with torch.cuda.stream(stream):
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
             return causal_product_bwd_delta(q, k, v, g, beta, grad_out, ckpt, grad_q, grad_k, grad_v,
                                             grad_g, grad_beta, workspace, None, scale,
                                             grad_state_out, return_state_grad, grad_state_in)
@@ -895,7 +909,7 @@ def causal_product_bwd_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         *(t.data_ptr() for t in outs),
         _state_arg(grad_state_in, shape, v.device, "grad_state_in"),
         float(scale), B, H, Hk, N, D, M, code, workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(stream, dev))
+        _raw_stream(dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_bwd_delta")
     return tuple(outs) + ((grad_state_in,) if return_state_grad else ())
@@ -913,9 +927,10 @@ def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     state; one outside [0, P) is an idle row (out zero, no state touched).
     Without ``slots`` sequence b has state b.  No two sequences may share a
     slot."""
-    if stream is not None and out is None:
-        with torch.cuda.stream(stream):
-            return causal_product_decode_delta(q, k, v, g, beta, state, None, None, scale, slots)
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return causal_product_decode_delta(q, k, v, g, beta, state, out, None, scale, slots)
     qs, vs = q.shape, v.shape
     if (len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or qs[1] == 0
             or vs[1] % qs[1] != 0):
@@ -946,7 +961,7 @@ def causal_product_decode_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     rc = load_library().causal_product_decode_delta(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), out.data_ptr(),
         state.data_ptr(), 0 if slots is None else slots.data_ptr(), P, scale, B, H, Hk, D, M,
-        code, _raw_stream(stream, dev))
+        code, _raw_stream(dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_decode_delta")
     return out
@@ -1028,8 +1043,9 @@ def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torc
     sin (float32 [N,R/2] or [B,N,R/2]; None = no rotation).  xq and xk may be
     strided views (rows dense): a projection's ``x.view(B,N,H,D).transpose(1,
     2)`` is read in place.  q and k come dense."""
-    if stream is not None:  # what is allocated below belongs to it
-        with torch.cuda.stream(stream):
+    place = _elsewhere(xq, stream)
+    if place is not None:
+        with place:
             return causal_product_qk_rope(xq, xk, wq, wk, cos, sin, norm, eps, q, k)
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
     if q is None:
@@ -1041,7 +1057,7 @@ def causal_product_qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torc
     else:
         a.dense(k, a.k_shape, xq.dtype, "k")
     rc = load_library().causal_product_qk_rope(*a.head, q.data_ptr(), k.data_ptr(), *a.tail,
-                                               _raw_stream(stream, a.dev))
+                                               _raw_stream(a.dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_qk_rope")
     return q, k
@@ -1056,8 +1072,9 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     """(dxq, dxk, dwq, dwk) of L = <grad_q, q> + <grad_k, k> for
     causal_product_qk_rope; dxq and dxk dense, dwq and dwk None where the
     weight is."""
-    if stream is not None:  # what is allocated below belongs to it
-        with torch.cuda.stream(stream):
+    place = _elsewhere(xq, stream)
+    if place is not None:
+        with place:
             return causal_product_qk_rope_bwd(xq, xk, wq, wk, grad_q, grad_k, cos, sin, norm, eps,
                                               workspace)
     a = _QkRope(xq, xk, wq, wk, cos, sin, norm, eps)
@@ -1073,7 +1090,7 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     rc = lib.causal_product_qk_rope_bwd(
         *a.head, grad_q.data_ptr(), grad_k.data_ptr(), dxq.data_ptr(), dxk.data_ptr(),
         0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr(), *a.tail,
-        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, a.dev))
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(a.dev))
     if rc != CP_OK:
         raise CausalProductError(rc, "causal_product_qk_rope_bwd")
     return dxq, dxk, dwq, dwk
