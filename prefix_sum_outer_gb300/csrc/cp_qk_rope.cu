@@ -326,9 +326,11 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_kernel(Args a) {
                           BWD ? -1.f : 1.f);
       }
       const auto turn = [&](float2(&y8)[P][4]) {
-        if constexpr (FAST)
-          rotate8(y8, c, si);
-        else
+        if constexpr (FAST) {
+          // (what stands still is left alone: by a sine of 0, an infinite
+          // feature would make its neighbour in the lane NaN)
+          if (turned) rotate8(y8, c, si);
+        } else
           rotate8_any(y8[0], c, si, a.R, l, lanes);
       };
       T* to = y + (int64_t)q.out_row[u] * a.D;
