@@ -398,9 +398,9 @@ CP_API cp_status_t causal_product_bwd_favor(const void* xq, const void* xk, cons
  * causal_product_qk_rope leaves them with the norm the rule wants.
  *
  * State and sums are fp32.  bf16 with D <= 128 runs on the tensor cores, each
- * computed factor of a product as the sum of two bf16 numbers (16 bits) or
- * three; other shapes, fp32 and fp16 run on the CUDA cores in fp32.  Results
- * are bitwise reproducible.
+ * computed factor of a product as the sum of three bf16 numbers (24 bits), and
+ * is as exact as the other shapes, fp32 and fp16, which run on the CUDA cores in
+ * fp32.  Results are bitwise reproducible.
  *
  * Training: the forward leaves what the backward needs of it (the states
  * before its chunks of rows, and on the tensor cores the chunks' inverses) in

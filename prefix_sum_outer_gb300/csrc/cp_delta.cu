@@ -9,8 +9,9 @@
 // solve by substitution, a lane to a row.  Tiles lie so that both operands of a
 // product run along its contraction and load 16 bytes at a time; the rows of
 // the next chunk are loaded under the solve.  What bounds the walk is the
-// latency of its steps on the few SMs a small batch fills: about 12,000 cycles
-// a chunk, half of them issue slots (fp32, D = M = 64, 8 heads, N = 509: 107 us).
+// latency of its steps on the SMs that its heads fill: about 14,000 cycles a
+// chunk, half of those SMs' issue slots in use (fp32, D = M = 64, 8 heads, N = 509,
+// cold: 108 us on 32 SMs; 128 heads, N = 4096: 1.26 ms for a floor of 80 us).
 //
 // Backward: the same walk in reverse with the state's gradient in shared
 // memory, from the states the forward left before each chunk:
@@ -27,8 +28,8 @@
 // running totals, which would cancel.  Every gradient of q, k, b and g is a
 // sum over value columns, so the column blocks (and the value heads that share
 // a key head) leave fp32 parts that one more launch adds in a fixed order.
-// Bound as the forward is: fp32, D = M = 64, 8 heads, N = 509: 235 us, and 9 us
-// for the parts' sums.
+// Bound as the forward is: fp32, D = M = 64, 8 heads, N = 509, cold: 235 us, and 9
+// us for the parts' sums.
 #include <algorithm>
 
 #include "cp_delta.cuh"
@@ -712,9 +713,11 @@ __global__ void __launch_bounds__(256) delta_join_kernel(DeltaJoin x) {
 // Value columns of a CTA: 64 while the state's tiles and the row tiles fit the
 // shared memory (D <= 128), else 32; halved while the halves still get an SM
 // each: the walk's time is its own latency then, and the columns lengthen it.
-// (fp32, D = M = 64, N = 512, forward and gradients' kernels: 8 heads 106 + 266
-// us with 16 columns, 163 + 438 with 64; 64 heads 127 + 362 with 32, 163 + 442
-// with 64, 204 + 555 with 16, two turns of the SMs.)
+// (fp32, D = M = 64, N = 512, forward and backward calls back to back, the parts'
+// sums with the latter: 8 heads 102 + 233 us with 16 columns, 122 + 294 with 32,
+// 163 + 408 with 64; 64 heads 122 + 332 with 32, 163 + 410 with 64, 198 + 522 with
+// 16, two turns of the SMs.  The 64-column backward spills 72 to 76 bytes a thread,
+// the 64- and 32-column forward 4 to 16.)
 int block_cols(int64_t BH, int64_t D, int64_t M) {
   int mb = D <= 128 && M > 32 ? 64 : 32;
   while (mb > 16 && BH * ((M + mb / 2 - 1) / (mb / 2)) <= kPlanSMs) mb /= 2;

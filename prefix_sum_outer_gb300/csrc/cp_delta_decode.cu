@@ -4,12 +4,12 @@
 //     S'^T q = a S^T q + (k . q) u,
 // so both sums over the rows of S run while S is in registers and the state is
 // read and written once: 8 D M bytes per head, which bound the step.  The state's
-// decay is applied as hi + lo, for it is applied token after token (cp_delta.cuh).  A CTA
-// takes 32 value columns of one head, as 8 groups of four or, where rows are
-// not whole 16-byte pieces, one by one; its threads hold every row of them,
-// ROWS each.
+// decay is applied as hi + lo, for it is applied token after token (cp_delta.cuh).
+// A CTA takes 32 value columns of one head, as 8 groups of four or, where rows
+// are not whole 16-byte pieces, one by one; its threads hold every row of them,
+// ROWS each (64 rows, one by one at D > 64, take 255 registers and spill 16 bytes).
 //
-// bf16, B = 512, H = 16, D = M = 64: 47.5 us a step back to back, 5.7 TB/s; every
+// bf16, B = 512, H = 16, D = M = 64: 48.5 us a step back to back, 5.6 TB/s; every
 // store of a head waits for all of its loads, which the plain step's do not
 // (42.8 us for the same state).
 //

@@ -10,15 +10,16 @@
 //        T^T dU                         -> dX
 //        [K; Q]^T [-gam b dX; s gam dO]  -> dS = gam_C dS' + it, -> shared memory
 //    P^T dO of the next chunk is issued behind the last product; while that
-//    one runs, dX, dV = b dX and dX . V go out.  dU enters in three parts: P^T
-//    dO sums up to 64 rows, of which T^T leaves the differences when keys
-//    repeat, so dU's rounding is the largest error of dX.  It leaves dX and the
-//    dS' of every chunk as hi and lo parts.  Bound by its latency as the forward's
-//    is: B = 8, H = 16, N = 4096, D = M = 64, 213 us, 4.4 TB/s.
+//    one runs, dX, dV = b dX and dX . V go out.  It leaves dX and the dS' of
+//    every chunk in fp32.  T, P, the states and their third parts take 152 KB, one
+//    CTA to an SM.  Bound by its latency as the forward's is: B = 8, H = 16, N =
+//    4096, D = M = 64, 256 CTAs, two turns of the SMs, 350 us, 4.4 TB/s; B = 4, H =
+//    8, N = 1024, 64 CTAs, 41 us, 5.1k cycles a chunk.
 //
-// 2. The gradients, one CTA per head and chunk, all chunks at once: every factor
-//    comes as the operand tile that the chains left.  Lanes 0-63 are the rows of
-//    K, 64-127 those of Q:
+// 2. The gradients, one CTA per head and chunk, all chunks at once: the chains'
+//    fp32 tiles come by plain loads, a block of 32 value columns ahead, and are
+//    split into operand tiles here.  Lanes 0-63 are the rows of K, 64-127 those of
+//    Q:
 //        [dX; dO] U^T  -> Ma (A's part), Mq (P's part), by the decays
 //        [dX; dO] S^T,  U dS'^T,  [Ma; Mq] K,  Ma^T K + Mq^T Q
 //        dK = -gam b dX S^T + del U dS'^T + Ma K + Ma^T K + Mq^T Q
@@ -26,13 +27,13 @@
 //    and the sums for the gates (cp_delta.cu has the formulas):
 //        db_i = dX_i . U_i / b_i,                        where b_i is not 0,
 //             = dX_i . V_i - gam_i k_i . (S dX_i) + sum_j Ma_ij / b_i k_i.k_j
-//    (Ma / b is what is at hand), with dX . V from the chain.  The first is the
-//    diagonal of dX U^T; the second, its value at b_i = 0 too, is a difference
-//    of terms that nearly cancel when keys repeat.  Two CTAs fill an SM's tensor
-//    and shared memory (one at D > 64), and a CTA is a line of stages: 4k of its
-//    16k cycles are the products, 3k the copies, the rest the lanes' work, of
-//    which whatever can runs under the products.  B = 8, H = 16, N = 4096, D = M
-//    = 64: 252 us, 3.5 TB/s, 45 % of the issue slots.
+//    (Ma / b is what is at hand), with dX . V from the chain.  The first is summed
+//    in fp32 where the tiles are split; the second, its value at b_i = 0 too, is a
+//    difference of terms that nearly cancel when keys repeat.  Two CTAs fill an
+//    SM's tensor memory (one at D > 64, and where M > 64 leaves sums to hold in
+//    registers, 255 a thread and 4 bytes spilled), and a CTA is a line of stages,
+//    of which whatever can runs under the products.  B = 8, H = 16, N = 4096, D = M
+//    = 64: 318 us, 2.6 TB/s, 41 % of the issue slots, the tensor pipe 31 % active.
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"

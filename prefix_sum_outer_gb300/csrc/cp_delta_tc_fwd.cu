@@ -6,8 +6,8 @@
 //    A)^-1 by blocks, P T by MMA; the tiles of T, P T (and, for a backward, P)
 //    go to memory as they lie in shared memory.  A CTA's steps wait for one
 //    another, so what counts is CTAs to an SM: T lies over what it is made from
-//    and P T over P, in both memories, and six fit (D <= 64; four fit before,
-//    122 us).  B = 8, H = 16, N = 4096, D = 64, with P kept: 94 us, 5.1 TB/s.
+//    and P T over P, in both memories, and four fit.  B = 8, H = 16, N = 4096, D =
+//    64, with P kept: 158 us, 4.3 TB/s.
 //
 // 2. The chain.  A CTA walks one head's chunks of 64 rows for 32 value columns
 //    (columns never meet), two warpgroups of 16 columns each; lane d holds row
@@ -19,15 +19,15 @@
 //        K^T (del U)       -> S = gam_C S + it, -> shared memory
 //    P T in place of P takes a fourth dependent step (P U) off the chain and
 //    gives both products one 128-lane MMA.  The chain is bound by its own
-//    latency, some 550 cycles to a product of four MMAs and 150 to 250 to a
-//    conversion of 16 columns, so it is cut into few columns a CTA (64 columns
-//    took 4.6k cycles a chunk at D = 64).  Past 32 KB of instructions every one
-//    of them takes 3.1 cycles to fetch (measured): the two launches' work in
-//    one kernel, with a chunk's matrices made two ahead by warps beside the
-//    chain, took 7.4k cycles a chunk.  B = 8, H = 16, N = 4096, D = M = 64, two
-//    CTAs to an SM: 161 us with what a backward needs kept, 5.4 TB/s.  B = 4, H =
-//    8, N = 8229, D = 128, M = 64, 64 CTAs: 223 us, 3.3k cycles a chunk, in one
-//    piece.
+//    latency, 400 to 700 cycles to a product and 300 to 700 to a conversion of 16
+//    columns, so it is cut into few columns a CTA (64 columns took 4.6k cycles a
+//    chunk where 32 took 3.4k, with factors in two parts).  Past 32 KB of
+//    instructions every one of them takes 3.1 cycles to fetch (measured): the two
+//    launches' work in one kernel, with a chunk's matrices made two ahead by
+//    warps beside the chain, took 7.4k cycles a chunk.  B = 8, H = 16, N = 4096, D =
+//    M = 64, two CTAs to an SM: 204 us with what a backward needs kept, 5.5 TB/s.
+//    B = 4, H = 8, N = 8229, D = 128, M = 64, 64 CTAs: 297 us in four pieces, 4.5k
+//    cycles a chunk (4.0k where the copies' source is in L2).
 #include <algorithm>
 
 #include "cp_delta_tc.cuh"
@@ -467,8 +467,9 @@ size_t tiles_bytes(const DeltaShape& s) {
 
 // Pieces of the sequence: where the chain leaves half of the SMs idle, a
 // piece's matrices are made under the chain over the piece before, at a few
-// microseconds a piece (B = 4, H = 8, N = 8229, D = 128, M = 64: 254 us in four
-// pieces, 274 whole; B = 2, H = 8, N = 32768, D = M = 128: 896 in six, 969).
+// microseconds a piece (with factors in two parts, B = 4, H = 8, N = 8229, D =
+// 128, M = 64: 254 us in four pieces, 274 whole; B = 2, H = 8, N = 32768, D = M =
+// 128: 896 in six, 969; in three parts 302 and 1079, in as many pieces).
 int n_pieces(const DeltaShape& s) {
   const int64_t ctas = s.B * s.H * ((s.M + kCB - 1) / kCB), n = (s.N + kCh - 1) / kCh;
   if (ctas > kPlanSMs / 2) return 1;

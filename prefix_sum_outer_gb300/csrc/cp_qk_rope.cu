@@ -16,11 +16,16 @@
 // to a warp as fit, two turns of them at once (backward: one), and the next
 // ones loaded before these are worked on.  Where R or D is not a multiple of 16
 // a lane has eight features, asks for their partners by shuffle and takes twice
-// the turns (what follows at N = 2048: 33 + 55 us by pairs, with R = 40 80 + 123
-// us by shuffles).  Everything between the load and the store is fp32 and
-// rounded once.  bf16, B = 8, H = 16, N = 4096, D = R = 64, with weights:
-// forward 59 us, 4.6 TB/s, backward 96 us, 4.2 TB/s; registers hold the loads in
-// flight, two CTAs to an SM.
+// the turns (bf16, B = 8, H = 16, N = 2048, D = 64, cold: 33 + 54 us at R = 32, by
+// pairs, 78 + 120 us at R = 40, by shuffles).  Everything between the load and the
+// store is fp32 and rounded once.  bf16, B = 8, H = 16, N = 4096, D = 64, with
+// weights, cold: at R = 16 forward 60 us, backward 105 us, at R = 64 62 and 102 us,
+// 4.3 to 4.5 and 3.8 to 3.9 TB/s, and 5 us to join the weights' gradients.
+// Registers hold the loads in flight, two CTAs to an SM, and not all of them: rows
+// of fp32 take twice the registers of 16-bit ones at as many turns and spill 40
+// bytes a thread forward, 60 backward (B = 8, H = 16, N = 2048, D = R = 64: 49 + 81
+// us, 5.5 and 4.9 TB/s); the shuffles' copies spill 40 to 70 bytes for 16-bit rows,
+// 184 and 236 for fp32 ones.
 #include <algorithm>
 
 #include "cp_delta.cuh"
