@@ -494,6 +494,94 @@ CP_API cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* str
                                               void* workspace, size_t workspace_bytes,
                                               void* stream);
 
+/* Linear attention with a decay for each head: the causal product whose state
+ * decays by a constant factor per token.  For every (b, h), from S_0 (D x M, zero
+ * when absent), with a = e^{g_h}:
+ *     S_t = a S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t.
+ * q, k [B][Hk][N][D] in `dtype`, Hk a divisor of H: value head h reads key
+ * head h / (H / Hk).  v, out [B][H][N][M] in `dtype`; g (log decay, <= 0) [H]
+ * fp32; states [B][H][D][M] fp32.  D, M in [1, 256], multiples of 8 for bf16.
+ * Contiguous device pointers, 16-byte aligned (g, lengths: 4); outputs overlap
+ * nothing.  N = 0 passes the state through.
+ *
+ * g = 0 keeps everything (the causal product); g = -inf (and any below -120)
+ * keeps the token alone; a positive or NaN g makes that head's results NaN.  g is
+ * a constant: it has no gradient here.  A NaN or inf among a head's inputs
+ * reaches that head's later outputs, and may reach those of the same 128 rows.
+ *
+ * lengths ([B] int32, device; NULL: N each): sequence b is its first
+ * lengths[b] rows (taken into [0, N]); the rows behind them are padding, whose
+ * inputs reach nothing (NaN among them), whose outputs and gradients are zero;
+ * S_N is the state after the sequence's own last row.
+ *
+ * The backward writes the gradients of
+ *     L = <grad_out, out> + <grad_state_out, S_N>
+ * (grad_state_out NULL: zero) from the forward's own inputs, S_0 among them:
+ * grad_q, grad_k [B][Hk][N][D] (summed over the value heads that share a key
+ * head), grad_v, and grad_state_in = dL/dS_0 (NULL: not written).
+ *
+ * State and sums are fp32.  Results are bitwise reproducible.  Workspace:
+ * causal_product_decay_workspace_size bytes, or NULL (allocated and freed on
+ * `stream`).  Errors as causal_product_fwd; CP_ERR_INVALID_ARG too when Hk does
+ * not divide H or scale is not finite. */
+CP_API size_t causal_product_decay_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N,
+                                                  int64_t D, int64_t M, cp_dtype_t dtype,
+                                                  int backward);
+CP_API cp_status_t causal_product_fwd_decay(const void* q, const void* k, const void* v,
+                                            const float* g, void* out, const float* state_in,
+                                            float* state_out, const int32_t* lengths, float scale,
+                                            int64_t B, int64_t H, int64_t Hk, int64_t N, int64_t D,
+                                            int64_t M, cp_dtype_t dtype, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+CP_API cp_status_t causal_product_bwd_decay(const void* q, const void* k, const void* v,
+                                            const float* g, const void* grad_out,
+                                            const float* state_in, const float* grad_state_out,
+                                            void* grad_q, void* grad_k, void* grad_v,
+                                            float* grad_state_in, const int32_t* lengths,
+                                            float scale, int64_t B, int64_t H, int64_t Hk,
+                                            int64_t N, int64_t D, int64_t M, cp_dtype_t dtype,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of it for every (b, h), the state updated in place:
+ * causal_product_fwd_decay with N = 1.  q, k [B][Hk][D], v, out [B][H][M] in
+ * `dtype`; g [H] fp32.  state, slots and pool as
+ * causal_product_decode_delta's.  fp32 arithmetic for every dtype.  No
+ * workspace. */
+CP_API cp_status_t causal_product_decode_decay(const void* q, const void* k, const void* v,
+                                               const float* g, void* out, float* state,
+                                               const int32_t* slots, int64_t pool, float scale,
+                                               int64_t B, int64_t H, int64_t Hk, int64_t D,
+                                               int64_t M, cp_dtype_t dtype, void* stream);
+
+/* Layer norm: for every row x of C features, mu its mean,
+ *     y = (x - mu) r o w + b,   r = (mean (x - mu)^2 + eps)^-1/2.
+ * x: rows [B][H][N] of C dense features in `dtype`, at the strides (batch, head,
+ * row; elements, >= 0) given in stride_x.  w, b: [C], or [H][C] with per_head,
+ * in `dtype`; NULL for ones and zeros.  y: dense, [B][H][N][C] or with
+ * token_major [B][N][H][C] (the rows an output projection reads from a causal
+ * product's heads), 16-byte aligned.  C in [1, 32768], H at most 65535, fewer
+ * than 2^31 rows to a head; eps finite, >= 0 (with eps = 0 a constant row gives
+ * NaN).  fp32 arithmetic, rounded once.  Outputs overlap nothing.
+ *
+ * Backward, from grad_y (dense, laid out as y): grad_x, dense [B][H][N][C], and
+ * grad_w and grad_b (as w and b, in `dtype`; NULL: not written; grad_w only where
+ * there is a w), summed in a fixed order.  Workspace:
+ * causal_product_layer_norm_workspace_size bytes, or NULL (allocated on
+ * `stream`). */
+CP_API cp_status_t causal_product_layer_norm(const void* x, const int64_t* stride_x,
+                                             const void* w, const void* b, int per_head, void* y,
+                                             int token_major, float eps, int64_t B, int64_t H,
+                                             int64_t N, int64_t C, cp_dtype_t dtype, void* stream);
+CP_API size_t causal_product_layer_norm_workspace_size(int64_t B, int64_t H, int64_t N, int64_t C,
+                                                       cp_dtype_t dtype);
+CP_API cp_status_t causal_product_layer_norm_bwd(const void* x, const int64_t* stride_x,
+                                                 const void* w, int per_head, const void* grad_y,
+                                                 int token_major, void* grad_x, void* grad_w,
+                                                 void* grad_b, float eps, int64_t B, int64_t H,
+                                                 int64_t N, int64_t C, cp_dtype_t dtype,
+                                                 void* workspace, size_t workspace_bytes,
+                                                 void* stream);
+
 /* Size of the static device scratch array behind causal_product_fwd_noalloc. */
 #define CP_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 

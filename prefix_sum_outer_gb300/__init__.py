@@ -40,6 +40,9 @@ __all__ = [
     "causal_product_decode_delta", "causal_product_delta_workspace_size",
     "causal_product_delta_checkpoint_size",
     "causal_product_qk_rope", "causal_product_qk_rope_bwd", "qk_rope", "QK_NORMS",
+    "causal_product_fwd_decay", "causal_product_bwd_decay", "causal_product_decay",
+    "causal_product_decode_decay", "causal_product_decay_workspace_size",
+    "causal_product_layer_norm", "causal_product_layer_norm_bwd", "layer_norm",
     "causal_product_error_string", "library_path", "load_library",
 ]
 
@@ -176,6 +179,22 @@ def load_library(rebuild: bool = True) -> ctypes.CDLL:
             lib.causal_product_qk_rope_bwd.argtypes = ([p, p64, p, p64, p, p, p, p, i64] + [p] * 6
                                                        + [c_int, f32] + [i64] * 6 + [c_int, p, sz, p])
             lib.causal_product_qk_rope_bwd.restype = c_int
+            lib.causal_product_decay_workspace_size.argtypes = [i64] * 6 + [c_int, c_int]
+            lib.causal_product_decay_workspace_size.restype = sz
+            lib.causal_product_fwd_decay.argtypes = [p] * 8 + [f32] + [i64] * 6 + [c_int, p, sz, p]
+            lib.causal_product_fwd_decay.restype = c_int
+            lib.causal_product_bwd_decay.argtypes = [p] * 12 + [f32] + [i64] * 6 + [c_int, p, sz, p]
+            lib.causal_product_bwd_decay.restype = c_int
+            lib.causal_product_decode_decay.argtypes = [p] * 7 + [i64, f32] + [i64] * 5 + [c_int, p]
+            lib.causal_product_decode_decay.restype = c_int
+            lib.causal_product_layer_norm.argtypes = ([p, p64, p, p, c_int, p, c_int, f32] + [i64] * 4
+                                                      + [c_int, p])
+            lib.causal_product_layer_norm.restype = c_int
+            lib.causal_product_layer_norm_workspace_size.argtypes = [i64] * 4 + [c_int]
+            lib.causal_product_layer_norm_workspace_size.restype = sz
+            lib.causal_product_layer_norm_bwd.argtypes = ([p, p64, p, c_int, p, c_int] + [p] * 3 + [f32]
+                                                          + [i64] * 4 + [c_int, p, sz, p])
+            lib.causal_product_layer_norm_bwd.restype = c_int
             lib.causal_product_status.argtypes = [p, p]
             lib.causal_product_status.restype = c_int
             lib.causal_product_error_string.argtypes = [c_int]
@@ -1096,6 +1115,281 @@ def causal_product_qk_rope_bwd(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[
     return dxq, dxk, dwq, dwk
 
 
+def _decay_dims(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                lengths: Optional[torch.Tensor]):
+    qs, vs = q.shape, v.shape
+    if (len(qs) != 4 or k.shape != qs or len(vs) != 4 or vs[0] != qs[0] or vs[2] != qs[2]
+            or qs[1] == 0 or vs[1] % qs[1] != 0):
+        raise ValueError(f"expected q,k [B,Hk,N,D] and v [B,H,N,M], H a multiple of Hk; got "
+                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
+    B, Hk, N, D = qs
+    H, M = vs[1], vs[3]
+    if log_decay.shape != (H,) or log_decay.dtype is not torch.float32:
+        _check_like(log_decay, (H,), torch.float32, "log_decay")
+    if lengths is not None:
+        _check_like(lengths, (B,), torch.int32, "lengths")
+        _check_plain(v.get_device(), v, lengths)
+    return B, H, Hk, N, D, M
+
+
+def causal_product_decay_workspace_size(B: int, H: int, Hk: int, N: int, D: int, M: int,
+                                        dtype: torch.dtype = torch.bfloat16,
+                                        backward: bool = False) -> int:
+    """Workspace bytes of causal_product_fwd_decay / _bwd_decay."""
+    return int(load_library().causal_product_decay_workspace_size(B, H, Hk, N, D, M, _DTYPES[dtype],
+                                                                  int(bool(backward))))
+
+
+def causal_product_fwd_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             log_decay: torch.Tensor, out: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None,
+                             state_in: Optional[torch.Tensor] = None, return_state: bool = False,
+                             state_out: Optional[torch.Tensor] = None, scale: float = 1.0,
+                             lengths: Optional[torch.Tensor] = None):
+    """Linear attention with a decay for each head: S_t = a S_{t-1} + k_t v_t^T
+    with a = exp(log_decay[h]); out_t = scale S_t^T q_t.
+
+    q, k: [B,Hk,N,D]; v: [B,H,N,M], value head h reading key head h // (H //
+    Hk); log_decay: float32 [H], at most 0 (a positive or NaN one makes its
+    head's results NaN; -inf keeps the token alone); ``state_in`` is S_0
+    (float32 [B,H,D,M], None = zero).  ``lengths`` (int32 [B], on the device):
+    sequence b is its first lengths[b] rows; rows behind them reach nothing and
+    give zero.  Returns out, with ``return_state`` followed by the state after
+    each sequence's last row."""
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return causal_product_fwd_decay(q, k, v, log_decay, out, workspace, None, state_in,
+                                            return_state, state_out, scale, lengths)
+    B, H, Hk, N, D, M = _decay_dims(q, k, v, log_decay, lengths)
+    code = _dtype_code(q, k, v)
+    dev = v.get_device()
+    if out is None:
+        _check_plain(dev, q, k, v, log_decay)
+        out = torch.empty_like(v)
+    else:
+        _check_like(out, (B, H, N, M), v.dtype, "out")
+        _check_plain(dev, q, k, v, log_decay, out)
+    if return_state and state_out is None:
+        state_out = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
+    lib = load_library()
+    need = lib.causal_product_decay_workspace_size(B, H, Hk, N, D, M, code, 0)
+    workspace = _delta_workspace(workspace, need, v.device)
+    rc = lib.causal_product_fwd_decay(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), out.data_ptr(),
+        _state_arg(state_in, (B, H, D, M), v.device, "state_in"),
+        _state_arg(state_out, (B, H, D, M), v.device, "state_out"),
+        0 if lengths is None else lengths.data_ptr(), float(scale), B, H, Hk, N, D, M, code,
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_fwd_decay")
+    return (out, state_out) if return_state else out
+
+
+def causal_product_bwd_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             log_decay: torch.Tensor, grad_out: torch.Tensor,
+                             grad_q: Optional[torch.Tensor] = None,
+                             grad_k: Optional[torch.Tensor] = None,
+                             grad_v: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None,
+                             state_in: Optional[torch.Tensor] = None,
+                             grad_state_out: Optional[torch.Tensor] = None,
+                             return_state_grad: bool = False,
+                             grad_state_in: Optional[torch.Tensor] = None, scale: float = 1.0,
+                             lengths: Optional[torch.Tensor] = None):
+    """(dq, dk, dv) of L = <grad_out, out> + <grad_state_out, S_N> for
+    causal_product_fwd_decay on the same inputs (nothing is kept from it); with
+    ``return_state_grad`` dL/dS_0 follows.  dq and dk are summed over the value
+    heads of a key head; rows behind a sequence's length get zero."""
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return causal_product_bwd_decay(q, k, v, log_decay, grad_out, grad_q, grad_k, grad_v,
+                                            workspace, None, state_in, grad_state_out,
+                                            return_state_grad, grad_state_in, scale, lengths)
+    B, H, Hk, N, D, M = _decay_dims(q, k, v, log_decay, lengths)
+    code = _dtype_code(q, k, v, grad_out)
+    if grad_out.shape != v.shape:
+        raise ValueError("grad_out must have v's shape")
+    outs = []
+    for t, ref, name in ((grad_q, q, "grad_q"), (grad_k, k, "grad_k"), (grad_v, v, "grad_v")):
+        t = torch.empty_like(ref) if t is None else t
+        _check_like(t, ref.shape, ref.dtype, name)
+        outs.append(t)
+    dev = v.get_device()
+    _check_plain(dev, q, k, v, log_decay, grad_out, *outs)
+    if return_state_grad and grad_state_in is None:
+        grad_state_in = torch.empty((B, H, D, M), dtype=torch.float32, device=v.device)
+    lib = load_library()
+    need = lib.causal_product_decay_workspace_size(B, H, Hk, N, D, M, code, 1)
+    workspace = _delta_workspace(workspace, need, v.device)
+    shape = (B, H, D, M)
+    rc = lib.causal_product_bwd_decay(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), grad_out.data_ptr(),
+        _state_arg(state_in, shape, v.device, "state_in"),
+        _state_arg(grad_state_out, shape, v.device, "grad_state_out"),
+        *(t.data_ptr() for t in outs),
+        _state_arg(grad_state_in, shape, v.device, "grad_state_in"),
+        0 if lengths is None else lengths.data_ptr(), float(scale), B, H, Hk, N, D, M, code,
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_bwd_decay")
+    return tuple(outs) + ((grad_state_in,) if return_state_grad else ())
+
+
+def causal_product_decode_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                log_decay: torch.Tensor, state: torch.Tensor,
+                                out: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None, scale: float = 1.0,
+                                slots: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of linear attention with a decay for each head, the state
+    updated in place.
+
+    q, k: [B,Hk,D]; v: [B,H,M]; log_decay: float32 [H]; state: float32
+    [P,H,D,M].  ``slots`` (int32 [B], on the device) names each sequence's
+    state; one outside [0, P) is an idle row (out zero, no state touched).
+    Without ``slots`` sequence b has state b.  No two sequences may share a
+    slot."""
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return causal_product_decode_decay(q, k, v, log_decay, state, out, None, scale, slots)
+    qs, vs = q.shape, v.shape
+    if (len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0] or qs[1] == 0
+            or vs[1] % qs[1] != 0):
+        raise ValueError(f"expected q,k [B,Hk,D] and v [B,H,M], H a multiple of Hk; got "
+                         f"{tuple(qs)}, {tuple(k.shape)}, {tuple(vs)}")
+    B, Hk, D = qs
+    _, H, M = vs
+    code = _dtype_code(q, k, v)
+    if log_decay.shape != (H,) or log_decay.dtype is not torch.float32:
+        _check_like(log_decay, (H,), torch.float32, "log_decay")
+    dev = q.get_device()
+    if out is None:
+        _check_plain(dev, q, k, v, log_decay, state)
+        out = torch.empty_like(v)
+    else:
+        _check_like(out, vs, v.dtype, "out")
+        _check_plain(dev, q, k, v, log_decay, state, out)
+    ss = state.shape
+    if len(ss) != 4 or ss[1:] != (H, D, M) or state.dtype is not torch.float32:
+        _check_like(state, (ss[0] if len(ss) == 4 else 0, H, D, M), torch.float32, "state")
+    P = ss[0]
+    if slots is not None:
+        _check_like(slots, (B,), torch.int32, "slots")
+        _check_plain(dev, q, slots)
+    elif P < B:
+        raise ValueError(f"state holds {P} sequences, fewer than the {B} of this call")
+    rc = load_library().causal_product_decode_decay(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), out.data_ptr(),
+        state.data_ptr(), 0 if slots is None else slots.data_ptr(), P, scale, B, H, Hk, D, M,
+        code, _raw_stream(dev))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_decode_decay")
+    return out
+
+
+def _layer_norm_args(x, weight, bias, token_major):
+    """(rows as the C ABI takes them, their (B,H,N,C), dtype code, device,
+    whether the weights are per head, the result's shape) of a layer norm."""
+    xs, st = x.shape, x.stride()
+    n = len(xs)
+    if not 2 <= n <= 4 or (token_major and n != 4):
+        raise ValueError(f"expected x [R,C], [B,N,C] or [B,H,N,C] (with token_major: [B,H,N,C]); "
+                         f"got {tuple(xs)}")
+    C = xs[-1]
+    if n == 2:
+        dims, strides = (1, 1, xs[0], C), (0, 0, st[0])
+    elif n == 3:
+        dims, strides = (xs[0], 1, xs[1], C), (st[0], 0, st[1])
+    else:
+        dims, strides = tuple(xs), st[:3]
+    code = _dtype_code(x)
+    dev = x.get_device()
+    if dev < 0:
+        raise RuntimeError("causal_product runs on CUDA tensors only (no CPU path)")
+    if st[-1] != 1 and C > 1:
+        raise ValueError("the rows of x must be dense (stride 1 in the last dimension)")
+    per_head = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype is not x.dtype:
+            _dtype_code(x, t)
+        wide = n == 4 and t.shape == (xs[1], C)
+        if not wide and t.shape != (C,):
+            raise ValueError(f"{name} must have shape ({C},) or, for x [B,H,N,C], (H, {C}); got "
+                             f"{tuple(t.shape)}")
+        if per_head is not None and per_head != wide:
+            raise ValueError("weight and bias must have one shape")
+        per_head = wide
+        if not _all_plain(dev, t):
+            _check_device(t)
+            raise RuntimeError("all tensors must be on the same CUDA device")
+    shape = (xs[0], xs[2], xs[1], C) if token_major else tuple(xs)
+    return (x.data_ptr(), _Strides(*strides)), dims, code, dev, int(bool(per_head)), shape
+
+
+def causal_product_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                              bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                              token_major: bool = False, out: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Layer norm of the rows of x ([R,C], [B,N,C] or a causal product's heads
+    [B,H,N,C]) over their C features, times ``weight`` plus ``bias`` ([C], or
+    [H,C] for weights of each head; None = ones, zeros).  x may be a strided view
+    (rows dense).  The result is dense: x's shape, or with ``token_major``
+    [B,N,H,C], the rows an output projection reads."""
+    place = _elsewhere(x, stream)
+    if place is not None:
+        with place:
+            return causal_product_layer_norm(x, weight, bias, eps, token_major, out)
+    rows, dims, code, dev, per_head, shape = _layer_norm_args(x, weight, bias, token_major)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _check_like(out, shape, x.dtype, "out")
+        _check_plain(dev, out)
+    rc = load_library().causal_product_layer_norm(
+        *rows, 0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+        per_head, out.data_ptr(), int(bool(token_major)), eps, *dims, code, _raw_stream(dev))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_layer_norm")
+    return out
+
+
+def causal_product_layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor],
+                                  bias: Optional[torch.Tensor], grad_out: torch.Tensor,
+                                  eps: float = 1e-5, token_major: bool = False,
+                                  workspace: Optional[torch.Tensor] = None,
+                                  stream: Optional[torch.cuda.Stream] = None):
+    """(dx, dweight, dbias) of L = <grad_out, y> for causal_product_layer_norm;
+    dx dense in x's shape, dweight and dbias None where the argument is."""
+    place = _elsewhere(x, stream)
+    if place is not None:
+        with place:
+            return causal_product_layer_norm_bwd(x, weight, bias, grad_out, eps, token_major,
+                                                 workspace)
+    rows, dims, code, dev, per_head, shape = _layer_norm_args(x, weight, bias, token_major)
+    _check_like(grad_out, shape, x.dtype, "grad_out")
+    _check_plain(dev, grad_out)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    lib = load_library()
+    need = lib.causal_product_layer_norm_workspace_size(*dims, code)
+    workspace = _delta_workspace(workspace, need, x.device)
+    rc = lib.causal_product_layer_norm_bwd(
+        *rows, 0 if weight is None else weight.data_ptr(), per_head, grad_out.data_ptr(),
+        int(bool(token_major)), dx.data_ptr(), 0 if dw is None else dw.data_ptr(),
+        0 if db is None else db.data_ptr(), eps, *dims, code, workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev))
+    if rc != CP_OK:
+        raise CausalProductError(rc, "causal_product_layer_norm_bwd")
+    return dx, dw, db
+
+
 class CausalProduct(torch.autograd.Function):
     """Autograd wrapper: forward and backward both call the C ABI; the
     forward keeps checkpoints of the state for the backward's dq scans."""
@@ -1263,6 +1557,75 @@ def qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor] = Non
             sin: Optional[torch.Tensor] = None, norm: str = "rms", eps: float = 1e-6):
     """causal_product_qk_rope with autograd support for xq, xk, wq and wk."""
     return QkRope.apply(xq, xk, wq, wk, cos, sin, norm, eps)
+
+
+class CausalProductDecay(torch.autograd.Function):
+    """Autograd wrapper of linear attention with a decay for each head: (q, k,
+    v, S_0) -> (out, S_N), the decay a constant."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, state, scale, lengths):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        log_decay = log_decay.contiguous()
+        state = None if state is None else state.contiguous()
+        out, s_n = causal_product_fwd_decay(q, k, v, log_decay, state_in=state, return_state=True,
+                                            scale=scale, lengths=lengths)
+        ctx.save_for_backward(q, k, v, log_decay, state, lengths)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, s_n
+
+    @staticmethod
+    def backward(ctx, go, gs):
+        q, k, v, log_decay, state, lengths = ctx.saved_tensors
+        go = torch.zeros_like(v) if go is None else go.contiguous().to(v.dtype)
+        gs = None if gs is None else gs.contiguous().float()
+        d = causal_product_bwd_decay(q, k, v, log_decay, go, state_in=state, grad_state_out=gs,
+                                     return_state_grad=state is not None, scale=ctx.scale,
+                                     lengths=lengths)
+        return d[:3] + (None, d[3] if state is not None else None, None, None)
+
+
+def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         log_decay: torch.Tensor, state: Optional[torch.Tensor] = None,
+                         return_state: bool = False, scale: float = 1.0,
+                         lengths: Optional[torch.Tensor] = None):
+    """Linear attention with a decay for each head, with autograd support for q,
+    k, v and the state (causal_product_fwd_decay); with ``return_state`` the
+    result is (out, state after each sequence's last row).  The decay is a
+    constant: one that asks for a gradient is refused."""
+    if torch.is_grad_enabled():
+        if log_decay.requires_grad:
+            raise ValueError("log_decay is a constant of the head; it has no gradient")
+        if any(t is not None and t.requires_grad for t in (q, k, v, state)):
+            out, s_n = CausalProductDecay.apply(q, k, v, log_decay, state, scale, lengths)
+            return (out, s_n) if return_state else out
+    return causal_product_fwd_decay(q.contiguous(), k.contiguous(), v.contiguous(),
+                                    log_decay.contiguous(),
+                                    state_in=None if state is None else state.contiguous(),
+                                    return_state=return_state, scale=scale, lengths=lengths)
+
+
+class LayerNorm(torch.autograd.Function):
+    """Autograd wrapper of the layer norm."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, token_major):
+        ctx.save_for_backward(x, weight, bias)
+        ctx.eps, ctx.token_major = eps, token_major
+        return causal_product_layer_norm(x, weight, bias, eps, token_major)
+
+    @staticmethod
+    def backward(ctx, gy):
+        x, weight, bias = ctx.saved_tensors
+        return causal_product_layer_norm_bwd(x, weight, bias, gy.contiguous().to(x.dtype), ctx.eps,
+                                             ctx.token_major) + (None, None)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5, token_major: bool = False):
+    """causal_product_layer_norm with autograd support for x, weight and bias."""
+    return LayerNorm.apply(x, weight, bias, eps, token_major)
 
 
 def causal_product(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

@@ -1362,3 +1362,240 @@ cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* stride_q, 
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------ a decay for each head
+namespace cp {
+namespace {
+
+cp_status_t check_decay(const DecayShape& s) {
+  const cp_status_t st = check_dims(s.B, s.H, s.N, s.D, s.M, s.dtype);
+  if (st != CP_OK) return st;
+  if (s.Hk <= 0 || s.H % s.Hk != 0 || !std::isfinite(s.scale)) return CP_ERR_INVALID_ARG;
+  // a sequence's rows and a launch's CTAs are counted in 32 bits
+  if (s.N > (int64_t)INT32_MAX || s.B * s.H > (int64_t)INT32_MAX / std::max<int64_t>(256, s.N / 64 + 1))
+    return CP_ERR_UNSUPPORTED_SHAPE;
+  return CP_OK;
+}
+
+size_t decay_ws_bytes(const DecayShape& s, bool backward) {
+  if (s.N == 0) return kStatusBytes;
+  return kStatusBytes + round_up(decay_simt_scratch(s, backward));
+}
+
+// Sizes in bytes of one call's tensors.
+struct DecayBytes {
+  size_t qk, vo, g, state, lengths;
+  explicit DecayBytes(const DecayShape& s) {
+    const size_t es = s.dtype == CP_DTYPE_F32 ? 4 : 2;
+    qk = (size_t)s.B * s.Hk * s.N * s.D * es;
+    vo = (size_t)s.B * s.H * s.N * s.M * es;
+    g = (size_t)s.H * sizeof(float);
+    state = (size_t)s.B * s.H * s.D * s.M * sizeof(float);
+    lengths = (size_t)s.B * sizeof(int32_t);
+  }
+};
+
+}  // namespace
+}  // namespace cp
+
+extern "C" {
+
+size_t causal_product_decay_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int64_t D,
+                                           int64_t M, cp_dtype_t dtype, int backward) {
+  const cp::DecayShape s{B, H, Hk, N, D, M, dtype, 1.f, nullptr};
+  return cp::check_decay(s) == CP_OK ? cp::decay_ws_bytes(s, backward != 0) : 0;
+}
+
+cp_status_t causal_product_fwd_decay(const void* q, const void* k, const void* v, const float* g,
+                                     void* out, const float* state_in, float* state_out,
+                                     const int32_t* lengths, float scale, int64_t B, int64_t H,
+                                     int64_t Hk, int64_t N, int64_t D, int64_t M, cp_dtype_t dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream_) {
+  const cp::DecayShape s{B, H, Hk, N, D, M, dtype, scale, lengths};
+  cp_status_t st = cp::check_decay(s);
+  if (st != CP_OK) return st;
+  if (N > 0 && (!q || !k || !v || !g || !out)) return CP_ERR_INVALID_ARG;
+  const cp::DecayBytes n(s);
+  const cp::Span in[6] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {state_in, n.state}, {g, n.g},
+                          {lengths, n.lengths}};
+  const cp::Span outs[2] = {{out, n.vo}, {state_out, n.state}};
+  const cp::Span wide[4] = {in[0], in[1], in[2], in[3]};
+  if (!cp::all_aligned(wide) || !cp::all_aligned(outs) || !cp::aligned4(g) ||
+      !cp::aligned4(lengths))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::decay_ws_bytes(s, false);
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) return cp::pass_state(state_in, state_out, n.state, stream);
+  cp::Scratch sc;
+  st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+  if (st != CP_OK) return st;
+  void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  const cp::DecayFwd f{q, k, v, g, state_in, out, state_out};
+  return cp::decay_simt_fwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_bwd_decay(const void* q, const void* k, const void* v, const float* g,
+                                     const void* grad_out, const float* state_in,
+                                     const float* grad_state_out, void* grad_q, void* grad_k,
+                                     void* grad_v, float* grad_state_in, const int32_t* lengths,
+                                     float scale, int64_t B, int64_t H, int64_t Hk, int64_t N,
+                                     int64_t D, int64_t M, cp_dtype_t dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream_) {
+  const cp::DecayShape s{B, H, Hk, N, D, M, dtype, scale, lengths};
+  cp_status_t st = cp::check_decay(s);
+  if (st != CP_OK) return st;
+  if (N > 0 && (!q || !k || !v || !g || !grad_out || !grad_q || !grad_k || !grad_v))
+    return CP_ERR_INVALID_ARG;
+  const cp::DecayBytes n(s);
+  const cp::Span in[8] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {grad_out, n.vo}, {state_in, n.state},
+                          {grad_state_out, n.state}, {g, n.g}, {lengths, n.lengths}};
+  const cp::Span outs[4] = {{grad_q, n.qk}, {grad_k, n.qk}, {grad_v, n.vo},
+                            {grad_state_in, n.state}};
+  const cp::Span wide[6] = {in[0], in[1], in[2], in[3], in[4], in[5]};
+  if (!cp::all_aligned(wide) || !cp::all_aligned(outs) || !cp::aligned4(g) ||
+      !cp::aligned4(lengths))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::decay_ws_bytes(s, true);
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) return cp::pass_state(grad_state_out, grad_state_in, n.state, stream);
+  cp::Scratch sc;
+  st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+  if (st != CP_OK) return st;
+  void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  const cp::DecayBwd f{q,      k,      v,      g,      grad_out, state_in, grad_state_out,
+                       grad_q, grad_k, grad_v, grad_state_in};
+  return cp::decay_simt_bwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_decode_decay(const void* q, const void* k, const void* v,
+                                        const float* g, void* out, float* state,
+                                        const int32_t* slots, int64_t pool, float scale, int64_t B,
+                                        int64_t H, int64_t Hk, int64_t D, int64_t M,
+                                        cp_dtype_t dtype, void* stream) {
+  const cp::DecayShape s{B, H, Hk, 1, D, M, dtype, scale, nullptr};
+  const cp_status_t st = cp::check_decay(s);
+  if (st != CP_OK) return st;
+  if (!q || !k || !v || !g || !out || !state || pool < 1 || (!slots && pool < B))
+    return CP_ERR_INVALID_ARG;
+  const cp::DecayBytes n(s);
+  const cp::Span in[5] = {{q, n.qk}, {k, n.qk}, {v, n.vo}, {g, n.g}, {slots, n.lengths}};
+  const cp::Span outs[2] = {{out, n.vo}, {state, (size_t)pool * H * D * M * sizeof(float)}};
+  const cp::Span wide[3] = {in[0], in[1], in[2]};
+  if (!cp::all_aligned(wide) || !cp::all_aligned(outs) || !cp::aligned4(g) || !cp::aligned4(slots))
+    return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const cp::DecayDecode f{q, k, v, g, slots, out, state, pool};
+  return cp::decay_decode_launch(s, f, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ layer norm
+namespace cp {
+namespace {
+
+cp_status_t check_layer_norm(const LayerNorm& f) {
+  if (f.B <= 0 || f.H <= 0 || f.N < 0) return CP_ERR_INVALID_ARG;
+  if (f.dtype != CP_DTYPE_F32 && f.dtype != CP_DTYPE_BF16 && f.dtype != CP_DTYPE_F16)
+    return CP_ERR_UNSUPPORTED_DTYPE;
+  if (f.C < 1 || f.C > kLayerNormMaxC) return CP_ERR_UNSUPPORTED_SHAPE;
+  // rows are counted in 32 bits, and heads are one dimension of a grid
+  if (f.H > 65535 || f.B > (int64_t)1 << 31 || f.N > (int64_t)1 << 31 ||
+      f.B * f.N >= (int64_t)1 << 31)
+    return CP_ERR_UNSUPPORTED_SHAPE;
+  if (!(f.eps >= 0.f) || !std::isfinite(f.eps)) return CP_ERR_INVALID_ARG;
+  return CP_OK;
+}
+
+}  // namespace
+}  // namespace cp
+
+extern "C" {
+
+size_t causal_product_layer_norm_workspace_size(int64_t B, int64_t H, int64_t N, int64_t C,
+                                                cp_dtype_t dtype) {
+  cp::LayerNorm f{};
+  f.B = B; f.H = H; f.N = N; f.C = C; f.dtype = dtype;
+  if (cp::check_layer_norm(f) != CP_OK) return 0;
+  return cp::kStatusBytes + cp::round_up(cp::layer_norm_scratch(f));
+}
+
+cp_status_t causal_product_layer_norm(const void* x, const int64_t* stride_x, const void* w,
+                                      const void* b, int per_head, void* y, int token_major,
+                                      float eps, int64_t B, int64_t H, int64_t N, int64_t C,
+                                      cp_dtype_t dtype, void* stream) {
+  cp::LayerNorm f{};
+  f.x = x; f.w = w; f.b = b; f.y = y; f.B = B; f.H = H; f.N = N; f.C = C;
+  f.per_head = per_head != 0; f.token_major = token_major != 0; f.eps = eps; f.dtype = dtype;
+  const cp_status_t st = cp::check_layer_norm(f);
+  if (st != CP_OK) return st;
+  if (!stride_x) return CP_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (stride_x[i] < 0) return CP_ERR_INVALID_ARG;
+    f.stride[i] = stride_x[i];
+  }
+  if (N > 0 && (!x || !y)) return CP_ERR_INVALID_ARG;
+  const size_t es = dtype == CP_DTYPE_F32 ? 4 : 2;
+  const size_t nw = (size_t)(f.per_head ? H : 1) * C * es;
+  const cp::Span in[3] = {{x, cp::strided_bytes(stride_x, B, H, N, C, es)}, {w, nw}, {b, nw}};
+  const cp::Span outs[1] = {{y, (size_t)B * H * N * C * es}};
+  for (const void* p : {x, w, b})
+    if ((reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0) return CP_ERR_MISALIGNED;
+  if (!cp::all_aligned(outs)) return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  if (N == 0) return CP_OK;
+  return cp::layer_norm_launch(f, nullptr, false, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+cp_status_t causal_product_layer_norm_bwd(const void* x, const int64_t* stride_x, const void* w,
+                                          int per_head, const void* grad_y, int token_major,
+                                          void* grad_x, void* grad_w, void* grad_b, float eps,
+                                          int64_t B, int64_t H, int64_t N, int64_t C,
+                                          cp_dtype_t dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream_) {
+  cp::LayerNorm f{};
+  f.x = x; f.w = w; f.gy = grad_y; f.dx = grad_x; f.dw = grad_w; f.db = grad_b;
+  f.B = B; f.H = H; f.N = N; f.C = C;
+  f.per_head = per_head != 0; f.token_major = token_major != 0; f.eps = eps; f.dtype = dtype;
+  cp_status_t st = cp::check_layer_norm(f);
+  if (st != CP_OK) return st;
+  if (!stride_x) return CP_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (stride_x[i] < 0) return CP_ERR_INVALID_ARG;
+    f.stride[i] = stride_x[i];
+  }
+  if (N > 0 && (!x || !grad_y || !grad_x)) return CP_ERR_INVALID_ARG;
+  if (grad_w != nullptr && w == nullptr) return CP_ERR_INVALID_ARG;
+  const size_t es = dtype == CP_DTYPE_F32 ? 4 : 2, n = (size_t)B * H * N * C * es;
+  const size_t nw = (size_t)(f.per_head ? H : 1) * C * es;
+  const cp::Span in[3] = {{x, cp::strided_bytes(stride_x, B, H, N, C, es)}, {w, nw}, {grad_y, n}};
+  const cp::Span outs[3] = {{grad_x, n}, {grad_w, nw}, {grad_b, nw}};
+  for (const void* p : {x, w, (const void*)grad_w, (const void*)grad_b})
+    if ((reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0) return CP_ERR_MISALIGNED;
+  if (!cp::aligned16(grad_y) || !cp::aligned16(grad_x)) return CP_ERR_MISALIGNED;
+  if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
+  const size_t need = cp::kStatusBytes + cp::round_up(cp::layer_norm_scratch(f));
+  if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (N == 0) {
+    // no rows: the weights' gradients are sums of nothing
+    for (void* p : {grad_w, grad_b})
+      if (p != nullptr && cudaMemsetAsync(p, 0, nw, stream) != cudaSuccess) return CP_ERR_CUDA;
+    return CP_OK;
+  }
+  cp::Scratch sc;
+  st = cp::acquire(sc, workspace, workspace_bytes, need, stream);
+  if (st != CP_OK) return st;
+  void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
+  return cp::layer_norm_launch(f, area, true, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+}  // extern "C"

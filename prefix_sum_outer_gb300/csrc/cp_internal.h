@@ -312,6 +312,62 @@ struct QkRope {
 size_t qk_rope_scratch(const QkRope& f);
 cudaError_t qk_rope_launch(const QkRope& f, void* scratch, bool backward, cudaStream_t stream);
 
+// ---- linear attention with a decay for each head: S_t = a S_{t-1} + k_t v_t^T,
+// out_t = scale S_t^T q_t, a = e^{g_h}.  Layouts as the delta rule's; g is [H]
+// fp32, lengths [B] (rows of each sequence; null: N).
+struct DecayShape {
+  int64_t B, H, Hk, N, D, M;
+  cp_dtype_t dtype;
+  float scale;
+  const int* lengths;
+};
+struct DecayFwd {
+  const void *q, *k, *v;
+  const float *g, *state_in;  // state_in may be null (zero)
+  void* out;
+  float* state_out;           // may be null
+};
+struct DecayBwd {
+  const void *q, *k, *v;
+  const float* g;
+  const void* grad_out;
+  const float *state_in, *grad_state_out;  // may be null (zero)
+  void *dq, *dk, *dv;
+  float* grad_state_in;                    // may be null
+};
+struct DecayDecode {
+  const void *q, *k, *v;
+  const float* g;
+  const int* slots;  // [B], or null: sequence b has state b
+  void* out;
+  float* state;      // [pool][H][D][M]
+  int64_t pool;
+};
+// CUDA-core path (any dtype)
+size_t decay_simt_scratch(const DecayShape& s, bool backward);
+cudaError_t decay_simt_fwd(const DecayShape& s, const DecayFwd& f, void* scratch,
+                           cudaStream_t stream);
+cudaError_t decay_simt_bwd(const DecayShape& s, const DecayBwd& f, void* scratch,
+                           cudaStream_t stream);
+cudaError_t decay_decode_launch(const DecayShape& s, const DecayDecode& f, cudaStream_t stream);
+
+// ---- layer norm of rows of C features; forward: y from x; backward: dx, dw and
+// db from x and gy, through layer_norm_scratch bytes
+struct LayerNorm {
+  const void *x, *w, *b, *gy;  // w, b may be null
+  void *y, *dx, *dw, *db;      // dw, db may be null (not wanted)
+  int64_t stride[3];           // batch, head, row strides of x (elements)
+  int64_t B, H, N, C;
+  bool per_head;               // w and b are [H][C], else [C]
+  bool token_major;            // y and gy are [B][N][H][C], else [B][H][N][C]
+  float eps;
+  cp_dtype_t dtype;
+};
+constexpr int64_t kLayerNormMaxC = 32768;
+size_t layer_norm_scratch(const LayerNorm& f);
+cudaError_t layer_norm_launch(const LayerNorm& f, void* scratch, bool backward,
+                              cudaStream_t stream);
+
 // ---- failure-path self-test: records CP_ERR_TIMEOUT after `wait_ns`
 cudaError_t selftest_timeout_launch(int* status, uint64_t wait_ns, cudaStream_t stream);
 
