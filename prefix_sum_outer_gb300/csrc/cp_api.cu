@@ -1379,7 +1379,8 @@ cp_status_t check_decay(const DecayShape& s) {
 
 size_t decay_ws_bytes(const DecayShape& s, bool backward) {
   if (s.N == 0) return kStatusBytes;
-  return kStatusBytes + round_up(decay_simt_scratch(s, backward));
+  return kStatusBytes + round_up(decay_tc_supported(s) ? decay_tc_scratch(s, backward)
+                                                       : decay_simt_scratch(s, backward));
 }
 
 // Sizes in bytes of one call's tensors.
@@ -1433,6 +1434,8 @@ cp_status_t causal_product_fwd_decay(const void* q, const void* k, const void* v
   if (st != CP_OK) return st;
   void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
   const cp::DecayFwd f{q, k, v, g, state_in, out, state_out};
+  if (cp::decay_tc_supported(s))
+    return cp::decay_tc_fwd(s, f, area, static_cast<int*>(sc.base), stream);
   return cp::decay_simt_fwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -1468,6 +1471,8 @@ cp_status_t causal_product_bwd_decay(const void* q, const void* k, const void* v
   void* area = static_cast<char*>(sc.base) + cp::kStatusBytes;
   const cp::DecayBwd f{q,      k,      v,      g,      grad_out, state_in, grad_state_out,
                        grad_q, grad_k, grad_v, grad_state_in};
+  if (cp::decay_tc_supported(s))
+    return cp::decay_tc_bwd(s, f, area, static_cast<int*>(sc.base), stream);
   return cp::decay_simt_bwd(s, f, area, stream) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

@@ -34,8 +34,21 @@ __device__ __forceinline__ float power(float g, int n) {
   return fmaf(expf(x), fmaf(g, (float)n, -x), expf(x));
 }
 __device__ __forceinline__ float2 power_parts(float g, int n) {
-  const float x = g * (float)n;
-  return decay_parts(x, fmaf(g, (float)n, -x));
+  float x = g * (float)n, f = fmaf(g, (float)n, -x);
+  // decay_parts knows its lo for |x| < 0.34; a state of more than that a step
+  // still remembers a few steps, so its power is squared up from a smaller one
+  int k = 0;
+  while (x < -0.3f && k < 8) {
+    x *= 0.5f;
+    f *= 0.5f;
+    ++k;
+  }
+  float2 p = decay_parts(x, f);
+  for (; k > 0; --k) {
+    const float h = p.x * p.x;
+    p = make_float2(h, fmaf(p.x, p.x, -h) + 2.f * p.x * p.y);
+  }
+  return p;
 }
 // rows of sequence b
 __device__ __forceinline__ int64_t rows_of(const int* lengths, int64_t b, int64_t N) {

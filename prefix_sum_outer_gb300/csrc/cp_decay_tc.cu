@@ -1,0 +1,960 @@
+// Linear attention with a decay for each head on the 5th-generation tensor cores
+// (bf16, D and M at most 128; formulas in cp_decay.cuh).
+//
+// Forward, and each of the backward's dq, dv and dk, is one product of three row
+// arrays a, b, c with a state (DA x DC), walked in tiles of 128 rows, forward or
+// in reverse.  With S the fp32 state before tile t and w_ij = e^{g |i - j|}:
+//     P   = w o A_t B_t^T           masked to the tile's causal triangle
+//     C'  = (e^{g (127 - r)} c_r)   the tile's rows as the state takes them
+//     O_t = P C_t + (e^{g (r + 1)}) o (A_t S)
+//     S   = e^{128 g} S + B_t^T C'
+// Nothing in a tile but A S waits for the state, and the state's update is one
+// fma, so the tiles stream through a pipeline of warps:
+//   warp 0        TMA producer: B tiles into one ring, A and C boxes into another
+//   warps 1..3    MMA issuers: B^T C'; A B^T and A S; P C
+//   warps 4..7    state group: fp32 S in registers (thread = row); its hi + lo
+//                 copy, the operand of A S
+//   warps 8..11   P group: P times its powers, masked, hi + lo, back into TMEM
+//   warps 12..15  O group: O from its two accumulators, to bf16, TMA store
+//   warps 16..19  C' group: a row times its power, as two or three bf16 numbers
+// A CTA walks one piece of one head's sequence for 64 columns of c.
+//
+// Precision.  S lives in registers in fp32 and takes each tile's B^T C' by an fma
+// that rounds to nearest, its decay as hi + lo: an accumulator kept in tensor
+// memory would be rounded toward zero at every MMA and lose 1e-5 of a state that
+// remembers thousands of rows.  Where the state itself is a result (S_N, dS_0) C'
+// is three bf16 numbers, all 24 bits; for bf16 results two (2^-17) are far below
+// their rounding, as they are for P and for S as an operand.
+//
+// Powers come from a table of e^{g n}, n <= 128, of products in shared memory: a
+// 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
+// e^{g (31 - (j - j0))}, two numbers at most 1, one per row and one per column.
+//
+// Sequences of few heads are cut into pieces: the same kernel with the output
+// left out (AGG) sums each piece's B^T C', a prefix launch turns the sums into
+// the states the pieces start from, and the pieces run side by side.
+#include <algorithm>
+#include <atomic>
+
+#include "cp_decay.cuh"
+#include "cp_delta_tc.cuh"
+
+namespace cp {
+namespace {
+
+using namespace decay;
+using namespace cp::ptx;
+using tc::kBoxBytes;
+using tc::kSmemLimit;
+using tc::kTile;
+using tc::record_timeout;
+using tc::sw128_offset;
+
+constexpr int kMB = 64;   // columns of c to a CTA
+constexpr int kBarBytes = 1024, kTableBytes = 1024;
+constexpr int kNP = 2;    // buffers of P
+constexpr uint32_t kHi = desc_hi(1024);
+
+struct Args {
+  const float* g;
+  const int* lengths;
+  const float* state_in;   // may be null (zero)
+  float* state_out;        // may be null
+  float* slots;            // [problems][G][DP][64]: sums, then the pieces' first states
+  float* out_f32;          // not null: the result goes here in fp32, [BH][N][DC]
+  int* status;
+  int64_t N, st_r, st_c;   // strides of a state's rows and columns
+  int H, Hk, group, BH, n_mb, n_tiles, seg_tiles, G;
+  int DA, DC;
+  int a_key, b_key, c_key, o_key;   // whether an array has key heads
+  int reverse;
+  float s_p, s_o, s_c;     // factors of P, of A S and of C'
+};
+
+// PARTS: bf16 numbers to an element of C'
+template <int DP, int PARTS, bool AGG>
+struct Layout {
+  static constexpr int kABoxes = DP / 64;
+  static constexpr int kBStage = kABoxes * kBoxBytes;
+  static constexpr int kBoxesPerTile = AGG ? 1 : kABoxes + 1;  // of the A / C ring
+  static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
+  static constexpr int kHalf = kBoxBytes / 2;                  // a part of half a tile's C'
+  static constexpr int kTotal = (kSmemLimit - 1024 - kBarBytes - kTableBytes) / kBoxBytes;  // boxes
+  static constexpr int NSB = DP == 64 ? 2 : 1;                 // copies of S
+  static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
+  static constexpr int NB = DP == 64 ? 3 : 2;                  // stages of the B ring
+  static constexpr int kOBoxes = AGG ? 0 : 1;
+  static constexpr int R =
+      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - PARTS - kOBoxes;
+  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes + PARTS + kOBoxes;
+  static constexpr int kSmem = kBoxes * kBoxBytes + kBarBytes + kTableBytes + 1024;
+  static constexpr int kVGroup = AGG ? 8 : 16;                 // first warp of the C' group
+  static constexpr int kThreads = 32 * (kVGroup + 4);
+  static constexpr int kSWarps = DP / 32;                      // warps that hold state rows
+  // tensor memory: P, A S, P C, and B^T C' as [hi | rest]
+  static constexpr int kColO1 = kNP * 128, kColO2 = kColO1 + kMB;
+  static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
+  static constexpr int kCols = AGG ? 128 : 512;
+  static_assert(R >= kBoxesPerTile, "a tile does not fit");
+  static_assert(kSmem <= kSmemLimit && kColS + 128 <= kCols, "no room");
+};
+
+// hi = bf16(x), and x - hi
+__device__ __forceinline__ uint32_t split_hi(float2& x) {
+  const uint32_t h = tc::pack_bf16x2(x.x, x.y);
+  x = sub2(x, make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)));
+  return h;
+}
+
+// the upper halves of two floats, as two bf16 numbers
+__device__ __forceinline__ uint32_t upper(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+// the first 8 bits of x as bf16 (cut off, not rounded), and what is left
+__device__ __forceinline__ uint32_t cut_hi(float2& x) {
+  const uint32_t h = upper(x);
+  x = sub2(x, make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                          __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)));
+  return h;
+}
+
+// Twenty warps walk eight different pieces of code, so what stalls them first is
+// the instruction cache: loops stay rolled, and a wait is a few instructions, its
+// limit a count (a try takes tens of nanoseconds to a microsecond, so a third of a
+// second at least) and not a clock's.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint32_t tries = 0;
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag != 0 || ++tries > (1u << 24)) return false;
+  return true;
+}
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <int DP, int PARTS, bool AGG>
+__global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
+    decay_tc_kernel(const __grid_constant__ CUtensorMap tm_a,
+                    const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_c,
+                    const __grid_constant__ CUtensorMap tm_o, const Args a) {
+  using L = Layout<DP, PARTS, AGG>;
+  constexpr int NB = L::NB, R = L::R, BPT = L::kBoxesPerTile, NSB = L::NSB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_tiles(smem_raw);
+  uint8_t* b_ring = smem;                            // [NB] B tiles
+  uint8_t* ring = b_ring + NB * L::kBStage;          // [R] boxes: a tile's A, then its C
+  uint8_t* vp = ring + R * kBoxBytes;                // [PARTS] C'
+  uint8_t* s_tile = vp + PARTS * kBoxBytes;          // [NSB] hi | lo copies of S
+  uint8_t* o_tile = s_tile + L::kSBoxes * kBoxBytes;
+  uint64_t* full_b = reinterpret_cast<uint64_t*>(o_tile + L::kOBoxes * kBoxBytes);
+  uint64_t* empty_b = full_b + NB;
+  uint64_t* full = empty_b + NB;       // [R]
+  uint64_t* empty = full + R;          // [R]
+  uint64_t* p_done = empty + R;        // [kNP] A B^T in TMEM
+  uint64_t* p_ready = p_done + kNP;    // [kNP] P packed
+  uint64_t* pc_done = p_ready + kNP;   // [kNP] P C done: the buffer is free
+  uint64_t* s_ready = pc_done + kNP;   // [2] copy of S written
+  uint64_t* as_done = s_ready + 2;     // [2] A S done: the copy is free
+  uint64_t* o1_done = as_done + 2;     // A S
+  uint64_t* o2_done = o1_done + 1;     // P C
+  uint64_t* o_free = o2_done + 1;      // both read
+  uint64_t* vp_ready = o_free + 1;     // [2] half of C' written
+  uint64_t* vp_free = vp_ready + 2;    // [2] its products done
+  uint64_t* kv_done = vp_free + 2;     // B^T C' in TMEM
+  uint64_t* kv_free = kv_done + 1;     // B^T C' read
+  uint64_t* fixed = kv_free + 1;       // rows past the sequence's end cleared
+  uint64_t* fin = fixed + 1;           // [3]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(fin + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(fin + 4);
+  float* pw = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full_b) + kBarBytes);  // [129]
+  float* cf = pw + 132;                // [32] a chunk's column powers
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int idx = blockIdx.x;
+  const int mb = idx % a.n_mb;
+  idx /= a.n_mb;
+  const int bh = idx % a.BH;
+  int seg = idx / a.BH;
+  if (AGG && a.reverse) seg += 1;  // the first piece in scan order needs no sum of others
+  const int b = bh / a.H, h = bh % a.H;
+  const bool rev = a.reverse != 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&full_b[i], 1);
+      mbar_init(&empty_b[i], AGG ? 1 : 2);
+    }
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], AGG ? 1 : 2);
+    }
+    for (int i = 0; i < kNP; ++i) {
+      mbar_init(&p_done[i], 1);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&pc_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_ready[i], L::kSWarps);
+      mbar_init(&as_done[i], 1);
+    }
+    mbar_init(o1_done, 1);
+    mbar_init(o2_done, 1);
+    mbar_init(o_free, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&vp_ready[i], 1);
+      mbar_init(&vp_free[i], 1);
+    }
+    mbar_init(kv_done, 1);
+    mbar_init(kv_free, L::kSWarps);
+    mbar_init(fixed, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_c);
+    if (!AGG) {
+      tma_prefetch_desc(&tm_a);
+      tma_prefetch_desc(&tm_o);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, L::kCols);
+    tmem_relinquish();
+  }
+  grid_dep_wait();  // what the kernel before this one wrote is visible from here
+  const float g = head_decay(a.g[h]);
+  if (threadIdx.x <= kTile) pw[threadIdx.x] = power(g, threadIdx.x);
+  if (threadIdx.x >= 160 && threadIdx.x < 192) {
+    const int c = threadIdx.x - 160;
+    cf[c] = power(g, rev ? c : 31 - c);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int wq = warp & 3, row = wq * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+
+  // ---- the piece's tiles: those that hold rows, in scan order
+  const int64_t rows = rows_of(a.lengths, b, a.N);
+  const int live = (int)((rows + kTile - 1) / kTile);
+  const int t_first = seg * a.seg_tiles, t_stop = min(a.n_tiles, t_first + a.seg_tiles);
+  const int t_end = max(t_first, min(t_stop, live));
+  const int n_it = t_end - t_first;
+  auto tile_of = [&](int it) { return rev ? t_end - 1 - it : t_first + it; };
+  auto rows_in = [&](int tile) { return tile == live - 1 ? (int)(rows - (int64_t)tile * kTile) : kTile; };
+  // the gradient of S_N is seen from the last row itself, other states from the
+  // row behind the tile
+  auto shift = [&](int tile) { return rev && tile == live - 1 ? 1 : 0; };
+  // tiles whose B^T C' is wanted: not the last of a piece that hands nothing on
+  const bool last_seg = rev ? seg == 0 : seg == a.G - 1;
+  const bool hands_on = AGG || (last_seg && a.state_out != nullptr);
+  const int n_kv = hands_on ? n_it : n_it - 1;
+
+  if (warp < 4) {
+    if constexpr (!AGG) fewer_registers<56>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        const uint64_t pol = AGG ? policy_evict_last() : policy_evict_first();
+        const int hk = b * a.Hk + h / a.group;
+        const int ia = a.a_key ? hk : bh, ib = a.b_key ? hk : bh, ic = a.c_key ? hk : bh;
+        bool ok = true;
+        int it = 0;
+#pragma unroll 1
+        for (; it < n_it && ok; ++it) {
+          const int row0 = tile_of(it) * kTile;
+#pragma unroll 1
+          for (int x = 0; x <= BPT && ok; ++x) {
+            // the tile's C, its B, its A
+            const int j = it * BPT + (x == 0 ? 0 : x - 1), st = x == 1 ? it % NB : j % R;
+            const int turn = x == 1 ? it / NB : j / R;
+            ok = turn == 0 || wait(x == 1 ? &empty_b[st] : &empty[st], (turn - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (x == 1) {
+              mbar_arrive_expect_tx(&full_b[st], L::kBStage);
+#pragma unroll
+              for (int y = 0; y < L::kABoxes; ++y)
+                tma_load_3d(b_ring + st * L::kBStage + y * kBoxBytes, &tm_b, &full_b[st], y * 64,
+                            row0, ib, pol);
+            } else {
+              mbar_arrive_expect_tx(&full[st], kBoxBytes);
+              tma_load_3d(ring + st * kBoxBytes, x == 0 ? &tm_c : &tm_a, &full[st],
+                          x == 0 ? mb * kMB : (x - 2) * 64, row0, x == 0 ? ic : ia, pol);
+            }
+          }
+        }
+        if (!ok) record_timeout(a.status, abort_flag);
+        if (*abort_flag) {
+          // let the copies already issued land before the CTA's memory goes
+          // away: all but the last of a ring's were waited for by their users
+          // or land with it; a barrier without a copy just runs out
+          for (int i = 0; i < NB && i < n_it; ++i) {
+            const int j = max(0, it - 1 - i);
+            mbar_wait_timeout(&full_b[j % NB], (j / NB) & 1, CP_WAIT_TIMEOUT_NS / 64);
+          }
+          for (int i = 0; i < R && i < n_it * BPT; ++i) {
+            const int j = max(0, it * BPT - 1 - i);
+            mbar_wait_timeout(&full[j % R], (j / R) & 1, CP_WAIT_TIMEOUT_NS / 64);
+          }
+        }
+      }
+    } else if (lane == 0 && (warp == 1 || !AGG)) {
+      // ------------------------------------------------------- MMA issuers
+      constexpr uint32_t idesc_p = idesc_bf16_f32(128, 128, 0, 0);   // A . B^T
+      constexpr uint32_t idesc_s2 = idesc_bf16_f32(128, 128, 1, 1);  // B^T . [C'_1 | C'_2]
+      constexpr uint32_t idesc_s1 = idesc_bf16_f32(128, kMB, 1, 1);  // B^T . C'_3
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, kMB, 0, 1);   // A . S, P . C
+      auto b_addr = [&](int it) { return smem_u32(b_ring + (it % NB) * L::kBStage); };
+      // a tile's boxes in the ring: C, then A
+      auto box = [&](int it, int x) { return (it * BPT + x) % R; };
+      auto box_phase = [&](int it, int x) { return ((it * BPT + x) / R) & 1; };
+      auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
+      bool ok = true;
+      if (warp == 1) {
+        // B^T C', half a tile's rows at a time
+        for (int it = 0; it < n_kv && ok; ++it) {
+          ok = wait(&full_b[it % NB], (it / NB) & 1, abort_flag) &&
+               (it == 0 || wait(kv_free, (it - 1) & 1, abort_flag)) &&
+               (!tail(it) || wait(fixed, 0, abort_flag));
+          // (A = B^T, 128 rows of it: past a 64-wide B's own the next bytes,
+          // whose lanes nobody reads)
+          const uint32_t bt_lo = desc_lo(b_addr(it), kBoxBytes);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!ok || !wait(&vp_ready[half], it & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t v_lo = desc_lo(smem_u32(vp + half * PARTS * L::kHalf), L::kHalf);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              mma_ss_lo<kHi, kHi>(tmem + L::kColS, bt_lo + ((half * 8192 + kk * 2048) >> 4),
+                                  v_lo + ((kk * 2048) >> 4), idesc_s2, (half | kk) > 0);
+            if constexpr (PARTS == 3)
+#pragma unroll
+              for (int kk = 0; kk < kTile / 32; ++kk)
+                mma_ss_lo<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((half * 8192 + kk * 2048) >> 4),
+                                    v_lo + ((2 * L::kHalf + kk * 2048) >> 4), idesc_s1, 1u);
+            mma_commit(&vp_free[half]);
+          }
+          if (!ok) break;
+          mma_commit(kv_done);
+          mma_commit(&empty_b[it % NB]);
+        }
+      } else if (warp == 2) {
+        // A B^T, as far ahead as there are buffers, and A S: whichever can go
+        int nP = 0, nQ = 0;
+        uint32_t idle = 0;
+#pragma unroll 1
+        while (nQ < n_it) {
+          ++idle;
+          if (nP < n_it && mbar_test_wait(&full[box(nP, BPT - 1)], box_phase(nP, BPT - 1)) &&
+              (nP < kNP || mbar_test_wait(&pc_done[nP % kNP], ((nP - kNP) / kNP) & 1)) &&
+              (!tail(nP) || mbar_test_wait(fixed, 0))) {
+            // (the other boxes and B were asked for before the last box)
+            ok = wait(&full_b[nP % NB], (nP / NB) & 1, abort_flag);
+#pragma unroll
+            for (int x = 1; x < BPT - 1; ++x)
+              ok = ok && wait(&full[box(nP, x)], box_phase(nP, x), abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t t_p = tmem + (nP % kNP) * 128;
+            const uint32_t k_lo = desc_lo(b_addr(nP), 16);
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+              const uint32_t in = ((kk & 3) * 32) >> 4;
+              mma_ss_lo<kHi, kHi>(
+                  t_p, desc_lo(smem_u32(ring + box(nP, 1 + (kk >> 2)) * kBoxBytes), 16) + in,
+                  k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0);
+            }
+            mma_commit(&p_done[nP % kNP]);
+            mma_commit(&empty_b[nP % NB]);
+#pragma unroll
+            for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(nP, x)]);
+            ++nP;
+            idle = 0;
+          }
+          if (nQ < nP && mbar_test_wait(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
+              (nQ == 0 || mbar_test_wait(o_free, (nQ - 1) & 1))) {
+            tc_fence_after();
+            const uint32_t s_lo = desc_lo(smem_u32(s_tile + (nQ % NSB) * 2 * L::kSOne), L::kSOne);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < DP / 16; ++kk)
+                mma_ss_lo<kHi, kHi>(
+                    tmem + L::kColO1,
+                    desc_lo(smem_u32(ring + box(nQ, 1 + (kk >> 2)) * kBoxBytes), 16) +
+                        (((kk & 3) * 32) >> 4),
+                    s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0);
+            mma_commit(&as_done[nQ % NSB]);
+            mma_commit(o1_done);
+#pragma unroll
+            for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(nQ, x)]);
+            ++nQ;
+            idle = 0;
+          }
+          if (idle > 0) __nanosleep(20);
+          if (*abort_flag || idle > (1u << 24)) {
+            ok = false;
+            break;
+          }
+        }
+      } else {
+        // P C
+        for (int it = 0; it < n_it && ok; ++it) {
+          const int bf = it % kNP, x = box(it, 0);
+          ok = wait(&p_ready[bf], (it / kNP) & 1, abort_flag) &&
+               wait(&full[x], box_phase(it, 0), abort_flag) &&
+               (it == 0 || wait(o_free, (it - 1) & 1, abort_flag)) &&
+               (!tail(it) || wait(fixed, 0, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t c_lo = desc_lo(smem_u32(ring + x * kBoxBytes), kBoxBytes);
+          // 32 columns of P: hi in their first 16 TMEM columns, lo in the next,
+          // two j to a column
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ts_lo<kHi>(tmem + L::kColO2,
+                             tmem + bf * 128 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                             c_lo + ((kk * 2048) >> 4), idesc_o, (part | kk) > 0);
+          mma_commit(&pc_done[bf]);
+          mma_commit(o2_done);
+          mma_commit(&empty[x]);
+        }
+      }
+      if (!ok) record_timeout(a.status, abort_flag);
+      // every MMA this thread issued completes before TMEM is released
+      mma_commit(&fin[warp - 1]);
+      mbar_wait_timeout(&fin[warp - 1], 0, CP_WAIT_TIMEOUT_NS);
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------- state group
+    if constexpr (!AGG) more_registers<136>();
+    if (wq < L::kSWarps) {
+      const int pidx = bh * a.n_mb + mb;
+      float* slot = a.slots + ((int64_t)pidx * a.G + seg) * DP * kMB + row * kMB;
+      float2 S[kMB / 2];
+      const bool first_seg = rev ? seg == a.G - 1 : seg == 0;
+      if (!AGG && !first_seg) {
+#pragma unroll
+        for (int x = 0; x < kMB / 4; ++x) {
+          const float4 f = reinterpret_cast<const float4*>(slot)[x];
+          S[2 * x] = make_float2(f.x, f.y);
+          S[2 * x + 1] = make_float2(f.z, f.w);
+        }
+      } else {
+        const bool on = !AGG && a.state_in != nullptr && row < a.DA;
+        const float* s = a.state_in + (int64_t)bh * a.DA * a.DC + row * a.st_r;
+        const int m0 = mb * kMB;
+#pragma unroll
+        for (int x = 0; x < kMB / 2; ++x) {
+          S[x].x = on && m0 + 2 * x < a.DC ? s[(m0 + 2 * x) * a.st_c] : 0.f;
+          S[x].y = on && m0 + 2 * x + 1 < a.DC ? s[(m0 + 2 * x + 1) * a.st_c] : 0.f;
+        }
+      }
+      const float2 full_step = power_parts(g, kTile);
+      bool ok = true;
+      for (int it = 0; it < n_it; ++it) {
+        if constexpr (!AGG) {
+          const int sb = it % NSB;
+          uint8_t* sbuf = s_tile + sb * 2 * L::kSOne;
+          // the A S that last read this copy has completed
+          if (it >= NSB && !wait(&as_done[sb], ((it - NSB) / NSB) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < kMB / 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float2 s = S[4 * c + x];
+              hi[x] = split_hi(s);
+              lo[x] = tc::pack_bf16x2(s.x, s.y);
+            }
+            const uint32_t off = sw128_offset(row, 8 * c, 0);
+            *reinterpret_cast<uint4*>(sbuf + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(sbuf + L::kSOne + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_ready[sb]);
+        }
+        if (it < n_kv) {
+          const int tile = tile_of(it), nv = rows_in(tile);
+          const float2 f = nv == kTile && shift(tile) == 0 ? full_step : power_parts(g, nv - shift(tile));
+          if (!wait(kv_done, it & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kMB / 16; ++c) {
+            uint32_t p[16], q[16];
+            tmem_ld16(lane_base + L::kColS + 16 * c, p);
+            tmem_ld16(lane_base + L::kColS + kMB + 16 * c, q);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              float2& s = S[8 * c + x];
+              const float2 t = add2(make_float2(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1])),
+                                    make_float2(__uint_as_float(q[2 * x]), __uint_as_float(q[2 * x + 1])));
+              s = fma2(both(f.x), s, fma2(both(f.y), s, t));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_free);
+        }
+      }
+      if (!ok) record_timeout(a.status, abort_flag);
+      if (AGG && ok && n_it > 0) {
+#pragma unroll
+        for (int x = 0; x < kMB / 4; ++x)
+          reinterpret_cast<float4*>(slot)[x] =
+              make_float4(S[2 * x].x, S[2 * x].y, S[2 * x + 1].x, S[2 * x + 1].y);
+      }
+      if (!AGG && ok && hands_on && row < a.DA) {
+        if (rev && live > 0) {
+          const float2 f = power_parts(g, 1);
+#pragma unroll
+          for (int x = 0; x < kMB / 2; ++x) S[x] = fma2(both(f.x), S[x], mul2(both(f.y), S[x]));
+        }
+        float* s = a.state_out + (int64_t)bh * a.DA * a.DC + row * a.st_r;
+        const int m0 = mb * kMB;
+#pragma unroll
+        for (int x = 0; x < kMB / 2; ++x) {
+          if (m0 + 2 * x < a.DC) s[(m0 + 2 * x) * a.st_c] = S[x].x;
+          if (m0 + 2 * x + 1 < a.DC) s[(m0 + 2 * x + 1) * a.st_c] = S[x].y;
+        }
+      }
+    }
+  } else if (warp >= L::kVGroup) {
+    // ------------------------------------------------------------- C' group
+    const int tid = threadIdx.x - 32 * L::kVGroup;
+    bool ok = true;
+    for (int it = 0; it < n_it && ok; ++it) {
+      const int tile = tile_of(it), nv = rows_in(tile);
+      const int j = it * BPT, st = j % R;
+      uint8_t* c_s = ring + st * kBoxBytes;
+      if (!wait(&full[st], (j / R) & 1, abort_flag)) { ok = false; break; }
+      if (nv < kTile) {
+        // rows of B and C past the sequence's end, which a shorter sequence of
+        // a batch finds filled, are cleared before any product reads them
+        if (!wait(&full_b[it % NB], (it / NB) & 1, abort_flag)) { ok = false; break; }
+        uint8_t* b_s = b_ring + (it % NB) * L::kBStage;
+        for (int i = nv * 8 + tid; i < kTile * 8; i += 128) {
+          reinterpret_cast<uint4*>(c_s)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int x = 0; x < L::kABoxes; ++x)
+            reinterpret_cast<uint4*>(b_s + x * kBoxBytes)[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        named_barrier_sync(3, 128);
+        if (tid == 0) mbar_arrive(fixed);
+      }
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (it >= n_kv) break;
+        if (it > 0 && !wait(&vp_free[half], (it - 1) & 1, abort_flag)) { ok = false; break; }
+        uint8_t* to = vp + half * PARTS * L::kHalf;
+        // a thread's pieces of 8 columns are 16 rows apart, two at a time
+#pragma unroll 1
+        for (int i = 0; i < 4; i += 2) {
+          uint4 v[2];
+          float w[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int r = 64 * half + tid / 8 + 16 * (i + y);
+            v[y] = reinterpret_cast<const uint4*>(c_s)[512 * half + tid + 128 * (i + y)];
+            w[y] = r < nv ? a.s_c * pw[rev ? r : nv - 1 - r] : 0.f;
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+            uint32_t out[PARTS][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float2 f = mul2(both(w[y]), make_float2(__uint_as_float(in[x] << 16),
+                                                      __uint_as_float(in[x] & 0xffff0000u)));
+#pragma unroll
+              for (int p = 0; p < PARTS - 1; ++p) out[p][x] = cut_hi(f);
+              // the third takes what is left of 24 bits, at most 8
+              out[PARTS - 1][x] = PARTS == 3 ? upper(f) : tc::pack_bf16x2(f.x, f.y);
+            }
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+              reinterpret_cast<uint4*>(to + p * L::kHalf)[tid + 128 * (i + y)] =
+                  make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        named_barrier_sync(3, 128);
+        if (tid == 0) mbar_arrive(&vp_ready[half]);
+      }
+      if (tid == 0) mbar_arrive(&empty[st]);
+    }
+    if (!ok) record_timeout(a.status, abort_flag);
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- P group
+    bool ok = true;
+    for (int it = 0; it < n_it; ++it) {
+      const int bf = it % kNP;
+      if (!wait(&p_done[bf], (it / kNP) & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t pc = lane_base + bf * 128;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];               // then hi in the first 16, lo in the next
+        if (rev ? c < wq : c > wq) {  // masked as a whole
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+          tmem_st32(pc + 32 * c, r);
+          continue;
+        }
+        tmem_ld32(pc + 32 * c, r);
+        uint32_t lo[16];
+        if (c == wq) {
+          // the diagonal chunk: a power per element, masked places 0 whatever
+          // the accumulators hold
+          const float* w = rev ? pw - lane : pw + lane;
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float2 p;
+            const bool k0 = rev ? 2 * x >= lane : 2 * x <= lane;
+            const bool k1 = rev ? 2 * x + 1 >= lane : 2 * x + 1 <= lane;
+            p.x = k0 ? __uint_as_float(r[2 * x]) * (a.s_p * w[rev ? 2 * x : -2 * x]) : 0.f;
+            p.y = k1 ? __uint_as_float(r[2 * x + 1]) * (a.s_p * w[rev ? 2 * x + 1 : -2 * x - 1]) : 0.f;
+            r[x] = split_hi(p);
+            lo[x] = tc::pack_bf16x2(p.x, p.y);
+          }
+        } else {
+          const float2 rf = both(a.s_p * pw[rev ? 32 * c - row : row - 32 * c - 31]);
+          const float4* f = reinterpret_cast<const float4*>(cf);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float2 w = x % 2 ? make_float2(f[x / 2].z, f[x / 2].w) : make_float2(f[x / 2].x, f[x / 2].y);
+            float2 p = mul2(mul2(rf, w),
+                            make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
+            r[x] = split_hi(p);
+            lo[x] = tc::pack_bf16x2(p.x, p.y);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) r[16 + x] = lo[x];
+        tmem_st32(pc + 32 * c, r);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[bf]);
+    }
+    if (!ok) record_timeout(a.status, abort_flag);
+  } else {
+    // -------------------------------------------------------------- O group
+    const int o_tid = threadIdx.x - 32 * 12;
+    const int oh = a.o_key ? b * a.Hk + h / a.group : bh;
+    const float full_row = a.s_o * pw[rev ? kTile - row : row + 1];
+    bool ok = true;
+    for (int it = 0; it < n_it; ++it) {
+      const int tile = tile_of(it), nv = rows_in(tile);
+      const float rf = !rev || (nv == kTile && shift(tile) == 0) ? full_row
+                       : row < nv ? a.s_o * pw[nv - row - shift(tile)] : 0.f;
+      // the store that last read the staging box has finished reading it
+      if (o_tid == 0) tma_store_wait_read_all();
+      named_barrier_sync(1, 128);
+      if (!wait(o1_done, it & 1, abort_flag) || !wait(o2_done, it & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float* to = a.out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * a.DC + mb * kMB;
+#pragma unroll 1
+      for (int c = 0; c < kMB / 16; ++c) {
+        uint32_t p[16], q[16];
+        tmem_ld16(lane_base + L::kColO1 + 16 * c, p);
+        tmem_ld16(lane_base + L::kColO2 + 16 * c, q);
+        tmem_ld_wait();
+        float2 t[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          t[x] = fma2(both(rf), make_float2(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1])),
+                      make_float2(__uint_as_float(q[2 * x]), __uint_as_float(q[2 * x + 1])));
+        }
+        if (nv < kTile && row >= nv)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) t[x] = make_float2(0.f, 0.f);
+        if (a.out_f32 == nullptr) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 16 * c + 8 * y, 0)) =
+                make_uint4(tc::pack_bf16x2(t[4 * y].x, t[4 * y].y),
+                           tc::pack_bf16x2(t[4 * y + 1].x, t[4 * y + 1].y),
+                           tc::pack_bf16x2(t[4 * y + 2].x, t[4 * y + 2].y),
+                           tc::pack_bf16x2(t[4 * y + 3].x, t[4 * y + 3].y));
+        } else if ((int64_t)tile * kTile + row < a.N) {
+          // fp32 parts, which a later launch sums over the heads of a group
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (mb * kMB + 16 * c + 4 * x < a.DC)
+              reinterpret_cast<float4*>(to + 16 * c)[x] =
+                  make_float4(t[2 * x].x, t[2 * x].y, t[2 * x + 1].x, t[2 * x + 1].y);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      if (a.out_f32 == nullptr) {
+        fence_proxy_async_smem();
+        named_barrier_sync(1, 128);
+        if (o_tid == 0) {
+          tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
+          tma_store_commit();
+        }
+      }
+    }
+    if (!ok) record_timeout(a.status, abort_flag);
+    // tiles behind the sequence's end: zeros
+    if (ok && max(t_first, live) < t_stop) {
+      if (a.out_f32 == nullptr) {
+        if (o_tid == 0) tma_store_wait_read_all();
+        named_barrier_sync(1, 128);
+#pragma unroll
+        for (int c = 0; c < kMB / 8; ++c)
+          *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 8 * c, 0)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        named_barrier_sync(1, 128);
+        if (o_tid == 0) {
+          for (int tile = max(t_first, live); tile < t_stop; ++tile)
+            tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
+          tma_store_commit();
+        }
+      } else {
+        const int64_t r0 = (int64_t)max(t_first, live) * kTile, r1 = min(a.N, (int64_t)t_stop * kTile);
+        const int cols = min(kMB, a.DC - mb * kMB) / 4;
+        float* to = a.out_f32 + (int64_t)bh * a.N * a.DC + mb * kMB;
+        for (int64_t i = o_tid; i < (r1 - r0) * cols; i += 128)
+          *reinterpret_cast<float4*>(to + (r0 + i / cols) * a.DC + i % cols * 4) =
+              make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    if (o_tid == 0) tma_store_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  grid_dep_launch_dependents();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+}
+
+// Pieces' sums [problems][G][E] become, in place, the states the pieces start
+// from: a thread walks one element over the pieces, in scan order.
+struct PrefixArgs {
+  const float* g;
+  const int* lengths;
+  const float* state_in;
+  float* slots;
+  int64_t N, st_r, st_c;
+  int H, BH, n_mb, seg_tiles, G, DA, DC, DP, reverse;
+};
+__global__ void __launch_bounds__(256) decay_tc_prefix_kernel(const PrefixArgs a) {
+  const int E = a.DP * kMB, per = E / 256;
+  const int problem = blockIdx.x / per, e = (blockIdx.x % per) * 256 + threadIdx.x;
+  const int bh = problem / a.n_mb, mb = problem % a.n_mb;
+  const float g = head_decay(a.g[bh % a.H]);
+  const int64_t rows = rows_of(a.lengths, bh / a.H, a.N), len = (int64_t)a.seg_tiles * kTile;
+  const int r = e / kMB, c = mb * kMB + e % kMB;
+  float* s = a.slots + (int64_t)problem * a.G * E + e;
+  float S = 0.f;
+  if (a.state_in != nullptr && r < a.DA && c < a.DC)
+    S = a.state_in[(int64_t)bh * a.DA * a.DC + r * a.st_r + c * a.st_c];
+  float sum = s[(int64_t)(a.reverse ? a.G - 1 : 0) * E];
+  for (int i = 0; i < a.G - 1; ++i) {
+    const int seg = a.reverse ? a.G - 1 - i : i, next = a.reverse ? seg - 1 : seg + 1;
+    const int64_t n = min(rows, (seg + 1) * len) - seg * len;  // rows of the piece
+    if (n > 0) {
+      const int sh = a.reverse && rows <= (seg + 1) * len ? 1 : 0;
+      const float2 f = power_parts(g, (int)n - sh);
+      S = fmaf(f.x, S, fmaf(f.y, S, sum));
+    }
+    if (i < a.G - 2) sum = s[(int64_t)next * E];
+    s[(int64_t)next * E] = S;
+  }
+}
+
+// ---------------------------------------------------------------- host
+struct Plan {
+  int DP, n_mb, n_tiles, seg_tiles, G;
+  int64_t problems;
+  size_t slot_bytes;
+};
+Plan plan(const DecayShape& s, int64_t DA, int64_t DC) {
+  Plan p;
+  p.DP = DA <= 64 ? 64 : 128;
+  p.n_mb = (int)((DC + kMB - 1) / kMB);
+  p.n_tiles = (int)((s.N + kTile - 1) / kTile);
+  p.problems = s.B * s.H * p.n_mb;
+  int64_t G = 1;
+  if (p.problems * 4 < (int64_t)kPlanSMs * 3) G = std::max<int64_t>(1, kPlanSMs / p.problems);
+  G = std::min<int64_t>(G, std::max(1, p.n_tiles));
+  p.seg_tiles = (int)((p.n_tiles + G - 1) / G);
+  p.G = (p.n_tiles + p.seg_tiles - 1) / p.seg_tiles;
+  p.slot_bytes = p.G > 1 ? sizeof(float) * (size_t)p.problems * p.G * p.DP * kMB : 0;
+  return p;
+}
+
+template <int DP, int PARTS, bool AGG>
+cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc,
+                   const CUtensorMap& mo, const Args& a, unsigned grid, cudaStream_t stream) {
+  using L = Layout<DP, PARTS, AGG>;
+  auto kern = decay_tc_kernel<DP, PARTS, AGG>;
+  // the shared-memory opt-in is set once per device for each instantiation
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((configured.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmem, stream, ma, mb, mc, mo, a);
+}
+
+struct Product {
+  const void *a, *b, *c;
+  void* out;
+  bool a_key, b_key, c_key, o_key, turned, reverse;  // turned: the state is held [DC][DA]
+  int64_t DA, DC;
+  const float* state_in;
+  float *state_out, *out_f32;
+  float s_p, s_o, s_c;
+};
+
+cp_status_t run(const DecayShape& s, const float* g, const Product& p, float* slots, int* status,
+                cudaStream_t stream) {
+  // the maps are made by the driver, which wants a context bound to this thread:
+  // a thread that autograd starts may not have called the runtime yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return CP_ERR_CUDA;
+  const Plan pl = plan(s, p.DA, p.DC);
+  const int64_t vh = s.B * s.H, kh = s.B * s.Hk;
+  CUtensorMap ma, mb, mc, mo;
+  if (!tc::make_map(&ma, p.a, p.a_key ? kh : vh, s.N, p.DA) ||
+      !tc::make_map(&mb, p.b, p.b_key ? kh : vh, s.N, p.DA) ||
+      !tc::make_map(&mc, p.c, p.c_key ? kh : vh, s.N, p.DC) ||
+      !tc::make_map(&mo, p.out, p.o_key ? kh : vh, s.N, p.DC))
+    return CP_ERR_UNSUPPORTED_SHAPE;
+  Args a{};
+  a.g = g;
+  a.lengths = s.lengths;
+  a.state_in = p.state_in;
+  a.state_out = p.state_out;
+  a.slots = slots;
+  a.out_f32 = p.out_f32;
+  a.status = status;
+  a.N = s.N;
+  a.st_r = p.turned ? 1 : p.DC;
+  a.st_c = p.turned ? p.DA : 1;
+  a.H = (int)s.H; a.Hk = (int)s.Hk; a.group = (int)(s.H / s.Hk); a.BH = (int)vh;
+  a.n_mb = pl.n_mb; a.n_tiles = pl.n_tiles; a.seg_tiles = pl.seg_tiles; a.G = pl.G;
+  a.DA = (int)p.DA; a.DC = (int)p.DC;
+  a.a_key = p.a_key; a.b_key = p.b_key; a.c_key = p.c_key; a.o_key = p.o_key;
+  a.reverse = p.reverse;
+  a.s_p = p.s_p; a.s_o = p.s_o; a.s_c = p.s_c;
+  const unsigned sums = (unsigned)(pl.problems * (pl.G - 1)), all = (unsigned)(pl.problems * pl.G);
+  cudaError_t e = cudaSuccess;
+#define CP_DECAY_CASE(DP_, PARTS_)                                                          \
+  if (pl.DP == DP_ && (p.state_out != nullptr ? 3 : 2) == PARTS_) {                         \
+    if (pl.G > 1) {                                                                         \
+      e = launch<DP_, PARTS_, true>(ma, mb, mc, mo, a, sums, stream);                       \
+      if (e != cudaSuccess) return CP_ERR_CUDA;                                             \
+      const PrefixArgs x{g,       s.lengths, p.state_in, slots,        s.N,   a.st_r, a.st_c, \
+                         a.H,     a.BH,      a.n_mb,     a.seg_tiles,  a.G,   a.DA,   a.DC, \
+                         DP_,     a.reverse};                                               \
+      decay_tc_prefix_kernel<<<(unsigned)(pl.problems * DP_ * kMB / 256), 256, 0, stream>>>(x); \
+      if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;                            \
+    }                                                                                       \
+    e = launch<DP_, PARTS_, false>(ma, mb, mc, mo, a, all, stream);                         \
+  }
+  CP_DECAY_CASE(64, 2)
+  CP_DECAY_CASE(64, 3)
+  CP_DECAY_CASE(128, 2)
+  CP_DECAY_CASE(128, 3)
+#undef CP_DECAY_CASE
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t part_bytes(const DecayShape& s) {
+  return s.H == s.Hk ? 0 : round256(sizeof(float) * (size_t)s.B * s.H * s.N * s.D);
+}
+
+}  // namespace
+
+bool decay_tc_supported(const DecayShape& s) {
+  return s.dtype == CP_DTYPE_BF16 && s.D <= 128 && s.M <= 128;
+}
+
+size_t decay_tc_scratch(const DecayShape& s, bool backward) {
+  const size_t fwd = plan(s, s.D, s.M).slot_bytes;
+  if (!backward) return fwd;
+  return std::max(fwd, plan(s, s.M, s.D).slot_bytes) + 256 + 2 * part_bytes(s);
+}
+
+cp_status_t decay_tc_fwd(const DecayShape& s, const DecayFwd& f, void* scratch, int* status,
+                         cudaStream_t stream) {
+  return run(s, f.g,
+             {f.q, f.k, f.v, f.out, true, true, false, false, false, false, s.D, s.M, f.state_in,
+              f.state_out, nullptr, s.scale, s.scale, 1.f},
+             static_cast<float*>(scratch), status, stream);
+}
+
+cp_status_t decay_tc_bwd(const DecayShape& s, const DecayBwd& f, void* scratch, int* status,
+                         cudaStream_t stream) {
+  float* slots = static_cast<float*>(scratch);
+  const size_t n = round256(std::max(plan(s, s.D, s.M).slot_bytes, plan(s, s.M, s.D).slot_bytes));
+  const bool grouped = s.H != s.Hk;
+  float* dq_part = grouped ? slots + n / sizeof(float) : nullptr;
+  float* dk_part = grouped ? dq_part + part_bytes(s) / sizeof(float) : nullptr;
+  cp_status_t st =
+      run(s, f.g,
+          {f.grad_out, f.v, f.k, f.dq, false, false, true, true, true, false, s.M, s.D, f.state_in,
+           nullptr, dq_part, s.scale, s.scale, 1.f},
+          slots, status, stream);
+  if (st != CP_OK) return st;
+  st = run(s, f.g,
+           {f.k, f.q, f.grad_out, f.dv, true, true, false, false, false, true, s.D, s.M,
+            f.grad_state_out, f.grad_state_in, nullptr, s.scale, 1.f, s.scale},
+           slots, status, stream);
+  if (st != CP_OK) return st;
+  st = run(s, f.g,
+           {f.v, f.grad_out, f.q, f.dk, false, false, true, true, true, true, s.M, s.D,
+            f.grad_state_out, nullptr, dk_part, s.scale, 1.f, s.scale},
+           slots, status, stream);
+  if (st != CP_OK || !grouped) return st;
+  return delta_join_launch({dq_part, dk_part, nullptr, nullptr, f.dq, f.dk, nullptr, nullptr, s.N,
+                            s.D, s.B * s.Hk, (int)(s.H / s.Hk), 1},
+                           s.dtype, stream) == cudaSuccess
+             ? CP_OK
+             : CP_ERR_CUDA;
+}
+
+}  // namespace cp

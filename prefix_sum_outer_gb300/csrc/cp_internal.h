@@ -349,6 +349,13 @@ cudaError_t decay_simt_fwd(const DecayShape& s, const DecayFwd& f, void* scratch
                            cudaStream_t stream);
 cudaError_t decay_simt_bwd(const DecayShape& s, const DecayBwd& f, void* scratch,
                            cudaStream_t stream);
+// tensor-core path (bf16, D and M <= 128)
+bool decay_tc_supported(const DecayShape& s);
+size_t decay_tc_scratch(const DecayShape& s, bool backward);
+cp_status_t decay_tc_fwd(const DecayShape& s, const DecayFwd& f, void* scratch, int* status,
+                         cudaStream_t stream);
+cp_status_t decay_tc_bwd(const DecayShape& s, const DecayBwd& f, void* scratch, int* status,
+                         cudaStream_t stream);
 cudaError_t decay_decode_launch(const DecayShape& s, const DecayDecode& f, cudaStream_t stream);
 
 // ---- layer norm of rows of C features; forward: y from x; backward: dx, dw and

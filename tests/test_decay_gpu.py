@@ -151,7 +151,7 @@ def test_lengths(dt, D, M):
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_nan_and_inf_stay_in_their_head(dt):
     x = make(1, 4, 4, 300, 64, 64, DT[dt], seed=8, rates=[-0.01] * 4)
-    clean = cp.causal_product_fwd_decay(*args(x))
+    clean, _ = cp.causal_product_fwd_decay(*args(x), return_state=True)
     x["v"][0, 1, 140, 3], x["k"][0, 2, 180, 0] = float("nan"), float("inf")
     x["g"][3] = float("nan")
     out, s = cp.causal_product_fwd_decay(*args(x), return_state=True)
