@@ -14,9 +14,9 @@
 //   warps 1..3    MMA issuers: B^T C'; A B^T and A S; P C
 //   warps 4..7    state group: fp32 S in registers (thread = row); its hi + lo
 //                 copy, the operand of A S
-//   warps 8..11   P group: P times its powers, masked, hi + lo, back into TMEM
-//   warps 12..15  O group: O from its two accumulators, to bf16, TMA store
-//   warps 16..19  C' group: a row times its power, as two or three bf16 numbers
+//   warps 8..15   P groups: P times its powers, masked, hi + lo, back into TMEM
+//   warps 16..19  O group: O from its two accumulators, to bf16, TMA store
+//   warps 20..27  C' groups: a row times its power, as two or three bf16 numbers
 // A CTA walks one piece of one head's sequence for 64 columns of c.
 //
 // Precision.  S lives in registers in fp32 and takes each tile's B^T C' by an fma
@@ -88,8 +88,8 @@ struct Layout {
       AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - PARTS - kOBoxes;
   static constexpr int kBoxes = NB * kABoxes + R + kSBoxes + PARTS + kOBoxes;
   static constexpr int kSmem = kBoxes * kBoxBytes + kBarBytes + kTableBytes + 1024;
-  static constexpr int kVGroup = AGG ? 8 : 16;                 // first warp of the C' group
-  static constexpr int kThreads = 32 * (kVGroup + 4);
+  static constexpr int kVGroup = AGG ? 8 : 20;                 // first warp of the C' groups
+  static constexpr int kThreads = 32 * (kVGroup + 8);
   static constexpr int kSWarps = DP / 32;                      // warps that hold state rows
   // tensor memory: P, A S, P C, and B^T C' as [hi | rest]
   static constexpr int kColO1 = kNP * 128, kColO2 = kColO1 + kMB;
@@ -118,7 +118,7 @@ __device__ __forceinline__ uint32_t cut_hi(float2& x) {
   return h;
 }
 
-// Twenty warps walk eight different pieces of code, so what stalls them first is
+// Twenty-eight warps walk eight different pieces of code, so what stalls them first is
 // the instruction cache: loops stay rolled, and a wait is a few instructions, its
 // limit a count (a try takes tens of nanoseconds to a microsecond, so a third of a
 // second at least) and not a clock's.
@@ -127,6 +127,19 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   while (!mbar_try_wait(bar, parity))
     if (*abort_flag != 0 || ++tries > (1u << 24)) return false;
   return true;
+}
+
+// A barrier of a group's threads that also agrees whether all of them go on: one
+// that gave up waiting must not leave the others at the next barrier.
+__device__ __forceinline__ bool agree(uint32_t id, uint32_t nthreads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
 }
 
 template <int REGS>
@@ -193,11 +206,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     }
     for (int i = 0; i < R; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], AGG ? 1 : 2);
+      mbar_init(&empty[i], AGG ? 2 : 3);  // C: both C' groups and P C; A: A B^T, A S twice
     }
     for (int i = 0; i < kNP; ++i) {
       mbar_init(&p_done[i], 1);
-      mbar_init(&p_ready[i], 4);
+      mbar_init(&p_ready[i], 8);
       mbar_init(&pc_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -260,7 +273,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   const int n_kv = hands_on ? n_it : n_it - 1;
 
   if (warp < 4) {
-    if constexpr (!AGG) fewer_registers<56>();
+    if constexpr (!AGG) fewer_registers<40>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
@@ -397,7 +410,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
             mma_commit(&as_done[nQ % NSB]);
             mma_commit(o1_done);
 #pragma unroll
-            for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(nQ, x)]);
+            for (int x = 1; x < BPT; ++x) {
+              mma_commit(&empty[box(nQ, x)]);
+              mma_commit(&empty[box(nQ, x)]);
+            }
             ++nQ;
             idle = 0;
           }
@@ -540,37 +556,44 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       }
     }
   } else if (warp >= L::kVGroup) {
-    // ------------------------------------------------------------- C' group
-    const int tid = threadIdx.x - 32 * L::kVGroup;
+    // ------------------------------------------------ C' groups, one per half
+    if constexpr (!AGG) fewer_registers<48>();
+    const int half = (warp - L::kVGroup) / 4;
+    const int tid = threadIdx.x - 32 * L::kVGroup - 128 * half;
+    uint8_t* to = vp + half * PARTS * L::kHalf;
     bool ok = true;
-    for (int it = 0; it < n_it && ok; ++it) {
+#pragma unroll 1
+    for (int it = 0; it < n_it; ++it) {
       const int tile = tile_of(it), nv = rows_in(tile);
       const int j = it * BPT, st = j % R;
       uint8_t* c_s = ring + st * kBoxBytes;
-      if (!wait(&full[st], (j / R) & 1, abort_flag)) { ok = false; break; }
+      ok = wait(&full[st], (j / R) & 1, abort_flag);
       if (nv < kTile) {
         // rows of B and C past the sequence's end, which a shorter sequence of
         // a batch finds filled, are cleared before any product reads them
-        if (!wait(&full_b[it % NB], (it / NB) & 1, abort_flag)) { ok = false; break; }
-        uint8_t* b_s = b_ring + (it % NB) * L::kBStage;
-        for (int i = nv * 8 + tid; i < kTile * 8; i += 128) {
-          reinterpret_cast<uint4*>(c_s)[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int x = 0; x < L::kABoxes; ++x)
-            reinterpret_cast<uint4*>(b_s + x * kBoxBytes)[i] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        named_barrier_sync(3, 128);
-        if (tid == 0) mbar_arrive(fixed);
-      }
+        if (half == 0) {
+          ok = ok && wait(&full_b[it % NB], (it / NB) & 1, abort_flag);
+          uint8_t* b_s = b_ring + (it % NB) * L::kBStage;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (it >= n_kv) break;
-        if (it > 0 && !wait(&vp_free[half], (it - 1) & 1, abort_flag)) { ok = false; break; }
-        uint8_t* to = vp + half * PARTS * L::kHalf;
+          for (int i = nv * 8 + tid; ok && i < kTile * 8; i += 128) {
+            reinterpret_cast<uint4*>(c_s)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < L::kABoxes; ++x)
+              reinterpret_cast<uint4*>(b_s + x * kBoxBytes)[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          ok = agree(3, 128, ok);
+          if (!ok) break;
+          if (tid == 0) mbar_arrive(fixed);
+        } else {
+          ok = ok && wait(fixed, 0, abort_flag);
+        }
+      }
+      if (it < n_kv) {
+        if (it > 0) ok = ok && wait(&vp_free[half], (it - 1) & 1, abort_flag);
         // a thread's pieces of 8 columns are 16 rows apart, two at a time
 #pragma unroll 1
-        for (int i = 0; i < 4; i += 2) {
+        for (int i = 0; ok && i < 4; i += 2) {
           uint4 v[2];
           float w[2];
 #pragma unroll
@@ -599,14 +622,17 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        named_barrier_sync(3, 128);
-        if (tid == 0) mbar_arrive(&vp_ready[half]);
+        ok = agree(3 + half, 128, ok);
+        if (tid == 0 && ok) mbar_arrive(&vp_ready[half]);
       }
+      if (!ok) break;
       if (tid == 0) mbar_arrive(&empty[st]);
     }
     if (!ok) record_timeout(a.status, abort_flag);
-  } else if (warp < 12) {
-    // -------------------------------------------------------------- P group
+  } else if (warp < 16) {
+    // ------------------------- P groups: columns 0 .. 63 and 64 .. 127 of a tile
+    if constexpr (!AGG) more_registers<80>();
+    const int c_first = warp < 12 ? 0 : 2;
     bool ok = true;
     for (int it = 0; it < n_it; ++it) {
       const int bf = it % kNP;
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       tc_fence_after();
       const uint32_t pc = lane_base + bf * 128;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = c_first; c < c_first + 2; ++c) {
         uint32_t r[32];               // then hi in the first 16, lo in the next
         if (rev ? c < wq : c > wq) {  // masked as a whole
 #pragma unroll
@@ -664,7 +690,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     if (!ok) record_timeout(a.status, abort_flag);
   } else {
     // -------------------------------------------------------------- O group
-    const int o_tid = threadIdx.x - 32 * 12;
+    const int o_tid = threadIdx.x - 32 * 16;
     const int oh = a.o_key ? b * a.Hk + h / a.group : bh;
     const float full_row = a.s_o * pw[rev ? kTile - row : row + 1];
     bool ok = true;
@@ -674,15 +700,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
                        : row < nv ? a.s_o * pw[nv - row - shift(tile)] : 0.f;
       // the store that last read the staging box has finished reading it
       if (o_tid == 0) tma_store_wait_read_all();
-      named_barrier_sync(1, 128);
-      if (!wait(o1_done, it & 1, abort_flag) || !wait(o2_done, it & 1, abort_flag)) {
-        ok = false;
-        break;
-      }
+      ok = agree(1, 128, ok);
+      if (!ok) break;
+      ok = wait(o1_done, it & 1, abort_flag) && wait(o2_done, it & 1, abort_flag);
       tc_fence_after();
       float* to = a.out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * a.DC + mb * kMB;
-#pragma unroll 1
-      for (int c = 0; c < kMB / 16; ++c) {
+#pragma unroll 2
+      for (int c = 0; ok && c < kMB / 16; ++c) {
         uint32_t p[16], q[16];
         tmem_ld16(lane_base + L::kColO1 + 16 * c, p);
         tmem_ld16(lane_base + L::kColO2 + 16 * c, q);
@@ -718,14 +742,15 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       if (lane == 0) mbar_arrive(o_free);
       if (a.out_f32 == nullptr) {
         fence_proxy_async_smem();
-        named_barrier_sync(1, 128);
-        if (o_tid == 0) {
+        ok = agree(1, 128, ok);
+        if (o_tid == 0 && ok) {
           tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
           tma_store_commit();
         }
       }
     }
     if (!ok) record_timeout(a.status, abort_flag);
+    ok = agree(1, 128, ok);
     // tiles behind the sequence's end: zeros
     if (ok && max(t_first, live) < t_stop) {
       if (a.out_f32 == nullptr) {
