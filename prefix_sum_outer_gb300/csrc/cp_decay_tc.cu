@@ -78,19 +78,20 @@ struct Layout {
   static constexpr int kBStage = kABoxes * kBoxBytes;
   static constexpr int kBoxesPerTile = AGG ? 1 : kABoxes + 1;  // of the A / C ring
   static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
-  static constexpr int kHalf = kBoxBytes / 2;                  // a part of half a tile's C'
+  static constexpr int kQuarter = kBoxBytes / 4;               // a part of 32 rows of C'
+  static constexpr int kVBytes = 4 * PARTS * kQuarter;         // C'
   static constexpr int kTotal = (kSmemLimit - 1024 - kBarBytes - kTableBytes) / kBoxBytes;  // boxes
-  static constexpr int NSB = DP == 64 ? 2 : 1;                 // copies of S
+  static constexpr int NSB = 1;                                // copies of S
   static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
-  static constexpr int NB = DP == 64 ? 3 : 2;                  // stages of the B ring
+  static constexpr int NB = 2;                                 // stages of the B ring
   static constexpr int kOBoxes = AGG ? 0 : 1;
   static constexpr int R =
-      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - PARTS - kOBoxes;
-  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes + PARTS + kOBoxes;
-  static constexpr int kSmem = kBoxes * kBoxBytes + kBarBytes + kTableBytes + 1024;
+      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - kOBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
+  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes + kOBoxes;
+  static constexpr int kSmem = kBoxes * kBoxBytes + kVBytes + kBarBytes + kTableBytes + 1024;
   static constexpr int kVGroup = AGG ? 8 : 20;                 // first warp of the C' groups
   static constexpr int kThreads = 32 * (kVGroup + 8);
-  static constexpr int kSWarps = DP / 32;                      // warps that hold state rows
+  static constexpr int SC = DP / 2;                            // columns of S to a thread
   // tensor memory: P, A S, P C, and B^T C' as [hi | rest]
   static constexpr int kColO1 = kNP * 128, kColO2 = kColO1 + kMB;
   static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
@@ -99,23 +100,25 @@ struct Layout {
   static_assert(kSmem <= kSmemLimit && kColS + 128 <= kCols, "no room");
 };
 
-// hi = bf16(x), and x - hi
+// hi = bf16(x), and x - hi: the differences by mixed fma, whose bf16 operand needs
+// no widening (shifts and masks go to the pipe that has the least to spare here:
+// 19 cycles a pair and scheduler with them in three parts, 16 without)
 __device__ __forceinline__ uint32_t split_hi(float2& x) {
   const uint32_t h = tc::pack_bf16x2(x.x, x.y);
-  x = sub2(x, make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)));
+  asm("{\n\t.reg .b16 a, b, m;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, a, m, %3;\n\tfma.rn.f32.bf16 %1, b, m, %4;\n\t}"
+      : "=f"(x.x), "=f"(x.y)
+      : "r"(h), "f"(x.x), "f"(x.y));
   return h;
 }
-
-// the upper halves of two floats, as two bf16 numbers
-__device__ __forceinline__ uint32_t upper(float2 x) {
-  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-}
-// the first 8 bits of x as bf16 (cut off, not rounded), and what is left
-__device__ __forceinline__ uint32_t cut_hi(float2& x) {
-  const uint32_t h = upper(x);
-  x = sub2(x, make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
-                          __uint_as_float(__float_as_uint(x.y) & 0xffff0000u)));
-  return h;
+// two bf16 numbers as fp32
+__device__ __forceinline__ float2 widen(uint32_t h) {
+  float2 r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "add.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h), "f"(0.f));
+  return r;
 }
 
 // Twenty-eight warps walk eight different pieces of code, so what stalls them first is
@@ -163,8 +166,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   uint8_t* smem = align_tiles(smem_raw);
   uint8_t* b_ring = smem;                            // [NB] B tiles
   uint8_t* ring = b_ring + NB * L::kBStage;          // [R] boxes: a tile's A, then its C
-  uint8_t* vp = ring + R * kBoxBytes;                // [PARTS] C'
-  uint8_t* s_tile = vp + PARTS * kBoxBytes;          // [NSB] hi | lo copies of S
+  uint8_t* vp = ring + R * kBoxBytes;                // [4][PARTS] 32 rows of C'
+  uint8_t* s_tile = vp + L::kVBytes;                 // [NSB] hi | lo copies of S
   uint8_t* o_tile = s_tile + L::kSBoxes * kBoxBytes;
   uint64_t* full_b = reinterpret_cast<uint64_t*>(o_tile + L::kOBoxes * kBoxBytes);
   uint64_t* empty_b = full_b + NB;
@@ -177,10 +180,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   uint64_t* as_done = s_ready + 2;     // [2] A S done: the copy is free
   uint64_t* o1_done = as_done + 2;     // A S
   uint64_t* o2_done = o1_done + 1;     // P C
-  uint64_t* o_free = o2_done + 1;      // both read
-  uint64_t* vp_ready = o_free + 1;     // [2] half of C' written
-  uint64_t* vp_free = vp_ready + 2;    // [2] its products done
-  uint64_t* kv_done = vp_free + 2;     // B^T C' in TMEM
+  uint64_t* o1_free = o2_done + 1;     // read
+  uint64_t* o2_free = o1_free + 1;
+  uint64_t* vp_ready = o2_free + 1;    // [4] 32 rows of C' written
+  uint64_t* vp_free = vp_ready + 4;    // [4] their products done
+  uint64_t* kv_done = vp_free + 4;     // B^T C' in TMEM
   uint64_t* kv_free = kv_done + 1;     // B^T C' read
   uint64_t* fixed = kv_free + 1;       // rows past the sequence's end cleared
   uint64_t* fin = fixed + 1;           // [3]
@@ -214,18 +218,19 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       mbar_init(&pc_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_ready[i], L::kSWarps);
+      mbar_init(&s_ready[i], 4);
       mbar_init(&as_done[i], 1);
     }
     mbar_init(o1_done, 1);
     mbar_init(o2_done, 1);
-    mbar_init(o_free, 4);
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(o1_free, 4);
+    mbar_init(o2_free, 4);
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&vp_ready[i], 1);
       mbar_init(&vp_free[i], 1);
     }
     mbar_init(kv_done, 1);
-    mbar_init(kv_free, L::kSWarps);
+    mbar_init(kv_free, 4);
     mbar_init(fixed, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
     *abort_flag = 0;
@@ -333,29 +338,29 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
       bool ok = true;
       if (warp == 1) {
-        // B^T C', half a tile's rows at a time
+        // B^T C', 32 rows at a time, from either C' group in turn
         for (int it = 0; it < n_kv && ok; ++it) {
           ok = wait(&full_b[it % NB], (it / NB) & 1, abort_flag) &&
                (it == 0 || wait(kv_free, (it - 1) & 1, abort_flag)) &&
                (!tail(it) || wait(fixed, 0, abort_flag));
-          // (A = B^T, 128 rows of it: past a 64-wide B's own the next bytes,
-          // whose lanes nobody reads)
-          const uint32_t bt_lo = desc_lo(b_addr(it), kBoxBytes);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!ok || !wait(&vp_ready[half], it & 1, abort_flag)) { ok = false; break; }
+          // (A = B^T, 128 rows of it: a 64-wide B's own twice over, so that both
+          // halves of the lanes hold the state's rows)
+          const uint32_t bt_lo = desc_lo(b_addr(it), DP == 64 ? 0 : kBoxBytes);
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            if (!ok || !wait(&vp_ready[x], it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t v_lo = desc_lo(smem_u32(vp + half * PARTS * L::kHalf), L::kHalf);
+            const uint32_t v_lo = desc_lo(smem_u32(vp + x * PARTS * L::kQuarter), L::kQuarter);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 32; ++kk)
-              mma_ss_lo<kHi, kHi>(tmem + L::kColS, bt_lo + ((half * 8192 + kk * 2048) >> 4),
-                                  v_lo + ((kk * 2048) >> 4), idesc_s2, (half | kk) > 0);
+            for (int kk = 0; kk < 2; ++kk)
+              mma_ss_lo<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * 4096 + kk * 2048) >> 4),
+                                  v_lo + ((kk * 2048) >> 4), idesc_s2, (x | kk) > 0);
             if constexpr (PARTS == 3)
 #pragma unroll
-              for (int kk = 0; kk < kTile / 32; ++kk)
-                mma_ss_lo<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((half * 8192 + kk * 2048) >> 4),
-                                    v_lo + ((2 * L::kHalf + kk * 2048) >> 4), idesc_s1, 1u);
-            mma_commit(&vp_free[half]);
+              for (int kk = 0; kk < 2; ++kk)
+                mma_ss_lo<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * 4096 + kk * 2048) >> 4),
+                                    v_lo + ((2 * L::kQuarter + kk * 2048) >> 4), idesc_s1, 1u);
+            mma_commit(&vp_free[x]);
           }
           if (!ok) break;
           mma_commit(kv_done);
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
             idle = 0;
           }
           if (nQ < nP && mbar_test_wait(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
-              (nQ == 0 || mbar_test_wait(o_free, (nQ - 1) & 1))) {
+              (nQ == 0 || mbar_test_wait(o1_free, (nQ - 1) & 1))) {
             tc_fence_after();
             const uint32_t s_lo = desc_lo(smem_u32(s_tile + (nQ % NSB) * 2 * L::kSOne), L::kSOne);
 #pragma unroll
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           const int bf = it % kNP, x = box(it, 0);
           ok = wait(&p_ready[bf], (it / kNP) & 1, abort_flag) &&
                wait(&full[x], box_phase(it, 0), abort_flag) &&
-               (it == 0 || wait(o_free, (it - 1) & 1, abort_flag)) &&
+               (it == 0 || wait(o2_free, (it - 1) & 1, abort_flag)) &&
                (!tail(it) || wait(fixed, 0, abort_flag));
           if (!ok) break;
           tc_fence_after();
@@ -455,31 +460,35 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------- state group
-    if constexpr (!AGG) more_registers<136>();
-    if (wq < L::kSWarps) {
-      const int pidx = bh * a.n_mb + mb;
-      float* slot = a.slots + ((int64_t)pidx * a.G + seg) * DP * kMB + row * kMB;
-      float2 S[kMB / 2];
+    if constexpr (!AGG) more_registers<(DP == 64 ? 88 : 136)>();
+    {
+      // thread: a row of S; with 64 rows two threads share one, half of its
+      // columns each
+      constexpr int SC = L::SC;
+      const int d = DP == 64 ? row & 63 : row, c0 = DP == 64 ? (row >> 6) * SC : 0;
+      const int pidx = bh * a.n_mb + mb, m0 = mb * kMB + c0;
+      float* slot = a.slots + (((int64_t)pidx * a.G + seg) * DP + d) * kMB + c0;
+      float2 S[SC / 2];
       const bool first_seg = rev ? seg == a.G - 1 : seg == 0;
       if (!AGG && !first_seg) {
 #pragma unroll
-        for (int x = 0; x < kMB / 4; ++x) {
+        for (int x = 0; x < SC / 4; ++x) {
           const float4 f = reinterpret_cast<const float4*>(slot)[x];
           S[2 * x] = make_float2(f.x, f.y);
           S[2 * x + 1] = make_float2(f.z, f.w);
         }
       } else {
-        const bool on = !AGG && a.state_in != nullptr && row < a.DA;
-        const float* s = a.state_in + (int64_t)bh * a.DA * a.DC + row * a.st_r;
-        const int m0 = mb * kMB;
+        const bool on = !AGG && a.state_in != nullptr && d < a.DA;
+        const float* s = a.state_in + (int64_t)bh * a.DA * a.DC + d * a.st_r;
 #pragma unroll
-        for (int x = 0; x < kMB / 2; ++x) {
+        for (int x = 0; x < SC / 2; ++x) {
           S[x].x = on && m0 + 2 * x < a.DC ? s[(m0 + 2 * x) * a.st_c] : 0.f;
           S[x].y = on && m0 + 2 * x + 1 < a.DC ? s[(m0 + 2 * x + 1) * a.st_c] : 0.f;
         }
       }
       const float2 full_step = power_parts(g, kTile);
       bool ok = true;
+#pragma unroll 1
       for (int it = 0; it < n_it; ++it) {
         if constexpr (!AGG) {
           const int sb = it % NSB;
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
             break;
           }
 #pragma unroll
-          for (int c = 0; c < kMB / 8; ++c) {
+          for (int c = 0; c < SC / 8; ++c) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -498,7 +507,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
               hi[x] = split_hi(s);
               lo[x] = tc::pack_bf16x2(s.x, s.y);
             }
-            const uint32_t off = sw128_offset(row, 8 * c, 0);
+            const uint32_t off = sw128_offset(d, c0 + 8 * c, 0);
             *reinterpret_cast<uint4*>(sbuf + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(sbuf + L::kSOne + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
@@ -515,10 +524,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < kMB / 16; ++c) {
+          for (int c = 0; c < SC / 16; ++c) {
             uint32_t p[16], q[16];
-            tmem_ld16(lane_base + L::kColS + 16 * c, p);
-            tmem_ld16(lane_base + L::kColS + kMB + 16 * c, q);
+            tmem_ld16(lane_base + L::kColS + c0 + 16 * c, p);
+            tmem_ld16(lane_base + L::kColS + kMB + c0 + 16 * c, q);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -536,31 +545,32 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       if (!ok) record_timeout(a.status, abort_flag);
       if (AGG && ok && n_it > 0) {
 #pragma unroll
-        for (int x = 0; x < kMB / 4; ++x)
+        for (int x = 0; x < SC / 4; ++x)
           reinterpret_cast<float4*>(slot)[x] =
               make_float4(S[2 * x].x, S[2 * x].y, S[2 * x + 1].x, S[2 * x + 1].y);
       }
-      if (!AGG && ok && hands_on && row < a.DA) {
+      if (!AGG && ok && hands_on && d < a.DA) {
         if (rev && live > 0) {
           const float2 f = power_parts(g, 1);
 #pragma unroll
-          for (int x = 0; x < kMB / 2; ++x) S[x] = fma2(both(f.x), S[x], mul2(both(f.y), S[x]));
+          for (int x = 0; x < SC / 2; ++x) S[x] = fma2(both(f.x), S[x], mul2(both(f.y), S[x]));
         }
-        float* s = a.state_out + (int64_t)bh * a.DA * a.DC + row * a.st_r;
-        const int m0 = mb * kMB;
+        float* s = a.state_out + (int64_t)bh * a.DA * a.DC + d * a.st_r;
 #pragma unroll
-        for (int x = 0; x < kMB / 2; ++x) {
+        for (int x = 0; x < SC / 2; ++x) {
           if (m0 + 2 * x < a.DC) s[(m0 + 2 * x) * a.st_c] = S[x].x;
           if (m0 + 2 * x + 1 < a.DC) s[(m0 + 2 * x + 1) * a.st_c] = S[x].y;
         }
       }
     }
   } else if (warp >= L::kVGroup) {
-    // ------------------------------------------------ C' groups, one per half
-    if constexpr (!AGG) fewer_registers<48>();
+    // -------------------------------- C' groups: every other 32 rows of a tile
+    if constexpr (!AGG) {
+      if constexpr (DP == 64) fewer_registers<56>();
+      else fewer_registers<40>();
+    }
     const int half = (warp - L::kVGroup) / 4;
     const int tid = threadIdx.x - 32 * L::kVGroup - 128 * half;
-    uint8_t* to = vp + half * PARTS * L::kHalf;
     bool ok = true;
 #pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
@@ -590,16 +600,18 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
         }
       }
       if (it < n_kv) {
-        if (it > 0) ok = ok && wait(&vp_free[half], (it - 1) & 1, abort_flag);
-        // a thread's pieces of 8 columns are 16 rows apart, two at a time
 #pragma unroll 1
-        for (int i = 0; ok && i < 4; i += 2) {
+        for (int x = 0; x < 2 && ok; ++x) {
+          const int first = 64 * x + 32 * half;  // row
+          uint8_t* to = vp + (2 * x + half) * PARTS * L::kQuarter;
+          if (it > 0) ok = wait(&vp_free[2 * x + half], (it - 1) & 1, abort_flag);
           uint4 v[2];
           float w[2];
+          // a thread's pieces of 8 columns are 16 rows apart
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int r = 64 * half + tid / 8 + 16 * (i + y);
-            v[y] = reinterpret_cast<const uint4*>(c_s)[512 * half + tid + 128 * (i + y)];
+            const int r = first + tid / 8 + 16 * y;
+            v[y] = reinterpret_cast<const uint4*>(c_s)[8 * first + tid + 128 * y];
             w[y] = r < nv ? a.s_c * pw[rev ? r : nv - 1 - r] : 0.f;
           }
 #pragma unroll
@@ -607,23 +619,22 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
             const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
             uint32_t out[PARTS][4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float2 f = mul2(both(w[y]), make_float2(__uint_as_float(in[x] << 16),
-                                                      __uint_as_float(in[x] & 0xffff0000u)));
+            for (int z = 0; z < 4; ++z) {
+              float2 f = mul2(both(w[y]), widen(in[z]));
 #pragma unroll
-              for (int p = 0; p < PARTS - 1; ++p) out[p][x] = cut_hi(f);
-              // the third takes what is left of 24 bits, at most 8
-              out[PARTS - 1][x] = PARTS == 3 ? upper(f) : tc::pack_bf16x2(f.x, f.y);
+              for (int p = 0; p < PARTS - 1; ++p) out[p][z] = split_hi(f);
+              out[PARTS - 1][z] = tc::pack_bf16x2(f.x, f.y);
             }
+            if (ok)
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-              reinterpret_cast<uint4*>(to + p * L::kHalf)[tid + 128 * (i + y)] =
-                  make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
+              for (int p = 0; p < PARTS; ++p)
+                reinterpret_cast<uint4*>(to + p * L::kQuarter)[tid + 128 * y] =
+                    make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
           }
+          fence_proxy_async_smem();
+          ok = agree(3 + half, 128, ok);
+          if (tid == 0 && ok) mbar_arrive(&vp_ready[2 * x + half]);
         }
-        fence_proxy_async_smem();
-        ok = agree(3 + half, 128, ok);
-        if (tid == 0 && ok) mbar_arrive(&vp_ready[half]);
       }
       if (!ok) break;
       if (tid == 0) mbar_arrive(&empty[st]);
@@ -631,7 +642,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     if (!ok) record_timeout(a.status, abort_flag);
   } else if (warp < 16) {
     // ------------------------- P groups: columns 0 .. 63 and 64 .. 127 of a tile
-    if constexpr (!AGG) more_registers<80>();
+    if constexpr (!AGG && DP == 64) more_registers<80>();
     const int c_first = warp < 12 ? 0 : 2;
     bool ok = true;
     for (int it = 0; it < n_it; ++it) {
@@ -690,6 +701,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     if (!ok) record_timeout(a.status, abort_flag);
   } else {
     // -------------------------------------------------------------- O group
+    if constexpr (!AGG) more_registers<104>();
     const int o_tid = threadIdx.x - 32 * 16;
     const int oh = a.o_key ? b * a.Hk + h / a.group : bh;
     const float full_row = a.s_o * pw[rev ? kTile - row : row + 1];
@@ -698,55 +710,68 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       const int tile = tile_of(it), nv = rows_in(tile);
       const float rf = !rev || (nv == kTile && shift(tile) == 0) ? full_row
                        : row < nv ? a.s_o * pw[nv - row - shift(tile)] : 0.f;
-      // the store that last read the staging box has finished reading it
-      if (o_tid == 0) tma_store_wait_read_all();
-      ok = agree(1, 128, ok);
-      if (!ok) break;
-      ok = wait(o1_done, it & 1, abort_flag) && wait(o2_done, it & 1, abort_flag);
+      // A S, scaled, waits in registers for P C, whose accumulator is given back
+      // as soon as it is read: the next tile's P C waits for it
+      float2 o[kMB / 2];
+      ok = wait(o1_done, it & 1, abort_flag);
       tc_fence_after();
-      float* to = a.out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * a.DC + mb * kMB;
-#pragma unroll 2
-      for (int c = 0; ok && c < kMB / 16; ++c) {
-        uint32_t p[16], q[16];
+#pragma unroll
+      for (int c = 0; c < kMB / 16; ++c) {
+        uint32_t p[16];
         tmem_ld16(lane_base + L::kColO1 + 16 * c, p);
-        tmem_ld16(lane_base + L::kColO2 + 16 * c, q);
         tmem_ld_wait();
-        float2 t[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          t[x] = fma2(both(rf), make_float2(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1])),
-                      make_float2(__uint_as_float(q[2 * x]), __uint_as_float(q[2 * x + 1])));
-        }
-        if (nv < kTile && row >= nv)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) t[x] = make_float2(0.f, 0.f);
-        if (a.out_f32 == nullptr) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 16 * c + 8 * y, 0)) =
-                make_uint4(tc::pack_bf16x2(t[4 * y].x, t[4 * y].y),
-                           tc::pack_bf16x2(t[4 * y + 1].x, t[4 * y + 1].y),
-                           tc::pack_bf16x2(t[4 * y + 2].x, t[4 * y + 2].y),
-                           tc::pack_bf16x2(t[4 * y + 3].x, t[4 * y + 3].y));
-        } else if ((int64_t)tile * kTile + row < a.N) {
-          // fp32 parts, which a later launch sums over the heads of a group
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (mb * kMB + 16 * c + 4 * x < a.DC)
-              reinterpret_cast<float4*>(to + 16 * c)[x] =
-                  make_float4(t[2 * x].x, t[2 * x].y, t[2 * x + 1].x, t[2 * x + 1].y);
-        }
+        for (int x = 0; x < 8; ++x)
+          o[8 * c + x] = mul2(both(rf), make_float2(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1])));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) mbar_arrive(o1_free);
+      ok = ok && wait(o2_done, it & 1, abort_flag);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kMB / 16; ++c) {
+        uint32_t p[16];
+        tmem_ld16(lane_base + L::kColO2 + 16 * c, p);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          o[8 * c + x] = add2(o[8 * c + x], make_float2(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1])));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o2_free);
+      if (nv < kTile && row >= nv)
+#pragma unroll
+        for (int x = 0; x < kMB / 2; ++x) o[x] = make_float2(0.f, 0.f);
       if (a.out_f32 == nullptr) {
-        fence_proxy_async_smem();
+        // the store that last read the staging box has finished reading it
+        if (o_tid == 0) tma_store_wait_read_all();
         ok = agree(1, 128, ok);
-        if (o_tid == 0 && ok) {
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kMB / 8; ++c)
+          *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 8 * c, 0)) =
+              make_uint4(tc::pack_bf16x2(o[4 * c].x, o[4 * c].y),
+                         tc::pack_bf16x2(o[4 * c + 1].x, o[4 * c + 1].y),
+                         tc::pack_bf16x2(o[4 * c + 2].x, o[4 * c + 2].y),
+                         tc::pack_bf16x2(o[4 * c + 3].x, o[4 * c + 3].y));
+        fence_proxy_async_smem();
+        named_barrier_sync(1, 128);
+        if (o_tid == 0) {
           tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
           tma_store_commit();
         }
+      } else {
+        // fp32 parts, which a later launch sums over the heads of a group
+        if (!ok) break;
+        float* to = a.out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * a.DC + mb * kMB;
+        if ((int64_t)tile * kTile + row < a.N)
+#pragma unroll
+          for (int x = 0; x < kMB / 4; ++x)
+            if (mb * kMB + 4 * x < a.DC)
+              reinterpret_cast<float4*>(to)[x] =
+                  make_float4(o[2 * x].x, o[2 * x].y, o[2 * x + 1].x, o[2 * x + 1].y);
       }
     }
     if (!ok) record_timeout(a.status, abort_flag);
