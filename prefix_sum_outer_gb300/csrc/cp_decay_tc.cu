@@ -79,15 +79,15 @@ struct Layout {
   static constexpr int kBoxesPerTile = AGG ? 1 : kABoxes + 1;  // of the A / C ring
   static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
   static constexpr int kQuarter = kBoxBytes / 4;               // a part of 32 rows of C'
-  static constexpr int kVBytes = 4 * PARTS * kQuarter;         // C'
+  static constexpr int NV = DP == 128 && PARTS == 3 ? 2 : 4;   // buffers of 32 rows of C'
+  static constexpr int kVBytes = NV * PARTS * kQuarter;
   static constexpr int kTotal = (kSmemLimit - 1024 - kBarBytes - kTableBytes) / kBoxBytes;  // boxes
   static constexpr int NSB = 1;                                // copies of S
   static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
   static constexpr int NB = 2;                                 // stages of the B ring
-  static constexpr int kOBoxes = AGG ? 0 : 1;
   static constexpr int R =
-      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - kOBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
-  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes + kOBoxes;
+      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
+  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes;
   static constexpr int kSmem = kBoxes * kBoxBytes + kVBytes + kBarBytes + kTableBytes + 1024;
   static constexpr int kVGroup = AGG ? 8 : 20;                 // first warp of the C' groups
   static constexpr int kThreads = 32 * (kVGroup + 8);
@@ -166,10 +166,9 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   uint8_t* smem = align_tiles(smem_raw);
   uint8_t* b_ring = smem;                            // [NB] B tiles
   uint8_t* ring = b_ring + NB * L::kBStage;          // [R] boxes: a tile's A, then its C
-  uint8_t* vp = ring + R * kBoxBytes;                // [4][PARTS] 32 rows of C'
+  uint8_t* vp = ring + R * kBoxBytes;                // [NV][PARTS] 32 rows of C'
   uint8_t* s_tile = vp + L::kVBytes;                 // [NSB] hi | lo copies of S
-  uint8_t* o_tile = s_tile + L::kSBoxes * kBoxBytes;
-  uint64_t* full_b = reinterpret_cast<uint64_t*>(o_tile + L::kOBoxes * kBoxBytes);
+  uint64_t* full_b = reinterpret_cast<uint64_t*>(s_tile + L::kSBoxes * kBoxBytes);
   uint64_t* empty_b = full_b + NB;
   uint64_t* full = empty_b + NB;       // [R]
   uint64_t* empty = full + R;          // [R]
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     }
     for (int i = 0; i < R; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], AGG ? 2 : 3);  // C: both C' groups and P C; A: A B^T, A S twice
+      mbar_init(&empty[i], AGG ? 2 : 3);  // C: both C' groups and the O group; A: A B^T, A S twice
     }
     for (int i = 0; i < kNP; ++i) {
       mbar_init(&p_done[i], 1);
@@ -348,9 +347,9 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           const uint32_t bt_lo = desc_lo(b_addr(it), DP == 64 ? 0 : kBoxBytes);
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
-            if (!ok || !wait(&vp_ready[x], it & 1, abort_flag)) { ok = false; break; }
+            if (!ok || !wait(&vp_ready[x % L::NV], L::NV == 4 ? it & 1 : x >> 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t v_lo = desc_lo(smem_u32(vp + x * PARTS * L::kQuarter), L::kQuarter);
+            const uint32_t v_lo = desc_lo(smem_u32(vp + x % L::NV * PARTS * L::kQuarter), L::kQuarter);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
               mma_ss_lo<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * 4096 + kk * 2048) >> 4),
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
               for (int kk = 0; kk < 2; ++kk)
                 mma_ss_lo<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * 4096 + kk * 2048) >> 4),
                                     v_lo + ((2 * L::kQuarter + kk * 2048) >> 4), idesc_s1, 1u);
-            mma_commit(&vp_free[x]);
+            mma_commit(&vp_free[x % L::NV]);
           }
           if (!ok) break;
           mma_commit(kv_done);
@@ -450,7 +449,6 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
                              c_lo + ((kk * 2048) >> 4), idesc_o, (part | kk) > 0);
           mma_commit(&pc_done[bf]);
           mma_commit(o2_done);
-          mma_commit(&empty[x]);
         }
       }
       if (!ok) record_timeout(a.status, abort_flag);
@@ -603,8 +601,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
 #pragma unroll 1
         for (int x = 0; x < 2 && ok; ++x) {
           const int first = 64 * x + 32 * half;  // row
-          uint8_t* to = vp + (2 * x + half) * PARTS * L::kQuarter;
-          if (it > 0) ok = wait(&vp_free[2 * x + half], (it - 1) & 1, abort_flag);
+          const int bf = (2 * x + half) % L::NV;
+          uint8_t* to = vp + bf * PARTS * L::kQuarter;
+          if (L::NV == 4 ? it > 0 : it + x > 0)
+            ok = wait(&vp_free[bf], (L::NV == 4 ? it + 1 : x + 1) & 1, abort_flag);
           uint4 v[2];
           float w[2];
           // a thread's pieces of 8 columns are 16 rows apart
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           }
           fence_proxy_async_smem();
           ok = agree(3 + half, 128, ok);
-          if (tid == 0 && ok) mbar_arrive(&vp_ready[2 * x + half]);
+          if (tid == 0 && ok) mbar_arrive(&vp_ready[bf]);
         }
       }
       if (!ok) break;
@@ -744,9 +744,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       if (nv < kTile && row >= nv)
 #pragma unroll
         for (int x = 0; x < kMB / 2; ++x) o[x] = make_float2(0.f, 0.f);
+      // (both C' groups and P C are done with this tile's C: its box takes O)
+      const int st = it * BPT % R;
+      uint8_t* o_tile = ring + st * kBoxBytes;
       if (a.out_f32 == nullptr) {
-        // the store that last read the staging box has finished reading it
-        if (o_tid == 0) tma_store_wait_read_all();
         ok = agree(1, 128, ok);
         if (!ok) break;
 #pragma unroll
@@ -761,6 +762,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
         if (o_tid == 0) {
           tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
           tma_store_commit();
+          tma_store_wait_read_all();
+          mbar_arrive(&empty[st]);
         }
       } else {
         // fp32 parts, which a later launch sums over the heads of a group
@@ -772,6 +775,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
             if (mb * kMB + 4 * x < a.DC)
               reinterpret_cast<float4*>(to)[x] =
                   make_float4(o[2 * x].x, o[2 * x].y, o[2 * x + 1].x, o[2 * x + 1].y);
+        if (o_tid == 0) mbar_arrive(&empty[st]);
       }
     }
     if (!ok) record_timeout(a.status, abort_flag);
@@ -779,7 +783,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     // tiles behind the sequence's end: zeros
     if (ok && max(t_first, live) < t_stop) {
       if (a.out_f32 == nullptr) {
-        if (o_tid == 0) tma_store_wait_read_all();
+        // (the box that took the last O is this group's alone by now)
+        uint8_t* o_tile = ring + max(0, n_it - 1) * BPT % R * kBoxBytes;
         named_barrier_sync(1, 128);
 #pragma unroll
         for (int c = 0; c < kMB / 8; ++c)
