@@ -11,7 +11,7 @@
 // Nothing in a tile but A S waits for the state, and the state's update is one
 // fma, so the tiles stream through a pipeline of warps:
 //   warp 0        TMA producer: B tiles into one ring, A and C boxes into another
-//   warps 1..3    MMA issuers: B^T C'; A B^T and A S; P C
+//   warps 1..3    MMA issuers: B^T C'; A B^T; P C; A S by one of the last two
 //   warps 4..7    state group: fp32 S in registers (thread = row); its hi + lo
 //                 copy, the operand of A S
 //   warps 8..15   P groups: P times its powers, masked, hi + lo, back into TMEM
@@ -51,7 +51,7 @@ using tc::record_timeout;
 using tc::sw128_offset;
 
 constexpr int kMB = 64;   // columns of c to a CTA
-constexpr int kBarBytes = 1024, kTableBytes = 1024;
+constexpr int kBarBytes = 512, kTableBytes = 1536;
 constexpr int kNP = 2;    // buffers of P
 constexpr uint32_t kHi = desc_hi(1024);
 
@@ -97,6 +97,7 @@ struct Layout {
   static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
   static constexpr int kCols = AGG ? 128 : 512;
   static_assert(R >= kBoxesPerTile, "a tile does not fit");
+  static_assert((2 * NB + 2 * R + 34) * 8 <= kBarBytes, "barriers");
   static_assert(kSmem <= kSmemLimit && kColS + 128 <= kCols, "no room");
 };
 
@@ -336,8 +337,55 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
       auto box_phase = [&](int it, int x) { return ((it * BPT + x) / R) & 1; };
       auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
       bool ok = true;
+      // A S is issued by the warp of A B^T, or by that of P C: 72 against 79 us
+      // with D = M = 64 (B=8 H=16 N=4096), 304 against 296 with 128 (B=2 H=8
+      // N=32768)
+      constexpr bool kMixed = DP == 64;
+      [[maybe_unused]] auto issue_p = [&](int it) {
+        bool there = wait(&full_b[it % NB], (it / NB) & 1, abort_flag);
+#pragma unroll
+        for (int x = 1; x < BPT - 1; ++x)
+          there = there && wait(&full[box(it, x)], box_phase(it, x), abort_flag);
+        if (!there) return false;
+        tc_fence_after();
+        const uint32_t t_p = tmem + (it % kNP) * 128;
+        const uint32_t k_lo = desc_lo(b_addr(it), 16);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint32_t in = ((kk & 3) * 32) >> 4;
+          mma_ss_lo<kHi, kHi>(
+              t_p, desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) + in,
+              k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0);
+        }
+        mma_commit(&p_done[it % kNP]);
+        mma_commit(&empty_b[it % NB]);
+#pragma unroll
+        for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(it, x)]);
+        return true;
+      };
+      [[maybe_unused]] auto issue_as = [&](int it) {
+        tc_fence_after();
+        const uint32_t s_lo = desc_lo(smem_u32(s_tile + (it % NSB) * 2 * L::kSOne), L::kSOne);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_ss_lo<kHi, kHi>(
+                tmem + L::kColO1,
+                desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) +
+                    (((kk & 3) * 32) >> 4),
+                s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0);
+        mma_commit(&as_done[it % NSB]);
+        mma_commit(o1_done);
+#pragma unroll
+        for (int x = 1; x < BPT; ++x) {
+          mma_commit(&empty[box(it, x)]);
+          mma_commit(&empty[box(it, x)]);
+        }
+      };
       if (warp == 1) {
         // B^T C', 32 rows at a time, from either C' group in turn
+#pragma unroll 1
         for (int it = 0; it < n_kv && ok; ++it) {
           ok = wait(&full_b[it % NB], (it / NB) & 1, abort_flag) &&
                (it == 0 || wait(kv_free, (it - 1) & 1, abort_flag)) &&
@@ -366,58 +414,25 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           mma_commit(&empty_b[it % NB]);
         }
       } else if (warp == 2) {
-        // A B^T, as far ahead as there are buffers, and A S: whichever can go
+        // A B^T, as far ahead as there are buffers; with 64-wide A, A S too,
+        // whichever can go
         int nP = 0, nQ = 0;
         uint32_t idle = 0;
 #pragma unroll 1
-        while (nQ < n_it) {
+        while (nP < n_it || (kMixed && nQ < n_it)) {
           ++idle;
+          // (the tile's other boxes and its B were asked for before its last box)
           if (nP < n_it && mbar_test_wait(&full[box(nP, BPT - 1)], box_phase(nP, BPT - 1)) &&
               (nP < kNP || mbar_test_wait(&pc_done[nP % kNP], ((nP - kNP) / kNP) & 1)) &&
               (!tail(nP) || mbar_test_wait(fixed, 0))) {
-            // (the other boxes and B were asked for before the last box)
-            ok = wait(&full_b[nP % NB], (nP / NB) & 1, abort_flag);
-#pragma unroll
-            for (int x = 1; x < BPT - 1; ++x)
-              ok = ok && wait(&full[box(nP, x)], box_phase(nP, x), abort_flag);
+            ok = issue_p(nP);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t t_p = tmem + (nP % kNP) * 128;
-            const uint32_t k_lo = desc_lo(b_addr(nP), 16);
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-              const uint32_t in = ((kk & 3) * 32) >> 4;
-              mma_ss_lo<kHi, kHi>(
-                  t_p, desc_lo(smem_u32(ring + box(nP, 1 + (kk >> 2)) * kBoxBytes), 16) + in,
-                  k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0);
-            }
-            mma_commit(&p_done[nP % kNP]);
-            mma_commit(&empty_b[nP % NB]);
-#pragma unroll
-            for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(nP, x)]);
             ++nP;
             idle = 0;
           }
-          if (nQ < nP && mbar_test_wait(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
+          if (kMixed && nQ < nP && mbar_test_wait(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
               (nQ == 0 || mbar_test_wait(o1_free, (nQ - 1) & 1))) {
-            tc_fence_after();
-            const uint32_t s_lo = desc_lo(smem_u32(s_tile + (nQ % NSB) * 2 * L::kSOne), L::kSOne);
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int kk = 0; kk < DP / 16; ++kk)
-                mma_ss_lo<kHi, kHi>(
-                    tmem + L::kColO1,
-                    desc_lo(smem_u32(ring + box(nQ, 1 + (kk >> 2)) * kBoxBytes), 16) +
-                        (((kk & 3) * 32) >> 4),
-                    s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0);
-            mma_commit(&as_done[nQ % NSB]);
-            mma_commit(o1_done);
-#pragma unroll
-            for (int x = 1; x < BPT; ++x) {
-              mma_commit(&empty[box(nQ, x)]);
-              mma_commit(&empty[box(nQ, x)]);
-            }
+            issue_as(nQ);
             ++nQ;
             idle = 0;
           }
@@ -428,9 +443,17 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
           }
         }
       } else {
-        // P C
+        // P C; with 128-wide A, A S before it
+#pragma unroll 1
         for (int it = 0; it < n_it && ok; ++it) {
           const int bf = it % kNP, x = box(it, 0);
+          if (!kMixed) {
+            ok = wait(&p_done[bf], (it / kNP) & 1, abort_flag) &&  // A has landed
+                 wait(&s_ready[it % NSB], (it / NSB) & 1, abort_flag) &&
+                 (it == 0 || wait(o1_free, (it - 1) & 1, abort_flag));
+            if (!ok) break;
+            issue_as(it);
+          }
           ok = wait(&p_ready[bf], (it / kNP) & 1, abort_flag) &&
                wait(&full[x], box_phase(it, 0), abort_flag) &&
                (it == 0 || wait(o2_free, (it - 1) & 1, abort_flag)) &&

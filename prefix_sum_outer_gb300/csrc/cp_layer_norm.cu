@@ -12,6 +12,7 @@
 // summed in order by a second launch, so results are the same every time.  No
 // statistics are kept from the forward: the row is in registers anyway.
 #include <algorithm>
+#include <atomic>
 
 #include "cp_delta.cuh"
 
@@ -62,9 +63,100 @@ struct Raw<T, 8> {
     const T t = from_f32<T>(f);
     const uint32_t s = *reinterpret_cast<const unsigned short*>(&t);
     uint32_t& w = (&x.x)[i / 2];
-    w = i % 2 ? (w & 0xffffu) | (s << 16) : (w & 0xffff0000u) | s;
+    w = i % 2 ? (w & 0xffffu) | (s << 16) : s;  // (the even one goes first)
   }
 };
+
+// Arithmetic on a vector's elements in fp32.  16-bit elements enter it by the
+// mixed-precision instructions, two of a word at a time: shifts and masks that
+// widen them, done at each of their three uses, would take half of the backward's
+// time.
+#define CP_MIXED_OPS(TYPE, NAME)                                                              \
+  __device__ __forceinline__ float2 plus(TYPE, uint32_t a, float2 c) { /* a + c */            \
+    float2 r;                                                                                 \
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32." NAME " %0, x, %3;\n\t"     \
+        "add.rn.f32." NAME " %1, y, %4;\n\t}"                                                 \
+        : "=f"(r.x), "=f"(r.y) : "r"(a), "f"(c.x), "f"(c.y));                                 \
+    return r;                                                                                 \
+  }                                                                                           \
+  __device__ __forceinline__ float2 minus(TYPE, uint32_t a, float c) { /* a - c */            \
+    float2 r;                                                                                 \
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tsub.rn.f32." NAME " %0, x, %3;\n\t"     \
+        "sub.rn.f32." NAME " %1, y, %3;\n\t}"                                                 \
+        : "=f"(r.x), "=f"(r.y) : "r"(a), "f"(c));                                             \
+    return r;                                                                                 \
+  }                                                                                           \
+  __device__ __forceinline__ float2 times(TYPE, uint32_t a, uint32_t b, float2 c) { /* ab + c */ \
+    float2 r;                                                                                 \
+    asm("{\n\t.reg .b16 x, y, u, v;\n\tmov.b32 {x, y}, %2;\n\tmov.b32 {u, v}, %3;\n\t"          \
+        "fma.rn.f32." NAME " %0, x, u, %4;\n\tfma.rn.f32." NAME " %1, y, v, %5;\n\t}"         \
+        : "=f"(r.x), "=f"(r.y) : "r"(a), "r"(b), "f"(c.x), "f"(c.y));                         \
+    return r;                                                                                 \
+  }
+CP_MIXED_OPS(__nv_bfloat16, "bf16")
+CP_MIXED_OPS(__half, "f16")
+#undef CP_MIXED_OPS
+constexpr float2 kZero2 = {0.f, 0.f};
+
+// s += x (two running sums)
+template <typename T, int VEC>
+__device__ __forceinline__ void sum_into(float2& s, const Raw<T, VEC>& x) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = plus(T(), (&x.x.x)[i], s);
+  } else if constexpr (VEC == 4) {
+    s = add2(add2(s, make_float2(x.x.x, x.x.y)), make_float2(x.x.z, x.x.w));
+  } else {
+    s.x += x.get(0);
+  }
+}
+// x - c
+template <typename T, int VEC>
+__device__ __forceinline__ void diff(float (&d)[VEC], const Raw<T, VEC>& x, float c) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 r = minus(T(), (&x.x.x)[i], c);
+      d[2 * i] = r.x;
+      d[2 * i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d[e] = x.get(e) - c;
+  }
+}
+// g w, or without W g
+template <bool W, typename T, int VEC>
+__device__ __forceinline__ void product(float (&t)[VEC], const Raw<T, VEC>& g, const Raw<T, VEC>& w) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 r;
+      if constexpr (W) r = times(T(), (&g.x.x)[i], (&w.x.x)[i], kZero2);
+      else r = plus(T(), (&g.x.x)[i], kZero2);
+      t[2 * i] = r.x;
+      t[2 * i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) t[e] = W ? g.get(e) * w.get(e) : g.get(e);
+  }
+}
+// s += g w, or without W g (two running sums)
+template <bool W, typename T, int VEC>
+__device__ __forceinline__ void sum_product_into(float2& s, const Raw<T, VEC>& g, const Raw<T, VEC>& w) {
+  if constexpr (!W) {
+    sum_into(s, g);
+  } else if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = times(T(), (&g.x.x)[i], (&w.x.x)[i], s);
+  } else if constexpr (VEC == 4) {
+    s = fma2(make_float2(g.x.x, g.x.y), make_float2(w.x.x, w.x.y), s);
+    s = fma2(make_float2(g.x.z, g.x.w), make_float2(w.x.z, w.x.w), s);
+  } else {
+    s.x = fmaf(g.get(0), w.get(0), s.x);
+  }
+}
 
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load(const T* p) {
@@ -78,7 +170,9 @@ __device__ __forceinline__ Raw<T, VEC> zero() {
   return r;
 }
 
-// Sums of NS values over a row's group: GL lanes, or a CTA of whole warps
+// Sums of NS values over a row's group: GL lanes, or a CTA of whole warps, whose
+// parts meet in `red`.  (A row's two sums have a `red` each, so the barrier of the
+// one keeps the next row's from the other's readers.)
 template <int GL, bool MULTI, int NS>
 __device__ __forceinline__ void group_sum(float (&v)[NS], float (*red)[33]) {
 #pragma unroll
@@ -97,7 +191,6 @@ __device__ __forceinline__ void group_sum(float (&v)[NS], float (*red)[33]) {
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    __syncthreads();
   }
 }
 
@@ -110,7 +203,7 @@ template <typename T, int VEC, int GL, int KV, int MT>
 __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const Args a) {
   constexpr bool MULTI = MT > 0;
   constexpr int RPT = kRpt<VEC, KV, MT>;
-  __shared__ float red[1][33];
+  __shared__ float red[2][1][33];
   const int G = MULTI ? blockDim.x : GL;
   const int t = threadIdx.x % G, grp = threadIdx.x / G, groups = blockDim.x / G;
   const int h = blockIdx.y;
@@ -139,23 +232,22 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
   const float inv = 1.f / (float)a.C;
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
-    float s[1] = {0.f};
+    float2 two = kZero2;
 #pragma unroll
-    for (int i = 0; i < KV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s[0] += raw[r][i].get(e);
-    group_sum<GL, MULTI, 1>(s, red);
+    for (int i = 0; i < KV; ++i) sum_into(two, raw[r][i]);
+    float s[1] = {two.x + two.y};
+    group_sum<GL, MULTI, 1>(s, red[0]);
     const float mu = s[0] * inv;
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < KV; ++i)
-      if ((i * G + t) * VEC < a.C)
+      if ((i * G + t) * VEC < a.C) {
+        float d[VEC];
+        diff(d, raw[r][i], mu);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = raw[r][i].get(e) - mu;
-          s[0] = fmaf(d, d, s[0]);
-        }
-    group_sum<GL, MULTI, 1>(s, red);
+        for (int e = 0; e < VEC; ++e) s[0] = fmaf(d[e], d[e], s[0]);
+      }
+    group_sum<GL, MULTI, 1>(s, red[1]);
     const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
     if (at[r] >= 0) {
       const T* w = a.w == nullptr ? nullptr : static_cast<const T*>(a.w) + h * a.w_head;
@@ -165,13 +257,19 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
         const int c = (i * G + t) * VEC;
         if (c < a.C) {
           Raw<T, VEC> o, ww, bb;
-          if (w != nullptr) ww = load<T, VEC>(w + c);
-          if (b != nullptr) bb = load<T, VEC>(b + c);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float xh = (raw[r][i].get(e) - mu) * rs;
-            o.set(e, fmaf(xh, w != nullptr ? ww.get(e) : 1.f, b != nullptr ? bb.get(e) : 0.f));
+          float d[VEC], fw[VEC], fb[VEC];
+          diff(d, raw[r][i], mu);
+          if (w != nullptr) {
+            ww = load<T, VEC>(w + c);
+            product<false>(fw, ww, ww);
           }
+          if (b != nullptr) {
+            bb = load<T, VEC>(b + c);
+            product<false>(fb, bb, bb);
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            o.set(e, fmaf(d[e] * rs, w != nullptr ? fw[e] : 1.f, b != nullptr ? fb[e] : 0.f));
           *reinterpret_cast<Raw<T, VEC>*>(y + at[r] + c) = o;
         }
       }
@@ -179,112 +277,189 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
   }
 }
 
-template <typename T, int VEC, int GL, int KV, int MT>
-__global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads) layer_norm_bwd_kernel(const Args a) {
-  constexpr bool MULTI = MT > 0;
+// CTAs to an SM
+template <int VEC, int KV, int MT>
+constexpr int kBwdMin = MT > 0 ? (MT <= 512 ? 512 / MT : 1) : KV * VEC <= 8 ? 8 : KV * VEC <= 16 ? 5 : 3;
+
+// Rows first, first + step, ... of a head's B * N: a row's offset in a tensor goes
+// by steps, without a division a row.
+struct Walk {
+  int64_t at, by, wrap;  // elements
+  __device__ __forceinline__ Walk(const Args& a, unsigned row, unsigned sb, unsigned sn, int64_t b,
+                                  int64_t n)
+      : at((row / a.n) * b + (row % a.n) * n), by(sb * b + sn * n), wrap(b - a.n * n) {}
+};
+
+// WEIGHTED: there is a w.  SUMS: where the weight's and the bias's gradients
+// gather: shared memory (a CTA to a row, whose threads would not hold them beside
+// the row) or registers
+template <typename T, int VEC, int GL, int KV, int MT, bool SUMS, bool WEIGHTED>
+__global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads, kBwdMin<VEC, KV, MT>)
+    layer_norm_bwd_kernel(const Args a) {
+  constexpr bool MULTI = MT > 0, AHEAD = VEC > 1;
   constexpr int E = KV * VEC;
-  extern __shared__ float sums[];  // [2][groups][G * E], unless MULTI
-  __shared__ float red[2][33];
+  constexpr int W = VEC > 1 ? 4 : 1;  // floats to an access of the sums
+  extern __shared__ __align__(16) float sums[];  // SUMS: [2][E / W][G][W]; else [2][groups][G * E]
+  __shared__ float red[2][2][33];
   const int G = MULTI ? blockDim.x : GL;
   const int t = threadIdx.x % G, grp = threadIdx.x / G, groups = blockDim.x / G;
   const int h = blockIdx.y;
-  const T* x = static_cast<const T*>(a.x) + h * a.sh;
-  const T* gy = static_cast<const T*>(a.gy) + h * a.yh;
-  T* dx = static_cast<T*>(a.dx) + (int64_t)h * a.N * a.C;
-  const T* w = a.w == nullptr ? nullptr : static_cast<const T*>(a.w) + h * a.w_head;
+  const T* w = static_cast<const T*>(a.w) + (WEIGHTED ? h * a.w_head + t * VEC : 0);
   const float inv = 1.f / (float)a.C;
-  float dw[E] = {}, db[E] = {};
-  Raw<T, VEC> nx[KV], ng[KV];
-  // a row's loads go out under the arithmetic of the row before it
-  auto fetch = [&](unsigned row) {
-    if (row < a.rows) {
-      const unsigned b = row / a.n, n = row - b * a.n;
-      const T *px = x + b * a.sb + n * a.sn, *pg = gy + b * a.yb + n * a.yn;
-#pragma unroll
-      for (int i = 0; i < KV; ++i) {
-        const int c = (i * G + t) * VEC;
-        if (c < a.C) {
-          nx[i] = load<T, VEC>(px + c);
-          ng[i] = load<T, VEC>(pg + c);
-        } else {
-          nx[i] = ng[i] = zero<T, VEC>();
-        }
-      }
-    }
-  };
-  const unsigned step = gridDim.x * groups;
+  float dw[SUMS ? 1 : E] = {}, db[SUMS ? 1 : E] = {};
+  auto place = [&](int which, int e) { return sums + ((which * (E / W) + e / W) * G + t) * W; };
+  if constexpr (SUMS) {
+    for (int i = threadIdx.x; i < 2 * E * G; i += blockDim.x) sums[i] = 0.f;
+    __syncthreads();
+  }
+  const unsigned step = gridDim.x * groups, sb = step / a.n, sn = step % a.n;
   unsigned row = blockIdx.x * groups + grp;
-  fetch(row);
+  unsigned n_now = row % a.n, n_next = n_now;
+  // x and gy of the row to load, dx of the row at hand
+  Walk wx(a, row, sb, sn, a.sb, a.sn), wg(a, row, sb, sn, a.yb, a.yn);
+  Walk wd(a, row, sb, sn, (int64_t)a.H * a.N * a.C, a.C);
+  const T* x = static_cast<const T*>(a.x) + h * a.sh + t * VEC;
+  const T* gy = static_cast<const T*>(a.gy) + h * a.yh + t * VEC;
+  T* dx = static_cast<T*>(a.dx) + (int64_t)h * a.N * a.C + t * VEC;
+  bool in[KV];
+#pragma unroll
+  for (int i = 0; i < KV; ++i) in[i] = (i * G + t) * VEC < a.C;
+  Raw<T, VEC> nx[KV], ng[KV];
+  unsigned left = row < a.rows ? (a.rows - 1 - row) / step + 1 : 0;  // rows of this group
+  unsigned to_load = left;
+  auto fetch = [&]() {
+#pragma unroll
+    for (int i = 0; i < KV; ++i) {
+      if (to_load > 0 && in[i]) {
+        nx[i] = load<T, VEC>(x + wx.at + i * G * VEC);
+        ng[i] = load<T, VEC>(gy + wg.at + i * G * VEC);
+      } else {
+        nx[i] = ng[i] = zero<T, VEC>();
+      }
+    }
+    if (to_load > 0) --to_load;
+    n_next += sn;
+    const bool over = n_next >= a.n;
+    n_next -= over ? a.n : 0;
+    wx.at += wx.by + (over ? wx.wrap : 0);
+    wg.at += wg.by + (over ? wg.wrap : 0);
+  };
+  if constexpr (AHEAD) fetch();
   // every group of a warp makes as many turns (shuffles span the warp)
-  for (unsigned first = blockIdx.x * groups; first < a.rows; first += step, row += step) {
-    const bool on = row < a.rows;
-    float xh[E];
-    Raw<T, VEC> g[KV];
-    float s[2] = {0.f, 0.f};
+  const unsigned first = blockIdx.x * groups;
+  unsigned turns = first < a.rows ? (a.rows - 1 - first) / step + 1 : 0;
+#pragma unroll 1
+  for (; turns > 0; --turns) {
+    Raw<T, VEC> xr[KV], g[KV];
+    if constexpr (!AHEAD) fetch();
 #pragma unroll
     for (int i = 0; i < KV; ++i) {
+      xr[i] = nx[i];
       g[i] = ng[i];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        xh[i * VEC + e] = on ? nx[i].get(e) : 0.f;
-        s[0] += xh[i * VEC + e];
-      }
     }
-    if (row + step > row) fetch(row + step);
-    float m[1] = {s[0]};
-    group_sum<GL, MULTI, 1>(m, red);
-    const float mu = m[0] * inv;
-    m[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < KV; ++i)
-      if ((i * G + t) * VEC < a.C)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float& d = xh[i * VEC + e];
-          d -= mu;
-          m[0] = fmaf(d, d, m[0]);
-        }
-    group_sum<GL, MULTI, 1>(m, red);
-    const float rs = rsqrtf(fmaf(m[0], inv, a.eps));
-    s[0] = 0.f;
+    // a row's loads go out under the arithmetic of the row before it
+    if constexpr (AHEAD) fetch();
+    // sums of x and of t = gy w
+    float2 sx = kZero2, st = kZero2;
+    Raw<T, VEC> ww[KV];
 #pragma unroll
     for (int i = 0; i < KV; ++i) {
-      const int c = (i * G + t) * VEC;
-      Raw<T, VEC> ww;
-      if (w != nullptr && c < a.C) ww = load<T, VEC>(w + c);
+      if constexpr (WEIGHTED) ww[i] = in[i] ? load<T, VEC>(w + i * G * VEC) : zero<T, VEC>();
+      sum_into(sx, xr[i]);
+      sum_product_into<WEIGHTED>(st, g[i], ww[i]);
+    }
+    float s[2] = {sx.x + sx.y, st.x + st.y};
+    group_sum<GL, MULTI, 2>(s, red[0]);
+    const float mu = s[0] * inv, s0 = s[1] * inv;
+    // of d = x - mu squared and of t d
+    sx = st = kZero2;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float& xx = xh[i * VEC + e];
-        xx *= rs;
-        const float gg = on && c < a.C ? g[i].get(e) : 0.f;
-        const float tt = w != nullptr && c < a.C ? gg * ww.get(e) : gg;
-        s[0] += tt;
-        s[1] = fmaf(tt, xx, s[1]);
-        if (on) {
-          dw[i * VEC + e] = fmaf(gg, xx, dw[i * VEC + e]);
-          db[i * VEC + e] += gg;
+    for (int i = 0; i < KV; ++i) {
+      if (!in[i]) continue;
+      float tt[VEC], d[VEC];
+      product<WEIGHTED>(tt, g[i], ww[i]);
+      diff(d, xr[i], mu);
+      if constexpr (VEC > 1) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          const float2 dd = make_float2(d[e], d[e + 1]);
+          sx = fma2(dd, dd, sx);
+          st = fma2(dd, make_float2(tt[e], tt[e + 1]), st);
         }
+      } else {
+        sx.x = fmaf(d[0], d[0], sx.x);
+        st.x = fmaf(d[0], tt[0], st.x);
       }
     }
-    group_sum<GL, MULTI, 2>(s, red);
-    const float s0 = s[0] * inv, s1 = s[1] * inv;
-    if (on) {
-      const unsigned b = row / a.n, n = row - b * a.n;
-      T* p = dx + ((int64_t)b * a.H * a.N + n) * a.C;
+    s[0] = sx.x + sx.y;
+    s[1] = st.x + st.y;
+    group_sum<GL, MULTI, 2>(s, red[1]);
+    const float rs = rsqrtf(fmaf(s[0], inv, a.eps)), s1 = s[1] * rs * inv;
+    if (left > 0) {
+      --left;
 #pragma unroll
       for (int i = 0; i < KV; ++i) {
-        const int c = (i * G + t) * VEC;
-        if (c < a.C) {
-          Raw<T, VEC> o, ww;
-          if (w != nullptr) ww = load<T, VEC>(w + c);
+        if (!in[i]) continue;
+        float tt[VEC], gg[VEC], out[VEC], d[VEC];
+        product<WEIGHTED>(tt, g[i], ww[i]);
+        product<false>(gg, g[i], g[i]);
+        diff(d, xr[i], mu);
+        if constexpr (VEC > 1) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float gg = g[i].get(e), tt = w != nullptr ? gg * ww.get(e) : gg;
-            o.set(e, rs * (tt - s0 - xh[i * VEC + e] * s1));
+          for (int e = 0; e < VEC; e += 2) {
+            const float2 xx = mul2(make_float2(d[e], d[e + 1]), both(rs));
+            // rs (tt - s0 - xx s1)
+            const float2 y = mul2(both(rs), fma2(xx, both(-s1), add2(make_float2(tt[e], tt[e + 1]), both(-s0))));
+            d[e] = xx.x;
+            d[e + 1] = xx.y;
+            out[e] = y.x;
+            out[e + 1] = y.y;
           }
-          *reinterpret_cast<Raw<T, VEC>*>(p + c) = o;
+        } else {
+          d[0] *= rs;
+          out[0] = rs * fmaf(d[0], -s1, tt[0] - s0);
+        }
+        Raw<T, VEC> o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o.set(e, out[e]);
+        *reinterpret_cast<Raw<T, VEC>*>(dx + wd.at + i * G * VEC) = o;
+#pragma unroll
+        for (int e0 = 0; e0 < VEC; e0 += W) {
+          if constexpr (SUMS) {
+            float *qw = place(0, i * VEC + e0), *qb = place(1, i * VEC + e0);
+            if constexpr (W == 4) {
+              float4 z = *reinterpret_cast<float4*>(qw), y = *reinterpret_cast<float4*>(qb);
+              z.x = fmaf(gg[e0], d[e0], z.x);
+              z.y = fmaf(gg[e0 + 1], d[e0 + 1], z.y);
+              z.z = fmaf(gg[e0 + 2], d[e0 + 2], z.z);
+              z.w = fmaf(gg[e0 + 3], d[e0 + 3], z.w);
+              y.x += gg[e0]; y.y += gg[e0 + 1]; y.z += gg[e0 + 2]; y.w += gg[e0 + 3];
+              *reinterpret_cast<float4*>(qw) = z;
+              *reinterpret_cast<float4*>(qb) = y;
+            } else {
+              *qw = fmaf(gg[e0], d[e0], *qw);
+              *qb += gg[e0];
+            }
+          } else if constexpr (W == 4) {
+#pragma unroll
+            for (int e = e0; e < e0 + 4; e += 2) {
+              const int j = SUMS ? 0 : i * VEC + e, k = SUMS ? 0 : j + 1;
+              const float2 z = fma2(make_float2(gg[e], gg[e + 1]), make_float2(d[e], d[e + 1]),
+                                    make_float2(dw[j], dw[k]));
+              const float2 y = add2(make_float2(gg[e], gg[e + 1]), make_float2(db[j], db[k]));
+              dw[j] = z.x; dw[k] = z.y; db[j] = y.x; db[k] = y.y;
+            }
+          } else {
+            const int j = SUMS ? 0 : i * VEC + e0;
+            dw[j] = fmaf(gg[e0], d[e0], dw[j]);
+            db[j] += gg[e0];
+          }
         }
       }
+      n_now += sn;
+      const bool over = n_now >= a.n;
+      n_now -= over ? a.n : 0;
+      wd.at += wd.by + (over ? wd.wrap : 0);
     }
   }
   if (a.part == nullptr) return;
@@ -296,8 +471,8 @@ __global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads) layer_norm_bwd_kern
       for (int e = 0; e < VEC; ++e) {
         const int c = (i * G + t) * VEC + e;
         if (c < a.C) {
-          part[c] = dw[i * VEC + e];
-          part[a.C + c] = db[i * VEC + e];
+          part[c] = SUMS ? place(0, i * VEC + e)[e % W] : dw[SUMS ? 0 : i * VEC + e];
+          part[a.C + c] = SUMS ? place(1, i * VEC + e)[e % W] : db[SUMS ? 0 : i * VEC + e];
         }
       }
   } else {
@@ -307,8 +482,8 @@ __global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads) layer_norm_bwd_kern
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const int c = (i * G + t) * VEC + e;
-        sums[grp * width + c] = dw[i * VEC + e];
-        sums[(groups + grp) * width + c] = db[i * VEC + e];
+        sums[grp * width + c] = dw[SUMS ? 0 : i * VEC + e];
+        sums[(groups + grp) * width + c] = db[SUMS ? 0 : i * VEC + e];
       }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * width; c += blockDim.x) {
@@ -322,17 +497,18 @@ __global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads) layer_norm_bwd_kern
 }
 
 // The parts [P][2][C] of blockIdx.y's weights, summed in order: 32 columns to a
-// CTA, eight lines of parts
+// CTA, 32 lines of parts
+constexpr int kLines = 32;
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kLines)
     layer_norm_join_kernel(const float* __restrict__ part, T* dw, T* db, int P, int C) {
-  __shared__ float s[2][8][33];
+  __shared__ float s[2][kLines][33];
   const int lane = threadIdx.x % 32, line = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   const float* p = part + (int64_t)blockIdx.y * P * 2 * C;
   float x = 0.f, y = 0.f;
   if (c < C)
 #pragma unroll 4
-    for (int i = line; i < P; i += 8) {
+    for (int i = line; i < P; i += kLines) {
       x += p[(int64_t)i * 2 * C + c];
       y += p[(int64_t)i * 2 * C + C + c];
     }
@@ -344,7 +520,7 @@ __global__ void __launch_bounds__(256)
     if (to != nullptr) {
       float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z += s[line][i][lane];
+      for (int i = 0; i < kLines; ++i) z += s[line][i][lane];
       to[(int64_t)blockIdx.y * C + c] = from_f32<T>(z);
     }
   }
@@ -353,37 +529,39 @@ __global__ void __launch_bounds__(256)
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // How a row is shared out: vectors of 16 bytes where every row starts on such a
-// boundary, else elements; G threads of KV of them.  The backward holds three
-// more numbers to an element, so a thread of it takes half as many.
+// boundary, else elements; G threads of KV of them.
+// In the backward a thread of several warps' rows takes half as many, so that the
+// sums of its columns stay in registers, up to rows of 1024 vectors.
 struct Split {
   bool vec;
   int G, KV;
 };
 Split split(int64_t n, bool vec, bool backward) {  // n: vectors or elements of a row
   if (vec) {
+    if (n <= 4) return {true, 4, 1};
     for (int G = 4; G <= 32; G *= 2)
-      if (n <= G) return {true, G, 1};
-    if (n <= 64) return {true, 32, 2};
+      if (n <= 2 * G) return {true, G, 2};
     if (n <= 128) return {true, 32, 4};
-    for (int G = 64; G <= 512; G *= 2)
-      if (n <= (backward ? 2 : 4) * G) return {true, G, backward ? 2 : 4};
-    if (n <= 2048) return {true, 512, 4};
-    return {true, 1024, n <= 4096 ? 4 : 8};
+    if (backward)
+      for (int G = 128; G <= 512; G *= 2)
+        if (n <= 2 * G) return {true, G, 2};
+    for (int G = 64; G <= 1024; G *= 2)
+      if (n <= 4 * G) return {true, G, 4};
+    return {true, 1024, 8};
   }
   if (n <= 128) return {false, 32, 4};
-  if (n <= 512) return {false, 32, 16};
-  for (int G = 64; G <= 1024; G *= 2)
+  for (int G = 32; G <= 1024; G *= 2)
     if (n <= 16 * G) return {false, G, 16};
   return {false, 1024, 32};
 }
 
-// CTAs to a head in the backward: a few rounds of warps to an SM, and no more
-// than there are rows.  Of the sizes alone, as the workspace is.
-int64_t bwd_ctas(const LayerNorm& f, int G) {
-  const int64_t groups = G > 32 ? 1 : kBwdThreads / G;
-  const int64_t want = (int64_t)kPlanSMs * std::max<int64_t>(1, 16 * 32 / std::max(G, kBwdThreads));
+// CTAs to a head in the backward: as many as an SM holds, and no more than there
+// are rows.  Of the sizes alone, as the workspace is.
+int64_t bwd_ctas(const LayerNorm& f, const Split& s, int64_t V) {
+  const int64_t E = s.KV * (s.vec ? V : 1), groups = s.G > 32 ? 1 : kBwdThreads / s.G;
+  const int64_t per_sm = s.G > 32 ? std::max(1, 512 / s.G) : E <= 8 ? 8 : E <= 16 ? 5 : 3;
   const int64_t rows = (f.B * f.N + groups - 1) / groups;
-  return std::max<int64_t>(1, std::min<int64_t>(rows, (want + f.H - 1) / f.H));
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (kPlanSMs * per_sm + f.H - 1) / f.H));
 }
 
 template <typename T, int VEC, int GL, int KV, int MT>
@@ -395,17 +573,33 @@ cudaError_t forward(const LayerNorm& f, const Args& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int GL, int KV, int MT>
-cudaError_t backward(const LayerNorm& f, const Args& a, cudaStream_t stream) {
+template <typename T, int VEC, int GL, int KV, int MT, bool SUMS = false>
+cudaError_t backward(const LayerNorm& f, const Args& a, const Split& s, cudaStream_t stream) {
   const int threads = MT > 0 ? a.G : kBwdThreads;
-  const unsigned ctas = (unsigned)bwd_ctas(f, a.G);
-  const size_t smem =
-      MT > 0 || a.part == nullptr ? 0 : (size_t)2 * threads * KV * VEC * sizeof(float);
-  layer_norm_bwd_kernel<T, VEC, GL, KV, MT>
-      <<<dim3(ctas, (unsigned)f.H), threads, smem, stream>>>(a);
+  const unsigned ctas = (unsigned)bwd_ctas(f, s, 16 / sizeof(T));
+  const size_t smem = SUMS || (MT == 0 && a.part != nullptr)
+                          ? (size_t)2 * threads * KV * VEC * sizeof(float) : 0;
+  auto kern = f.w != nullptr ? layer_norm_bwd_kernel<T, VEC, GL, KV, MT, SUMS, true>
+                             : layer_norm_bwd_kernel<T, VEC, GL, KV, MT, SUMS, false>;
+  if constexpr (SUMS) {
+    // more than 48 KB wants asking for, once per device
+    static std::atomic<uint64_t> asked_with{0}, asked_without{0};
+    std::atomic<uint64_t>& asked = f.w != nullptr ? asked_with : asked_without;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if ((asked.load(std::memory_order_acquire) & bit) == 0) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               2 * MT * KV * VEC * (int)sizeof(float));
+      if (e != cudaSuccess) return e;
+      asked.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  kern<<<dim3(ctas, (unsigned)f.H), threads, smem, stream>>>(a);
   if (a.part != nullptr) {
     const int heads = f.per_head ? (int)f.H : 1;
-    layer_norm_join_kernel<T><<<dim3((unsigned)((f.C + 31) / 32), heads), 256, 0, stream>>>(
+    layer_norm_join_kernel<T><<<dim3((unsigned)((f.C + 31) / 32), heads), 32 * kLines, 0, stream>>>(
         a.part, static_cast<T*>(f.dw), static_cast<T*>(f.db), (int)(ctas * f.H / heads), a.C);
   }
   return cudaGetLastError();
@@ -439,33 +633,36 @@ cudaError_t run(const LayerNorm& f, void* scratch, bool back, cudaStream_t strea
       if (s.KV == 8) return forward<T, V, 32, 8, 1024>(f, a, stream);
     if (s.G > 512) return forward<T, V, 32, 4, 1024>(f, a, stream);
     if (s.G > 32) return forward<T, V, 32, 4, 512>(f, a, stream);
-    if (s.G == 4) return forward<T, V, 4, 1, 0>(f, a, stream);
-    if (s.G == 8) return forward<T, V, 8, 1, 0>(f, a, stream);
-    if (s.G == 16) return forward<T, V, 16, 1, 0>(f, a, stream);
-    if (s.KV == 1) return forward<T, V, 32, 1, 0>(f, a, stream);
+    if (s.KV == 1) return forward<T, V, 4, 1, 0>(f, a, stream);
+    if (s.G == 4) return forward<T, V, 4, 2, 0>(f, a, stream);
+    if (s.G == 8) return forward<T, V, 8, 2, 0>(f, a, stream);
+    if (s.G == 16) return forward<T, V, 16, 2, 0>(f, a, stream);
     if (s.KV == 2) return forward<T, V, 32, 2, 0>(f, a, stream);
     return forward<T, V, 32, 4, 0>(f, a, stream);
   }
   a.part = f.dw != nullptr || f.db != nullptr ? static_cast<float*>(scratch) : nullptr;
+  // (2 E fp32 sums a thread: 128 KB of shared memory for 16,384 features; past
+  // that they stay in registers, and some of them in local memory)
   if (!vec) {
-    if (s.KV == 32) return backward<T, 1, 32, 32, 1024>(f, a, stream);
-    if (s.G > 512) return backward<T, 1, 32, 16, 1024>(f, a, stream);
-    if (s.G > 32) return backward<T, 1, 32, 16, 512>(f, a, stream);
-    return s.KV == 4 ? backward<T, 1, 32, 4, 0>(f, a, stream)
-                     : backward<T, 1, 32, 16, 0>(f, a, stream);
+    if (s.KV == 32) return backward<T, 1, 32, 32, 1024>(f, a, s, stream);
+    if (s.G > 512) return backward<T, 1, 32, 16, 1024, true>(f, a, s, stream);
+    if (s.G > 32) return backward<T, 1, 32, 16, 512, true>(f, a, s, stream);
+    return s.KV == 4 ? backward<T, 1, 32, 4, 0>(f, a, s, stream)
+                     : backward<T, 1, 32, 16, 0>(f, a, s, stream);
   }
   if constexpr (V == 4)
-    if (s.KV == 8) return backward<T, V, 32, 8, 1024>(f, a, stream);
-  if (s.G > 512) return backward<T, V, 32, 4, 1024>(f, a, stream);
-  if (s.G > 32)
-    return s.KV == 2 ? backward<T, V, 32, 2, 512>(f, a, stream)
-                     : backward<T, V, 32, 4, 512>(f, a, stream);
-  if (s.G == 4) return backward<T, V, 4, 1, 0>(f, a, stream);
-  if (s.G == 8) return backward<T, V, 8, 1, 0>(f, a, stream);
-  if (s.G == 16) return backward<T, V, 16, 1, 0>(f, a, stream);
-  if (s.KV == 1) return backward<T, V, 32, 1, 0>(f, a, stream);
-  if (s.KV == 2) return backward<T, V, 32, 2, 0>(f, a, stream);
-  return backward<T, V, 32, 4, 0>(f, a, stream);
+    if (s.KV == 8) return backward<T, V, 32, 8, 1024>(f, a, s, stream);
+  if (s.G > 512) return backward<T, V, 32, 4, 1024, V == 4>(f, a, s, stream);
+  if (s.KV == 4 && s.G > 32) return backward<T, V, 32, 4, 512, true>(f, a, s, stream);
+  if (s.G > 256) return backward<T, V, 32, 2, 512>(f, a, s, stream);
+  if (s.G > 128) return backward<T, V, 32, 2, 256>(f, a, s, stream);
+  if (s.G > 32) return backward<T, V, 32, 2, 128>(f, a, s, stream);
+  if (s.KV == 1) return backward<T, V, 4, 1, 0>(f, a, s, stream);
+  if (s.G == 4) return backward<T, V, 4, 2, 0>(f, a, s, stream);
+  if (s.G == 8) return backward<T, V, 8, 2, 0>(f, a, s, stream);
+  if (s.G == 16) return backward<T, V, 16, 2, 0>(f, a, s, stream);
+  if (s.KV == 2) return backward<T, V, 32, 2, 0>(f, a, s, stream);
+  return backward<T, V, 32, 4, 0>(f, a, s, stream);
 }
 
 }  // namespace
@@ -473,8 +670,8 @@ cudaError_t run(const LayerNorm& f, void* scratch, bool back, cudaStream_t strea
 // Whether rows move as vectors is known at the call alone: room for either.
 size_t layer_norm_scratch(const LayerNorm& f) {
   const int64_t V = f.dtype == CP_DTYPE_F32 ? 4 : 8;
-  int64_t ctas = bwd_ctas(f, split(f.C, false, true).G);
-  if (f.C % V == 0) ctas = std::max(ctas, bwd_ctas(f, split(f.C / V, true, true).G));
+  int64_t ctas = bwd_ctas(f, split(f.C, false, true), V);
+  if (f.C % V == 0) ctas = std::max(ctas, bwd_ctas(f, split(f.C / V, true, true), V));
   return (size_t)ctas * f.H * 2 * f.C * sizeof(float);
 }
 
