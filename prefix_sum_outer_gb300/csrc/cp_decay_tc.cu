@@ -60,11 +60,12 @@ struct Args {
   const int* lengths;
   const float* state_in;   // may be null (zero)
   float* state_out;        // may be null
-  float* slots;            // [problems][G][DP][64]: sums, then the pieces' first states
+  float* slots;            // [problems][G][sub][DP][64]: sums, then the pieces' first states
   float* out_f32;          // not null: the result goes here in fp32, [BH][N][DC]
   int* status;
   int64_t N, st_r, st_c;   // strides of a state's rows and columns
   int H, Hk, group, BH, n_mb, n_tiles, seg_tiles, G;
+  int sub, sub_tiles;      // parts of a piece in the summing launch, and their tiles
   int DA, DC;
   int a_key, b_key, c_key, o_key;   // whether an array has key heads
   int reverse;
@@ -79,12 +80,12 @@ struct Layout {
   static constexpr int kBoxesPerTile = AGG ? 1 : kABoxes + 1;  // of the A / C ring
   static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
   static constexpr int kQuarter = kBoxBytes / 4;               // a part of 32 rows of C'
-  static constexpr int NV = DP == 128 && PARTS == 3 ? 2 : 4;   // buffers of 32 rows of C'
+  static constexpr int NV = AGG || (DP == 128 && PARTS == 3) ? 2 : 4;  // buffers of 32 rows of C'
   static constexpr int kVBytes = NV * PARTS * kQuarter;
   static constexpr int kTotal = (kSmemLimit - 1024 - kBarBytes - kTableBytes) / kBoxBytes;  // boxes
   static constexpr int NSB = 1;                                // copies of S
   static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
-  static constexpr int NB = 2;                                 // stages of the B ring
+  static constexpr int NB = AGG && DP == 128 ? 1 : 2;          // stages of the B ring
   static constexpr int R =
       AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
   static constexpr int kBoxes = NB * kABoxes + R + kSBoxes;
@@ -156,7 +157,7 @@ __device__ __forceinline__ void fewer_registers() {
 }
 
 template <int DP, int PARTS, bool AGG>
-__global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
+__global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     decay_tc_kernel(const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_c,
@@ -198,8 +199,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   const int mb = idx % a.n_mb;
   idx /= a.n_mb;
   const int bh = idx % a.BH;
-  int seg = idx / a.BH;
-  if (AGG && a.reverse) seg += 1;  // the first piece in scan order needs no sum of others
+  int seg = idx / a.BH, part = 0;
+  if (AGG) {
+    part = seg % a.sub;
+    seg = seg / a.sub + (a.reverse ? 1 : 0);  // (nothing follows the last in scan order)
+  }
   const int b = bh / a.H, h = bh % a.H;
   const bool rev = a.reverse != 0;
 
@@ -264,7 +268,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   // ---- the piece's tiles: those that hold rows, in scan order
   const int64_t rows = rows_of(a.lengths, b, a.N);
   const int live = (int)((rows + kTile - 1) / kTile);
-  const int t_first = seg * a.seg_tiles, t_stop = min(a.n_tiles, t_first + a.seg_tiles);
+  const int t_first = seg * a.seg_tiles + (AGG ? part * a.sub_tiles : 0);
+  const int t_stop = min(a.n_tiles, min((seg + 1) * a.seg_tiles, t_first + (AGG ? a.sub_tiles : a.seg_tiles)));
   const int t_end = max(t_first, min(t_stop, live));
   const int n_it = t_end - t_first;
   auto tile_of = [&](int it) { return rev ? t_end - 1 - it : t_first + it; };
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   const int n_kv = hands_on ? n_it : n_it - 1;
 
   if (warp < 4) {
-    if constexpr (!AGG) fewer_registers<40>();
+    fewer_registers<40>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
@@ -481,14 +486,15 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------- state group
-    if constexpr (!AGG) more_registers<(DP == 64 ? 88 : 136)>();
+    more_registers<(AGG ? 104 : 88) + (DP == 64 ? 0 : AGG ? 16 : 48)>();
     {
       // thread: a row of S; with 64 rows two threads share one, half of its
       // columns each
       constexpr int SC = L::SC;
       const int d = DP == 64 ? row & 63 : row, c0 = DP == 64 ? (row >> 6) * SC : 0;
       const int pidx = bh * a.n_mb + mb, m0 = mb * kMB + c0;
-      float* slot = a.slots + (((int64_t)pidx * a.G + seg) * DP + d) * kMB + c0;
+      const int at = AGG ? part : rev ? a.sub - 1 : 0;  // where the prefix launch leaves a piece's first state
+      float* slot = a.slots + ((((int64_t)pidx * a.G + seg) * a.sub + at) * DP + d) * kMB + c0;
       float2 S[SC / 2];
       const bool first_seg = rev ? seg == a.G - 1 : seg == 0;
       if (!AGG && !first_seg) {
@@ -586,10 +592,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
     }
   } else if (warp >= L::kVGroup) {
     // -------------------------------- C' groups: every other 32 rows of a tile
-    if constexpr (!AGG) {
-      if constexpr (DP == 64) fewer_registers<56>();
-      else fewer_registers<40>();
-    }
+    fewer_registers<DP == 64 ? 56 : AGG ? 48 : 40>();
     const int half = (warp - L::kVGroup) / 4;
     const int tid = threadIdx.x - 32 * L::kVGroup - 128 * half;
     bool ok = true;
@@ -840,44 +843,64 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, 1)
   }
 }
 
-// Pieces' sums [problems][G][E] become, in place, the states the pieces start
-// from: a thread walks one element over the pieces, in scan order.
+// Sums [problems][G][sub][E] of the pieces' parts give the states the pieces start
+// from, each in the place of its piece's first part in scan order: a thread walks
+// one element over the parts, whose loads go out ahead.
 struct PrefixArgs {
   const float* g;
   const int* lengths;
   const float* state_in;
   float* slots;
   int64_t N, st_r, st_c;
-  int H, BH, n_mb, seg_tiles, G, DA, DC, DP, reverse;
+  int H, BH, n_mb, n_tiles, seg_tiles, G, sub, sub_tiles, DA, DC, DP, reverse;
 };
 __global__ void __launch_bounds__(256) decay_tc_prefix_kernel(const PrefixArgs a) {
   const int E = a.DP * kMB, per = E / 256;
   const int problem = blockIdx.x / per, e = (blockIdx.x % per) * 256 + threadIdx.x;
   const int bh = problem / a.n_mb, mb = problem % a.n_mb;
   const float g = head_decay(a.g[bh % a.H]);
-  const int64_t rows = rows_of(a.lengths, bh / a.H, a.N), len = (int64_t)a.seg_tiles * kTile;
+  const int64_t rows = rows_of(a.lengths, bh / a.H, a.N);
   const int r = e / kMB, c = mb * kMB + e % kMB;
-  float* s = a.slots + (int64_t)problem * a.G * E + e;
+  float* s = a.slots + (int64_t)problem * a.G * a.sub * E + e;
   float S = 0.f;
   if (a.state_in != nullptr && r < a.DA && c < a.DC)
     S = a.state_in[(int64_t)bh * a.DA * a.DC + r * a.st_r + c * a.st_c];
-  float sum = s[(int64_t)(a.reverse ? a.G - 1 : 0) * E];
-  for (int i = 0; i < a.G - 1; ++i) {
-    const int seg = a.reverse ? a.G - 1 - i : i, next = a.reverse ? seg - 1 : seg + 1;
-    const int64_t n = min(rows, (seg + 1) * len) - seg * len;  // rows of the piece
-    if (n > 0) {
-      const int sh = a.reverse && rows <= (seg + 1) * len ? 1 : 0;
-      const float2 f = power_parts(g, (int)n - sh);
-      S = fmaf(f.x, S, fmaf(f.y, S, sum));
+  const int n = (a.G - 1) * a.sub;  // parts that were summed, in scan order
+  auto slot = [&](int i) { return a.reverse ? a.G * a.sub - 1 - i : i; };
+  constexpr int kAhead = 4;
+  float next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) next[i] = i < n ? s[(int64_t)slot(i) * E] : 0.f;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    float now[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      now[i] = next[i];
+      next[i] = i0 + kAhead + i < n ? s[(int64_t)slot(i0 + kAhead + i) * E] : 0.f;
     }
-    if (i < a.G - 2) sum = s[(int64_t)next * E];
-    s[(int64_t)next * E] = S;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= n) break;
+      const int at = slot(i0 + i), seg = at / a.sub, part = at % a.sub;
+      const int64_t t0 = (int64_t)seg * a.seg_tiles + part * a.sub_tiles;
+      const int64_t t1 = min((int64_t)a.n_tiles, min((int64_t)(seg + 1) * a.seg_tiles, t0 + a.sub_tiles));
+      const int64_t lo = t0 * kTile, hi = min(rows, t1 * kTile);  // the part's rows
+      if (hi > lo) {
+        const int sh = a.reverse && rows == hi ? 1 : 0;
+        const float2 f = power_parts(g, (int)(hi - lo) - sh);
+        S = fmaf(f.x, S, fmaf(f.y, S, now[i]));
+      }
+      // (the next piece's first sum is read by now: it is among those ahead, or is
+      // not wanted)
+      const int to = a.reverse ? at - 1 : at + 1;
+      if (part == (a.reverse ? 0 : a.sub - 1)) s[(int64_t)to * E] = S;
+    }
   }
 }
 
 // ---------------------------------------------------------------- host
 struct Plan {
-  int DP, n_mb, n_tiles, seg_tiles, G;
+  int DP, n_mb, n_tiles, seg_tiles, G, sub, sub_tiles;
   int64_t problems;
   size_t slot_bytes;
 };
@@ -892,7 +915,12 @@ Plan plan(const DecayShape& s, int64_t DA, int64_t DC) {
   G = std::min<int64_t>(G, std::max(1, p.n_tiles));
   p.seg_tiles = (int)((p.n_tiles + G - 1) / G);
   p.G = (p.n_tiles + p.seg_tiles - 1) / p.seg_tiles;
-  p.slot_bytes = p.G > 1 ? sizeof(float) * (size_t)p.problems * p.G * p.DP * kMB : 0;
+  // the summing launch has two CTAs to an SM
+  const int64_t sums = p.problems * (p.G - 1);
+  const int64_t sub = sums > 0 ? std::max<int64_t>(1, 2 * kPlanSMs / sums) : 1;
+  p.sub_tiles = (int)std::max<int64_t>(1, (p.seg_tiles + sub - 1) / sub);
+  p.sub = (p.seg_tiles + p.sub_tiles - 1) / p.sub_tiles;
+  p.slot_bytes = p.G > 1 ? sizeof(float) * (size_t)p.problems * p.G * p.sub * p.DP * kMB : 0;
   return p;
 }
 
@@ -952,20 +980,22 @@ cp_status_t run(const DecayShape& s, const float* g, const Product& p, float* sl
   a.st_c = p.turned ? p.DA : 1;
   a.H = (int)s.H; a.Hk = (int)s.Hk; a.group = (int)(s.H / s.Hk); a.BH = (int)vh;
   a.n_mb = pl.n_mb; a.n_tiles = pl.n_tiles; a.seg_tiles = pl.seg_tiles; a.G = pl.G;
+  a.sub = pl.sub; a.sub_tiles = pl.sub_tiles;
   a.DA = (int)p.DA; a.DC = (int)p.DC;
   a.a_key = p.a_key; a.b_key = p.b_key; a.c_key = p.c_key; a.o_key = p.o_key;
   a.reverse = p.reverse;
   a.s_p = p.s_p; a.s_o = p.s_o; a.s_c = p.s_c;
-  const unsigned sums = (unsigned)(pl.problems * (pl.G - 1)), all = (unsigned)(pl.problems * pl.G);
+  const unsigned sums = (unsigned)(pl.problems * (pl.G - 1) * pl.sub), all = (unsigned)(pl.problems * pl.G);
   cudaError_t e = cudaSuccess;
 #define CP_DECAY_CASE(DP_, PARTS_)                                                          \
   if (pl.DP == DP_ && (p.state_out != nullptr ? 3 : 2) == PARTS_) {                         \
     if (pl.G > 1) {                                                                         \
       e = launch<DP_, PARTS_, true>(ma, mb, mc, mo, a, sums, stream);                       \
       if (e != cudaSuccess) return CP_ERR_CUDA;                                             \
-      const PrefixArgs x{g,       s.lengths, p.state_in, slots,        s.N,   a.st_r, a.st_c, \
-                         a.H,     a.BH,      a.n_mb,     a.seg_tiles,  a.G,   a.DA,   a.DC, \
-                         DP_,     a.reverse};                                               \
+      const PrefixArgs x{g,       s.lengths, p.state_in,  slots,   s.N,   a.st_r,        \
+                         a.st_c,  a.H,       a.BH,        a.n_mb,  a.n_tiles, a.seg_tiles, \
+                         a.G,     a.sub,     a.sub_tiles, a.DA,    a.DC,  DP_,           \
+                         a.reverse};                                                     \
       decay_tc_prefix_kernel<<<(unsigned)(pl.problems * DP_ * kMB / 256), 256, 0, stream>>>(x); \
       if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;                            \
     }                                                                                       \

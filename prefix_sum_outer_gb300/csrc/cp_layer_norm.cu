@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
 
 // CTAs to an SM
 template <int VEC, int KV, int MT>
-constexpr int kBwdMin = MT > 0 ? (MT <= 512 ? 512 / MT : 1) : KV * VEC <= 8 ? 8 : KV * VEC <= 16 ? 5 : 3;
+constexpr int kBwdMin = MT > 0 ? (MT <= 512 ? 512 / MT : 1) : KV * VEC <= 8 ? 8 : KV * VEC <= 16 ? 4 : 2;
 
 // Rows first, first + step, ... of a head's B * N: a row's offset in a tensor goes
 // by steps, without a division a row.
@@ -559,7 +559,7 @@ Split split(int64_t n, bool vec, bool backward) {  // n: vectors or elements of 
 // are rows.  Of the sizes alone, as the workspace is.
 int64_t bwd_ctas(const LayerNorm& f, const Split& s, int64_t V) {
   const int64_t E = s.KV * (s.vec ? V : 1), groups = s.G > 32 ? 1 : kBwdThreads / s.G;
-  const int64_t per_sm = s.G > 32 ? std::max(1, 512 / s.G) : E <= 8 ? 8 : E <= 16 ? 5 : 3;
+  const int64_t per_sm = s.G > 32 ? std::max(1, 512 / s.G) : E <= 8 ? 8 : E <= 16 ? 4 : 2;
   const int64_t rows = (f.B * f.N + groups - 1) / groups;
   return std::max<int64_t>(1, std::min<int64_t>(rows, (kPlanSMs * per_sm + f.H - 1) / f.H));
 }
