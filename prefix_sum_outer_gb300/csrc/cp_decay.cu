@@ -6,6 +6,9 @@
 //           state (one fma a chunk, the decay as hi + lo);
 //   out     the chunks' rows from their decayed scores and the state, a CTA per
 //           chunk and 64 columns.
+// A sequence of one chunk needs no prefix: out reads the given states, and sums,
+// launched where a state is wanted, writes it.
+//
 // Backward, the two directions' sums and prefixes and the three products (dq, dk,
 // dv) share the launches; dq and dk of a key head walk its value heads inside
 // the CTA, in order.  Only the prefix is sequential, so short calls of few heads
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   const int h = (int)(bh % a.H);
   const int64_t rows = rows_of(a.lengths, b, a.N);
   const int nv = (int)max((int64_t)0, min((int64_t)kC, rows - c * kC));
-  if (nv == 0) return;
+  if (nv == 0 && a.n > 1) return;
   const int mb = (a.M + kC - 1) / kC;
   const int d0 = (blockIdx.y / mb) * kC, m0 = (blockIdx.y % mb) * kC;
   const int64_t row0 = bh * a.N + c * kC, krow0 = (b * a.Hk + h / a.group) * a.N + c * kC;
@@ -124,7 +127,15 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   float2 acc[4][4];
   clear(acc);
   gemm(acc, x.x, y.x, nv, rg, cg);
-  float* s = (rev ? a.rev : a.fwd) + (bh * a.n + c) * (int64_t)a.D * a.M;
+  const bool end = a.n == 1;  // the state after the only chunk, itself
+  float* s = end ? (rev ? a.ds0 : a.s_end) : (rev ? a.rev : a.fwd);
+  if (s == nullptr) return;
+  s += (bh * a.n + c) * (int64_t)a.D * a.M;
+  const float* from = !end || (rev ? a.gs : a.s0) == nullptr
+                          ? nullptr : (rev ? a.gs : a.s0) + bh * (int64_t)a.D * a.M;
+  // (dL/dS_0 is a times the gradient seen from the first row)
+  const float2 keep = power_parts(g, nv);
+  const float by = rev && nv > 0 ? power(g, 1) : 1.f;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const int d = d0 + rg * 8 + r;
@@ -132,7 +143,13 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + cg * 4 + i;
-      if (m < a.M) s[(int64_t)d * a.M + m] = r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x;
+      if (m >= a.M) continue;
+      float x = r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x;
+      if (end) {
+        const float S = from == nullptr ? 0.f : from[(int64_t)d * a.M + m];
+        x = fmaf(keep.x, S, fmaf(keep.y, S, by * x));
+      }
+      s[(int64_t)d * a.M + m] = x;
     }
   }
 }
@@ -252,7 +269,9 @@ __global__ void __launch_bounds__(kThreads) decay_out_kernel(const Args a) {
     __syncthreads();
     gemm(acc, P.x, y.x, nv, rg, cg);
     // the state's part
-    const float* s = (rev ? a.rev : a.fwd) + ((b * a.H + h) * a.n + c) * (int64_t)a.D * a.M;
+    const float* s = a.n > 1 ? (rev ? a.rev : a.fwd) : (rev ? a.gs : a.s0);
+    if (s == nullptr) continue;
+    s += ((b * a.H + h) * a.n + c) * (int64_t)a.D * a.M;
     for (int k0 = 0; k0 < DA; k0 += kK) {
       __syncthreads();
       load_turned<T>(x, pa, DA, k0, nv, f);
@@ -292,6 +311,7 @@ __global__ void __launch_bounds__(kThreads) decay_out_kernel(const Args a) {
 int64_t chunks(const DecayShape& s) { return (s.N + kC - 1) / kC; }
 
 size_t states_bytes(const DecayShape& s) {
+  if (chunks(s) == 1) return 0;
   return (size_t)chunks(s) * s.B * s.H * s.D * s.M * sizeof(float);
 }
 
@@ -301,9 +321,12 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   const unsigned dirs = a.backward ? 2 : 1;
   const unsigned db = (a.D + kC - 1) / kC, mb = (a.M + kC - 1) / kC;
   if (BH * a.n > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-  decay_sums_kernel<T><<<dim3((unsigned)(BH * a.n), db * mb, dirs), kThreads, 0, stream>>>(a);
-  const int blocks = (a.D * a.M + 255) / 256;
-  decay_prefix_kernel<<<dim3((unsigned)(BH * blocks), dirs), 256, 0, stream>>>(a, blocks);
+  if (a.n > 1 || (a.backward ? a.ds0 : a.s_end) != nullptr)
+    decay_sums_kernel<T><<<dim3((unsigned)(BH * a.n), db * mb, dirs), kThreads, 0, stream>>>(a);
+  if (a.n > 1) {
+    const int blocks = (a.D * a.M + 255) / 256;
+    decay_prefix_kernel<<<dim3((unsigned)(BH * blocks), dirs), 256, 0, stream>>>(a, blocks);
+  }
   decay_out_kernel<T>
       <<<dim3((unsigned)(BH * a.n), a.backward ? std::max(db, mb) : mb, a.backward ? 3 : 1),
          kThreads, 0, stream>>>(a);

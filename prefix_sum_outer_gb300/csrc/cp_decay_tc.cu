@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 
 // Sums [problems][G][sub][E] of the pieces' parts give the states the pieces start
 // from, each in the place of its piece's first part in scan order: a thread walks
-// one element over the parts, whose loads go out ahead.
+// four elements over the parts, whose loads go out ahead.
 struct PrefixArgs {
   const float* g;
   const int* lengths;
@@ -854,46 +854,54 @@ struct PrefixArgs {
   int64_t N, st_r, st_c;
   int H, BH, n_mb, n_tiles, seg_tiles, G, sub, sub_tiles, DA, DC, DP, reverse;
 };
-__global__ void __launch_bounds__(256) decay_tc_prefix_kernel(const PrefixArgs a) {
-  const int E = a.DP * kMB, per = E / 256;
-  const int problem = blockIdx.x / per, e = (blockIdx.x % per) * 256 + threadIdx.x;
+constexpr int kPrefixThreads = 128;
+__global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const PrefixArgs a) {
+  const int E4 = a.DP * kMB / 4, per = E4 / kPrefixThreads;
+  const int problem = blockIdx.x / per, e = (blockIdx.x % per) * kPrefixThreads + threadIdx.x;
   const int bh = problem / a.n_mb, mb = problem % a.n_mb;
+  float4* s = reinterpret_cast<float4*>(a.slots) + (int64_t)problem * a.G * a.sub * E4 + e;
+  const int n = (a.G - 1) * a.sub;  // parts that were summed, in scan order
+  grid_dep_wait();
+  auto slot = [&](int i) { return (int64_t)(a.reverse ? a.G * a.sub - 1 - i : i); };
+  constexpr int kAhead = 8;
+  float4 next[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) next[i] = i < n ? s[slot(i) * E4] : float4{};
   const float g = head_decay(a.g[bh % a.H]);
   const int64_t rows = rows_of(a.lengths, bh / a.H, a.N);
-  const int r = e / kMB, c = mb * kMB + e % kMB;
-  float* s = a.slots + (int64_t)problem * a.G * a.sub * E + e;
-  float S = 0.f;
-  if (a.state_in != nullptr && r < a.DA && c < a.DC)
-    S = a.state_in[(int64_t)bh * a.DA * a.DC + r * a.st_r + c * a.st_c];
-  const int n = (a.G - 1) * a.sub;  // parts that were summed, in scan order
-  auto slot = [&](int i) { return a.reverse ? a.G * a.sub - 1 - i : i; };
-  constexpr int kAhead = 4;
-  float next[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) next[i] = i < n ? s[(int64_t)slot(i) * E] : 0.f;
+  const int r = 4 * e / kMB, c = mb * kMB + 4 * e % kMB;
+  float4 S{};
+  if (a.state_in != nullptr && r < a.DA && c < a.DC) {  // (columns come in eights)
+    const float* p = a.state_in + (int64_t)bh * a.DA * a.DC + r * a.st_r + c * a.st_c;
+    S = make_float4(p[0], p[a.st_c], p[2 * a.st_c], p[3 * a.st_c]);
+  }
+  const float2 whole = power_parts(g, a.sub_tiles * kTile);
   for (int i0 = 0; i0 < n; i0 += kAhead) {
-    float now[kAhead];
+    float4 now[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       now[i] = next[i];
-      next[i] = i0 + kAhead + i < n ? s[(int64_t)slot(i0 + kAhead + i) * E] : 0.f;
+      next[i] = i0 + kAhead + i < n ? s[slot(i0 + kAhead + i) * E4] : float4{};
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (i0 + i >= n) break;
-      const int at = slot(i0 + i), seg = at / a.sub, part = at % a.sub;
+#pragma unroll 1
+    for (int i = 0; i < kAhead && i0 + i < n; ++i) {
+      const int at = (int)slot(i0 + i), seg = at / a.sub, part = at % a.sub;
       const int64_t t0 = (int64_t)seg * a.seg_tiles + part * a.sub_tiles;
       const int64_t t1 = min((int64_t)a.n_tiles, min((int64_t)(seg + 1) * a.seg_tiles, t0 + a.sub_tiles));
       const int64_t lo = t0 * kTile, hi = min(rows, t1 * kTile);  // the part's rows
+      float4 x = now[0];
       if (hi > lo) {
-        const int sh = a.reverse && rows == hi ? 1 : 0;
-        const float2 f = power_parts(g, (int)(hi - lo) - sh);
-        S = fmaf(f.x, S, fmaf(f.y, S, now[i]));
+        const int m = (int)(hi - lo) - (a.reverse && rows == hi ? 1 : 0);
+        const float2 f = m == a.sub_tiles * kTile ? whole : power_parts(g, m);
+        S.x = fmaf(f.x, S.x, fmaf(f.y, S.x, x.x));
+        S.y = fmaf(f.x, S.y, fmaf(f.y, S.y, x.y));
+        S.z = fmaf(f.x, S.z, fmaf(f.y, S.z, x.z));
+        S.w = fmaf(f.x, S.w, fmaf(f.y, S.w, x.w));
       }
-      // (the next piece's first sum is read by now: it is among those ahead, or is
-      // not wanted)
-      const int to = a.reverse ? at - 1 : at + 1;
-      if (part == (a.reverse ? 0 : a.sub - 1)) s[(int64_t)to * E] = S;
+#pragma unroll
+      for (int y = 0; y + 1 < kAhead; ++y) now[y] = now[y + 1];
+      // (the next piece's first sum has been read, being among those ahead)
+      if (part == (a.reverse ? 0 : a.sub - 1)) s[(int64_t)(a.reverse ? at - 1 : at + 1) * E4] = S;
     }
   }
 }
@@ -996,9 +1004,11 @@ cp_status_t run(const DecayShape& s, const float* g, const Product& p, float* sl
                          a.st_c,  a.H,       a.BH,        a.n_mb,  a.n_tiles, a.seg_tiles, \
                          a.G,     a.sub,     a.sub_tiles, a.DA,    a.DC,  DP_,           \
                          a.reverse};                                                     \
-      decay_tc_prefix_kernel<<<(unsigned)(pl.problems * DP_ * kMB / 256), 256, 0, stream>>>(x); \
-      if (cudaGetLastError() != cudaSuccess) return CP_ERR_CUDA;                            \
-    }                                                                                       \
+      e = launch_dependent(decay_tc_prefix_kernel,                                       \
+                           dim3((unsigned)(pl.problems * DP_ * kMB / 4 / kPrefixThreads)),  \
+                           kPrefixThreads, 0, stream, x);                                \
+      if (e != cudaSuccess) return CP_ERR_CUDA;                                          \
+    }                                                                                    \
     e = launch<DP_, PARTS_, false>(ma, mb, mc, mo, a, all, stream);                         \
   }
   CP_DECAY_CASE(64, 2)
