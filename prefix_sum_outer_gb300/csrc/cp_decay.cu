@@ -47,11 +47,11 @@ struct Tile {
   float x[kC][kLd];
 };
 
-// acc(8 x 4) += x^T y over K rows of two shared tiles
+// acc(8 x 4) += x^T y over rows k0 .. k1 - 1 of two shared tiles
 __device__ __forceinline__ void gemm(float2 (&acc)[4][4], const float (*x)[kLd],
-                                     const float (*y)[kLd], int K, int rg, int cg) {
+                                     const float (*y)[kLd], int k0, int k1, int rg, int cg) {
 #pragma unroll 4
-  for (int k = 0; k < K; ++k) {
+  for (int k = k0; k < k1; ++k) {
     const float4 a0 = *reinterpret_cast<const float4*>(&x[k][rg * 8]);
     const float4 a1 = *reinterpret_cast<const float4*>(&x[k][rg * 8 + 4]);
     const float4 b = *reinterpret_cast<const float4*>(&y[k][cg * 4]);
@@ -72,29 +72,118 @@ __device__ __forceinline__ void clear(float2 (&acc)[4][4]) {
     for (int c = 0; c < 4; ++c) acc[r][c] = make_float2(0.f, 0.f);
 }
 
-// [row][col] of a row array -> tile[col][row]: columns c0 .. c0 + kK - 1, rows
-// past nv and columns past C as zero; a row's factor f[row] where given
+// A block on its way from global to shared memory, in registers: its loads go out
+// together, and under the products on the block before it.  A thread moves four
+// neighbours at a time, by one load where rows are whole fours.
+constexpr int kTurned = kC * kK / kThreads / 4, kWhole = kC * kC / kThreads / 4;  // fours to a thread
+
 template <typename T>
-__device__ __forceinline__ void load_turned(float (*t)[kLd], const T* p, int C, int c0, int nv,
-                                            const float* f) {
-#pragma unroll 4
-  for (int i = threadIdx.x; i < kC * kK; i += kThreads) {
-    const int c = i % kK, r = i / kK;
-    float x = r < nv && c0 + c < C ? ld_f32<T>(p + (int64_t)r * C + c0 + c) : 0.f;
-    if (f != nullptr) x *= f[r];
-    t[c][r] = x;
+__device__ __forceinline__ float4 ld4(const T* p, int left, bool vec) {
+  if (left <= 0) return make_float4(0.f, 0.f, 0.f, 0.f);
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+      return *reinterpret_cast<const float4*>(p);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      const T* t = reinterpret_cast<const T*>(&w);
+      return make_float4(ld_f32<T>(t), ld_f32<T>(t + 1), ld_f32<T>(t + 2), ld_f32<T>(t + 3));
+    }
+  }
+  return make_float4(ld_f32<T>(p), left > 1 ? ld_f32<T>(p + 1) : 0.f, left > 2 ? ld_f32<T>(p + 2) : 0.f,
+                     left > 3 ? ld_f32<T>(p + 3) : 0.f);
+}
+
+template <typename T>
+__device__ __forceinline__ void st4(T* p, const float (&v)[4], int left, bool vec) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint2 w;
+      T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = from_f32<T>(v[i]);
+      *reinterpret_cast<uint2*>(p) = w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) p[i] = from_f32<T>(v[i]);
+}
+
+// columns c0 .. c0 + kK - 1 of 64 rows, rows past nv and columns past C as zero, to
+// tile[col][row], a row's factor f[row] applied where given
+template <typename T>
+__device__ __forceinline__ void fetch_turned(float4 (&v)[kTurned], const T* p, int C, int c0, int nv) {
+  const int c = 4 * (threadIdx.x % (kK / 4));
+#pragma unroll
+  for (int i = 0; i < kTurned; ++i) {
+    const int r = threadIdx.x / (kK / 4) + i * (kThreads / (kK / 4));
+    v[i] = ld4<T>(p + (int64_t)r * C + c0 + c, r < nv ? C - c0 - c : 0, C % 4 == 0);
   }
 }
-// [row][col] -> tile[row][col]: 64 columns from c0
+__device__ __forceinline__ void put_turned(float (*t)[kLd], const float4 (&v)[kTurned], const float* f) {
+  const int c = 4 * (threadIdx.x % (kK / 4));
+#pragma unroll
+  for (int i = 0; i < kTurned; ++i) {
+    const int r = threadIdx.x / (kK / 4) + i * (kThreads / (kK / 4));
+    const float by = f != nullptr ? f[r] : 1.f;
+    t[c][r] = v[i].x * by;
+    t[c + 1][r] = v[i].y * by;
+    t[c + 2][r] = v[i].z * by;
+    t[c + 3][r] = v[i].w * by;
+  }
+}
+// 64 columns from c0 of 64 rows, to tile[row][col]
 template <typename T>
-__device__ __forceinline__ void load_rows(float (*t)[kLd], const T* p, int C, int c0, int nv,
-                                          const float* f) {
-#pragma unroll 4
-  for (int i = threadIdx.x; i < kC * kC; i += kThreads) {
-    const int c = i % kC, r = i / kC;
-    float x = r < nv && c0 + c < C ? ld_f32<T>(p + (int64_t)r * C + c0 + c) : 0.f;
-    if (f != nullptr) x *= f[r];
-    t[r][c] = x;
+__device__ __forceinline__ void fetch_rows(float4 (&v)[kWhole], const T* p, int C, int c0, int nv) {
+  const int c = 4 * (threadIdx.x % (kC / 4));
+#pragma unroll
+  for (int i = 0; i < kWhole; ++i) {
+    const int r = threadIdx.x / (kC / 4) + i * (kThreads / (kC / 4));
+    v[i] = ld4<T>(p + (int64_t)r * C + c0 + c, r < nv ? C - c0 - c : 0, C % 4 == 0);
+  }
+}
+__device__ __forceinline__ void put_rows(float (*t)[kLd], const float4 (&v)[kWhole], const float* f) {
+  const int c = 4 * (threadIdx.x % (kC / 4));
+#pragma unroll
+  for (int i = 0; i < kWhole; ++i) {
+    const int r = threadIdx.x / (kC / 4) + i * (kThreads / (kC / 4));
+    const float by = f != nullptr ? f[r] : 1.f;
+    *reinterpret_cast<float4*>(&t[r][c]) =
+        make_float4(v[i].x * by, v[i].y * by, v[i].z * by, v[i].w * by);
+  }
+}
+// rows k0 .. k0 + kK - 1 of 64 columns from c0 of a state [.][M], or of its
+// transpose, to tile[row][col]
+__device__ __forceinline__ void fetch_state(float4 (&v)[kTurned], const float* s, int M, bool turned,
+                                            int DA, int DC, int k0, int c0) {
+#pragma unroll
+  for (int i = 0; i < kTurned; ++i) {
+    const int j = threadIdx.x + i * kThreads;
+    if (turned) {
+      const int k = k0 + 4 * (j % (kK / 4)), c = c0 + j / (kK / 4);
+      v[i] = ld4<float>(s + (int64_t)c * M + k, c < DC ? DA - k : 0, M % 4 == 0);
+    } else {
+      const int k = k0 + j / (kC / 4), c = c0 + 4 * (j % (kC / 4));
+      v[i] = ld4<float>(s + (int64_t)k * M + c, k < DA ? DC - c : 0, M % 4 == 0);
+    }
+  }
+}
+__device__ __forceinline__ void put_state(float (*t)[kLd], const float4 (&v)[kTurned], bool turned) {
+#pragma unroll
+  for (int i = 0; i < kTurned; ++i) {
+    const int j = threadIdx.x + i * kThreads;
+    if (turned) {
+      const int k = 4 * (j % (kK / 4)), c = j / (kK / 4);
+      t[k][c] = v[i].x;
+      t[k + 1][c] = v[i].y;
+      t[k + 2][c] = v[i].z;
+      t[k + 3][c] = v[i].w;
+    } else {
+      *reinterpret_cast<float4*>(&t[j / (kC / 4)][4 * (j % (kC / 4))]) = v[i];
+    }
   }
 }
 
@@ -113,20 +202,21 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   const int d0 = (blockIdx.y / mb) * kC, m0 = (blockIdx.y % mb) * kC;
   const int64_t row0 = bh * a.N + c * kC, krow0 = (b * a.Hk + h / a.group) * a.N + c * kC;
   const float g = head_decay(a.g[h]);
+  float4 vx[kWhole], vy[kWhole];
+  fetch_rows<T>(vx, static_cast<const T*>(rev ? a.q : a.k) + krow0 * a.D, a.D, d0, nv);
+  fetch_rows<T>(vy, static_cast<const T*>(rev ? a.go : a.v) + row0 * a.M, a.M, m0, nv);
   if (threadIdx.x < kC) {
     const int r = threadIdx.x;
     f[r] = r < nv ? (rev ? a.scale * power(g, r) : power(g, nv - 1 - r)) : 0.f;
   }
   __syncthreads();
-  const T* xr = static_cast<const T*>(rev ? a.q : a.k) + krow0 * a.D;
-  const T* yr = static_cast<const T*>(rev ? a.go : a.v) + row0 * a.M;
-  load_rows<T>(x.x, xr, a.D, d0, nv, f);
-  load_rows<T>(y.x, yr, a.M, m0, nv, nullptr);
+  put_rows(x.x, vx, f);
+  put_rows(y.x, vy, nullptr);
   __syncthreads();
   const int cg = threadIdx.x % 16, rg = threadIdx.x / 16;
   float2 acc[4][4];
   clear(acc);
-  gemm(acc, x.x, y.x, nv, rg, cg);
+  gemm(acc, x.x, y.x, 0, nv, rg, cg);
   const bool end = a.n == 1;  // the state after the only chunk, itself
   float* s = end ? (rev ? a.ds0 : a.s_end) : (rev ? a.rev : a.fwd);
   if (s == nullptr) return;
@@ -138,19 +228,18 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   const float by = rev && nv > 0 ? power(g, 1) : 1.f;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const int d = d0 + rg * 8 + r;
-    if (d >= a.D) continue;
+    const int d = d0 + rg * 8 + r, m = m0 + cg * 4;
+    if (d >= a.D || m >= a.M) continue;
+    float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int m = m0 + cg * 4 + i;
-      if (m >= a.M) continue;
-      float x = r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x;
+      v[i] = r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x;
       if (end) {
-        const float S = from == nullptr ? 0.f : from[(int64_t)d * a.M + m];
-        x = fmaf(keep.x, S, fmaf(keep.y, S, by * x));
+        const float S = from == nullptr || m + i >= a.M ? 0.f : from[(int64_t)d * a.M + m + i];
+        v[i] = fmaf(keep.x, S, fmaf(keep.y, S, by * v[i]));
       }
-      s[(int64_t)d * a.M + m] = x;
     }
+    st4<float>(s + (int64_t)d * a.M + m, v, a.M - m, a.M % 4 == 0);
   }
 }
 
@@ -202,7 +291,7 @@ __global__ void __launch_bounds__(256) decay_prefix_kernel(const Args a, int blo
 
 // out: blockIdx.y = 64 columns of the result, z = product
 template <typename T>
-__global__ void __launch_bounds__(kThreads) decay_out_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) decay_out_kernel(const Args a) {
   __shared__ __align__(16) float x[kK][kLd];
   __shared__ __align__(16) Tile y, P;
   __shared__ float pw[kC + 1], f[kC];
@@ -246,14 +335,23 @@ __global__ void __launch_bounds__(kThreads) decay_out_kernel(const Args a) {
                        : a.scale * power(g, r + 1);
     }
     // scores
+    float4 va[kTurned], vb[kTurned], vc[kWhole];
+    fetch_turned<T>(va, pa, DA, 0, nv);
+    fetch_turned<T>(vb, pb, DA, 0, nv);
     float2 p[4][4];
     clear(p);
     for (int k0 = 0; k0 < DA; k0 += kK) {
       __syncthreads();
-      load_turned<T>(x, pa, DA, k0, nv, nullptr);
-      load_turned<T>(y.x, pb, DA, k0, nv, nullptr);
+      put_turned(x, va, nullptr);
+      put_turned(y.x, vb, nullptr);
       __syncthreads();
-      gemm(p, x, y.x, min(kK, DA - k0), rg, cg);
+      if (k0 + kK < DA) {
+        fetch_turned<T>(va, pa, DA, k0 + kK, nv);
+        fetch_turned<T>(vb, pb, DA, k0 + kK, nv);
+      } else {
+        fetch_rows<T>(vc, pc, DC, c0, nv);
+      }
+      gemm(p, x, y.x, 0, min(kK, DA - k0), rg, cg);
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r)
@@ -265,46 +363,39 @@ __global__ void __launch_bounds__(kThreads) decay_out_kernel(const Args a) {
         P.x[j][row] = on ? w * (r % 2 ? p[r / 2][i].y : p[r / 2][i].x) : 0.f;
       }
     __syncthreads();
-    load_rows<T>(y.x, pc, DC, c0, nv, nullptr);
+    put_rows(y.x, vc, nullptr);
     __syncthreads();
-    gemm(acc, P.x, y.x, nv, rg, cg);
-    // the state's part
     const float* s = a.n > 1 ? (rev ? a.rev : a.fwd) : (rev ? a.gs : a.s0);
-    if (s == nullptr) continue;
-    s += ((b * a.H + h) * a.n + c) * (int64_t)a.D * a.M;
-    for (int k0 = 0; k0 < DA; k0 += kK) {
+    if (s != nullptr) {
+      s += ((b * a.H + h) * a.n + c) * (int64_t)a.D * a.M;
+      fetch_turned<T>(va, pa, DA, 0, nv);
+      fetch_state(vb, s, a.M, turned, DA, DC, 0, c0);
+    }
+    // (a warp has 16 rows, whose scores past the diagonal are 0)
+    gemm(acc, P.x, y.x, rev ? (rg & ~1) * 8 : 0, rev ? nv : min(nv, (rg & ~1) * 8 + 16), rg, cg);
+    // the state's part
+    for (int k0 = 0; s != nullptr && k0 < DA; k0 += kK) {
       __syncthreads();
-      load_turned<T>(x, pa, DA, k0, nv, f);
-      if (turned) {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < kC * kK; i += kThreads) {
-          const int kk = i % kK, col = i / kK;
-          y.x[kk][col] = k0 + kk < DA && c0 + col < DC ? s[(int64_t)(c0 + col) * a.M + k0 + kk] : 0.f;
-        }
-      } else {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < kC * kK; i += kThreads) {
-          const int kk = i / kC, col = i % kC;
-          y.x[kk][col] = k0 + kk < DA && c0 + col < DC ? s[(int64_t)(k0 + kk) * a.M + c0 + col] : 0.f;
-        }
+      put_turned(x, va, f);
+      put_state(y.x, vb, turned);
+      __syncthreads();
+      if (k0 + kK < DA) {
+        fetch_turned<T>(va, pa, DA, k0 + kK, nv);
+        fetch_state(vb, s, a.M, turned, DA, DC, k0 + kK, c0);
       }
-      __syncthreads();
-      gemm(acc, x, y.x, min(kK, DA - k0), rg, cg);
+      gemm(acc, x, y.x, 0, min(kK, DA - k0), rg, cg);
     }
   }
   T* out = static_cast<T*>(kind < 0 ? a.out : kind == 0 ? a.dq : kind == 1 ? a.dv : a.dk) +
            (oh * a.N + c * kC) * DC;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const int row = rg * 8 + r;
-    if (c * kC + row >= a.N) continue;
+    const int row = rg * 8 + r, col = c0 + cg * 4;
+    if (c * kC + row >= a.N || col >= DC) continue;
+    float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = c0 + cg * 4 + i;
-      if (col < DC)
-        out[(int64_t)row * DC + col] =
-            from_f32<T>(row < nv ? (r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x) : 0.f);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = row < nv ? (r % 2 ? acc[r / 2][i].y : acc[r / 2][i].x) : 0.f;
+    st4<T>(out + (int64_t)row * DC + col, v, DC - col, DC % 4 == 0);
   }
 }
 
