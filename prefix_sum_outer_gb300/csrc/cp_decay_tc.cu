@@ -55,21 +55,35 @@ constexpr int kBarBytes = 512, kTableBytes = 1536;
 constexpr int kNP = 2;    // buffers of P
 constexpr uint32_t kHi = desc_hi(1024);
 
-struct Args {
+// What the products of a launch share, and what is each one's own.
+struct Common {
   const float* g;
   const int* lengths;
+  int* status;
+  int64_t N;
+  int H, Hk, group, BH, n_mb, n_tiles, seg_tiles, G;
+  int sub, sub_tiles;      // parts of a piece in the summing launch, and their tiles
+  int products;
+};
+struct Own {
   const float* state_in;   // may be null (zero)
   float* state_out;        // may be null
   float* slots;            // [problems][G][sub][DP][64]: sums, then the pieces' first states
   float* out_f32;          // not null: the result goes here in fp32, [BH][N][DC]
-  int* status;
-  int64_t N, st_r, st_c;   // strides of a state's rows and columns
-  int H, Hk, group, BH, n_mb, n_tiles, seg_tiles, G;
-  int sub, sub_tiles;      // parts of a piece in the summing launch, and their tiles
+  int64_t st_r, st_c;      // strides of a state's rows and columns
   int DA, DC;
   int a_key, b_key, c_key, o_key;   // whether an array has key heads
   int reverse;
   float s_p, s_o, s_c;     // factors of P, of A S and of C'
+};
+template <int MAX>
+struct Set {
+  Common all;
+  Own own[MAX];
+};
+template <int MAX>
+struct Maps {
+  CUtensorMap a[MAX], b[MAX], c[MAX], o[MAX];
 };
 
 // PARTS: bf16 numbers to an element of C'
@@ -156,12 +170,11 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-template <int DP, int PARTS, bool AGG>
+// MAX: products that share a launch, at most (their CTAs in turn, so that those of
+// one head, which read the same rows, run side by side)
+template <int DP, int PARTS, bool AGG, int MAX>
 __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
-    decay_tc_kernel(const __grid_constant__ CUtensorMap tm_a,
-                    const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_c,
-                    const __grid_constant__ CUtensorMap tm_o, const Args a) {
+    decay_tc_kernel(const __grid_constant__ Maps<MAX> maps, const __grid_constant__ Set<MAX> set) {
   using L = Layout<DP, PARTS, AGG>;
   constexpr int NB = L::NB, R = L::R, BPT = L::kBoxesPerTile, NSB = L::NSB;
   extern __shared__ uint8_t smem_raw[];
@@ -195,17 +208,24 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   float* cf = pw + 132;                // [32] a chunk's column powers
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int idx = blockIdx.x;
+  const Common& a = set.all;
+  const int which = MAX == 1 ? 0 : blockIdx.x % a.products;
+  const Own& own = set.own[which];
+  const CUtensorMap &tm_a = maps.a[which], &tm_b = maps.b[which], &tm_c = maps.c[which],
+                    &tm_o = maps.o[which];
+  int idx = MAX == 1 ? blockIdx.x : blockIdx.x / a.products;
   const int mb = idx % a.n_mb;
   idx /= a.n_mb;
   const int bh = idx % a.BH;
   int seg = idx / a.BH, part = 0;
   if (AGG) {
     part = seg % a.sub;
-    seg = seg / a.sub + (a.reverse ? 1 : 0);  // (nothing follows the last in scan order)
+    seg = seg / a.sub + (own.reverse ? 1 : 0);  // (nothing follows the last in scan order)
   }
   const int b = bh / a.H, h = bh % a.H;
-  const bool rev = a.reverse != 0;
+  const bool rev = own.reverse != 0;
+  const float s_p = own.s_p, s_o = own.s_o, s_c = own.s_c;
+  float* const out_f32 = own.out_f32;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NB; ++i) {
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   auto shift = [&](int tile) { return rev && tile == live - 1 ? 1 : 0; };
   // tiles whose B^T C' is wanted: not the last of a piece that hands nothing on
   const bool last_seg = rev ? seg == 0 : seg == a.G - 1;
-  const bool hands_on = AGG || (last_seg && a.state_out != nullptr);
+  const bool hands_on = AGG || (last_seg && own.state_out != nullptr);
   const int n_kv = hands_on ? n_it : n_it - 1;
 
   if (warp < 4) {
@@ -289,7 +309,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       if (lane == 0) {
         const uint64_t pol = AGG ? policy_evict_last() : policy_evict_first();
         const int hk = b * a.Hk + h / a.group;
-        const int ia = a.a_key ? hk : bh, ib = a.b_key ? hk : bh, ic = a.c_key ? hk : bh;
+        const int ia = own.a_key ? hk : bh, ib = own.b_key ? hk : bh, ic = own.c_key ? hk : bh;
         bool ok = true;
         int it = 0;
 #pragma unroll 1
@@ -494,7 +514,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       const int d = DP == 64 ? row & 63 : row, c0 = DP == 64 ? (row >> 6) * SC : 0;
       const int pidx = bh * a.n_mb + mb, m0 = mb * kMB + c0;
       const int at = AGG ? part : rev ? a.sub - 1 : 0;  // where the prefix launch leaves a piece's first state
-      float* slot = a.slots + ((((int64_t)pidx * a.G + seg) * a.sub + at) * DP + d) * kMB + c0;
+      float* slot = own.slots + ((((int64_t)pidx * a.G + seg) * a.sub + at) * DP + d) * kMB + c0;
       float2 S[SC / 2];
       const bool first_seg = rev ? seg == a.G - 1 : seg == 0;
       if (!AGG && !first_seg) {
@@ -505,12 +525,12 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           S[2 * x + 1] = make_float2(f.z, f.w);
         }
       } else {
-        const bool on = !AGG && a.state_in != nullptr && d < a.DA;
-        const float* s = a.state_in + (int64_t)bh * a.DA * a.DC + d * a.st_r;
+        const bool on = !AGG && own.state_in != nullptr && d < own.DA;
+        const float* s = own.state_in + (int64_t)bh * own.DA * own.DC + d * own.st_r;
 #pragma unroll
         for (int x = 0; x < SC / 2; ++x) {
-          S[x].x = on && m0 + 2 * x < a.DC ? s[(m0 + 2 * x) * a.st_c] : 0.f;
-          S[x].y = on && m0 + 2 * x + 1 < a.DC ? s[(m0 + 2 * x + 1) * a.st_c] : 0.f;
+          S[x].x = on && m0 + 2 * x < own.DC ? s[(m0 + 2 * x) * own.st_c] : 0.f;
+          S[x].y = on && m0 + 2 * x + 1 < own.DC ? s[(m0 + 2 * x + 1) * own.st_c] : 0.f;
         }
       }
       const float2 full_step = power_parts(g, kTile);
@@ -576,17 +596,17 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           reinterpret_cast<float4*>(slot)[x] =
               make_float4(S[2 * x].x, S[2 * x].y, S[2 * x + 1].x, S[2 * x + 1].y);
       }
-      if (!AGG && ok && hands_on && d < a.DA) {
+      if (!AGG && ok && hands_on && d < own.DA) {
         if (rev && live > 0) {
           const float2 f = power_parts(g, 1);
 #pragma unroll
           for (int x = 0; x < SC / 2; ++x) S[x] = fma2(both(f.x), S[x], mul2(both(f.y), S[x]));
         }
-        float* s = a.state_out + (int64_t)bh * a.DA * a.DC + d * a.st_r;
+        float* s = own.state_out + (int64_t)bh * own.DA * own.DC + d * own.st_r;
 #pragma unroll
         for (int x = 0; x < SC / 2; ++x) {
-          if (m0 + 2 * x < a.DC) s[(m0 + 2 * x) * a.st_c] = S[x].x;
-          if (m0 + 2 * x + 1 < a.DC) s[(m0 + 2 * x + 1) * a.st_c] = S[x].y;
+          if (m0 + 2 * x < own.DC) s[(m0 + 2 * x) * own.st_c] = S[x].x;
+          if (m0 + 2 * x + 1 < own.DC) s[(m0 + 2 * x + 1) * own.st_c] = S[x].y;
         }
       }
     }
@@ -638,7 +658,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           for (int y = 0; y < 2; ++y) {
             const int r = first + tid / 8 + 16 * y;
             v[y] = reinterpret_cast<const uint4*>(c_s)[8 * first + tid + 128 * y];
-            w[y] = r < nv ? a.s_c * pw[rev ? r : nv - 1 - r] : 0.f;
+            w[y] = r < nv ? s_c * pw[rev ? r : nv - 1 - r] : 0.f;
           }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -697,13 +717,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             float2 p;
             const bool k0 = rev ? 2 * x >= lane : 2 * x <= lane;
             const bool k1 = rev ? 2 * x + 1 >= lane : 2 * x + 1 <= lane;
-            p.x = k0 ? __uint_as_float(r[2 * x]) * (a.s_p * w[rev ? 2 * x : -2 * x]) : 0.f;
-            p.y = k1 ? __uint_as_float(r[2 * x + 1]) * (a.s_p * w[rev ? 2 * x + 1 : -2 * x - 1]) : 0.f;
+            p.x = k0 ? __uint_as_float(r[2 * x]) * (s_p * w[rev ? 2 * x : -2 * x]) : 0.f;
+            p.y = k1 ? __uint_as_float(r[2 * x + 1]) * (s_p * w[rev ? 2 * x + 1 : -2 * x - 1]) : 0.f;
             r[x] = split_hi(p);
             lo[x] = tc::pack_bf16x2(p.x, p.y);
           }
         } else {
-          const float2 rf = both(a.s_p * pw[rev ? 32 * c - row : row - 32 * c - 31]);
+          const float2 rf = both(s_p * pw[rev ? 32 * c - row : row - 32 * c - 31]);
           const float4* f = reinterpret_cast<const float4*>(cf);
           tmem_ld_wait();
 #pragma unroll
@@ -729,13 +749,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     // -------------------------------------------------------------- O group
     if constexpr (!AGG) more_registers<104>();
     const int o_tid = threadIdx.x - 32 * 16;
-    const int oh = a.o_key ? b * a.Hk + h / a.group : bh;
-    const float full_row = a.s_o * pw[rev ? kTile - row : row + 1];
+    const int oh = own.o_key ? b * a.Hk + h / a.group : bh;
+    const float full_row = s_o * pw[rev ? kTile - row : row + 1];
     bool ok = true;
     for (int it = 0; it < n_it; ++it) {
       const int tile = tile_of(it), nv = rows_in(tile);
       const float rf = !rev || (nv == kTile && shift(tile) == 0) ? full_row
-                       : row < nv ? a.s_o * pw[nv - row - shift(tile)] : 0.f;
+                       : row < nv ? s_o * pw[nv - row - shift(tile)] : 0.f;
       // A S, scaled, waits in registers for P C, whose accumulator is given back
       // as soon as it is read: the next tile's P C waits for it
       float2 o[kMB / 2];
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       // (both C' groups and P C are done with this tile's C: its box takes O)
       const int st = it * BPT % R;
       uint8_t* o_tile = ring + st * kBoxBytes;
-      if (a.out_f32 == nullptr) {
+      if (out_f32 == nullptr) {
         ok = agree(1, 128, ok);
         if (!ok) break;
 #pragma unroll
@@ -794,11 +814,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       } else {
         // fp32 parts, which a later launch sums over the heads of a group
         if (!ok) break;
-        float* to = a.out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * a.DC + mb * kMB;
+        float* to = out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * own.DC + mb * kMB;
         if ((int64_t)tile * kTile + row < a.N)
 #pragma unroll
           for (int x = 0; x < kMB / 4; ++x)
-            if (mb * kMB + 4 * x < a.DC)
+            if (mb * kMB + 4 * x < own.DC)
               reinterpret_cast<float4*>(to)[x] =
                   make_float4(o[2 * x].x, o[2 * x].y, o[2 * x + 1].x, o[2 * x + 1].y);
         if (o_tid == 0) mbar_arrive(&empty[st]);
@@ -808,7 +828,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     ok = agree(1, 128, ok);
     // tiles behind the sequence's end: zeros
     if (ok && max(t_first, live) < t_stop) {
-      if (a.out_f32 == nullptr) {
+      if (out_f32 == nullptr) {
         // (the box that took the last O is this group's alone by now)
         uint8_t* o_tile = ring + max(0, n_it - 1) * BPT % R * kBoxBytes;
         named_barrier_sync(1, 128);
@@ -824,10 +844,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         }
       } else {
         const int64_t r0 = (int64_t)max(t_first, live) * kTile, r1 = min(a.N, (int64_t)t_stop * kTile);
-        const int cols = min(kMB, a.DC - mb * kMB) / 4;
-        float* to = a.out_f32 + (int64_t)bh * a.N * a.DC + mb * kMB;
+        const int cols = min(kMB, own.DC - mb * kMB) / 4;
+        float* to = out_f32 + (int64_t)bh * a.N * own.DC + mb * kMB;
         for (int64_t i = o_tid; i < (r1 - r0) * cols; i += 128)
-          *reinterpret_cast<float4*>(to + (r0 + i / cols) * a.DC + i % cols * 4) =
+          *reinterpret_cast<float4*>(to + (r0 + i / cols) * own.DC + i % cols * 4) =
               make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
@@ -846,23 +866,19 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 // Sums [problems][G][sub][E] of the pieces' parts give the states the pieces start
 // from, each in the place of its piece's first part in scan order: a thread walks
 // four elements over the parts, whose loads go out ahead.
-struct PrefixArgs {
-  const float* g;
-  const int* lengths;
-  const float* state_in;
-  float* slots;
-  int64_t N, st_r, st_c;
-  int H, BH, n_mb, n_tiles, seg_tiles, G, sub, sub_tiles, DA, DC, DP, reverse;
-};
 constexpr int kPrefixThreads = 128;
-__global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const PrefixArgs a) {
-  const int E4 = a.DP * kMB / 4, per = E4 / kPrefixThreads;
+template <int MAX>
+__global__ void __launch_bounds__(kPrefixThreads)
+    decay_tc_prefix_kernel(const __grid_constant__ Set<MAX> set, int DP) {
+  const Common& a = set.all;
+  const Own& own = set.own[MAX == 1 ? 0 : blockIdx.y];
+  const int E4 = DP * kMB / 4, per = E4 / kPrefixThreads;
   const int problem = blockIdx.x / per, e = (blockIdx.x % per) * kPrefixThreads + threadIdx.x;
   const int bh = problem / a.n_mb, mb = problem % a.n_mb;
-  float4* s = reinterpret_cast<float4*>(a.slots) + (int64_t)problem * a.G * a.sub * E4 + e;
+  float4* s = reinterpret_cast<float4*>(own.slots) + (int64_t)problem * a.G * a.sub * E4 + e;
   const int n = (a.G - 1) * a.sub;  // parts that were summed, in scan order
   grid_dep_wait();
-  auto slot = [&](int i) { return (int64_t)(a.reverse ? a.G * a.sub - 1 - i : i); };
+  auto slot = [&](int i) { return (int64_t)(own.reverse ? a.G * a.sub - 1 - i : i); };
   constexpr int kAhead = 8;
   float4 next[kAhead];
 #pragma unroll
@@ -871,9 +887,9 @@ __global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const P
   const int64_t rows = rows_of(a.lengths, bh / a.H, a.N);
   const int r = 4 * e / kMB, c = mb * kMB + 4 * e % kMB;
   float4 S{};
-  if (a.state_in != nullptr && r < a.DA && c < a.DC) {  // (columns come in eights)
-    const float* p = a.state_in + (int64_t)bh * a.DA * a.DC + r * a.st_r + c * a.st_c;
-    S = make_float4(p[0], p[a.st_c], p[2 * a.st_c], p[3 * a.st_c]);
+  if (own.state_in != nullptr && r < own.DA && c < own.DC) {  // (columns come in eights)
+    const float* p = own.state_in + (int64_t)bh * own.DA * own.DC + r * own.st_r + c * own.st_c;
+    S = make_float4(p[0], p[own.st_c], p[2 * own.st_c], p[3 * own.st_c]);
   }
   const float2 whole = power_parts(g, a.sub_tiles * kTile);
   for (int i0 = 0; i0 < n; i0 += kAhead) {
@@ -891,7 +907,7 @@ __global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const P
       const int64_t lo = t0 * kTile, hi = min(rows, t1 * kTile);  // the part's rows
       float4 x = now[0];
       if (hi > lo) {
-        const int m = (int)(hi - lo) - (a.reverse && rows == hi ? 1 : 0);
+        const int m = (int)(hi - lo) - (own.reverse && rows == hi ? 1 : 0);
         const float2 f = m == a.sub_tiles * kTile ? whole : power_parts(g, m);
         S.x = fmaf(f.x, S.x, fmaf(f.y, S.x, x.x));
         S.y = fmaf(f.x, S.y, fmaf(f.y, S.y, x.y));
@@ -901,7 +917,7 @@ __global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const P
 #pragma unroll
       for (int y = 0; y + 1 < kAhead; ++y) now[y] = now[y + 1];
       // (the next piece's first sum has been read, being among those ahead)
-      if (part == (a.reverse ? 0 : a.sub - 1)) s[(int64_t)(a.reverse ? at - 1 : at + 1) * E4] = S;
+      if (part == (own.reverse ? 0 : a.sub - 1)) s[(int64_t)(own.reverse ? at - 1 : at + 1) * E4] = S;
     }
   }
 }
@@ -909,22 +925,38 @@ __global__ void __launch_bounds__(kPrefixThreads) decay_tc_prefix_kernel(const P
 // ---------------------------------------------------------------- host
 struct Plan {
   int DP, n_mb, n_tiles, seg_tiles, G, sub, sub_tiles;
-  int64_t problems;
-  size_t slot_bytes;
+  int64_t problems;    // of one product
+  size_t slot_bytes;   // of one product
+  double tiles;        // in line, as estimated
 };
-Plan plan(const DecayShape& s, int64_t DA, int64_t DC) {
+// G, the pieces to a sequence, is the one with the least tiles in line: rounds of
+// CTAs on the SMs times the tiles of a piece, a round's start and end worth
+// four; and with G > 1 the summing launch, which reads all pieces but one at
+// three times that rate, and the two launches more, worth four.  (A tile is 2 to 3
+// us.)
+Plan plan(const DecayShape& s, int64_t DA, int64_t DC, int products) {
   Plan p;
   p.DP = DA <= 64 ? 64 : 128;
   p.n_mb = (int)((DC + kMB - 1) / kMB);
   p.n_tiles = (int)((s.N + kTile - 1) / kTile);
   p.problems = s.B * s.H * p.n_mb;
+  const int64_t all = p.problems * products;
   int64_t G = 1;
-  if (p.problems * 4 < (int64_t)kPlanSMs * 3) G = std::max<int64_t>(1, kPlanSMs / p.problems);
-  G = std::min<int64_t>(G, std::max(1, p.n_tiles));
+  double best = 0;
+  for (int64_t g = 1; g <= std::min<int64_t>(p.n_tiles, 64) && (g == 1 || all < 4 * kPlanSMs); ++g) {
+    const int64_t rounds = (all * g + kPlanSMs - 1) / kPlanSMs, tiles = (p.n_tiles + g - 1) / g;
+    double t = rounds * (tiles + 4.0);
+    if (g > 1) t += 4 + 0.33 * all * (g - 1) / g * p.n_tiles / kPlanSMs;
+    if (g == 1 || t < best) {
+      best = t;
+      G = g;
+    }
+  }
+  p.tiles = best;
   p.seg_tiles = (int)((p.n_tiles + G - 1) / G);
   p.G = (p.n_tiles + p.seg_tiles - 1) / p.seg_tiles;
   // the summing launch has two CTAs to an SM
-  const int64_t sums = p.problems * (p.G - 1);
+  const int64_t sums = all * (p.G - 1);
   const int64_t sub = sums > 0 ? std::max<int64_t>(1, 2 * kPlanSMs / sums) : 1;
   p.sub_tiles = (int)std::max<int64_t>(1, (p.seg_tiles + sub - 1) / sub);
   p.sub = (p.seg_tiles + p.sub_tiles - 1) / p.sub_tiles;
@@ -932,11 +964,10 @@ Plan plan(const DecayShape& s, int64_t DA, int64_t DC) {
   return p;
 }
 
-template <int DP, int PARTS, bool AGG>
-cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc,
-                   const CUtensorMap& mo, const Args& a, unsigned grid, cudaStream_t stream) {
+template <int DP, int PARTS, bool AGG, int MAX>
+cudaError_t launch(const Maps<MAX>& maps, const Set<MAX>& set, unsigned grid, cudaStream_t stream) {
   using L = Layout<DP, PARTS, AGG>;
-  auto kern = decay_tc_kernel<DP, PARTS, AGG>;
+  auto kern = decay_tc_kernel<DP, PARTS, AGG, MAX>;
   // the shared-memory opt-in is set once per device for each instantiation
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -948,10 +979,24 @@ cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmem, stream, ma, mb, mc, mo, a);
+  return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmem, stream, maps, set);
 }
 
-struct Product {
+template <int DP, int PARTS, int MAX>
+cudaError_t launch_all(const Plan& pl, const Maps<MAX>& maps, const Set<MAX>& set,
+                       cudaStream_t stream) {
+  const unsigned n = (unsigned)(pl.problems * set.all.products);
+  if (pl.G > 1) {
+    cudaError_t e = launch<DP, PARTS, true, MAX>(maps, set, n * (pl.G - 1) * pl.sub, stream);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(pl.problems * DP * kMB / 4 / kPrefixThreads), set.all.products);
+    e = launch_dependent(decay_tc_prefix_kernel<MAX>, grid, kPrefixThreads, 0, stream, set, DP);
+    if (e != cudaSuccess) return e;
+  }
+  return launch<DP, PARTS, false, MAX>(maps, set, n * pl.G, stream);
+}
+
+struct RowProduct {
   const void *a, *b, *c;
   void* out;
   bool a_key, b_key, c_key, o_key, turned, reverse;  // turned: the state is held [DC][DA]
@@ -961,61 +1006,53 @@ struct Product {
   float s_p, s_o, s_c;
 };
 
-cp_status_t run(const DecayShape& s, const float* g, const Product& p, float* slots, int* status,
-                cudaStream_t stream) {
+// The products of one launch: of one class of widths, DA and DC each at most 64 or
+// above
+template <int MAX>
+cp_status_t run(const DecayShape& s, const float* g, const RowProduct* products, int n, float* slots,
+                int* status, cudaStream_t stream) {
   // the maps are made by the driver, which wants a context bound to this thread:
   // a thread that autograd starts may not have called the runtime yet
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return CP_ERR_CUDA;
-  const Plan pl = plan(s, p.DA, p.DC);
+  const Plan pl = plan(s, products[0].DA, products[0].DC, n);
   const int64_t vh = s.B * s.H, kh = s.B * s.Hk;
-  CUtensorMap ma, mb, mc, mo;
-  if (!tc::make_map(&ma, p.a, p.a_key ? kh : vh, s.N, p.DA) ||
-      !tc::make_map(&mb, p.b, p.b_key ? kh : vh, s.N, p.DA) ||
-      !tc::make_map(&mc, p.c, p.c_key ? kh : vh, s.N, p.DC) ||
-      !tc::make_map(&mo, p.out, p.o_key ? kh : vh, s.N, p.DC))
-    return CP_ERR_UNSUPPORTED_SHAPE;
-  Args a{};
+  Maps<MAX> maps;
+  Set<MAX> set{};
+  Common& a = set.all;
   a.g = g;
   a.lengths = s.lengths;
-  a.state_in = p.state_in;
-  a.state_out = p.state_out;
-  a.slots = slots;
-  a.out_f32 = p.out_f32;
   a.status = status;
   a.N = s.N;
-  a.st_r = p.turned ? 1 : p.DC;
-  a.st_c = p.turned ? p.DA : 1;
   a.H = (int)s.H; a.Hk = (int)s.Hk; a.group = (int)(s.H / s.Hk); a.BH = (int)vh;
   a.n_mb = pl.n_mb; a.n_tiles = pl.n_tiles; a.seg_tiles = pl.seg_tiles; a.G = pl.G;
   a.sub = pl.sub; a.sub_tiles = pl.sub_tiles;
-  a.DA = (int)p.DA; a.DC = (int)p.DC;
-  a.a_key = p.a_key; a.b_key = p.b_key; a.c_key = p.c_key; a.o_key = p.o_key;
-  a.reverse = p.reverse;
-  a.s_p = p.s_p; a.s_o = p.s_o; a.s_c = p.s_c;
-  const unsigned sums = (unsigned)(pl.problems * (pl.G - 1) * pl.sub), all = (unsigned)(pl.problems * pl.G);
-  cudaError_t e = cudaSuccess;
-#define CP_DECAY_CASE(DP_, PARTS_)                                                          \
-  if (pl.DP == DP_ && (p.state_out != nullptr ? 3 : 2) == PARTS_) {                         \
-    if (pl.G > 1) {                                                                         \
-      e = launch<DP_, PARTS_, true>(ma, mb, mc, mo, a, sums, stream);                       \
-      if (e != cudaSuccess) return CP_ERR_CUDA;                                             \
-      const PrefixArgs x{g,       s.lengths, p.state_in,  slots,   s.N,   a.st_r,        \
-                         a.st_c,  a.H,       a.BH,        a.n_mb,  a.n_tiles, a.seg_tiles, \
-                         a.G,     a.sub,     a.sub_tiles, a.DA,    a.DC,  DP_,           \
-                         a.reverse};                                                     \
-      e = launch_dependent(decay_tc_prefix_kernel,                                       \
-                           dim3((unsigned)(pl.problems * DP_ * kMB / 4 / kPrefixThreads)),  \
-                           kPrefixThreads, 0, stream, x);                                \
-      if (e != cudaSuccess) return CP_ERR_CUDA;                                          \
-    }                                                                                    \
-    e = launch<DP_, PARTS_, false>(ma, mb, mc, mo, a, all, stream);                         \
+  a.products = n;
+  bool state = false;
+  for (int i = 0; i < n; ++i) {
+    const RowProduct& p = products[i];
+    if (!tc::make_map(&maps.a[i], p.a, p.a_key ? kh : vh, s.N, p.DA) ||
+        !tc::make_map(&maps.b[i], p.b, p.b_key ? kh : vh, s.N, p.DA) ||
+        !tc::make_map(&maps.c[i], p.c, p.c_key ? kh : vh, s.N, p.DC) ||
+        !tc::make_map(&maps.o[i], p.out, p.o_key ? kh : vh, s.N, p.DC))
+      return CP_ERR_UNSUPPORTED_SHAPE;
+    Own& o = set.own[i];
+    o.state_in = p.state_in;
+    o.state_out = p.state_out;
+    o.slots = slots + i * (pl.slot_bytes / sizeof(float));
+    o.out_f32 = p.out_f32;
+    o.st_r = p.turned ? 1 : p.DC;
+    o.st_c = p.turned ? p.DA : 1;
+    o.DA = (int)p.DA; o.DC = (int)p.DC;
+    o.a_key = p.a_key; o.b_key = p.b_key; o.c_key = p.c_key; o.o_key = p.o_key;
+    o.reverse = p.reverse;
+    o.s_p = p.s_p; o.s_o = p.s_o; o.s_c = p.s_c;
+    state = state || p.state_out != nullptr;
   }
-  CP_DECAY_CASE(64, 2)
-  CP_DECAY_CASE(64, 3)
-  CP_DECAY_CASE(128, 2)
-  CP_DECAY_CASE(128, 3)
-#undef CP_DECAY_CASE
+  const cudaError_t e = pl.DP == 64 ? (state ? launch_all<64, 3>(pl, maps, set, stream)
+                                             : launch_all<64, 2>(pl, maps, set, stream))
+                                    : (state ? launch_all<128, 3>(pl, maps, set, stream)
+                                             : launch_all<128, 2>(pl, maps, set, stream));
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
@@ -1031,42 +1068,53 @@ bool decay_tc_supported(const DecayShape& s) {
   return s.dtype == CP_DTYPE_BF16 && s.D <= 128 && s.M <= 128;
 }
 
+// Products of one class of widths may share a launch: where that saves rounds of
+// CTAs or launches, for a CTA whose product is chosen as it runs is a tenth slower.
+// The backward, three products in one launch against three launches: B=2 H=8 N=1000
+// D=M=64 35 against 51 us, D=M=128 30 against 68, B=3 H=10 N=3000 D=M=64 58 against
+// 88, and B=8 H=16 N=4096 D=M=64, three rounds either way, 224 against 201.
+static int in_one_launch(const DecayShape& s) {
+  const double dq = plan(s, s.M, s.D, 1).tiles;
+  auto pays = [&](int n) { return 1.1 * plan(s, s.M, s.D, n).tiles < n * (dq + 1); };
+  if ((s.D <= 64) == (s.M <= 64) && pays(3)) return 3;  // dq, dk, dv
+  return pays(2) ? 2 : 1;                               // dq, dk
+}
+
 size_t decay_tc_scratch(const DecayShape& s, bool backward) {
-  const size_t fwd = plan(s, s.D, s.M).slot_bytes;
-  if (!backward) return fwd;
-  return std::max(fwd, plan(s, s.M, s.D).slot_bytes) + 256 + 2 * part_bytes(s);
+  if (!backward) return plan(s, s.D, s.M, 1).slot_bytes;
+  const int n = in_one_launch(s);
+  const size_t slots = std::max(n * plan(s, s.M, s.D, n).slot_bytes,
+                                n < 3 ? plan(s, s.D, s.M, 1).slot_bytes : 0);
+  return round256(slots) + 2 * part_bytes(s);
 }
 
 cp_status_t decay_tc_fwd(const DecayShape& s, const DecayFwd& f, void* scratch, int* status,
                          cudaStream_t stream) {
-  return run(s, f.g,
-             {f.q, f.k, f.v, f.out, true, true, false, false, false, false, s.D, s.M, f.state_in,
-              f.state_out, nullptr, s.scale, s.scale, 1.f},
-             static_cast<float*>(scratch), status, stream);
+  const RowProduct p{f.q, f.k, f.v, f.out, true, true, false, false, false, false, s.D, s.M,
+                  f.state_in, f.state_out, nullptr, s.scale, s.scale, 1.f};
+  return run<1>(s, f.g, &p, 1, static_cast<float*>(scratch), status, stream);
 }
 
 cp_status_t decay_tc_bwd(const DecayShape& s, const DecayBwd& f, void* scratch, int* status,
                          cudaStream_t stream) {
-  float* slots = static_cast<float*>(scratch);
-  const size_t n = round256(std::max(plan(s, s.D, s.M).slot_bytes, plan(s, s.M, s.D).slot_bytes));
   const bool grouped = s.H != s.Hk;
-  float* dq_part = grouped ? slots + n / sizeof(float) : nullptr;
-  float* dk_part = grouped ? dq_part + part_bytes(s) / sizeof(float) : nullptr;
-  cp_status_t st =
-      run(s, f.g,
-          {f.grad_out, f.v, f.k, f.dq, false, false, true, true, true, false, s.M, s.D, f.state_in,
-           nullptr, dq_part, s.scale, s.scale, 1.f},
-          slots, status, stream);
-  if (st != CP_OK) return st;
-  st = run(s, f.g,
-           {f.k, f.q, f.grad_out, f.dv, true, true, false, false, false, true, s.D, s.M,
-            f.grad_state_out, f.grad_state_in, nullptr, s.scale, 1.f, s.scale},
-           slots, status, stream);
-  if (st != CP_OK) return st;
-  st = run(s, f.g,
-           {f.v, f.grad_out, f.q, f.dk, false, false, true, true, true, true, s.M, s.D,
-            f.grad_state_out, nullptr, dk_part, s.scale, 1.f, s.scale},
-           slots, status, stream);
+  float* slots = static_cast<float*>(scratch);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(scratch) +
+                                          (decay_tc_scratch(s, true) - 2 * part_bytes(s)));
+  float* dq_part = grouped ? parts : nullptr;
+  float* dk_part = grouped ? parts + part_bytes(s) / sizeof(float) : nullptr;
+  const RowProduct p[3] = {
+      {f.grad_out, f.v, f.k, f.dq, false, false, true, true, true, false, s.M, s.D, f.state_in,
+       nullptr, dq_part, s.scale, s.scale, 1.f},
+      {f.v, f.grad_out, f.q, f.dk, false, false, true, true, true, true, s.M, s.D,
+       f.grad_state_out, nullptr, dk_part, s.scale, 1.f, s.scale},
+      {f.k, f.q, f.grad_out, f.dv, true, true, false, false, false, true, s.D, s.M,
+       f.grad_state_out, f.grad_state_in, nullptr, s.scale, 1.f, s.scale}};
+  const int n = in_one_launch(s);
+  cp_status_t st = CP_OK;
+  if (n > 1) st = run<3>(s, f.g, p, n, slots, status, stream);
+  for (int i = n > 1 ? n : 0; i < 3 && st == CP_OK; ++i)
+    st = run<1>(s, f.g, p + i, 1, slots, status, stream);
   if (st != CP_OK || !grouped) return st;
   return delta_join_launch({dq_part, dk_part, nullptr, nullptr, f.dq, f.dk, nullptr, nullptr, s.N,
                             s.D, s.B * s.Hk, (int)(s.H / s.Hk), 1},
