@@ -366,6 +366,12 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       // with D = M = 64 (B=8 H=16 N=4096), 304 against 296 with 128 (B=2 H=8
       // N=32768)
       constexpr bool kMixed = DP == 64;
+      // The issuers' loops stay rolled as far as that does not hold up their MMAs:
+      // their code competes with the other roles' for the instruction cache.  Rolled
+      // and unrolled: forward 68 and 74 us, forward and backward 249 and 269 (B=8
+      // H=16 N=4096 D=M=64); with 128-wide A the reverse in these two, 86 and 84
+      // (B=4 H=8 N=8229 D=128 M=64).
+      constexpr int kUnrollP = DP == 64 ? 1 : 8, kUnrollPC = DP == 64 ? 2 : 8;
       [[maybe_unused]] auto issue_p = [&](int it) {
         bool there = wait(&full_b[it % NB], (it / NB) & 1, abort_flag);
 #pragma unroll
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         tc_fence_after();
         const uint32_t t_p = tmem + (it % kNP) * 128;
         const uint32_t k_lo = desc_lo(b_addr(it), 16);
-#pragma unroll
+#pragma unroll kUnrollP
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint32_t in = ((kk & 3) * 32) >> 4;
           mma_ss_lo<kHi, kHi>(
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       [[maybe_unused]] auto issue_as = [&](int it) {
         tc_fence_after();
         const uint32_t s_lo = desc_lo(smem_u32(s_tile + (it % NSB) * 2 * L::kSOne), L::kSOne);
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk)
@@ -488,9 +494,9 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           const uint32_t c_lo = desc_lo(smem_u32(ring + x * kBoxBytes), kBoxBytes);
           // 32 columns of P: hi in their first 16 TMEM columns, lo in the next,
           // two j to a column
-#pragma unroll
+#pragma unroll 1
           for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll kUnrollPC
             for (int kk = 0; kk < kTile / 16; ++kk)
               mma_ts_lo<kHi>(tmem + L::kColO2,
                              tmem + bf * 128 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
