@@ -30,6 +30,13 @@
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
 // e^{g (31 - (j - j0))}, two numbers at most 1, one per row and one per column.
 //
+// No memory or matrix rate bounds it: with any one of the products, or of the
+// groups' stores, left out it is at most 4 % faster, without the P groups' work 10 %.
+// The roles share four schedulers, and a tile takes about 3,100 cycles at 64-wide A
+// (two products of bf16 parts more than the plain ones, so 1,700 of tensor core) and
+// 4,800 at 128.  Forward with the state, D = M = 64, B=8 H=16 N=4096: 62 us, 66 % of
+// the copy rate on 128 SMs; D = M = 128, B=2 H=8 N=32768: 237.
+//
 // Sequences of few heads are cut into pieces: the same kernel with the output
 // left out (AGG) sums each piece's B^T C', a prefix launch turns the sums into
 // the states the pieces start from, and the pieces run side by side.
@@ -51,7 +58,7 @@ using tc::record_timeout;
 using tc::sw128_offset;
 
 constexpr int kMB = 64;   // columns of c to a CTA
-constexpr int kBarBytes = 512, kTableBytes = 1536;
+constexpr int kBarBytes = 768, kTableBytes = 1280;
 constexpr int kNP = 2;    // buffers of P
 constexpr uint32_t kHi = desc_hi(1024);
 
@@ -112,7 +119,7 @@ struct Layout {
   static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
   static constexpr int kCols = AGG ? 128 : 512;
   static_assert(R >= kBoxesPerTile, "a tile does not fit");
-  static_assert((2 * NB + 2 * R + 34) * 8 <= kBarBytes, "barriers");
+  static_assert((2 * NB + 3 * R + 34) * 8 <= kBarBytes, "barriers");
   static_assert(kSmem <= kSmemLimit && kColS + 128 <= kCols, "no room");
 };
 
@@ -140,25 +147,23 @@ __device__ __forceinline__ float2 widen(uint32_t h) {
 // Twenty-eight warps walk eight different pieces of code, so what stalls them first is
 // the instruction cache: loops stay rolled, and a wait is a few instructions, its
 // limit a count (a try takes tens of nanoseconds to a microsecond, so a third of a
-// second at least) and not a clock's.
+// second at least) and not a clock's.  A warp's lanes wait together and agree, so that
+// the code behind a wait is uniform: its addresses and descriptors stay in uniform
+// registers, where one lane alone in a branch moves each there first (forward and
+// backward of B=8 H=16 N=4096 D=M=64: 249 us with the issuers and the producer as
+// single lanes, 219 so).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint32_t tries = 0;
+  bool there = true;
   while (!mbar_try_wait(bar, parity))
-    if (*abort_flag != 0 || ++tries > (1u << 24)) return false;
-  return true;
+    if (*abort_flag != 0 || ++tries > (1u << 24)) {
+      there = false;
+      break;
+    }
+  return __all_sync(~0u, there);
 }
-
-// A barrier of a group's threads that also agrees whether all of them go on: one
-// that gave up waiting must not leave the others at the next barrier.
-__device__ __forceinline__ bool agree(uint32_t id, uint32_t nthreads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "r"(id), "r"(nthreads)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+  return __all_sync(~0u, mbar_test_wait(bar, parity));
 }
 
 template <int REGS>
@@ -187,7 +192,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   uint64_t* empty_b = full_b + NB;
   uint64_t* full = empty_b + NB;       // [R]
   uint64_t* empty = full + R;          // [R]
-  uint64_t* p_done = empty + R;        // [kNP] A B^T in TMEM
+  uint64_t* c_read = empty + R;        // [R] a tile's C read by the C' groups
+  uint64_t* p_done = c_read + R;       // [kNP] A B^T in TMEM
   uint64_t* p_ready = p_done + kNP;    // [kNP] P packed
   uint64_t* pc_done = p_ready + kNP;   // [kNP] P C done: the buffer is free
   uint64_t* s_ready = pc_done + kNP;   // [2] copy of S written
@@ -207,7 +213,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   float* pw = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full_b) + kBarBytes);  // [129]
   float* cf = pw + 132;                // [32] a chunk's column powers
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle's result is the warp's own)
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Common& a = set.all;
   const int which = MAX == 1 ? 0 : blockIdx.x % a.products;
   const Own& own = set.own[which];
@@ -234,7 +241,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     }
     for (int i = 0; i < R; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], AGG ? 2 : 3);  // C: both C' groups and the O group; A: A B^T, A S twice
+      mbar_init(&empty[i], AGG ? 8 : 4);  // C: the O warps; A: A B^T, A S three times; summing, C: the C' warps
+      mbar_init(&c_read[i], 8);
     }
     for (int i = 0; i < kNP; ++i) {
       mbar_init(&p_done[i], 1);
@@ -250,12 +258,12 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     mbar_init(o1_free, 4);
     mbar_init(o2_free, 4);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&vp_ready[i], 1);
+      mbar_init(&vp_ready[i], 4);
       mbar_init(&vp_free[i], 1);
     }
     mbar_init(kv_done, 1);
     mbar_init(kv_free, 4);
-    mbar_init(fixed, 1);
+    mbar_init(fixed, 4);
     for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -281,12 +289,12 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_holder, 0);
   const int wq = warp & 3, row = wq * 32 + lane;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
 
   // ---- the piece's tiles: those that hold rows, in scan order
-  const int64_t rows = rows_of(a.lengths, b, a.N);
+  const int64_t rows = __shfl_sync(~0u, rows_of(a.lengths, b, a.N), 0);
   const int live = (int)((rows + kTile - 1) / kTile);
   const int t_first = seg * a.seg_tiles + (AGG ? part * a.sub_tiles : 0);
   const int t_stop = min(a.n_tiles, min((seg + 1) * a.seg_tiles, t_first + (AGG ? a.sub_tiles : a.seg_tiles)));
@@ -306,7 +314,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     fewer_registers<40>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      if (lane == 0) {
+      {
+        const uint32_t el = elect_one();
         const uint64_t pol = AGG ? policy_evict_last() : policy_evict_first();
         const int hk = b * a.Hk + h / a.group;
         const int ia = own.a_key ? hk : bh, ib = own.b_key ? hk : bh, ic = own.c_key ? hk : bh;
@@ -323,19 +332,19 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             ok = turn == 0 || wait(x == 1 ? &empty_b[st] : &empty[st], (turn - 1) & 1, abort_flag);
             if (!ok) break;
             if (x == 1) {
-              mbar_arrive_expect_tx(&full_b[st], L::kBStage);
+              if (el) mbar_arrive_expect_tx(&full_b[st], L::kBStage);
 #pragma unroll
               for (int y = 0; y < L::kABoxes; ++y)
-                tma_load_3d(b_ring + st * L::kBStage + y * kBoxBytes, &tm_b, &full_b[st], y * 64,
+                if (el) tma_load_3d(b_ring + st * L::kBStage + y * kBoxBytes, &tm_b, &full_b[st], y * 64,
                             row0, ib, pol);
             } else {
-              mbar_arrive_expect_tx(&full[st], kBoxBytes);
-              tma_load_3d(ring + st * kBoxBytes, x == 0 ? &tm_c : &tm_a, &full[st],
+              if (el) mbar_arrive_expect_tx(&full[st], kBoxBytes);
+              if (el) tma_load_3d(ring + st * kBoxBytes, x == 0 ? &tm_c : &tm_a, &full[st],
                           x == 0 ? mb * kMB : (x - 2) * 64, row0, x == 0 ? ic : ia, pol);
             }
           }
         }
-        if (!ok) record_timeout(a.status, abort_flag);
+        if (!ok && el) record_timeout(a.status, abort_flag);
         if (*abort_flag) {
           // let the copies already issued land before the CTA's memory goes
           // away: all but the last of a ring's were waited for by their users
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           }
         }
       }
-    } else if (lane == 0 && (warp == 1 || !AGG)) {
+    } else if (warp == 1 || !AGG) {
       // ------------------------------------------------------- MMA issuers
       constexpr uint32_t idesc_p = idesc_bf16_f32(128, 128, 0, 0);   // A . B^T
       constexpr uint32_t idesc_s2 = idesc_bf16_f32(128, 128, 1, 1);  // B^T . [C'_1 | C'_2]
@@ -362,16 +371,12 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       auto box_phase = [&](int it, int x) { return ((it * BPT + x) / R) & 1; };
       auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
       bool ok = true;
-      // A S is issued by the warp of A B^T, or by that of P C: 72 against 79 us
-      // with D = M = 64 (B=8 H=16 N=4096), 304 against 296 with 128 (B=2 H=8
-      // N=32768)
+      const uint32_t el = elect_one();
+      // A S is issued by the warp of A B^T, or by that of P C: with 64-wide A 72 and
+      // 79 us (B=8 H=16 N=4096), with 128-wide 245 and 240 (B=2 H=8 N=32768)
       constexpr bool kMixed = DP == 64;
-      // The issuers' loops stay rolled as far as that does not hold up their MMAs:
-      // their code competes with the other roles' for the instruction cache.  Rolled
-      // and unrolled: forward 68 and 74 us, forward and backward 249 and 269 (B=8
-      // H=16 N=4096 D=M=64); with 128-wide A the reverse in these two, 86 and 84
-      // (B=4 H=8 N=8229 D=128 M=64).
-      constexpr int kUnrollP = DP == 64 ? 1 : 8, kUnrollPC = DP == 64 ? 2 : 8;
+      // (these loops stay rolled: with four MMAs to a turn forward and backward of the
+      // same take 223 against 220 us)
       [[maybe_unused]] auto issue_p = [&](int it) {
         bool there = wait(&full_b[it % NB], (it / NB) & 1, abort_flag);
 #pragma unroll
@@ -381,17 +386,17 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         tc_fence_after();
         const uint32_t t_p = tmem + (it % kNP) * 128;
         const uint32_t k_lo = desc_lo(b_addr(it), 16);
-#pragma unroll kUnrollP
+#pragma unroll 1
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint32_t in = ((kk & 3) * 32) >> 4;
-          mma_ss_lo<kHi, kHi>(
+          mma_ss_lo_elect<kHi, kHi>(
               t_p, desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) + in,
-              k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0);
+              k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0, el);
         }
-        mma_commit(&p_done[it % kNP]);
-        mma_commit(&empty_b[it % NB]);
+        mma_commit_elect(&p_done[it % kNP], el);
+        mma_commit_elect(&empty_b[it % NB], el);
 #pragma unroll
-        for (int x = 1; x < BPT; ++x) mma_commit(&empty[box(it, x)]);
+        for (int x = 1; x < BPT; ++x) mma_commit_elect(&empty[box(it, x)], el);
         return true;
       };
       [[maybe_unused]] auto issue_as = [&](int it) {
@@ -399,20 +404,19 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         const uint32_t s_lo = desc_lo(smem_u32(s_tile + (it % NSB) * 2 * L::kSOne), L::kSOne);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < DP / 16; ++kk)
-            mma_ss_lo<kHi, kHi>(
+            mma_ss_lo_elect<kHi, kHi>(
                 tmem + L::kColO1,
                 desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) +
                     (((kk & 3) * 32) >> 4),
-                s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0);
-        mma_commit(&as_done[it % NSB]);
-        mma_commit(o1_done);
+                s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0, el);
+        mma_commit_elect(&as_done[it % NSB], el);
+        mma_commit_elect(o1_done, el);
 #pragma unroll
-        for (int x = 1; x < BPT; ++x) {
-          mma_commit(&empty[box(it, x)]);
-          mma_commit(&empty[box(it, x)]);
-        }
+        for (int x = 1; x < BPT; ++x)
+#pragma unroll 1
+          for (int y = 0; y < 3; ++y) mma_commit_elect(&empty[box(it, x)], el);
       };
       if (warp == 1) {
         // B^T C', 32 rows at a time, from either C' group in turn
@@ -431,18 +435,18 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             const uint32_t v_lo = desc_lo(smem_u32(vp + x % L::NV * PARTS * L::kQuarter), L::kQuarter);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-              mma_ss_lo<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * 4096 + kk * 2048) >> 4),
-                                  v_lo + ((kk * 2048) >> 4), idesc_s2, (x | kk) > 0);
+              mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * 4096 + kk * 2048) >> 4),
+                                  v_lo + ((kk * 2048) >> 4), idesc_s2, (x | kk) > 0, el);
             if constexpr (PARTS == 3)
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk)
-                mma_ss_lo<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * 4096 + kk * 2048) >> 4),
-                                    v_lo + ((2 * L::kQuarter + kk * 2048) >> 4), idesc_s1, 1u);
-            mma_commit(&vp_free[x % L::NV]);
+                mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * 4096 + kk * 2048) >> 4),
+                                    v_lo + ((2 * L::kQuarter + kk * 2048) >> 4), idesc_s1, 1u, el);
+            mma_commit_elect(&vp_free[x % L::NV], el);
           }
           if (!ok) break;
-          mma_commit(kv_done);
-          mma_commit(&empty_b[it % NB]);
+          mma_commit_elect(kv_done, el);
+          mma_commit_elect(&empty_b[it % NB], el);
         }
       } else if (warp == 2) {
         // A B^T, as far ahead as there are buffers; with 64-wide A, A S too,
@@ -453,22 +457,22 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         while (nP < n_it || (kMixed && nQ < n_it)) {
           ++idle;
           // (the tile's other boxes and its B were asked for before its last box)
-          if (nP < n_it && mbar_test_wait(&full[box(nP, BPT - 1)], box_phase(nP, BPT - 1)) &&
-              (nP < kNP || mbar_test_wait(&pc_done[nP % kNP], ((nP - kNP) / kNP) & 1)) &&
-              (!tail(nP) || mbar_test_wait(fixed, 0))) {
+          if (nP < n_it && test(&full[box(nP, BPT - 1)], box_phase(nP, BPT - 1)) &&
+              (nP < kNP || test(&pc_done[nP % kNP], ((nP - kNP) / kNP) & 1)) &&
+              (!tail(nP) || test(fixed, 0))) {
             ok = issue_p(nP);
             if (!ok) break;
             ++nP;
             idle = 0;
           }
-          if (kMixed && nQ < nP && mbar_test_wait(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
-              (nQ == 0 || mbar_test_wait(o1_free, (nQ - 1) & 1))) {
+          if (kMixed && nQ < nP && test(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
+              (nQ == 0 || test(o1_free, (nQ - 1) & 1))) {
             issue_as(nQ);
             ++nQ;
             idle = 0;
           }
           if (idle > 0) __nanosleep(20);
-          if (*abort_flag || idle > (1u << 24)) {
+          if (__any_sync(~0u, *abort_flag != 0) || idle > (1u << 24)) {
             ok = false;
             break;
           }
@@ -496,18 +500,18 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           // two j to a column
 #pragma unroll 1
           for (int part = 0; part < 2; ++part)
-#pragma unroll kUnrollPC
+#pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_ts_lo<kHi>(tmem + L::kColO2,
+              mma_ts_lo_elect<kHi>(tmem + L::kColO2,
                              tmem + bf * 128 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
-                             c_lo + ((kk * 2048) >> 4), idesc_o, (part | kk) > 0);
-          mma_commit(&pc_done[bf]);
-          mma_commit(o2_done);
+                             c_lo + ((kk * 2048) >> 4), idesc_o, (part | kk) > 0, el);
+          mma_commit_elect(&pc_done[bf], el);
+          mma_commit_elect(o2_done, el);
         }
       }
-      if (!ok) record_timeout(a.status, abort_flag);
+      if (!ok && el) record_timeout(a.status, abort_flag);
       // every MMA this thread issued completes before TMEM is released
-      mma_commit(&fin[warp - 1]);
+      mma_commit_elect(&fin[warp - 1], el);
       mbar_wait_timeout(&fin[warp - 1], 0, CP_WAIT_TIMEOUT_NS);
     }
   } else if (warp < 8) {
@@ -642,12 +646,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
               reinterpret_cast<uint4*>(b_s + x * kBoxBytes)[i] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-          ok = agree(3, 128, ok);
-          if (!ok) break;
-          if (tid == 0) mbar_arrive(fixed);
-        } else {
-          ok = ok && wait(fixed, 0, abort_flag);
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(fixed);
         }
+        ok = ok && wait(fixed, 0, abort_flag);
       }
       if (it < n_kv) {
 #pragma unroll 1
@@ -655,8 +657,6 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           const int first = 64 * x + 32 * half;  // row
           const int bf = (2 * x + half) % L::NV;
           uint8_t* to = vp + bf * PARTS * L::kQuarter;
-          if (L::NV == 4 ? it > 0 : it + x > 0)
-            ok = wait(&vp_free[bf], (L::NV == 4 ? it + 1 : x + 1) & 1, abort_flag);
           uint4 v[2];
           float w[2];
           // a thread's pieces of 8 columns are 16 rows apart
@@ -666,6 +666,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             v[y] = reinterpret_cast<const uint4*>(c_s)[8 * first + tid + 128 * y];
             w[y] = r < nv ? s_c * pw[rev ? r : nv - 1 - r] : 0.f;
           }
+          if (L::NV == 4 ? it > 0 : it + x > 0)
+            ok = wait(&vp_free[bf], (L::NV == 4 ? it + 1 : x + 1) & 1, abort_flag);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
@@ -684,12 +686,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
                     make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
           }
           fence_proxy_async_smem();
-          ok = agree(3 + half, 128, ok);
-          if (tid == 0 && ok) mbar_arrive(&vp_ready[bf]);
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&vp_ready[bf]);
         }
       }
       if (!ok) break;
-      if (tid == 0) mbar_arrive(&empty[st]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(AGG ? &empty[st] : &c_read[it % R]);
     }
     if (!ok) record_timeout(a.status, abort_flag);
   } else if (warp < 16) {
@@ -765,7 +768,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       // A S, scaled, waits in registers for P C, whose accumulator is given back
       // as soon as it is read: the next tile's P C waits for it
       float2 o[kMB / 2];
-      ok = wait(o1_done, it & 1, abort_flag);
+      ok = wait(&c_read[it % R], (it / R) & 1, abort_flag);
+      ok = ok && wait(o1_done, it & 1, abort_flag);
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kMB / 16; ++c) {
@@ -796,12 +800,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       if (nv < kTile && row >= nv)
 #pragma unroll
         for (int x = 0; x < kMB / 2; ++x) o[x] = make_float2(0.f, 0.f);
-      // (both C' groups and P C are done with this tile's C: its box takes O)
+      // (this tile's C has been read, by the C' groups and P C: its box takes O)
       const int st = it * BPT % R;
       uint8_t* o_tile = ring + st * kBoxBytes;
+      if (!ok) break;
       if (out_f32 == nullptr) {
-        ok = agree(1, 128, ok);
-        if (!ok) break;
 #pragma unroll
         for (int c = 0; c < kMB / 8; ++c)
           *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 8 * c, 0)) =
@@ -810,16 +813,17 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
                          tc::pack_bf16x2(o[4 * c + 2].x, o[4 * c + 2].y),
                          tc::pack_bf16x2(o[4 * c + 3].x, o[4 * c + 3].y));
         fence_proxy_async_smem();
-        named_barrier_sync(1, 128);
-        if (o_tid == 0) {
-          tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
-          tma_store_commit();
-          tma_store_wait_read_all();
+        __syncwarp();
+        if (lane == 0) {
+          if ((int64_t)tile * kTile + 32 * wq < a.N) {
+            tma_store_3d(&tm_o, o_tile + 32 * wq * 128, mb * kMB, tile * kTile + 32 * wq, oh);
+            tma_store_commit();
+            tma_store_wait_read_all();
+          }
           mbar_arrive(&empty[st]);
         }
       } else {
         // fp32 parts, which a later launch sums over the heads of a group
-        if (!ok) break;
         float* to = out_f32 + ((int64_t)bh * a.N + (int64_t)tile * kTile + row) * own.DC + mb * kMB;
         if ((int64_t)tile * kTile + row < a.N)
 #pragma unroll
@@ -827,25 +831,25 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             if (mb * kMB + 4 * x < own.DC)
               reinterpret_cast<float4*>(to)[x] =
                   make_float4(o[2 * x].x, o[2 * x].y, o[2 * x + 1].x, o[2 * x + 1].y);
-        if (o_tid == 0) mbar_arrive(&empty[st]);
+        if (lane == 0) mbar_arrive(&empty[st]);
       }
     }
     if (!ok) record_timeout(a.status, abort_flag);
-    ok = agree(1, 128, ok);
     // tiles behind the sequence's end: zeros
     if (ok && max(t_first, live) < t_stop) {
       if (out_f32 == nullptr) {
-        // (the box that took the last O is this group's alone by now)
+        // (the rows that took the last O are this warp's alone by now)
+        __syncwarp();
         uint8_t* o_tile = ring + max(0, n_it - 1) * BPT % R * kBoxBytes;
-        named_barrier_sync(1, 128);
 #pragma unroll
         for (int c = 0; c < kMB / 8; ++c)
           *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 8 * c, 0)) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
-        named_barrier_sync(1, 128);
-        if (o_tid == 0) {
+        __syncwarp();
+        if (lane == 0) {
           for (int tile = max(t_first, live); tile < t_stop; ++tile)
-            tma_store_3d(&tm_o, o_tile, mb * kMB, tile * kTile, oh);
+            if ((int64_t)tile * kTile + 32 * wq < a.N)
+              tma_store_3d(&tm_o, o_tile + 32 * wq * 128, mb * kMB, tile * kTile + 32 * wq, oh);
           tma_store_commit();
         }
       } else {
@@ -857,7 +861,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
               make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    if (o_tid == 0) tma_store_wait_all();
+    if (lane == 0) tma_store_wait_all();
   }
 
   tc_fence_before();
@@ -1040,7 +1044,7 @@ cp_status_t run(const DecayShape& s, const float* g, const RowProduct* products,
     if (!tc::make_map(&maps.a[i], p.a, p.a_key ? kh : vh, s.N, p.DA) ||
         !tc::make_map(&maps.b[i], p.b, p.b_key ? kh : vh, s.N, p.DA) ||
         !tc::make_map(&maps.c[i], p.c, p.c_key ? kh : vh, s.N, p.DC) ||
-        !tc::make_map(&maps.o[i], p.out, p.o_key ? kh : vh, s.N, p.DC))
+        !tc::make_map(&maps.o[i], p.out, p.o_key ? kh : vh, s.N, p.DC, 0, 32))
       return CP_ERR_UNSUPPORTED_SHAPE;
     Own& o = set.own[i];
     o.state_in = p.state_in;
