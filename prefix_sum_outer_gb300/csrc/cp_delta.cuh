@@ -129,5 +129,26 @@ __device__ __forceinline__ float2 warp_scan(float2 x, int lane) {
   return x;
 }
 
+// Launched as a programmatic dependent, as the product kernels are: a kernel's
+// launch (and, in the chains, its set-up) runs under the end of the one before
+// it in the stream, and it touches no global memory before that one has
+// completed; a CTA lets the next kernel be scheduled only when its own work is
+// done.
+template <class K, class... A>
+inline cudaError_t launch_dependent(K kern, dim3 grid, unsigned threads, size_t smem,
+                                    cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace delta
 }  // namespace cp

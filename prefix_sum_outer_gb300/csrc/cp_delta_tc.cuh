@@ -550,27 +550,6 @@ __device__ __forceinline__ void decayed_row(uint32_t t_kk, const GateSlot* gs, i
   }
 }
 
-// Launched as a programmatic dependent, as the product kernels are: a kernel's
-// launch (and, in the chains, its set-up) runs under the end of the one before
-// it in the stream, and it touches no global memory before that one has
-// completed; a CTA lets the next kernel be scheduled only when its own work is
-// done.
-template <class K, class... A>
-inline cudaError_t launch_dependent(K kern, dim3 grid, unsigned threads, size_t smem,
-                                    cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // one contiguous shared -> global copy (16-byte aligned, a multiple of 16)
 __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst),

@@ -15,6 +15,7 @@
 #include <atomic>
 
 #include "cp_delta.cuh"
+#include "sm103_ptx.cuh"
 
 namespace cp {
 namespace {
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
   const int h = blockIdx.y;
   const T* x = static_cast<const T*>(a.x) + h * a.sh;
   T* y = static_cast<T*>(a.y) + h * a.yh;
+  ptx::grid_dep_wait();
   Raw<T, VEC> raw[RPT][KV];
   int64_t at[RPT];
 #pragma unroll
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads, kBwdMin<VEC, KV, MT
   const float inv = 1.f / (float)a.C;
   float dw[SUMS ? 1 : E] = {}, db[SUMS ? 1 : E] = {};
   auto place = [&](int which, int e) { return sums + ((which * (E / W) + e / W) * G + t) * W; };
+  ptx::grid_dep_wait();
   if constexpr (SUMS) {
     for (int i = threadIdx.x; i < 2 * E * G; i += blockDim.x) sums[i] = 0.f;
     __syncthreads();
@@ -501,11 +504,12 @@ __global__ void __launch_bounds__(MT > 0 ? MT : kBwdThreads, kBwdMin<VEC, KV, MT
 constexpr int kLines = 32;
 template <typename T>
 __global__ void __launch_bounds__(32 * kLines)
-    layer_norm_join_kernel(const float* __restrict__ part, T* dw, T* db, int P, int C) {
+    layer_norm_join_kernel(const float* part, T* dw, T* db, int P, int C) {
   __shared__ float s[2][kLines][33];
   const int lane = threadIdx.x % 32, line = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   const float* p = part + (int64_t)blockIdx.y * P * 2 * C;
   float x = 0.f, y = 0.f;
+  ptx::grid_dep_wait();
   if (c < C)
 #pragma unroll 4
     for (int i = line; i < P; i += kLines) {
@@ -569,8 +573,7 @@ cudaError_t forward(const LayerNorm& f, const Args& a, cudaStream_t stream) {
   const int threads = MT > 0 ? a.G : 256;
   const int64_t per = (int64_t)kRpt<VEC, KV, MT> * (threads / (MT > 0 ? a.G : GL));
   const dim3 grid((unsigned)((a.rows + per - 1) / per), (unsigned)f.H);
-  layer_norm_fwd_kernel<T, VEC, GL, KV, MT><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(layer_norm_fwd_kernel<T, VEC, GL, KV, MT>, grid, threads, 0, stream, a);
 }
 
 template <typename T, int VEC, int GL, int KV, int MT, bool SUMS = false>
@@ -596,13 +599,12 @@ cudaError_t backward(const LayerNorm& f, const Args& a, const Split& s, cudaStre
       asked.fetch_or(bit, std::memory_order_release);
     }
   }
-  kern<<<dim3(ctas, (unsigned)f.H), threads, smem, stream>>>(a);
-  if (a.part != nullptr) {
-    const int heads = f.per_head ? (int)f.H : 1;
-    layer_norm_join_kernel<T><<<dim3((unsigned)((f.C + 31) / 32), heads), 32 * kLines, 0, stream>>>(
-        a.part, static_cast<T*>(f.dw), static_cast<T*>(f.db), (int)(ctas * f.H / heads), a.C);
-  }
-  return cudaGetLastError();
+  cudaError_t e = launch_dependent(kern, dim3(ctas, (unsigned)f.H), threads, smem, stream, a);
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  const int heads = f.per_head ? (int)f.H : 1;
+  return launch_dependent(layer_norm_join_kernel<T>, dim3((unsigned)((f.C + 31) / 32), heads),
+                          32 * kLines, 0, stream, a.part, static_cast<T*>(f.dw),
+                          static_cast<T*>(f.db), (int)(ctas * f.H / heads), a.C);
 }
 
 template <typename T>
