@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "cp_decay.cuh"
+#include "sm103_ptx.cuh"
 
 namespace cp {
 namespace {
@@ -192,6 +193,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   __shared__ __align__(16) Tile x, y;
   __shared__ float f[kC];
+  ptx::grid_dep_wait();
   const bool rev = blockIdx.z != 0;
   const int64_t bh = blockIdx.x / a.n, c = blockIdx.x % a.n, b = bh / a.H;
   const int h = (int)(bh % a.H);
@@ -245,6 +247,7 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
 
 // prefix: a thread walks one element of a head's state over the chunks
 __global__ void __launch_bounds__(256) decay_prefix_kernel(const Args a, int blocks) {
+  ptx::grid_dep_wait();
   const bool rev = blockIdx.y != 0;
   const int64_t bh = blockIdx.x / blocks, b = bh / a.H;
   const int64_t DM = (int64_t)a.D * a.M, e = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
@@ -295,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 3) decay_out_kernel(const Args a) {
   __shared__ __align__(16) float x[kK][kLd];
   __shared__ __align__(16) Tile y, P;
   __shared__ float pw[kC + 1], f[kC];
+  ptx::grid_dep_wait();
   // 0: the forward's out or dq, 1: dv, 2: dk
   const int kind = a.backward ? (int)blockIdx.z : -1;
   const bool rev = kind > 0;              // order, and which states
@@ -412,16 +416,20 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   const unsigned dirs = a.backward ? 2 : 1;
   const unsigned db = (a.D + kC - 1) / kC, mb = (a.M + kC - 1) / kC;
   if (BH * a.n > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
   if (a.n > 1 || (a.backward ? a.ds0 : a.s_end) != nullptr)
-    decay_sums_kernel<T><<<dim3((unsigned)(BH * a.n), db * mb, dirs), kThreads, 0, stream>>>(a);
-  if (a.n > 1) {
+    e = launch_dependent(decay_sums_kernel<T>, dim3((unsigned)(BH * a.n), db * mb, dirs), kThreads,
+                         0, stream, a);
+  if (e == cudaSuccess && a.n > 1) {
     const int blocks = (a.D * a.M + 255) / 256;
-    decay_prefix_kernel<<<dim3((unsigned)(BH * blocks), dirs), 256, 0, stream>>>(a, blocks);
+    e = launch_dependent(decay_prefix_kernel, dim3((unsigned)(BH * blocks), dirs), 256, 0, stream, a,
+                         blocks);
   }
-  decay_out_kernel<T>
-      <<<dim3((unsigned)(BH * a.n), a.backward ? std::max(db, mb) : mb, a.backward ? 3 : 1),
-         kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(
+      decay_out_kernel<T>,
+      dim3((unsigned)(BH * a.n), a.backward ? std::max(db, mb) : mb, a.backward ? 3 : 1), kThreads, 0,
+      stream, a);
 }
 
 cudaError_t run(const DecayShape& s, Args& a, cudaStream_t stream) {
