@@ -873,6 +873,9 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   }
 }
 
+// power_parts of a part that is not whole, out of line
+static __device__ __noinline__ float2 short_part(float g, int n) { return power_parts(g, n); }
+
 // Sums [problems][G][sub][E] of the pieces' parts give the states the pieces start
 // from, each in the place of its piece's first part in scan order: a thread walks
 // four elements over the parts, whose loads go out ahead.
@@ -902,6 +905,10 @@ __global__ void __launch_bounds__(kPrefixThreads)
     S = make_float4(p[0], p[own.st_c], p[2 * own.st_c], p[3 * own.st_c]);
   }
   const float2 whole = power_parts(g, a.sub_tiles * kTile);
+  // the part at hand, and where the sum behind a piece's last part goes
+  int seg = own.reverse ? a.G - 1 : 0, part = own.reverse ? a.sub - 1 : 0;
+  const int last = own.reverse ? 0 : a.sub - 1;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += kAhead) {
     float4 now[kAhead];
 #pragma unroll
@@ -909,25 +916,28 @@ __global__ void __launch_bounds__(kPrefixThreads)
       now[i] = next[i];
       next[i] = i0 + kAhead + i < n ? s[slot(i0 + kAhead + i) * E4] : float4{};
     }
-#pragma unroll 1
-    for (int i = 0; i < kAhead && i0 + i < n; ++i) {
-      const int at = (int)slot(i0 + i), seg = at / a.sub, part = at % a.sub;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= n) break;
       const int64_t t0 = (int64_t)seg * a.seg_tiles + part * a.sub_tiles;
       const int64_t t1 = min((int64_t)a.n_tiles, min((int64_t)(seg + 1) * a.seg_tiles, t0 + a.sub_tiles));
       const int64_t lo = t0 * kTile, hi = min(rows, t1 * kTile);  // the part's rows
-      float4 x = now[0];
       if (hi > lo) {
         const int m = (int)(hi - lo) - (own.reverse && rows == hi ? 1 : 0);
-        const float2 f = m == a.sub_tiles * kTile ? whole : power_parts(g, m);
-        S.x = fmaf(f.x, S.x, fmaf(f.y, S.x, x.x));
-        S.y = fmaf(f.x, S.y, fmaf(f.y, S.y, x.y));
-        S.z = fmaf(f.x, S.z, fmaf(f.y, S.z, x.z));
-        S.w = fmaf(f.x, S.w, fmaf(f.y, S.w, x.w));
+        const float2 f = m == a.sub_tiles * kTile ? whole : short_part(g, m);
+        S.x = fmaf(f.x, S.x, fmaf(f.y, S.x, now[i].x));
+        S.y = fmaf(f.x, S.y, fmaf(f.y, S.y, now[i].y));
+        S.z = fmaf(f.x, S.z, fmaf(f.y, S.z, now[i].z));
+        S.w = fmaf(f.x, S.w, fmaf(f.y, S.w, now[i].w));
       }
-#pragma unroll
-      for (int y = 0; y + 1 < kAhead; ++y) now[y] = now[y + 1];
       // (the next piece's first sum has been read, being among those ahead)
-      if (part == (own.reverse ? 0 : a.sub - 1)) s[(int64_t)(own.reverse ? at - 1 : at + 1) * E4] = S;
+      const int at = seg * a.sub + part;
+      if (part == last) {
+        s[(int64_t)(own.reverse ? at - 1 : at + 1) * E4] = S;
+        part = own.reverse ? a.sub : -1;
+        seg += own.reverse ? -1 : 1;
+      }
+      part += own.reverse ? -1 : 1;
     }
   }
 }
