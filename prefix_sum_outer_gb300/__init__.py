@@ -1627,7 +1627,9 @@ class LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                bias: Optional[torch.Tensor] = None, eps: float = 1e-5, token_major: bool = False):
     """causal_product_layer_norm with autograd support for x, weight and bias."""
-    return LayerNorm.apply(x, weight, bias, eps, token_major)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+        return LayerNorm.apply(x, weight, bias, eps, token_major)
+    return causal_product_layer_norm(x, weight, bias, eps, token_major)
 
 
 def causal_product(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
