@@ -15,6 +15,8 @@
 // still fill the card.
 //
 // A CTA has 128 threads of 8 rows x 4 columns, on pairs of fp32 (fma.f32x2).
+// The fma pipes and the shared-memory reads that feed them bound it: B=8 H=16 N=4096
+// D=M=64 in fp32, forward 510 us (34 TFLOP/s, scores counted whole), backward 1,334.
 #include <algorithm>
 
 #include "cp_decay.cuh"

