@@ -40,10 +40,10 @@ def heads(x, p):
     return cut(0, HK, D), cut(HK * D, HK, D), cut(2 * HK * D, H, M)
 
 
-def layer(x, p, cos, sin, **kw):
+def layer(x, p, cos, sin, g=None, **kw):
     xq, xk, v = heads(x, p)
     q, k = cp.qk_rope(xq, xk, None, None, cos, sin, "l2")
-    got = cp.causal_product_decay(q, k, v.contiguous(), G.to(DEV), scale=SCALE, **kw)
+    got = cp.causal_product_decay(q, k, v.contiguous(), G.to(DEV) if g is None else g, scale=SCALE, **kw)
     out, s = got if kw.get("return_state") else (got, None)
     y = cp.layer_norm(out, p["h_w"], p["h_b"], token_major=True).flatten(2)
     return x + y @ p["out"], s
@@ -133,3 +133,38 @@ def test_serving():
         assert (step - want).norm() <= 2e-2 * want.norm()
         at = at + 1
     assert not pool[[1, 2, 4]].any() and np.isfinite(float(pool.sum()))
+
+
+def test_training_step_in_a_graph():
+    """A whole step (forward, gradients by autograd) captured after a few on a side
+    stream, replayed on new inputs: bitwise what the same step gives outside."""
+    p = {n: t.requires_grad_() for n, t in weights(torch.bfloat16, seed=3).items()}
+    cos, sin = tables(300)
+    g = G.to(DEV)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x, go = (torch.randn((2, 300, W), device=DEV, generator=gen).bfloat16() for _ in range(2))
+
+    def step():
+        for t in p.values():
+            t.grad = None
+        y, _ = layer(x, p, cos, sin, g)
+        y.backward(go)
+        return y.detach(), [t.grad for t in p.values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, grads = step()
+    for t in (x, go):
+        t.copy_(torch.randn(t.shape, device=DEV, generator=gen))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, *grads)]
+    want, grads = step()
+    for a, b in zip(got, (want, *grads)):
+        assert torch.equal(a, b)
