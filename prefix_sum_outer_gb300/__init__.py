@@ -23,6 +23,7 @@ import threading
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -1563,21 +1564,22 @@ def qk_rope(xq: torch.Tensor, xk: torch.Tensor, wq: Optional[torch.Tensor] = Non
 
 class CausalProductDecay(torch.autograd.Function):
     """Autograd wrapper of linear attention with a decay for each head: (q, k,
-    v, S_0) -> (out, S_N), the decay a constant."""
+    v, S_0) -> (out, S_N or None), the decay a constant."""
 
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, state, scale, lengths):
+    def forward(ctx, q, k, v, log_decay, state, scale, lengths, return_state):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         log_decay = log_decay.contiguous()
         state = None if state is None else state.contiguous()
-        out, s_n = causal_product_fwd_decay(q, k, v, log_decay, state_in=state, return_state=True,
-                                            scale=scale, lengths=lengths)
+        got = causal_product_fwd_decay(q, k, v, log_decay, state_in=state,
+                                       return_state=return_state, scale=scale, lengths=lengths)
         ctx.save_for_backward(q, k, v, log_decay, state, lengths)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
-        return out, s_n
+        return got if return_state else (got, None)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, go, gs):
         q, k, v, log_decay, state, lengths = ctx.saved_tensors
         go = torch.zeros_like(v) if go is None else go.contiguous().to(v.dtype)
@@ -1585,7 +1587,7 @@ class CausalProductDecay(torch.autograd.Function):
         d = causal_product_bwd_decay(q, k, v, log_decay, go, state_in=state, grad_state_out=gs,
                                      return_state_grad=state is not None, scale=ctx.scale,
                                      lengths=lengths)
-        return d[:3] + (None, d[3] if state is not None else None, None, None)
+        return d[:3] + (None, d[3] if state is not None else None, None, None, None)
 
 
 def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1595,12 +1597,14 @@ def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Linear attention with a decay for each head, with autograd support for q,
     k, v and the state (causal_product_fwd_decay); with ``return_state`` the
     result is (out, state after each sequence's last row).  The decay is a
-    constant: one that asks for a gradient is refused."""
+    constant: one that asks for a gradient is refused, as second derivatives
+    are."""
     if torch.is_grad_enabled():
         if log_decay.requires_grad:
             raise ValueError("log_decay is a constant of the head; it has no gradient")
         if any(t is not None and t.requires_grad for t in (q, k, v, state)):
-            out, s_n = CausalProductDecay.apply(q, k, v, log_decay, state, scale, lengths)
+            out, s_n = CausalProductDecay.apply(q, k, v, log_decay, state, scale, lengths,
+                                                bool(return_state))
             return (out, s_n) if return_state else out
     return causal_product_fwd_decay(q.contiguous(), k.contiguous(), v.contiguous(),
                                     log_decay.contiguous(),
@@ -1618,6 +1622,7 @@ class LayerNorm(torch.autograd.Function):
         return causal_product_layer_norm(x, weight, bias, eps, token_major)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x, weight, bias = ctx.saved_tensors
         return causal_product_layer_norm_bwd(x, weight, bias, gy.contiguous().to(x.dtype), ctx.eps,
@@ -1626,7 +1631,8 @@ class LayerNorm(torch.autograd.Function):
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                bias: Optional[torch.Tensor] = None, eps: float = 1e-5, token_major: bool = False):
-    """causal_product_layer_norm with autograd support for x, weight and bias."""
+    """causal_product_layer_norm with autograd support for x, weight and bias (first
+    derivatives; a second one is refused)."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return LayerNorm.apply(x, weight, bias, eps, token_major)
     return causal_product_layer_norm(x, weight, bias, eps, token_major)
