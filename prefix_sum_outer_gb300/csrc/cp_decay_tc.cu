@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   uint64_t* full_c = empty_a + RA;     // [RC]
   uint64_t* empty_c = full_c + RC;     // [RC]
   uint64_t* c_read = empty_c + RC;     // [RC] read by the C' groups
-  uint64_t* p_done = c_read + RC;       // [kNP] A B^T in TMEM
+  uint64_t* p_done = c_read + RC;      // [kNP] A B^T in TMEM
   uint64_t* p_ready = p_done + kNP;    // [kNP] P packed
   uint64_t* pc_done = p_ready + kNP;   // [kNP] P C done: the buffer is free
   uint64_t* s_ready = pc_done + kNP;   // [2] copy of S written
