@@ -521,11 +521,10 @@ CP_API cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* str
  * head), grad_v, and grad_state_in = dL/dS_0 (NULL: not written).
  *
  * State and sums are fp32, and a state that is returned is as exact as fp32
- * arithmetic on every path.  bf16 rows (D, M <= 128) enter their products on the
- * tensor cores as sums of bf16 numbers, two where only bf16 results are wanted,
- * three where the state (or its gradient) is: out may differ in its last bf16 bit
- * between a call with state_out and one without.  Results are bitwise
- * reproducible.  Workspace: causal_product_decay_workspace_size bytes, or NULL
+ * arithmetic on every path.  On the tensor cores (bf16, D, M <= 128) the state and
+ * the rows that it takes enter their products as sums of three bf16 numbers, a
+ * tile's decayed scores as two (17 bits).  Results are bitwise reproducible, and
+ * whether a state is asked for changes no other result.  Workspace: causal_product_decay_workspace_size bytes, or NULL
  * (allocated and freed on `stream`).  Errors as causal_product_fwd; CP_ERR_INVALID_ARG too when Hk does
  * not divide H or scale is not finite. */
 CP_API size_t causal_product_decay_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N,

@@ -1157,9 +1157,8 @@ def causal_product_fwd_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     (float32 [B,H,D,M], None = zero).  ``lengths`` (int32 [B], on the device):
     sequence b is its first lengths[b] rows; rows behind them reach nothing and
     give zero.  Returns out, with ``return_state`` followed by the state after
-    each sequence's last row, as exact as fp32 arithmetic (bf16 rows then enter
-    the tensor cores in three numbers instead of two, and out may differ from
-    the same call without it in its last bit)."""
+    each sequence's last row, as exact as fp32 arithmetic (asking for it changes
+    no bit of out)."""
     place = _elsewhere(q, stream)
     if place is not None:
         with place:

@@ -11,20 +11,25 @@
 // Nothing in a tile but A S waits for the state, and the state's update is one
 // fma, so the tiles stream through a pipeline of warps:
 //   warp 0        TMA producer: A, B and C tiles into a ring each, whichever has room
-//   warps 1..3    MMA issuers: B^T C'; A B^T; P C; A S by one of the last two
-//   warps 4..7    state group: fp32 S in registers (thread = row); its hi + lo
-//                 copy, the operand of A S
+//   warps 1..3    MMA issuers: B^T C'; A B^T and A S; P C
+//   warps 4..7    state group: fp32 S in registers (thread = row); its copy as three
+//                 bf16 numbers, the operand of A S
 //   warps 8..15   P groups: P times its powers, masked, hi + lo, back into TMEM
 //   warps 16..19  O group: O from its two accumulators, to bf16, TMA store
-//   warps 20..27  C' groups: a row times its power, as two or three bf16 numbers
+//   warps 20..27  C' groups: a row times its power, as three bf16 numbers
 // A CTA walks one piece of one head's sequence for 64 columns of c.
 //
 // Precision.  S lives in registers in fp32 and takes each tile's B^T C' by an fma
 // that rounds to nearest, its decay as hi + lo: an accumulator kept in tensor
 // memory would be rounded toward zero at every MMA and lose 1e-5 of a state that
-// remembers thousands of rows.  Where the state itself is a result (S_N, dS_0) C'
-// is three bf16 numbers, all 24 bits; for bf16 results two (2^-17) are far below
-// their rounding, as they are for P and for S as an operand.
+// remembers thousands of rows.  C' and the copy of S enter their products as three bf16
+// numbers, all 24 bits, whether or not a state is asked for, so that asking changes no
+// other result.  P has two (17 bits): its rounding, 2e-6 of a score, is a hundredth of
+// a bf16 result's own step of 2^-9, and moves one result in a thousand or two to the next
+// bf16 number.  A third part of P would need 64 columns more of a tensor memory that is
+// full, a second accumulator for B^T C' given up for them: 96 against 66 us (B=8 H=16
+// N=4096 D=M=64), with the results 4.8e-5 from the rounded 64-bit ones instead of 5.4e-5
+// (two parts of everything: 1.1e-4).
 //
 // Powers come from a table of e^{g n}, n <= 128, of products in shared memory: a
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
@@ -32,11 +37,11 @@
 //
 // No memory or matrix rate bounds it: with any one of the products, or of the
 // groups' stores, left out it is at most 4 % faster, without the P groups' work 10 %.
-// The roles share four schedulers, and a tile takes about 3,100 cycles with 64-wide A
-// (1,700 of them the tensor core's, for the bf16 parts) and 4,500 with 128, where C's
-// two boxes, which wait for O, hold up the next.  Forward with the state: B=8 H=16
-// N=4096 D=M=64 63 us, 64 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 220;
-// forward and backward of the first 224.  O straight from the registers, 32 bytes of a
+// The roles share four schedulers, and a tile takes about 3,300 cycles with 64-wide A
+// (1,900 of them the tensor core's, for the bf16 parts) and 4,800 with 128, where C's
+// two boxes, which wait for O, hold up the next.  Forward: B=8 H=16 N=4096 D=M=64 66 us,
+// 61 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 231; forward and backward of
+// the first 252.  O straight from the registers, 32 bytes of a
 // row to a store, frees C sooner: 215 for the second, but 232 for the last.
 //
 // Sequences of few heads are cut into pieces: the same kernel with the output
@@ -95,31 +100,37 @@ struct Maps {
   CUtensorMap a[MAX], b[MAX], c[MAX], o[MAX];
 };
 
-// PARTS: bf16 numbers to an element of C'
-template <int DP, int PARTS, bool AGG>
+// The bf16 numbers that an element of C', and of the copy of S, enters its products as:
+// all of its 24 bits.
+constexpr int kParts = 3;
+
+template <int DP, bool AGG>
 struct Layout {
   static constexpr int kABoxes = DP / 64;
   static constexpr int kBStage = kABoxes * kBoxBytes;
   static constexpr int kSOne = DP * 128;                       // a bf16 copy of the state
-  static constexpr int kQuarter = kBoxBytes / 4;               // a part of 32 rows of C'
-  static constexpr int NV = AGG || (DP == 128 && PARTS == 3) ? 2 : 4;  // buffers of 32 rows of C'
-  static constexpr int kVBytes = NV * PARTS * kQuarter;
-  static constexpr int kTotal = (kSmemLimit - 1024 - kBarBytes - kTableBytes) / kBoxBytes;  // boxes
-  static constexpr int NSB = 1;                                // copies of S
-  static constexpr int kSBoxes = AGG ? 0 : NSB * 2 * kSOne / kBoxBytes;
+  static constexpr int kSBytes = AGG ? 0 : kParts * kSOne;
+  // C' goes a few rows at a time through NV buffers: with 128-wide A the copies of S
+  // leave room for two of 16 rows
+  static constexpr int kVRows = !AGG && DP == 128 ? 16 : 32;
+  static constexpr int kVOne = kVRows * 128;                   // a part of them
+  static constexpr int NV = AGG || DP == 128 ? 2 : 4;
+  static constexpr int kPieces = kTile / kVRows;               // to a tile
+  static constexpr int kVBytes = NV * kParts * kVOne;
+  static constexpr int kRoom = kSmemLimit - 1024 - kBarBytes - kTableBytes;
   static constexpr int NB = AGG && DP == 128 ? 1 : 2;          // stages of the B ring
   // tiles of A, which wait for the state, and of C, whose boxes take O: what is left.
   // In one ring, C before A, a 128-wide A waited for the O two tiles back: 235 against
   // 220 us (B=2 H=8 N=32768 D=M=128)
   static constexpr int RA = AGG ? 0 : DP == 128 ? 2 : 3;
-  static constexpr int RC =
-      AGG ? 3 : kTotal - (NB + RA) * kABoxes - kSBoxes - (kVBytes + kBoxBytes - 1) / kBoxBytes;
-  static constexpr int kBoxes = (NB + RA) * kABoxes + RC + kSBoxes;
-  static constexpr int kSmem = kBoxes * kBoxBytes + kVBytes + kBarBytes + kTableBytes + 1024;
+  static constexpr int RC = AGG ? 3 : (kRoom - (NB + RA) * kBStage - kSBytes - kVBytes) / kBoxBytes;
+  static constexpr int kBoxes = (NB + RA) * kABoxes + RC;
+  static constexpr int kSmem =
+      kBoxes * kBoxBytes + kSBytes + kVBytes + kBarBytes + kTableBytes + 1024;
   static constexpr int kVGroup = AGG ? 8 : 20;                 // first warp of the C' groups
   static constexpr int kThreads = 32 * (kVGroup + 8);
   static constexpr int SC = DP / 2;                            // columns of S to a thread
-  // tensor memory: P, A S, P C, and B^T C' as [hi | rest]
+  // tensor memory: P, A S, P C, and B^T C' as [first part | rest]
   static constexpr int kColO1 = kNP * 128, kColO2 = kColO1 + kMB;
   static constexpr int kColS = AGG ? 0 : kColO2 + kMB;
   static constexpr int kCols = AGG ? 128 : 512;
@@ -182,19 +193,19 @@ __device__ __forceinline__ void fewer_registers() {
 
 // MAX: products that share a launch, at most (their CTAs in turn, so that those of
 // one head, which read the same rows, run side by side)
-template <int DP, int PARTS, bool AGG, int MAX>
-__global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
+template <int DP, bool AGG, int MAX>
+__global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
     decay_tc_kernel(const __grid_constant__ Maps<MAX> maps, const __grid_constant__ Set<MAX> set) {
-  using L = Layout<DP, PARTS, AGG>;
-  constexpr int NB = L::NB, RA = L::RA, RC = L::RC, NSB = L::NSB;
+  using L = Layout<DP, AGG>;
+  constexpr int NB = L::NB, RA = L::RA, RC = L::RC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_tiles(smem_raw);
   uint8_t* b_ring = smem;                            // [NB] B tiles
   uint8_t* a_ring = b_ring + NB * L::kBStage;        // [RA] A tiles
   uint8_t* ring = a_ring + RA * L::kBStage;          // [RC] C boxes
-  uint8_t* vp = ring + RC * kBoxBytes;               // [NV][PARTS] 32 rows of C'
-  uint8_t* s_tile = vp + L::kVBytes;                 // [NSB] hi | lo copies of S
-  uint64_t* full_b = reinterpret_cast<uint64_t*>(s_tile + L::kSBoxes * kBoxBytes);
+  uint8_t* vp = ring + RC * kBoxBytes;               // [NV][kParts] a piece's rows of C'
+  uint8_t* s_tile = vp + L::kVBytes;                 // [kParts] the copy of S
+  uint64_t* full_b = reinterpret_cast<uint64_t*>(s_tile + L::kSBytes);
   uint64_t* empty_b = full_b + NB;
   uint64_t* full_a = empty_b + NB;     // [RA]
   uint64_t* empty_a = full_a + RA;     // [RA]
@@ -204,13 +215,13 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
   uint64_t* p_done = c_read + RC;      // [kNP] A B^T in TMEM
   uint64_t* p_ready = p_done + kNP;    // [kNP] P packed
   uint64_t* pc_done = p_ready + kNP;   // [kNP] P C done: the buffer is free
-  uint64_t* s_ready = pc_done + kNP;   // [2] copy of S written
-  uint64_t* as_done = s_ready + 2;     // [2] A S done: the copy is free
-  uint64_t* o1_done = as_done + 2;     // A S
+  uint64_t* s_ready = pc_done + kNP;   // copy of S written
+  uint64_t* as_done = s_ready + 1;     // A S done: the copy is free
+  uint64_t* o1_done = as_done + 1;     // A S
   uint64_t* o2_done = o1_done + 1;     // P C
   uint64_t* o1_free = o2_done + 1;     // read
   uint64_t* o2_free = o1_free + 1;
-  uint64_t* vp_ready = o2_free + 1;    // [4] 32 rows of C' written
+  uint64_t* vp_ready = o2_free + 1;    // [4] a piece of C' written
   uint64_t* vp_free = vp_ready + 4;    // [4] their products done
   uint64_t* kv_done = vp_free + 4;     // B^T C' in TMEM
   uint64_t* kv_free = kv_done + 1;     // B^T C' read
@@ -261,10 +272,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       mbar_init(&p_ready[i], 8);
       mbar_init(&pc_done[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_ready[i], 4);
-      mbar_init(&as_done[i], 1);
-    }
+    mbar_init(s_ready, 4);
+    mbar_init(as_done, 1);
     mbar_init(o1_done, 1);
     mbar_init(o2_done, 1);
     mbar_init(o1_free, 4);
@@ -403,9 +412,8 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       auto tail = [&](int it) { return rows_in(tile_of(it)) < kTile; };
       bool ok = true;
       const uint32_t el = elect_one();
-      // A S is issued by the warp of A B^T, or by that of P C: with 64-wide A 72 and
-      // 79 us (B=8 H=16 N=4096), with 128-wide 245 and 240 (B=2 H=8 N=32768)
-      constexpr bool kMixed = DP == 64;
+      // (A S is issued by the warp of A B^T: by that of P C it would take 234 against 232
+      // us with 128-wide A, B=2 H=8 N=32768, and more with 64-wide)
       // (these loops stay rolled: with four MMAs to a turn forward and backward of the
       // same take 223 against 220 us)
       [[maybe_unused]] auto issue_p = [&](int it) {
@@ -423,21 +431,22 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       };
       [[maybe_unused]] auto issue_as = [&](int it) {
         tc_fence_after();
-        const uint32_t s_lo = desc_lo(smem_u32(s_tile + (it % NSB) * 2 * L::kSOne), L::kSOne);
+        const uint32_t s_lo = desc_lo(smem_u32(s_tile), L::kSOne);
         const uint32_t q_lo = desc_lo(a_addr(it), 16);
+        // (the small parts first: an MMA rounds its sum toward zero)
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part)
+        for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll 2
           for (int kk = 0; kk < DP / 16; ++kk)
             mma_ss_lo_elect<kHi, kHi>(
                 tmem + L::kColO1, q_lo + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
-                s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, (part | kk) > 0, el);
-        mma_commit_elect(&as_done[it % NSB], el);
+                s_lo + ((part * L::kSOne + kk * 2048) >> 4), idesc_o, part < kParts - 1 || kk > 0, el);
+        mma_commit_elect(as_done, el);
         mma_commit_elect(o1_done, el);
         mma_commit_elect(&empty_a[it % max(RA, 1)], el);
       };
       if (warp == 1) {
-        // B^T C', 32 rows at a time, from either C' group in turn
+        // B^T C', a piece at a time, from either C' group in turn
 #pragma unroll 1
         for (int it = 0; it < n_kv && ok; ++it) {
           ok = wait(&full_b[it % NB], (it / NB) & 1, abort_flag) &&
@@ -447,19 +456,19 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           // halves of the lanes hold the state's rows)
           const uint32_t bt_lo = desc_lo(b_addr(it), DP == 64 ? 0 : kBoxBytes);
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            if (!ok || !wait(&vp_ready[x % L::NV], L::NV == 4 ? it & 1 : x >> 1, abort_flag)) { ok = false; break; }
+          for (int x = 0; x < L::kPieces; ++x) {
+            const uint32_t parity = L::NV == 4 ? it & 1 : x >> 1 & 1;
+            if (!ok || !wait(&vp_ready[x % L::NV], parity, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t v_lo = desc_lo(smem_u32(vp + x % L::NV * PARTS * L::kQuarter), L::kQuarter);
+            const uint32_t v_lo = desc_lo(smem_u32(vp + x % L::NV * kParts * L::kVOne), L::kVOne);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * 4096 + kk * 2048) >> 4),
+            for (int kk = 0; kk < L::kVRows / 16; ++kk)
+              mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS, bt_lo + ((x * L::kVOne + kk * 2048) >> 4),
                                   v_lo + ((kk * 2048) >> 4), idesc_s2, (x | kk) > 0, el);
-            if constexpr (PARTS == 3)
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
-                mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * 4096 + kk * 2048) >> 4),
-                                    v_lo + ((2 * L::kQuarter + kk * 2048) >> 4), idesc_s1, 1u, el);
+            for (int kk = 0; kk < L::kVRows / 16; ++kk)
+              mma_ss_lo_elect<kHi, kHi>(tmem + L::kColS + kMB, bt_lo + ((x * L::kVOne + kk * 2048) >> 4),
+                                  v_lo + ((2 * L::kVOne + kk * 2048) >> 4), idesc_s1, 1u, el);
             mma_commit_elect(&vp_free[x % L::NV], el);
           }
           if (!ok) break;
@@ -467,12 +476,11 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           mma_commit_elect(&empty_b[it % NB], el);
         }
       } else if (warp == 2) {
-        // A B^T, as far ahead as there are buffers; with 64-wide A, A S too,
-        // whichever can go
+        // A B^T, as far ahead as there are buffers, and A S, whichever can go
         int nP = 0, nQ = 0;
         uint32_t idle = 0;
 #pragma unroll 1
-        while (nP < n_it || (kMixed && nQ < n_it)) {
+        while (nP < n_it || nQ < n_it) {
           ++idle;
           if (nP < n_it && test(&full_a[nP % max(RA, 1)], (nP / max(RA, 1)) & 1) &&
               test(&full_b[nP % NB], (nP / NB) & 1) &&
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
             ++nP;
             idle = 0;
           }
-          if (kMixed && nQ < nP && test(&s_ready[nQ % NSB], (nQ / NSB) & 1) &&
+          if (nQ < nP && test(s_ready, nQ & 1) &&
               (nQ == 0 || test(o1_free, (nQ - 1) & 1))) {
             issue_as(nQ);
             ++nQ;
@@ -495,17 +503,10 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           }
         }
       } else {
-        // P C; with 128-wide A, A S before it
+        // P C
 #pragma unroll 1
         for (int it = 0; it < n_it && ok; ++it) {
           const int bf = it % kNP, x = it % RC;
-          if (!kMixed) {
-            ok = wait(&p_done[bf], (it / kNP) & 1, abort_flag) &&  // A has landed
-                 wait(&s_ready[it % NSB], (it / NSB) & 1, abort_flag) &&
-                 (it == 0 || wait(o1_free, (it - 1) & 1, abort_flag));
-            if (!ok) break;
-            issue_as(it);
-          }
           ok = wait(&p_ready[bf], (it / kNP) & 1, abort_flag) &&
                wait(&full_c[x], (it / RC) & 1, abort_flag) &&
                (it == 0 || wait(o2_free, (it - 1) & 1, abort_flag)) &&
@@ -514,14 +515,14 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           tc_fence_after();
           const uint32_t c_lo = desc_lo(smem_u32(ring + x * kBoxBytes), kBoxBytes);
           // 32 columns of P: hi in their first 16 TMEM columns, lo in the next,
-          // two j to a column
+          // two j to a column (lo first, as in A S)
 #pragma unroll 1
-          for (int part = 0; part < 2; ++part)
+          for (int part = 1; part >= 0; --part)
 #pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
               mma_ts_lo_elect<kHi>(tmem + L::kColO2,
                              tmem + bf * 128 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
-                             c_lo + ((kk * 2048) >> 4), idesc_o, (part | kk) > 0, el);
+                             c_lo + ((kk * 2048) >> 4), idesc_o, part < 1 || kk > 0, el);
           mma_commit_elect(&pc_done[bf], el);
           mma_commit_elect(o2_done, el);
         }
@@ -565,29 +566,30 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
 #pragma unroll 1
       for (int it = 0; it < n_it; ++it) {
         if constexpr (!AGG) {
-          const int sb = it % NSB;
-          uint8_t* sbuf = s_tile + sb * 2 * L::kSOne;
-          // the A S that last read this copy has completed
-          if (it >= NSB && !wait(&as_done[sb], ((it - NSB) / NSB) & 1, abort_flag)) {
+          // the A S that last read the copy has completed
+          if (it > 0 && !wait(as_done, (it - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
 #pragma unroll
           for (int c = 0; c < SC / 8; ++c) {
-            uint32_t hi[4], lo[4];
+            uint32_t p[kParts][4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               float2 s = S[4 * c + x];
-              hi[x] = split_hi(s);
-              lo[x] = tc::pack_bf16x2(s.x, s.y);
+#pragma unroll
+              for (int y = 0; y < kParts - 1; ++y) p[y][x] = split_hi(s);
+              p[kParts - 1][x] = tc::pack_bf16x2(s.x, s.y);
             }
             const uint32_t off = sw128_offset(d, c0 + 8 * c, 0);
-            *reinterpret_cast<uint4*>(sbuf + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(sbuf + L::kSOne + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int y = 0; y < kParts; ++y)
+              *reinterpret_cast<uint4*>(s_tile + y * L::kSOne + off) =
+                  make_uint4(p[y][0], p[y][1], p[y][2], p[y][3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_ready[sb]);
+          if (lane == 0) mbar_arrive(s_ready);
         }
         if (it < n_kv) {
           const int tile = tile_of(it), nv = rows_in(tile);
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
       }
     }
   } else if (warp >= L::kVGroup) {
-    // -------------------------------- C' groups: every other 32 rows of a tile
+    // -------------------------------- C' groups: every other piece of a tile
     fewer_registers<DP == 64 ? 56 : AGG ? 48 : 40>();
     const int half = (warp - L::kVGroup) / 4;
     const int tid = threadIdx.x - 32 * L::kVGroup - 128 * half;
@@ -669,16 +671,16 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
         ok = ok && wait(fixed, 0, abort_flag);
       }
       if (it < n_kv) {
+        constexpr int kEach = L::kVRows / 16;   // pieces of 8 columns to a thread, 16 rows apart
 #pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
-          const int first = 64 * x + 32 * half;  // row
+        for (int x = 0; x < L::kPieces / 2 && ok; ++x) {
+          const int first = L::kVRows * (2 * x + half);  // row
           const int bf = (2 * x + half) % L::NV;
-          uint8_t* to = vp + bf * PARTS * L::kQuarter;
-          uint4 v[2];
-          float w[2];
-          // a thread's pieces of 8 columns are 16 rows apart
+          uint8_t* to = vp + bf * kParts * L::kVOne;
+          uint4 v[kEach];
+          float w[kEach];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < kEach; ++y) {
             const int r = first + tid / 8 + 16 * y;
             v[y] = reinterpret_cast<const uint4*>(c_s)[8 * first + tid + 128 * y];
             w[y] = r < nv ? s_c * pw[rev ? r : nv - 1 - r] : 0.f;
@@ -686,20 +688,20 @@ __global__ void __launch_bounds__(Layout<DP, PARTS, AGG>::kThreads, AGG ? 2 : 1)
           if (L::NV == 4 ? it > 0 : it + x > 0)
             ok = wait(&vp_free[bf], (L::NV == 4 ? it + 1 : x + 1) & 1, abort_flag);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < kEach; ++y) {
             const uint32_t in[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-            uint32_t out[PARTS][4];
+            uint32_t out[kParts][4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               float2 f = mul2(both(w[y]), widen(in[z]));
 #pragma unroll
-              for (int p = 0; p < PARTS - 1; ++p) out[p][z] = split_hi(f);
-              out[PARTS - 1][z] = tc::pack_bf16x2(f.x, f.y);
+              for (int p = 0; p < kParts - 1; ++p) out[p][z] = split_hi(f);
+              out[kParts - 1][z] = tc::pack_bf16x2(f.x, f.y);
             }
             if (ok)
 #pragma unroll
-              for (int p = 0; p < PARTS; ++p)
-                reinterpret_cast<uint4*>(to + p * L::kQuarter)[tid + 128 * y] =
+              for (int p = 0; p < kParts; ++p)
+                reinterpret_cast<uint4*>(to + p * L::kVOne)[tid + 128 * y] =
                     make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
           }
           fence_proxy_async_smem();
@@ -1001,10 +1003,10 @@ Plan plan(const DecayShape& s, int64_t DA, int64_t DC, int products) {
   return p;
 }
 
-template <int DP, int PARTS, bool AGG, int MAX>
+template <int DP, bool AGG, int MAX>
 cudaError_t launch(const Maps<MAX>& maps, const Set<MAX>& set, unsigned grid, cudaStream_t stream) {
-  using L = Layout<DP, PARTS, AGG>;
-  auto kern = decay_tc_kernel<DP, PARTS, AGG, MAX>;
+  using L = Layout<DP, AGG>;
+  auto kern = decay_tc_kernel<DP, AGG, MAX>;
   // the shared-memory opt-in is set once per device for each instantiation
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -1019,18 +1021,18 @@ cudaError_t launch(const Maps<MAX>& maps, const Set<MAX>& set, unsigned grid, cu
   return launch_dependent(kern, dim3(grid), L::kThreads, L::kSmem, stream, maps, set);
 }
 
-template <int DP, int PARTS, int MAX>
+template <int DP, int MAX>
 cudaError_t launch_all(const Plan& pl, const Maps<MAX>& maps, const Set<MAX>& set,
                        cudaStream_t stream) {
   const unsigned n = (unsigned)(pl.problems * set.all.products);
   if (pl.G > 1) {
-    cudaError_t e = launch<DP, PARTS, true, MAX>(maps, set, n * (pl.G - 1) * pl.sub, stream);
+    cudaError_t e = launch<DP, true, MAX>(maps, set, n * (pl.G - 1) * pl.sub, stream);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(pl.problems * DP * kMB / 4 / kPrefixThreads), set.all.products);
     e = launch_dependent(decay_tc_prefix_kernel<MAX>, grid, kPrefixThreads, 0, stream, set, DP);
     if (e != cudaSuccess) return e;
   }
-  return launch<DP, PARTS, false, MAX>(maps, set, n * pl.G, stream);
+  return launch<DP, false, MAX>(maps, set, n * pl.G, stream);
 }
 
 struct RowProduct {
@@ -1065,7 +1067,6 @@ cp_status_t run(const DecayShape& s, const float* g, const RowProduct* products,
   a.n_mb = pl.n_mb; a.n_tiles = pl.n_tiles; a.seg_tiles = pl.seg_tiles; a.G = pl.G;
   a.sub = pl.sub; a.sub_tiles = pl.sub_tiles;
   a.products = n;
-  bool state = false;
   for (int i = 0; i < n; ++i) {
     const RowProduct& p = products[i];
     if (!tc::make_map(&maps.a[i], p.a, p.a_key ? kh : vh, s.N, p.DA) ||
@@ -1084,12 +1085,9 @@ cp_status_t run(const DecayShape& s, const float* g, const RowProduct* products,
     o.a_key = p.a_key; o.b_key = p.b_key; o.c_key = p.c_key; o.o_key = p.o_key;
     o.reverse = p.reverse;
     o.s_p = p.s_p; o.s_o = p.s_o; o.s_c = p.s_c;
-    state = state || p.state_out != nullptr;
   }
-  const cudaError_t e = pl.DP == 64 ? (state ? launch_all<64, 3>(pl, maps, set, stream)
-                                             : launch_all<64, 2>(pl, maps, set, stream))
-                                    : (state ? launch_all<128, 3>(pl, maps, set, stream)
-                                             : launch_all<128, 2>(pl, maps, set, stream));
+  const cudaError_t e = pl.DP == 64 ? launch_all<64>(pl, maps, set, stream)
+                                    : launch_all<128>(pl, maps, set, stream);
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
