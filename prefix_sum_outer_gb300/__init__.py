@@ -23,6 +23,7 @@ import threading
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import build as _build
@@ -1495,6 +1496,14 @@ def causal_product_favor(xq: torch.Tensor, xk: torch.Tensor, v: torch.Tensor,
     return CausalProductFavor.apply(xq, xk, v, W)
 
 
+def _no_tangents(*tensors: Optional[torch.Tensor]) -> None:
+    """Refuses forward-mode derivatives: a dual tensor asks for no gradient, so a
+    call that goes past autograd where none is wanted would lose its tangent."""
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("this operator has no forward-mode derivative")
+
+
 class CausalProductDelta(torch.autograd.Function):
     """Autograd wrapper of the gated delta rule: (q, k, v, g, beta, S_0) ->
     (out, S_N)."""
@@ -1525,7 +1534,9 @@ def causal_product_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
                          beta: torch.Tensor, state: Optional[torch.Tensor] = None,
                          return_state: bool = False, scale: float = 1.0):
     """The gated delta rule with autograd support (causal_product_fwd_delta);
-    with ``return_state`` the result is (out, state after the last row)."""
+    with ``return_state`` the result is (out, state after the last row).
+    Forward-mode derivatives are refused."""
+    _no_tangents(q, k, v, g, beta, state)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                        for t in (q, k, v, g, beta, state)):
         out, s_n = CausalProductDelta.apply(q, k, v, g, beta, state, scale)
@@ -1596,8 +1607,9 @@ def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Linear attention with a decay for each head, with autograd support for q,
     k, v and the state (causal_product_fwd_decay); with ``return_state`` the
     result is (out, state after each sequence's last row).  The decay is a
-    constant: one that asks for a gradient is refused, as second derivatives
-    are."""
+    constant: one that asks for a gradient is refused, as second and
+    forward-mode derivatives are."""
+    _no_tangents(q, k, v, log_decay, state)
     if torch.is_grad_enabled():
         if log_decay.requires_grad:
             raise ValueError("log_decay is a constant of the head; it has no gradient")
@@ -1631,7 +1643,8 @@ class LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                bias: Optional[torch.Tensor] = None, eps: float = 1e-5, token_major: bool = False):
     """causal_product_layer_norm with autograd support for x, weight and bias (first
-    derivatives; a second one is refused)."""
+    derivatives; a second or a forward-mode one is refused)."""
+    _no_tangents(x, weight, bias)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return LayerNorm.apply(x, weight, bias, eps, token_major)
     return causal_product_layer_norm(x, weight, bias, eps, token_major)
