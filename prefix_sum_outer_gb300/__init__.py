@@ -1393,13 +1393,23 @@ def causal_product_layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor
     return dx, dw, db
 
 
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """The tensor as the C entry points take it: contiguous, at a whole 16-byte
+    address.  A dense view may start anywhere: a slice of a batch of odd widths,
+    the gradient that torch.cat hands to one of its parts."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class CausalProduct(torch.autograd.Function):
     """Autograd wrapper: forward and backward both call the C ABI; the
     forward keeps checkpoints of the state for the backward's dq scans."""
 
     @staticmethod
     def forward(ctx, q, k, v):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
         out, ckpt = causal_product_fwd_ckpt(q, k, v)
         ctx.save_for_backward(q, k, v, ckpt)
         return out
@@ -1407,7 +1417,7 @@ class CausalProduct(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         q, k, v, ckpt = ctx.saved_tensors
-        return causal_product_bwd_ckpt(q, k, v, g.contiguous().to(q.dtype), ckpt)
+        return causal_product_bwd_ckpt(q, k, v, _dense(g.to(q.dtype)), ckpt)
 
 
 class Normalizer(torch.autograd.Function):
@@ -1415,7 +1425,7 @@ class Normalizer(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, feature):
-        q, k = q.contiguous(), k.contiguous()
+        q, k = _dense(q), _dense(k)
         ctx.save_for_backward(q, k)
         ctx.feature = feature
         return causal_product_normalizer(q, k, feature=feature)
@@ -1423,7 +1433,7 @@ class Normalizer(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gz):
         q, k = ctx.saved_tensors
-        dq, dk = causal_product_normalizer_bwd(q, k, gz.contiguous().float(), feature=ctx.feature)
+        dq, dk = causal_product_normalizer_bwd(q, k, _dense(gz.float()), feature=ctx.feature)
         return dq, dk, None
 
 
@@ -1438,7 +1448,7 @@ class CausalProductFeature(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, feature):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
         ctx.save_for_backward(q, k, v)
         ctx.feature = feature
         return causal_product_fwd_feature(q, k, v, feature)
@@ -1446,7 +1456,7 @@ class CausalProductFeature(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         q, k, v = ctx.saved_tensors
-        dq, dk, dv = causal_product_bwd_feature(q, k, v, g.contiguous().to(q.dtype), ctx.feature)
+        dq, dk, dv = causal_product_bwd_feature(q, k, v, _dense(g.to(q.dtype)), ctx.feature)
         return dq, dk, dv, None
 
 
@@ -1455,8 +1465,8 @@ class CausalProductState(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, state):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        state = None if state is None else state.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
+        state = _dense(state)
         ctx.save_for_backward(q, k, v, state)
         ctx.has_state = state is not None
         return causal_product_fwd(q, k, v, state_in=state, return_state=True)
@@ -1464,8 +1474,8 @@ class CausalProductState(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, g_state):
         q, k, v, state = ctx.saved_tensors
-        g = torch.zeros_like(v) if g is None else g.contiguous().to(q.dtype)
-        g_state = None if g_state is None else g_state.contiguous().float()
+        g = torch.zeros_like(v) if g is None else _dense(g.to(q.dtype))
+        g_state = None if g_state is None else _dense(g_state.float())
         dq, dk, dv, ds = causal_product_bwd(q, k, v, g, state_in=state if ctx.has_state else None,
                                             grad_state_out=g_state, return_state_grad=True)
         return dq, dk, dv, (ds if ctx.has_state else None)
@@ -1477,14 +1487,14 @@ class CausalProductFavor(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, xq, xk, v, W):
-        xq, xk, v, W = xq.contiguous(), xk.contiguous(), v.contiguous(), W.contiguous()
+        xq, xk, v, W = _dense(xq), _dense(xk), _dense(v), _dense(W)
         ctx.save_for_backward(xq, xk, v, W)
         return causal_product_fwd_favor(xq, xk, v, W)
 
     @staticmethod
     def backward(ctx, g):
         xq, xk, v, W = ctx.saved_tensors
-        dxq, dxk, dv = causal_product_bwd_favor(xq, xk, v, W, g.contiguous().to(v.dtype))
+        dxq, dxk, dv = causal_product_bwd_favor(xq, xk, v, W, _dense(g.to(v.dtype)))
         return dxq, dxk, dv, None
 
 
@@ -1510,9 +1520,9 @@ class CausalProductDelta(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, state, scale):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        g, beta = g.contiguous(), beta.contiguous()
-        state = None if state is None else state.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
+        g, beta = _dense(g), _dense(beta)
+        state = _dense(state)
         out, s_n, ckpt = causal_product_fwd_delta(q, k, v, g, beta, state_in=state,
                                                   return_state=True, scale=scale, save=True)
         ctx.save_for_backward(q, k, v, g, beta, ckpt)
@@ -1523,8 +1533,8 @@ class CausalProductDelta(torch.autograd.Function):
     @staticmethod
     def backward(ctx, go, gs):
         q, k, v, g, beta, ckpt = ctx.saved_tensors
-        go = torch.zeros_like(v) if go is None else go.contiguous().to(v.dtype)
-        gs = None if gs is None else gs.contiguous().float()
+        go = torch.zeros_like(v) if go is None else _dense(go.to(v.dtype))
+        gs = None if gs is None else _dense(gs.float())
         d = causal_product_bwd_delta(q, k, v, g, beta, go, ckpt, scale=ctx.scale,
                                      grad_state_out=gs, return_state_grad=ctx.has_state)
         return d[:5] + (d[5] if ctx.has_state else None, None)
@@ -1542,10 +1552,8 @@ def causal_product_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
         out, s_n = CausalProductDelta.apply(q, k, v, g, beta, state, scale)
         return (out, s_n) if return_state else out
     # no gradient is wanted: no checkpoints
-    return causal_product_fwd_delta(q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous(),
-                                    beta.contiguous(),
-                                    state_in=None if state is None else state.contiguous(),
-                                    return_state=return_state, scale=scale)
+    return causal_product_fwd_delta(_dense(q), _dense(k), _dense(v), _dense(g), _dense(beta),
+                                    state_in=_dense(state), return_state=return_state, scale=scale)
 
 
 class QkRope(torch.autograd.Function):
@@ -1560,7 +1568,7 @@ class QkRope(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gq, gk):
         xq, xk, wq, wk, cos, sin = ctx.saved_tensors
-        gq, gk = gq.contiguous().to(xq.dtype), gk.contiguous().to(xq.dtype)
+        gq, gk = _dense(gq.to(xq.dtype)), _dense(gk.to(xq.dtype))
         return causal_product_qk_rope_bwd(xq, xk, wq, wk, gq, gk, cos, sin, ctx.norm,
                                           ctx.eps) + (None, None, None, None)
 
@@ -1578,9 +1586,9 @@ class CausalProductDecay(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, log_decay, state, scale, lengths, return_state):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        log_decay = log_decay.contiguous()
-        state = None if state is None else state.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
+        log_decay = _dense(log_decay)
+        state = _dense(state)
         got = causal_product_fwd_decay(q, k, v, log_decay, state_in=state,
                                        return_state=return_state, scale=scale, lengths=lengths)
         ctx.save_for_backward(q, k, v, log_decay, state, lengths)
@@ -1592,8 +1600,8 @@ class CausalProductDecay(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, go, gs):
         q, k, v, log_decay, state, lengths = ctx.saved_tensors
-        go = torch.zeros_like(v) if go is None else go.contiguous().to(v.dtype)
-        gs = None if gs is None else gs.contiguous().float()
+        go = torch.zeros_like(v) if go is None else _dense(go.to(v.dtype))
+        gs = None if gs is None else _dense(gs.float())
         d = causal_product_bwd_decay(q, k, v, log_decay, go, state_in=state, grad_state_out=gs,
                                      return_state_grad=state is not None, scale=ctx.scale,
                                      lengths=lengths)
@@ -1617,10 +1625,9 @@ def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             out, s_n = CausalProductDecay.apply(q, k, v, log_decay, state, scale, lengths,
                                                 bool(return_state))
             return (out, s_n) if return_state else out
-    return causal_product_fwd_decay(q.contiguous(), k.contiguous(), v.contiguous(),
-                                    log_decay.contiguous(),
-                                    state_in=None if state is None else state.contiguous(),
-                                    return_state=return_state, scale=scale, lengths=lengths)
+    return causal_product_fwd_decay(_dense(q), _dense(k), _dense(v), _dense(log_decay),
+                                    state_in=_dense(state), return_state=return_state, scale=scale,
+                                    lengths=lengths)
 
 
 class LayerNorm(torch.autograd.Function):
@@ -1636,7 +1643,7 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         x, weight, bias = ctx.saved_tensors
-        return causal_product_layer_norm_bwd(x, weight, bias, gy.contiguous().to(x.dtype), ctx.eps,
+        return causal_product_layer_norm_bwd(x, weight, bias, _dense(gy.to(x.dtype)), ctx.eps,
                                              ctx.token_major) + (None, None)
 
 
