@@ -1602,10 +1602,10 @@ class CausalProductDecay(torch.autograd.Function):
         q, k, v, log_decay, state, lengths = ctx.saved_tensors
         go = torch.zeros_like(v) if go is None else _dense(go.to(v.dtype))
         gs = None if gs is None else _dense(gs.float())
+        want = ctx.needs_input_grad[4]
         d = causal_product_bwd_decay(q, k, v, log_decay, go, state_in=state, grad_state_out=gs,
-                                     return_state_grad=state is not None, scale=ctx.scale,
-                                     lengths=lengths)
-        return d[:3] + (None, d[3] if state is not None else None, None, None, None)
+                                     return_state_grad=want, scale=ctx.scale, lengths=lengths)
+        return d[:3] + (None, d[3] if want else None, None, None, None)
 
 
 def causal_product_decay(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
