@@ -569,8 +569,8 @@ CP_API cp_status_t causal_product_decode_decay(const void* q, const void* k, con
  * Backward, from grad_y (dense, laid out as y): grad_x, dense [B][H][N][C], and
  * grad_w and grad_b (as w and b, in `dtype`; NULL: not written; grad_w only where
  * there is a w), summed in a fixed order.  Workspace:
- * causal_product_layer_norm_workspace_size bytes, or NULL (allocated on
- * `stream`). */
+ * causal_product_layer_norm_workspace_size bytes (256 with neither grad_w nor
+ * grad_b), or NULL (allocated on `stream`). */
 CP_API cp_status_t causal_product_layer_norm(const void* x, const int64_t* stride_x,
                                              const void* w, const void* b, int per_head, void* y,
                                              int token_major, float eps, int64_t B, int64_t H,

@@ -1366,22 +1366,25 @@ def causal_product_layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor
                                   bias: Optional[torch.Tensor], grad_out: torch.Tensor,
                                   eps: float = 1e-5, token_major: bool = False,
                                   workspace: Optional[torch.Tensor] = None,
-                                  stream: Optional[torch.cuda.Stream] = None):
+                                  stream: Optional[torch.cuda.Stream] = None,
+                                  weight_grad: bool = True, bias_grad: bool = True):
     """(dx, dweight, dbias) of L = <grad_out, y> for causal_product_layer_norm;
-    dx dense in x's shape, dweight and dbias None where the argument is."""
+    dx dense in x's shape, dweight and dbias None where the argument is, and not
+    computed (None) where ``weight_grad`` or ``bias_grad`` is false."""
     place = _elsewhere(x, stream)
     if place is not None:
         with place:
             return causal_product_layer_norm_bwd(x, weight, bias, grad_out, eps, token_major,
-                                                 workspace)
+                                                 workspace, None, weight_grad, bias_grad)
     rows, dims, code, dev, per_head, shape = _layer_norm_args(x, weight, bias, token_major)
     _check_like(grad_out, shape, x.dtype, "grad_out")
     _check_plain(dev, grad_out)
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = None if weight is None else torch.empty_like(weight)
-    db = None if bias is None else torch.empty_like(bias)
+    dw = None if weight is None or not weight_grad else torch.empty_like(weight)
+    db = None if bias is None or not bias_grad else torch.empty_like(bias)
     lib = load_library()
-    need = lib.causal_product_layer_norm_workspace_size(*dims, code)
+    gathers = dw is not None or db is not None
+    need = lib.causal_product_layer_norm_workspace_size(*dims, code) if gathers else 0
     workspace = _delta_workspace(workspace, need, x.device)
     rc = lib.causal_product_layer_norm_bwd(
         *rows, 0 if weight is None else weight.data_ptr(), per_head, grad_out.data_ptr(),
@@ -1644,7 +1647,8 @@ class LayerNorm(torch.autograd.Function):
     def backward(ctx, gy):
         x, weight, bias = ctx.saved_tensors
         return causal_product_layer_norm_bwd(x, weight, bias, _dense(gy.to(x.dtype)), ctx.eps,
-                                             ctx.token_major) + (None, None)
+                                             ctx.token_major, weight_grad=ctx.needs_input_grad[1],
+                                             bias_grad=ctx.needs_input_grad[2]) + (None, None)
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,

@@ -1587,7 +1587,8 @@ cp_status_t causal_product_layer_norm_bwd(const void* x, const int64_t* stride_x
     if ((reinterpret_cast<uintptr_t>(p) & (es - 1)) != 0) return CP_ERR_MISALIGNED;
   if (!cp::aligned16(grad_y) || !cp::aligned16(grad_x)) return CP_ERR_MISALIGNED;
   if (!cp::disjoint(in, outs)) return CP_ERR_INVALID_ARG;
-  const size_t need = cp::kStatusBytes + cp::round_up(cp::layer_norm_scratch(f));
+  const bool gathers = grad_w != nullptr || grad_b != nullptr;
+  const size_t need = cp::kStatusBytes + (gathers ? cp::round_up(cp::layer_norm_scratch(f)) : 0);
   if (workspace != nullptr && workspace_bytes < need) return CP_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (N == 0) {
