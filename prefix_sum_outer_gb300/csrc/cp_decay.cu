@@ -202,6 +202,9 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   const int64_t rows = rows_of(a.lengths, b, a.N);
   const int nv = (int)max((int64_t)0, min((int64_t)kC, rows - c * kC));
   if (nv == 0 && a.n > 1) return;
+  const bool end = a.n == 1;  // the state after the only chunk, itself
+  float* s = end ? (rev ? a.ds0 : a.s_end) : (rev ? a.rev : a.fwd);
+  if (s == nullptr) return;   // (the backward of one chunk has no S_N to write)
   const int mb = (a.M + kC - 1) / kC;
   const int d0 = (blockIdx.y / mb) * kC, m0 = (blockIdx.y % mb) * kC;
   const int64_t row0 = bh * a.N + c * kC, krow0 = (b * a.Hk + h / a.group) * a.N + c * kC;
@@ -221,9 +224,6 @@ __global__ void __launch_bounds__(kThreads) decay_sums_kernel(const Args a) {
   float2 acc[4][4];
   clear(acc);
   gemm(acc, x.x, y.x, 0, nv, rg, cg);
-  const bool end = a.n == 1;  // the state after the only chunk, itself
-  float* s = end ? (rev ? a.ds0 : a.s_end) : (rev ? a.rev : a.fwd);
-  if (s == nullptr) return;
   s += (bh * a.n + c) * (int64_t)a.D * a.M;
   const float* from = !end || (rev ? a.gs : a.s0) == nullptr
                           ? nullptr : (rev ? a.gs : a.s0) + bh * (int64_t)a.D * a.M;
