@@ -45,6 +45,7 @@ __all__ = [
     "causal_product_fwd_decay", "causal_product_bwd_decay", "causal_product_decay",
     "causal_product_decode_decay", "causal_product_decay_workspace_size",
     "causal_product_layer_norm", "causal_product_layer_norm_bwd", "layer_norm",
+    "causal_product_layer_norm_workspace_size",
     "causal_product_error_string", "library_path", "load_library",
 ]
 
@@ -1333,6 +1334,13 @@ def _layer_norm_args(x, weight, bias, token_major):
             raise RuntimeError("all tensors must be on the same CUDA device")
     shape = (xs[0], xs[2], xs[1], C) if token_major else tuple(xs)
     return (x.data_ptr(), _Strides(*strides)), dims, code, dev, int(bool(per_head)), shape
+
+
+def causal_product_layer_norm_workspace_size(B: int, H: int, N: int, C: int,
+                                             dtype: torch.dtype = torch.bfloat16) -> int:
+    """Workspace bytes of causal_product_layer_norm_bwd for x [B,H,N,C]; rows [B,N,C]
+    count as one head, [R,C] as one sequence of one head (0: a shape that is refused)."""
+    return int(load_library().causal_product_layer_norm_workspace_size(B, H, N, C, _DTYPES[dtype]))
 
 
 def causal_product_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
