@@ -1310,6 +1310,8 @@ def _layer_norm_args(x, weight, bias, token_major):
         dims, strides = (xs[0], 1, xs[1], C), (st[0], 0, st[1])
     else:
         dims, strides = tuple(xs), st[:3]
+    if dims[0] == 0:
+        dims = (1, dims[1], 0, C)  # no sequences: no rows (the C side wants B > 0)
     code = _dtype_code(x)
     dev = x.get_device()
     if dev < 0:
@@ -1350,7 +1352,7 @@ def causal_product_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = 
     """Layer norm of the rows of x ([R,C], [B,N,C] or a causal product's heads
     [B,H,N,C]) over their C features, times ``weight`` plus ``bias`` ([C], or
     [H,C] for weights of each head; None = ones, zeros).  x may be a strided view
-    (rows dense).  The result is dense: x's shape, or with ``token_major``
+    (rows dense), or empty.  The result is dense: x's shape, or with ``token_major``
     [B,N,H,C], the rows an output projection reads."""
     place = _elsewhere(x, stream)
     if place is not None:
