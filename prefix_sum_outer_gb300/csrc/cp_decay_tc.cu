@@ -35,14 +35,15 @@
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
 // e^{g (31 - (j - j0))}, two numbers at most 1, one per row and one per column.
 //
-// No memory or matrix rate bounds it: with any one of the products, or of the
-// groups' stores, left out it is at most 4 % faster, without the P groups' work 10 %.
-// The roles share four schedulers, and a tile takes about 3,300 cycles with 64-wide A
-// (1,900 of them the tensor core's, for the bf16 parts) and 4,800 with 128, where C's
-// two boxes, which wait for O, hold up the next.  Forward: B=8 H=16 N=4096 D=M=64 66 us,
-// 61 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 231; forward and backward of
-// the first 252.  O straight from the registers, 32 bytes of a
-// row to a store, frees C sooner: 215 for the second, but 232 for the last.
+// No memory or matrix rate bounds it: when every factor had two parts, leaving out any
+// one of the products, or of the groups' stores, gave at most 4 %, the P groups' work
+// 10 %.  The roles share four schedulers, and a tile takes about 3,300 cycles with
+// 64-wide A (1,900 of them the tensor core's, for the bf16 parts) and 4,800 with 128,
+// where C's two boxes, which wait for O, hold up the next.  Forward: B=8 H=16 N=4096
+// D=M=64 66 us, 61 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 231; forward
+// and backward of the first 252.  O straight from the registers, 32 bytes of a row to a
+// store, frees C sooner: 215 against 220 us for the second as it was then, but 232
+// against 224 for the last.
 //
 // Sequences of few heads are cut into pieces: the same kernel with the output
 // left out (AGG) sums each piece's B^T C', a prefix launch turns the sums into
@@ -121,7 +122,7 @@ struct Layout {
   static constexpr int NB = AGG && DP == 128 ? 1 : 2;          // stages of the B ring
   // tiles of A, which wait for the state, and of C, whose boxes take O: what is left.
   // In one ring, C before A, a 128-wide A waited for the O two tiles back: 235 against
-  // 220 us (B=2 H=8 N=32768 D=M=128)
+  // 220 us (B=2 H=8 N=32768 D=M=128, with two parts to every factor)
   static constexpr int RA = AGG ? 0 : DP == 128 ? 2 : 3;
   static constexpr int RC = AGG ? 3 : (kRoom - (NB + RA) * kBStage - kSBytes - kVBytes) / kBoxBytes;
   static constexpr int kBoxes = (NB + RA) * kABoxes + RC;
@@ -167,7 +168,7 @@ __device__ __forceinline__ float2 widen(uint32_t h) {
 // the code behind a wait is uniform: its addresses and descriptors stay in uniform
 // registers, where one lane alone in a branch moves each there first (forward and
 // backward of B=8 H=16 N=4096 D=M=64: 249 us with the issuers and the producer as
-// single lanes, 219 so).
+// single lanes, 219 so, when every factor had two parts).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint32_t tries = 0;
   bool there = true;
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
       const uint32_t el = elect_one();
       // (A S is issued by the warp of A B^T: by that of P C it would take 234 against 232
       // us with 128-wide A, B=2 H=8 N=32768, and more with 64-wide)
-      // (these loops stay rolled: with four MMAs to a turn forward and backward of the
-      // same take 223 against 220 us)
+      // (these loops stay rolled: with four MMAs to a turn the backward of B=8 H=16
+      // N=4096 D=M=64 takes the same 184 us)
       [[maybe_unused]] auto issue_p = [&](int it) {
         tc_fence_after();
         const uint32_t t_p = tmem + (it % kNP) * 128;
@@ -971,8 +972,10 @@ struct Plan {
 // G, the pieces to a sequence, is the one with the least tiles in line: rounds of
 // CTAs on the SMs times the tiles of a piece, a round's start and end worth
 // four; and with G > 1 the summing launch, which reads all pieces but one at
-// three times that rate, and the two launches more, worth four.  (A tile is 2 to 3
-// us.)
+// three times that rate, and the two launches more, worth four.  (A tile is 1.6 to
+// 2.4 us.)  At most 64 pieces: the prefix walks them one after the other, which this
+// estimate leaves out.  With up to 152 B=1 H=2 N=65536 D=M=64 takes 71 us, not 47,
+// H=1 D=M=128 79, not 57; H=1 D=M=64 alone gains, 51 for 56, at N=262144 84 for 105.
 Plan plan(const DecayShape& s, int64_t DA, int64_t DC, int products) {
   Plan p;
   p.DP = DA <= 64 ? 64 : 128;
@@ -1106,8 +1109,8 @@ bool decay_tc_supported(const DecayShape& s) {
 // Products of one class of widths may share a launch: where that saves rounds of
 // CTAs or launches, for a CTA whose product is chosen as it runs is a tenth slower.
 // The backward, three products in one launch against three launches: B=2 H=8 N=1000
-// D=M=64 35 against 51 us, D=M=128 30 against 68, B=3 H=10 N=3000 D=M=64 58 against
-// 88, and B=8 H=16 N=4096 D=M=64, three rounds either way, 224 against 201.
+// D=M=64 34 against 50 us, D=M=128 27 against 63, B=3 H=10 N=3000 D=M=64 54 against
+// 82, and B=8 H=16 N=4096 D=M=64, three rounds either way, 213 against 184.
 static int in_one_launch(const DecayShape& s) {
   const double dq = plan(s, s.M, s.D, 1).tiles;
   auto pays = [&](int n) { return 1.1 * plan(s, s.M, s.D, n).tiles < n * (dq + 1); };
