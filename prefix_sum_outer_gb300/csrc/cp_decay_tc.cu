@@ -37,8 +37,8 @@
 //
 // No memory or matrix rate bounds it: when every factor had two parts, leaving out any
 // one of the products, or of the groups' stores, gave at most 4 %, the P groups' work
-// 10 %.  The roles share four schedulers, and a tile takes about 3,300 cycles with
-// 64-wide A (1,900 of them the tensor core's, for the bf16 parts) and 4,800 with 128,
+// 10 %.  The roles share four schedulers, and a tile takes about 3,400 cycles with
+// 64-wide A (1,900 of them the tensor core's, for the bf16 parts) and 4,900 with 128,
 // where C's two boxes, which wait for O, hold up the next.  Forward: B=8 H=16 N=4096
 // D=M=64 66 us, 61 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 231; forward
 // and backward of the first 252.  O straight from the registers, 32 bytes of a row to a
