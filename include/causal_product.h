@@ -523,7 +523,7 @@ CP_API cp_status_t causal_product_qk_rope_bwd(const void* xq, const int64_t* str
  * State and sums are fp32, and a state that is returned is as exact as fp32
  * arithmetic on every path.  On the tensor cores (bf16, D, M <= 128) the state and
  * the rows that it takes enter their products as sums of three bf16 numbers, a
- * tile's decayed scores as two (17 bits).  Results are bitwise reproducible, and
+ * tile's decayed scores as two (17 bits; three where N <= 128).  Results are bitwise reproducible, and
  * whether a state is asked for changes no other result.  Workspace: causal_product_decay_workspace_size bytes, or NULL
  * (allocated and freed on `stream`).  Errors as causal_product_fwd; CP_ERR_INVALID_ARG too when Hk does
  * not divide H or scale is not finite. */

@@ -29,7 +29,8 @@
 // bf16 number.  A third part of P would need 64 columns more of a tensor memory that is
 // full, a second accumulator for B^T C' given up for them: 96 against 66 us (B=8 H=16
 // N=4096 D=M=64), with the results 4.8e-5 from the rounded 64-bit ones instead of 5.4e-5
-// (two parts of everything: 1.1e-4).
+// (two parts of everything: 1.1e-4).  A call of one tile, whose results are P's alone
+// but for a carried state's part, has a buffer of P free for its third parts.
 //
 // Powers come from a table of e^{g n}, n <= 128, of products in shared memory: a
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
@@ -41,7 +42,7 @@
 // 64-wide A (1,900 of them the tensor core's, for the bf16 parts) and 4,900 with 128,
 // where C's two boxes, which wait for O, hold up the next.  Forward: B=8 H=16 N=4096
 // D=M=64 66 us, 61 % of the copy rate on 128 SMs; B=2 H=8 N=32768 D=M=128 231; forward
-// and backward of the first 252.  O straight from the registers, 32 bytes of a row to a
+// and backward of the first 245 to 252.  O straight from the registers, 32 bytes of a row to a
 // store, frees C sooner: 215 against 220 us for the second as it was then, but 232
 // against 224 for the last.
 //
@@ -193,8 +194,9 @@ __device__ __forceinline__ void fewer_registers() {
 }
 
 // MAX: products that share a launch, at most (their CTAs in turn, so that those of
-// one head, which read the same rows, run side by side)
-template <int DP, bool AGG, int MAX>
+// one head, which read the same rows, run side by side).  ONE: a sequence is one tile,
+// and P has three parts
+template <int DP, bool AGG, bool ONE, int MAX>
 __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
     decay_tc_kernel(const __grid_constant__ Maps<MAX> maps, const __grid_constant__ Set<MAX> set) {
   using L = Layout<DP, AGG>;
@@ -515,15 +517,19 @@ __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t c_lo = desc_lo(smem_u32(ring + x * kBoxBytes), kBoxBytes);
-          // 32 columns of P: hi in their first 16 TMEM columns, lo in the next,
-          // two j to a column (lo first, as in A S)
+          // 32 columns of P: the first parts in their first 16 TMEM columns, the second
+          // in the next, two j to a column; the third parts of an only tile in the other
+          // buffer (the small parts first, as in A S)
+          constexpr int parts = ONE ? 3 : 2;
 #pragma unroll 1
-          for (int part = 1; part >= 0; --part)
+          for (int part = parts - 1; part >= 0; --part) {
+            const uint32_t p = tmem + (part == 2 ? 128 : bf * 128 + part * 16);
+            const int step = part == 2 ? 16 : 32;
 #pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_ts_lo_elect<kHi>(tmem + L::kColO2,
-                             tmem + bf * 128 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
-                             c_lo + ((kk * 2048) >> 4), idesc_o, part < 1 || kk > 0, el);
+              mma_ts_lo_elect<kHi>(tmem + L::kColO2, p + (kk >> 1) * step + (kk & 1) * 8,
+                             c_lo + ((kk * 2048) >> 4), idesc_o, part < parts - 1 || kk > 0, el);
+          }
           mma_commit_elect(&pc_done[bf], el);
           mma_commit_elect(o2_done, el);
         }
@@ -732,10 +738,20 @@ __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = 0u;
           tmem_st32(pc + 32 * c, r);
+          if constexpr (ONE) tmem_st16(pc + 128 + 16 * c, r);
           continue;
         }
         tmem_ld32(pc + 32 * c, r);
-        uint32_t lo[16];
+        uint32_t lo[16], third[ONE ? 16 : 1];
+        auto put = [&](int x, float2 p) {
+          r[x] = split_hi(p);
+          if constexpr (ONE) {
+            lo[x] = split_hi(p);
+            third[x] = tc::pack_bf16x2(p.x, p.y);
+          } else {
+            lo[x] = tc::pack_bf16x2(p.x, p.y);
+          }
+        };
         if (c == wq) {
           // the diagonal chunk: a power per element, masked places 0 whatever
           // the accumulators hold
@@ -748,8 +764,7 @@ __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
             const bool k1 = rev ? 2 * x + 1 >= lane : 2 * x + 1 <= lane;
             p.x = k0 ? __uint_as_float(r[2 * x]) * (s_p * w[rev ? 2 * x : -2 * x]) : 0.f;
             p.y = k1 ? __uint_as_float(r[2 * x + 1]) * (s_p * w[rev ? 2 * x + 1 : -2 * x - 1]) : 0.f;
-            r[x] = split_hi(p);
-            lo[x] = tc::pack_bf16x2(p.x, p.y);
+            put(x, p);
           }
         } else {
           const float2 rf = both(s_p * pw[rev ? 32 * c - row : row - 32 * c - 31]);
@@ -760,13 +775,14 @@ __global__ void __launch_bounds__(Layout<DP, AGG>::kThreads, AGG ? 2 : 1)
             const float2 w = x % 2 ? make_float2(f[x / 2].z, f[x / 2].w) : make_float2(f[x / 2].x, f[x / 2].y);
             float2 p = mul2(mul2(rf, w),
                             make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
-            r[x] = split_hi(p);
-            lo[x] = tc::pack_bf16x2(p.x, p.y);
+            put(x, p);
           }
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) r[16 + x] = lo[x];
         tmem_st32(pc + 32 * c, r);
+        // (the only tile is buffer 0's: buffer 1 takes the third parts)
+        if constexpr (ONE) tmem_st16(pc + 128 + 16 * c, third);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1006,10 +1022,10 @@ Plan plan(const DecayShape& s, int64_t DA, int64_t DC, int products) {
   return p;
 }
 
-template <int DP, bool AGG, int MAX>
+template <int DP, bool AGG, bool ONE, int MAX>
 cudaError_t launch(const Maps<MAX>& maps, const Set<MAX>& set, unsigned grid, cudaStream_t stream) {
   using L = Layout<DP, AGG>;
-  auto kern = decay_tc_kernel<DP, AGG, MAX>;
+  auto kern = decay_tc_kernel<DP, AGG, ONE, MAX>;
   // the shared-memory opt-in is set once per device for each instantiation
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -1029,13 +1045,14 @@ cudaError_t launch_all(const Plan& pl, const Maps<MAX>& maps, const Set<MAX>& se
                        cudaStream_t stream) {
   const unsigned n = (unsigned)(pl.problems * set.all.products);
   if (pl.G > 1) {
-    cudaError_t e = launch<DP, true, MAX>(maps, set, n * (pl.G - 1) * pl.sub, stream);
+    cudaError_t e = launch<DP, true, false, MAX>(maps, set, n * (pl.G - 1) * pl.sub, stream);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(pl.problems * DP * kMB / 4 / kPrefixThreads), set.all.products);
     e = launch_dependent(decay_tc_prefix_kernel<MAX>, grid, kPrefixThreads, 0, stream, set, DP);
     if (e != cudaSuccess) return e;
   }
-  return launch<DP, false, MAX>(maps, set, n * pl.G, stream);
+  return pl.n_tiles == 1 ? launch<DP, false, true, MAX>(maps, set, n, stream)
+                         : launch<DP, false, false, MAX>(maps, set, n * pl.G, stream);
 }
 
 struct RowProduct {

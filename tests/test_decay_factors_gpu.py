@@ -14,7 +14,11 @@ hundreds before it, five times as many or more at all but the first tiles: P car
 at most 0.5 of the result in the 2-norm, mean|e| = 0.8 * 0.5 * 2.2e-6 = 9e-7.  The
 accumulators' rounding toward zero adds 8 steps of 2^-24, 5e-7 at most.  In all
 1.4e-6, and sqrt(0.0044 * 1.4e-6) = 7.8e-5.  With the state and its rows as two bf16
-numbers as well it would be mean|e| = 0.8 * sqrt(2) * 2.2e-6 = 2.5e-6, 1.05e-4."""
+numbers as well it would be mean|e| = 0.8 * sqrt(2) * 2.2e-6 = 2.5e-6, 1.05e-4.
+
+A call of one tile has its scores in three bf16 numbers, in full: what is left is the
+rounding toward zero, 8 steps of 2^-24 in a score and as many in its product, 1e-6 at
+most, sqrt(0.0044 * 1e-6) = 6.6e-5; with two numbers it would be 0.8 * 2.2e-6, 8.8e-5."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +61,14 @@ def test_the_state_enters_in_full(shape):
     for name, got in zip(("out", "dq", "dk", "dv"), without_states(x)):
         r = f64(torch.from_numpy(np.ascontiguousarray(want[name])).to(torch.bfloat16))
         assert err(got, r) <= 7.8e-5, f"{name}: {err(got, r):.3g}"
+
+
+@pytest.mark.parametrize("shape", [(32, 8, 8, 100, 64, 64), (16, 4, 4, 128, 128, 128), (64, 8, 4, 17, 96, 72),
+                                   (128, 8, 8, 3, 64, 64)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("carry", [False, True])
+def test_one_tile_is_held_in_full(shape, carry):
+    x = make(*shape, DT["bf16"], seed=63, carry=carry)
+    want = wanted(x)
+    for name, got in zip(("out", "dq", "dk", "dv"), without_states(x)):
+        r = f64(torch.from_numpy(np.ascontiguousarray(want[name])).to(torch.bfloat16))
+        assert err(got, r) <= 6.6e-5, f"{name}: {err(got, r):.3g}"
