@@ -30,7 +30,8 @@
 // full, a second accumulator for B^T C' given up for them: 96 against 66 us (B=8 H=16
 // N=4096 D=M=64), with the results 4.8e-5 from the rounded 64-bit ones instead of 5.4e-5
 // (two parts of everything: 1.1e-4).  A call of one tile, whose results are P's alone
-// but for a carried state's part, has a buffer of P free for its third parts.
+// but for a carried state's part, has a buffer of P free for its third parts (1e-4 with
+// two, 6e-5 and less with three; 26 us either way, the call's).
 //
 // Powers come from a table of e^{g n}, n <= 128, of products in shared memory: a
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
