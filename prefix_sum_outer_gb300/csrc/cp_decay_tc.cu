@@ -24,14 +24,15 @@
 // memory would be rounded toward zero at every MMA and lose 1e-5 of a state that
 // remembers thousands of rows.  C' and the copy of S enter their products as three bf16
 // numbers, all 24 bits, whether or not a state is asked for, so that asking changes no
-// other result.  P has two (17 bits): its rounding, 2e-6 of a score, is a hundredth of
-// a bf16 result's own step of 2^-9, and moves one result in a thousand or two to the next
+// other result.  P has two (17 bits): its rounding, 2e-6 of a score, is a thousandth
+// of a bf16 result's own, 2^-9, and moves one result in a thousand or two to the next
 // bf16 number.  A third part of P would need 64 columns more of a tensor memory that is
 // full, a second accumulator for B^T C' given up for them: 96 against 66 us (B=8 H=16
 // N=4096 D=M=64), with the results 4.8e-5 from the rounded 64-bit ones instead of 5.4e-5
 // (two parts of everything: 1.1e-4).  A call of one tile, whose results are P's alone
-// but for a carried state's part, has a buffer of P free for its third parts (1e-4 with
-// two, 6e-5 and less with three; 26 us either way, the call's).
+// but for a carried state's part, has a buffer of P free for its third parts: 6e-5 and
+// less with three, 1e-4 with two, 43 against 40 us for B=64 H=16 N=128 D=M=64, and 17
+// either way, the call's, for B=8.
 //
 // Powers come from a table of e^{g n}, n <= 128, of products in shared memory: a
 // 32-column chunk of P left of the diagonal one has w_ij = e^{g (i - j0 - 31)}
